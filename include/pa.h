@@ -368,6 +368,107 @@ PA_API int pa_prefill_chunk(void* out, const void* q, const int32_t* cu_q_lens, 
                      void* stream);
 
 /*
+ * e4m3 pools with one scale for each (block, kv head) ("KV cache 显存管理…", KV
+ * size formula: dtype_size a free factor).  One scale per pool (above) has to
+ * be chosen before the first token and is shared by heads of different size;
+ * here the write chooses it: the pools are uint8 [num_blocks][block_size]
+ * [num_kv_heads][head_dim] e4m3 codes as before, k_scales / v_scales are
+ * float [num_blocks][num_kv_heads], and an element reads back as
+ * code * scales[its block][its kv head].
+ *
+ * The write, pa_write_kv_paged_fp8 for such pools: token t's bf16 rows go to
+ * the slot that (block_tables, seq_idx, pos) gives (exactly pa_slot_mapping's;
+ * pos < 0 is skipped, invalid indices are counted and skipped; slot_mapping,
+ * int64 [num_tokens], may be NULL).  For every block b that a call stores rows
+ * into, and every head h, separately for K and V:
+ *     s_new = 2^e, e the smallest integer >= -100 with max|x| <= 448 * 2^e over
+ *             the finite elements x of head h of the rows stored into b,
+ *     s     = max(s_new, scales[b][h]); s_new alone if the call stores b's
+ *             first slot: that starts the block anew,
+ *     code  = e4m3(x / s) (nearest, ties to even; beyond 448 held at 448; NaN
+ *             stays NaN),
+ * and scales[b][h] = s.  Where s is larger than before (and the block is not
+ * started anew) the codes of b's other slots are replaced by
+ * e4m3(code * old / s), so that they keep their values: exact for scales that
+ * are powers of two, but for e4m3's subnormals.  Tokens may come in any order
+ * and several sequences may store into one block; of several tokens for one
+ * slot the last in the arrays is stored.  Nothing outside the named blocks is
+ * written.  Copying a block (pa_copy_blocks moves the codes of pools viewed as
+ * bf16 of half the head_dim) takes its scales along.
+ *   k_new, v_new        bf16 [num_tokens][num_kv_heads][head_dim]  (read)
+ *   k_scales, v_scales  float [num_blocks][num_kv_heads] (read and written);
+ *                       finite, and 0 or positive (0: nothing stored yet)
+ * Supported: head_dim a multiple of 16, num_kv_heads * head_dim <= 2^20,
+ * block_size 1..1024; the four row arrays 16-byte aligned.  workspace:
+ * pa_write_fp8_block_workspace_size(...) bytes (0 up to 1024 tokens, then NULL
+ * is fine), 256-byte aligned, zeroed once before its first use and left zeroed
+ * for reuse; one made for more tokens of the same pool serves fewer.  One
+ * workspace must not serve two calls that may overlap on the GPU, and two
+ * overlapping calls must not store into the same block.
+ */
+PA_API size_t pa_write_fp8_block_workspace_size(int num_tokens, int num_blocks, int block_size);
+PA_API int pa_write_kv_paged_fp8_block(const void* k_new, const void* v_new, int num_tokens, int num_kv_heads,
+                                       int head_dim, void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                                       int num_blocks, int block_size, const int32_t* block_tables, int num_seqs,
+                                       int max_blocks_per_seq, const int32_t* seq_idx, const int32_t* pos,
+                                       int64_t* slot_mapping, void* workspace, size_t workspace_bytes,
+                                       int32_t* error_count, void* stream);
+
+/*
+ * The read back: row t of k_out / v_out ([num_tokens][num_kv_heads][head_dim],
+ * dtype PA_BF16 or PA_F32) becomes code * scale of the token at position
+ * pos[t] of sequence seq_idx[t], the product in float, rounded once (bf16
+ * holds every value of a power-of-two scale exactly).  Rows with pos < 0 and
+ * rows with an invalid index (counted) are left as they were.  Any token may
+ * be named any number of times.  Shapes and alignment as for the write.
+ */
+PA_API int pa_read_kv_paged_fp8_block(void* k_out, void* v_out, int num_tokens, int num_kv_heads, int head_dim,
+                                      int dtype, const void* k_cache, const void* v_cache, const float* k_scales,
+                                      const float* v_scales, int num_blocks, int block_size,
+                                      const int32_t* block_tables, int num_seqs, int max_blocks_per_seq,
+                                      const int32_t* seq_idx, const int32_t* pos, int32_t* error_count,
+                                      void* stream);
+
+/*
+ * pa_decode over e4m3 pools with a scale per (block, kv head): the attention
+ * of pa_decode on the values that pa_read_kv_paged_fp8_block reads back; q and
+ * out bf16.  Scales must be finite and 0 or at least 2^-110 in the blocks that
+ * hold a sequence's tokens; those of other blocks are not used.  Tokens in a
+ * block with an invalid table entry are masked (and counted).  Shapes, context
+ * clamping and the workspace's rules are pa_decode's
+ * (pa_decode_fp8_block_workspace_size bytes).
+ */
+PA_API size_t pa_decode_fp8_block_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                                 int block_size, int max_context_len);
+PA_API int pa_decode_fp8_block(void* out, const void* q, int num_seqs, int num_q_heads, int num_kv_heads,
+                               int head_dim, const void* k_cache, const void* v_cache, const float* k_scales,
+                               const float* v_scales, int num_blocks, int block_size, const int32_t* block_tables,
+                               int max_blocks_per_seq, const int32_t* context_lens, int max_context_len, float scale,
+                               void* workspace, size_t workspace_bytes, int32_t* error_count, void* stream);
+
+/*
+ * pa_prefill_chunk over e4m3 pools with a scale per (block, kv head): the
+ * attention of pa_prefill_chunk on the values that are read back; q and out
+ * bf16, the chunks' own K and V written by pa_write_kv_paged_fp8_block first.
+ * max_context_len bounds q_start_pos[c] + n_c (keys at or beyond it are not
+ * read, and counted).  workspace: pa_prefill_fp8_block_workspace_size bytes
+ * (may be 0, then NULL is fine), 256-byte aligned; it needs no zeroing.  One
+ * workspace must not serve two calls that may overlap on the GPU.  Scales as
+ * for pa_decode_fp8_block, shapes as for pa_prefill_chunk.
+ */
+PA_API size_t pa_prefill_fp8_block_workspace_size(int num_chunks, int total_q, int max_q_len, int num_q_heads,
+                                                  int num_kv_heads, int head_dim, int block_size,
+                                                  int max_context_len);
+PA_API int pa_prefill_chunk_fp8_block(void* out, const void* q, const int32_t* cu_q_lens,
+                                      const int32_t* q_start_pos, const int32_t* seq_of_chunk, int num_chunks,
+                                      int total_q, int max_q_len, int num_seqs, int num_q_heads, int num_kv_heads,
+                                      int head_dim, const void* k_cache, const void* v_cache, const float* k_scales,
+                                      const float* v_scales, int num_blocks, int block_size,
+                                      const int32_t* block_tables, int max_blocks_per_seq,
+                                      const int32_t* context_lens, int max_context_len, float scale, void* workspace,
+                                      size_t workspace_bytes, int32_t* error_count, void* stream);
+
+/*
  * Kernel-side block tables for a block manager whose blocks hold `ratio`
  * kernel blocks ("PagedAttention学习笔记", 代码实现部分 › 块表与槽位映射, 混合块:
  * map_to_kernel_blocks).  The manager's pool [P][ratio*B][Hkv][D] is the same

@@ -20,7 +20,7 @@ namespace pa {
 // block table can cover; clamping counts one error when `report` is set.
 __device__ __forceinline__ int decode_context(const DecodeParams& p, int s, bool report) {
     int L = p.context_lens[s];
-    int cap = min(p.max_context_len, p.max_blocks_per_seq * p.block_size);
+    int cap = (int)min((long long)p.max_context_len, (long long)p.max_blocks_per_seq * p.block_size);
     if (L < 0 || L > cap) {
         if (report) count_error(p.error_count);
         L = L < 0 ? 0 : cap;

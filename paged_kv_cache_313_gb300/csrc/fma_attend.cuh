@@ -15,6 +15,8 @@
 // with x_j = scale*log2(e) * q.k_j (base-2 units).
 #pragma once
 
+#include <type_traits>
+
 #include "pa_internal.cuh"
 
 namespace pa {
@@ -39,14 +41,17 @@ struct FmaShape {
     }
 };
 
-// Attend q (G rows of D, storage type T) to tokens [j0, j1).  On return (after
+// Attend q (G rows of D, storage type T) to tokens [j0, j1) of pools of TP (T itself, or e4m3_t with a scale per
+// (block, kv head): a token's K scale multiplies its scores, its V scale its weight).  On return (after
 // a __syncthreads) m_s[g], l_s[g] hold the softmax state and acc[it] the
 // unnormalised output of item threadIdx.x + it*kFmaThreads = g*D + d.
-template <typename T, int D>
-__device__ void fma_attend(const T* __restrict__ q, int G, const T* __restrict__ kc, const T* __restrict__ vc,
+template <typename T, int D, typename TP = T>
+__device__ void fma_attend(const T* __restrict__ q, int G, const TP* __restrict__ kc, const TP* __restrict__ vc,
                            const int32_t* __restrict__ table, int block_size, int num_kv_heads, int kvh,
                            int num_blocks, int j0, int j1, float scale_log2, int32_t* error_count, float* smem,
-                           float (&acc)[FmaShape<D>::kItems], float* m_s, float* l_s, float* alpha_s) {
+                           float (&acc)[FmaShape<D>::kItems], float* m_s, float* l_s, float* alpha_s,
+                           const float* __restrict__ k_scales = nullptr, const float* __restrict__ v_scales = nullptr) {
+    constexpr bool kScaled = !std::is_same<T, TP>::value;
     using S = FmaShape<D>;
     constexpr int kPerLane = S::kPerLane;
     float* q_s = S::q_s(smem);
@@ -54,15 +59,15 @@ __device__ void fma_attend(const T* __restrict__ q, int G, const T* __restrict__
     int* blk_s = S::blk_s(smem);
     const int B = block_size, Hkv = num_kv_heads;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    T* rows = reinterpret_cast<T*>(S::row_s(smem));  // [kFmaPiece][D], rows of the piece's tokens
+    TP* rows = reinterpret_cast<TP*>(S::row_s(smem));  // [kFmaPiece][D], rows of the piece's tokens
     const bool vec16 = ((reinterpret_cast<uintptr_t>(kc) | reinterpret_cast<uintptr_t>(vc)) & 15u) == 0;
     // rows of tokens [c0 + p0, c0 + p0 + np) of `pool` (this kv head) into `rows`, zeros for a token without a
     // valid block; every thread's loads go out together.  Bracketed by barriers: the previous piece's readers
     // are done before, and the rows are visible to every warp after.
-    auto stage_rows = [&](const T* __restrict__ pool, int c0, int p0, int np, int lb0) {
+    auto stage_rows = [&](const TP* __restrict__ pool, int c0, int p0, int np, int lb0) {
         __syncthreads();
         if (vec16) {
-            constexpr int kChunks = D * (int)sizeof(T) / 16;  // 16-byte pieces of a row
+            constexpr int kChunks = D * (int)sizeof(TP) / 16;  // 16-byte pieces of a row
             for (int i = threadIdx.x; i < np * kChunks; i += kFmaThreads) {
                 const int t = i / kChunks, c = i - t * kChunks, j = c0 + p0 + t;
                 const int pb = blk_s[j / B - lb0];
@@ -75,7 +80,7 @@ __device__ void fma_attend(const T* __restrict__ q, int G, const T* __restrict__
             for (int i = threadIdx.x; i < np * D; i += kFmaThreads) {
                 const int t = i / D, d = i - t * D, j = c0 + p0 + t;
                 const int pb = blk_s[j / B - lb0];
-                rows[t * D + d] = pb >= 0 ? pool[(((size_t)pb * B + (j % B)) * Hkv + kvh) * D + d] : T{};
+                rows[t * D + d] = pb >= 0 ? pool[(((size_t)pb * B + (j % B)) * Hkv + kvh) * D + d] : TP{};
             }
         }
         __syncthreads();
@@ -103,6 +108,8 @@ __device__ void fma_attend(const T* __restrict__ q, int G, const T* __restrict__
             for (int t = warp; t < np; t += kFmaThreads / 32) {
                 const int j = c0 + p0 + t;
                 const int pb = blk_s[j / B - lb0];
+                const float to_log2 =
+                    kScaled && pb >= 0 ? scale_log2 * __ldg(k_scales + (size_t)pb * Hkv + kvh) : scale_log2;
                 float kr[kPerLane];
 #pragma unroll
                 for (int e = 0; e < kPerLane; ++e) kr[e] = to_float(rows[t * D + lane * kPerLane + e]);
@@ -111,7 +118,7 @@ __device__ void fma_attend(const T* __restrict__ q, int G, const T* __restrict__
 #pragma unroll
                     for (int e = 0; e < kPerLane; ++e) part = fmaf(q_s[g * D + lane * kPerLane + e], kr[e], part);
                     part = warp_sum(part);
-                    if (lane == 0) p_s[g * kFmaSub + p0 + t] = pb >= 0 ? part * scale_log2 : -INFINITY;
+                    if (lane == 0) p_s[g * kFmaSub + p0 + t] = pb >= 0 ? part * to_log2 : -INFINITY;
                 }
             }
         }
@@ -125,8 +132,12 @@ __device__ void fma_attend(const T* __restrict__ q, int G, const T* __restrict__
             float sum = 0.f;
             for (int t = lane; t < n; t += 32) {
                 float e = m_new == -INFINITY ? 0.f : exp2f(p_s[g * kFmaSub + t] - m_new);
-                p_s[g * kFmaSub + t] = e;
                 sum += e;
+                if (kScaled) {
+                    const int pb = blk_s[(c0 + t) / B - lb0];
+                    if (pb >= 0) e *= __ldg(v_scales + (size_t)pb * Hkv + kvh);
+                }
+                p_s[g * kFmaSub + t] = e;
             }
             sum = warp_sum(sum);
             if (lane == 0) {

@@ -1,0 +1,405 @@
+// kv_fp8_block.cu — e4m3 pools with one scale for each (block, kv head): the
+// quantising write and the read back.
+//
+// A block's values are code * scale[block][head].  The write takes, for the
+// rows a call stores into a block, the smallest power of two s with
+// max|x| <= 448 s and never goes below the block's scale from before, unless
+// the call stores the block's first slot, which starts the block anew.  Where
+// the scale grows the block's other codes are stored again under the new one.
+// Powers of two make both steps exact in float: x / s shifts an exponent, and
+// so does a code's move to a larger scale (only e4m3's subnormals round), so
+// a block that grows token by token loses nothing by being stored again.
+//
+// The work unit is a physical block: one CTA gathers all of the call's tokens
+// that fall into the block (whatever their order in the arrays), so the
+// maximum needs no atomics and every code is written once.  A warp takes one
+// (head, K or V) of the block: it loads the rows once into registers (up to
+// 256 16-byte pieces, a 16-token block of head_dim 128; larger blocks are read
+// twice, the second time from L1/L2), takes the maximum with one warp
+// reduction and stores the codes.
+//
+// Finding a block's tokens:
+//   * up to kScanTokens tokens (decode steps): one launch, a CTA per token;
+//     every CTA resolves all tokens itself and only the first token of each
+//     block goes on.  No workspace, no second launch.
+//   * more tokens: a first launch resolves each token once, records it as its
+//     slot's writer (atomicMax, so of several tokens naming one slot the last
+//     is stored, as in the one-launch form) and lists each block once; a second
+//     launch walks the list.  It leaves the workspace zeroed again.
+//
+// Bound: HBM for long calls, launch and memory latency for a decode step.
+#include "pa_internal.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kScanTokens = 1024;  // largest call of the one-launch form
+constexpr int kMaxBlock = 1024;    // slots per block
+constexpr int kCached = 8;         // 16-byte pieces of a (block, head, side) that a lane keeps in registers
+constexpr int kMinExponent = -100; // scale of an all-zero block: 2^-100
+
+struct BlockWriteParams {
+    const uint4* k_new;  // [num_tokens][num_kv_heads][head_dim] bf16
+    const uint4* v_new;
+    uint8_t* k_cache;
+    uint8_t* v_cache;
+    float* k_scales;
+    float* v_scales;
+    const int32_t* block_tables;
+    const int32_t* seq_idx;
+    const int32_t* pos;
+    int64_t* slots;
+    int32_t* error_count;
+    int num_tokens, num_kv_heads, head_dim, num_blocks, block_size, num_seqs, max_blocks_per_seq;
+    // two-launch form (workspace)
+    int32_t* counters;  // [0] blocks listed, [1] CTAs done
+    int32_t* listed;    // [num_blocks] 1: the block is on the list
+    int32_t* finished;  // [num_blocks] CTAs (grid.y) that have read the block's writers
+    int32_t* writer;    // [num_blocks][block_size] token + 1 of the slot's writer, 0: none
+    int32_t* list;      // [min(num_tokens, num_blocks)] the listed blocks
+};
+
+// Physical block and offset of token t; -1 when it is not stored (pos < 0), -2 when an index is invalid.
+__device__ __forceinline__ int resolve(const BlockWriteParams& p, int t, int& off) {
+    const int pos = p.pos[t], s = p.seq_idx[t];
+    off = 0;
+    if (pos < 0) return -1;
+    const int lb = pos / p.block_size;
+    off = pos - lb * p.block_size;
+    if (s < 0 || s >= p.num_seqs || lb >= p.max_blocks_per_seq) return -2;
+    const int pb = p.block_tables[(long long)s * p.max_blocks_per_seq + lb];
+    return pb >= 0 && pb < p.num_blocks ? pb : -2;
+}
+
+// Largest finite magnitude of eight bf16 as bf16 bits (infinities and NaN take no part in the scale).
+__device__ __forceinline__ uint32_t amax_bits8(const uint4& x, uint32_t m) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
+        m = max(m, lo >= 0x7F80u ? 0u : lo);
+        m = max(m, hi >= 0x7F80u ? 0u : hi);
+    }
+    return m;
+}
+
+// 2^e with e the smallest integer such that amax <= 448 * 2^e = 1.75 * 2^(e + 8), at least kMinExponent.
+__device__ __forceinline__ float scale_of_amax(uint32_t bf16_bits) {
+    const int e = (int)(bf16_bits >> 7) - 127 - 8 + ((bf16_bits & 0x7Fu) > 0x60u ? 1 : 0);
+    return __uint_as_float((uint32_t)((bf16_bits == 0 ? kMinExponent : max(e, kMinExponent)) + 127) << 23);
+}
+
+// Four bf16 to four e4m3 codes of x / s: a product with the exact reciprocal when s is a power of two.
+__device__ __forceinline__ uint32_t codes4(uint2 x, float s, float inv, bool pow2) {
+    if (pow2) return e4m3x4_of_bf16x4(x, inv);
+    const float a = __fdiv_rn(__uint_as_float(x.x << 16), s), b = __fdiv_rn(__uint_as_float(x.x & 0xFFFF0000u), s);
+    const float c = __fdiv_rn(__uint_as_float(x.y << 16), s), d = __fdiv_rn(__uint_as_float(x.y & 0xFFFF0000u), s);
+    return (uint32_t)pack_e4m3x2(a, b) | ((uint32_t)pack_e4m3x2(c, d) << 16);
+}
+
+// Two codes moved to a scale 1 / f times as large (f <= 1).
+__device__ __forceinline__ uint16_t recode2(uint16_t c, float f) {
+    const float2 v = e4m3x2_to_float2(c);
+    return pack_e4m3x2(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
+}
+
+// One warp stores the call's rows of (block pb, head h, K or V): members [n] pairs (token, offset).
+__device__ void store_rows(const BlockWriteParams& p, int pb, int pair, const int2* members, int n,
+                           const int32_t* writer, bool fresh, int lane) {
+    const int h = pair >> 1, D = p.head_dim, pieces = D / 8, row_pieces = p.num_kv_heads * pieces;
+    const uint4* src = ((pair & 1) ? p.v_new : p.k_new) + h * pieces;
+    uint8_t* cache = ((pair & 1) ? p.v_cache : p.k_cache) + (size_t)h * D;
+    float* scale_ptr = ((pair & 1) ? p.v_scales : p.k_scales) + (size_t)pb * p.num_kv_heads + h;
+    const size_t row_bytes = (size_t)p.num_kv_heads * D, slot0 = (size_t)pb * p.block_size;
+    const int total = n * pieces;
+    const float old = *scale_ptr;
+    uint4 x[kCached];
+    uint32_t am = 0;
+#pragma unroll
+    for (int k = 0; k < kCached; ++k) {
+        const int i = lane + 32 * k;
+        if (i < total) x[k] = __ldg(src + (size_t)members[i / pieces].x * row_pieces + i % pieces);
+    }
+#pragma unroll
+    for (int k = 0; k < kCached; ++k)
+        if (lane + 32 * k < total) am = amax_bits8(x[k], am);
+    for (int i = lane + 32 * kCached; i < total; i += 32)
+        am = amax_bits8(__ldg(src + (size_t)members[i / pieces].x * row_pieces + i % pieces), am);
+    am = __reduce_max_sync(0xffffffffu, am);
+    const float base = !fresh && old > 0.f ? old : 0.f;
+    const float s = fmaxf(base, scale_of_amax(am));
+    const float inv = 1.0f / s;
+    const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;
+    auto put = [&](int i, const uint4& v) {
+        const uint2 c = make_uint2(codes4(make_uint2(v.x, v.y), s, inv, pow2),
+                                   codes4(make_uint2(v.z, v.w), s, inv, pow2));
+        *reinterpret_cast<uint2*>(cache + (slot0 + members[i / pieces].y) * row_bytes + (i % pieces) * 8) = c;
+    };
+#pragma unroll
+    for (int k = 0; k < kCached; ++k)
+        if (lane + 32 * k < total) put(lane + 32 * k, x[k]);
+    for (int i = lane + 32 * kCached; i < total; i += 32)
+        put(i, __ldg(src + (size_t)members[i / pieces].x * row_pieces + i % pieces));
+    if (!fresh && s > base) {  // the block's other codes keep their values under the larger scale
+        const float f = __fdiv_rn(base, s);
+        const int kept = p.block_size * pieces;
+        for (int i = lane; i < kept; i += 32) {
+            const int off = i / pieces;
+            if (writer[off] != 0) continue;
+            uint2* c = reinterpret_cast<uint2*>(cache + (slot0 + off) * row_bytes + (i % pieces) * 8);
+            const uint2 v = *c;
+            *c = make_uint2((uint32_t)recode2((uint16_t)v.x, f) | ((uint32_t)recode2((uint16_t)(v.x >> 16), f) << 16),
+                            (uint32_t)recode2((uint16_t)v.y, f) | ((uint32_t)recode2((uint16_t)(v.y >> 16), f) << 16));
+        }
+    }
+    __syncwarp();  // every lane has read the old scale
+    if (lane == 0) *scale_ptr = s;
+}
+
+// The block's stored rows as (token, offset) pairs in offset order, from writer[0..B); all threads; returns how many.
+__device__ int gather_members(const int32_t* writer, int B, int2* members, int* warp_count) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    int base = 0;
+    for (int b0 = 0; b0 < B; b0 += kThreads) {
+        const int off = b0 + threadIdx.x, w = off < B ? writer[off] : 0;
+        const uint32_t hit = __ballot_sync(0xffffffffu, w != 0);
+        __syncthreads();  // the previous round's counts have been read
+        if (lane == 0) warp_count[warp] = __popc(hit);
+        __syncthreads();
+        int at = base;
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) at += warp_count[i];
+            base += warp_count[i];
+        }
+        if (w != 0) members[at + __popc(hit & ((1u << lane) - 1u))] = make_int2(w - 1, off);
+    }
+    __syncthreads();
+    return base;
+}
+
+// One launch: CTA (token, slice of the (head, side) pairs).  The first token of each block stores the block.
+__global__ void __launch_bounds__(kThreads) write_scan_kernel(const BlockWriteParams p) {
+    pdl_trigger();
+    pdl_wait();
+    __shared__ int32_t writer[kMaxBlock];
+    __shared__ int2 members[kMaxBlock];
+    __shared__ int warp_count[kWarps];
+    const int t = blockIdx.x, B = p.block_size;
+    for (int i = threadIdx.x; i < B; i += kThreads) writer[i] = 0;
+    int my_off;
+    const int mine = resolve(p, t, my_off);
+    if (blockIdx.y == 0 && threadIdx.x == 0) {
+        if (p.slots) p.slots[t] = mine < 0 ? -1 : (long long)mine * B + my_off;
+        if (mine == -2) count_error(p.error_count);
+    }
+    if (mine < 0) return;
+    __syncthreads();
+    bool earlier = false;
+    for (int i = threadIdx.x; i < p.num_tokens; i += kThreads) {
+        int off;
+        if (resolve(p, i, off) != mine) continue;
+        earlier |= i < t;
+        atomicMax(&writer[off], i + 1);
+    }
+    if (__syncthreads_or(earlier)) return;
+    const int n = gather_members(writer, B, members, warp_count);
+    for (int pair = blockIdx.y * kWarps + (threadIdx.x >> 5); pair < 2 * p.num_kv_heads; pair += gridDim.y * kWarps)
+        store_rows(p, mine, pair, members, n, writer, writer[0] != 0, threadIdx.x & 31);
+}
+
+// Two launches, first: each token becomes its slot's writer and lists its block.
+__global__ void __launch_bounds__(kThreads) write_list_kernel(const BlockWriteParams p) {
+    pdl_trigger();
+    pdl_wait();
+    const int t = blockIdx.x * kThreads + threadIdx.x;
+    if (t >= p.num_tokens) return;
+    int off;
+    const int pb = resolve(p, t, off);
+    if (p.slots) p.slots[t] = pb < 0 ? -1 : (long long)pb * p.block_size + off;
+    if (pb == -2) count_error(p.error_count);
+    if (pb < 0) return;
+    atomicMax(&p.writer[(size_t)pb * p.block_size + off], t + 1);
+    if (atomicExch(&p.listed[pb], 1) == 0) p.list[atomicAdd(&p.counters[0], 1)] = pb;
+}
+
+// Second: CTA (block of the list, slice of the pairs).
+__global__ void __launch_bounds__(kThreads) write_listed_kernel(const BlockWriteParams p) {
+    pdl_trigger();
+    pdl_wait();
+    __shared__ int32_t writer[kMaxBlock];
+    __shared__ int2 members[kMaxBlock];
+    __shared__ int warp_count[kWarps];
+    __shared__ int last;
+    const int B = p.block_size, count = p.counters[0];
+    for (int b = blockIdx.x; b < count; b += gridDim.x) {
+        const int pb = p.list[b];
+        int32_t* w = p.writer + (size_t)pb * B;
+        for (int i = threadIdx.x; i < B; i += kThreads) writer[i] = w[i];
+        __syncthreads();
+        // the last of the block's grid.y CTAs to have read its writers clears them for the next call
+        if (threadIdx.x == 0) {
+            __threadfence();
+            last = atomicAdd(&p.finished[pb], 1) == (int)gridDim.y - 1;
+        }
+        const int n = gather_members(writer, B, members, warp_count);
+        if (last) {
+            for (int i = threadIdx.x; i < B; i += kThreads) w[i] = 0;
+            if (threadIdx.x == 0) {
+                p.finished[pb] = 0;
+                p.listed[pb] = 0;
+                p.list[b] = 0;
+            }
+        }
+        for (int pair = blockIdx.y * kWarps + (threadIdx.x >> 5); pair < 2 * p.num_kv_heads;
+             pair += gridDim.y * kWarps)
+            store_rows(p, pb, pair, members, n, writer, writer[0] != 0, threadIdx.x & 31);
+        __syncthreads();  // writer and members are read until here
+    }
+    if (threadIdx.x == 0) {
+        __threadfence();
+        if (atomicAdd(&p.counters[1], 1) == (int)(gridDim.x * gridDim.y) - 1) {
+            atomicExch(&p.counters[0], 0);
+            atomicExch(&p.counters[1], 0);
+        }
+    }
+}
+
+// Read back: a CTA takes kReadTokens tokens, resolves them once, and its threads turn 16 codes at a time into
+// values (the product with the scale in float, rounded once to T).
+constexpr int kReadTokens = 8;
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads)
+    read_kernel(T* __restrict__ k_out, T* __restrict__ v_out, int num_tokens, int num_kv_heads, int head_dim,
+                const uint4* __restrict__ k_cache, const uint4* __restrict__ v_cache,
+                const float* __restrict__ k_scales, const float* __restrict__ v_scales, int num_blocks, int block_size,
+                const int32_t* __restrict__ block_tables, int num_seqs, int max_blocks_per_seq,
+                const int32_t* __restrict__ seq_idx, const int32_t* __restrict__ pos, int32_t* error_count) {
+    pdl_trigger();
+    pdl_wait();
+    __shared__ int s_block[kReadTokens], s_off[kReadTokens];
+    const int t0 = blockIdx.x * kReadTokens, nt = min(kReadTokens, num_tokens - t0);
+    if (threadIdx.x < nt) {
+        BlockWriteParams q = {};
+        q.block_tables = block_tables;
+        q.seq_idx = seq_idx;
+        q.pos = pos;
+        q.num_blocks = num_blocks;
+        q.block_size = block_size;
+        q.num_seqs = num_seqs;
+        q.max_blocks_per_seq = max_blocks_per_seq;
+        int off;
+        const int pb = resolve(q, t0 + threadIdx.x, off);
+        if (pb == -2) count_error(error_count);
+        s_block[threadIdx.x] = pb;
+        s_off[threadIdx.x] = off;
+    }
+    __syncthreads();
+    const int per_head = head_dim / 16, pieces = num_kv_heads * per_head, total = 2 * nt * pieces;
+#pragma unroll 4
+    for (int i = threadIdx.x; i < total; i += kThreads) {
+        const int row = i / pieces, c = i - row * pieces, t = row >> 1;
+        const bool v_side = row & 1;
+        const int pb = s_block[t];
+        if (pb < 0) continue;
+        const uint4 x = __ldg((v_side ? v_cache : k_cache) + ((size_t)pb * block_size + s_off[t]) * pieces + c);
+        const float s = __ldg((v_side ? v_scales : k_scales) + (size_t)pb * num_kv_heads + c / per_head);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        __align__(16) T y[16];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float2 f = e4m3x2_to_float2((uint16_t)(w[k >> 1] >> (16 * (k & 1))));
+            y[2 * k] = from_float<T>(__fmul_rn(f.x, s));
+            y[2 * k + 1] = from_float<T>(__fmul_rn(f.y, s));
+        }
+        uint4* dst = reinterpret_cast<uint4*>((v_side ? v_out : k_out) + ((size_t)(t0 + t) * pieces + c) * 16);
+#pragma unroll
+        for (int k = 0; k < (int)sizeof(T); ++k) dst[k] = reinterpret_cast<const uint4*>(y)[k];
+    }
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+struct WriteWorkspace {
+    size_t listed, finished, writer, list, total;
+};
+WriteWorkspace write_workspace(int num_tokens, int num_blocks, int block_size) {
+    WriteWorkspace w;
+    w.listed = 256;
+    w.finished = w.listed + up256((size_t)num_blocks * 4);
+    w.writer = w.finished + up256((size_t)num_blocks * 4);
+    w.list = w.writer + up256((size_t)num_blocks * block_size * 4);
+    w.total = w.list + up256((size_t)(num_tokens < num_blocks ? num_tokens : num_blocks) * 4);
+    return w;
+}
+
+}  // namespace
+
+size_t write_fp8_block_workspace(int num_tokens, int num_blocks, int block_size) {
+    return num_tokens <= kScanTokens ? 0 : write_workspace(num_tokens, num_blocks, block_size).total;
+}
+
+int launch_write_fp8_block(const void* k_new, const void* v_new, int num_tokens, int num_kv_heads, int head_dim,
+                           void* k_cache, void* v_cache, float* k_scales, float* v_scales, int num_blocks,
+                           int block_size, const int32_t* block_tables, int num_seqs, int max_blocks_per_seq,
+                           const int32_t* seq_idx, const int32_t* pos, int64_t* slot_mapping, void* workspace,
+                           int num_sms, int32_t* error_count, cudaStream_t stream) {
+    BlockWriteParams p = {};
+    p.k_new = static_cast<const uint4*>(k_new);
+    p.v_new = static_cast<const uint4*>(v_new);
+    p.k_cache = static_cast<uint8_t*>(k_cache);
+    p.v_cache = static_cast<uint8_t*>(v_cache);
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.block_tables = block_tables;
+    p.seq_idx = seq_idx;
+    p.pos = pos;
+    p.slots = slot_mapping;
+    p.error_count = error_count;
+    p.num_tokens = num_tokens;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.num_seqs = num_seqs;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    const int slices = (2 * num_kv_heads + kWarps - 1) / kWarps;
+    const int gy = slices < 64 ? slices : 64;
+    if (num_tokens <= kScanTokens)
+        return launch_kernel(write_scan_kernel, dim3(num_tokens, gy), dim3(kThreads), 0, stream, p);
+    const WriteWorkspace w = write_workspace(num_tokens, num_blocks, block_size);
+    char* ws = static_cast<char*>(workspace);
+    p.counters = reinterpret_cast<int32_t*>(ws);
+    p.listed = reinterpret_cast<int32_t*>(ws + w.listed);
+    p.finished = reinterpret_cast<int32_t*>(ws + w.finished);
+    p.writer = reinterpret_cast<int32_t*>(ws + w.writer);
+    p.list = reinterpret_cast<int32_t*>(ws + w.list);
+    const int rc = launch_kernel(write_list_kernel, dim3((num_tokens + kThreads - 1) / kThreads), dim3(kThreads), 0,
+                                 stream, p);
+    if (rc != PA_OK) return rc;
+    const int most = num_tokens < num_blocks ? num_tokens : num_blocks;
+    const int gx = most < 8 * num_sms ? most : 8 * num_sms;
+    return launch_kernel(write_listed_kernel, dim3(gx, gy), dim3(kThreads), 0, stream, p);
+}
+
+int launch_read_fp8_block(void* k_out, void* v_out, int num_tokens, int num_kv_heads, int head_dim, int dtype,
+                          const void* k_cache, const void* v_cache, const float* k_scales, const float* v_scales,
+                          int num_blocks, int block_size, const int32_t* block_tables, int num_seqs,
+                          int max_blocks_per_seq, const int32_t* seq_idx, const int32_t* pos, int32_t* error_count,
+                          cudaStream_t stream) {
+    const dim3 grid((num_tokens + kReadTokens - 1) / kReadTokens), block(kThreads);
+    const uint4 *kc = static_cast<const uint4*>(k_cache), *vc = static_cast<const uint4*>(v_cache);
+    if (dtype == PA_F32)
+        return launch_kernel(read_kernel<float>, grid, block, 0, stream, static_cast<float*>(k_out),
+                             static_cast<float*>(v_out), num_tokens, num_kv_heads, head_dim, kc, vc, k_scales,
+                             v_scales, num_blocks, block_size, block_tables, num_seqs, max_blocks_per_seq, seq_idx, pos,
+                             error_count);
+    return launch_kernel(read_kernel<__nv_bfloat16>, grid, block, 0, stream, static_cast<__nv_bfloat16*>(k_out),
+                         static_cast<__nv_bfloat16*>(v_out), num_tokens, num_kv_heads, head_dim, kc, vc, k_scales,
+                         v_scales, num_blocks, block_size, block_tables, num_seqs, max_blocks_per_seq, seq_idx, pos,
+                         error_count);
+}
+
+}  // namespace pa

@@ -1,0 +1,185 @@
+// pa_api_fp8_block.cu — C ABI of the e4m3 pools with a scale per (block, kv
+// head): argument checks and dispatch.  Like pa_api.cu, every entry point
+// validates on the host and launches nothing when a check fails.
+#include <cmath>
+#include <cstdint>
+
+#include "pa_internal.cuh"
+
+namespace pa {
+namespace {
+bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// Row shape of the write and the read back: 16-byte pieces of codes, blocks of at most 1024 slots.
+int rows_ok(int num_kv_heads, int head_dim, int block_size) {
+    if (num_kv_heads < 1 || head_dim < 1 || block_size < 1) return PA_ERR_INVALID_ARG;
+    if (head_dim % 16 != 0 || (long long)num_kv_heads * head_dim > (1 << 20) || block_size > 1024)
+        return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+size_t pa_write_fp8_block_workspace_size(int num_tokens, int num_blocks, int block_size) {
+    if (num_tokens < 0 || num_blocks < 0 || block_size < 1 || block_size > 1024) return 0;
+    return write_fp8_block_workspace(num_tokens, num_blocks, block_size);
+}
+
+int pa_write_kv_paged_fp8_block(const void* k_new, const void* v_new, int num_tokens, int num_kv_heads, int head_dim,
+                                void* k_cache, void* v_cache, float* k_scales, float* v_scales, int num_blocks,
+                                int block_size, const int32_t* block_tables, int num_seqs, int max_blocks_per_seq,
+                                const int32_t* seq_idx, const int32_t* pos, int64_t* slot_mapping, void* workspace,
+                                size_t workspace_bytes, int32_t* error_count, void* stream) {
+    if (num_tokens < 0 || num_blocks < 0 || num_seqs < 0 || max_blocks_per_seq < 0) return PA_ERR_INVALID_ARG;
+    int rc = rows_ok(num_kv_heads, head_dim, block_size);
+    if (rc != PA_OK) return rc;
+    if (num_tokens == 0) return PA_OK;
+    if (!k_new || !v_new || !k_cache || !v_cache || !k_scales || !v_scales || !seq_idx || !pos ||
+        (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+        return PA_ERR_UNSUPPORTED;
+    int num_sms = 0;
+    if ((rc = check_device(&num_sms)) != PA_OK) return rc;
+    const size_t need = write_fp8_block_workspace(num_tokens, num_blocks, block_size);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return PA_ERR_WORKSPACE;
+    return launch_write_fp8_block(k_new, v_new, num_tokens, num_kv_heads, head_dim, k_cache, v_cache, k_scales,
+                                  v_scales, num_blocks, block_size, block_tables, num_seqs, max_blocks_per_seq,
+                                  seq_idx, pos, slot_mapping, workspace, num_sms, error_count,
+                                  static_cast<cudaStream_t>(stream));
+}
+
+int pa_read_kv_paged_fp8_block(void* k_out, void* v_out, int num_tokens, int num_kv_heads, int head_dim, int dtype,
+                               const void* k_cache, const void* v_cache, const float* k_scales, const float* v_scales,
+                               int num_blocks, int block_size, const int32_t* block_tables, int num_seqs,
+                               int max_blocks_per_seq, const int32_t* seq_idx, const int32_t* pos,
+                               int32_t* error_count, void* stream) {
+    if (num_tokens < 0 || num_blocks < 0 || num_seqs < 0 || max_blocks_per_seq < 0) return PA_ERR_INVALID_ARG;
+    int rc = rows_ok(num_kv_heads, head_dim, block_size);
+    if (rc != PA_OK) return rc;
+    if (dtype != PA_F32 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if (num_tokens == 0) return PA_OK;
+    if (!k_out || !v_out || !k_cache || !v_cache || !k_scales || !v_scales || !seq_idx || !pos ||
+        (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables))
+        return PA_ERR_INVALID_ARG;
+    if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
+        return PA_ERR_UNSUPPORTED;
+    if ((rc = check_device(nullptr)) != PA_OK) return rc;
+    return launch_read_fp8_block(k_out, v_out, num_tokens, num_kv_heads, head_dim, dtype, k_cache, v_cache, k_scales,
+                                 v_scales, num_blocks, block_size, block_tables, num_seqs, max_blocks_per_seq, seq_idx,
+                                 pos, error_count, static_cast<cudaStream_t>(stream));
+}
+
+size_t pa_decode_fp8_block_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                          int block_size, int max_context_len) {
+    return pa_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len);
+}
+
+int pa_decode_fp8_block(void* out, const void* q, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                        const void* k_cache, const void* v_cache, const float* k_scales, const float* v_scales,
+                        int num_blocks, int block_size, const int32_t* block_tables, int max_blocks_per_seq,
+                        const int32_t* context_lens, int max_context_len, float scale, void* workspace,
+                        size_t workspace_bytes, int32_t* error_count, void* stream) {
+    if (num_seqs < 0 || num_blocks < 0 || max_blocks_per_seq < 0 || max_context_len < 0) return PA_ERR_INVALID_ARG;
+    int rc = decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size);
+    if (rc != PA_OK) return rc;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !k_scales || !v_scales || !context_lens ||
+        (max_blocks_per_seq > 0 && !block_tables))
+        return PA_ERR_INVALID_ARG;
+    int num_sms = 0;
+    if ((rc = check_device(&num_sms)) != PA_OK) return rc;
+    const DecodePlan plan =
+        plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, num_sms, SIZE_MAX, 0, true);
+    const DecodeWorkspace lay =
+        decode_workspace_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, plan.max_splits);
+    if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return PA_ERR_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    DecodeParams p;
+    p.out = out;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.error_count = error_count;
+    p.work = reinterpret_cast<int*>(ws + lay.work);
+    p.ws_ml = reinterpret_cast<float2*>(ws + lay.ml);
+    p.ws_o = reinterpret_cast<float*>(ws + lay.o);
+    p.num_seqs = num_seqs;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.group = num_q_heads / num_kv_heads;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.max_context_len = max_context_len;
+    p.partition = plan.partition;
+    p.max_splits = plan.max_splits;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if ((rc = launch_decode_fp8_block_fma(p, st)) != PA_OK) return rc;
+    return launch_decode_merge(p, PA_BF16, num_sms, st);
+}
+
+size_t pa_prefill_fp8_block_workspace_size(int num_chunks, int total_q, int max_q_len, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int block_size, int max_context_len) {
+    (void)num_chunks; (void)total_q; (void)max_q_len; (void)num_q_heads; (void)num_kv_heads; (void)head_dim;
+    (void)block_size; (void)max_context_len;
+    return 0;
+}
+
+int pa_prefill_chunk_fp8_block(void* out, const void* q, const int32_t* cu_q_lens, const int32_t* q_start_pos,
+                               const int32_t* seq_of_chunk, int num_chunks, int total_q, int max_q_len, int num_seqs,
+                               int num_q_heads, int num_kv_heads, int head_dim, const void* k_cache,
+                               const void* v_cache, const float* k_scales, const float* v_scales, int num_blocks,
+                               int block_size, const int32_t* block_tables, int max_blocks_per_seq,
+                               const int32_t* context_lens, int max_context_len, float scale, void* workspace,
+                               size_t workspace_bytes, int32_t* error_count, void* stream) {
+    (void)workspace; (void)workspace_bytes;
+    if (num_chunks < 0 || total_q < 0 || max_q_len < 0 || num_seqs < 0 || num_blocks < 0 || max_blocks_per_seq < 0 ||
+        max_context_len < 0)
+        return PA_ERR_INVALID_ARG;
+    int rc = decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size);
+    if (rc != PA_OK) return rc;
+    if (num_chunks == 0 || total_q == 0 || max_q_len == 0) return PA_OK;
+    if (!out || !q || !cu_q_lens || !q_start_pos || !seq_of_chunk || !k_cache || !v_cache || !k_scales || !v_scales ||
+        !context_lens || !block_tables || num_seqs == 0)
+        return PA_ERR_INVALID_ARG;
+    if ((rc = check_device(nullptr)) != PA_OK) return rc;
+    PrefillParams p;
+    p.out = out;
+    p.q = q;
+    p.cu_q_lens = cu_q_lens;
+    p.q_start_pos = q_start_pos;
+    p.seq_of_chunk = seq_of_chunk;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.error_count = error_count;
+    p.num_chunks = num_chunks;
+    p.total_q = total_q;
+    p.max_q_len = max_q_len;
+    p.num_seqs = num_seqs;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.group = num_q_heads / num_kv_heads;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    return launch_prefill_fp8_block_fma(p, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

@@ -5,6 +5,7 @@
 
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 #include "pa.h"
@@ -122,6 +123,9 @@ struct DecodeParams {
     // kernel's queue ends with them, so the last items handed out are short); 1 << 30: none.
     int small_partition = 0, small_from = 1 << 30;
     float scale_log2;  // scale * log2(e): scores are kept in base-2 units
+    // e4m3 pools with a scale per (block, kv head) (pa_decode_fp8_block): float [num_blocks][num_kv_heads]
+    const float* k_scales = nullptr;
+    const float* v_scales = nullptr;
 };
 
 struct PrefillParams {
@@ -150,6 +154,9 @@ struct PrefillParams {
     float* part_o = nullptr;
     float2* part_ml = nullptr;
     int part_splits = 0;
+    // e4m3 pools with a scale per (block, kv head) (pa_prefill_chunk_fp8_block): float [num_blocks][num_kv_heads]
+    const float* k_scales = nullptr;
+    const float* v_scales = nullptr;
 };
 
 // Kernel launchers (defined in the .cu files).
@@ -169,6 +176,21 @@ int launch_write_kv_paged_fp8(const void* k_new, const void* v_new, int num_toke
                               const int32_t* seq_idx, const int32_t* pos, int block_size, int num_blocks,
                               int64_t* slot_mapping, float k_inv, float v_inv, int32_t* error_count,
                               cudaStream_t stream);
+// e4m3 pools with a scale per (block, kv head): the write (workspace bytes it needs, 0 for short calls), the read
+// back, and attention on the CUDA cores.
+size_t write_fp8_block_workspace(int num_tokens, int num_blocks, int block_size);
+int launch_write_fp8_block(const void* k_new, const void* v_new, int num_tokens, int num_kv_heads, int head_dim,
+                           void* k_cache, void* v_cache, float* k_scales, float* v_scales, int num_blocks,
+                           int block_size, const int32_t* block_tables, int num_seqs, int max_blocks_per_seq,
+                           const int32_t* seq_idx, const int32_t* pos, int64_t* slot_mapping, void* workspace,
+                           int num_sms, int32_t* error_count, cudaStream_t stream);
+int launch_read_fp8_block(void* k_out, void* v_out, int num_tokens, int num_kv_heads, int head_dim, int dtype,
+                          const void* k_cache, const void* v_cache, const float* k_scales, const float* v_scales,
+                          int num_blocks, int block_size, const int32_t* block_tables, int num_seqs,
+                          int max_blocks_per_seq, const int32_t* seq_idx, const int32_t* pos, int32_t* error_count,
+                          cudaStream_t stream);
+int launch_decode_fp8_block_fma(const DecodeParams& p, cudaStream_t stream);
+int launch_prefill_fp8_block_fma(const PrefillParams& p, cudaStream_t stream);
 int launch_copy_blocks(void* k_cache, void* v_cache, int num_blocks, int block_size, int row_bytes,
                        const int32_t* src, const int32_t* dst, const int32_t* num_valid, int num_copies,
                        int32_t* error_count, cudaStream_t stream);
@@ -222,6 +244,19 @@ __device__ __forceinline__ uint32_t e4m3x4_of_bf16x4(uint2 x, float inv) {
                                    __fmul_rn(__uint_as_float(x.y & 0xFFFF0000u), inv));
     return (uint32_t)a | ((uint32_t)b << 16);
 }
+
+// Two e4m3 codes (low byte first) as floats; exact (an e4m3 value is an f16 value), NaN for the NaN codes.
+__device__ __forceinline__ float2 e4m3x2_to_float2(uint16_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(codes));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+// An element of an e4m3 pool.
+struct e4m3_t {
+    uint8_t code;
+};
+__device__ __forceinline__ float to_float(e4m3_t x) { return e4m3x2_to_float2(x.code).x; }
 
 __device__ __forceinline__ void count_error(int32_t* error_count, int n = 1) {
     if (error_count != nullptr && n != 0) atomicAdd(error_count, n);

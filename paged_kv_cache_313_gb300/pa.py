@@ -22,7 +22,9 @@ SYMBOLS = ("pa_version", "pa_status_string", "pa_last_cuda_error", "pa_slot_mapp
            "pa_write_kv_paged", "pa_write_kv_paged_fp8", "pa_decode_workspace_size", "pa_decode_plan", "pa_decode", "pa_decode_fp8", "pa_decode_write",
            "pa_decode_write_fp8",
            "pa_decode_cascade_workspace_size", "pa_decode_cascade", "pa_decode_noalloc", "pa_prefill_workspace_size",
-           "pa_prefill_chunk", "pa_copy_blocks", "pa_map_to_kernel_blocks", "pa_stage_copy",
+           "pa_prefill_chunk", "pa_write_fp8_block_workspace_size", "pa_write_kv_paged_fp8_block",
+           "pa_read_kv_paged_fp8_block", "pa_decode_fp8_block_workspace_size", "pa_decode_fp8_block",
+           "pa_prefill_fp8_block_workspace_size", "pa_prefill_chunk_fp8_block", "pa_copy_blocks", "pa_map_to_kernel_blocks", "pa_stage_copy",
            "pa_check_bounded_wait")
 
 
@@ -60,6 +62,15 @@ _SIGNATURES = {
     "pa_prefill_workspace_size": ([_i, _i, _i, _i, _i, _i], _sz),
     "pa_prefill_chunk": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _p, _p, _i, _i, _p, _i, _p, _f, _p,
                           _sz, _p, _p], _i),
+    "pa_write_fp8_block_workspace_size": ([_i, _i, _i], _sz),
+    "pa_write_kv_paged_fp8_block": ([_p, _p, _i, _i, _i, _p, _p, _p, _p, _i, _i, _p, _i, _i, _p, _p, _p, _p, _sz, _p,
+                                     _p], _i),
+    "pa_read_kv_paged_fp8_block": ([_p, _p, _i, _i, _i, _i, _p, _p, _p, _p, _i, _i, _p, _i, _i, _p, _p, _p, _p], _i),
+    "pa_decode_fp8_block_workspace_size": ([_i, _i, _i, _i, _i, _i], _sz),
+    "pa_decode_fp8_block": ([_p, _p, _i, _i, _i, _i, _p, _p, _p, _p, _i, _i, _p, _i, _p, _i, _f, _p, _sz, _p, _p], _i),
+    "pa_prefill_fp8_block_workspace_size": ([_i, _i, _i, _i, _i, _i, _i, _i], _sz),
+    "pa_prefill_chunk_fp8_block": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _p, _p, _p, _p, _i, _i, _p, _i,
+                                    _p, _i, _f, _p, _sz, _p, _p], _i),
     "pa_stage_copy": ([_p, _p, _sz, _p], _i),
     "pa_check_bounded_wait": ([_i, _i, _p, _p, _p], _i),
     "pa_map_to_kernel_blocks": ([_p, _i, _i, _i, _p, _i, _p], _i),
@@ -375,6 +386,164 @@ def pa_prefill_chunk(q, cu_q_lens, q_start_pos, seq_of_chunk, max_q_len: int, k_
         _dev(v_cache, "v_cache", q.dtype), P, B, _dev(block_tables, "block_tables", torch.int32),
         block_tables.shape[1], _dev(context_lens, "context_lens", torch.int32), float(scale), ws_ptr, ws_bytes,
         _dev(error_count, "error_count", torch.int32), _stream(stream)))
+    return out
+
+
+def _fp8_block_pools(k_cache, v_cache, k_scales, v_scales):
+    """Shapes of e4m3 pools with a scale per (block, kv head): (P, B, Hkv, D), checked."""
+    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8:
+        raise TypeError("fp8 pools are uint8 tensors of e4m3 codes")
+    P, B, H, D = k_cache.shape
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("shapes of k_cache and v_cache differ")
+    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+        if tuple(t.shape) != (P, H):
+            raise ValueError(f"{name} must be [num_blocks, num_kv_heads] = [{P}, {H}], got {list(t.shape)}")
+    return P, B, H, D
+
+
+def _same_device(first, **others):
+    """Every given tensor is on `first`'s device (or, an output, in pinned host memory)."""
+    for name, t in others.items():
+        if t is not None and t.is_cuda and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, the pools on {first.device}")
+
+
+def _ws(workspace):
+    if workspace is None:
+        return None, 0
+    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+
+
+def new_write_fp8_block_workspace(num_tokens, num_blocks, block_size, device=None) -> torch.Tensor | None:
+    """A zeroed workspace for pa_write_kv_paged_fp8_block calls of up to num_tokens tokens (None when they need none)."""
+    n = int(lib().pa_write_fp8_block_workspace_size(int(num_tokens), int(num_blocks), int(block_size)))
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda") if n else None
+
+
+def pa_write_kv_paged_fp8_block(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, seq_idx, pos,
+                                workspace=None, slot_mapping=None, error_count=None, stream=None):
+    """Slot mapping and a quantising K/V write into uint8 e4m3 pools with a scale per (block, kv head), chosen by the
+    write: the smallest power of two that holds the rows stored into the block, never below the block's scale from
+    before unless the block's first slot is stored; the block's other codes keep their values."""
+    T, H, D = k_new.shape
+    P, B, H2, D2 = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
+    if (H, D) != (H2, D2) or v_new.shape != k_new.shape:
+        raise ValueError("shapes of k_new, v_new and the pools disagree")
+    if seq_idx.numel() != T or pos.numel() != T or (slot_mapping is not None and slot_mapping.numel() != T):
+        raise ValueError(f"seq_idx, pos and slot_mapping must have one entry for each of the {T} tokens")
+    _same_device(k_cache, k_new=k_new, v_new=v_new, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
+                 block_tables=block_tables, seq_idx=seq_idx, pos=pos, workspace=workspace, slot_mapping=slot_mapping,
+                 error_count=error_count)
+    S, W = block_tables.shape
+    ws, ws_bytes = _ws(workspace)
+    with torch.cuda.device(k_cache.device):
+        _check("pa_write_kv_paged_fp8_block", lib().pa_write_kv_paged_fp8_block(
+            _dev(k_new, "k_new", torch.bfloat16), _dev(v_new, "v_new", torch.bfloat16), T, H, D,
+            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(k_scales, "k_scales", torch.float32),
+            _dev(v_scales, "v_scales", torch.float32), P, B, _dev(block_tables, "block_tables", torch.int32), S, W,
+            _dev(seq_idx, "seq_idx", torch.int32), _dev(pos, "pos", torch.int32),
+            _dev(slot_mapping, "slot_mapping", torch.int64), ws, ws_bytes,
+            _dev(error_count, "error_count", torch.int32), _stream(stream)))
+    return slot_mapping
+
+
+def pa_read_kv_paged_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables, seq_idx, pos, k_out=None,
+                               v_out=None, dtype=torch.bfloat16, error_count=None, stream=None):
+    """(K rows, V rows), each [T, Hkv, D] of `dtype` (bfloat16 or float32): code * scale of the token at pos[t] of
+    sequence seq_idx[t].  Rows with pos < 0 or an invalid index are left as they were (uninitialised where no k_out /
+    v_out is given)."""
+    P, B, H, D = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
+    T = seq_idx.numel()
+    if pos.numel() != T:
+        raise ValueError("seq_idx and pos differ in length")
+    k_out = torch.empty(T, H, D, dtype=dtype, device=k_cache.device) if k_out is None else k_out
+    v_out = torch.empty(T, H, D, dtype=k_out.dtype, device=k_cache.device) if v_out is None else v_out
+    if tuple(k_out.shape) != (T, H, D) or tuple(v_out.shape) != (T, H, D) or v_out.dtype != k_out.dtype:
+        raise ValueError(f"k_out and v_out must be [{T}, {H}, {D}] of one dtype")
+    _same_device(k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales, block_tables=block_tables,
+                 seq_idx=seq_idx, pos=pos, k_out=k_out, v_out=v_out, error_count=error_count)
+    S, W = block_tables.shape
+    with torch.cuda.device(k_cache.device):
+        _check("pa_read_kv_paged_fp8_block", lib().pa_read_kv_paged_fp8_block(
+            _dev(k_out, "k_out"), _dev(v_out, "v_out"), T, H, D, _dtype_code(k_out), _dev(k_cache, "k_cache"),
+            _dev(v_cache, "v_cache"), _dev(k_scales, "k_scales", torch.float32),
+            _dev(v_scales, "v_scales", torch.float32), P, B, _dev(block_tables, "block_tables", torch.int32), S, W,
+            _dev(seq_idx, "seq_idx", torch.int32), _dev(pos, "pos", torch.int32),
+            _dev(error_count, "error_count", torch.int32), _stream(stream)))
+    return k_out, v_out
+
+
+def new_decode_fp8_block_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                                   device=None) -> torch.Tensor:
+    """A zeroed workspace of the size pa_decode_fp8_block needs (reusable across calls on one stream)."""
+    n = int(lib().pa_decode_fp8_block_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                     max_context_len))
+    if n == 0:
+        raise PaError("pa_decode_fp8_block_workspace_size", PA_ERR_UNSUPPORTED, "unsupported sizes or device")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, max_context_len: int,
+                        scale: float, workspace, out=None, error_count=None, stream=None) -> torch.Tensor:
+    """pa_decode over uint8 e4m3 pools with a scale per (block, kv head); q and out bf16."""
+    N, Hq, D = q.shape
+    P, B, Hkv, D2 = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
+    if D2 != D:
+        raise ValueError("head_dim of q and k_cache differ")
+    if out is None:
+        out = torch.empty_like(q)
+    if out.shape != q.shape or block_tables.shape[0] != N or context_lens.numel() != N:
+        raise ValueError("shapes of q, out, block_tables and context_lens disagree")
+    _same_device(k_cache, q=q, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales, block_tables=block_tables,
+                 context_lens=context_lens, workspace=workspace, out=out, error_count=error_count)
+    ws, ws_bytes = _ws(workspace)
+    with torch.cuda.device(k_cache.device):
+        _check("pa_decode_fp8_block", lib().pa_decode_fp8_block(
+            _dev(out, "out", torch.bfloat16, host_ok=True), _dev(q, "q", torch.bfloat16), N, Hq, Hkv, D,
+            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(k_scales, "k_scales", torch.float32),
+            _dev(v_scales, "v_scales", torch.float32), P, B, _dev(block_tables, "block_tables", torch.int32),
+            block_tables.shape[1], _dev(context_lens, "context_lens", torch.int32), int(max_context_len),
+            float(scale), ws, ws_bytes, _dev(error_count, "error_count", torch.int32), _stream(stream)))
+    return out
+
+
+def new_prefill_fp8_block_workspace(num_chunks, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                                    max_context_len, device=None) -> torch.Tensor | None:
+    """A workspace of the size pa_prefill_chunk_fp8_block needs for these sizes (None when it needs none)."""
+    n = int(lib().pa_prefill_fp8_block_workspace_size(num_chunks, total_q, max_q_len, num_q_heads, num_kv_heads,
+                                                      head_dim, block_size, max_context_len))
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda") if n else None
+
+
+def pa_prefill_chunk_fp8_block(q, cu_q_lens, q_start_pos, seq_of_chunk, max_q_len: int, k_cache, v_cache, k_scales,
+                               v_scales, block_tables, context_lens, max_context_len: int, scale: float,
+                               workspace=None, out=None, error_count=None, stream=None) -> torch.Tensor:
+    """Causal chunked-prefill attention over uint8 e4m3 pools with a scale per (block, kv head); q and out bf16."""
+    T, Hq, D = q.shape
+    P, B, Hkv, D2 = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
+    if D2 != D:
+        raise ValueError("head_dim of q and k_cache differ")
+    C = q_start_pos.numel()
+    if out is None:
+        out = torch.empty_like(q)
+    if out.shape != q.shape or cu_q_lens.numel() != C + 1 or seq_of_chunk.numel() != C:
+        raise ValueError("shapes of q, out, cu_q_lens, q_start_pos and seq_of_chunk disagree")
+    if context_lens.numel() != block_tables.shape[0]:
+        raise ValueError("shapes of block_tables and context_lens disagree")
+    _same_device(k_cache, q=q, cu_q_lens=cu_q_lens, q_start_pos=q_start_pos, seq_of_chunk=seq_of_chunk,
+                 v_cache=v_cache, k_scales=k_scales, v_scales=v_scales, block_tables=block_tables,
+                 context_lens=context_lens, workspace=workspace, out=out, error_count=error_count)
+    ws, ws_bytes = _ws(workspace)
+    with torch.cuda.device(k_cache.device):
+        _check("pa_prefill_chunk_fp8_block", lib().pa_prefill_chunk_fp8_block(
+            _dev(out, "out", torch.bfloat16, host_ok=True), _dev(q, "q", torch.bfloat16),
+            _dev(cu_q_lens, "cu_q_lens", torch.int32), _dev(q_start_pos, "q_start_pos", torch.int32),
+            _dev(seq_of_chunk, "seq_of_chunk", torch.int32), C, T, int(max_q_len), block_tables.shape[0], Hq, Hkv, D,
+            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(k_scales, "k_scales", torch.float32),
+            _dev(v_scales, "v_scales", torch.float32), P, B, _dev(block_tables, "block_tables", torch.int32),
+            block_tables.shape[1], _dev(context_lens, "context_lens", torch.int32), int(max_context_len),
+            float(scale), ws, ws_bytes, _dev(error_count, "error_count", torch.int32), _stream(stream)))
     return out
 
 

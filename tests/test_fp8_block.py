@@ -1,0 +1,492 @@
+"""e4m3 pools with a scale per (block, kv head): the quantising write, the read back, decode and chunked prefill,
+against a float64 reference (tests/fp8_block_reference.py).
+
+Write and read back are bit-exact.  Attention: an output is off by at most its own rounding to bf16, 2^-8 |out|; by
+the rounding of the probabilities to bf16-like precision (two e4m3 terms: 2^-4 of a half step's 2^-4), 2^-8 of
+sum_j p_j |v_j|; and by the float32 products, exponentials and sums, for which 2^-10 of that sum leaves room (scores
+below about 64 in magnitude, rounded to 2^-24 of their terms' sum, plus 2^-20 of the largest query element)."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_block_reference as R
+from paged_kv_cache_313_gb300 import build as pa_build
+from paged_kv_cache_313_gb300 import pa
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def lib():
+    pa_build.build()
+    return pa.lib()
+
+
+def _i32(a):
+    return torch.as_tensor(np.asarray(a), dtype=torch.int32).cuda()
+
+
+def _bf16(rng, shape, gain=1.0):
+    return torch.from_numpy((rng.standard_normal(shape) * gain).astype(np.float32)).to(BF)
+
+
+def _tables(rng, lens, block, spare=3, width=None):
+    """Shuffled block table [S, width] for the lengths, -1 beyond, and the number of blocks of the pool."""
+    n = [-(-L // block) for L in lens]
+    P = sum(n) + spare
+    perm = rng.permutation(P)
+    t = np.full((len(lens), max(1, width or max(n, default=1))), -1, np.int32)
+    at = 0
+    for s, k in enumerate(n):
+        t[s, :k] = perm[at:at + k]
+        at += k
+    return t, P
+
+
+def _pools(rng, P, block, H, D, pow2=True):
+    """Random codes (no NaN) and scales that differ by block and head."""
+    codes = rng.integers(0, 0x7f, (P, block, H, D), dtype=np.uint8) | (rng.integers(0, 2, (P, block, H, D), dtype=np.uint8) << 7)
+    # magnitudes about 1: most codes' exponents near the middle
+    codes = np.where(rng.random(codes.shape) < 0.97, codes & 0x87 | (rng.integers(4, 9, codes.shape, dtype=np.uint8) << 3),
+                     codes).astype(np.uint8)
+    codes[(codes & 0x7f) == 0x7f] = 0x38
+    scales = 2.0 ** rng.integers(-4, 2, (P, H)).astype(np.float64)
+    if not pow2:
+        scales *= 1 + rng.random((P, H))
+    return codes, scales.astype(np.float32)
+
+
+# ---------------------------------------------------------------- CPU: refusals
+def test_refusals_need_no_device(lib):
+    P16 = ctypes.c_void_p(16)
+    w = lambda *a: lib.pa_write_kv_paged_fp8_block(*a)  # noqa: E731
+    ok = [P16, P16, 4, 8, 128, P16, P16, P16, P16, 10, 16, P16, 2, 4, P16, P16, None, None, 0, None, None]
+    bad = [(2, -1, 1), (3, 0, 1), (4, 0, 1), (4, 24, 2), (9, -1, 1), (10, 0, 1), (10, 1025, 2), (12, -1, 1),
+           (0, None, 1), (5, None, 1), (7, None, 1), (8, None, 1), (11, None, 1), (14, None, 1), (15, None, 1),
+           (0, ctypes.c_void_p(8), 2), (6, ctypes.c_void_p(24), 2), (3, 1 << 17, 2)]
+    for i, value, want in bad:
+        a = list(ok)
+        a[i] = value
+        assert w(*a) == want, (i, value)
+    a = list(ok)
+    a[2] = 0
+    assert w(*a) == pa.PA_OK
+    r_ok = [P16, P16, 4, 8, 128, pa.PA_BF16, P16, P16, P16, P16, 10, 16, P16, 2, 4, P16, P16, None, None]
+    for i, value, want in [(2, -1, 1), (5, 7, 2), (4, 8, 2), (11, 0, 1), (0, None, 1), (8, None, 1), (1, ctypes.c_void_p(4), 2)]:
+        a = list(r_ok)
+        a[i] = value
+        assert lib.pa_read_kv_paged_fp8_block(*a) == want, (i, value)
+    f = ctypes.c_float(1.0)
+    d_ok = [P16, P16, 2, 8, 2, 128, P16, P16, P16, P16, 10, 16, P16, 4, P16, 64, f, P16, 0, None, None]
+    for i, value, want in [(2, -1, 1), (3, 7, 1), (3, 34, 2), (5, 96, 2), (11, 0, 2), (11, 2048, 2), (15, -1, 1),
+                           (8, None, 1), (9, None, 1), (0, None, 1), (14, None, 1)]:
+        a = list(d_ok)
+        a[i] = value
+        assert lib.pa_decode_fp8_block(*a) == want, (i, value)
+    p_ok = [P16, P16, P16, P16, P16, 1, 4, 4, 1, 8, 2, 128, P16, P16, P16, P16, 10, 16, P16, 4, P16, 64, f, None, 0,
+            None, None]
+    for i, value, want in [(5, -1, 1), (6, -1, 1), (7, -1, 1), (9, 7, 1), (11, 96, 2), (17, 2048, 2), (21, -1, 1),
+                           (8, 0, 1), (14, None, 1), (2, None, 1), (20, None, 1)]:
+        a = list(p_ok)
+        a[i] = value
+        assert lib.pa_prefill_chunk_fp8_block(*a) == want, (i, value)
+    assert lib.pa_write_fp8_block_workspace_size(1024, 100, 16) == 0
+    assert lib.pa_write_fp8_block_workspace_size(1025, 100, 16) > 100 * 16 * 4
+    assert lib.pa_write_fp8_block_workspace_size(-1, 100, 16) == 0
+
+
+def test_binding_refuses_mismatched_arguments(lib):
+    kc = torch.zeros(4, 16, 2, 128, dtype=torch.uint8)
+    sc = torch.ones(4, 2)
+    bt = torch.zeros(1, 4, dtype=torch.int32)
+    i = torch.zeros(3, dtype=torch.int32)
+    kn = torch.zeros(3, 2, 128, dtype=BF)
+    q = torch.zeros(1, 4, 128, dtype=BF)
+    with pytest.raises(ValueError):  # not CUDA tensors
+        pa.pa_write_kv_paged_fp8_block(kn, kn, kc, kc, sc, sc, bt, i, i)
+    with pytest.raises(TypeError):
+        pa.pa_write_kv_paged_fp8_block(kn, kn, kc.to(BF), kc.to(BF), sc, sc, bt, i, i)
+    with pytest.raises(ValueError, match="k_scales"):
+        pa.pa_write_kv_paged_fp8_block(kn, kn, kc, kc, sc[:, :1], sc, bt, i, i)
+    with pytest.raises(ValueError, match="one entry"):
+        pa.pa_write_kv_paged_fp8_block(kn, kn, kc, kc, sc, sc, bt, i[:2], i)
+    with pytest.raises(ValueError, match="disagree"):
+        pa.pa_write_kv_paged_fp8_block(kn[:, :1], kn[:, :1], kc, kc, sc, sc, bt, i, i)
+    with pytest.raises(ValueError, match="differ"):
+        pa.pa_read_kv_paged_fp8_block(kc, kc, sc, sc, bt, i, i[:2])
+    with pytest.raises(ValueError, match="one dtype"):
+        pa.pa_read_kv_paged_fp8_block(kc, kc, sc, sc, bt, i, i, k_out=kn[:2])
+    with pytest.raises(ValueError, match="head_dim"):
+        pa.pa_decode_fp8_block(q[..., :64], kc, kc, sc, sc, bt, i[:1], 64, 1.0, None)
+    with pytest.raises(ValueError, match="disagree"):
+        pa.pa_decode_fp8_block(q, kc, kc, sc, sc, bt, i, 64, 1.0, None)
+    with pytest.raises(ValueError, match="disagree"):
+        pa.pa_prefill_chunk_fp8_block(q, i, i[:1], i[:1], 1, kc, kc, sc, sc, bt, i[:1], 64, 1.0)
+
+
+def test_reference_codes_match_the_c_oracle():
+    import oracle
+    for c in range(256):
+        want = oracle.e4m3_value(c)
+        assert (np.isnan(want) and np.isnan(R.E4M3[c])) or want == R.E4M3[c]
+    rng = np.random.default_rng(0)
+    x = np.concatenate([rng.standard_normal(400) * 10.0 ** rng.integers(-4, 4, 400), R.E4M3[np.isfinite(R.E4M3)],
+                        [0.0, -0.0, 448.0, 464.0, 1e9, 2.0 ** -10, 3 * 2.0 ** -10, 17.0, 19.0]]).astype(np.float32)
+    got = R.nearest_code(x.astype(np.float64))
+    assert [int(g) for g in got] == [oracle.e4m3_encode(float(v)) for v in x]
+
+
+# ---------------------------------------------------------------- GPU: write and read back
+def _check_write(kn, vn, codes, scales, table, seq, pos, steps=1, ws_tokens=None):
+    """The write against the reference, bit for bit: codes, scales, slots and errors."""
+    P, B, H, D = codes[0].shape
+    kc, vc = (torch.from_numpy(c.copy()).cuda() for c in codes)
+    ks, vs = (torch.from_numpy(s.copy()).cuda() for s in scales)
+    T = len(seq)
+    slot = torch.full((T,), -7, dtype=torch.int64, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = pa.new_write_fp8_block_workspace(ws_tokens or T, P, B)
+    for _ in range(steps):
+        pa.pa_write_kv_paged_fp8_block(kn.cuda(), vn.cuda(), kc, vc, ks, vs, _i32(table), _i32(seq), _i32(pos), ws,
+                                       slot_mapping=slot, error_count=err)
+    want_slot, want_err = R.slots(table, seq, pos, B, P)
+    assert np.array_equal(slot.cpu().numpy(), want_slot)
+    assert int(err.item()) == want_err * steps
+    for new, c, s, gc, gs in ((kn, codes[0], scales[0], kc, ks), (vn, codes[1], scales[1], vc, vs)):
+        c, s = c.copy(), s.astype(np.float64)
+        for _ in range(steps):
+            R.write(new.double().numpy(), c, s, want_slot)
+        assert np.array_equal(gs.cpu().numpy().astype(np.float64), s)
+        got = gc.cpu().numpy()
+        both_nan = ((got & 0x7f) == 0x7f) & ((c & 0x7f) == 0x7f)
+        assert np.array_equal(np.where(both_nan, 0, got), np.where(both_nan, 0, c))
+    if ws is not None:
+        assert int(torch.count_nonzero(ws)) == 0, "the workspace is left zeroed"
+    return kc, vc, ks, vs
+
+
+WRITE_SHAPES = [(8, 128, 16), (1, 128, 16), (2, 64, 8), (3, 48, 5), (4, 16, 1), (2, 128, 64), (1, 32, 1024), (5, 112, 33)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("H,D,B", WRITE_SHAPES)
+@pytest.mark.parametrize("T", [1, 2, 37, 300])
+def test_write_matches_reference(H, D, B, T):
+    """Chunks that begin inside blocks, in shuffled order, with padding and bad indices among them."""
+    rng = np.random.default_rng(100 * H + D + B + T)
+    S = min(T, 4)
+    first = rng.integers(0, 2 * B + 3, S)
+    counts = [T // S + (i < T % S) for i in range(S)]
+    lens = [int(f + c) for f, c in zip(first, counts)]
+    table, P = _tables(rng, lens, B)
+    seq = np.concatenate([[s] * c for s, c in enumerate(counts)]).astype(np.int32)
+    pos = np.concatenate([np.arange(f, f + c) for f, c in zip(first, counts)]).astype(np.int32)
+    if T >= 37:
+        pos[3], seq[5], seq[6], pos[7] = -1, -1, S, 10 ** 6
+        table[0, 0] = P  # no such block
+    order = rng.permutation(T)
+    seq, pos = seq[order], pos[order]
+    codes, scales = zip(_pools(rng, P, B, H, D), _pools(rng, P, B, H, D))
+    gain = 10.0 ** rng.integers(-3, 3, (T, H, 1))
+    _check_write(_bf16(rng, (T, H, D), gain), _bf16(rng, (T, H, D), gain[::-1]), codes, scales, table, seq, pos)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,B", [(1024, 16), (1025, 16), (2500, 64), (3001, 7), (1100, 1024)])
+def test_write_long_calls_match_reference(T, B):
+    """Both forms around the length where the second takes over; the workspace made for more tokens."""
+    rng = np.random.default_rng(T + B)
+    H, D, S = 2, 128, 5
+    first = rng.integers(0, 40, S)
+    counts = [T // S + (i < T % S) for i in range(S)]
+    table, P = _tables(rng, [int(f + c) for f, c in zip(first, counts)], B)
+    seq = np.concatenate([[s] * c for s, c in enumerate(counts)]).astype(np.int32)
+    pos = np.concatenate([np.arange(f, f + c) for f, c in zip(first, counts)]).astype(np.int32)
+    pos[11], seq[13] = -5, 99
+    order = rng.permutation(T) if B != 16 else np.arange(T)
+    codes, scales = zip(_pools(rng, P, B, H, D), _pools(rng, P, B, H, D))
+    _check_write(_bf16(rng, (T, H, D)), _bf16(rng, (T, H, D), 30.0), codes, scales, table, seq[order], pos[order],
+                 ws_tokens=T + 500)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T", [40, 1500])
+def test_write_same_slot_last_token_is_stored(T):
+    rng = np.random.default_rng(T)
+    table, P = _tables(rng, [T], 16)
+    pos = rng.integers(0, T // 3, T).astype(np.int32)
+    codes, scales = zip(_pools(rng, P, 16, 2, 64), _pools(rng, P, 16, 2, 64))
+    _check_write(_bf16(rng, (T, 2, 64)), _bf16(rng, (T, 2, 64)), codes, scales, table, np.zeros(T, np.int32), pos)
+
+
+@pytest.mark.gpu
+def test_write_special_values():
+    """Zeros, infinities, NaN, subnormals and the largest numbers; a block of zeros only; scales of 0 and old scales
+    that are no power of two."""
+    rng = np.random.default_rng(3)
+    H, D, B, T = 4, 32, 8, 24
+    table, P = _tables(rng, [T + 3], B)
+    kn = _bf16(rng, (T, H, D))
+    kn[0, 0, 0], kn[1, 0, 1], kn[2, 0, 2] = float("inf"), float("-inf"), float("nan")
+    kn[:, 1] = 0.0
+    kn[:, 2] = float("nan")
+    kn[3, 3, 3] = 3e38
+    kn[9, 3, :] = 1e-39  # subnormal in bf16
+    vn = torch.full((T, H, D), 1.0).to(BF) * torch.tensor([448.0, 449.0, 450.0, 2.0 ** -140]).to(BF)[None, :, None]
+    codes, scales = zip(_pools(rng, P, B, H, D), _pools(rng, P, B, H, D, pow2=False))
+    scales[0][:, 2:] = 0.0
+    _check_write(kn, vn, codes, scales, table, np.zeros(T, np.int32), np.arange(3, T + 3, dtype=np.int32))
+
+
+@pytest.mark.gpu
+def test_write_token_by_token_keeps_earlier_values():
+    """A block that grows token by token, each larger than all before: earlier tokens keep their values up to e4m3's
+    subnormals under the last scale, and a block that is used again starts anew."""
+    rng = np.random.default_rng(4)
+    H, D, B = 2, 64, 16
+    P = 2
+    kc = torch.zeros(P, B, H, D, dtype=torch.uint8, device="cuda")
+    vc, ks = kc.clone(), torch.zeros(P, H, device="cuda")
+    vs = ks.clone()
+    table = np.array([[1]], np.int32)
+    rows = _bf16(rng, (B, H, D), (2.0 ** np.arange(B) / 64)[:, None, None])
+    ref_c, ref_s = np.zeros((P, B, H, D), np.uint8), np.zeros((P, H))
+    first = []
+    for t in list(range(B)) + [0]:  # the last one starts the block anew
+        x = rows[t:t + 1]
+        pa.pa_write_kv_paged_fp8_block(x.cuda(), x.cuda(), kc, vc, ks, vs, _i32(table), _i32([0]), _i32([t]))
+        R.write(x.double().numpy(), ref_c, ref_s, [B + t])
+        assert np.array_equal(kc.cpu().numpy(), ref_c) and np.array_equal(ks.cpu().numpy().astype(np.float64), ref_s)
+        first.append(R.values(ref_c, ref_s)[1, t].copy())
+        if t == B - 1:
+            v = R.values(ref_c, ref_s)[1]
+            step = 2.0 ** -9 * ref_s[1][None, :, None]  # the subnormals' spacing; two roundings of half of it
+            for i in range(B):
+                assert np.all(np.abs(v[i] - first[i]) <= step[0])
+    assert float(ks[1].max()) < 1.0 and torch.equal(vc, kc) and torch.equal(vs, ks)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("H,D,B,T", [(8, 128, 16, 200), (1, 16, 1, 9), (3, 48, 5, 77), (2, 64, 64, 1), (5, 112, 1024, 1300)])
+def test_read_matches_reference(H, D, B, T, dtype):
+    rng = np.random.default_rng(H + D + B + T)
+    lens = [T, 1, max(1, T // 2)]
+    table, P = _tables(rng, lens, B)
+    codes, scales = zip(_pools(rng, P, B, H, D, pow2=dtype == torch.bfloat16), _pools(rng, P, B, H, D))
+    codes[0][0, 0, 0, 0] = 0x7f
+    seq = rng.integers(0, 3, T).astype(np.int32)
+    pos = np.array([rng.integers(0, lens[s]) for s in seq], np.int32)
+    if T > 5:
+        pos[1], seq[2], pos[4] = -1, 3, 10 ** 6
+    pools = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (*codes, *scales)]
+    ko = torch.full((T, H, D), 7.0, dtype=dtype, device="cuda")
+    vo = torch.full((T, H, D), 7.0, dtype=dtype, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    pa.pa_read_kv_paged_fp8_block(*pools, _i32(table), _i32(seq), _i32(pos), k_out=ko, v_out=vo, error_count=err)
+    slot, nerr = R.slots(table, seq, pos, B, P)
+    assert int(err.item()) == nerr
+    for out, c, s in ((ko, codes[0], scales[0]), (vo, codes[1], scales[1])):
+        want = np.full((T, H, D), 7.0)
+        ok = slot >= 0
+        want[ok] = R.E4M3[c.reshape(-1, H, D)[slot[ok]]] * s.astype(np.float64)[slot[ok] // B][:, :, None]
+        want = torch.from_numpy(want).float().to(dtype)  # one rounding of the exact product (float holds bf16's)
+        assert torch.equal(torch.nan_to_num(out.cpu(), nan=99.0), torch.nan_to_num(want, nan=99.0))
+
+
+# ---------------------------------------------------------------- GPU: attention
+def _tol(out, mag):
+    return 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2.0 ** -10) * mag + 1e-30
+
+
+def _close(got, want, mag):
+    got = got.float().cpu().double().numpy()
+    assert np.all(np.isfinite(got))
+    over = np.abs(got - want) / _tol(want, mag)
+    assert over.max(initial=0.0) <= 1.0, f"{over.max():.2f} times the tolerance at {np.unravel_index(over.argmax(), over.shape)}"
+
+
+def _poison(rng, codes, scales, table, lens, B):
+    """NaN codes in every slot that holds no token, and NaN or infinite scales for blocks without any."""
+    P = codes[0].shape[0]
+    held = np.zeros((P, B), bool)
+    for s, L in enumerate(lens):
+        for j in range(L):
+            if 0 <= table[s, j // B] < P:
+                held[table[s, j // B], j % B] = True
+    for c, s in zip(codes, scales):
+        c[~held] = 0x7f
+        s[~held.any(axis=1)] = np.array([np.nan, np.inf])[rng.integers(0, 2)]
+
+
+def _decode_case(lens, Hq, Hkv, D, B, seed, bad=(), scale=None, gain=1.0, max_len=None, pow2=True):
+    rng = np.random.default_rng(seed)
+    table, P = _tables(rng, lens, B)
+    codes, scales = zip(_pools(rng, P, B, Hkv, D, pow2), _pools(rng, P, B, Hkv, D, pow2))
+    for s, b, value in bad:
+        table[s, b] = value if value < 0 else P + value
+    _poison(rng, codes, scales, table, lens, B)
+    q = _bf16(rng, (len(lens), Hq, D), gain)
+    scale = D ** -0.5 if scale is None else scale
+    pools = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (*codes, *scales)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mx = max_len or max(max(lens), 1)
+    ws = pa.new_decode_fp8_block_workspace(len(lens), Hq, Hkv, D, B, mx)
+    got = pa.pa_decode_fp8_block(q.cuda(), *pools, _i32(table), _i32(lens), mx, scale, ws, error_count=err)
+    again = pa.pa_decode_fp8_block(q.cuda(), *pools, _i32(table), _i32(lens), mx, scale, ws, error_count=err)
+    assert torch.equal(got, again), "the same call twice"
+    s64 = [s.astype(np.float64) for s in scales]
+    want, mag = np.zeros((len(lens), Hq, D)), np.zeros((len(lens), Hq, D))
+    for s, L in enumerate(lens):
+        want[s:s + 1], mag[s:s + 1] = R.attend_rows(q[s:s + 1].double().numpy(), codes[0], s64[0], codes[1], s64[1],
+                                                    table[s], [L], scale)
+    _close(got, want, mag)
+    return int(err.item())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,D,B", [(32, 8, 128, 16), (8, 8, 128, 16), (8, 1, 128, 32), (14, 2, 128, 64),
+                                        (6, 2, 128, 8), (10, 2, 128, 128), (32, 2, 128, 16), (8, 2, 64, 16),
+                                        (4, 2, 128, 5), (4, 4, 64, 100)])
+def test_decode_matches_reference(Hq, Hkv, D, B):
+    lens = [1, 0, B, B + 1, 63, 64, 65, 127, 128, 129, 200, 5, 333, 2]
+    assert _decode_case(lens, Hq, Hkv, D, B, seed=Hq + Hkv + D + B) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [16, 64])
+@pytest.mark.parametrize("n", [1, 3])
+def test_decode_long_contexts(n, B):
+    """Contexts of many partitions, merged; scales that are no powers of two."""
+    assert _decode_case([2500, 1, 1025][:n], 8, 2, 128, B, seed=n + B, pow2=False) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [16, 100])
+def test_decode_bad_pages_are_masked_and_counted(B):
+    """Invalid table entries inside a context: negative, past the pool, a whole sequence without any."""
+    lens = [300, 40, 16, 129]
+    errors = _decode_case(lens, 4, 1, 128, B, seed=B, bad=[(0, 1, -1), (0, 2, 3), (1, 0, -9)] +
+                          [(2, b, -1) for b in range(-(-16 // B))])
+    assert errors > 0
+
+
+@pytest.mark.gpu
+def test_decode_large_and_small_queries():
+    """Queries far from 1, whose scores the softmax scale brings back: the kernel's query terms are scaled by row."""
+    assert _decode_case([200, 77], 8, 2, 128, 16, seed=1, gain=1e6, scale=1e-7) == 0
+    assert _decode_case([200, 77], 8, 2, 128, 16, seed=2, gain=1e-6, scale=1e5) == 0
+    assert _decode_case([200, 77], 8, 2, 128, 16, seed=3, scale=0.0) == 0
+    assert _decode_case([200, 77], 8, 2, 128, 16, seed=4, scale=-0.1) == 0
+
+
+@pytest.mark.gpu
+def test_decode_contexts_beyond_the_limit_are_clamped_and_counted():
+    rng = np.random.default_rng(5)
+    table, P = _tables(rng, [100, 100], 16)
+    codes, scales = zip(_pools(rng, P, 16, 2, 128), _pools(rng, P, 16, 2, 128))
+    pools = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (*codes, *scales)]
+    q = _bf16(rng, (2, 8, 128)).cuda()
+    ws = pa.new_decode_fp8_block_workspace(2, 8, 2, 128, 16, 64)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = pa.pa_decode_fp8_block(q, *pools, _i32(table), _i32([100, 64]), 64, 0.1, ws, error_count=err)
+    want = pa.pa_decode_fp8_block(q, *pools, _i32(table), _i32([64, 64]), 64, 0.1, ws)
+    assert torch.equal(got, want) and int(err.item()) >= 1
+
+
+def _prefill_case(chunks, Hq, Hkv, D, B, seed, extra=(), bad=(), ctx_short=0, pow2=True, splits_over=None):
+    """chunks: (offset, queries); extra: context tokens beyond each chunk's last query."""
+    rng = np.random.default_rng(seed)
+    lens = [o + n + (extra[c] if c < len(extra) else 0) for c, (o, n) in enumerate(chunks)]
+    table, P = _tables(rng, lens, B)
+    codes, scales = zip(_pools(rng, P, B, Hkv, D, pow2), _pools(rng, P, B, Hkv, D, pow2))
+    for s, b, value in bad:
+        table[s, b] = value if value < 0 else P + value
+    _poison(rng, codes, scales, table, lens, B)
+    order = rng.permutation(len(chunks))  # sequence of chunk c
+    table, ctx = table[np.argsort(order)], np.array(lens)[np.argsort(order)]
+    cu = np.concatenate([[0], np.cumsum([n for _, n in chunks])])
+    q = _bf16(rng, (int(cu[-1]), Hq, D))
+    pools = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (*codes, *scales)]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    mq, mx = max(max(n for _, n in chunks), 1), max(lens)
+    ws = pa.new_prefill_fp8_block_workspace(len(chunks), int(cu[-1]), mq, Hq, Hkv, D, B, mx)
+    out = torch.full(q.shape, 5.0, dtype=BF, device="cuda")
+    args = (_i32(cu), _i32([o for o, _ in chunks]), _i32(order), mq, *pools, _i32(table), _i32(ctx), mx, D ** -0.5, ws)
+    pa.pa_prefill_chunk_fp8_block(q.cuda(), *args, out=out, error_count=err)
+    first = out.clone()
+    pa.pa_prefill_chunk_fp8_block(q.cuda(), *args, out=out, error_count=err)
+    assert torch.equal(first, out), "the same call twice"
+    s64 = [s.astype(np.float64) for s in scales]
+    want, mag = np.zeros(q.shape), np.zeros(q.shape)
+    for c, (o, n) in enumerate(chunks):
+        r = slice(int(cu[c]), int(cu[c + 1]))
+        want[r], mag[r] = R.attend_rows(q[r].double().numpy(), codes[0], s64[0], codes[1], s64[1], table[order[c]],
+                                        [o + i + 1 for i in range(n)], D ** -0.5)
+    _close(out, want, mag)
+    return int(err.item())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,D,B", [(8, 2, 128, 16), (2, 2, 128, 32), (4, 2, 128, 64), (8, 1, 128, 128), (6, 2, 128, 8),
+                                        (5, 1, 128, 16), (16, 1, 128, 16), (4, 2, 64, 16), (2, 1, 128, 7)])
+def test_prefill_matches_reference(Hq, Hkv, D, B):
+    chunks = [(0, 1), (0, 40), (17, 33), (130, 7), (0, 0), (255, 2)]
+    assert _prefill_case(chunks, Hq, Hkv, D, B, seed=Hq + Hkv + D + B) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,Hkv,B", [(4, 1, 16), (8, 1, 64), (3, 1, 32)])
+def test_prefill_tiles_and_long_offsets(Hq, Hkv, B):
+    """Several query tiles and key tiles, a short chunk far into a context (split over keys), odd ends; scales that
+    are no powers of two."""
+    assert _prefill_case([(3, 200), (900, 3), (1, 129)], Hq, Hkv, 128, B, seed=Hq + B, extra=(9, 70, 0), pow2=False) == 0
+
+
+@pytest.mark.gpu
+def test_prefill_bad_pages_are_masked_and_counted():
+    assert _prefill_case([(100, 30), (5, 20)], 4, 1, 128, 16, seed=8, bad=[(0, 0, -1), (0, 3, 2), (1, 0, -1), (1, 1, -1)]) > 0
+
+
+# ---------------------------------------------------------------- GPU: together
+@pytest.mark.gpu
+def test_write_then_prefill_then_decode_then_read():
+    """A prompt in two chunks, then decode steps, as a serving loop makes them; the attention sees what the read back
+    gives, and every value is within e4m3's half step (2^-4) of what was written, or the scale's smallest step."""
+    rng = np.random.default_rng(9)
+    Hq, Hkv, D, B, n = 8, 2, 128, 16, 75
+    table, P = _tables(rng, [n + 5], B)
+    kc = torch.zeros(P, B, Hkv, D, dtype=torch.uint8, device="cuda")
+    vc = torch.full_like(kc, 0x7f)
+    ks, vs = torch.zeros(P, Hkv, device="cuda"), torch.full((P, Hkv), 1e30, device="cuda")
+    bt, kn, vn, q = _i32(table), _bf16(rng, (n + 5, Hkv, D)), _bf16(rng, (n + 5, Hkv, D), 3.0), _bf16(rng, (n + 5, Hq, D))
+    outs = []
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for a, b in [(0, 50), (50, n)] + [(t, t + 1) for t in range(n, n + 5)]:
+        T = b - a
+        pa.pa_write_kv_paged_fp8_block(kn[a:b].cuda(), vn[a:b].cuda(), kc, vc, ks, vs, bt, _i32([0] * T),
+                                       _i32(np.arange(a, b)), error_count=err)
+        x = q[a:b].cuda()
+        if T > 1:
+            ws = pa.new_prefill_fp8_block_workspace(1, T, T, Hq, Hkv, D, B, b)
+            outs.append(pa.pa_prefill_chunk_fp8_block(x, _i32([0, T]), _i32([a]), _i32([0]), T, kc, vc, ks, vs, bt,
+                                                      _i32([b]), b, D ** -0.5, ws, error_count=err))
+        else:
+            ws = pa.new_decode_fp8_block_workspace(1, Hq, Hkv, D, B, b)
+            outs.append(pa.pa_decode_fp8_block(x, kc, vc, ks, vs, bt, _i32([b]), b, D ** -0.5, ws, error_count=err))
+        k, v = pa.pa_read_kv_paged_fp8_block(kc, vc, ks, vs, bt, _i32([0] * b), _i32(np.arange(b)),
+                                             dtype=torch.float32, error_count=err)
+        k, v = k.double().cpu().numpy(), v.double().cpu().numpy()
+        want, mag = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
+        for i in range(T):
+            for h in range(Hkv):
+                g = slice(h * 4, h * 4 + 4)
+                want[i, g], mag[i, g] = R.attend(q[a + i, g].double().numpy(), k[:a + i + 1, h], v[:a + i + 1, h], D ** -0.5)
+        _close(outs[-1], want, mag)
+    assert int(err.item()) == 0
+    for new, got, s in ((kn, k, ks), (vn, v, vs)):
+        x = new.double().numpy()
+        small = 2.0 ** -9 * s.cpu().double().numpy()[table[0, np.arange(n + 5) // B]][:, :, None]
+        assert np.all(np.abs(got - x) <= 2.0 ** -4 * np.abs(x) + small)
