@@ -10,6 +10,24 @@ namespace pa {
 namespace {
 bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
+// The split of pa_decode_fp8_block's contexts: partitions of whole 128-token stages, long enough that a partition's
+// partial result is small beside the codes it reads, short enough that the batch (at its longest context: the
+// lengths live on the device) gives every SM kItemsPerSm items; at most 128 partials per (sequence, head).
+#ifndef PA_FP8_BLOCK_PARTITION
+#define PA_FP8_BLOCK_PARTITION 512
+#endif
+#ifndef PA_FP8_BLOCK_ITEMS_PER_SM
+#define PA_FP8_BLOCK_ITEMS_PER_SM 8
+#endif
+DecodePlan plan_decode_fp8_block(int num_seqs, int num_kv_heads, int max_context_len, int num_sms) {
+    auto splits = [&](long long part) { return max_context_len <= part ? 1LL : (max_context_len + part - 1) / part; };
+    long long part = PA_FP8_BLOCK_PARTITION;
+    while (part > 128 && splits(part) * num_seqs * num_kv_heads < (long long)PA_FP8_BLOCK_ITEMS_PER_SM * num_sms)
+        part /= 2;
+    while (splits(part) > 128) part *= 2;
+    return DecodePlan{(int)part, (int)splits(part), (int)part, num_seqs};
+}
+
 // Row shape of the write and the read back: 16-byte pieces of codes, blocks of at most 1024 slots.
 int rows_ok(int num_kv_heads, int head_dim, int block_size) {
     if (num_kv_heads < 1 || head_dim < 1 || block_size < 1) return PA_ERR_INVALID_ARG;
@@ -76,7 +94,12 @@ int pa_read_kv_paged_fp8_block(void* k_out, void* v_out, int num_tokens, int num
 
 size_t pa_decode_fp8_block_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                           int block_size, int max_context_len) {
-    return pa_decode_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len);
+    if (num_seqs < 0 || max_context_len < 0 || decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size))
+        return 0;
+    int num_sms = 0;
+    if (check_device(&num_sms) != PA_OK) return 0;
+    const DecodePlan plan = plan_decode_fp8_block(num_seqs, num_kv_heads, max_context_len, num_sms);
+    return decode_workspace_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, plan.max_splits).total;
 }
 
 int pa_decode_fp8_block(void* out, const void* q, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
@@ -93,8 +116,7 @@ int pa_decode_fp8_block(void* out, const void* q, int num_seqs, int num_q_heads,
         return PA_ERR_INVALID_ARG;
     int num_sms = 0;
     if ((rc = check_device(&num_sms)) != PA_OK) return rc;
-    const DecodePlan plan =
-        plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, num_sms, SIZE_MAX, 0, true);
+    const DecodePlan plan = plan_decode_fp8_block(num_seqs, num_kv_heads, max_context_len, num_sms);
     const DecodeWorkspace lay =
         decode_workspace_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, plan.max_splits);
     if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return PA_ERR_WORKSPACE;
@@ -125,7 +147,9 @@ int pa_decode_fp8_block(void* out, const void* q, int num_seqs, int num_q_heads,
     p.max_splits = plan.max_splits;
     p.scale_log2 = scale * 1.4426950408889634f;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if ((rc = launch_decode_fp8_block_fma(p, st)) != PA_OK) return rc;
+    rc = decode_fp8_block_tc_supported(p) ? launch_decode_fp8_block_tc(p, num_sms, st)
+                                          : launch_decode_fp8_block_fma(p, st);
+    if (rc != PA_OK) return rc;
     return launch_decode_merge(p, PA_BF16, num_sms, st);
 }
 

@@ -189,6 +189,8 @@ int launch_read_fp8_block(void* k_out, void* v_out, int num_tokens, int num_kv_h
                           int num_blocks, int block_size, const int32_t* block_tables, int num_seqs,
                           int max_blocks_per_seq, const int32_t* seq_idx, const int32_t* pos, int32_t* error_count,
                           cudaStream_t stream);
+bool decode_fp8_block_tc_supported(const DecodeParams& p);
+int launch_decode_fp8_block_tc(const DecodeParams& p, int num_sms, cudaStream_t stream);
 int launch_decode_fp8_block_fma(const DecodeParams& p, cudaStream_t stream);
 int launch_prefill_fp8_block_fma(const PrefillParams& p, cudaStream_t stream);
 int launch_copy_blocks(void* k_cache, void* v_cache, int num_blocks, int block_size, int row_bytes,

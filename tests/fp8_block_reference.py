@@ -105,3 +105,18 @@ def attend_rows(q, kc, ks, vc, vs, table_row, limits, scale):
             o, a = attend(q[i, h * g:(h + 1) * g], k[:, h], v[:, h], scale)
             out[i, h * g:(h + 1) * g], mag[i, h * g:(h + 1) * g] = o, a
     return out, mag
+
+
+def floor_rows(vc, vs, table_row, limits, hq):
+    """R sum_j |code_j| of each row's tokens, [m, Hq, D]: R the power of two not below any of their V scales."""
+    P, block, hkv, d = vc.shape
+    out = np.zeros((len(limits), hq, d))
+    for i, n in enumerate(limits):
+        rows = [(int(table_row[j // block]), j % block) for j in range(n)]
+        rows = [(b, o) for b, o in rows if 0 <= b < P]
+        if not rows:
+            continue
+        b, o = np.array(rows).T
+        r = 2.0 ** np.ceil(np.log2(np.maximum(vs[b].max(axis=0), 2.0 ** -110)))
+        out[i] = np.repeat(r[:, None] * np.abs(E4M3[vc[b, o]]).sum(axis=0), hq // hkv, axis=0)
+    return out

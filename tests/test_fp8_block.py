@@ -4,7 +4,10 @@ against a float64 reference (tests/fp8_block_reference.py).
 Write and read back are bit-exact.  Attention: an output is off by at most its own rounding to bf16, 2^-8 |out|; by
 the rounding of the probabilities to bf16-like precision (two e4m3 terms: 2^-4 of a half step's 2^-4), 2^-8 of
 sum_j p_j |v_j|; and by the float32 products, exponentials and sums, for which 2^-10 of that sum leaves room (scores
-below about 64 in magnitude, rounded to 2^-24 of their terms' sum, plus 2^-20 of the largest query element)."""
+below about 64 in magnitude, rounded to 2^-24 of their terms' sum, plus 2^-20 of the largest query element).
+The two terms have a floor: a weight w = 256 p vs_j / R (p <= 1, R the power of two not below any V scale) is hi + lo / 16
+with lo's subnormals 2^-9 apart, so it is off by max(2^-8 w, 2^-9 / 16 / 2 = 2^-14); the output then by
+sum_j 2^-14 (R / 256) |code_j| / l <= 2^-22 R sum_j |code_j|, since the sum l of the unrounded p has a term that is 1."""
 import ctypes
 
 import numpy as np
@@ -297,14 +300,14 @@ def test_read_matches_reference(H, D, B, T, dtype):
 
 
 # ---------------------------------------------------------------- GPU: attention
-def _tol(out, mag):
-    return 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2.0 ** -10) * mag + 1e-30
+def _tol(out, mag, floor):
+    return 2.0 ** -8 * np.abs(out) + (2.0 ** -8 + 2.0 ** -10) * mag + 2.0 ** -22 * floor + 1e-30
 
 
-def _close(got, want, mag):
+def _close(got, want, mag, floor):
     got = got.float().cpu().double().numpy()
     assert np.all(np.isfinite(got))
-    over = np.abs(got - want) / _tol(want, mag)
+    over = np.abs(got - want) / _tol(want, mag, floor)
     assert over.max(initial=0.0) <= 1.0, f"{over.max():.2f} times the tolerance at {np.unravel_index(over.argmax(), over.shape)}"
 
 
@@ -338,11 +341,12 @@ def _decode_case(lens, Hq, Hkv, D, B, seed, bad=(), scale=None, gain=1.0, max_le
     again = pa.pa_decode_fp8_block(q.cuda(), *pools, _i32(table), _i32(lens), mx, scale, ws, error_count=err)
     assert torch.equal(got, again), "the same call twice"
     s64 = [s.astype(np.float64) for s in scales]
-    want, mag = np.zeros((len(lens), Hq, D)), np.zeros((len(lens), Hq, D))
+    want, mag, floor = (np.zeros((len(lens), Hq, D)) for _ in range(3))
     for s, L in enumerate(lens):
         want[s:s + 1], mag[s:s + 1] = R.attend_rows(q[s:s + 1].double().numpy(), codes[0], s64[0], codes[1], s64[1],
                                                     table[s], [L], scale)
-    _close(got, want, mag)
+        floor[s:s + 1] = R.floor_rows(codes[1], s64[1], table[s], [L], Hq)
+    _close(got, want, mag, floor)
     return int(err.item())
 
 
@@ -420,12 +424,13 @@ def _prefill_case(chunks, Hq, Hkv, D, B, seed, extra=(), bad=(), ctx_short=0, po
     pa.pa_prefill_chunk_fp8_block(q.cuda(), *args, out=out, error_count=err)
     assert torch.equal(first, out), "the same call twice"
     s64 = [s.astype(np.float64) for s in scales]
-    want, mag = np.zeros(q.shape), np.zeros(q.shape)
+    want, mag, floor = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
     for c, (o, n) in enumerate(chunks):
         r = slice(int(cu[c]), int(cu[c + 1]))
         want[r], mag[r] = R.attend_rows(q[r].double().numpy(), codes[0], s64[0], codes[1], s64[1], table[order[c]],
                                         [o + i + 1 for i in range(n)], D ** -0.5)
-    _close(out, want, mag)
+        floor[r] = R.floor_rows(codes[1], s64[1], table[order[c]], [o + i + 1 for i in range(n)], Hq)
+    _close(out, want, mag, floor)
     return int(err.item())
 
 
@@ -480,11 +485,12 @@ def test_write_then_prefill_then_decode_then_read():
                                              dtype=torch.float32, error_count=err)
         k, v = k.double().cpu().numpy(), v.double().cpu().numpy()
         want, mag = np.zeros((T, Hq, D)), np.zeros((T, Hq, D))
+        floor = R.floor_rows(vc.cpu().numpy(), vs.cpu().double().numpy(), table[0], list(range(a + 1, b + 1)), Hq)
         for i in range(T):
             for h in range(Hkv):
                 g = slice(h * 4, h * 4 + 4)
                 want[i, g], mag[i, g] = R.attend(q[a + i, g].double().numpy(), k[:a + i + 1, h], v[:a + i + 1, h], D ** -0.5)
-        _close(outs[-1], want, mag)
+        _close(outs[-1], want, mag, floor)
     assert int(err.item()) == 0
     for new, got, s in ((kn, k, ks), (vn, v, vs)):
         x = new.double().numpy()
