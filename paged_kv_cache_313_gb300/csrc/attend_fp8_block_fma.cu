@@ -58,7 +58,8 @@ __global__ void __launch_bounds__(kFmaThreads) prefill_fp8_block_fma_kernel(Pref
         return;
     }
     if (i >= n) return;
-    const int cap = (int)min((long long)p.context_lens[s], (long long)p.max_blocks_per_seq * p.block_size);
+    const int cap = (int)min(min((long long)p.context_lens[s], (long long)p.max_context_len),
+                             (long long)p.max_blocks_per_seq * p.block_size);
     int L = start + i + 1;  // causal: keys 0..start+i
     if (L > cap) {
         if (threadIdx.x == 0 && kvh == 0) count_error(p.error_count);

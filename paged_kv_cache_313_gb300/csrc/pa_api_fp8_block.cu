@@ -155,9 +155,13 @@ int pa_decode_fp8_block(void* out, const void* q, int num_seqs, int num_q_heads,
 
 size_t pa_prefill_fp8_block_workspace_size(int num_chunks, int total_q, int max_q_len, int num_q_heads,
                                            int num_kv_heads, int head_dim, int block_size, int max_context_len) {
-    (void)num_chunks; (void)total_q; (void)max_q_len; (void)num_q_heads; (void)num_kv_heads; (void)head_dim;
-    (void)block_size; (void)max_context_len;
-    return 0;
+    int num_sms = 0;
+    if (num_chunks <= 0 || total_q <= 0 || max_q_len <= 0 || max_context_len < 0 ||
+        decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size) != PA_OK || head_dim != 128 ||
+        num_q_heads / num_kv_heads > 8 || check_device(&num_sms) != PA_OK)
+        return 0;
+    return prefill_fp8_block_workspace(num_chunks, total_q, max_q_len, num_q_heads, num_kv_heads, max_context_len,
+                                       num_sms);
 }
 
 int pa_prefill_chunk_fp8_block(void* out, const void* q, const int32_t* cu_q_lens, const int32_t* q_start_pos,
@@ -167,7 +171,6 @@ int pa_prefill_chunk_fp8_block(void* out, const void* q, const int32_t* cu_q_len
                                int block_size, const int32_t* block_tables, int max_blocks_per_seq,
                                const int32_t* context_lens, int max_context_len, float scale, void* workspace,
                                size_t workspace_bytes, int32_t* error_count, void* stream) {
-    (void)workspace; (void)workspace_bytes;
     if (num_chunks < 0 || total_q < 0 || max_q_len < 0 || num_seqs < 0 || num_blocks < 0 || max_blocks_per_seq < 0 ||
         max_context_len < 0)
         return PA_ERR_INVALID_ARG;
@@ -177,7 +180,8 @@ int pa_prefill_chunk_fp8_block(void* out, const void* q, const int32_t* cu_q_len
     if (!out || !q || !cu_q_lens || !q_start_pos || !seq_of_chunk || !k_cache || !v_cache || !k_scales || !v_scales ||
         !context_lens || !block_tables || num_seqs == 0)
         return PA_ERR_INVALID_ARG;
-    if ((rc = check_device(nullptr)) != PA_OK) return rc;
+    int num_sms = 0;
+    if ((rc = check_device(&num_sms)) != PA_OK) return rc;
     PrefillParams p;
     p.out = out;
     p.q = q;
@@ -202,8 +206,13 @@ int pa_prefill_chunk_fp8_block(void* out, const void* q, const int32_t* cu_q_len
     p.num_blocks = num_blocks;
     p.block_size = block_size;
     p.max_blocks_per_seq = max_blocks_per_seq;
+    p.max_context_len = max_context_len;
     p.scale_log2 = scale * 1.4426950408889634f;
-    return launch_prefill_fp8_block_fma(p, static_cast<cudaStream_t>(stream));
+    if (!prefill_fp8_block_tc_supported(p)) return launch_prefill_fp8_block_fma(p, static_cast<cudaStream_t>(stream));
+    const size_t need = prefill_fp8_block_workspace(num_chunks, total_q, max_q_len, num_q_heads, num_kv_heads,
+                                                    max_context_len, num_sms);
+    if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return PA_ERR_WORKSPACE;
+    return launch_prefill_fp8_block_tc(p, workspace, num_sms, static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

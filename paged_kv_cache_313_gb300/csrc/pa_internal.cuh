@@ -157,6 +157,7 @@ struct PrefillParams {
     // e4m3 pools with a scale per (block, kv head) (pa_prefill_chunk_fp8_block): float [num_blocks][num_kv_heads]
     const float* k_scales = nullptr;
     const float* v_scales = nullptr;
+    int max_context_len = 0x7FFFFFFF;  // keys at or beyond it are not read (block-scaled pools)
 };
 
 // Kernel launchers (defined in the .cu files).
@@ -192,6 +193,11 @@ int launch_read_fp8_block(void* k_out, void* v_out, int num_tokens, int num_kv_h
 bool decode_fp8_block_tc_supported(const DecodeParams& p);
 int launch_decode_fp8_block_tc(const DecodeParams& p, int num_sms, cudaStream_t stream);
 int launch_decode_fp8_block_fma(const DecodeParams& p, cudaStream_t stream);
+// Workspace of the block-scaled prefill: the partial rows of query tiles whose keys are cut into spans.
+size_t prefill_fp8_block_workspace(int num_chunks, int total_q, int max_q_len, int num_q_heads, int num_kv_heads,
+                                   int max_context_len, int num_sms);
+bool prefill_fp8_block_tc_supported(const PrefillParams& p);
+int launch_prefill_fp8_block_tc(const PrefillParams& p, void* workspace, int num_sms, cudaStream_t stream);
 int launch_prefill_fp8_block_fma(const PrefillParams& p, cudaStream_t stream);
 int launch_copy_blocks(void* k_cache, void* v_cache, int num_blocks, int block_size, int row_bytes,
                        const int32_t* src, const int32_t* dst, const int32_t* num_valid, int num_copies,

@@ -1,0 +1,841 @@
+// prefill_fp8_block_tc.cu — causal chunked prefill over e4m3 pools with a scale
+// per (block, kv head), on the 5th-generation tensor cores.
+//
+// What it computes: query i of chunk c, at position q_start_pos[c] + i, attends
+// the keys up to its own position, K_j = code ks[block(j)], V_j = code vs[block(j)].
+//
+// A work item is (query tile, kv head, chunk, span of keys).  A tile is 128
+// rows: 128 / G positions times the G query heads of the kv head.  Keys come
+// in tiles of 128, one TMA box per block.
+//
+// Products.
+//   S = Q K^T   kind::f8f6f4, 128 x 128 x 128: K as the box left it.  The
+//               queries, scaled by a power of two that puts a row's largest
+//               magnitude in [128, 256), are two e4m3 terms hi + lo that both
+//               accumulate into S: a bf16's 8 bits exactly, but for elements
+//               below 2^-10 of the row's largest (off by 2^-17 of it at most).
+//   O += P V    kind::f16: V's codes widened to f16 (exact) in shared memory by
+//               four converter warps, P in f16 in tensor memory, over the S it
+//               came from.  (P as two e4m3 terms would spare the widening, but
+//               its floor, 2^-17 of the largest weight, is too coarse for long
+//               diffuse contexts, and the split costs twice the widening.)
+// ks multiplies a key's scores.  vs / R is part of the exponent, P' =
+// 2^(x + log2(vs / R) - m), so it costs nothing per element; the softmax's sum
+// takes the float P' of 8 keys of one block times R / vs.  R is a power of two;
+// it changes (and O is rescaled) only when a V scale passes 64 R.  Ratios below
+// 2^-40 are held there: such a weight is 0 in f16, and its P' still counts in
+// the sum.
+//
+// Two softmax groups of four warps, a thread per row, take alternate key
+// tiles, each with its own S, running maximum, sum and O; while one group is at
+// its exponentials the tensor cores run the other's products.  The groups'
+// states are joined once per item.  A group passes P on in halves of 64 keys,
+// so that the first half's product runs under the second half's exponentials.
+// The maximum is lazy: O is rescaled only when it grows by more than 2^8.
+//
+// Few rows: the plan cuts the keys of a tile into spans, whose partial results
+// (float, in the workspace) a second kernel joins.
+//
+//   warps 0-7   softmax, group w / 4            warp 13  K tiles, masks, scales
+//   warps 8-11  V widening, query terms         warp 14  V tiles
+//   warp 12     tensor memory, MMA issue
+// Waits are bounded, copies and MMAs drained, as in prefill_tc.cu.
+#include "pa_internal.cuh"
+#include "sm100_ptx.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kTile = 128;             // rows of a query tile, keys of a key tile
+constexpr int kCodes = kTile * kD;     // bytes of a tile of codes
+constexpr int kHalfBytes = kTile * 128;  // bytes of a 64-column half of a widened tile
+constexpr int kThreads = 480;
+constexpr int kConverters = 4, kConvWarp = 8, kMmaWarp = 12, kKWarp = 13, kVWarp = 14;
+constexpr int kKStages = 3, kVStages = 2, kVhStages = 2, kInfo = 8;
+// The converters may be two items ahead of the softmax (items of one key tile), never four: four slots keep an item's
+// query factors, and the phase of its barrier, until the softmax has come to it.
+constexpr int kQSlots = 4;
+constexpr float kLazy = 8.f;
+constexpr float kScaleFloor = 7.703719777548943e-34f;  // 2^-110, the smallest R
+
+// shared memory, offsets from a 1024-aligned base
+constexpr int kQ = 0;                                      // [2 items][hi, lo]
+constexpr int kK = kQ + 2 * 2 * kCodes;
+constexpr int kV = kK + kKStages * kCodes;
+constexpr int kVh = kV + kVStages * kCodes;
+constexpr int kConsts = kVh + kVhStages * 2 * kHalfBytes;  // float4 [kInfo][16]: per 8 keys ks', log2(vs/R), R/vs
+constexpr int kMask = kConsts + kInfo * 16 * 16;           // uint32 [kInfo][4]
+constexpr int kR = kMask + kInfo * 16;                     // float [kInfo]
+constexpr int kQf = kR + kInfo * 4;                        // float [kQSlots][128]
+constexpr int kState = kQf + kQSlots * kTile * 4;          // float4 [2 items][2 groups][128]: m, l, R
+constexpr int kBars = kState + 2 * 2 * kTile * 16;
+constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 2 * kVhStages + 2 + 4 + 4 + kQSlots + 2 + kInfo + 2;
+constexpr int kTmemSlot = kBars + kNumBars * 8;
+constexpr size_t kSmemBytes = 1024 + kTmemSlot + 16;
+static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+
+struct Bars {
+    uint64_t* base;
+    __device__ uint64_t* k_full(int i) const { return base + i; }
+    __device__ uint64_t* k_empty(int i) const { return base + kKStages + i; }
+    __device__ uint64_t* v_full(int i) const { return base + 2 * kKStages + i; }
+    __device__ uint64_t* v_empty(int i) const { return v_full(kVStages + i); }
+    __device__ uint64_t* vh_full(int i) const { return v_full(2 * kVStages + i); }
+    __device__ uint64_t* vh_empty(int i) const { return vh_full(kVhStages + i); }
+    __device__ uint64_t* s_full(int x) const { return vh_full(2 * kVhStages + x); }
+    __device__ uint64_t* p_full(int x, int h) const { return s_full(2 + 2 * x + h); }
+    __device__ uint64_t* o_done(int x, int h) const { return s_full(6 + 2 * x + h); }
+    __device__ uint64_t* q_full(int i) const { return s_full(10 + i); }
+    __device__ uint64_t* q_empty(int i) const { return s_full(10 + kQSlots + i); }
+    __device__ uint64_t* info(int i) const { return s_full(12 + kQSlots + i); }
+    __device__ uint64_t* o_free() const { return info(kInfo); }
+    __device__ uint64_t* drain() const { return info(kInfo + 1); }
+};
+
+struct Item {
+    int kvh, r0, s, start, i0, nq, last_key, t0, nt, span, spans;  // key tiles t0 .. t0 + nt - 1
+};
+
+// The kernel's own parameters: the plan's key tiles per span and spans per tile.
+struct Spans {
+    int tiles, count;
+    float* o;    // [count][total_q][num_q_heads][kD]
+    float2* ml;  // [count][total_q][num_q_heads]
+};
+
+// A 32-byte global store (the address 32-byte aligned).
+__device__ __forceinline__ void store32(void* ptr, const uint32_t (&v)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// The queries of a chunk: first row, count, sequence and start; false when they make no sense.
+__device__ __forceinline__ bool chunk_of(const PrefillParams& p, int c, int& r0, int& n, int& s, int& start) {
+    r0 = p.cu_q_lens[c];
+    n = p.cu_q_lens[c + 1] - r0;
+    s = p.seq_of_chunk[c];
+    start = p.q_start_pos[c];
+    return n >= 0 && r0 >= 0 && r0 + n <= p.total_q && n <= p.max_q_len && s >= 0 && s < p.num_seqs && start >= 0;
+}
+// Keys that sequence s may be asked for.
+__device__ __forceinline__ int key_cap(const PrefillParams& p, int s) {
+    const long long table = (long long)p.max_blocks_per_seq * p.block_size;
+    return (int)min(min((long long)p.context_lens[s], (long long)p.max_context_len), table);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prefill_fp8_block_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                                const PrefillParams p, const Spans spans) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const Bars bars{reinterpret_cast<uint64_t*>(smem + kBars)};
+    uint32_t* mask = reinterpret_cast<uint32_t*>(smem + kMask);
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kTmemSlot);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = p.group, B = p.block_size, Hkv = p.num_kv_heads;
+    const int ppt = kTile / G;  // positions per tile; rows from ppt * G on are unused
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kKStages; ++i) {
+            mbar_init(bars.k_full(i), 1);
+            mbar_init(bars.k_empty(i), 1);
+        }
+        for (int i = 0; i < kVStages; ++i) {
+            mbar_init(bars.v_full(i), 1);
+            mbar_init(bars.v_empty(i), kConverters);
+        }
+        for (int i = 0; i < kVhStages; ++i) {
+            mbar_init(bars.vh_full(i), kConverters);
+            mbar_init(bars.vh_empty(i), 1);
+        }
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(bars.s_full(x), 1);
+            for (int h = 0; h < 2; ++h) {
+                mbar_init(bars.p_full(x, h), 4);
+                mbar_init(bars.o_done(x, h), 1);
+            }
+            mbar_init(bars.q_empty(x), 1);
+        }
+        for (int i = 0; i < kQSlots; ++i) mbar_init(bars.q_full(i), kConverters);
+        for (int i = 0; i < kInfo; ++i) mbar_init(bars.info(i), 1);
+        mbar_init(bars.o_free(), 8);
+        mbar_init(bars.drain(), 1);
+        fence_mbar_init();
+    }
+    pdl_trigger();
+    pdl_wait();
+    if (warp == kMmaWarp) {
+        tmem_alloc(tmem_slot, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;  // S of group 0, S of group 1, O of group 0, O of group 1; 128 columns each
+
+    // ---- items: (query tile rank, chunk, kv head, span), the latest tile of every chunk first; CTA b takes one of
+    // every pass of gridDim.x items, in serpentine order, so that heavy and light ones pair up.  Every warp walks the
+    // same items, so the roles agree without a word.
+    const int per_rank = p.num_chunks * Hkv * spans.count;
+    const long long num_items = (long long)((p.max_q_len + ppt - 1) / ppt) * per_rank;
+    const long long passes = (num_items + gridDim.x - 1) / gridDim.x;
+    // item of pass c; false for an empty one
+    auto describe = [&](long long c, Item& d) {
+        const long long g = gridDim.x, b = blockIdx.x, k = c * g + ((c & 1) ? g - 1 - b : b);
+        if (k >= num_items) return false;
+        const int rank = (int)(k / per_rank);
+        int rem = (int)(k - (long long)rank * per_rank);
+        d.span = rem % spans.count;
+        rem /= spans.count;
+        const int ch = rem / Hkv;
+        d.kvh = rem - ch * Hkv;
+        int n;
+        if (!chunk_of(p, ch, d.r0, n, d.s, d.start)) {
+            if (rank == 0 && d.kvh == 0 && d.span == 0 && threadIdx.x == 0) count_error(p.error_count);
+            return false;
+        }
+        const int tiles = (n + ppt - 1) / ppt;
+        if (rank >= tiles) return false;
+        d.i0 = (tiles - 1 - rank) * ppt;
+        d.nq = min(ppt, n - d.i0);
+        const int cap = key_cap(p, d.s);
+        d.last_key = (int)min((long long)d.start + d.i0 + d.nq - 1, 0x7FFFFFFELL);
+        if (d.last_key >= cap) {
+            if (d.span == 0 && threadIdx.x == 0) count_error(p.error_count);
+            d.last_key = cap - 1;
+        }
+        const int all = d.last_key >= 0 ? d.last_key / kTile + 1 : 0;
+        d.spans = max(1, (all + spans.tiles - 1) / spans.tiles);
+        d.t0 = d.span * spans.tiles;
+        d.nt = min(spans.tiles, all - d.t0);
+        if (d.nt < 0) d.nt = 0;
+        return d.span < d.spans;  // without any key, span 0 stores zeros
+    };
+    bool ok = true;
+
+    if (warp == kKWarp || warp == kVWarp) {
+        // ============================================================ producers
+        const bool v_side = warp == kVWarp;
+        const int bpt = kTile / B, tpc = 32 / bpt;  // blocks per tile, tiles per 32-entry chunk of the table
+        if (lane == 0) tma_prefetch_desc(v_side ? &tmv : &tmk);
+        uint32_t g = 0;  // key tiles so far
+        for (long long c = 0; c < passes && ok; ++c) {
+            Item d;
+            if (!describe(c, d)) continue;
+            const int first = d.t0 * bpt;  // first block
+            const int nblk = min((d.last_key + B) / B, (d.t0 + d.nt) * bpt) - first;
+            const int32_t* table = p.block_tables + (size_t)d.s * p.max_blocks_per_seq + first;
+            auto load_raw = [&](int chunk) {
+                const int i = chunk * 32 + lane;
+                return i < nblk ? table[i] : -1;
+            };
+            auto load_scales = [&](int pb) {
+                if (v_side || pb < 0 || pb >= p.num_blocks) return make_float2(0.f, 0.f);
+                const size_t i = (size_t)pb * Hkv + d.kvh;
+                return make_float2(__ldg(p.k_scales + i), __ldg(p.v_scales + i));
+            };
+            int raw = d.nt > 0 ? load_raw(0) : -1, raw_next = -1, pb = -1;
+            float2 sc = load_scales(raw), sc_next = make_float2(0.f, 0.f);
+            float R = 0.f;
+            for (int j = 0; j < d.nt; ++j, ++g) {
+                const int chunk = j / tpc, l = j - chunk * tpc;
+                if (l == 0) {
+                    if (chunk > 0) {
+                        raw = raw_next;
+                        sc = sc_next;
+                    }
+                    pb = raw;
+                    if (chunk * 32 + lane < nblk && (raw < 0 || raw >= p.num_blocks)) {
+                        if (!v_side) count_error(p.error_count);
+                        pb = -1;
+                    }
+                }
+                const uint32_t valid = __ballot_sync(0xffffffffu, pb >= 0);
+                const uint32_t mine = (valid >> (l * bpt)) & ((1u << bpt) - 1u);
+                const int stages = v_side ? kVStages : kKStages, st = g % stages;
+                uint64_t* full = v_side ? bars.v_full(st) : bars.k_full(st);
+                if (g >= (uint32_t)stages &&
+                    !mbar_wait_warp(v_side ? bars.v_empty(st) : bars.k_empty(st), ((g / stages) - 1) & 1)) {
+                    ok = false;
+                    break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)__popc(mine) * B * kD);
+                __syncwarp();  // armed before any copy is issued
+                const int src = l * bpt + (lane < bpt ? lane : 0);
+                const int my_pb = __shfl_sync(0xffffffffu, pb, src);
+                if (lane < bpt && my_pb >= 0)
+                    tma_load_3d(smem + (v_side ? kV : kK) + st * kCodes + lane * B * kD, v_side ? &tmv : &tmk, 0,
+                                my_pb * B, d.kvh, full);
+                if (!v_side) {
+                    // what the softmax needs of this tile's 16 groups of 8 keys
+                    const float my_vs = __shfl_sync(0xffffffffu, sc.y, src);
+                    const float vmax = redux_max(lane < bpt ? my_vs : 0.f);
+                    if (j == 0 || vmax > 64.f * R)
+                        R = __uint_as_float((__float_as_uint(fmaxf(vmax, kScaleFloor)) + 0x7FFFFFu) & 0x7F800000u);
+                    const int blk = (lane & 15) * 8 / B;  // block of this lane's group
+                    const float ks = __shfl_sync(0xffffffffu, sc.x, l * bpt + blk);
+                    const float vs = __shfl_sync(0xffffffffu, sc.y, l * bpt + blk);
+                    const int slot = g % kInfo;
+                    if (lane < 16) {
+                        const float off = __log2f(fmaxf(vs / R, 9.094947017729282e-13f));  // at least 2^-40
+                        reinterpret_cast<float4*>(smem + kConsts)[slot * 16 + lane] =
+                            make_float4(ks * fabsf(p.scale_log2), off, fast_exp2(-off), 0.f);
+                    }
+                    if (lane < 4) {  // key-validity mask: 32 keys a word
+                        const int left = d.last_key + 1 - (d.t0 + j) * kTile - 32 * lane;
+                        uint32_t m = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
+                        if (B >= 32) {
+                            if (!((mine >> (32 * lane / B)) & 1u)) m = 0u;
+                        } else {
+                            const int per = 32 / B;
+                            for (int b = 0; b < per; ++b)
+                                if (!((mine >> (lane * per + b)) & 1u)) m &= ~(((1u << B) - 1u) << (b * B));
+                        }
+                        mask[slot * 4 + lane] = m;
+                    }
+                    if (lane == 0) reinterpret_cast<float*>(smem + kR)[slot] = R;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bars.info(slot));
+                }
+                if (l == 0) raw_next = load_raw(chunk + 1);
+                if (l == 1) sc_next = load_scales(raw_next);
+            }
+        }
+        if (lane == 0) {
+            if (!ok) count_error(p.error_count);
+            if (!drain_ring(v_side ? bars.v_full(0) : bars.k_full(0), v_side ? kVStages : kKStages, g))
+                count_error(p.error_count);
+        }
+        __syncwarp();
+    } else if (warp == kMmaWarp) {
+        // ============================================================ MMA issuer
+        constexpr uint32_t idesc_s = umma_idesc_e4m3(128, 128, false, false);
+        // kind::f16 with f16 operands (format 0), V MN-major
+        constexpr uint32_t idesc_o = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
+        const uint64_t dq0 = umma_desc_sw128(smem_u32(smem + kQ), 16, 1024);
+        const uint64_t dk0 = umma_desc_sw128(smem_u32(smem + kK), 16, 1024);
+        const uint64_t dv0 = umma_desc_sw128(smem_u32(smem + kVh), kHalfBytes, 1024);
+        uint32_t g = 0, items = 0;   // key tiles and items with keys before this one
+        uint32_t done[2] = {0, 0};   // tiles of each group whose P V has been issued
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (ok && !mbar_wait_warp(bar, parity)) ok = false;
+            return ok;
+        };
+        for (long long c = 0; c < passes && ok; ++c) {
+            Item d;
+            if (!describe(c, d) || d.nt == 0) continue;
+            const int qb = items & 1;
+            auto issue_qk = [&](int j) {  // S of tile j, into its group's buffer, which the last P V has left
+                const uint32_t t = g + j, st = t % kKStages;
+                if (!wait(bars.k_full(st), (t / kKStages) & 1)) return;
+                tc_fence_after();
+#pragma unroll
+                for (int term = 0; term < 2; ++term)
+#pragma unroll
+                    for (int k = 0; k < kD / 32; ++k)
+                        umma_e4m3_warp(tmem + (j & 1) * 128,
+                                       dq0 + (uint64_t)(((qb * 2 + term) * kCodes + k * 32) >> 4),
+                                       dk0 + (uint64_t)((st * kCodes + k * 32) >> 4), idesc_s, term + k > 0);
+                umma_commit_warp(bars.s_full(j & 1));
+                umma_commit_warp(bars.k_empty(st));
+                if (j == d.nt - 1) umma_commit_warp(bars.q_empty(qb));
+            };
+            if (!wait(bars.q_full(items % kQSlots), (items / kQSlots) & 1)) break;
+            issue_qk(0);
+            if (d.nt > 1) issue_qk(1);
+            // the last item's epilogue has read both O
+            if (items > 0) wait(bars.o_free(), (items - 1) & 1);
+            for (int j = 0; j < d.nt && ok; ++j) {
+                const uint32_t t = g + j, vh = t % kVhStages;
+                const int x = j & 1;
+                if (!wait(bars.vh_full(vh), (t / kVhStages) & 1)) break;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {  // 64 keys: P in columns 64 h .. 64 h + 31 of the group's S
+                    if (!wait(bars.p_full(x, h), done[x] & 1)) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        umma_bf16_ta_warp(tmem + 256 + x * 128, tmem + x * 128 + h * 64 + k * 8,
+                                          dv0 + (uint64_t)((vh * 2 * kHalfBytes + (h * 4 + k) * 16 * 128) >> 4),
+                                          idesc_o, j > 1 || h > 0 || k > 0);
+                    umma_commit_warp(bars.o_done(x, h));
+                }
+                umma_commit_warp(bars.vh_empty(vh));
+                ++done[x];
+                if (ok && j + 2 < d.nt) issue_qk(j + 2);
+            }
+            g += d.nt;
+            ++items;
+        }
+        if (!ok && lane == 0) count_error(p.error_count);
+        umma_commit_warp(bars.drain());  // no MMA is running when the tensor memory is freed
+        if (!mbar_wait_warp(bars.drain(), 0) && lane == 0) count_error(p.error_count);
+        __syncwarp();
+    } else if (warp >= kConvWarp) {
+        // ============================================================ converters
+        const int w = warp - kConvWarp;
+        uint32_t g = 0, items = 0;
+        // rows w, w + 4, ... of an item's query tile: two e4m3 terms, and the factor that undoes their scaling
+        auto split_rows = [&](const Item& d, uint32_t item, int from, int to) {
+            const int qb = item & 1;
+            uint8_t* tile = smem + kQ + qb * 2 * kCodes;
+            for (int i = from; i < to; i += 4) {
+                uint2 x[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int r = (i + u) * 4 + w, pos = r / G;
+                    x[u] = make_uint2(0u, 0u);
+                    if (pos < d.nq)
+                        x[u] = __ldg(reinterpret_cast<const uint2*>(
+                                         static_cast<const __nv_bfloat16*>(p.q) +
+                                         ((size_t)(d.r0 + d.i0 + pos) * p.num_q_heads + (size_t)d.kvh * G + r % G) * kD) +
+                                     lane);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int r = (i + u) * 4 + w;
+                    const uint32_t m2 = __vmaxu2(x[u].x & 0x7FFF7FFFu, x[u].y & 0x7FFF7FFFu);
+                    const uint32_t am = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
+                    const int e = min(134 - (int)(am >> 7), 126);  // |x| 2^e in [128, 256)
+                    // a negative softmax scale negates the queries, so that scores only meet positive factors
+                    const float f = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), p.scale_log2);
+                    const float v[4] = {__uint_as_float(x[u].x << 16) * f, __uint_as_float(x[u].x & 0xFFFF0000u) * f,
+                                        __uint_as_float(x[u].y << 16) * f, __uint_as_float(x[u].y & 0xFFFF0000u) * f};
+                    uint32_t hi = 0, lo = 0;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const uint16_t c = pack_e4m3x2(v[2 * q], v[2 * q + 1]);
+                        const float2 b = e4m3x2_to_float2(c);
+                        hi |= (uint32_t)c << (16 * q);
+                        lo |= (uint32_t)pack_e4m3x2(v[2 * q] - b.x, v[2 * q + 1] - b.y) << (16 * q);
+                    }
+                    const int at = r * kD + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+                    *reinterpret_cast<uint32_t*>(tile + at) = hi;
+                    *reinterpret_cast<uint32_t*>(tile + kCodes + at) = lo;
+                    if (lane == 0)
+                        reinterpret_cast<float*>(smem + kQf)[item % kQSlots * kTile + r] =
+                            __uint_as_float((uint32_t)(127 - e) << 23);
+                }
+            }
+        };
+        auto finish_q = [&](uint32_t item) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.q_full(item % kQSlots));
+        };
+        // the next item with keys after pass c
+        auto next_item = [&](long long c, Item& d) {
+            for (++c; c < passes; ++c)
+                if (describe(c, d) && d.nt > 0) return c;
+            return passes;
+        };
+        Item d, nx;
+        long long c = next_item(-1, d);
+        if (c < passes) {
+            split_rows(d, 0, 0, 32);
+            finish_q(0);
+        }
+        while (c < passes && ok) {
+            const long long c2 = next_item(c, nx);
+            int rows = 0;  // rows of the next item's tile that are split (of this warp's 32)
+            for (int j = 0; j < d.nt; ++j, ++g) {
+                const uint32_t vs = g % kVStages, vh = g % kVhStages;
+                if (!mbar_wait_warp(bars.info(g % kInfo), (g / kInfo) & 1) ||
+                    (g >= kVhStages && !mbar_wait_warp(bars.vh_empty(vh), ((g / kVhStages) - 1) & 1)) ||
+                    !mbar_wait_warp(bars.v_full(vs), (g / kVStages) & 1)) {
+                    ok = false;
+                    break;
+                }
+                // a lane widens 16 codes of a key; 8 lanes a key, so a warp takes keys 4 i + (lane / 8)
+                const uint8_t* src = smem + kV + vs * kCodes;
+                uint8_t* dst = smem + kVh + vh * 2 * kHalfBytes;
+                const int ch = lane & 7;
+                const uint32_t* m = mask + (g % kInfo) * 4;
+#pragma unroll 4
+                for (int i = 0; i < kTile / 16; ++i) {
+                    const int key = (i * 4 + w) * 4 + (lane >> 3);
+                    uint4 x = *reinterpret_cast<const uint4*>(src + key * kD + ((ch ^ (key & 7)) << 4));
+                    if (!((m[key >> 5] >> (key & 31)) & 1u)) x = make_uint4(0u, 0u, 0u, 0u);
+                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                    uint32_t out[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        out[2 * k] = e4m3x2_to_f16x2(in[k] & 0xFFFFu);
+                        out[2 * k + 1] = e4m3x2_to_f16x2(in[k] >> 16);
+                    }
+                    uint8_t* row = dst + (ch >> 2) * kHalfBytes + key * 128;
+                    const int c0 = (ch & 3) * 2;
+                    *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
+                    *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) =
+                        make_uint4(out[4], out[5], out[6], out[7]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(bars.vh_full(vh));
+                    mbar_arrive(bars.v_empty(vs));
+                }
+                // between tiles, a quarter of the next item's query rows; its buffer is free once the item before
+                // this one is through its last S
+                if (c2 < passes && rows < 32) {
+                    if (rows == 0 && items > 0 && !mbar_wait_warp(bars.q_empty((items + 1) & 1), ((items - 1) >> 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    split_rows(nx, items + 1, rows, rows + 8);
+                    rows += 8;
+                    if (rows == 32) finish_q(items + 1);
+                }
+            }
+            if (!ok) break;
+            if (c2 < passes && rows < 32) {  // (rows > 0: an item with keys has a tile)
+                split_rows(nx, items + 1, rows, 32);
+                finish_q(items + 1);
+            }
+            ++items;
+            c = c2;
+            d = nx;
+        }
+        if (!ok && lane == 0) count_error(p.error_count);
+    } else {
+        // ============================================================ softmax and output
+        // Every thread runs every tile and the named barrier, even after a wait timed out.
+        const int x = warp >> 2;                       // group
+        const int r = (warp & 3) * 32 + lane;          // row = tensor-memory lane
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t t_s = tmem + lanes + x * 128, t_o = tmem + lanes + 256 + x * 128;
+        float4* state = reinterpret_cast<float4*>(smem + kState);
+        uint32_t g = 0, items = 0, done = 0;  // key tiles, items with keys, tiles of this group
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (ok && !mbar_wait_warp(bar, parity)) ok = false;
+        };
+        for (long long c = 0; c < passes; ++c) {
+            Item d;
+            if (!describe(c, d)) continue;
+            const int pos = d.i0 + min(r / G, d.nq - 1);  // (unused rows mask as the last used one)
+            const bool row_ok = r / G < d.nq;
+            const int my_last = min(d.start + pos, d.last_key);
+            float m = -INFINITY, l = 0.f, Rc = 1.f, qf = 0.f;
+            if (d.nt > 0) {
+                wait(bars.q_full(items % kQSlots), (items / kQSlots) & 1);
+                qf = reinterpret_cast<const float*>(smem + kQf)[items % kQSlots * kTile + r];
+            }
+            for (int j = x; j < d.nt; j += 2, ++done) {
+                const uint32_t t = g + j;
+                const int slot = t % kInfo;
+                wait(bars.info(slot), (t / kInfo) & 1);
+                const float4* consts = reinterpret_cast<const float4*>(smem + kConsts) + slot * 16;
+                const float R = reinterpret_cast<const float*>(smem + kR)[slot];
+                uint32_t vm[4];
+#pragma unroll
+                for (int w = 0; w < 4; ++w) vm[w] = mask[slot * 4 + w];
+                wait(bars.s_full(x), done & 1);
+                tc_fence_after();
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    float s[64];
+                    {
+                        float a[32];
+                        tmem_ld32(t_s + h * 64, a);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) s[i] = a[i];
+                        float b[32];
+                        tmem_ld32(t_s + h * 64 + 32, b);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) s[32 + i] = b[i];
+                    }
+                    tmem_wait_ld();
+                    const int key0 = (d.t0 + j) * kTile + h * 64;
+                    const uint32_t m0 = h ? vm[2] : vm[0], m1 = h ? vm[3] : vm[1];
+                    const float4* kc = consts + h * 8;
+                    // dense: every key is valid and every row of the warp sees it
+                    const bool dense = __all_sync(0xffffffffu, (m0 & m1) == ~0u && key0 + 63 <= my_last);
+                    float mx[8];
+                    if (dense) {
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            const float u = fmax3(s[8 * b], s[8 * b + 1], s[8 * b + 2]);
+                            const float v = fmax3(s[8 * b + 3], s[8 * b + 4], s[8 * b + 5]);
+                            mx[b] = fmax3(u, v, fmaxf(s[8 * b + 6], s[8 * b + 7])) * (kc[b].x * qf);
+                        }
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            const float a = kc[b].x * qf;
+                            mx[b] = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int k = 8 * b + i;
+                                const bool valid = (((k < 32 ? m0 : m1) >> (k & 31)) & 1u) && key0 + k <= my_last;
+                                s[k] = valid ? s[k] * a : -INFINITY;
+                                mx[b] = fmaxf(mx[b], s[k]);
+                            }
+                        }
+                    }
+                    const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
+                    const bool first = j == x && h == 0;  // nothing in O yet
+                    if (first) Rc = R;
+                    const float m_new = mt > m + kLazy ? mt : m;  // also the first finite maximum
+                    if (!first && __any_sync(0xffffffffu, m_new != m || R != Rc)) {
+                        // the products issued so far have to be done before O changes
+                        if (h) wait(bars.o_done(x, 0), done & 1);
+                        else wait(bars.o_done(x, 1), (done - 1) & 1);
+                        tc_fence_after();
+                        const float alpha = m_new == m ? 1.f : fast_exp2(m - m_new), f = alpha * (Rc / R);
+#pragma unroll 1
+                        for (int q = 0; q < 8; ++q) {
+                            float o[16];
+                            tmem_ld16(t_o + q * 16, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) o[i] *= f;
+                            tmem_st16(t_o + q * 16, o);
+                        }
+                        tmem_wait_st();
+                        l *= alpha;
+                        Rc = R;
+                    }
+                    m = m_new;
+                    uint32_t pk[32];
+                    float sum = 0.f;
+                    if (dense) {
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            const float4 k4 = kc[b];
+                            const float a = k4.x * qf, o = k4.y - m;
+                            const unsigned long long a2 = f32x2_pack(a, a), o2 = f32x2_pack(o, o);
+                            float e[8];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                float y0, y1;
+                                f32x2_unpack(fma_f32x2(f32x2_pack(s[8 * b + 2 * i], s[8 * b + 2 * i + 1]), a2, o2), y0, y1);
+                                e[2 * i] = fast_exp2(y0);
+                                e[2 * i + 1] = fast_exp2(y1);
+                                pk[4 * b + i] = pack_f16x2(e[2 * i], e[2 * i + 1]);
+                            }
+                            float u, v;
+                            f32x2_unpack(add_f32x2(add_f32x2(f32x2_pack(e[0], e[1]), f32x2_pack(e[2], e[3])),
+                                                   add_f32x2(f32x2_pack(e[4], e[5]), f32x2_pack(e[6], e[7]))), u, v);
+                            sum = fmaf(u + v, k4.z, sum);
+                        }
+                    } else {
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            const float4 k4 = kc[b];
+                            const float o = k4.y - m;
+                            float g8 = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float s0 = s[8 * b + 2 * i], s1 = s[8 * b + 2 * i + 1];
+                                const float e0 = s0 == -INFINITY ? 0.f : fast_exp2(s0 + o);
+                                const float e1 = s1 == -INFINITY ? 0.f : fast_exp2(s1 + o);
+                                pk[4 * b + i] = pack_f16x2(e0, e1);
+                                g8 += e0 + e1;
+                            }
+                            sum = fmaf(g8, k4.z, sum);
+                        }
+                    }
+                    l += sum;
+                    tmem_st32u(t_s + h * 64, pk);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0 && ok) mbar_arrive(bars.p_full(x, h));
+                }
+            }
+            // ---- the item's output: both groups' states joined, each group stores 64 columns of the row
+            float mo = -INFINITY, lo = 0.f, Ro = 1.f;
+            if (d.nt > 0) {
+                if (d.nt > x) {
+                    wait(bars.o_done(x, 1), (done - 1) & 1);
+                    tc_fence_after();
+                }
+                // (two copies by item: a group without a tile in the next item may be there already)
+                float4* st = state + (items & 1) * 2 * kTile;
+                st[x * kTile + r] = make_float4(m, l, Rc, 0.f);
+                tc_fence_before();
+                asm volatile("bar.sync 2, 256;" ::: "memory");
+                tc_fence_after();
+                const float4 o = st[(x ^ 1) * kTile + r];
+                mo = o.x;
+                lo = o.y;
+                Ro = o.z;
+            }
+            const float M = fmaxf(m, mo);
+            // (the weight of a state without a valid key is 0, and its O is not looked at)
+            const float w_own = m == -INFINITY ? 0.f : fast_exp2(m - M), w_oth = mo == -INFINITY ? 0.f : fast_exp2(mo - M);
+            const float L = w_own * l + w_oth * lo, inv = L == 0.f ? 0.f : 1.f / L;
+            const float f_own = w_own * Rc * inv, f_oth = w_oth * Ro * inv;
+            const bool use_own = w_own != 0.f, use_oth = w_oth != 0.f;
+            const size_t row = ((size_t)(d.r0 + pos) * p.num_q_heads + (size_t)d.kvh * G + r % G);
+            const bool direct = d.spans == 1;
+            const size_t part = (size_t)d.span * p.total_q * p.num_q_heads + row;
+            const uint32_t t_oth = tmem + lanes + 256 + (x ^ 1) * 128;
+            if (!direct && row_ok && x == 0) spans.ml[part] = make_float2(M, L);
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                const int col = x * 64 + q * 16;
+                float o[16];
+                if (d.nt > 0) {
+                    float a[16], b[16];
+                    tmem_ld16(t_o + col, a);
+                    tmem_ld16(t_oth + col, b);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = (use_own ? a[i] * f_own : 0.f) + (use_oth ? b[i] * f_oth : 0.f);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+                }
+                if (!row_ok) continue;
+                if (direct) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
+                    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * kD + col;
+                    if ((reinterpret_cast<uintptr_t>(p.out) & 31u) == 0) {
+                        store32(out, w);
+                    } else {
+                        reinterpret_cast<uint4*>(out)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                        reinterpret_cast<uint4*>(out)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(o[8 * k + i]);
+                        store32(spans.o + part * kD + col + 8 * k, w);
+                    }
+                }
+            }
+            if (d.nt > 0) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0 && ok) mbar_arrive(bars.o_free());
+                ++items;
+            }
+            g += d.nt;
+        }
+        if (!ok && lane == 0) count_error(p.error_count);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the spans of a tile's rows: a warp per (row, query head), a float4 of columns per lane, in span order.
+__global__ void __launch_bounds__(128) prefill_fp8_block_join_kernel(const PrefillParams p, const Spans spans) {
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, G = p.group, ppt = kTile / G;
+    const long long rows = (long long)p.total_q * p.num_q_heads, stride = (long long)gridDim.x * 4;
+    for (long long u = (long long)blockIdx.x * 4 + (threadIdx.x >> 5); u < rows; u += stride) {
+        const int q = (int)(u / p.num_q_heads);
+        // the chunk of row q: the largest c with cu_q_lens[c] <= q
+        int lo = 0, hi = p.num_chunks - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (p.cu_q_lens[mid] <= q) lo = mid; else hi = mid - 1;
+        }
+        int r0, n, s, start;
+        if (!chunk_of(p, lo, r0, n, s, start) || q < r0 || q >= r0 + n) continue;
+        const int tile_end = min((q - r0) / ppt * ppt + ppt, n);  // as the kernel above cuts the chunk
+        const int last = min((int)min((long long)start + tile_end - 1, 0x7FFFFFFELL), key_cap(p, s) - 1);
+        const int all = last >= 0 ? last / kTile + 1 : 0, count = max(1, (all + spans.tiles - 1) / spans.tiles);
+        if (count == 1) continue;  // stored directly
+        float m = -INFINITY;
+        for (int i = lane; i < count; i += 32) {
+            const float2 v = __ldcg(spans.ml + (size_t)i * rows + u);
+            if (v.y != 0.f) m = fmaxf(m, v.x);
+        }
+        m = warp_max(m);
+        float wsum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = 0; i < count; ++i) {
+            const float2 v = __ldcg(spans.ml + (size_t)i * rows + u);
+            const float4 o = __ldcg(reinterpret_cast<const float4*>(spans.o + ((size_t)i * rows + u) * kD) + lane);
+            const float w = v.y != 0.f ? v.y * exp2f(v.x - m) : 0.f;
+            wsum += w;
+            acc.x = fmaf(w, o.x, acc.x);
+            acc.y = fmaf(w, o.y, acc.y);
+            acc.z = fmaf(w, o.z, acc.z);
+            acc.w = fmaf(w, o.w, acc.w);
+        }
+        const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + u * kD + lane * 4) =
+            make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    }
+}
+
+long long work_items(int num_chunks, int max_q_len, int num_kv_heads, int group) {
+    const int ppt = kTile / group;
+    return (long long)((max_q_len + ppt - 1) / ppt) * num_chunks * num_kv_heads;
+}
+
+// Key tiles per span and spans per query tile: the keys are cut when the tiles alone would not give every SM two
+// items, into spans of at least four key tiles (a span's partial rows cost about half a key tile's time to store and
+// join).  The count comes from the largest context, the lengths live on the device.
+Spans plan_spans(int num_chunks, int max_q_len, int num_kv_heads, int group, int max_context_len, int num_sms) {
+    const int tiles = max_context_len > 0 ? (max_context_len - 1) / kTile + 1 : 1;
+    const long long items = work_items(num_chunks, max_q_len, num_kv_heads, group);
+    long long want = items > 0 ? (2LL * num_sms) / items : 1;
+    if (want > tiles / 4) want = tiles / 4;
+    Spans s{};
+    s.tiles = tiles;
+    if (want > 1) s.tiles = (int)((tiles + want - 1) / want);
+    s.count = (tiles + s.tiles - 1) / s.tiles;
+    return s;
+}
+
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+}  // namespace
+
+size_t prefill_fp8_block_workspace(int num_chunks, int total_q, int max_q_len, int num_q_heads, int num_kv_heads,
+                                   int max_context_len, int num_sms) {
+    const Spans s =
+        plan_spans(num_chunks, max_q_len, num_kv_heads, num_q_heads / num_kv_heads, max_context_len, num_sms);
+    if (s.count <= 1) return 0;
+    const size_t rows = (size_t)s.count * total_q * num_q_heads;
+    return up256(rows * kD * sizeof(float)) + up256(rows * sizeof(float2));
+}
+
+bool prefill_fp8_block_tc_supported(const PrefillParams& p) {
+    const int B = p.block_size;
+    if (p.head_dim != kD || p.group > 8 || B < 8 || B > 128 || (B & (B - 1)) != 0) return false;
+    if (((uintptr_t)p.k_cache & 15) || ((uintptr_t)p.v_cache & 15) || ((uintptr_t)p.q & 15) || ((uintptr_t)p.out & 15))
+        return false;
+    return (long long)p.num_blocks * B < (1LL << 31) && p.num_blocks > 0;
+}
+
+int launch_prefill_fp8_block_tc(const PrefillParams& p, void* workspace, int num_sms, cudaStream_t stream) {
+    CUtensorMap tmk, tmv;
+    int rc = pool_tensor_map_rows(&tmk, p.k_cache, p.num_blocks, p.block_size, p.num_kv_heads, kD, true);
+    if (rc != PA_OK) return rc;
+    if ((rc = pool_tensor_map_rows(&tmv, p.v_cache, p.num_blocks, p.block_size, p.num_kv_heads, kD, true)) != PA_OK)
+        return rc;
+    if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(prefill_fp8_block_tc_kernel), kSmemBytes)) != PA_OK)
+        return rc;
+    Spans s = plan_spans(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group, p.max_context_len, num_sms);
+    if (s.count > 1) {
+        const size_t rows = (size_t)s.count * p.total_q * p.num_q_heads;
+        s.o = static_cast<float*>(workspace);
+        s.ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + up256(rows * kD * sizeof(float)));
+    }
+    const long long items = work_items(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group) * s.count;
+    rc = launch_kernel(prefill_fp8_block_tc_kernel, dim3((unsigned)(items < num_sms ? items : num_sms)),
+                       dim3(kThreads), kSmemBytes, stream, tmk, tmv, p, s);
+    if (rc != PA_OK || s.count <= 1) return rc;
+    const long long warps = (long long)p.total_q * p.num_q_heads, ctas = (warps + 3) / 4;
+    return launch_kernel(prefill_fp8_block_join_kernel, dim3((unsigned)(ctas < 16LL * num_sms ? ctas : 16LL * num_sms)),
+                         dim3(128), 0, stream, p, s);
+}
+
+}  // namespace pa
