@@ -390,29 +390,50 @@ def pa_prefill_chunk(q, cu_q_lens, q_start_pos, seq_of_chunk, max_q_len: int, k_
 
 
 def _fp8_block_pools(k_cache, v_cache, k_scales, v_scales):
-    """Shapes of e4m3 pools with a scale per (block, kv head): (P, B, Hkv, D), checked."""
-    if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8:
+    """Shapes of e4m3 pools with a scale per (block, kv head), checked: (P, B, Hkv, D, device index)."""
+    if k_cache.dtype is not torch.uint8 or v_cache.dtype is not torch.uint8:
         raise TypeError("fp8 pools are uint8 tensors of e4m3 codes")
-    P, B, H, D = k_cache.shape
-    if v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    P, B, H, D = shape
+    if v_cache.shape != shape:
         raise ValueError("shapes of k_cache and v_cache differ")
-    for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-        if tuple(t.shape) != (P, H):
-            raise ValueError(f"{name} must be [num_blocks, num_kv_heads] = [{P}, {H}], got {list(t.shape)}")
-    return P, B, H, D
+    if k_scales.shape != (P, H) or v_scales.shape != (P, H):
+        raise ValueError(f"k_scales and v_scales must be [num_blocks, num_kv_heads] = [{P}, {H}], got "
+                         f"{list(k_scales.shape)} and {list(v_scales.shape)}")
+    return P, B, H, D, k_cache.get_device()
 
 
-def _same_device(first, **others):
-    """Every given tensor is on `first`'s device (or, an output, in pinned host memory)."""
-    for name, t in others.items():
-        if t is not None and t.is_cuda and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, the pools on {first.device}")
+def _on(t, name: str, dtype, dev: int, host_ok: bool = False):
+    """Pointer of a contiguous tensor of `dtype` on device `dev` (or, with host_ok, in pinned host memory).  The same
+    checks as _dev and the pools' device, in few calls: they are most of a small call's host time."""
+    if t is None:
+        return None
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev and not (host_ok and t.is_pinned()):
+        raise ValueError(f"{name} must be a CUDA tensor on the pools' device" +
+                         (" or pinned host memory" if host_ok else ""))
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
-def _ws(workspace):
-    if workspace is None:
-        return None, 0
-    return _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+def _ws_on(workspace, dev: int):
+    return (None, 0) if workspace is None else (_on(workspace, "workspace", torch.uint8, dev), workspace.numel())
+
+
+def _call(name: str, dev: int, stream, args) -> None:
+    """One library call with device `dev` current, on `stream` (None: the device's current stream)."""
+    if dev < 0:
+        raise ValueError("the pools must be CUDA tensors")
+    fn = getattr(_lib or lib(), name)
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
+    if status != PA_OK:
+        _check(name, status)
 
 
 def new_write_fp8_block_workspace(num_tokens, num_blocks, block_size, device=None) -> torch.Tensor | None:
@@ -427,24 +448,20 @@ def pa_write_kv_paged_fp8_block(k_new, v_new, k_cache, v_cache, k_scales, v_scal
     write: the smallest power of two that holds the rows stored into the block, never below the block's scale from
     before unless the block's first slot is stored; the block's other codes keep their values."""
     T, H, D = k_new.shape
-    P, B, H2, D2 = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
+    P, B, H2, D2, dev = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
     if (H, D) != (H2, D2) or v_new.shape != k_new.shape:
         raise ValueError("shapes of k_new, v_new and the pools disagree")
     if seq_idx.numel() != T or pos.numel() != T or (slot_mapping is not None and slot_mapping.numel() != T):
         raise ValueError(f"seq_idx, pos and slot_mapping must have one entry for each of the {T} tokens")
-    _same_device(k_cache, k_new=k_new, v_new=v_new, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales,
-                 block_tables=block_tables, seq_idx=seq_idx, pos=pos, workspace=workspace, slot_mapping=slot_mapping,
-                 error_count=error_count)
     S, W = block_tables.shape
-    ws, ws_bytes = _ws(workspace)
-    with torch.cuda.device(k_cache.device):
-        _check("pa_write_kv_paged_fp8_block", lib().pa_write_kv_paged_fp8_block(
-            _dev(k_new, "k_new", torch.bfloat16), _dev(v_new, "v_new", torch.bfloat16), T, H, D,
-            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(k_scales, "k_scales", torch.float32),
-            _dev(v_scales, "v_scales", torch.float32), P, B, _dev(block_tables, "block_tables", torch.int32), S, W,
-            _dev(seq_idx, "seq_idx", torch.int32), _dev(pos, "pos", torch.int32),
-            _dev(slot_mapping, "slot_mapping", torch.int64), ws, ws_bytes,
-            _dev(error_count, "error_count", torch.int32), _stream(stream)))
+    i32, f32, u8, bf16 = torch.int32, torch.float32, torch.uint8, torch.bfloat16
+    ws, ws_bytes = _ws_on(workspace, dev)
+    _call("pa_write_kv_paged_fp8_block", dev, stream, (
+        _on(k_new, "k_new", bf16, dev), _on(v_new, "v_new", bf16, dev), T, H, D, _on(k_cache, "k_cache", u8, dev),
+        _on(v_cache, "v_cache", u8, dev), _on(k_scales, "k_scales", f32, dev), _on(v_scales, "v_scales", f32, dev),
+        P, B, _on(block_tables, "block_tables", i32, dev), S, W, _on(seq_idx, "seq_idx", i32, dev),
+        _on(pos, "pos", i32, dev), _on(slot_mapping, "slot_mapping", torch.int64, dev), ws, ws_bytes,
+        _on(error_count, "error_count", i32, dev)))
     return slot_mapping
 
 
@@ -453,24 +470,24 @@ def pa_read_kv_paged_fp8_block(k_cache, v_cache, k_scales, v_scales, block_table
     """(K rows, V rows), each [T, Hkv, D] of `dtype` (bfloat16 or float32): code * scale of the token at pos[t] of
     sequence seq_idx[t].  Rows with pos < 0 or an invalid index are left as they were (uninitialised where no k_out /
     v_out is given)."""
-    P, B, H, D = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
+    P, B, H, D, dev = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
     T = seq_idx.numel()
     if pos.numel() != T:
         raise ValueError("seq_idx and pos differ in length")
-    k_out = torch.empty(T, H, D, dtype=dtype, device=k_cache.device) if k_out is None else k_out
-    v_out = torch.empty(T, H, D, dtype=k_out.dtype, device=k_cache.device) if v_out is None else v_out
-    if tuple(k_out.shape) != (T, H, D) or tuple(v_out.shape) != (T, H, D) or v_out.dtype != k_out.dtype:
+    if k_out is None:
+        k_out = torch.empty((T, H, D), dtype=dtype if v_out is None else v_out.dtype, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty_like(k_out)
+    dt = k_out.dtype
+    if k_out.shape != (T, H, D) or v_out.shape != (T, H, D) or v_out.dtype is not dt:
         raise ValueError(f"k_out and v_out must be [{T}, {H}, {D}] of one dtype")
-    _same_device(k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales, block_tables=block_tables,
-                 seq_idx=seq_idx, pos=pos, k_out=k_out, v_out=v_out, error_count=error_count)
     S, W = block_tables.shape
-    with torch.cuda.device(k_cache.device):
-        _check("pa_read_kv_paged_fp8_block", lib().pa_read_kv_paged_fp8_block(
-            _dev(k_out, "k_out"), _dev(v_out, "v_out"), T, H, D, _dtype_code(k_out), _dev(k_cache, "k_cache"),
-            _dev(v_cache, "v_cache"), _dev(k_scales, "k_scales", torch.float32),
-            _dev(v_scales, "v_scales", torch.float32), P, B, _dev(block_tables, "block_tables", torch.int32), S, W,
-            _dev(seq_idx, "seq_idx", torch.int32), _dev(pos, "pos", torch.int32),
-            _dev(error_count, "error_count", torch.int32), _stream(stream)))
+    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+    _call("pa_read_kv_paged_fp8_block", dev, stream, (
+        _on(k_out, "k_out", dt, dev), _on(v_out, "v_out", dt, dev), T, H, D, _dtype_code(k_out),
+        _on(k_cache, "k_cache", u8, dev), _on(v_cache, "v_cache", u8, dev), _on(k_scales, "k_scales", f32, dev),
+        _on(v_scales, "v_scales", f32, dev), P, B, _on(block_tables, "block_tables", i32, dev), S, W,
+        _on(seq_idx, "seq_idx", i32, dev), _on(pos, "pos", i32, dev), _on(error_count, "error_count", i32, dev)))
     return k_out, v_out
 
 
@@ -488,23 +505,21 @@ def pa_decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, c
                         scale: float, workspace, out=None, error_count=None, stream=None) -> torch.Tensor:
     """pa_decode over uint8 e4m3 pools with a scale per (block, kv head); q and out bf16."""
     N, Hq, D = q.shape
-    P, B, Hkv, D2 = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
+    P, B, Hkv, D2, dev = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
     if D2 != D:
         raise ValueError("head_dim of q and k_cache differ")
     if out is None:
         out = torch.empty_like(q)
-    if out.shape != q.shape or block_tables.shape[0] != N or context_lens.numel() != N:
+    S, W = block_tables.shape
+    if out.shape != q.shape or S != N or context_lens.numel() != N:
         raise ValueError("shapes of q, out, block_tables and context_lens disagree")
-    _same_device(k_cache, q=q, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales, block_tables=block_tables,
-                 context_lens=context_lens, workspace=workspace, out=out, error_count=error_count)
-    ws, ws_bytes = _ws(workspace)
-    with torch.cuda.device(k_cache.device):
-        _check("pa_decode_fp8_block", lib().pa_decode_fp8_block(
-            _dev(out, "out", torch.bfloat16, host_ok=True), _dev(q, "q", torch.bfloat16), N, Hq, Hkv, D,
-            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(k_scales, "k_scales", torch.float32),
-            _dev(v_scales, "v_scales", torch.float32), P, B, _dev(block_tables, "block_tables", torch.int32),
-            block_tables.shape[1], _dev(context_lens, "context_lens", torch.int32), int(max_context_len),
-            float(scale), ws, ws_bytes, _dev(error_count, "error_count", torch.int32), _stream(stream)))
+    i32, f32, u8, bf16 = torch.int32, torch.float32, torch.uint8, torch.bfloat16
+    ws, ws_bytes = _ws_on(workspace, dev)
+    _call("pa_decode_fp8_block", dev, stream, (
+        _on(out, "out", bf16, dev, True), _on(q, "q", bf16, dev), N, Hq, Hkv, D, _on(k_cache, "k_cache", u8, dev),
+        _on(v_cache, "v_cache", u8, dev), _on(k_scales, "k_scales", f32, dev), _on(v_scales, "v_scales", f32, dev),
+        P, B, _on(block_tables, "block_tables", i32, dev), W, _on(context_lens, "context_lens", i32, dev),
+        int(max_context_len), float(scale), ws, ws_bytes, _on(error_count, "error_count", i32, dev)))
     return out
 
 
@@ -521,7 +536,7 @@ def pa_prefill_chunk_fp8_block(q, cu_q_lens, q_start_pos, seq_of_chunk, max_q_le
                                workspace=None, out=None, error_count=None, stream=None) -> torch.Tensor:
     """Causal chunked-prefill attention over uint8 e4m3 pools with a scale per (block, kv head); q and out bf16."""
     T, Hq, D = q.shape
-    P, B, Hkv, D2 = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
+    P, B, Hkv, D2, dev = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
     if D2 != D:
         raise ValueError("head_dim of q and k_cache differ")
     C = q_start_pos.numel()
@@ -529,21 +544,18 @@ def pa_prefill_chunk_fp8_block(q, cu_q_lens, q_start_pos, seq_of_chunk, max_q_le
         out = torch.empty_like(q)
     if out.shape != q.shape or cu_q_lens.numel() != C + 1 or seq_of_chunk.numel() != C:
         raise ValueError("shapes of q, out, cu_q_lens, q_start_pos and seq_of_chunk disagree")
-    if context_lens.numel() != block_tables.shape[0]:
+    S, W = block_tables.shape
+    if context_lens.numel() != S:
         raise ValueError("shapes of block_tables and context_lens disagree")
-    _same_device(k_cache, q=q, cu_q_lens=cu_q_lens, q_start_pos=q_start_pos, seq_of_chunk=seq_of_chunk,
-                 v_cache=v_cache, k_scales=k_scales, v_scales=v_scales, block_tables=block_tables,
-                 context_lens=context_lens, workspace=workspace, out=out, error_count=error_count)
-    ws, ws_bytes = _ws(workspace)
-    with torch.cuda.device(k_cache.device):
-        _check("pa_prefill_chunk_fp8_block", lib().pa_prefill_chunk_fp8_block(
-            _dev(out, "out", torch.bfloat16, host_ok=True), _dev(q, "q", torch.bfloat16),
-            _dev(cu_q_lens, "cu_q_lens", torch.int32), _dev(q_start_pos, "q_start_pos", torch.int32),
-            _dev(seq_of_chunk, "seq_of_chunk", torch.int32), C, T, int(max_q_len), block_tables.shape[0], Hq, Hkv, D,
-            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(k_scales, "k_scales", torch.float32),
-            _dev(v_scales, "v_scales", torch.float32), P, B, _dev(block_tables, "block_tables", torch.int32),
-            block_tables.shape[1], _dev(context_lens, "context_lens", torch.int32), int(max_context_len),
-            float(scale), ws, ws_bytes, _dev(error_count, "error_count", torch.int32), _stream(stream)))
+    i32, f32, u8, bf16 = torch.int32, torch.float32, torch.uint8, torch.bfloat16
+    ws, ws_bytes = _ws_on(workspace, dev)
+    _call("pa_prefill_chunk_fp8_block", dev, stream, (
+        _on(out, "out", bf16, dev, True), _on(q, "q", bf16, dev), _on(cu_q_lens, "cu_q_lens", i32, dev),
+        _on(q_start_pos, "q_start_pos", i32, dev), _on(seq_of_chunk, "seq_of_chunk", i32, dev), C, T,
+        int(max_q_len), S, Hq, Hkv, D, _on(k_cache, "k_cache", u8, dev), _on(v_cache, "v_cache", u8, dev),
+        _on(k_scales, "k_scales", f32, dev), _on(v_scales, "v_scales", f32, dev), P, B,
+        _on(block_tables, "block_tables", i32, dev), W, _on(context_lens, "context_lens", i32, dev),
+        int(max_context_len), float(scale), ws, ws_bytes, _on(error_count, "error_count", i32, dev)))
     return out
 
 
