@@ -26,19 +26,22 @@
 // 2^-40 are held there: such a weight is 0 in f16, and its P' still counts in
 // the sum.
 //
-// Two softmax groups of four warps, a thread per row, take alternate key
-// tiles, each with its own S, running maximum, sum and O; while one group is at
-// its exponentials the tensor cores run the other's products.  The groups'
-// states are joined once per item.  A group passes P on in halves of 64 keys,
-// so that the first half's product runs under the second half's exponentials.
-// The maximum is lazy: O is rescaled only when it grows by more than 2^8.
+// Two softmax groups of four warps, a thread per row, take alternate pieces of
+// 64 keys (a half of every key tile each), with their own running maximum, sum
+// and O, joined once per item.  S is a ring of three pieces in tensor memory:
+// while a group is at one, its next is there already, so that neither waits for
+// the chain P -> P V -> Q K^T.  The query terms are in tensor memory too: as
+// shared-memory operands they were read again by every product, and shared
+// memory bandwidth set the pace (2.65k cycles per key tile against 1.0k of
+// tensor work).  The maximum is lazy: O is rescaled only when it grows by more
+// than 2^8.
 //
 // Few rows: the plan cuts the keys of a tile into spans, whose partial results
 // (float, in the workspace) a second kernel joins.
 //
 //   warps 0-7   softmax, group w / 4            warp 13  K tiles, masks, scales
 //   warps 8-11  V widening, query terms         warp 14  V tiles
-//   warp 12     tensor memory, MMA issue
+//   warp 12     tensor memory, issue of P V     warp 15  issue of Q K^T
 // Waits are bounded, copies and MMAs drained, as in prefill_tc.cu.
 #include "pa_internal.cuh"
 #include "sm100_ptx.cuh"
@@ -50,18 +53,23 @@ constexpr int kD = 128;
 constexpr int kTile = 128;             // rows of a query tile, keys of a key tile
 constexpr int kCodes = kTile * kD;     // bytes of a tile of codes
 constexpr int kHalfBytes = kTile * 128;  // bytes of a 64-column half of a widened tile
-constexpr int kThreads = 480;
-constexpr int kConverters = 4, kConvWarp = 8, kMmaWarp = 12, kKWarp = 13, kVWarp = 14;
-constexpr int kKStages = 3, kVStages = 2, kVhStages = 2, kInfo = 8;
+constexpr int kThreads = 512;
+constexpr int kConverters = 4, kConvWarp = 8, kMmaWarp = 12, kKWarp = 13, kVWarp = 14, kSWarp = 15;
+constexpr int kKStages = 4, kVStages = 3, kVhStages = 2, kInfo = 8;
 // The converters may be two items ahead of the softmax (items of one key tile), never four: four slots keep an item's
 // query factors, and the phase of its barrier, until the softmax has come to it.
 constexpr int kQSlots = 4;
+constexpr int kPieces = 3;  // ring of S pieces
+constexpr int kItems = 8;   // ring of item descriptions
+// tensor memory columns: O of group 0 and 1, the query terms (hi, lo; four codes a column), the S pieces
+constexpr uint32_t kTO = 0, kTQ = 256, kTS = 320;
 constexpr float kLazy = 8.f;
+constexpr float kTiny = 1e-37f;  // the least factor of a score: 0 would make NaN of a masked key's -inf
 constexpr float kScaleFloor = 7.703719777548943e-34f;  // 2^-110, the smallest R
 
 // shared memory, offsets from a 1024-aligned base
-constexpr int kQ = 0;                                      // [2 items][hi, lo]
-constexpr int kK = kQ + 2 * 2 * kCodes;
+constexpr int kQ = 0;  // [hi, lo][128 rows][128], 16-byte pieces swizzled by row: staged for tensor memory
+constexpr int kK = kQ + 2 * kCodes;
 constexpr int kV = kK + kKStages * kCodes;
 constexpr int kVh = kV + kVStages * kCodes;
 constexpr int kConsts = kVh + kVhStages * 2 * kHalfBytes;  // float4 [kInfo][16]: per 8 keys ks', log2(vs/R), R/vs
@@ -69,11 +77,19 @@ constexpr int kMask = kConsts + kInfo * 16 * 16;           // uint32 [kInfo][4]
 constexpr int kR = kMask + kInfo * 16;                     // float [kInfo]
 constexpr int kQf = kR + kInfo * 4;                        // float [kQSlots][128]
 constexpr int kState = kQf + kQSlots * kTile * 4;          // float4 [2 items][2 groups][128]: m, l, R
-constexpr int kBars = kState + 2 * 2 * kTile * 16;
-constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 2 * kVhStages + 2 + 4 + 4 + kQSlots + 2 + kInfo + 2;
+constexpr int kItem = kState + 2 * 2 * kTile * 16;  // Item [kItems]
+constexpr int kBars = kItem + kItems * 48;
+constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 2 * kVhStages + 3 * kPieces + 2 + kQSlots + 1 + kInfo + 2 * kItems + 3;
 constexpr int kTmemSlot = kBars + kNumBars * 8;
 constexpr size_t kSmemBytes = 1024 + kTmemSlot + 16;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+
+// A work item as the warps pass it on; nt key tiles from tile t0 on, nt < 0: no more items.
+struct Item {
+    int kvh, row, nq, pos;  // kv head; first query (row of q) and their number; position of the first
+    int last_key, t0, nt;   // the tile's last visible key
+    int s, span, spans, pad[2];
+};
 
 struct Bars {
     uint64_t* base;
@@ -83,18 +99,18 @@ struct Bars {
     __device__ uint64_t* v_empty(int i) const { return v_full(kVStages + i); }
     __device__ uint64_t* vh_full(int i) const { return v_full(2 * kVStages + i); }
     __device__ uint64_t* vh_empty(int i) const { return vh_full(kVhStages + i); }
-    __device__ uint64_t* s_full(int x) const { return vh_full(2 * kVhStages + x); }
-    __device__ uint64_t* p_full(int x, int h) const { return s_full(2 + 2 * x + h); }
-    __device__ uint64_t* o_done(int x, int h) const { return s_full(6 + 2 * x + h); }
-    __device__ uint64_t* q_full(int i) const { return s_full(10 + i); }
-    __device__ uint64_t* q_empty(int i) const { return s_full(10 + kQSlots + i); }
-    __device__ uint64_t* info(int i) const { return s_full(12 + kQSlots + i); }
-    __device__ uint64_t* o_free() const { return info(kInfo); }
-    __device__ uint64_t* drain() const { return info(kInfo + 1); }
-};
-
-struct Item {
-    int kvh, r0, s, start, i0, nq, last_key, t0, nt, span, spans;  // key tiles t0 .. t0 + nt - 1
+    __device__ uint64_t* s_full(int i) const { return vh_full(2 * kVhStages + i); }
+    __device__ uint64_t* p_full(int i) const { return s_full(kPieces + i); }
+    __device__ uint64_t* s_empty(int i) const { return s_full(2 * kPieces + i); }
+    __device__ uint64_t* o_done(int x) const { return s_full(3 * kPieces + x); }
+    __device__ uint64_t* q_full(int i) const { return o_done(2 + i); }
+    __device__ uint64_t* q_empty() const { return q_full(kQSlots); }
+    __device__ uint64_t* info(int i) const { return q_full(kQSlots + 1 + i); }
+    __device__ uint64_t* item_full(int i) const { return info(kInfo + i); }
+    __device__ uint64_t* item_empty(int i) const { return item_full(kItems + i); }
+    __device__ uint64_t* o_free() const { return item_full(2 * kItems); }
+    __device__ uint64_t* joined() const { return item_full(2 * kItems + 2); }  // the softmax warps' barrier
+    __device__ uint64_t* drain() const { return item_full(2 * kItems + 1); }  // by both issuing warps
 };
 
 // The kernel's own parameters: the plan's key tiles per span and spans per tile.
@@ -109,6 +125,34 @@ __device__ __forceinline__ void store32(void* ptr, const uint32_t (&v)[8]) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(ptr), "r"(v[0]), "r"(v[1]),
                  "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
+}
+
+// One piece's S (64 keys): two query terms in tensor memory (32 columns each from `a`), four steps of 32 dims, K
+// rows described by (lo, hi).  And one piece's P V: four steps of 16 keys.  Each is one election and its MMAs: the
+// issuing warp shares its scheduler with three busy ones, so its instructions are counted.
+__device__ __forceinline__ void issue_s(uint32_t d, uint32_t a, uint32_t lo, uint32_t hi, uint32_t idesc) {
+#define PA_STEP(A, B, ACC)                                                                     \
+    "add.u32 t, %1, " A ";\n\tadd.u32 l, %2, " B ";\n\tmov.b64 b, {l, %3};\n\t"               \
+    "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [t], b, %4, " ACC ";\n\t"
+    asm volatile(
+        "{\n\t.reg .pred e, y, n;\n\t.reg .b32 t, l;\n\t.reg .b64 b;\n\t"
+        "setp.eq.u32 y, 0, 0;\n\tsetp.ne.u32 n, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        PA_STEP("0", "0", "n") PA_STEP("8", "2", "y") PA_STEP("16", "4", "y") PA_STEP("24", "6", "y")
+        PA_STEP("32", "0", "y") PA_STEP("40", "2", "y") PA_STEP("48", "4", "y") PA_STEP("56", "6", "y")
+        "}" ::"r"(d), "r"(a), "r"(lo), "r"(hi), "r"(idesc) : "memory");
+#undef PA_STEP
+}
+__device__ __forceinline__ void issue_o(uint32_t d, uint32_t a, uint32_t lo, uint32_t hi, uint32_t idesc,
+                                        uint32_t accumulate) {
+#define PA_STEP(A, B, ACC)                                                                     \
+    "add.u32 t, %1, " A ";\n\tadd.u32 l, %2, " B ";\n\tmov.b64 b, {l, %3};\n\t"               \
+    "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %4, " ACC ";\n\t"
+    asm volatile(
+        "{\n\t.reg .pred e, y, f;\n\t.reg .b32 t, l;\n\t.reg .b64 b;\n\t"
+        "setp.eq.u32 y, 0, 0;\n\tsetp.ne.u32 f, %5, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
+        PA_STEP("0", "0", "f") PA_STEP("8", "128", "y") PA_STEP("16", "256", "y") PA_STEP("24", "384", "y")
+        "}" ::"r"(d), "r"(a), "r"(lo), "r"(hi), "r"(idesc), "r"(accumulate) : "memory");
+#undef PA_STEP
 }
 
 // The queries of a chunk: first row, count, sequence and start; false when they make no sense.
@@ -136,6 +180,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.group, B = p.block_size, Hkv = p.num_kv_heads;
     const int ppt = kTile / G;  // positions per tile; rows from ppt * G on are unused
+    const int log2b = 31 - __clz(B);
+    const uint32_t inv_g = (65536 + G - 1) / G;  // r / G = r * inv_g >> 16 for r < 128 and G <= 8 (checked for all)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < kKStages; ++i) {
@@ -150,18 +196,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bars.vh_full(i), kConverters);
             mbar_init(bars.vh_empty(i), 1);
         }
-        for (int x = 0; x < 2; ++x) {
-            mbar_init(bars.s_full(x), 1);
-            for (int h = 0; h < 2; ++h) {
-                mbar_init(bars.p_full(x, h), 4);
-                mbar_init(bars.o_done(x, h), 1);
-            }
-            mbar_init(bars.q_empty(x), 1);
+        for (int i = 0; i < kPieces; ++i) {
+            mbar_init(bars.s_full(i), 1);
+            mbar_init(bars.p_full(i), 4);
+            mbar_init(bars.s_empty(i), 1);
         }
+        for (int x = 0; x < 2; ++x) mbar_init(bars.o_done(x), 1);
+        mbar_init(bars.q_empty(), 1);
         for (int i = 0; i < kQSlots; ++i) mbar_init(bars.q_full(i), kConverters);
         for (int i = 0; i < kInfo; ++i) mbar_init(bars.info(i), 1);
+        for (int i = 0; i < kItems; ++i) {
+            mbar_init(bars.item_full(i), 1);
+            mbar_init(bars.item_empty(i), 8 + kConverters + 3);  // every other warp
+        }
         mbar_init(bars.o_free(), 8);
-        mbar_init(bars.drain(), 1);
+        mbar_init(bars.joined(), 8);
+        mbar_init(bars.drain(), 2);
         fence_mbar_init();
     }
     pdl_trigger();
@@ -173,59 +223,102 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;  // S of group 0, S of group 1, O of group 0, O of group 1; 128 columns each
+    const uint32_t tmem = *tmem_slot;
 
-    // ---- items: (query tile rank, chunk, kv head, span), the latest tile of every chunk first; CTA b takes one of
-    // every pass of gridDim.x items, in serpentine order, so that heavy and light ones pair up.  Every warp walks the
-    // same items, so the roles agree without a word.
-    const int per_rank = p.num_chunks * Hkv * spans.count;
-    const long long num_items = (long long)((p.max_q_len + ppt - 1) / ppt) * per_rank;
-    const long long passes = (num_items + gridDim.x - 1) / gridDim.x;
-    // item of pass c; false for an empty one
-    auto describe = [&](long long c, Item& d) {
-        const long long g = gridDim.x, b = blockIdx.x, k = c * g + ((c & 1) ? g - 1 - b : b);
-        if (k >= num_items) return false;
-        const int rank = (int)(k / per_rank);
-        int rem = (int)(k - (long long)rank * per_rank);
-        d.span = rem % spans.count;
-        rem /= spans.count;
-        const int ch = rem / Hkv;
-        d.kvh = rem - ch * Hkv;
-        int n;
-        if (!chunk_of(p, ch, d.r0, n, d.s, d.start)) {
-            if (rank == 0 && d.kvh == 0 && d.span == 0 && threadIdx.x == 0) count_error(p.error_count);
+    bool ok = true;
+    // Item n, from the warp that describes them (every lane gets it; false at the end, or after a wait that gave up).
+    auto take_item = [&](uint32_t n, Item& d) {
+        if (!mbar_wait_warp(bars.item_full(n % kItems), (n / kItems) & 1)) {
+            ok = false;
             return false;
         }
-        const int tiles = (n + ppt - 1) / ppt;
-        if (rank >= tiles) return false;
-        d.i0 = (tiles - 1 - rank) * ppt;
-        d.nq = min(ppt, n - d.i0);
-        const int cap = key_cap(p, d.s);
-        d.last_key = (int)min((long long)d.start + d.i0 + d.nq - 1, 0x7FFFFFFELL);
-        if (d.last_key >= cap) {
-            if (d.span == 0 && threadIdx.x == 0) count_error(p.error_count);
-            d.last_key = cap - 1;
-        }
-        const int all = d.last_key >= 0 ? d.last_key / kTile + 1 : 0;
-        d.spans = max(1, (all + spans.tiles - 1) / spans.tiles);
-        d.t0 = d.span * spans.tiles;
-        d.nt = min(spans.tiles, all - d.t0);
-        if (d.nt < 0) d.nt = 0;
-        return d.span < d.spans;  // without any key, span 0 stores zeros
+        d = *reinterpret_cast<const Item*>(smem + kItem + n % kItems * sizeof(Item));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.item_empty(n % kItems));
+        return d.nt >= 0;
     };
-    bool ok = true;
 
+    // Registers: 128 a thread at launch (512 threads take all of the SM's).  The softmax warps get 160 of them, for 64
+    // scores and what becomes of them, the converters keep 104, the others 88: 2 * 160 + 104 + 88 = 4 * 128.
+    if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kKWarp || warp == kVWarp) {
         // ============================================================ producers
         const bool v_side = warp == kVWarp;
-        const int bpt = kTile / B, tpc = 32 / bpt;  // blocks per tile, tiles per 32-entry chunk of the table
+        const int bpt = kTile >> log2b, tpc = 32 / bpt;  // blocks per tile, tiles per 32-entry chunk of the table
         if (lane == 0) tma_prefetch_desc(v_side ? &tmv : &tmk);
-        uint32_t g = 0;  // key tiles so far
-        for (long long c = 0; c < passes && ok; ++c) {
-            Item d;
-            if (!describe(c, d)) continue;
+        // The V warp describes the items.  (query tile rank, chunk, kv head, span), the latest tile of every chunk
+        // first; CTA b takes one of every pass of gridDim.x items, in serpentine order, so that heavy and light ones
+        // pair up.  It stays an item ahead of its own copies: when every warp described its items itself, that took
+        // each of them 3.3k cycles an item, between the epilogue of one and the first score of the next.
+        const int per_rank = p.num_chunks * Hkv * spans.count;
+        const int num_items = (p.max_q_len + ppt - 1) / ppt * per_rank;  // the host keeps it below 2^30
+        int pass = 0;
+        uint32_t published = 0;
+        auto describe = [&](Item& d) {  // the item of this pass; false for an empty one
+            const int g = gridDim.x, b = blockIdx.x, k = pass * g + ((pass & 1) ? g - 1 - b : b);
+            if (k >= num_items) return false;
+            const int rank = k / per_rank;
+            int rem = k - rank * per_rank;
+            d.span = rem % spans.count;
+            rem /= spans.count;
+            const int ch = rem / Hkv;
+            d.kvh = rem - ch * Hkv;
+            int r0, n, start;
+            if (!chunk_of(p, ch, r0, n, d.s, start)) {
+                if (rank == 0 && d.kvh == 0 && d.span == 0 && lane == 0) count_error(p.error_count);
+                return false;
+            }
+            const int tiles = (n + ppt - 1) / ppt;
+            if (rank >= tiles) return false;
+            const int i0 = (tiles - 1 - rank) * ppt;
+            d.row = r0 + i0;
+            d.nq = min(ppt, n - i0);
+            d.pos = (int)min((long long)start + i0, 0x7FFFFFFELL - kTile);
+            const int cap = key_cap(p, d.s);
+            d.last_key = d.pos + d.nq - 1;
+            if (d.last_key >= cap) {
+                if (d.span == 0 && lane == 0) count_error(p.error_count);
+                d.last_key = cap - 1;
+            }
+            const int all = d.last_key >= 0 ? d.last_key / kTile + 1 : 0;
+            d.spans = max(1, (all + spans.tiles - 1) / spans.tiles);
+            d.t0 = d.span * spans.tiles;
+            d.nt = max(0, min(spans.tiles, all - d.t0));
+            return d.span < d.spans;  // without any key, span 0 stores zeros
+        };
+        auto publish = [&](Item& d) {  // the next item, or the end
+            const int passes = (num_items + (int)gridDim.x - 1) / (int)gridDim.x;
+            d.nt = -1;
+            for (; pass < passes; ++pass)
+                if (describe(d)) break;
+                else d.nt = -1;
+            ++pass;
+            const int i = published % kItems;
+            if (published >= kItems && !mbar_wait_warp(bars.item_empty(i), ((published / kItems) - 1) & 1)) {
+                ok = false;
+                d.nt = -1;
+                return;
+            }
+            if (lane == 0) {
+                *reinterpret_cast<Item*>(smem + kItem + i * sizeof(Item)) = d;
+                mbar_arrive(bars.item_full(i));
+            }
+            __syncwarp();
+            ++published;
+        };
+        uint32_t g = 0, items = 0;  // key tiles and items so far
+        Item d{}, ahead{};
+        if (v_side) publish(ahead);
+        for (; ok; ++items) {
+            if (v_side) {
+                d = ahead;
+                if (d.nt < 0) break;
+                publish(ahead);
+            } else if (!take_item(items, d)) {
+                break;
+            }
             const int first = d.t0 * bpt;  // first block
-            const int nblk = min((d.last_key + B) / B, (d.t0 + d.nt) * bpt) - first;
+            const int nblk = min((d.last_key + B) >> log2b, (d.t0 + d.nt) * bpt) - first;
             const int32_t* table = p.block_tables + (size_t)d.s * p.max_blocks_per_seq + first;
             auto load_raw = [&](int chunk) {
                 const int i = chunk * 32 + lane;
@@ -239,8 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             int raw = d.nt > 0 ? load_raw(0) : -1, raw_next = -1, pb = -1;
             float2 sc = load_scales(raw), sc_next = make_float2(0.f, 0.f);
             float R = 0.f;
-            for (int j = 0; j < d.nt; ++j, ++g) {
-                const int chunk = j / tpc, l = j - chunk * tpc;
+            for (int j = 0, chunk = 0, l = 0; j < d.nt; ++j, ++g) {
                 if (l == 0) {
                     if (chunk > 0) {
                         raw = raw_next;
@@ -254,10 +346,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 const uint32_t valid = __ballot_sync(0xffffffffu, pb >= 0);
                 const uint32_t mine = (valid >> (l * bpt)) & ((1u << bpt) - 1u);
-                const int stages = v_side ? kVStages : kKStages, st = g % stages;
+                const int stages = v_side ? kVStages : kKStages, st = v_side ? g % kVStages : g % kKStages;
+                const int round = v_side ? g / kVStages : g / kKStages;
                 uint64_t* full = v_side ? bars.v_full(st) : bars.k_full(st);
-                if (g >= (uint32_t)stages &&
-                    !mbar_wait_warp(v_side ? bars.v_empty(st) : bars.k_empty(st), ((g / stages) - 1) & 1)) {
+                if (g >= (uint32_t)stages && !mbar_wait_warp(v_side ? bars.v_empty(st) : bars.k_empty(st), (round - 1) & 1)) {
                     ok = false;
                     break;
                 }
@@ -274,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float vmax = redux_max(lane < bpt ? my_vs : 0.f);
                     if (j == 0 || vmax > 64.f * R)
                         R = __uint_as_float((__float_as_uint(fmaxf(vmax, kScaleFloor)) + 0x7FFFFFu) & 0x7F800000u);
-                    const int blk = (lane & 15) * 8 / B;  // block of this lane's group
+                    const int blk = ((lane & 15) * 8) >> log2b;  // block of this lane's group
                     const float ks = __shfl_sync(0xffffffffu, sc.x, l * bpt + blk);
                     const float vs = __shfl_sync(0xffffffffu, sc.y, l * bpt + blk);
                     const int slot = g % kInfo;
@@ -287,9 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int left = d.last_key + 1 - (d.t0 + j) * kTile - 32 * lane;
                         uint32_t m = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
                         if (B >= 32) {
-                            if (!((mine >> (32 * lane / B)) & 1u)) m = 0u;
+                            if (!((mine >> ((32 * lane) >> log2b)) & 1u)) m = 0u;
                         } else {
-                            const int per = 32 / B;
+                            const int per = 32 >> log2b;
                             for (int b = 0; b < per; ++b)
                                 if (!((mine >> (lane * per + b)) & 1u)) m &= ~(((1u << B) - 1u) << (b * B));
                         }
@@ -301,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 if (l == 0) raw_next = load_raw(chunk + 1);
                 if (l == 1) sc_next = load_scales(raw_next);
+                if (++l == tpc) l = 0, ++chunk;
             }
         }
         if (lane == 0) {
@@ -309,93 +402,85 @@ __global__ void __launch_bounds__(kThreads, 1)
                 count_error(p.error_count);
         }
         __syncwarp();
-    } else if (warp == kMmaWarp) {
-        // ============================================================ MMA issuer
-        constexpr uint32_t idesc_s = umma_idesc_e4m3(128, 128, false, false);
+    } else if (warp == kMmaWarp || warp == kSWarp) {
+        // ============================================================ MMA issuers
+        // Warp kSWarp issues every piece's S = Q K^T, warp kMmaWarp every piece's O += P V: one warp doing both in
+        // turn took 1.55k cycles a piece, most of it in waking up and in queueing behind its own last product.
+        const bool s_side = warp == kSWarp;
+        constexpr uint32_t idesc_s = umma_idesc_e4m3(128, 64, false, false);
         // kind::f16 with f16 operands (format 0), V MN-major
         constexpr uint32_t idesc_o = (1u << 4) | (1u << 16) | ((128u >> 3) << 17) | ((128u >> 4) << 24);
-        const uint64_t dq0 = umma_desc_sw128(smem_u32(smem + kQ), 16, 1024);
         const uint64_t dk0 = umma_desc_sw128(smem_u32(smem + kK), 16, 1024);
         const uint64_t dv0 = umma_desc_sw128(smem_u32(smem + kVh), kHalfBytes, 1024);
-        uint32_t g = 0, items = 0;   // key tiles and items with keys before this one
-        uint32_t done[2] = {0, 0};   // tiles of each group whose P V has been issued
+        // (the same in every lane; said so, it goes to the uniform registers that an MMA's operands need)
+        auto uniform = [](uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); };
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             if (ok && !mbar_wait_warp(bar, parity)) ok = false;
             return ok;
         };
-        for (long long c = 0; c < passes && ok; ++c) {
-            Item d;
-            if (!describe(c, d) || d.nt == 0) continue;
-            const int qb = items & 1;
-            auto issue_qk = [&](int j) {  // S of tile j, into its group's buffer, which the last P V has left
-                const uint32_t t = g + j, st = t % kKStages;
-                if (!wait(bars.k_full(st), (t / kKStages) & 1)) return;
-                tc_fence_after();
+        uint32_t g = 0, items = 0, piece = 0;  // key tiles, items with keys, pieces so far
+        Item d;
+        for (uint32_t n = 0; ok && take_item(n, d); ++n) {
+            if (d.nt == 0) continue;
+            // an item's first S waits for its query terms, its first product until the last item's epilogue has read O
+            if (s_side) wait(bars.q_full(items % kQSlots), (items / kQSlots) & 1);
+            else if (items > 0) wait(bars.o_free(), (items - 1) & 1);
+            for (int j = 0; j < d.nt && ok; ++j, ++g) {
+                const uint32_t st = g % kKStages, vh = g % kVhStages;
+                if (s_side) wait(bars.k_full(st), (g / kKStages) & 1);
+                else wait(bars.vh_full(vh), (g / kVhStages) & 1);
 #pragma unroll
-                for (int term = 0; term < 2; ++term)
-#pragma unroll
-                    for (int k = 0; k < kD / 32; ++k)
-                        umma_e4m3_warp(tmem + (j & 1) * 128,
-                                       dq0 + (uint64_t)(((qb * 2 + term) * kCodes + k * 32) >> 4),
-                                       dk0 + (uint64_t)((st * kCodes + k * 32) >> 4), idesc_s, term + k > 0);
-                umma_commit_warp(bars.s_full(j & 1));
-                umma_commit_warp(bars.k_empty(st));
-                if (j == d.nt - 1) umma_commit_warp(bars.q_empty(qb));
-            };
-            if (!wait(bars.q_full(items % kQSlots), (items / kQSlots) & 1)) break;
-            issue_qk(0);
-            if (d.nt > 1) issue_qk(1);
-            // the last item's epilogue has read both O
-            if (items > 0) wait(bars.o_free(), (items - 1) & 1);
-            for (int j = 0; j < d.nt && ok; ++j) {
-                const uint32_t t = g + j, vh = t % kVhStages;
-                const int x = j & 1;
-                if (!wait(bars.vh_full(vh), (t / kVhStages) & 1)) break;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {  // 64 keys: P in columns 64 h .. 64 h + 31 of the group's S
-                    if (!wait(bars.p_full(x, h), done[x] & 1)) break;
-                    tc_fence_after();
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        umma_bf16_ta_warp(tmem + 256 + x * 128, tmem + x * 128 + h * 64 + k * 8,
-                                          dv0 + (uint64_t)((vh * 2 * kHalfBytes + (h * 4 + k) * 16 * 128) >> 4),
-                                          idesc_o, j > 1 || h > 0 || k > 0);
-                    umma_commit_warp(bars.o_done(x, h));
+                for (int x = 0; x < 2; ++x, ++piece) {
+                    const uint32_t sb = piece % kPieces, round = piece / kPieces;
+                    if (s_side) {
+                        if (round > 0 && !wait(bars.s_empty(sb), (round - 1) & 1)) break;
+                        tc_fence_after();
+                        issue_s(tmem + kTS + uniform(sb * 64), tmem + kTQ,
+                                (uint32_t)dk0 + uniform((st * kCodes + x * 64 * kD) >> 4), (uint32_t)(dk0 >> 32), idesc_s);
+                        umma_commit_warp(bars.s_full(sb));
+                        if (x) umma_commit_warp(bars.k_empty(st));
+                        if (x && j == d.nt - 1) umma_commit_warp(bars.q_empty());
+                    } else {
+                        if (!wait(bars.p_full(sb), round & 1)) break;
+                        tc_fence_after();
+                        issue_o(tmem + kTO + x * 128, tmem + kTS + uniform(sb * 64),
+                                (uint32_t)dv0 + uniform((vh * 2 * kHalfBytes + x * 64 * 128) >> 4),
+                                (uint32_t)(dv0 >> 32), idesc_o, uniform(j > 0));
+                        umma_commit_warp(bars.s_empty(sb));
+                        umma_commit_warp(bars.o_done(x));
+                        if (x) umma_commit_warp(bars.vh_empty(vh));
+                    }
                 }
-                umma_commit_warp(bars.vh_empty(vh));
-                ++done[x];
-                if (ok && j + 2 < d.nt) issue_qk(j + 2);
             }
-            g += d.nt;
             ++items;
         }
         if (!ok && lane == 0) count_error(p.error_count);
         umma_commit_warp(bars.drain());  // no MMA is running when the tensor memory is freed
         if (!mbar_wait_warp(bars.drain(), 0) && lane == 0) count_error(p.error_count);
         __syncwarp();
-    } else if (warp >= kConvWarp) {
+    } else if (warp >= kConvWarp && warp < kMmaWarp) {
         // ============================================================ converters
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         const int w = warp - kConvWarp;
         uint32_t g = 0, items = 0;
-        // rows w, w + 4, ... of an item's query tile: two e4m3 terms, and the factor that undoes their scaling
+        // rows 32 w + from .. of an item's query tile: two e4m3 terms, and the factor that undoes their scaling
         auto split_rows = [&](const Item& d, uint32_t item, int from, int to) {
-            const int qb = item & 1;
-            uint8_t* tile = smem + kQ + qb * 2 * kCodes;
-            for (int i = from; i < to; i += 4) {
-                uint2 x[4];
+            uint8_t* tile = smem + kQ;
+            for (int i = from; i < to; i += 8) {
+                uint2 x[8];  // eight rows' loads go out together
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int r = (i + u) * 4 + w, pos = r / G;
+                for (int u = 0; u < 8; ++u) {
+                    const int r = w * 32 + i + u, pos = r * inv_g >> 16;
                     x[u] = make_uint2(0u, 0u);
                     if (pos < d.nq)
                         x[u] = __ldg(reinterpret_cast<const uint2*>(
                                          static_cast<const __nv_bfloat16*>(p.q) +
-                                         ((size_t)(d.r0 + d.i0 + pos) * p.num_q_heads + (size_t)d.kvh * G + r % G) * kD) +
+                                         ((size_t)(d.row + pos) * p.num_q_heads + d.kvh * G + (r - pos * G)) * kD) +
                                      lane);
                 }
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const int r = (i + u) * 4 + w;
+                for (int u = 0; u < 8; ++u) {
+                    const int r = w * 32 + i + u;
                     const uint32_t m2 = __vmaxu2(x[u].x & 0x7FFF7FFFu, x[u].y & 0x7FFF7FFFu);
                     const uint32_t am = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
                     const int e = min(134 - (int)(am >> 7), 126);  // |x| 2^e in [128, 256)
@@ -420,25 +505,49 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
         };
+        // the staged rows into tensor memory (a lane's row is its tensor-memory lane), once the item before is through
+        // its last S
         auto finish_q = [&](uint32_t item) {
-            fence_proxy_async_smem();
+            __syncwarp();
+            if (item > 0 && !mbar_wait_warp(bars.q_empty(), (item - 1) & 1)) {
+                ok = false;
+                return;
+            }
+            tc_fence_after();
+            const int r = w * 32 + lane;
+#pragma unroll
+            for (int term = 0; term < 2; ++term) {
+                uint32_t v[32];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(smem + kQ + term * kCodes + r * kD + ((k ^ (r & 7)) << 4));
+                    v[4 * k] = x.x;
+                    v[4 * k + 1] = x.y;
+                    v[4 * k + 2] = x.z;
+                    v[4 * k + 3] = x.w;
+                }
+                tmem_st32u(tmem + ((uint32_t)(w * 32) << 16) + kTQ + term * 32, v);
+            }
+            tmem_wait_st();
+            tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.q_full(item % kQSlots));
         };
-        // the next item with keys after pass c
-        auto next_item = [&](long long c, Item& d) {
-            for (++c; c < passes; ++c)
-                if (describe(c, d) && d.nt > 0) return c;
-            return passes;
+        uint32_t taken = 0;
+        auto next_item = [&](Item& d) {  // the next item with keys; false at the end
+            while (ok && take_item(taken++, d))
+                if (d.nt > 0) return true;
+            return false;
         };
         Item d, nx;
-        long long c = next_item(-1, d);
-        if (c < passes) {
+        bool have = next_item(d);
+        if (have) {
             split_rows(d, 0, 0, 32);
             finish_q(0);
         }
-        while (c < passes && ok) {
-            const long long c2 = next_item(c, nx);
+        while (have && ok) {
+            const bool have_next = next_item(nx);
+            if (!ok) break;
             int rows = 0;  // rows of the next item's tile that are split (of this warp's 32)
             for (int j = 0; j < d.nt; ++j, ++g) {
                 const uint32_t vs = g % kVStages, vh = g % kVhStages;
@@ -452,12 +561,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint8_t* src = smem + kV + vs * kCodes;
                 uint8_t* dst = smem + kVh + vh * 2 * kHalfBytes;
                 const int ch = lane & 7;
-                const uint32_t* m = mask + (g % kInfo) * 4;
+                const uint4 m = *reinterpret_cast<const uint4*>(mask + (g % kInfo) * 4);
+                const bool all_valid = (m.x & m.y & m.z & m.w) == ~0u;
 #pragma unroll 4
                 for (int i = 0; i < kTile / 16; ++i) {
                     const int key = (i * 4 + w) * 4 + (lane >> 3);
                     uint4 x = *reinterpret_cast<const uint4*>(src + key * kD + ((ch ^ (key & 7)) << 4));
-                    if (!((m[key >> 5] >> (key & 31)) & 1u)) x = make_uint4(0u, 0u, 0u, 0u);
+                    if (!all_valid) {
+                        const uint32_t word = i < 2 ? m.x : i < 4 ? m.y : i < 6 ? m.z : m.w;
+                        if (!((word >> (key & 31)) & 1u)) x = make_uint4(0u, 0u, 0u, 0u);
+                    }
                     const uint32_t in[4] = {x.x, x.y, x.z, x.w};
                     uint32_t out[8];
 #pragma unroll
@@ -477,111 +590,91 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(bars.vh_full(vh));
                     mbar_arrive(bars.v_empty(vs));
                 }
-                // between tiles, a quarter of the next item's query rows; its buffer is free once the item before
-                // this one is through its last S
-                if (c2 < passes && rows < 32) {
-                    if (rows == 0 && items > 0 && !mbar_wait_warp(bars.q_empty((items + 1) & 1), ((items - 1) >> 1) & 1)) {
-                        ok = false;
-                        break;
-                    }
+                // between tiles, a quarter of the next item's query rows
+                if (have_next && rows < 32) {
                     split_rows(nx, items + 1, rows, rows + 8);
                     rows += 8;
-                    if (rows == 32) finish_q(items + 1);
                 }
             }
             if (!ok) break;
-            if (c2 < passes && rows < 32) {  // (rows > 0: an item with keys has a tile)
+            if (have_next) {
                 split_rows(nx, items + 1, rows, 32);
                 finish_q(items + 1);
             }
             ++items;
-            c = c2;
+            have = have_next;
             d = nx;
         }
         if (!ok && lane == 0) count_error(p.error_count);
-    } else {
+    } else if (warp < kConvWarp) {
         // ============================================================ softmax and output
-        // Every thread runs every tile and the named barrier, even after a wait timed out.
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
         const int x = warp >> 2;                       // group
         const int r = (warp & 3) * 32 + lane;          // row = tensor-memory lane
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t t_s = tmem + lanes + x * 128, t_o = tmem + lanes + 256 + x * 128;
+        const uint32_t t_o = tmem + lanes + kTO + x * 128;
         float4* state = reinterpret_cast<float4*>(smem + kState);
-        uint32_t g = 0, items = 0, done = 0;  // key tiles, items with keys, tiles of this group
+        uint32_t g = 0, items = 0;  // key tiles (pieces of this group), and items with keys
+        BoundedWarpBarrier joined{bars.joined(), 0};
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             if (ok && !mbar_wait_warp(bar, parity)) ok = false;
         };
-        for (long long c = 0; c < passes; ++c) {
-            Item d;
-            if (!describe(c, d)) continue;
-            const int pos = d.i0 + min(r / G, d.nq - 1);  // (unused rows mask as the last used one)
-            const bool row_ok = r / G < d.nq;
-            const int my_last = min(d.start + pos, d.last_key);
+        const int my_pos = r * inv_g >> 16;  // the row's position in a tile, and its head of the group
+        Item d;
+        for (uint32_t n = 0; take_item(n, d); ++n) {
+            const bool row_ok = my_pos < d.nq;
+            const int my_last = min(d.pos + min(my_pos, d.nq - 1), d.last_key);  // (unused rows mask as the last used one)
             float m = -INFINITY, l = 0.f, Rc = 1.f, qf = 0.f;
             if (d.nt > 0) {
                 wait(bars.q_full(items % kQSlots), (items / kQSlots) & 1);
                 qf = reinterpret_cast<const float*>(smem + kQf)[items % kQSlots * kTile + r];
             }
-            for (int j = x; j < d.nt; j += 2, ++done) {
-                const uint32_t t = g + j;
+            for (int j = 0; j < d.nt; ++j) {
+                const uint32_t t = g + j, piece = 2 * t + x, sb = piece % kPieces, t_s = tmem + lanes + kTS + sb * 64;
                 const int slot = t % kInfo;
                 wait(bars.info(slot), (t / kInfo) & 1);
-                const float4* consts = reinterpret_cast<const float4*>(smem + kConsts) + slot * 16;
+                const float4* kc = reinterpret_cast<const float4*>(smem + kConsts) + slot * 16 + x * 8;
                 const float R = reinterpret_cast<const float*>(smem + kR)[slot];
-                uint32_t vm[4];
-#pragma unroll
-                for (int w = 0; w < 4; ++w) vm[w] = mask[slot * 4 + w];
-                wait(bars.s_full(x), done & 1);
+                const uint2 vm = *reinterpret_cast<const uint2*>(mask + slot * 4 + x * 2);
+                wait(bars.s_full(sb), (piece / kPieces) & 1);
+                if (!ok) break;
                 tc_fence_after();
-#pragma unroll 1
-                for (int h = 0; h < 2; ++h) {
+                {
                     float s[64];
                     {
-                        float a[32];
-                        tmem_ld32(t_s + h * 64, a);
+                        float a[32], b[32];
+                        tmem_ld32(t_s, a);
+                        tmem_ld32(t_s + 32, b);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i) s[i] = a[i];
-                        float b[32];
-                        tmem_ld32(t_s + h * 64 + 32, b);
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) s[32 + i] = b[i];
+                        for (int i = 0; i < 32; ++i) s[i] = a[i], s[32 + i] = b[i];
                     }
                     tmem_wait_ld();
-                    const int key0 = (d.t0 + j) * kTile + h * 64;
-                    const uint32_t m0 = h ? vm[2] : vm[0], m1 = h ? vm[3] : vm[1];
-                    const float4* kc = consts + h * 8;
+                    const int key0 = (d.t0 + j) * kTile + x * 64;
+                    const uint32_t m0 = vm.x, m1 = vm.y;
                     // dense: every key is valid and every row of the warp sees it
                     const bool dense = __all_sync(0xffffffffu, (m0 & m1) == ~0u && key0 + 63 <= my_last);
+                    if (!dense) {  // the row's visible and valid keys as 64 bits; the others get -inf
+                        const int vis = my_last - key0 + 1;
+                        const uint32_t w0 = m0 & (vis >= 32 ? ~0u : vis > 0 ? (1u << vis) - 1u : 0u);
+                        const uint32_t w1 = m1 & (vis >= 64 ? ~0u : vis > 32 ? (1u << (vis - 32)) - 1u : 0u);
+#pragma unroll
+                        for (int k = 0; k < 64; ++k)
+                            if (!((k < 32 ? w0 : w1) & (1u << (k & 31)))) s[k] = -INFINITY;
+                    }
                     float mx[8];
-                    if (dense) {
 #pragma unroll
-                        for (int b = 0; b < 8; ++b) {
-                            const float u = fmax3(s[8 * b], s[8 * b + 1], s[8 * b + 2]);
-                            const float v = fmax3(s[8 * b + 3], s[8 * b + 4], s[8 * b + 5]);
-                            mx[b] = fmax3(u, v, fmaxf(s[8 * b + 6], s[8 * b + 7])) * (kc[b].x * qf);
-                        }
-                    } else {
-#pragma unroll
-                        for (int b = 0; b < 8; ++b) {
-                            const float a = kc[b].x * qf;
-                            mx[b] = -INFINITY;
-#pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int k = 8 * b + i;
-                                const bool valid = (((k < 32 ? m0 : m1) >> (k & 31)) & 1u) && key0 + k <= my_last;
-                                s[k] = valid ? s[k] * a : -INFINITY;
-                                mx[b] = fmaxf(mx[b], s[k]);
-                            }
-                        }
+                    for (int b = 0; b < 8; ++b) {
+                        const float u = fmax3(s[8 * b], s[8 * b + 1], s[8 * b + 2]);
+                        const float v = fmax3(s[8 * b + 3], s[8 * b + 4], s[8 * b + 5]);
+                        mx[b] = fmax3(u, v, fmaxf(s[8 * b + 6], s[8 * b + 7])) * fmaxf(kc[b].x * qf, kTiny);
                     }
                     const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
-                    const bool first = j == x && h == 0;  // nothing in O yet
+                    const bool first = j == 0;  // nothing in O yet
                     if (first) Rc = R;
                     const float m_new = mt > m + kLazy ? mt : m;  // also the first finite maximum
                     if (!first && __any_sync(0xffffffffu, m_new != m || R != Rc)) {
                         // the products issued so far have to be done before O changes
-                        if (h) wait(bars.o_done(x, 0), done & 1);
-                        else wait(bars.o_done(x, 1), (done - 1) & 1);
+                        wait(bars.o_done(x), (t - 1) & 1);
                         tc_fence_after();
                         const float alpha = m_new == m ? 1.f : fast_exp2(m - m_new), f = alpha * (Rc / R);
 #pragma unroll 1
@@ -600,63 +693,46 @@ __global__ void __launch_bounds__(kThreads, 1)
                     m = m_new;
                     uint32_t pk[32];
                     float sum = 0.f;
-                    if (dense) {
+                    const float m_fin = m == -INFINITY ? 0.f : m;  // no key yet: every P' is 2^-inf
 #pragma unroll
-                        for (int b = 0; b < 8; ++b) {
-                            const float4 k4 = kc[b];
-                            const float a = k4.x * qf, o = k4.y - m;
-                            const unsigned long long a2 = f32x2_pack(a, a), o2 = f32x2_pack(o, o);
-                            float e[8];
+                    for (int b = 0; b < 8; ++b) {
+                        const float4 k4 = kc[b];
+                        const float a = fmaxf(k4.x * qf, kTiny), o = k4.y - m_fin;
+                        const unsigned long long a2 = f32x2_pack(a, a), o2 = f32x2_pack(o, o);
+                        float e[8];
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                float y0, y1;
-                                f32x2_unpack(fma_f32x2(f32x2_pack(s[8 * b + 2 * i], s[8 * b + 2 * i + 1]), a2, o2), y0, y1);
-                                e[2 * i] = fast_exp2(y0);
-                                e[2 * i + 1] = fast_exp2(y1);
-                                pk[4 * b + i] = pack_f16x2(e[2 * i], e[2 * i + 1]);
-                            }
-                            float u, v;
-                            f32x2_unpack(add_f32x2(add_f32x2(f32x2_pack(e[0], e[1]), f32x2_pack(e[2], e[3])),
-                                                   add_f32x2(f32x2_pack(e[4], e[5]), f32x2_pack(e[6], e[7]))), u, v);
-                            sum = fmaf(u + v, k4.z, sum);
+                        for (int i = 0; i < 4; ++i) {
+                            float y0, y1;
+                            f32x2_unpack(fma_f32x2(f32x2_pack(s[8 * b + 2 * i], s[8 * b + 2 * i + 1]), a2, o2), y0, y1);
+                            e[2 * i] = fast_exp2(y0);
+                            e[2 * i + 1] = fast_exp2(y1);
+                            pk[4 * b + i] = pack_f16x2(e[2 * i], e[2 * i + 1]);
                         }
-                    } else {
-#pragma unroll
-                        for (int b = 0; b < 8; ++b) {
-                            const float4 k4 = kc[b];
-                            const float o = k4.y - m;
-                            float g8 = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float s0 = s[8 * b + 2 * i], s1 = s[8 * b + 2 * i + 1];
-                                const float e0 = s0 == -INFINITY ? 0.f : fast_exp2(s0 + o);
-                                const float e1 = s1 == -INFINITY ? 0.f : fast_exp2(s1 + o);
-                                pk[4 * b + i] = pack_f16x2(e0, e1);
-                                g8 += e0 + e1;
-                            }
-                            sum = fmaf(g8, k4.z, sum);
-                        }
+                        float u, v;
+                        f32x2_unpack(add_f32x2(add_f32x2(f32x2_pack(e[0], e[1]), f32x2_pack(e[2], e[3])),
+                                               add_f32x2(f32x2_pack(e[4], e[5]), f32x2_pack(e[6], e[7]))), u, v);
+                        sum = fmaf(u + v, k4.z, sum);
                     }
                     l += sum;
-                    tmem_st32u(t_s + h * 64, pk);
+                    tmem_st32u(t_s, pk);
                     tmem_wait_st();
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0 && ok) mbar_arrive(bars.p_full(x, h));
+                    if (lane == 0 && ok) mbar_arrive(bars.p_full(sb));
                 }
             }
             // ---- the item's output: both groups' states joined, each group stores 64 columns of the row
             float mo = -INFINITY, lo = 0.f, Ro = 1.f;
             if (d.nt > 0) {
-                if (d.nt > x) {
-                    wait(bars.o_done(x, 1), (done - 1) & 1);
-                    tc_fence_after();
-                }
-                // (two copies by item: a group without a tile in the next item may be there already)
+                wait(bars.o_done(x), (g + d.nt - 1) & 1);
+                // (two copies by item: the other group may be an item behind)
                 float4* st = state + (items & 1) * 2 * kTile;
                 st[x * kTile + r] = make_float4(m, l, Rc, 0.f);
                 tc_fence_before();
-                asm volatile("bar.sync 2, 256;" ::: "memory");
+                if (!ok || !joined.sync()) {
+                    ok = false;
+                    break;
+                }
                 tc_fence_after();
                 const float4 o = st[(x ^ 1) * kTile + r];
                 mo = o.x;
@@ -669,10 +745,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float L = w_own * l + w_oth * lo, inv = L == 0.f ? 0.f : 1.f / L;
             const float f_own = w_own * Rc * inv, f_oth = w_oth * Ro * inv;
             const bool use_own = w_own != 0.f, use_oth = w_oth != 0.f;
-            const size_t row = ((size_t)(d.r0 + pos) * p.num_q_heads + (size_t)d.kvh * G + r % G);
+            const size_t row = (size_t)(d.row + my_pos) * p.num_q_heads + d.kvh * G + (r - my_pos * G);
             const bool direct = d.spans == 1;
             const size_t part = (size_t)d.span * p.total_q * p.num_q_heads + row;
-            const uint32_t t_oth = tmem + lanes + 256 + (x ^ 1) * 128;
+            const uint32_t t_oth = tmem + lanes + kTO + (x ^ 1) * 128;
             if (!direct && row_ok && x == 0) spans.ml[part] = make_float2(M, L);
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
@@ -774,6 +850,7 @@ __global__ void __launch_bounds__(128) prefill_fp8_block_join_kernel(const Prefi
     }
 }
 
+// Query tiles times kv heads.
 long long work_items(int num_chunks, int max_q_len, int num_kv_heads, int group) {
     const int ppt = kTile / group;
     return (long long)((max_q_len + ppt - 1) / ppt) * num_chunks * num_kv_heads;
@@ -812,7 +889,9 @@ bool prefill_fp8_block_tc_supported(const PrefillParams& p) {
     if (p.head_dim != kD || p.group > 8 || B < 8 || B > 128 || (B & (B - 1)) != 0) return false;
     if (((uintptr_t)p.k_cache & 15) || ((uintptr_t)p.v_cache & 15) || ((uintptr_t)p.q & 15) || ((uintptr_t)p.out & 15))
         return false;
-    return (long long)p.num_blocks * B < (1LL << 31) && p.num_blocks > 0;
+    // (items: at most 2 * 152 more than the tiles of every chunk and kv head, by the spans' rule)
+    return (long long)p.num_blocks * B < (1LL << 31) && p.num_blocks > 0 &&
+           work_items(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group) < (1LL << 29);
 }
 
 int launch_prefill_fp8_block_tc(const PrefillParams& p, void* workspace, int num_sms, cudaStream_t stream) {
