@@ -33,8 +33,8 @@
 // the chain P -> P V -> Q K^T.  The query terms are in tensor memory too: as
 // shared-memory operands they were read again by every product, and shared
 // memory bandwidth set the pace (2.65k cycles per key tile against 1.0k of
-// tensor work).  The maximum is lazy: O is rescaled only when it grows by more
-// than 2^8.
+// tensor work).  The maximum is lazy: it is looked for, and O rescaled, only
+// when a piece's weights under the old one come to more than 2^9.
 //
 // Few rows: the plan cuts the keys of a tile into spans, whose partial results
 // (float, in the workspace) a second kernel joins.
@@ -63,7 +63,7 @@ constexpr int kPieces = 3;  // ring of S pieces
 constexpr int kItems = 8;   // ring of item descriptions
 // tensor memory columns: O of group 0 and 1, the query terms (hi, lo; four codes a column), the S pieces
 constexpr uint32_t kTO = 0, kTQ = 256, kTS = 320;
-constexpr float kLazy = 8.f;
+constexpr float kMost = 512.f;  // largest sum of a piece's weights before a row's maximum is looked for again
 constexpr float kTiny = 1e-37f;  // the least factor of a score: 0 would make NaN of a masked key's -inf
 constexpr float kScaleFloor = 7.703719777548943e-34f;  // 2^-110, the smallest R
 
@@ -79,7 +79,7 @@ constexpr int kQf = kR + kInfo * 4;                        // float [kQSlots][12
 constexpr int kState = kQf + kQSlots * kTile * 4;          // float4 [2 items][2 groups][128]: m, l, R
 constexpr int kItem = kState + 2 * 2 * kTile * 16;  // Item [kItems]
 constexpr int kBars = kItem + kItems * 48;
-constexpr int kNumBars = 2 * kKStages + 2 * kVStages + 2 * kVhStages + 3 * kPieces + 2 + kQSlots + 1 + kInfo + 2 * kItems + 3;
+constexpr int kNumBars = 2 * kKStages + 2 * kVStages + kVhStages + 3 * kPieces + kQSlots + 1 + kInfo + 2 * kItems + 3;
 constexpr int kTmemSlot = kBars + kNumBars * 8;
 constexpr size_t kSmemBytes = 1024 + kTmemSlot + 16;
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
@@ -98,12 +98,10 @@ struct Bars {
     __device__ uint64_t* v_full(int i) const { return base + 2 * kKStages + i; }
     __device__ uint64_t* v_empty(int i) const { return v_full(kVStages + i); }
     __device__ uint64_t* vh_full(int i) const { return v_full(2 * kVStages + i); }
-    __device__ uint64_t* vh_empty(int i) const { return vh_full(kVhStages + i); }
-    __device__ uint64_t* s_full(int i) const { return vh_full(2 * kVhStages + i); }
+    __device__ uint64_t* s_full(int i) const { return vh_full(kVhStages + i); }
     __device__ uint64_t* p_full(int i) const { return s_full(kPieces + i); }
-    __device__ uint64_t* s_empty(int i) const { return s_full(2 * kPieces + i); }
-    __device__ uint64_t* o_done(int x) const { return s_full(3 * kPieces + x); }
-    __device__ uint64_t* q_full(int i) const { return o_done(2 + i); }
+    __device__ uint64_t* pv_done(int i) const { return s_full(2 * kPieces + i); }
+    __device__ uint64_t* q_full(int i) const { return pv_done(kPieces + i); }
     __device__ uint64_t* q_empty() const { return q_full(kQSlots); }
     __device__ uint64_t* info(int i) const { return q_full(kQSlots + 1 + i); }
     __device__ uint64_t* item_full(int i) const { return info(kInfo + i); }
@@ -169,6 +167,9 @@ __device__ __forceinline__ int key_cap(const PrefillParams& p, int s) {
     return (int)min(min((long long)p.context_lens[s], (long long)p.max_context_len), table);
 }
 
+// kKeys: keys that share a block, and so their factors, as far as the softmax goes by it: 8, 16 or 32 (the block size up
+// to 32).  Fewer factors are fewer instructions of the loop that sets the pace.
+template <int kKeys>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_fp8_block_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                                 const PrefillParams p, const Spans spans) {
@@ -192,16 +193,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(bars.v_full(i), 1);
             mbar_init(bars.v_empty(i), kConverters);
         }
-        for (int i = 0; i < kVhStages; ++i) {
-            mbar_init(bars.vh_full(i), kConverters);
-            mbar_init(bars.vh_empty(i), 1);
-        }
+        for (int i = 0; i < kVhStages; ++i) mbar_init(bars.vh_full(i), kConverters);
         for (int i = 0; i < kPieces; ++i) {
             mbar_init(bars.s_full(i), 1);
             mbar_init(bars.p_full(i), 4);
-            mbar_init(bars.s_empty(i), 1);
+            mbar_init(bars.pv_done(i), 1);
         }
-        for (int x = 0; x < 2; ++x) mbar_init(bars.o_done(x), 1);
         mbar_init(bars.q_empty(), 1);
         for (int i = 0; i < kQSlots; ++i) mbar_init(bars.q_full(i), kConverters);
         for (int i = 0; i < kInfo; ++i) mbar_init(bars.info(i), 1);
@@ -418,38 +415,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && !mbar_wait_warp(bar, parity)) ok = false;
             return ok;
         };
-        uint32_t g = 0, items = 0, piece = 0;  // key tiles, items with keys, pieces so far
+        uint32_t g = 0, items = 0, sb = 0, round = 0;  // key tiles, items with keys; the piece's buffer and its round
         Item d;
         for (uint32_t n = 0; ok && take_item(n, d); ++n) {
-            if (d.nt == 0) continue;
+            const uint32_t nt = uniform(d.nt);
+            if (nt == 0) continue;
             // an item's first S waits for its query terms, its first product until the last item's epilogue has read O
             if (s_side) wait(bars.q_full(items % kQSlots), (items / kQSlots) & 1);
             else if (items > 0) wait(bars.o_free(), (items - 1) & 1);
-            for (int j = 0; j < d.nt && ok; ++j, ++g) {
+            for (uint32_t j = 0; j < nt && ok; ++j, ++g) {
                 const uint32_t st = g % kKStages, vh = g % kVhStages;
                 if (s_side) wait(bars.k_full(st), (g / kKStages) & 1);
                 else wait(bars.vh_full(vh), (g / kVhStages) & 1);
 #pragma unroll
-                for (int x = 0; x < 2; ++x, ++piece) {
-                    const uint32_t sb = piece % kPieces, round = piece / kPieces;
+                for (uint32_t x = 0; x < 2; ++x) {
                     if (s_side) {
-                        if (round > 0 && !wait(bars.s_empty(sb), (round - 1) & 1)) break;
+                        if (round > 0 && !wait(bars.pv_done(sb), (round - 1) & 1)) break;
                         tc_fence_after();
-                        issue_s(tmem + kTS + uniform(sb * 64), tmem + kTQ,
-                                (uint32_t)dk0 + uniform((st * kCodes + x * 64 * kD) >> 4), (uint32_t)(dk0 >> 32), idesc_s);
+                        issue_s(tmem + kTS + sb * 64, tmem + kTQ,
+                                (uint32_t)dk0 + ((st * kCodes + x * 64 * kD) >> 4), (uint32_t)(dk0 >> 32), idesc_s);
                         umma_commit_warp(bars.s_full(sb));
                         if (x) umma_commit_warp(bars.k_empty(st));
-                        if (x && j == d.nt - 1) umma_commit_warp(bars.q_empty());
+                        if (x && j == nt - 1) umma_commit_warp(bars.q_empty());
                     } else {
                         if (!wait(bars.p_full(sb), round & 1)) break;
                         tc_fence_after();
-                        issue_o(tmem + kTO + x * 128, tmem + kTS + uniform(sb * 64),
-                                (uint32_t)dv0 + uniform((vh * 2 * kHalfBytes + x * 64 * 128) >> 4),
-                                (uint32_t)(dv0 >> 32), idesc_o, uniform(j > 0));
-                        umma_commit_warp(bars.s_empty(sb));
-                        umma_commit_warp(bars.o_done(x));
-                        if (x) umma_commit_warp(bars.vh_empty(vh));
+                        issue_o(tmem + kTO + x * 128, tmem + kTS + sb * 64,
+                                (uint32_t)dv0 + ((vh * 2 * kHalfBytes + x * 64 * 128) >> 4), (uint32_t)(dv0 >> 32),
+                                idesc_o, j);
+                        umma_commit_warp(bars.pv_done(sb));  // frees the piece, and the widened V with its second
                     }
+                    if (++sb == kPieces) sb = 0, ++round;
                 }
             }
             ++items;
@@ -551,25 +547,27 @@ __global__ void __launch_bounds__(kThreads, 1)
             int rows = 0;  // rows of the next item's tile that are split (of this warp's 32)
             for (int j = 0; j < d.nt; ++j, ++g) {
                 const uint32_t vs = g % kVStages, vh = g % kVhStages;
+                const uint32_t last = 2 * (g - kVhStages) + 1;  // the piece that read this buffer last
                 if (!mbar_wait_warp(bars.info(g % kInfo), (g / kInfo) & 1) ||
-                    (g >= kVhStages && !mbar_wait_warp(bars.vh_empty(vh), ((g / kVhStages) - 1) & 1)) ||
+                    (g >= kVhStages && !mbar_wait_warp(bars.pv_done(last % kPieces), (last / kPieces) & 1)) ||
                     !mbar_wait_warp(bars.v_full(vs), (g / kVStages) & 1)) {
                     ok = false;
                     break;
                 }
-                // a lane widens 16 codes of a key; 8 lanes a key, so a warp takes keys 4 i + (lane / 8)
-                const uint8_t* src = smem + kV + vs * kCodes;
-                uint8_t* dst = smem + kVh + vh * 2 * kHalfBytes;
-                const int ch = lane & 7;
+                // a lane widens 16 codes of a key, 8 lanes a key; a warp takes keys 16 i + 4 w .. + 3, whose swizzle is
+                // the same for every i
+                const uint32_t key0 = 4 * w + (lane >> 3), ch = lane & 7, sw = key0 & 7;
+                const uint8_t* src = smem + kV + vs * kCodes + key0 * kD + ((ch ^ sw) << 4);
+                uint8_t* dst = smem + kVh + vh * 2 * kHalfBytes + (ch >> 2) * kHalfBytes + key0 * 128;
+                uint8_t *dst0 = dst + ((((ch & 3) * 2) ^ sw) << 4), *dst1 = dst + ((((ch & 3) * 2 + 1) ^ sw) << 4);
                 const uint4 m = *reinterpret_cast<const uint4*>(mask + (g % kInfo) * 4);
                 const bool all_valid = (m.x & m.y & m.z & m.w) == ~0u;
-#pragma unroll 4
+#pragma unroll
                 for (int i = 0; i < kTile / 16; ++i) {
-                    const int key = (i * 4 + w) * 4 + (lane >> 3);
-                    uint4 x = *reinterpret_cast<const uint4*>(src + key * kD + ((ch ^ (key & 7)) << 4));
+                    uint4 x = *reinterpret_cast<const uint4*>(src + i * 16 * kD);
                     if (!all_valid) {
                         const uint32_t word = i < 2 ? m.x : i < 4 ? m.y : i < 6 ? m.z : m.w;
-                        if (!((word >> (key & 31)) & 1u)) x = make_uint4(0u, 0u, 0u, 0u);
+                        if (!((word >> ((i & 1) * 16 + key0)) & 1u)) x = make_uint4(0u, 0u, 0u, 0u);
                     }
                     const uint32_t in[4] = {x.x, x.y, x.z, x.w};
                     uint32_t out[8];
@@ -578,11 +576,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         out[2 * k] = e4m3x2_to_f16x2(in[k] & 0xFFFFu);
                         out[2 * k + 1] = e4m3x2_to_f16x2(in[k] >> 16);
                     }
-                    uint8_t* row = dst + (ch >> 2) * kHalfBytes + key * 128;
-                    const int c0 = (ch & 3) * 2;
-                    *reinterpret_cast<uint4*>(row + ((c0 ^ (key & 7)) << 4)) = make_uint4(out[0], out[1], out[2], out[3]);
-                    *reinterpret_cast<uint4*>(row + (((c0 + 1) ^ (key & 7)) << 4)) =
-                        make_uint4(out[4], out[5], out[6], out[7]);
+                    *reinterpret_cast<uint4*>(dst0 + i * 16 * 128) = make_uint4(out[0], out[1], out[2], out[3]);
+                    *reinterpret_cast<uint4*>(dst1 + i * 16 * 128) = make_uint4(out[4], out[5], out[6], out[7]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
@@ -639,7 +634,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 wait(bars.s_full(sb), (piece / kPieces) & 1);
                 if (!ok) break;
                 tc_fence_after();
-                {
+                const int key0 = (d.t0 + j) * kTile + x * 64;
+                // the row's visible and valid keys as 64 bits; dense: all of them, for every row of the warp
+                const int vis = my_last - key0 + 1;
+                const uint32_t w0 = vm.x & (vis >= 32 ? ~0u : vis > 0 ? (1u << vis) - 1u : 0u);
+                const uint32_t w1 = vm.y & (vis >= 64 ? ~0u : vis > 32 ? (1u << (vis - 32)) - 1u : 0u);
+                const bool dense = __all_sync(0xffffffffu, (w0 & w1) == ~0u);
+                const bool first = j == 0;  // nothing in O yet
+                if (first) Rc = R;
+                // The weights are taken with the maximum so far.  Only when a row's 64 of them come to more than 2^9
+                // (which is how a larger score shows, without a pass for the maximum), when R has changed or at the
+                // item's first piece, the maximum is looked for, O brought to it, and the weights taken again.
+                bool look = first || R != Rc || __any_sync(0xffffffffu, m == -INFINITY);
+                uint32_t pk[32];
+                float sum;
+                while (true) {
                     float s[64];
                     {
                         float a[32], b[32];
@@ -649,70 +658,65 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 32; ++i) s[i] = a[i], s[32 + i] = b[i];
                     }
                     tmem_wait_ld();
-                    const int key0 = (d.t0 + j) * kTile + x * 64;
-                    const uint32_t m0 = vm.x, m1 = vm.y;
-                    // dense: every key is valid and every row of the warp sees it
-                    const bool dense = __all_sync(0xffffffffu, (m0 & m1) == ~0u && key0 + 63 <= my_last);
-                    if (!dense) {  // the row's visible and valid keys as 64 bits; the others get -inf
-                        const int vis = my_last - key0 + 1;
-                        const uint32_t w0 = m0 & (vis >= 32 ? ~0u : vis > 0 ? (1u << vis) - 1u : 0u);
-                        const uint32_t w1 = m1 & (vis >= 64 ? ~0u : vis > 32 ? (1u << (vis - 32)) - 1u : 0u);
+                    if (!dense) {
 #pragma unroll
                         for (int k = 0; k < 64; ++k)
                             if (!((k < 32 ? w0 : w1) & (1u << (k & 31)))) s[k] = -INFINITY;
                     }
-                    float mx[8];
+                    if (look) {
+                        float mt = m;
 #pragma unroll
-                    for (int b = 0; b < 8; ++b) {
-                        const float u = fmax3(s[8 * b], s[8 * b + 1], s[8 * b + 2]);
-                        const float v = fmax3(s[8 * b + 3], s[8 * b + 4], s[8 * b + 5]);
-                        mx[b] = fmax3(u, v, fmaxf(s[8 * b + 6], s[8 * b + 7])) * fmaxf(kc[b].x * qf, kTiny);
-                    }
-                    const float mt = fmaxf(fmax3(mx[0], mx[1], mx[2]), fmax3(fmax3(mx[3], mx[4], mx[5]), mx[6], mx[7]));
-                    const bool first = j == 0;  // nothing in O yet
-                    if (first) Rc = R;
-                    const float m_new = mt > m + kLazy ? mt : m;  // also the first finite maximum
-                    if (!first && __any_sync(0xffffffffu, m_new != m || R != Rc)) {
-                        // the products issued so far have to be done before O changes
-                        wait(bars.o_done(x), (t - 1) & 1);
-                        tc_fence_after();
-                        const float alpha = m_new == m ? 1.f : fast_exp2(m - m_new), f = alpha * (Rc / R);
-#pragma unroll 1
-                        for (int q = 0; q < 8; ++q) {
-                            float o[16];
-                            tmem_ld16(t_o + q * 16, o);
-                            tmem_wait_ld();
+                        for (int b = 0; b < 64; b += kKeys) {
+                            float u[2] = {s[b], s[b + 1]};
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] *= f;
-                            tmem_st16(t_o + q * 16, o);
+                            for (int i = 2; i < kKeys; i += 2) u[i / 2 & 1] = fmax3(u[i / 2 & 1], s[b + i], s[b + i + 1]);
+                            mt = fmaxf(mt, fmaxf(u[0], u[1]) * fmaxf(kc[b / 8].x * qf, kTiny));
                         }
-                        tmem_wait_st();
-                        l *= alpha;
-                        Rc = R;
+                        if (!first) {
+                            // the products issued so far have to be done before O changes
+                            wait(bars.pv_done((piece - 2) % kPieces), ((piece - 2) / kPieces) & 1);
+                            tc_fence_after();
+                            const float alpha = mt == m ? 1.f : fast_exp2(m - mt), f = alpha * (Rc / R);
+#pragma unroll 1
+                            for (int q = 0; q < 8; ++q) {
+                                float o[16];
+                                tmem_ld16(t_o + q * 16, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] *= f;
+                                tmem_st16(t_o + q * 16, o);
+                            }
+                            tmem_wait_st();
+                            l *= alpha;
+                            Rc = R;
+                        }
+                        m = mt;
                     }
-                    m = m_new;
-                    uint32_t pk[32];
-                    float sum = 0.f;
+                    sum = 0.f;
                     const float m_fin = m == -INFINITY ? 0.f : m;  // no key yet: every P' is 2^-inf
 #pragma unroll
-                    for (int b = 0; b < 8; ++b) {
-                        const float4 k4 = kc[b];
+                    for (int b = 0; b < 64; b += kKeys) {
+                        const float4 k4 = kc[b / 8];
                         const float a = fmaxf(k4.x * qf, kTiny), o = k4.y - m_fin;
                         const unsigned long long a2 = f32x2_pack(a, a), o2 = f32x2_pack(o, o);
-                        float e[8];
+                        unsigned long long part[2];  // the keys' weights, in pairs and two chains
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) {
+                        for (int i = 0; i < kKeys / 2; ++i) {
                             float y0, y1;
-                            f32x2_unpack(fma_f32x2(f32x2_pack(s[8 * b + 2 * i], s[8 * b + 2 * i + 1]), a2, o2), y0, y1);
-                            e[2 * i] = fast_exp2(y0);
-                            e[2 * i + 1] = fast_exp2(y1);
-                            pk[4 * b + i] = pack_f16x2(e[2 * i], e[2 * i + 1]);
+                            f32x2_unpack(fma_f32x2(f32x2_pack(s[b + 2 * i], s[b + 2 * i + 1]), a2, o2), y0, y1);
+                            const float e0 = fast_exp2(y0), e1 = fast_exp2(y1);
+                            pk[b / 2 + i] = pack_f16x2(e0, e1);
+                            part[i & 1] = i < 2 ? f32x2_pack(e0, e1) : add_f32x2(part[i & 1], f32x2_pack(e0, e1));
                         }
                         float u, v;
-                        f32x2_unpack(add_f32x2(add_f32x2(f32x2_pack(e[0], e[1]), f32x2_pack(e[2], e[3])),
-                                               add_f32x2(f32x2_pack(e[4], e[5]), f32x2_pack(e[6], e[7]))), u, v);
+                        f32x2_unpack(add_f32x2(part[0], part[1]), u, v);
                         sum = fmaf(u + v, k4.z, sum);
                     }
+                    // (at most 2^9, times the 64 that vs / R may reach, is below f16's largest number)
+                    if (look || !__any_sync(0xffffffffu, sum > kMost)) break;
+                    look = true;
+                }
+                {
                     l += sum;
                     tmem_st32u(t_s, pk);
                     tmem_wait_st();
@@ -724,7 +728,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- the item's output: both groups' states joined, each group stores 64 columns of the row
             float mo = -INFINITY, lo = 0.f, Ro = 1.f;
             if (d.nt > 0) {
-                wait(bars.o_done(x), (g + d.nt - 1) & 1);
+                const uint32_t last = 2 * (g + d.nt - 1) + x;  // this group's last piece
+                wait(bars.pv_done(last % kPieces), (last / kPieces) & 1);
                 // (two copies by item: the other group may be an item behind)
                 float4* st = state + (items & 1) * 2 * kTile;
                 st[x * kTile + r] = make_float4(m, l, Rc, 0.f);
@@ -900,8 +905,10 @@ int launch_prefill_fp8_block_tc(const PrefillParams& p, void* workspace, int num
     if (rc != PA_OK) return rc;
     if ((rc = pool_tensor_map_rows(&tmv, p.v_cache, p.num_blocks, p.block_size, p.num_kv_heads, kD, true)) != PA_OK)
         return rc;
-    if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(prefill_fp8_block_tc_kernel), kSmemBytes)) != PA_OK)
-        return rc;
+    auto kernel = p.block_size == 8    ? prefill_fp8_block_tc_kernel<8>
+                  : p.block_size == 16 ? prefill_fp8_block_tc_kernel<16>
+                                       : prefill_fp8_block_tc_kernel<32>;
+    if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), kSmemBytes)) != PA_OK) return rc;
     Spans s = plan_spans(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group, p.max_context_len, num_sms);
     if (s.count > 1) {
         const size_t rows = (size_t)s.count * p.total_q * p.num_q_heads;
@@ -909,7 +916,7 @@ int launch_prefill_fp8_block_tc(const PrefillParams& p, void* workspace, int num
         s.ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + up256(rows * kD * sizeof(float)));
     }
     const long long items = work_items(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group) * s.count;
-    rc = launch_kernel(prefill_fp8_block_tc_kernel, dim3((unsigned)(items < num_sms ? items : num_sms)),
+    rc = launch_kernel(kernel, dim3((unsigned)(items < num_sms ? items : num_sms)),
                        dim3(kThreads), kSmemBytes, stream, tmk, tmv, p, s);
     if (rc != PA_OK || s.count <= 1) return rc;
     const long long warps = (long long)p.total_q * p.num_q_heads, ctas = (warps + 3) / 4;
