@@ -10,13 +10,13 @@
 // so does a code's move to a larger scale (only e4m3's subnormals round), so
 // a block that grows token by token loses nothing by being stored again.
 //
-// The work unit is a physical block: one CTA gathers all of the call's tokens
-// that fall into the block (whatever their order in the arrays), so the
-// maximum needs no atomics and every code is written once.  A warp takes one
-// (head, K or V) of the block: it loads the rows once into registers (up to
-// 256 16-byte pieces, a 16-token block of head_dim 128; larger blocks are read
-// twice, the second time from L1/L2), takes the maximum with one warp
-// reduction and stores the codes.
+// The work unit is a physical block with all of the call's tokens that fall
+// into it (whatever their order in the arrays), so the maximum needs no atomics
+// and every code is written once.  A warp takes one (head, K or V) of the block:
+// it loads the rows into registers (256 16-byte
+// pieces at a time, a 16-token block of head_dim 128; of larger blocks all but
+// the last 256 are loaded twice, the second time from L1/L2), takes the maximum
+// with one warp reduction and stores the codes.
 //
 // Finding a block's tokens:
 //   * up to kScanTokens tokens (decode steps): one launch, a CTA per token;
@@ -25,7 +25,8 @@
 //   * more tokens: a first launch resolves each token once, records it as its
 //     slot's writer (atomicMax, so of several tokens naming one slot the last
 //     is stored, as in the one-launch form) and lists each block once; a second
-//     launch walks the list.  It leaves the workspace zeroed again.
+//     launch walks the list, a warp per (block, head, side) without a barrier
+//     among them.  It leaves the workspace zeroed again.
 //
 // Bound: HBM for long calls, launch and memory latency for a decode step.
 #include "pa_internal.cuh"
@@ -56,7 +57,7 @@ struct BlockWriteParams {
     // two-launch form (workspace)
     int32_t* counters;  // [0] blocks listed, [1] CTAs done
     int32_t* listed;    // [num_blocks] 1: the block is on the list
-    int32_t* finished;  // [num_blocks] CTAs (grid.y) that have read the block's writers
+    int32_t* finished;  // [num_blocks] warps that are through with the block's writers
     int32_t* writer;    // [num_blocks][block_size] token + 1 of the slot's writer, 0: none
     int32_t* list;      // [min(num_tokens, num_blocks)] the listed blocks
 };
@@ -73,14 +74,18 @@ __device__ __forceinline__ int resolve(const BlockWriteParams& p, int t, int& of
     return pb >= 0 && pb < p.num_blocks ? pb : -2;
 }
 
-// Largest finite magnitude of eight bf16 as bf16 bits (infinities and NaN take no part in the scale).
+// Magnitudes of eight bf16, the larger of each pair of halves, as two 16-bit maxima in one word.
 __device__ __forceinline__ uint32_t amax_bits8(const uint4& x, uint32_t m) {
+    m = __vmaxu2(m, __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu));
+    return __vmaxu2(m, __vmaxu2(x.z & 0x7FFF7FFFu, x.w & 0x7FFF7FFFu));
+}
+// The same with infinities and NaN left out: they take no part in the scale.
+__device__ __forceinline__ uint32_t amax_finite8(const uint4& x, uint32_t m) {
     const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = w[i] & 0x7FFFu, hi = (w[i] >> 16) & 0x7FFFu;
-        m = max(m, lo >= 0x7F80u ? 0u : lo);
-        m = max(m, hi >= 0x7F80u ? 0u : hi);
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t v = (w[i >> 1] >> (16 * (i & 1))) & 0x7FFFu;
+        m = __vmaxu2(m, v >= 0x7F80u ? 0u : v);
     }
     return m;
 }
@@ -91,12 +96,14 @@ __device__ __forceinline__ float scale_of_amax(uint32_t bf16_bits) {
     return __uint_as_float((uint32_t)((bf16_bits == 0 ? kMinExponent : max(e, kMinExponent)) + 127) << 23);
 }
 
-// Four bf16 to four e4m3 codes of x / s: a product with the exact reciprocal when s is a power of two.
-__device__ __forceinline__ uint32_t codes4(uint2 x, float s, float inv, bool pow2) {
-    if (pow2) return e4m3x4_of_bf16x4(x, inv);
-    const float a = __fdiv_rn(__uint_as_float(x.x << 16), s), b = __fdiv_rn(__uint_as_float(x.x & 0xFFFF0000u), s);
-    const float c = __fdiv_rn(__uint_as_float(x.y << 16), s), d = __fdiv_rn(__uint_as_float(x.y & 0xFFFF0000u), s);
-    return (uint32_t)pack_e4m3x2(a, b) | ((uint32_t)pack_e4m3x2(c, d) << 16);
+// Eight bf16 to eight e4m3 codes of x / s for an s that is no power of two (one that the caller put there).
+__device__ __forceinline__ uint2 codes8_div(const uint4& x, float s) {
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint32_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        c[i] = pack_e4m3x2(__fdiv_rn(__uint_as_float(w[i] << 16), s), __fdiv_rn(__uint_as_float(w[i] & 0xFFFF0000u), s));
+    return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
 
 // Two codes moved to a scale 1 / f times as large (f <= 1).
@@ -105,87 +112,110 @@ __device__ __forceinline__ uint16_t recode2(uint16_t c, float f) {
     return pack_e4m3x2(__fmul_rn(v.x, f), __fmul_rn(v.y, f));
 }
 
-// One warp stores the call's rows of (block pb, head h, K or V): members [n] pairs (token, offset).
-__device__ void store_rows(const BlockWriteParams& p, int pb, int pair, const int2* members, int n,
-                           const int32_t* writer, bool fresh, int lane) {
-    const int h = pair >> 1, D = p.head_dim, pieces = D / 8, row_pieces = p.num_kv_heads * pieces;
+// One warp stores the call's rows of (block pb, head h, K or V); writer[off] is the token + 1 that the call stores in
+// slot off, 0 for none.  kPieces: 16-byte pieces of a row's head (head_dim / 8), 0 for a head_dim that is no 64 or
+// 128, whose pieces take a division each.
+template <int kPieces>
+__device__ __forceinline__ void store_rows(const BlockWriteParams& p, int pb, int pair, const int32_t* writer,
+                                           int lane) {
+    const int h = pair >> 1, D = p.head_dim, pieces = kPieces ? kPieces : D / 8, row_pieces = p.num_kv_heads * pieces;
     const uint4* src = ((pair & 1) ? p.v_new : p.k_new) + h * pieces;
-    uint8_t* cache = ((pair & 1) ? p.v_cache : p.k_cache) + (size_t)h * D;
+    const size_t row_bytes = (size_t)p.num_kv_heads * D;
+    uint8_t* cache = ((pair & 1) ? p.v_cache : p.k_cache) + (size_t)pb * p.block_size * row_bytes + (size_t)h * D;
     float* scale_ptr = ((pair & 1) ? p.v_scales : p.k_scales) + (size_t)pb * p.num_kv_heads + h;
-    const size_t row_bytes = (size_t)p.num_kv_heads * D, slot0 = (size_t)pb * p.block_size;
-    const int total = n * pieces;
+    const int total = p.block_size * pieces;
     const float old = *scale_ptr;
+    const bool fresh = writer[0] != 0;
+    // the block's pieces in batches of kCached a lane, whose loads go out together; the last batch of the first pass
+    // stays in registers for the second, which walks them the other way
+    constexpr int kBatch = 32 * kCached;
+    const int last = (total - 1) / kBatch * kBatch;
     uint4 x[kCached];
+    int tok[kCached];
+    auto load_batch = [&](int i0) {
+#pragma unroll
+        for (int k = 0; k < kCached; ++k) {
+            const int i = i0 + lane + 32 * k;
+            tok[k] = i < total ? writer[i / pieces] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < kCached; ++k) {
+            const int i = i0 + lane + 32 * k;
+            x[k] = make_uint4(0u, 0u, 0u, 0u);
+            if (tok[k] != 0) x[k] = __ldg(src + (size_t)(tok[k] - 1) * row_pieces + i % pieces);
+        }
+    };
     uint32_t am = 0;
+#pragma unroll 1
+    for (int i0 = 0; i0 <= last; i0 += kBatch) {
+        load_batch(i0);
 #pragma unroll
-    for (int k = 0; k < kCached; ++k) {
-        const int i = lane + 32 * k;
-        if (i < total) x[k] = __ldg(src + (size_t)members[i / pieces].x * row_pieces + i % pieces);
+        for (int k = 0; k < kCached; ++k) am = amax_bits8(x[k], am);
     }
-#pragma unroll
-    for (int k = 0; k < kCached; ++k)
-        if (lane + 32 * k < total) am = amax_bits8(x[k], am);
-    for (int i = lane + 32 * kCached; i < total; i += 32)
-        am = amax_bits8(__ldg(src + (size_t)members[i / pieces].x * row_pieces + i % pieces), am);
-    am = __reduce_max_sync(0xffffffffu, am);
+    am = __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
+    if (am >= 0x7F80u) {  // an infinity or a NaN among them: once more, without
+        am = 0;
+#pragma unroll 1
+        for (int i = lane; i < total; i += 32) {
+            const int t = writer[i / pieces];
+            if (t != 0) am = amax_finite8(__ldg(src + (size_t)(t - 1) * row_pieces + i % pieces), am);
+        }
+        am = __reduce_max_sync(0xffffffffu, max(am & 0xFFFFu, am >> 16));
+    }
     const float base = !fresh && old > 0.f ? old : 0.f;
     const float s = fmaxf(base, scale_of_amax(am));
-    const float inv = 1.0f / s;
+    const float inv = 1.0f / s;  // exact for a power of two
     const bool pow2 = (__float_as_uint(s) & 0x7FFFFFu) == 0;
-    auto put = [&](int i, const uint4& v) {
-        const uint2 c = make_uint2(codes4(make_uint2(v.x, v.y), s, inv, pow2),
-                                   codes4(make_uint2(v.z, v.w), s, inv, pow2));
-        *reinterpret_cast<uint2*>(cache + (slot0 + members[i / pieces].y) * row_bytes + (i % pieces) * 8) = c;
+    auto slot = [&](int i) {  // the eight codes of piece i
+        const int off = i / pieces;
+        return reinterpret_cast<uint2*>(cache + off * row_bytes + (i - off * pieces) * 8);
     };
+#pragma unroll 1
+    for (int i0 = last; i0 >= 0; i0 -= kBatch) {
+        if (i0 != last) load_batch(i0);
 #pragma unroll
-    for (int k = 0; k < kCached; ++k)
-        if (lane + 32 * k < total) put(lane + 32 * k, x[k]);
-    for (int i = lane + 32 * kCached; i < total; i += 32)
-        put(i, __ldg(src + (size_t)members[i / pieces].x * row_pieces + i % pieces));
+        for (int k = 0; k < kCached; ++k)
+            if (tok[k] != 0)
+                *slot(i0 + lane + 32 * k) = make_uint2(e4m3x4_of_bf16x4(make_uint2(x[k].x, x[k].y), inv),
+                                                       e4m3x4_of_bf16x4(make_uint2(x[k].z, x[k].w), inv));
+    }
+    if (!pow2) {  // under a scale that the caller put there: the quotients, not the products with a rounded reciprocal
+#pragma unroll 1
+        for (int i = lane; i < total; i += 32) {
+            const int t = writer[i / pieces];
+            if (t != 0) *slot(i) = codes8_div(__ldg(src + (size_t)(t - 1) * row_pieces + i % pieces), s);
+        }
+    }
     if (!fresh && s > base) {  // the block's other codes keep their values under the larger scale
         const float f = __fdiv_rn(base, s);
-        const int kept = p.block_size * pieces;
-        for (int i = lane; i < kept; i += 32) {
-            const int off = i / pieces;
-            if (writer[off] != 0) continue;
-            uint2* c = reinterpret_cast<uint2*>(cache + (slot0 + off) * row_bytes + (i % pieces) * 8);
-            const uint2 v = *c;
-            *c = make_uint2((uint32_t)recode2((uint16_t)v.x, f) | ((uint32_t)recode2((uint16_t)(v.x >> 16), f) << 16),
-                            (uint32_t)recode2((uint16_t)v.y, f) | ((uint32_t)recode2((uint16_t)(v.y >> 16), f) << 16));
+#pragma unroll 1
+        for (int i0 = lane; i0 < total; i0 += 32 * 4) {
+            uint2 v[4];
+            bool keep[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int i = i0 + 32 * k;
+                keep[k] = i < total && writer[i / pieces] == 0;
+                if (keep[k]) v[k] = *slot(i);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (keep[k])
+                    *slot(i0 + 32 * k) = make_uint2(
+                        (uint32_t)recode2((uint16_t)v[k].x, f) | ((uint32_t)recode2((uint16_t)(v[k].x >> 16), f) << 16),
+                        (uint32_t)recode2((uint16_t)v[k].y, f) | ((uint32_t)recode2((uint16_t)(v[k].y >> 16), f) << 16));
         }
     }
     __syncwarp();  // every lane has read the old scale
     if (lane == 0) *scale_ptr = s;
 }
 
-// The block's stored rows as (token, offset) pairs in offset order, from writer[0..B); all threads; returns how many.
-__device__ int gather_members(const int32_t* writer, int B, int2* members, int* warp_count) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int base = 0;
-    for (int b0 = 0; b0 < B; b0 += kThreads) {
-        const int off = b0 + threadIdx.x, w = off < B ? writer[off] : 0;
-        const uint32_t hit = __ballot_sync(0xffffffffu, w != 0);
-        __syncthreads();  // the previous round's counts have been read
-        if (lane == 0) warp_count[warp] = __popc(hit);
-        __syncthreads();
-        int at = base;
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) at += warp_count[i];
-            base += warp_count[i];
-        }
-        if (w != 0) members[at + __popc(hit & ((1u << lane) - 1u))] = make_int2(w - 1, off);
-    }
-    __syncthreads();
-    return base;
-}
-
 // One launch: CTA (token, slice of the (head, side) pairs).  The first token of each block stores the block.
-__global__ void __launch_bounds__(kThreads) write_scan_kernel(const BlockWriteParams p) {
+template <int kPieces>
+__global__ void __launch_bounds__(kThreads, 4) write_scan_kernel(const BlockWriteParams p) {
     pdl_trigger();
     pdl_wait();
     __shared__ int32_t writer[kMaxBlock];
-    __shared__ int2 members[kMaxBlock];
-    __shared__ int warp_count[kWarps];
     const int t = blockIdx.x, B = p.block_size;
     for (int i = threadIdx.x; i < B; i += kThreads) writer[i] = 0;
     int my_off;
@@ -204,9 +234,8 @@ __global__ void __launch_bounds__(kThreads) write_scan_kernel(const BlockWritePa
         atomicMax(&writer[off], i + 1);
     }
     if (__syncthreads_or(earlier)) return;
-    const int n = gather_members(writer, B, members, warp_count);
     for (int pair = blockIdx.y * kWarps + (threadIdx.x >> 5); pair < 2 * p.num_kv_heads; pair += gridDim.y * kWarps)
-        store_rows(p, mine, pair, members, n, writer, writer[0] != 0, threadIdx.x & 31);
+        store_rows<kPieces>(p, mine, pair, writer, threadIdx.x & 31);
 }
 
 // Two launches, first: each token becomes its slot's writer and lists its block.
@@ -224,45 +253,34 @@ __global__ void __launch_bounds__(kThreads) write_list_kernel(const BlockWritePa
     if (atomicExch(&p.listed[pb], 1) == 0) p.list[atomicAdd(&p.counters[0], 1)] = pb;
 }
 
-// Second: CTA (block of the list, slice of the pairs).
-__global__ void __launch_bounds__(kThreads) write_listed_kernel(const BlockWriteParams p) {
+// Second: a warp per (block of the list, pair), each on its own.
+template <int kPieces>
+__global__ void __launch_bounds__(kThreads, 4) write_listed_kernel(const BlockWriteParams p) {
     pdl_trigger();
     pdl_wait();
-    __shared__ int32_t writer[kMaxBlock];
-    __shared__ int2 members[kMaxBlock];
-    __shared__ int warp_count[kWarps];
-    __shared__ int last;
-    const int B = p.block_size, count = p.counters[0];
-    for (int b = blockIdx.x; b < count; b += gridDim.x) {
-        const int pb = p.list[b];
-        int32_t* w = p.writer + (size_t)pb * B;
-        for (int i = threadIdx.x; i < B; i += kThreads) writer[i] = w[i];
-        __syncthreads();
-        // the last of the block's grid.y CTAs to have read its writers clears them for the next call
-        if (threadIdx.x == 0) {
-            __threadfence();
-            last = atomicAdd(&p.finished[pb], 1) == (int)gridDim.y - 1;
-        }
-        const int n = gather_members(writer, B, members, warp_count);
-        if (last) {
-            for (int i = threadIdx.x; i < B; i += kThreads) w[i] = 0;
-            if (threadIdx.x == 0) {
+    const int lane = threadIdx.x & 31, pairs = 2 * p.num_kv_heads, B = p.block_size;
+    const long long units = (long long)p.counters[0] * pairs, stride = (long long)gridDim.x * kWarps;
+    for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += stride) {
+        const int b = (int)(u / pairs), pb = p.list[b];
+        int32_t* writer = p.writer + (size_t)pb * B;
+        store_rows<kPieces>(p, pb, (int)(u - (long long)b * pairs), writer, lane);
+        // the last of the block's warps to have read its writers clears them for the next call
+        int done = 0;
+        if (lane == 0) done = atomicAdd(&p.finished[pb], 1);
+        if (__shfl_sync(0xffffffffu, done, 0) == pairs - 1) {
+            for (int i = lane; i < B; i += 32) writer[i] = 0;
+            if (lane == 0) {
                 p.finished[pb] = 0;
                 p.listed[pb] = 0;
                 p.list[b] = 0;
             }
         }
-        for (int pair = blockIdx.y * kWarps + (threadIdx.x >> 5); pair < 2 * p.num_kv_heads;
-             pair += gridDim.y * kWarps)
-            store_rows(p, pb, pair, members, n, writer, writer[0] != 0, threadIdx.x & 31);
-        __syncthreads();  // writer and members are read until here
     }
-    if (threadIdx.x == 0) {
-        __threadfence();
-        if (atomicAdd(&p.counters[1], 1) == (int)(gridDim.x * gridDim.y) - 1) {
-            atomicExch(&p.counters[0], 0);
-            atomicExch(&p.counters[1], 0);
-        }
+    // (every warp has read the count before its CTA adds its tick)
+    __syncthreads();
+    if (threadIdx.x == 0 && atomicAdd(&p.counters[1], 1) == (int)gridDim.x - 1) {
+        p.counters[0] = 0;
+        p.counters[1] = 0;
     }
 }
 
@@ -365,10 +383,12 @@ int launch_write_fp8_block(const void* k_new, const void* v_new, int num_tokens,
     p.block_size = block_size;
     p.num_seqs = num_seqs;
     p.max_blocks_per_seq = max_blocks_per_seq;
-    const int slices = (2 * num_kv_heads + kWarps - 1) / kWarps;
-    const int gy = slices < 64 ? slices : 64;
-    if (num_tokens <= kScanTokens)
-        return launch_kernel(write_scan_kernel, dim3(num_tokens, gy), dim3(kThreads), 0, stream, p);
+    const int slices = (2 * num_kv_heads + kWarps - 1) / kWarps, gy = slices < 64 ? slices : 64;
+    if (num_tokens <= kScanTokens) {
+        auto kernel = head_dim == 128 ? write_scan_kernel<16> : head_dim == 64 ? write_scan_kernel<8> : write_scan_kernel<0>;
+        // every slice scans the tokens again: worth it while the tokens alone leave SMs idle
+        return launch_kernel(kernel, dim3(num_tokens, num_tokens < 2 * num_sms ? gy : 1), dim3(kThreads), 0, stream, p);
+    }
     const WriteWorkspace w = write_workspace(num_tokens, num_blocks, block_size);
     char* ws = static_cast<char*>(workspace);
     p.counters = reinterpret_cast<int32_t*>(ws);
@@ -379,9 +399,11 @@ int launch_write_fp8_block(const void* k_new, const void* v_new, int num_tokens,
     const int rc = launch_kernel(write_list_kernel, dim3((num_tokens + kThreads - 1) / kThreads), dim3(kThreads), 0,
                                  stream, p);
     if (rc != PA_OK) return rc;
-    const int most = num_tokens < num_blocks ? num_tokens : num_blocks;
-    const int gx = most < 8 * num_sms ? most : 8 * num_sms;
-    return launch_kernel(write_listed_kernel, dim3(gx, gy), dim3(kThreads), 0, stream, p);
+    const long long most = ((long long)(num_tokens < num_blocks ? num_tokens : num_blocks) * 2 * num_kv_heads + kWarps - 1) / kWarps;
+    const int fill = 4 * num_sms;  // CTAs that fit the GPU
+    auto kernel =
+        head_dim == 128 ? write_listed_kernel<16> : head_dim == 64 ? write_listed_kernel<8> : write_listed_kernel<0>;
+    return launch_kernel(kernel, dim3((unsigned)(most < fill ? most : fill)), dim3(kThreads), 0, stream, p);
 }
 
 int launch_read_fp8_block(void* k_out, void* v_out, int num_tokens, int num_kv_heads, int head_dim, int dtype,
