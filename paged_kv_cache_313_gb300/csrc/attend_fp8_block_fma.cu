@@ -4,8 +4,8 @@
 // block sizes that are no power of two from 8 to 128).
 //
 // The loop is fma_attend.cuh's; codes are widened as they are read from the
-// staged rows.  Decode: one CTA per (sequence, kv head, partition), joined by
-// decode_merge.cu.  Prefill: one CTA per (query, kv head).
+// staged rows.  Decode: one CTA per (sequence, kv head, partition), joined as in
+// decode_fp8_block_tc.cu.  Prefill: one CTA per (query, kv head).
 #include "decode_common.cuh"
 #include "fma_attend.cuh"
 
@@ -21,9 +21,9 @@ __global__ void __launch_bounds__(kFmaThreads) decode_fp8_block_fma_kernel(Decod
     pdl_wait();
     const int s = blockIdx.x, kvh = blockIdx.y, split = blockIdx.z, G = p.group;
     const int L = decode_context(p, s, split == 0 && kvh == 0 && threadIdx.x == 0);
-    const int nsplit = num_partitions(L, p.partition);
+    const int part = partition_of(p, s), nsplit = num_partitions(L, part);
     if (split >= nsplit) return;
-    const int j0 = split * p.partition, j1 = min(L, j0 + p.partition);
+    const int j0 = split * part, j1 = min(L, j0 + part);
     extern __shared__ float smem[];
     __shared__ float m_s[kFmaMaxGroup], l_s[kFmaMaxGroup], alpha_s[kFmaMaxGroup];
     float acc[S::kItems];

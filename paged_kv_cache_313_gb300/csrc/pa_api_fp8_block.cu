@@ -14,10 +14,16 @@ bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_
 // partial result is small beside the codes it reads, short enough that the batch (at its longest context: the
 // lengths live on the device) gives every SM kItemsPerSm items; at most 128 partials per (sequence, head).
 #ifndef PA_FP8_BLOCK_PARTITION
-#define PA_FP8_BLOCK_PARTITION 512
+#define PA_FP8_BLOCK_PARTITION 1024
 #endif
 #ifndef PA_FP8_BLOCK_ITEMS_PER_SM
 #define PA_FP8_BLOCK_ITEMS_PER_SM 8
+#endif
+#ifndef PA_FP8_BLOCK_TAIL_PCT
+#define PA_FP8_BLOCK_TAIL_PCT 10
+#endif
+#ifndef PA_FP8_BLOCK_TAIL_DIV
+#define PA_FP8_BLOCK_TAIL_DIV 4
 #endif
 DecodePlan plan_decode_fp8_block(int num_seqs, int num_kv_heads, int max_context_len, int num_sms) {
     auto splits = [&](long long part) { return max_context_len <= part ? 1LL : (max_context_len + part - 1) / part; };
@@ -25,7 +31,10 @@ DecodePlan plan_decode_fp8_block(int num_seqs, int num_kv_heads, int max_context
     while (part > 128 && splits(part) * num_seqs * num_kv_heads < (long long)PA_FP8_BLOCK_ITEMS_PER_SM * num_sms)
         part /= 2;
     while (splits(part) > 128) part *= 2;
-    return DecodePlan{(int)part, (int)splits(part), (int)part, num_seqs};
+    long long small = part / PA_FP8_BLOCK_TAIL_DIV < 128 ? 128 : part / PA_FP8_BLOCK_TAIL_DIV;
+    while (splits(small) > 128) small *= 2;
+    const int tail = small < part ? (int)((long long)num_seqs * PA_FP8_BLOCK_TAIL_PCT / 100) : 0;
+    return DecodePlan{(int)part, (int)splits(tail ? small : part), (int)small, num_seqs - tail};
 }
 
 // Row shape of the write and the read back: 16-byte pieces of codes, blocks of at most 1024 slots.
@@ -144,13 +153,15 @@ int pa_decode_fp8_block(void* out, const void* q, int num_seqs, int num_q_heads,
     p.max_blocks_per_seq = max_blocks_per_seq;
     p.max_context_len = max_context_len;
     p.partition = plan.partition;
+    p.small_partition = plan.small_partition;
+    p.small_from = plan.small_from;
     p.max_splits = plan.max_splits;
     p.scale_log2 = scale * 1.4426950408889634f;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     rc = decode_fp8_block_tc_supported(p) ? launch_decode_fp8_block_tc(p, num_sms, st)
                                           : launch_decode_fp8_block_fma(p, st);
     if (rc != PA_OK) return rc;
-    return launch_decode_merge(p, PA_BF16, num_sms, st);
+    return launch_decode_fp8_block_join(p, st);
 }
 
 size_t pa_prefill_fp8_block_workspace_size(int num_chunks, int total_q, int max_q_len, int num_q_heads,

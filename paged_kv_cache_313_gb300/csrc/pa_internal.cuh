@@ -192,6 +192,7 @@ int launch_read_fp8_block(void* k_out, void* v_out, int num_tokens, int num_kv_h
                           cudaStream_t stream);
 bool decode_fp8_block_tc_supported(const DecodeParams& p);
 int launch_decode_fp8_block_tc(const DecodeParams& p, int num_sms, cudaStream_t stream);
+int launch_decode_fp8_block_join(const DecodeParams& p, cudaStream_t stream);
 int launch_decode_fp8_block_fma(const DecodeParams& p, cudaStream_t stream);
 // Workspace of the block-scaled prefill: the partial rows of query tiles whose keys are cut into spans.
 size_t prefill_fp8_block_workspace(int num_chunks, int total_q, int max_q_len, int num_q_heads, int num_kv_heads,

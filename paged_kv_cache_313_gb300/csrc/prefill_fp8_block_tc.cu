@@ -459,47 +459,48 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         const int w = warp - kConvWarp;
         uint32_t g = 0, items = 0;
-        // rows 32 w + from .. of an item's query tile: two e4m3 terms, and the factor that undoes their scaling
-        auto split_rows = [&](const Item& d, uint32_t item, int from, int to) {
-            uint8_t* tile = smem + kQ;
-            for (int i = from; i < to; i += 8) {
-                uint2 x[8];  // eight rows' loads go out together
+        // an item's query rows, one a lane: two e4m3 terms staged in shared memory, and the factor that undoes their
+        // scaling.  In f16, which holds a scaled bf16 exactly down to 2^-24.
+        auto stage_q = [&](const Item& d, uint32_t item) {
+            const int r = w * 32 + lane, pos = r * inv_g >> 16;
+            const uint4* src = reinterpret_cast<const uint4*>(
+                static_cast<const __nv_bfloat16*>(p.q) +
+                ((size_t)(d.row + pos) * p.num_q_heads + d.kvh * G + (r - pos * G)) * kD);
+            uint4 x[kD / 8];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const int r = w * 32 + i + u, pos = r * inv_g >> 16;
-                    x[u] = make_uint2(0u, 0u);
-                    if (pos < d.nq)
-                        x[u] = __ldg(reinterpret_cast<const uint2*>(
-                                         static_cast<const __nv_bfloat16*>(p.q) +
-                                         ((size_t)(d.row + pos) * p.num_q_heads + d.kvh * G + (r - pos * G)) * kD) +
-                                     lane);
-                }
+            for (int k = 0; k < kD / 8; ++k) x[k] = pos < d.nq ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+            uint32_t m2 = 0;
 #pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    const int r = w * 32 + i + u;
-                    const uint32_t m2 = __vmaxu2(x[u].x & 0x7FFF7FFFu, x[u].y & 0x7FFF7FFFu);
-                    const uint32_t am = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
-                    const int e = min(134 - (int)(am >> 7), 126);  // |x| 2^e in [128, 256)
-                    // a negative softmax scale negates the queries, so that scores only meet positive factors
-                    const float f = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), p.scale_log2);
-                    const float v[4] = {__uint_as_float(x[u].x << 16) * f, __uint_as_float(x[u].x & 0xFFFF0000u) * f,
-                                        __uint_as_float(x[u].y << 16) * f, __uint_as_float(x[u].y & 0xFFFF0000u) * f};
-                    uint32_t hi = 0, lo = 0;
+            for (int k = 0; k < kD / 8; ++k)
+                m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(x[k].x & 0x7FFF7FFFu, x[k].y & 0x7FFF7FFFu),
+                                           __vmaxu2(x[k].z & 0x7FFF7FFFu, x[k].w & 0x7FFF7FFFu)));
+            const int e = min(134 - (int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7), 126);  // |x| 2^e in [128, 256)
+            // a negative softmax scale negates the queries, so that scores only meet positive factors
+            const float f = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), p.scale_log2);
+            uint8_t* row = smem + kQ + r * kD;
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        const uint16_t c = pack_e4m3x2(v[2 * q], v[2 * q + 1]);
-                        const float2 b = e4m3x2_to_float2(c);
-                        hi |= (uint32_t)c << (16 * q);
-                        lo |= (uint32_t)pack_e4m3x2(v[2 * q] - b.x, v[2 * q + 1] - b.y) << (16 * q);
+            for (int k = 0; k < kD / 16; ++k) {
+                const uint32_t in[8] = {x[2 * k].x,     x[2 * k].y,     x[2 * k].z,     x[2 * k].w,
+                                        x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t c[2], b[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const uint32_t v = in[2 * i + j];
+                        const uint32_t h = pack_f16x2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
+                        c[j] = e4m3x2_of_f16x2(h);
+                        b[j] = e4m3x2_of_f16x2(sub_f16x2(h, e4m3x2_to_f16x2(c[j])));
                     }
-                    const int at = r * kD + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
-                    *reinterpret_cast<uint32_t*>(tile + at) = hi;
-                    *reinterpret_cast<uint32_t*>(tile + kCodes + at) = lo;
-                    if (lane == 0)
-                        reinterpret_cast<float*>(smem + kQf)[item % kQSlots * kTile + r] =
-                            __uint_as_float((uint32_t)(127 - e) << 23);
+                    hi[i] = c[0] | (c[1] << 16);
+                    lo[i] = b[0] | (b[1] << 16);
                 }
+                const int at = (k ^ (r & 7)) << 4;
+                *reinterpret_cast<uint4*>(row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(row + kCodes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }
+            reinterpret_cast<float*>(smem + kQf)[item % kQSlots * kTile + r] = __uint_as_float((uint32_t)(127 - e) << 23);
         };
         // the staged rows into tensor memory (a lane's row is its tensor-memory lane), once the item before is through
         // its last S
@@ -538,13 +539,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         Item d, nx;
         bool have = next_item(d);
         if (have) {
-            split_rows(d, 0, 0, 32);
+            stage_q(d, 0);
             finish_q(0);
         }
         while (have && ok) {
             const bool have_next = next_item(nx);
             if (!ok) break;
-            int rows = 0;  // rows of the next item's tile that are split (of this warp's 32)
             for (int j = 0; j < d.nt; ++j, ++g) {
                 const uint32_t vs = g % kVStages, vh = g % kVhStages;
                 const uint32_t last = 2 * (g - kVhStages) + 1;  // the piece that read this buffer last
@@ -585,17 +585,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     mbar_arrive(bars.vh_full(vh));
                     mbar_arrive(bars.v_empty(vs));
                 }
-                // between tiles, a quarter of the next item's query rows
-                if (have_next && rows < 32) {
-                    split_rows(nx, items + 1, rows, rows + 8);
-                    rows += 8;
-                }
+                if (j == 0 && have_next) stage_q(nx, items + 1);  // early, while the softmax is at this item's first keys
             }
             if (!ok) break;
-            if (have_next) {
-                split_rows(nx, items + 1, rows, 32);
-                finish_q(items + 1);
-            }
+            if (have_next) finish_q(items + 1);
             ++items;
             have = have_next;
             d = nx;
@@ -614,6 +607,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             if (ok && !mbar_wait_warp(bar, parity)) ok = false;
         };
+        const bool out_al32 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
         const int my_pos = r * inv_g >> 16;  // the row's position in a tile, and its head of the group
         Item d;
         for (uint32_t n = 0; take_item(n, d); ++n) {
@@ -756,35 +750,37 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t t_oth = tmem + lanes + kTO + (x ^ 1) * 128;
             if (!direct && row_ok && x == 0) spans.ml[part] = make_float2(M, L);
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
-                const int col = x * 64 + q * 16;
-                float o[16];
+            for (int col = x * 64; col < x * 64 + 64; col += 32) {
+                float o[32];
                 if (d.nt > 0) {
-                    float a[16], b[16];
-                    tmem_ld16(t_o + col, a);
-                    tmem_ld16(t_oth + col, b);
+                    float b[32];
+                    tmem_ld32(t_o + col, o);
+                    tmem_ld32(t_oth + col, b);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = (use_own ? a[i] * f_own : 0.f) + (use_oth ? b[i] * f_oth : 0.f);
+                    for (int i = 0; i < 32; ++i) o[i] = (use_own ? o[i] * f_own : 0.f) + (use_oth ? b[i] * f_oth : 0.f);
                 } else {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = 0.f;
+                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
                 }
                 if (!row_ok) continue;
                 if (direct) {
-                    uint32_t w[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(o[2 * i], o[2 * i + 1]);
                     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + row * kD + col;
-                    if ((reinterpret_cast<uintptr_t>(p.out) & 31u) == 0) {
-                        store32(out, w);
-                    } else {
-                        reinterpret_cast<uint4*>(out)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-                        reinterpret_cast<uint4*>(out)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(o[16 * k + 2 * i], o[16 * k + 2 * i + 1]);
+                        if (out_al32) {
+                            store32(out + 16 * k, w);
+                        } else {
+                            reinterpret_cast<uint4*>(out + 16 * k)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+                            reinterpret_cast<uint4*>(out + 16 * k)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
                     }
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
+                    for (int k = 0; k < 4; ++k) {
                         uint32_t w[8];
 #pragma unroll
                         for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(o[8 * k + i]);
@@ -810,44 +806,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
 }
 
-// Joins the spans of a tile's rows: a warp per (row, query head), a float4 of columns per lane, in span order.
+// Joins the spans of a tile's rows: a warp per (row, query head), a float4 of columns per lane, in span order.  The
+// first kAhead spans' rows are asked for before it is known how many there are (their addresses hold for every row),
+// and the row's chunk is found by all lanes at once, so that two loads follow one another instead of six.
 __global__ void __launch_bounds__(128) prefill_fp8_block_join_kernel(const PrefillParams p, const Spans spans) {
+    constexpr int kAhead = 8;
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, G = p.group, ppt = kTile / G;
     const long long rows = (long long)p.total_q * p.num_q_heads, stride = (long long)gridDim.x * 4;
     for (long long u = (long long)blockIdx.x * 4 + (threadIdx.x >> 5); u < rows; u += stride) {
         const int q = (int)(u / p.num_q_heads);
+        float4 o[kAhead];
+        float2 ml[kAhead];
+        auto load = [&](int i0) {
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (i0 + k < spans.count) {
+                    ml[k] = __ldcg(spans.ml + (size_t)(i0 + k) * rows + u);
+                    o[k] = __ldcg(reinterpret_cast<const float4*>(spans.o + ((size_t)(i0 + k) * rows + u) * kD) + lane);
+                }
+        };
+        load(0);
         // the chunk of row q: the largest c with cu_q_lens[c] <= q
-        int lo = 0, hi = p.num_chunks - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (p.cu_q_lens[mid] <= q) lo = mid; else hi = mid - 1;
+        int c = -1;
+        for (int c0 = 0; c0 < p.num_chunks; c0 += 32) {
+            const uint32_t le = __ballot_sync(0xffffffffu, c0 + lane < p.num_chunks && p.cu_q_lens[c0 + lane] <= q);
+            if (le != 0) c = c0 + 31 - __clz(le);
         }
         int r0, n, s, start;
-        if (!chunk_of(p, lo, r0, n, s, start) || q < r0 || q >= r0 + n) continue;
+        if (c < 0 || !chunk_of(p, c, r0, n, s, start) || q >= r0 + n) continue;
         const int tile_end = min((q - r0) / ppt * ppt + ppt, n);  // as the kernel above cuts the chunk
         const int last = min((int)min((long long)start + tile_end - 1, 0x7FFFFFFELL), key_cap(p, s) - 1);
         const int all = last >= 0 ? last / kTile + 1 : 0, count = max(1, (all + spans.tiles - 1) / spans.tiles);
         if (count == 1) continue;  // stored directly
-        float m = -INFINITY;
-        for (int i = lane; i < count; i += 32) {
-            const float2 v = __ldcg(spans.ml + (size_t)i * rows + u);
-            if (v.y != 0.f) m = fmaxf(m, v.x);
-        }
-        m = warp_max(m);
-        float wsum = 0.f;
+        float m = -INFINITY, wsum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int i = 0; i < count; ++i) {
-            const float2 v = __ldcg(spans.ml + (size_t)i * rows + u);
-            const float4 o = __ldcg(reinterpret_cast<const float4*>(spans.o + ((size_t)i * rows + u) * kD) + lane);
-            const float w = v.y != 0.f ? v.y * exp2f(v.x - m) : 0.f;
-            wsum += w;
-            acc.x = fmaf(w, o.x, acc.x);
-            acc.y = fmaf(w, o.y, acc.y);
-            acc.z = fmaf(w, o.z, acc.z);
-            acc.w = fmaf(w, o.w, acc.w);
+        for (int i0 = 0; i0 < count; i0 += kAhead) {
+            if (i0 > 0) load(i0);
+            float mx = m;
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k)
+                if (i0 + k < count && ml[k].y != 0.f) mx = fmaxf(mx, ml[k].x);
+            const float f = m == mx ? 1.f : exp2f(m - mx);
+            m = mx;
+            wsum *= f;
+            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                if (i0 + k >= count || ml[k].y == 0.f) continue;
+                const float w = ml[k].y * exp2f(ml[k].x - m);
+                wsum += w;
+                acc.x = fmaf(w, o[k].x, acc.x);
+                acc.y = fmaf(w, o[k].y, acc.y);
+                acc.z = fmaf(w, o[k].z, acc.z);
+                acc.w = fmaf(w, o[k].w, acc.w);
+            }
         }
         const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
         *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + u * kD + lane * 4) =
@@ -861,14 +875,17 @@ long long work_items(int num_chunks, int max_q_len, int num_kv_heads, int group)
     return (long long)((max_q_len + ppt - 1) / ppt) * num_chunks * num_kv_heads;
 }
 
-// Key tiles per span and spans per query tile: the keys are cut when the tiles alone would not give every SM two
-// items, into spans of at least four key tiles (a span's partial rows cost about half a key tile's time to store and
-// join).  The count comes from the largest context, the lengths live on the device.
+// Key tiles per span and spans per query tile.  Where the tiles alone leave SMs idle their keys are cut so that the
+// items make up one round of the GPU, into spans of at least two key tiles (a span's partial rows cost about one key
+// tile's time to store and join); where they make up less than two rounds and have 16 key tiles or more, in two, so
+// that the second round is shorter.  The count comes from the largest context, the lengths live on the device.
 Spans plan_spans(int num_chunks, int max_q_len, int num_kv_heads, int group, int max_context_len, int num_sms) {
     const int tiles = max_context_len > 0 ? (max_context_len - 1) / kTile + 1 : 1;
     const long long items = work_items(num_chunks, max_q_len, num_kv_heads, group);
-    long long want = items > 0 ? (2LL * num_sms) / items : 1;
-    if (want > tiles / 4) want = tiles / 4;
+    long long want = 1;
+    if (items > 0 && items < num_sms) want = num_sms / items;
+    else if (items < 2LL * num_sms && tiles >= 16) want = 2;
+    if (want > tiles / 2) want = tiles / 2;
     Spans s{};
     s.tiles = tiles;
     if (want > 1) s.tiles = (int)((tiles + want - 1) / want);

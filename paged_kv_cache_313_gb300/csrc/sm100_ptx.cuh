@@ -229,6 +229,18 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes16) {
     return d;
 }
 
+// Two f16 (low half first) to their nearest e4m3 codes, ties to even, held at 448; low byte first.
+__device__ __forceinline__ uint16_t e4m3x2_of_f16x2(uint32_t h) {
+    uint16_t d;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(d) : "r"(h));
+    return d;
+}
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
 // Two floats to an f16x2 word (round to nearest even), lo in the low half.
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t r;
