@@ -74,7 +74,8 @@ constexpr int kV = kK + kKStages * kCodes;
 constexpr int kVh = kV + kVStages * kCodes;
 constexpr int kConsts = kVh + kVhStages * 2 * kHalfBytes;  // float4 [kInfo][16]: per 8 keys ks', log2(vs/R), R/vs
 constexpr int kMask = kConsts + kInfo * 16 * 16;           // uint32 [kInfo][4]
-constexpr int kR = kMask + kInfo * 16;                     // float [kInfo]
+constexpr int kVMask = kMask + kInfo * 16;                 // uint32 [kVStages][4]: the same for the converters
+constexpr int kR = kVMask + kVStages * 16;                 // float [kInfo]
 constexpr int kQf = kR + kInfo * 4;                        // float [kQSlots][128]
 constexpr int kState = kQf + kQSlots * kTile * 4;          // float4 [2 items][2 groups][128]: m, l, R
 constexpr int kItem = kState + 2 * 2 * kTile * 16;  // Item [kItems]
@@ -126,9 +127,11 @@ __device__ __forceinline__ void store32(void* ptr, const uint32_t (&v)[8]) {
 }
 
 // One piece's S (64 keys): two query terms in tensor memory (32 columns each from `a`), four steps of 32 dims, K
-// rows described by (lo, hi).  And one piece's P V: four steps of 16 keys.  Each is one election and its MMAs: the
-// issuing warp shares its scheduler with three busy ones, so its instructions are counted.
-__device__ __forceinline__ void issue_s(uint32_t d, uint32_t a, uint32_t lo, uint32_t hi, uint32_t idesc) {
+// rows described by (lo, hi); `bar`, and `bar2` if given, complete with it.  And one piece's P V: four steps of 16 keys.
+// Each is one election, its MMAs and commits: the issuing warp shares its scheduler with three busy ones, so its
+// instructions are counted.
+__device__ __forceinline__ void issue_s(uint32_t d, uint32_t a, uint32_t lo, uint32_t hi, uint32_t idesc, uint64_t* bar,
+                                        uint64_t* bar2) {
 #define PA_STEP(A, B, ACC)                                                                     \
     "add.u32 t, %1, " A ";\n\tadd.u32 l, %2, " B ";\n\tmov.b64 b, {l, %3};\n\t"               \
     "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [t], b, %4, " ACC ";\n\t"
@@ -137,11 +140,15 @@ __device__ __forceinline__ void issue_s(uint32_t d, uint32_t a, uint32_t lo, uin
         "setp.eq.u32 y, 0, 0;\n\tsetp.ne.u32 n, 0, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
         PA_STEP("0", "0", "n") PA_STEP("8", "2", "y") PA_STEP("16", "4", "y") PA_STEP("24", "6", "y")
         PA_STEP("32", "0", "y") PA_STEP("40", "2", "y") PA_STEP("48", "4", "y") PA_STEP("56", "6", "y")
-        "}" ::"r"(d), "r"(a), "r"(lo), "r"(hi), "r"(idesc) : "memory");
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%5];\n\t"
+        "setp.ne.u32 y, %6, 0;\n\tand.pred e, e, y;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t"
+        "}" ::"r"(d), "r"(a), "r"(lo), "r"(hi), "r"(idesc), "r"(smem_u32(bar)), "r"(bar2 ? smem_u32(bar2) : 0u)
+        : "memory");
 #undef PA_STEP
 }
 __device__ __forceinline__ void issue_o(uint32_t d, uint32_t a, uint32_t lo, uint32_t hi, uint32_t idesc,
-                                        uint32_t accumulate) {
+                                        uint32_t accumulate, uint64_t* bar) {
 #define PA_STEP(A, B, ACC)                                                                     \
     "add.u32 t, %1, " A ";\n\tadd.u32 l, %2, " B ";\n\tmov.b64 b, {l, %3};\n\t"               \
     "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [t], b, %4, " ACC ";\n\t"
@@ -149,7 +156,8 @@ __device__ __forceinline__ void issue_o(uint32_t d, uint32_t a, uint32_t lo, uin
         "{\n\t.reg .pred e, y, f;\n\t.reg .b32 t, l;\n\t.reg .b64 b;\n\t"
         "setp.eq.u32 y, 0, 0;\n\tsetp.ne.u32 f, %5, 0;\n\telect.sync _|e, 0xffffffff;\n\t"
         PA_STEP("0", "0", "f") PA_STEP("8", "128", "y") PA_STEP("16", "256", "y") PA_STEP("24", "384", "y")
-        "}" ::"r"(d), "r"(a), "r"(lo), "r"(hi), "r"(idesc), "r"(accumulate) : "memory");
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%6];\n\t"
+        "}" ::"r"(d), "r"(a), "r"(lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(smem_u32(bar)) : "memory");
 #undef PA_STEP
 }
 
@@ -235,8 +243,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         return d.nt >= 0;
     };
 
-    // Registers: 128 a thread at launch (512 threads take all of the SM's).  The softmax warps get 160 of them, for 64
-    // scores and what becomes of them, the converters keep 104, the others 88: 2 * 160 + 104 + 88 = 4 * 128.
+    // Registers: 128 a thread at launch (512 threads take all of the SM's).  The softmax warps get 152 of them, for 64
+    // scores and what becomes of them, the converters keep 120, the others 88: 2 * 152 + 120 + 88 = 4 * 128.
     if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kKWarp || warp == kVWarp) {
         // ============================================================ producers
@@ -350,6 +358,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
+                const int slot = g % kInfo;
+                if (lane < 4) {  // key-validity mask: 32 keys a word
+                    const int left = d.last_key + 1 - (d.t0 + j) * kTile - 32 * lane;
+                    uint32_t m = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
+                    if (B >= 32) {
+                        if (!((mine >> ((32 * lane) >> log2b)) & 1u)) m = 0u;
+                    } else {
+                        const int per = 32 >> log2b;
+                        for (int b = 0; b < per; ++b)
+                            if (!((mine >> (lane * per + b)) & 1u)) m &= ~(((1u << B) - 1u) << (b * B));
+                    }
+                    if (v_side) reinterpret_cast<uint32_t*>(smem + kVMask)[st * 4 + lane] = m;
+                    else mask[slot * 4 + lane] = m;
+                }
+                __syncwarp();
                 if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)__popc(mine) * B * kD);
                 __syncwarp();  // armed before any copy is issued
                 const int src = l * bpt + (lane < bpt ? lane : 0);
@@ -366,23 +389,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int blk = ((lane & 15) * 8) >> log2b;  // block of this lane's group
                     const float ks = __shfl_sync(0xffffffffu, sc.x, l * bpt + blk);
                     const float vs = __shfl_sync(0xffffffffu, sc.y, l * bpt + blk);
-                    const int slot = g % kInfo;
                     if (lane < 16) {
                         const float off = __log2f(fmaxf(vs / R, 9.094947017729282e-13f));  // at least 2^-40
                         reinterpret_cast<float4*>(smem + kConsts)[slot * 16 + lane] =
                             make_float4(ks * fabsf(p.scale_log2), off, fast_exp2(-off), 0.f);
-                    }
-                    if (lane < 4) {  // key-validity mask: 32 keys a word
-                        const int left = d.last_key + 1 - (d.t0 + j) * kTile - 32 * lane;
-                        uint32_t m = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
-                        if (B >= 32) {
-                            if (!((mine >> ((32 * lane) >> log2b)) & 1u)) m = 0u;
-                        } else {
-                            const int per = 32 >> log2b;
-                            for (int b = 0; b < per; ++b)
-                                if (!((mine >> (lane * per + b)) & 1u)) m &= ~(((1u << B) - 1u) << (b * B));
-                        }
-                        mask[slot * 4 + lane] = m;
                     }
                     if (lane == 0) reinterpret_cast<float*>(smem + kR)[slot] = R;
                     __syncwarp();
@@ -433,17 +443,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (round > 0 && !wait(bars.pv_done(sb), (round - 1) & 1)) break;
                         tc_fence_after();
                         issue_s(tmem + kTS + sb * 64, tmem + kTQ,
-                                (uint32_t)dk0 + ((st * kCodes + x * 64 * kD) >> 4), (uint32_t)(dk0 >> 32), idesc_s);
-                        umma_commit_warp(bars.s_full(sb));
-                        if (x) umma_commit_warp(bars.k_empty(st));
+                                (uint32_t)dk0 + ((st * kCodes + x * 64 * kD) >> 4), (uint32_t)(dk0 >> 32), idesc_s,
+                                bars.s_full(sb), x ? bars.k_empty(st) : nullptr);
                         if (x && j == nt - 1) umma_commit_warp(bars.q_empty());
                     } else {
                         if (!wait(bars.p_full(sb), round & 1)) break;
                         tc_fence_after();
                         issue_o(tmem + kTO + x * 128, tmem + kTS + sb * 64,
                                 (uint32_t)dv0 + ((vh * 2 * kHalfBytes + x * 64 * 128) >> 4), (uint32_t)(dv0 >> 32),
-                                idesc_o, j);
-                        umma_commit_warp(bars.pv_done(sb));  // frees the piece, and the widened V with its second
+                                idesc_o, j, bars.pv_done(sb));  // which frees the piece, and with its second the widened V
                     }
                     if (++sb == kPieces) sb = 0, ++round;
                 }
@@ -456,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= kConvWarp && warp < kMmaWarp) {
         // ============================================================ converters
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
         const int w = warp - kConvWarp;
         uint32_t g = 0, items = 0;
         // an item's query rows, one a lane: two e4m3 terms staged in shared memory, and the factor that undoes their
@@ -548,28 +556,36 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < d.nt; ++j, ++g) {
                 const uint32_t vs = g % kVStages, vh = g % kVhStages;
                 const uint32_t last = 2 * (g - kVhStages) + 1;  // the piece that read this buffer last
-                if (!mbar_wait_warp(bars.info(g % kInfo), (g / kInfo) & 1) ||
-                    (g >= kVhStages && !mbar_wait_warp(bars.pv_done(last % kPieces), (last / kPieces) & 1)) ||
-                    !mbar_wait_warp(bars.v_full(vs), (g / kVStages) & 1)) {
-                    ok = false;
-                    break;
-                }
                 // a lane widens 16 codes of a key, 8 lanes a key; a warp takes keys 16 i + 4 w .. + 3, whose swizzle is
-                // the same for every i
+                // the same for every i.  The codes are loaded while the buffer is still being read.
                 const uint32_t key0 = 4 * w + (lane >> 3), ch = lane & 7, sw = key0 & 7;
                 const uint8_t* src = smem + kV + vs * kCodes + key0 * kD + ((ch ^ sw) << 4);
                 uint8_t* dst = smem + kVh + vh * 2 * kHalfBytes + (ch >> 2) * kHalfBytes + key0 * 128;
                 uint8_t *dst0 = dst + ((((ch & 3) * 2) ^ sw) << 4), *dst1 = dst + ((((ch & 3) * 2 + 1) ^ sw) << 4);
-                const uint4 m = *reinterpret_cast<const uint4*>(mask + (g % kInfo) * 4);
-                const bool all_valid = (m.x & m.y & m.z & m.w) == ~0u;
+                if (!mbar_wait_warp(bars.v_full(vs), (g / kVStages) & 1)) {
+                    ok = false;
+                    break;
+                }
+                uint4 x[kTile / 16];
+#pragma unroll
+                for (int i = 0; i < kTile / 16; ++i) x[i] = *reinterpret_cast<const uint4*>(src + i * 16 * kD);
+                const uint4 m = *reinterpret_cast<const uint4*>(smem + kVMask + vs * 16);
+                if ((m.x & m.y & m.z & m.w) != ~0u) {
+#pragma unroll
+                    for (int i = 0; i < kTile / 16; ++i) {
+                        const uint32_t word = i < 2 ? m.x : i < 4 ? m.y : i < 6 ? m.z : m.w;
+                        if (!((word >> ((i & 1) * 16 + key0)) & 1u)) x[i] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bars.v_empty(vs));
+                if (g >= kVhStages && !mbar_wait_warp(bars.pv_done(last % kPieces), (last / kPieces) & 1)) {
+                    ok = false;
+                    break;
+                }
 #pragma unroll
                 for (int i = 0; i < kTile / 16; ++i) {
-                    uint4 x = *reinterpret_cast<const uint4*>(src + i * 16 * kD);
-                    if (!all_valid) {
-                        const uint32_t word = i < 2 ? m.x : i < 4 ? m.y : i < 6 ? m.z : m.w;
-                        if (!((word >> ((i & 1) * 16 + key0)) & 1u)) x = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                    const uint32_t in[4] = {x.x, x.y, x.z, x.w};
+                    const uint32_t in[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
                     uint32_t out[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -581,10 +597,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(bars.vh_full(vh));
-                    mbar_arrive(bars.v_empty(vs));
-                }
+                if (lane == 0) mbar_arrive(bars.vh_full(vh));
                 if (j == 0 && have_next) stage_q(nx, items + 1);  // early, while the softmax is at this item's first keys
             }
             if (!ok) break;
@@ -596,7 +609,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok && lane == 0) count_error(p.error_count);
     } else if (warp < kConvWarp) {
         // ============================================================ softmax and output
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
         const int x = warp >> 2;                       // group
         const int r = (warp & 3) * 32 + lane;          // row = tensor-memory lane
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -625,9 +638,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const float4* kc = reinterpret_cast<const float4*>(smem + kConsts) + slot * 16 + x * 8;
                 const float R = reinterpret_cast<const float*>(smem + kR)[slot];
                 const uint2 vm = *reinterpret_cast<const uint2*>(mask + slot * 4 + x * 2);
-                wait(bars.s_full(sb), (piece / kPieces) & 1);
-                if (!ok) break;
-                tc_fence_after();
+                // (all of this before the wait for S, which it does not need)
                 const int key0 = (d.t0 + j) * kTile + x * 64;
                 // the row's visible and valid keys as 64 bits; dense: all of them, for every row of the warp
                 const int vis = my_last - key0 + 1;
@@ -640,8 +651,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // (which is how a larger score shows, without a pass for the maximum), when R has changed or at the
                 // item's first piece, the maximum is looked for, O brought to it, and the weights taken again.
                 bool look = first || R != Rc || __any_sync(0xffffffffu, m == -INFINITY);
+                float4 k4[64 / kKeys];
+#pragma unroll
+                for (int b = 0; b < 64 / kKeys; ++b) {
+                    k4[b] = kc[b * kKeys / 8];
+                    k4[b].x = fmaxf(k4[b].x * qf, kTiny);
+                }
                 uint32_t pk[32];
                 float sum;
+                wait(bars.s_full(sb), (piece / kPieces) & 1);
+                if (!ok) break;
+                tc_fence_after();
                 while (true) {
                     float s[64];
                     {
@@ -664,7 +684,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float u[2] = {s[b], s[b + 1]};
 #pragma unroll
                             for (int i = 2; i < kKeys; i += 2) u[i / 2 & 1] = fmax3(u[i / 2 & 1], s[b + i], s[b + i + 1]);
-                            mt = fmaxf(mt, fmaxf(u[0], u[1]) * fmaxf(kc[b / 8].x * qf, kTiny));
+                            mt = fmaxf(mt, fmaxf(u[0], u[1]) * k4[b / kKeys].x);
                         }
                         if (!first) {
                             // the products issued so far have to be done before O changes
@@ -690,8 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float m_fin = m == -INFINITY ? 0.f : m;  // no key yet: every P' is 2^-inf
 #pragma unroll
                     for (int b = 0; b < 64; b += kKeys) {
-                        const float4 k4 = kc[b / 8];
-                        const float a = fmaxf(k4.x * qf, kTiny), o = k4.y - m_fin;
+                        const float a = k4[b / kKeys].x, o = k4[b / kKeys].y - m_fin;
                         const unsigned long long a2 = f32x2_pack(a, a), o2 = f32x2_pack(o, o);
                         unsigned long long part[2];  // the keys' weights, in pairs and two chains
 #pragma unroll
@@ -704,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         float u, v;
                         f32x2_unpack(add_f32x2(part[0], part[1]), u, v);
-                        sum = fmaf(u + v, k4.z, sum);
+                        sum = fmaf(u + v, k4[b / kKeys].z, sum);
                     }
                     // (at most 2^9, times the 64 that vs / R may reach, is below f16's largest number)
                     if (look || !__any_sync(0xffffffffu, sum > kMost)) break;
