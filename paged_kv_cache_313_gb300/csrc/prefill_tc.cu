@@ -487,28 +487,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                                     fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
                 if (dense) mpart *= sl2;
                 const float mt = mpart;
-                if (mt > m_run + kRescaleThreshold) {  // also true for the first finite max
-                    if (m_run != -INFINITY) {
-                        const float alpha = fast_exp2(m_run - mt);
-                        l_run *= alpha;
-                        if (j > 0) {
-                            // every PV issued so far (the last is PV_{j-1}) must be done before O changes
-                            if (ok && !mbar_wait(bars.o_done((g - 1) & 1), ((g - 1) >> 1) & 1)) ok = false;
-                            tc_fence_after();
+                const bool grow = mt > m_run + kRescaleThreshold;  // also true for the first finite max
+                // rescale when any row of the warp must: the tensor-memory accesses are the whole warp's together,
+                // and a row that need not is multiplied by 1 (rows entering them one by one would wait for ever)
+                const bool rescale = grow && m_run != -INFINITY;
+                if (__any_sync(0xffffffffu, rescale)) {
+                    const float alpha = rescale ? fast_exp2(m_run - mt) : 1.f;
+                    l_run *= alpha;
+                    if (j > 0) {
+                        // every PV issued so far (the last is PV_{j-1}) must be done before O changes
+                        if (ok && !mbar_wait(bars.o_done((g - 1) & 1), ((g - 1) >> 1) & 1)) ok = false;
+                        __syncwarp();
+                        tc_fence_after();
 #pragma unroll 1
-                            for (int q2 = 0; q2 < 8; ++q2) {  // all 128 columns of this half's O row
-                                float t[16];
-                                tmem_ld16(t_own + q2 * 16, t);
-                                tmem_wait_ld();
+                        for (int q2 = 0; q2 < 8; ++q2) {  // all 128 columns of this half's O row
+                            float t[16];
+                            tmem_ld16(t_own + q2 * 16, t);
+                            tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) t[i] *= alpha;
-                                tmem_st16(t_own + q2 * 16, t);
-                            }
-                            tmem_wait_st();
+                            for (int i = 0; i < 16; ++i) t[i] *= alpha;
+                            tmem_st16(t_own + q2 * 16, t);
                         }
+                        tmem_wait_st();
                     }
-                    m_run = mt;
                 }
+                if (grow) m_run = mt;
                 // P = 2^(x - m) in bf16, my 64 keys of row r packed in pairs into 32 columns of S buffer j%2
                 // (its first 32 columns for keys 0-63, columns 64-95 for keys 64-127: each thread
                 // overwrites only S values it has already read)
