@@ -65,11 +65,19 @@ class DeviceStep:
         self.error_count = torch.zeros(1, dtype=torch.int32, device=dev) if with_error_count else None
         self.max_context_len = w.max_decode_context
         nd = w.num_decode
-        self.workspace = (pa.new_decode_workspace(nd, w.num_q_heads, w.num_kv_heads, w.head_dim, w.block_size,
-                                                  self.max_context_len, device=dev) if nd else None)
+        # e4m3 pools with a scale for each block and kv head: their own write, decode and prefill
+        self.block_scales = w.k_scales is not None
+        if self.block_scales:
+            self.k_scales, self.v_scales = up(w.k_scales), up(w.v_scales)
+            self.write_workspace = pa.new_write_fp8_block_workspace(w.seq_idx.numel(), w.num_blocks, w.block_size,
+                                                                    device=dev)
+        new_decode_workspace = pa.new_decode_fp8_block_workspace if self.block_scales else pa.new_decode_workspace
+        self.workspace = (new_decode_workspace(nd, w.num_q_heads, w.num_kv_heads, w.head_dim, w.block_size,
+                                               self.max_context_len, device=dev) if nd else None)
         # cascade decode when decode sequences share prefixes (and the shapes allow it)
-        if w.kv_fp8 and w.num_chunks:
-            raise ValueError("e4m3 pools are read by decode only; prefill chunks need bf16 or fp32 pools")
+        if w.kv_fp8 and w.num_chunks and not self.block_scales:
+            raise ValueError("e4m3 pools of one scale are read by decode only; prefill chunks need bf16 or fp32 pools, "
+                             "or e4m3 pools with a scale per block and head")
         self.use_cascade = bool(cascade and nd and not w.kv_fp8 and int(w.prefix_lens.max()) > 0
                                 and w.dtype == torch.bfloat16
                                 and w.head_dim == 128 and w.num_q_heads // w.num_kv_heads in (1, 2, 4, 8)
@@ -84,8 +92,14 @@ class DeviceStep:
             torch.equal(w.pos[:nd], w.context_lens[:nd].to(w.pos.dtype) - 1)
         dims = (128,) if w.kv_fp8 else (64, 128)  # e4m3 pools: the decode kernel takes head_dim 128
         self.fused_decode_write = bool(fused_decode_write and newest and not self.use_cascade
-                                       and w.dtype == torch.bfloat16 and w.head_dim in dims and G <= 8
+                                       and not self.block_scales and w.dtype == torch.bfloat16 and w.head_dim in dims and G <= 8
                                        and w.block_size in (8, 16, 32, 64))
+        if self.block_scales:
+            self.max_prefill_context = int(w.context_lens[nd:].max()) if w.num_chunks else 0
+            self.prefill_workspace = pa.new_prefill_fp8_block_workspace(
+                w.num_chunks, int(w.cu_q_lens[-1]), w.max_q_len, w.num_q_heads, w.num_kv_heads, w.head_dim,
+                w.block_size, self.max_prefill_context, device=dev) if w.num_chunks else None
+            return
         n = pa.pa_prefill_workspace_size(w.num_chunks, w.max_q_len, w.num_q_heads, w.num_kv_heads, w.head_dim,
                                          w.block_size) if w.num_chunks else 0
         self.prefill_workspace = torch.zeros(max(n, 1), dtype=torch.uint8, device=dev) if n else None
@@ -101,7 +115,13 @@ class DeviceStep:
                        error_count=self.error_count, stream=stream)
 
     def write_kv_paged(self, stream=None):
-        """Slot mapping and K/V write in one launch (the slots are still recorded)."""
+        """Slot mapping and K/V write in one call (the slots are still recorded)."""
+        if self.block_scales:
+            pa.pa_write_kv_paged_fp8_block(self.k_new, self.v_new, self.k_cache, self.v_cache, self.k_scales,
+                                           self.v_scales, self.block_tables, self.seq_idx, self.pos,
+                                           self.write_workspace, slot_mapping=self.slots,
+                                           error_count=self.error_count, stream=stream)
+            return
         if self.w.kv_fp8:
             pa.pa_write_kv_paged_fp8(self.k_new, self.v_new, self.k_cache, self.v_cache, self.block_tables,
                                      self.seq_idx, self.pos, self.w.k_scale, self.w.v_scale, slot_mapping=self.slots,
@@ -115,6 +135,11 @@ class DeviceStep:
         if not w.num_decode:
             return self.out_decode
         nd = w.num_decode
+        if self.block_scales:
+            return pa.pa_decode_fp8_block(self.q_decode, self.k_cache, self.v_cache, self.k_scales, self.v_scales,
+                                          self.block_tables[:nd], self.context_lens[:nd], self.max_context_len,
+                                          w.scale, self.workspace, out=self.out_decode, error_count=self.error_count,
+                                          stream=stream)
         if w.kv_fp8:
             return pa.pa_decode_fp8(self.q_decode, self.k_cache, self.v_cache, self.block_tables[:nd],
                                     self.context_lens[:nd], self.max_context_len, w.scale, w.k_scale, w.v_scale,
@@ -133,6 +158,12 @@ class DeviceStep:
         w = self.w
         if not w.num_chunks:
             return self.out_prefill
+        if self.block_scales:
+            return pa.pa_prefill_chunk_fp8_block(self.q_prefill, self.cu_q_lens, self.q_start_pos, self.seq_of_chunk,
+                                                 w.max_q_len, self.k_cache, self.v_cache, self.k_scales,
+                                                 self.v_scales, self.block_tables, self.context_lens,
+                                                 self.max_prefill_context, w.scale, workspace=self.prefill_workspace,
+                                                 out=self.out_prefill, error_count=self.error_count, stream=stream)
         return pa.pa_prefill_chunk(self.q_prefill, self.cu_q_lens, self.q_start_pos, self.seq_of_chunk,
                                    w.max_q_len, self.k_cache, self.v_cache, self.block_tables, self.context_lens,
                                    w.scale, workspace=self.prefill_workspace, out=self.out_prefill,

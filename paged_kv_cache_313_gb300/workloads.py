@@ -66,6 +66,9 @@ class Workload:
     kv_fp8: bool = False
     k_scale: float = 1.0
     v_scale: float = 1.0
+    # with kv_fp8, instead of one scale per pool: float32 [P, Hkv], one for each block and kv head (as_fp8_block)
+    k_scales: torch.Tensor | None = None
+    v_scales: torch.Tensor | None = None
 
     @property
     def num_seqs(self) -> int:
@@ -221,6 +224,20 @@ def as_fp8(w: Workload, seed: int, k_scale: float = 1.0 / 64, v_scale: float = 1
                                      (rng.integers(0, 2, size=shape, dtype=np.uint8) << 7))
     w.k_cache, w.v_cache = codes(), codes()
     w.kv_fp8, w.k_scale, w.v_scale = True, float(k_scale), float(v_scale)
+    return w
+
+
+def as_fp8_block(w: Workload, seed: int, lo: int = 0x30, hi: int = 0x60) -> Workload:
+    """The same batch (decode sequences and prefill chunks) over e4m3 pools with a scale for each block and kv head:
+    codes as in ``as_fp8``, scales powers of two from 2^-8 to 2^-4 that differ by block and head.  Queries and the new
+    tokens' K/V stay bf16."""
+    w = as_fp8(w, seed, lo=lo, hi=hi)
+    rng = np.random.default_rng(seed + 6000)
+    scales = lambda: torch.from_numpy(np.exp2(rng.integers(-8, -3, size=(w.num_blocks, w.num_kv_heads))  # noqa: E731
+                                              .astype(np.float32)))
+    w.k_scale = w.v_scale = 1.0
+    w.k_scales, w.v_scales = scales(), scales()
+    w.name = w.name.replace("_bf16", "") + "_fp8_block"
     return w
 
 

@@ -17,6 +17,8 @@ import torch
 import fp8_block_reference as R
 from paged_kv_cache_313_gb300 import build as pa_build
 from paged_kv_cache_313_gb300 import pa
+from paged_kv_cache_313_gb300 import workloads as W
+from paged_kv_cache_313_gb300.runner import DeviceStep
 
 BF = torch.bfloat16
 
@@ -496,3 +498,178 @@ def test_write_then_prefill_then_decode_then_read():
         x = new.double().numpy()
         small = 2.0 ** -9 * s.cpu().double().numpy()[table[0, np.arange(n + 5) // B]][:, :, None]
         assert np.all(np.abs(got - x) <= 2.0 ** -4 * np.abs(x) + small)
+
+
+def _step_expected(w):
+    """(slots, K codes, V codes, K scales, V scales, decode, prefill with magnitudes and floors) of a step."""
+    table = w.block_tables.numpy()
+    slot, err = R.slots(table, w.seq_idx.numpy(), w.pos.numpy(), w.block_size, w.num_blocks)
+    assert err == 0
+    pools = []
+    for new, c, s in ((w.k_new, w.k_cache, w.k_scales), (w.v_new, w.v_cache, w.v_scales)):
+        c, s = c.numpy().copy(), s.double().numpy()
+        R.write(new.double().numpy(), c, s, slot)
+        pools.append((c, s))
+    (kc, ks), (vc, vs) = pools
+    ctx = w.context_lens.numpy()
+
+    def rows(q, s, limits):
+        out, mag = R.attend_rows(q.double().numpy(), kc, ks, vc, vs, table[s], limits, w.scale)
+        return out, mag, R.floor_rows(vc, vs, table[s], limits, w.num_q_heads)
+
+    dec = [rows(w.q_decode[s:s + 1], s, [int(ctx[s])]) for s in range(w.num_decode)]
+    pre = []
+    for c in range(w.num_chunks):
+        a, b, start = int(w.cu_q_lens[c]), int(w.cu_q_lens[c + 1]), int(w.q_start_pos[c])
+        pre.append(rows(w.q_prefill[a:b], int(w.seq_of_chunk[c]), [start + i + 1 for i in range(b - a)]))
+    cat = lambda parts: [np.concatenate(x) for x in zip(*parts)]  # noqa: E731
+    return slot, kc, vc, ks, vs, cat(dec) if dec else None, cat(pre) if pre else None
+
+
+def test_as_fp8_block_draws_scales_for_every_block_and_head():
+    w = W.as_fp8_block(W.small("mixed_bf16"), 0)
+    assert w.kv_fp8 and w.k_cache.dtype == torch.uint8 and tuple(w.k_scales.shape) == (w.num_blocks, w.num_kv_heads)
+    assert w.num_chunks > 0 and w.k_scales.dtype == torch.float32 and not torch.equal(w.k_scales, w.v_scales)
+    assert torch.equal(torch.exp2(torch.log2(w.v_scales).round()), w.v_scales)
+    again = W.as_fp8_block(W.small("mixed_bf16"), 0)
+    assert torch.equal(w.k_scales, again.k_scales) and torch.equal(w.v_cache, again.v_cache)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("how", ["eager", "graph", "host"])
+def test_device_step_over_block_scaled_pools(how):
+    """Write, decode and prefill as DeviceStep runs them: eagerly, as a captured graph replayed twice, and from pinned
+    host memory; a continuous-batching step of decode sequences and chunks."""
+    w = W.as_fp8_block(W.mixed_bf16(3, num_decode=5, num_chunks=2, chunk_len=40, max_off=200), 3)
+    w.context_lens[:5] = torch.clamp(w.context_lens[:5], max=300)
+    w.pos[:5] = w.context_lens[:5] - 1
+    slot, kc, vc, ks, vs, dec, pre = _step_expected(w)
+    st = DeviceStep(w)
+    assert st.block_scales and not st.fused_decode_write
+    if how == "eager":
+        st.run()
+    elif how == "graph":
+        first = [t.clone() for t in st.run()]
+        st.capture()
+        for _ in range(2):
+            st.out_decode.zero_()
+            st.out_prefill.zero_()
+            st.replay()
+            assert all(torch.equal(a, b) for a, b in zip(first, (st.out_decode, st.out_prefill)))
+    else:
+        hin, hout = st.pinned_inputs(), st.pinned_outputs()
+        st.run_from_host(hin, hout)
+        torch.cuda.synchronize()
+        st.capture_from_host(hin, hout)
+        hout.zero_()
+        st.run_from_host(hin, hout)
+        torch.cuda.synchronize()
+        st.out_decode, st.out_prefill = (t.cuda() for t in st.output_views(hout))
+    torch.cuda.synchronize()
+    assert st.errors() == 0
+    assert np.array_equal(st.slots.cpu().numpy(), slot)
+    assert np.array_equal(st.k_cache.cpu().numpy(), kc) and np.array_equal(st.v_cache.cpu().numpy(), vc)
+    assert np.array_equal(st.k_scales.double().cpu().numpy(), ks) and np.array_equal(st.v_scales.double().cpu().numpy(), vs)
+    _close(st.out_decode, *dec)
+    _close(st.out_prefill, *pre)
+
+
+@pytest.mark.gpu
+def test_calls_on_another_stream_and_without_workspace():
+    """A stream given by the caller; a workspace that is too small or absent is refused."""
+    rng = np.random.default_rng(12)
+    table, P = _tables(rng, [2000], 16)
+    codes, scales = zip(_pools(rng, P, 16, 1, 128), _pools(rng, P, 16, 1, 128))
+    pools = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (*codes, *scales)]
+    q, bt, ctx = _bf16(rng, (1, 4, 128)).cuda(), _i32(table), _i32([2000])
+    ws = pa.new_decode_fp8_block_workspace(1, 4, 1, 128, 16, 2000)
+    want = pa.pa_decode_fp8_block(q, *pools, bt, ctx, 2000, 0.1, ws)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = pa.pa_decode_fp8_block(q, *pools, bt, ctx, 2000, 0.1, ws, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    for bad in (None, ws[:256]):
+        with pytest.raises(pa.PaError, match="workspace"):
+            pa.pa_decode_fp8_block(q, *pools, bt, ctx, 2000, 0.1, bad)
+    cu, z = _i32([0, 1]), _i32([0])
+    pws = pa.new_prefill_fp8_block_workspace(1, 1, 1, 4, 1, 128, 16, 2000)
+    assert pws is not None  # one query, 16 key tiles: cut into spans
+    args = (q, cu, _i32([1999]), z, 1, *pools, bt, ctx, 2000, 0.1)
+    a = pa.pa_prefill_chunk_fp8_block(*args, workspace=pws)
+    assert float((a.float() - want.float()).abs().max()) <= 2.0 ** -6 * float(want.float().abs().max())
+    with pytest.raises(pa.PaError, match="workspace"):
+        pa.pa_prefill_chunk_fp8_block(*args)
+    new = torch.zeros(1500, 1, 128, dtype=BF, device="cuda")
+    with pytest.raises(pa.PaError, match="workspace"):
+        pa.pa_write_kv_paged_fp8_block(new, new, *pools, bt, _i32([0] * 1500), _i32(np.arange(1500)))
+
+
+@pytest.mark.gpu
+def test_empty_calls():
+    kc = torch.zeros(4, 16, 2, 128, dtype=torch.uint8, device="cuda")
+    sc, i0 = torch.zeros(4, 2, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")
+    bt = torch.zeros(1, 4, dtype=torch.int32, device="cuda")
+    none = torch.zeros(0, 2, 128, dtype=BF, device="cuda")
+    pa.pa_write_kv_paged_fp8_block(none, none, kc, kc.clone(), sc, sc.clone(), bt, i0, i0)
+    k, v = pa.pa_read_kv_paged_fp8_block(kc, kc, sc, sc, bt, i0, i0)
+    assert k.shape == (0, 2, 128) and v.dtype == BF
+    q = torch.zeros(0, 4, 128, dtype=BF, device="cuda")
+    ws = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    assert pa.pa_decode_fp8_block(q, kc, kc, sc, sc, bt[:0], i0, 16, 1.0, ws).numel() == 0
+    out = pa.pa_prefill_chunk_fp8_block(q, torch.zeros(1, dtype=torch.int32, device="cuda"), i0, i0, 0, kc, kc, sc, sc, bt,
+                                        torch.ones(1, dtype=torch.int32, device="cuda"), 16, 1.0)
+    assert out.numel() == 0
+    # all contexts empty: zeros, whatever the pools hold
+    q = torch.ones(3, 4, 128, dtype=BF, device="cuda")
+    nan = torch.full_like(kc, 0x7f)
+    out = pa.pa_decode_fp8_block(q, nan, nan, sc * float("nan"), sc, bt.expand(3, 4).contiguous(),
+                                 torch.zeros(3, dtype=torch.int32, device="cuda"), 0, 1.0, ws)
+    assert int(torch.count_nonzero(out)) == 0
+
+
+@pytest.mark.gpu
+def test_decode_of_more_sequences_than_one_launch_takes():
+    """1100 short sequences: the call cuts the batch into launches of 512."""
+    rng = np.random.default_rng(13)
+    lens = [int(x) for x in rng.integers(0, 40, 1100)]
+    assert _decode_case(lens, 4, 1, 128, 16, seed=14) == 0
+
+
+@pytest.mark.gpu
+def test_prefill_rows_outside_the_chunks_are_left():
+    """Chunk descriptors that make no sense are counted, and their rows keep what they held; so do rows of no chunk."""
+    rng = np.random.default_rng(15)
+    table, P = _tables(rng, [64, 64], 16)
+    codes, scales = zip(_pools(rng, P, 16, 1, 128), _pools(rng, P, 16, 1, 128))
+    pools = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (*codes, *scales)]
+    q = _bf16(rng, (30, 4, 128)).cuda()
+    out = torch.full_like(q, 5.0)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ws = pa.new_prefill_fp8_block_workspace(3, 30, 10, 4, 1, 128, 16, 64)
+    pa.pa_prefill_chunk_fp8_block(q, _i32([0, 10, 20, 25]), _i32([3, -1, 7]), _i32([0, 1, 2]), 10, *pools, _i32(table),
+                                  _i32([64, 64]), 64, 0.1, ws, out=out, error_count=err)
+    assert int(err.item()) >= 2  # chunk 1 starts before 0, chunk 2 names no sequence
+    assert torch.all(out[10:] == 5.0) and not torch.any(torch.all((out[:10] == 5.0).flatten(1), dim=1))
+
+
+@pytest.mark.gpu
+def test_read_back_then_bf16_prefill_agrees():
+    """The read back's rows, written into bf16 pools, give the existing prefill the values the e4m3 prefill sees."""
+    rng = np.random.default_rng(16)
+    n, T = 300, 50
+    table, P = _tables(rng, [n], 16)
+    codes, scales = zip(_pools(rng, P, 16, 2, 128), _pools(rng, P, 16, 2, 128))
+    pools = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (*codes, *scales)]
+    bt, seq, pos = _i32(table), _i32([0] * n), _i32(np.arange(n))
+    k, v = pa.pa_read_kv_paged_fp8_block(*pools, bt, seq, pos)
+    kb, vb = (torch.zeros(P, 16, 2, 128, dtype=BF, device="cuda") for _ in range(2))
+    pa.pa_write_kv_paged(k, v, kb, vb, bt, seq, pos)
+    q = _bf16(rng, (T, 8, 128)).cuda()
+    cu, st, so, ctx = _i32([0, T]), _i32([n - T]), _i32([0]), _i32([n])
+    want = pa.pa_prefill_chunk(q, cu, st, so, T, kb, vb, bt, ctx, 128 ** -0.5)
+    ws = pa.new_prefill_fp8_block_workspace(1, T, T, 8, 2, 128, 16, n)
+    got = pa.pa_prefill_chunk_fp8_block(q, cu, st, so, T, *pools, bt, ctx, n, 128 ** -0.5, ws)
+    # the bf16 prefill takes 2^x of bf16-rounded exponents: with x up to 2^4 from the maximum, off by 2^-5 relative
+    mag = float(v.float().abs().max())
+    assert float((got.float() - want.float()).abs().max()) <= 2.0 ** -4 * mag
