@@ -16,6 +16,12 @@
 
 namespace pa {
 
+// A context length as far as the grid and the block table can cover it.
+__device__ __forceinline__ int clamp_context(const DecodeParams& p, int L) {
+    const int cap = (int)min((long long)p.max_context_len, (long long)p.max_blocks_per_seq * p.block_size);
+    return L < 0 ? 0 : min(L, cap);
+}
+
 // Effective context length of sequence s: clamped to what the grid and the
 // block table can cover; clamping counts one error when `report` is set.
 __device__ __forceinline__ int decode_context(const DecodeParams& p, int s, bool report) {

@@ -136,6 +136,14 @@ __global__ void __launch_bounds__(kThreads, 2)
     fence_proxy_async_smem();
     pdl_trigger();
     pdl_wait();
+    // the first item of most CTAs begins its sequence: its length and table entries are asked for before the set-up ends
+    const int n_first = N * Hkv;  // partition-0 items
+    int early = -1, early_len = 0;
+    if (warp == kProducer && (int)blockIdx.x < n_first) {
+        const int s0 = blockIdx.x / Hkv;
+        early_len = p.context_lens[s0];
+        if (lane < p.max_blocks_per_seq) early = p.block_tables[(size_t)s0 * p.max_blocks_per_seq + lane];
+    }
     if (warp == kMma) {  // after the wait: a kernel before this one may still be about to take its tensor memory
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
@@ -145,7 +153,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    const int n_first = N * Hkv;  // partition-0 items
     auto later_items = [&](int s) {
         return (num_partitions(decode_context(p, s, false), partition_of(p, s)) - 1) * Hkv;
     };
@@ -184,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         struct Item {
             int s, split, kvh, nsplit, j0, ntok, nblk;
         };
-        auto describe = [&](int it) {
+        auto describe = [&](int it, int known_len) {  // known_len: the item's context_lens entry, or INT_MIN
             Item d;
             if (it < n_first) {
                 d.s = it / Hkv;
@@ -202,7 +209,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 d.split = r / Hkv + 1;
                 d.kvh = r - (d.split - 1) * Hkv;
             }
-            const int L = decode_context(p, d.s, false), part = partition_of(p, d.s);
+            const int L = known_len == INT_MIN ? decode_context(p, d.s, false) : clamp_context(p, known_len);
+            const int part = partition_of(p, d.s);
             d.nsplit = num_partitions(L, part);
             d.j0 = d.split * part;
             d.ntok = max(0, min(L - d.j0, part));
@@ -237,10 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         int raw = -1;
         float2 sc = make_float2(0.f, 0.f);
         if (is_item(item)) {
-            // the first item of most CTAs begins its sequence: its table entries are asked for beside its length
-            const bool begins = item < n_first && lane < p.max_blocks_per_seq;
-            const int early = begins ? __ldg(p.block_tables + (size_t)(item / Hkv) * p.max_blocks_per_seq + lane) : -1;
-            d = describe(item);
+            d = describe(item, item < n_first ? early_len : INT_MIN);
             raw = item < n_first ? (lane < d.nblk ? early : -1) : load_raw(d, 0);
             sc = load_scales(d, raw);
         }
@@ -317,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 if (st == describe_at) {
                     item2 = __shfl_sync(0xffffffffu, nxt, 0);
                     if (is_item(item2)) {
-                        d2 = describe(item2);
+                        d2 = describe(item2, INT_MIN);
                         raw2 = load_raw(d2, 0);
                     }
                 }

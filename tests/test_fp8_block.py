@@ -402,8 +402,9 @@ def test_decode_contexts_beyond_the_limit_are_clamped_and_counted():
     assert torch.equal(got, want) and int(err.item()) >= 1
 
 
-def _prefill_case(chunks, Hq, Hkv, D, B, seed, extra=(), bad=(), ctx_short=0, pow2=True, splits_over=None):
+def _prefill_case(chunks, Hq, Hkv, D, B, seed, extra=(), bad=(), pow2=True, gain=1.0, scale=None):
     """chunks: (offset, queries); extra: context tokens beyond each chunk's last query."""
+    scale = D ** -0.5 if scale is None else scale
     rng = np.random.default_rng(seed)
     lens = [o + n + (extra[c] if c < len(extra) else 0) for c, (o, n) in enumerate(chunks)]
     table, P = _tables(rng, lens, B)
@@ -414,13 +415,13 @@ def _prefill_case(chunks, Hq, Hkv, D, B, seed, extra=(), bad=(), ctx_short=0, po
     order = rng.permutation(len(chunks))  # sequence of chunk c
     table, ctx = table[np.argsort(order)], np.array(lens)[np.argsort(order)]
     cu = np.concatenate([[0], np.cumsum([n for _, n in chunks])])
-    q = _bf16(rng, (int(cu[-1]), Hq, D))
+    q = _bf16(rng, (int(cu[-1]), Hq, D), gain)
     pools = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (*codes, *scales)]
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     mq, mx = max(max(n for _, n in chunks), 1), max(lens)
     ws = pa.new_prefill_fp8_block_workspace(len(chunks), int(cu[-1]), mq, Hq, Hkv, D, B, mx)
     out = torch.full(q.shape, 5.0, dtype=BF, device="cuda")
-    args = (_i32(cu), _i32([o for o, _ in chunks]), _i32(order), mq, *pools, _i32(table), _i32(ctx), mx, D ** -0.5, ws)
+    args = (_i32(cu), _i32([o for o, _ in chunks]), _i32(order), mq, *pools, _i32(table), _i32(ctx), mx, scale, ws)
     pa.pa_prefill_chunk_fp8_block(q.cuda(), *args, out=out, error_count=err)
     first = out.clone()
     pa.pa_prefill_chunk_fp8_block(q.cuda(), *args, out=out, error_count=err)
@@ -430,7 +431,7 @@ def _prefill_case(chunks, Hq, Hkv, D, B, seed, extra=(), bad=(), ctx_short=0, po
     for c, (o, n) in enumerate(chunks):
         r = slice(int(cu[c]), int(cu[c + 1]))
         want[r], mag[r] = R.attend_rows(q[r].double().numpy(), codes[0], s64[0], codes[1], s64[1], table[order[c]],
-                                        [o + i + 1 for i in range(n)], D ** -0.5)
+                                        [o + i + 1 for i in range(n)], scale)
         floor[r] = R.floor_rows(codes[1], s64[1], table[order[c]], [o + i + 1 for i in range(n)], Hq)
     _close(out, want, mag, floor)
     return int(err.item())
@@ -455,6 +456,43 @@ def test_prefill_tiles_and_long_offsets(Hq, Hkv, B):
 @pytest.mark.gpu
 def test_prefill_bad_pages_are_masked_and_counted():
     assert _prefill_case([(100, 30), (5, 20)], 4, 1, 128, 16, seed=8, bad=[(0, 0, -1), (0, 3, 2), (1, 0, -1), (1, 1, -1)]) > 0
+
+
+@pytest.mark.gpu
+def test_prefill_large_and_small_queries():
+    """Queries far from 1; a softmax scale of 0 and a negative one; scores whose maxima grow late in single rows."""
+    chunks = [(60, 70), (0, 35)]
+    assert _prefill_case(chunks, 8, 2, 128, 16, seed=21, gain=1e6, scale=1e-7) == 0
+    assert _prefill_case(chunks, 8, 2, 128, 16, seed=22, gain=1e-6, scale=1e5) == 0
+    assert _prefill_case(chunks, 8, 2, 128, 32, seed=23, scale=0.0) == 0
+    assert _prefill_case(chunks, 8, 2, 128, 64, seed=24, scale=-0.1) == 0
+    assert _prefill_case([(500, 40)], 4, 1, 128, 8, seed=25, gain=np.exp(np.arange(40) / 12)[:, None, None]) == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [16, 64])
+def test_scales_far_apart(B):
+    """Blocks whose scales differ by 2^60: the large ones' values rule, the small ones still count in the softmax."""
+    rng = np.random.default_rng(30 + B)
+    n, Hq = 400, 4
+    table, P = _tables(rng, [n], B)
+    codes, scales = zip(_pools(rng, P, B, 1, 128), _pools(rng, P, B, 1, 128))
+    scales[1][:] = 2.0 ** rng.choice([-60.0, -3.0, 0.0], (P, 1)).astype(np.float32)
+    scales[1][table[0, 1], 0] = 0.0
+    scales[0][:] = 2.0 ** -5
+    pools = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (*codes, *scales)]
+    s64 = [s.astype(np.float64) for s in scales]
+    q = _bf16(rng, (3, Hq, 128))
+    limits = [n - 2, n - 1, n]
+    want, mag = R.attend_rows(q.double().numpy(), codes[0], s64[0], codes[1], s64[1], table[0], limits, 0.05)
+    floor = R.floor_rows(codes[1], s64[1], table[0], limits, Hq)
+    ws = pa.new_prefill_fp8_block_workspace(1, 3, 3, Hq, 1, 128, B, n)
+    out = pa.pa_prefill_chunk_fp8_block(q.cuda(), _i32([0, 3]), _i32([n - 3]), _i32([0]), 3, *pools, _i32(table), _i32([n]),
+                                        n, 0.05, ws)
+    _close(out, want, mag, floor)
+    ws = pa.new_decode_fp8_block_workspace(1, Hq, 1, 128, B, n)
+    out = pa.pa_decode_fp8_block(q[2:].cuda(), *pools, _i32(table), _i32([n]), n, 0.05, ws)
+    _close(out, want[2:], mag[2:], floor[2:])
 
 
 # ---------------------------------------------------------------- GPU: together
