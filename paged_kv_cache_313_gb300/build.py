@@ -1,8 +1,10 @@
-"""Build libpa.so in-tree with nvcc for sm_103a (GB300).
+"""Build libpa.so in-tree with nvcc for sm_103a (GB300), and _pa_bind.so, the
+compiled part of the Python binding, with g++.
 
-Each CUDA translation unit compiles in parallel to an object file, then nvcc
-links the shared library.  The CUDA runtime is linked statically, so the
-library needs only the driver at load time.  Usage: ``python -m
+Each translation unit compiles in parallel to an object file, then nvcc links
+the library.  The CUDA runtime is linked statically, so the library needs only
+the driver at load time; _pa_bind.so links to it and to PyTorch's libraries.
+Usage: ``python -m
 paged_kv_cache_313_gb300.build [--force]``.
 """
 from __future__ import annotations
@@ -13,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -20,6 +23,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libpa.so")
+BIND = os.path.join(BUILD, "_pa_bind.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
@@ -38,18 +42,53 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "pa.h")]
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "pa.h"),
+                                                                 os.path.join(CSRC, "bind.cpp")]
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BIND):
         return True
     t = os.path.getmtime(LIB)
     return any(os.path.getmtime(f) > t for f in _deps())
 
 
+def _torch_dir() -> str:
+    """Where PyTorch is installed (found without importing it)."""
+    import importlib.util
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        raise RuntimeError("PyTorch not found: the Python binding is built against its headers")
+    return list(spec.submodule_search_locations)[0]
+
+
+def _compile_bind() -> str:
+    obj = os.path.join(BUILD, "bind.o")
+    inc = os.path.join(_torch_dir(), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", INCLUDE, "-isystem", inc, "-isystem",
+           os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", cuda, "-isystem",
+           sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "bind.cpp"), "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on bind.cpp:\n{r.stderr}")
+    return obj
+
+
+def _link_bind(obj: str) -> None:
+    libs = os.path.join(_torch_dir(), "lib")
+    tmp = BIND + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", BUILD, "-l:libpa.so", "-L", libs, "-lc10", "-lc10_cuda", "-ltorch_cpu",
+           "-ltorch", "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{libs}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"linking the Python binding failed:\n{r.stderr}")
+    os.replace(tmp, BIND)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every .cu under csrc/ and link _build/libpa.so; returns its path."""
+    """Compile every .cu under csrc/ and bind.cpp, link _build/libpa.so and _build/_pa_bind.so; returns the library's
+    path."""
     if not force and not _stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -67,13 +106,16 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+        bind = ex.submit(_compile_bind)
         objs = list(ex.map(compile_one, srcs))
+        bind_obj = bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-Xlinker", "--no-undefined"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_bind(bind_obj)
     return LIB
 
 

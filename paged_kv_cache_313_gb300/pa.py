@@ -1,11 +1,14 @@
 """Python binding of libpa.so: the C ABI in include/pa.h, same names, torch
-CUDA tensors in and out.  Argument marshalling only — every step runs in the
+CUDA tensors in and out.  Argument marshalling only (in ctypes, and in the
+compiled module _pa_bind.so for the calls over block-scaled e4m3 pools) — every step runs in the
 library's CUDA kernels.  There is no CPU fallback: if the library is missing
 or fails to load, every call raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import threading
 
@@ -13,6 +16,7 @@ import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "_build", "libpa.so")
+BIND_PATH = os.path.join(PKG, "_build", "_pa_bind.so")
 
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_CUDA, PA_ERR_WORKSPACE, PA_ERR_UNSUPPORTED_DEVICE = range(6)
 PA_F32, PA_BF16 = 0, 1
@@ -389,51 +393,22 @@ def pa_prefill_chunk(q, cu_q_lens, q_start_pos, seq_of_chunk, max_q_len: int, k_
     return out
 
 
-def _fp8_block_pools(k_cache, v_cache, k_scales, v_scales):
-    """Shapes of e4m3 pools with a scale per (block, kv head), checked: (P, B, Hkv, D, device index)."""
-    if k_cache.dtype is not torch.uint8 or v_cache.dtype is not torch.uint8:
-        raise TypeError("fp8 pools are uint8 tensors of e4m3 codes")
-    shape = k_cache.shape
-    P, B, H, D = shape
-    if v_cache.shape != shape:
-        raise ValueError("shapes of k_cache and v_cache differ")
-    if k_scales.shape != (P, H) or v_scales.shape != (P, H):
-        raise ValueError(f"k_scales and v_scales must be [num_blocks, num_kv_heads] = [{P}, {H}], got "
-                         f"{list(k_scales.shape)} and {list(v_scales.shape)}")
-    return P, B, H, D, k_cache.get_device()
+_bind_module = None
 
 
-def _on(t, name: str, dtype, dev: int, host_ok: bool = False):
-    """Pointer of a contiguous tensor of `dtype` on device `dev` (or, with host_ok, in pinned host memory).  The same
-    checks as _dev and the pools' device, in few calls: they are most of a small call's host time."""
-    if t is None:
-        return None
-    if t.dtype is not dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != dev and not (host_ok and t.is_pinned()):
-        raise ValueError(f"{name} must be a CUDA tensor on the pools' device" +
-                         (" or pinned host memory" if host_ok else ""))
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _ws_on(workspace, dev: int):
-    return (None, 0) if workspace is None else (_on(workspace, "workspace", torch.uint8, dev), workspace.numel())
-
-
-def _call(name: str, dev: int, stream, args) -> None:
-    """One library call with device `dev` current, on `stream` (None: the device's current stream)."""
-    if dev < 0:
-        raise ValueError("the pools must be CUDA tensors")
-    fn = getattr(_lib or lib(), name)
-    if torch.cuda.current_device() == dev:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream))
-    if status != PA_OK:
-        _check(name, status)
+def _bind():
+    """The compiled binding of the calls over block-scaled e4m3 pools (csrc/bind.cpp; raises if it was not built)."""
+    global _bind_module
+    if _bind_module is None:
+        lib()
+        if not os.path.exists(BIND_PATH):
+            raise RuntimeError(f"_pa_bind.so is not built ({BIND_PATH}); run "
+                               "`python -m paged_kv_cache_313_gb300.build` first")
+        loader = importlib.machinery.ExtensionFileLoader("_pa_bind", BIND_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_pa_bind", loader))
+        loader.exec_module(module)
+        _bind_module = module
+    return _bind_module
 
 
 def new_write_fp8_block_workspace(num_tokens, num_blocks, block_size, device=None) -> torch.Tensor | None:
@@ -447,22 +422,11 @@ def pa_write_kv_paged_fp8_block(k_new, v_new, k_cache, v_cache, k_scales, v_scal
     """Slot mapping and a quantising K/V write into uint8 e4m3 pools with a scale per (block, kv head), chosen by the
     write: the smallest power of two that holds the rows stored into the block, never below the block's scale from
     before unless the block's first slot is stored; the block's other codes keep their values."""
-    T, H, D = k_new.shape
-    P, B, H2, D2, dev = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
-    if (H, D) != (H2, D2) or v_new.shape != k_new.shape:
-        raise ValueError("shapes of k_new, v_new and the pools disagree")
-    if seq_idx.numel() != T or pos.numel() != T or (slot_mapping is not None and slot_mapping.numel() != T):
-        raise ValueError(f"seq_idx, pos and slot_mapping must have one entry for each of the {T} tokens")
-    S, W = block_tables.shape
-    i32, f32, u8, bf16 = torch.int32, torch.float32, torch.uint8, torch.bfloat16
-    ws, ws_bytes = _ws_on(workspace, dev)
-    _call("pa_write_kv_paged_fp8_block", dev, stream, (
-        _on(k_new, "k_new", bf16, dev), _on(v_new, "v_new", bf16, dev), T, H, D, _on(k_cache, "k_cache", u8, dev),
-        _on(v_cache, "v_cache", u8, dev), _on(k_scales, "k_scales", f32, dev), _on(v_scales, "v_scales", f32, dev),
-        P, B, _on(block_tables, "block_tables", i32, dev), S, W, _on(seq_idx, "seq_idx", i32, dev),
-        _on(pos, "pos", i32, dev), _on(slot_mapping, "slot_mapping", torch.int64, dev), ws, ws_bytes,
-        _on(error_count, "error_count", i32, dev)))
-    return slot_mapping
+    r = (_bind_module or _bind()).write(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, seq_idx, pos,
+                                        workspace, slot_mapping, error_count, stream)
+    if r.__class__ is int:
+        _check("pa_write_kv_paged_fp8_block", r)
+    return r
 
 
 def pa_read_kv_paged_fp8_block(k_cache, v_cache, k_scales, v_scales, block_tables, seq_idx, pos, k_out=None,
@@ -470,25 +434,13 @@ def pa_read_kv_paged_fp8_block(k_cache, v_cache, k_scales, v_scales, block_table
     """(K rows, V rows), each [T, Hkv, D] of `dtype` (bfloat16 or float32): code * scale of the token at pos[t] of
     sequence seq_idx[t].  Rows with pos < 0 or an invalid index are left as they were (uninitialised where no k_out /
     v_out is given)."""
-    P, B, H, D, dev = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
-    T = seq_idx.numel()
-    if pos.numel() != T:
-        raise ValueError("seq_idx and pos differ in length")
-    if k_out is None:
-        k_out = torch.empty((T, H, D), dtype=dtype if v_out is None else v_out.dtype, device=k_cache.device)
-    if v_out is None:
-        v_out = torch.empty_like(k_out)
-    dt = k_out.dtype
-    if k_out.shape != (T, H, D) or v_out.shape != (T, H, D) or v_out.dtype is not dt:
-        raise ValueError(f"k_out and v_out must be [{T}, {H}, {D}] of one dtype")
-    S, W = block_tables.shape
-    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
-    _call("pa_read_kv_paged_fp8_block", dev, stream, (
-        _on(k_out, "k_out", dt, dev), _on(v_out, "v_out", dt, dev), T, H, D, _dtype_code(k_out),
-        _on(k_cache, "k_cache", u8, dev), _on(v_cache, "v_cache", u8, dev), _on(k_scales, "k_scales", f32, dev),
-        _on(v_scales, "v_scales", f32, dev), P, B, _on(block_tables, "block_tables", i32, dev), S, W,
-        _on(seq_idx, "seq_idx", i32, dev), _on(pos, "pos", i32, dev), _on(error_count, "error_count", i32, dev)))
-    return k_out, v_out
+    if dtype is not torch.bfloat16 and dtype is not torch.float32:
+        raise TypeError(f"unsupported dtype {dtype} (float32 or bfloat16)")
+    r = (_bind_module or _bind()).read(k_cache, v_cache, k_scales, v_scales, block_tables, seq_idx, pos, k_out, v_out,
+                                       dtype is torch.float32, error_count, stream)
+    if r.__class__ is int:
+        _check("pa_read_kv_paged_fp8_block", r)
+    return r
 
 
 def new_decode_fp8_block_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
@@ -504,23 +456,11 @@ def new_decode_fp8_block_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim
 def pa_decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, max_context_len: int,
                         scale: float, workspace, out=None, error_count=None, stream=None) -> torch.Tensor:
     """pa_decode over uint8 e4m3 pools with a scale per (block, kv head); q and out bf16."""
-    N, Hq, D = q.shape
-    P, B, Hkv, D2, dev = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
-    if D2 != D:
-        raise ValueError("head_dim of q and k_cache differ")
-    if out is None:
-        out = torch.empty_like(q)
-    S, W = block_tables.shape
-    if out.shape != q.shape or S != N or context_lens.numel() != N:
-        raise ValueError("shapes of q, out, block_tables and context_lens disagree")
-    i32, f32, u8, bf16 = torch.int32, torch.float32, torch.uint8, torch.bfloat16
-    ws, ws_bytes = _ws_on(workspace, dev)
-    _call("pa_decode_fp8_block", dev, stream, (
-        _on(out, "out", bf16, dev, True), _on(q, "q", bf16, dev), N, Hq, Hkv, D, _on(k_cache, "k_cache", u8, dev),
-        _on(v_cache, "v_cache", u8, dev), _on(k_scales, "k_scales", f32, dev), _on(v_scales, "v_scales", f32, dev),
-        P, B, _on(block_tables, "block_tables", i32, dev), W, _on(context_lens, "context_lens", i32, dev),
-        int(max_context_len), float(scale), ws, ws_bytes, _on(error_count, "error_count", i32, dev)))
-    return out
+    r = (_bind_module or _bind()).decode(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens,
+                                         max_context_len, scale, workspace, out, error_count, stream)
+    if r.__class__ is int:
+        _check("pa_decode_fp8_block", r)
+    return r
 
 
 def new_prefill_fp8_block_workspace(num_chunks, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
@@ -535,28 +475,12 @@ def pa_prefill_chunk_fp8_block(q, cu_q_lens, q_start_pos, seq_of_chunk, max_q_le
                                v_scales, block_tables, context_lens, max_context_len: int, scale: float,
                                workspace=None, out=None, error_count=None, stream=None) -> torch.Tensor:
     """Causal chunked-prefill attention over uint8 e4m3 pools with a scale per (block, kv head); q and out bf16."""
-    T, Hq, D = q.shape
-    P, B, Hkv, D2, dev = _fp8_block_pools(k_cache, v_cache, k_scales, v_scales)
-    if D2 != D:
-        raise ValueError("head_dim of q and k_cache differ")
-    C = q_start_pos.numel()
-    if out is None:
-        out = torch.empty_like(q)
-    if out.shape != q.shape or cu_q_lens.numel() != C + 1 or seq_of_chunk.numel() != C:
-        raise ValueError("shapes of q, out, cu_q_lens, q_start_pos and seq_of_chunk disagree")
-    S, W = block_tables.shape
-    if context_lens.numel() != S:
-        raise ValueError("shapes of block_tables and context_lens disagree")
-    i32, f32, u8, bf16 = torch.int32, torch.float32, torch.uint8, torch.bfloat16
-    ws, ws_bytes = _ws_on(workspace, dev)
-    _call("pa_prefill_chunk_fp8_block", dev, stream, (
-        _on(out, "out", bf16, dev, True), _on(q, "q", bf16, dev), _on(cu_q_lens, "cu_q_lens", i32, dev),
-        _on(q_start_pos, "q_start_pos", i32, dev), _on(seq_of_chunk, "seq_of_chunk", i32, dev), C, T,
-        int(max_q_len), S, Hq, Hkv, D, _on(k_cache, "k_cache", u8, dev), _on(v_cache, "v_cache", u8, dev),
-        _on(k_scales, "k_scales", f32, dev), _on(v_scales, "v_scales", f32, dev), P, B,
-        _on(block_tables, "block_tables", i32, dev), W, _on(context_lens, "context_lens", i32, dev),
-        int(max_context_len), float(scale), ws, ws_bytes, _on(error_count, "error_count", i32, dev)))
-    return out
+    r = (_bind_module or _bind()).prefill(q, cu_q_lens, q_start_pos, seq_of_chunk, max_q_len, k_cache, v_cache, k_scales,
+                                          v_scales, block_tables, context_lens, max_context_len, scale, workspace, out,
+                                          error_count, stream)
+    if r.__class__ is int:
+        _check("pa_prefill_chunk_fp8_block", r)
+    return r
 
 
 def pa_copy_blocks(k_cache, v_cache, src_blocks, dst_blocks, num_valid, error_count=None, stream=None) -> None:
