@@ -112,9 +112,23 @@ struct Bars {
     __device__ uint64_t* drain() const { return item_full(2 * kItems + 1); }  // by both issuing warps
 };
 
-// The kernel's own parameters: the plan's key tiles per span and spans per tile.
+// Division of n < 2^30 by a number known to the host: n / d = (hi32(n mul) + n) >> shift with shift the least such that
+// 2^shift >= d and mul = floor(2^32 (2^shift - d) / d) + 1 (multiplication by a rounded-up reciprocal; checked against
+// the quotient for divisors up to 2^30).
+struct Divisor {
+    uint32_t mul, shift, d;
+    explicit Divisor(uint32_t d_ = 1) : mul(0), shift(0), d(d_) {
+        while ((1u << shift) < d) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - d)) / d + 1);
+    }
+    __device__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+};
+
+// The kernel's own parameters: the plan's key tiles per span and spans per tile, and what items are numbered by.
 struct Spans {
     int tiles, count;
+    int items;  // query tiles x chunks x kv heads x spans
+    Divisor per_rank, per_count, per_heads, per_tiles, per_ppt;
     float* o;    // [count][total_q][num_q_heads][kD]
     float2* ml;  // [count][total_q][num_q_heads]
 };
@@ -192,31 +206,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int log2b = 31 - __clz(B);
     const uint32_t inv_g = (65536 + G - 1) / G;  // r / G = r * inv_g >> 16 for r < 128 and G <= 8 (checked for all)
 
-    if (threadIdx.x == 0) {
-        for (int i = 0; i < kKStages; ++i) {
-            mbar_init(bars.k_full(i), 1);
-            mbar_init(bars.k_empty(i), 1);
+    if (warp == 0) {  // the barriers, a lane each: in this order in memory, with these numbers of arrivals
+        for (int i = lane; i < kNumBars; i += 32) {
+            uint64_t* bar = bars.base + i;
+            const bool conv = (bar >= bars.v_empty(0) && bar < bars.vh_full(kVhStages)) ||
+                              (bar >= bars.q_full(0) && bar < bars.q_full(kQSlots));
+            const int n = conv                                                        ? kConverters
+                          : bar >= bars.p_full(0) && bar < bars.p_full(kPieces)       ? 4
+                          : bar >= bars.item_empty(0) && bar < bars.item_empty(kItems) ? 8 + kConverters + 3  // every other warp
+                          : bar == bars.o_free() || bar == bars.joined()              ? 8
+                          : bar == bars.drain()                                       ? 2
+                                                                                      : 1;
+            mbar_init(bar, n);
         }
-        for (int i = 0; i < kVStages; ++i) {
-            mbar_init(bars.v_full(i), 1);
-            mbar_init(bars.v_empty(i), kConverters);
-        }
-        for (int i = 0; i < kVhStages; ++i) mbar_init(bars.vh_full(i), kConverters);
-        for (int i = 0; i < kPieces; ++i) {
-            mbar_init(bars.s_full(i), 1);
-            mbar_init(bars.p_full(i), 4);
-            mbar_init(bars.pv_done(i), 1);
-        }
-        mbar_init(bars.q_empty(), 1);
-        for (int i = 0; i < kQSlots; ++i) mbar_init(bars.q_full(i), kConverters);
-        for (int i = 0; i < kInfo; ++i) mbar_init(bars.info(i), 1);
-        for (int i = 0; i < kItems; ++i) {
-            mbar_init(bars.item_full(i), 1);
-            mbar_init(bars.item_empty(i), 8 + kConverters + 3);  // every other warp
-        }
-        mbar_init(bars.o_free(), 8);
-        mbar_init(bars.joined(), 8);
-        mbar_init(bars.drain(), 2);
         fence_mbar_init();
     }
     pdl_trigger();
@@ -255,25 +257,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         // first; CTA b takes one of every pass of gridDim.x items, in serpentine order, so that heavy and light ones
         // pair up.  It stays an item ahead of its own copies: when every warp described its items itself, that took
         // each of them 3.3k cycles an item, between the epilogue of one and the first score of the next.
-        const int per_rank = p.num_chunks * Hkv * spans.count;
-        const int num_items = (p.max_q_len + ppt - 1) / ppt * per_rank;  // the host keeps it below 2^30
+        const int num_items = spans.items;  // below 2^30
+        const int passes = (num_items - 1) / (int)gridDim.x + 1;
         int pass = 0;
         uint32_t published = 0;
         auto describe = [&](Item& d) {  // the item of this pass; false for an empty one
             const int g = gridDim.x, b = blockIdx.x, k = pass * g + ((pass & 1) ? g - 1 - b : b);
             if (k >= num_items) return false;
-            const int rank = k / per_rank;
-            int rem = k - rank * per_rank;
-            d.span = rem % spans.count;
-            rem /= spans.count;
-            const int ch = rem / Hkv;
-            d.kvh = rem - ch * Hkv;
+            const int rank = spans.per_rank.div(k);
+            int rem = k - rank * (int)spans.per_rank.d;
+            const int unit = spans.per_count.div(rem), ch = spans.per_heads.div(unit);
+            d.span = rem - unit * spans.count;
+            d.kvh = unit - ch * Hkv;
             int r0, n, start;
             if (!chunk_of(p, ch, r0, n, d.s, start)) {
                 if (rank == 0 && d.kvh == 0 && d.span == 0 && lane == 0) count_error(p.error_count);
                 return false;
             }
-            const int tiles = (n + ppt - 1) / ppt;
+            const int tiles = n > (1 << 29) ? (n + ppt - 1) / ppt : spans.per_ppt.div(n + ppt - 1);
             if (rank >= tiles) return false;
             const int i0 = (tiles - 1 - rank) * ppt;
             d.row = r0 + i0;
@@ -286,13 +287,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 d.last_key = cap - 1;
             }
             const int all = d.last_key >= 0 ? d.last_key / kTile + 1 : 0;
-            d.spans = max(1, (all + spans.tiles - 1) / spans.tiles);
+            d.spans = max(1, spans.per_tiles.div(all + spans.tiles - 1));  // (tiles of 128 keys: below 2^25)
             d.t0 = d.span * spans.tiles;
             d.nt = max(0, min(spans.tiles, all - d.t0));
             return d.span < d.spans;  // without any key, span 0 stores zeros
         };
         auto publish = [&](Item& d) {  // the next item, or the end
-            const int passes = (num_items + (int)gridDim.x - 1) / (int)gridDim.x;
             d.nt = -1;
             for (; pass < passes; ++pass)
                 if (describe(d)) break;
@@ -905,8 +905,10 @@ Spans plan_spans(int num_chunks, int max_q_len, int num_kv_heads, int group, int
     if (items > 0 && items < num_sms) want = num_sms / items;
     else if (items < 2LL * num_sms && tiles >= 16) want = 2;
     if (want > tiles / 2) want = tiles / 2;
-    Spans s{};
+    Spans s;
     s.tiles = tiles;
+    s.o = nullptr;
+    s.ml = nullptr;
     if (want > 1) s.tiles = (int)((tiles + want - 1) / want);
     s.count = (tiles + s.tiles - 1) / s.tiles;
     return s;
@@ -952,6 +954,12 @@ int launch_prefill_fp8_block_tc(const PrefillParams& p, void* workspace, int num
         s.ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + up256(rows * kD * sizeof(float)));
     }
     const long long items = work_items(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group) * s.count;
+    s.items = (int)items;
+    s.per_rank = Divisor((uint32_t)(p.num_chunks * p.num_kv_heads * s.count));
+    s.per_count = Divisor((uint32_t)s.count);
+    s.per_heads = Divisor((uint32_t)p.num_kv_heads);
+    s.per_tiles = Divisor((uint32_t)s.tiles);
+    s.per_ppt = Divisor((uint32_t)(kTile / p.group));
     rc = launch_kernel(kernel, dim3((unsigned)(items < num_sms ? items : num_sms)),
                        dim3(kThreads), kSmemBytes, stream, tmk, tmv, p, s);
     if (rc != PA_OK || s.count <= 1) return rc;
