@@ -15,13 +15,12 @@
 //   * queries: scaled by a power of two that puts the row's largest magnitude
 //     in [128, 256); two terms hold a bf16's 8 bits exactly (an element below
 //     2^-14 of the row's largest is off by 2^-20 of that largest at most);
-//   * probabilities: 256 p vs / R, two terms off by 2^-8 relative, a bf16's
-//     rounding, and at least 2^-14 (2^-22 of the largest).  The sum of the
-//     softmax takes p in float, unrounded.
-// ks multiplies a token's scores, vs its probability.  p = 2^(x - the stage's
-// maximum) and R, the power of two not below any vs of the stage, keep
-// p vs / R <= 1 whatever the scales, and the terms' floor relative to the stage
-// alone; a stage's output and sum are brought to the running maximum in float.
+//   * weights: 256 p', two terms off by 2^-8 relative, a bf16's rounding, and at
+//     least 2^-14 (2^-22 of the stage's largest p').
+// ks multiplies a token's scores; vs is part of the exponent, p' = 2^(x + log2(vs) - m)
+// with m the stage's maximum of x + log2(vs): the terms' floor is relative to the
+// stage's largest p vs.  The sum of the softmax takes p' / vs in float, unrounded.
+// A stage's output and sum are brought to the running maximum in float.
 //
 // Work.  An item is (sequence, partition, kv head); items are numbered as in
 // decode_tc.cu (partition 0 of every (sequence, head) directly, later
@@ -63,7 +62,8 @@ constexpr int kProducer = 4, kMma = 5;
 constexpr int kMaxSeqs = 512;  // per launch (the prefix sum lives in shared memory)
 constexpr int kMaxBlocks = kTok / 8;  // blocks of a stage
 constexpr uint32_t kTmemCols = 64;    // S0 | S1 | O0 | O1, 16 columns each
-constexpr float kScaleFloor = 7.703719777548943e-34f;  // 2^-110, the smallest R
+// A V scale below 2^-80 of the stage's largest or 2^-100 (the smallest that the write makes) counts as 0.
+constexpr float kHold = 8.271806125530277e-25f, kLeastScale = 7.888609052210118e-31f;
 
 struct Stage {
     int s, kvh, split, flags;  // flags: 1 first stage of the item, 2 last, 4 the item writes the output, 8 no more
@@ -486,6 +486,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             const bool valid = t < g.ntok && ((g.blocks >> (t >> log2b)) & 1u);
             const float ks = reinterpret_cast<const float*>(smem + kKs)[slot * kMaxBlocks + (t >> log2b)];
             const float vs = reinterpret_cast<const float*>(smem + kVs)[slot * kMaxBlocks + (t >> log2b)];
+            // (a V below `hold` adds nothing, its key's weight still counts in the sum)
+            const float hold = fmaxf(g.vmax * kHold, kLeastScale);
+            const float off = __log2f(fmaxf(vs, hold)), inv_vs = fast_exp2(-off), unit = vs >= hold ? 256.f : 0.f;
             if (g.flags & 1) {
                 if (!mbar_wait_warp(&q_ready[items & 1], (items >> 1) & 1)) {
                     ok = false;
@@ -513,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int h = 0; h < 8; ++h) wm[h] = -INFINITY;
 #pragma unroll
                 for (int h = 0; h < kHeads; ++h) {
-                    x[h] = valid ? fmaf(lo[h], 1.f / 16, hi[h]) * qf[h] * c : -INFINITY;
+                    x[h] = valid ? fmaf(fmaf(lo[h], 1.f / 16, hi[h]) * qf[h], c, off) : -INFINITY;
                     wm[h] = redux_max(x[h]);
                 }
                 if (lane == 0) {
@@ -551,10 +554,6 @@ __global__ void __launch_bounds__(kThreads, 2)
                     beta[h] = mx[h] == -INFINITY ? 0.f : fast_exp2(mx[h] - m[h]);
                 }
             }
-            // R: the stage's largest V scale, rounded up to a power of two
-            const float R =
-                __uint_as_float((__float_as_uint(fmaxf(g.vmax, kScaleFloor)) + 0x7FFFFFu) & 0x7F800000u);
-            const float pv_scale = vs * (256.f / R), unit = R * (1.f / 256);
             uint32_t row[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
             for (int h2 = 0; h2 < kHeads / 2; ++h2) {
@@ -563,8 +562,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int j = 0; j < 2; ++j) {
                     const int h = 2 * h2 + j;
                     const float e = valid ? fast_exp2(x[h] - mx[h]) : 0.f;
-                    l[h] = fmaf(l[h], alpha[h], e * beta[h]);
-                    w[j] = e * pv_scale;
+                    l[h] = fmaf(l[h], alpha[h], e * inv_vs * beta[h]);
+                    w[j] = e * unit;
                 }
                 const uint16_t hi = pack_e4m3x2(w[0], w[1]);
                 const float2 r = e4m3x2_to_float2(hi);
@@ -589,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
                 acc[h] *= alpha[h];
-                bring[h] = beta[h] * unit;
+                bring[h] = beta[h] * (1.f / 256);
             }
             if (!(g.flags & 2)) continue;
             // ---- end of the item: the sums over all tokens, then this thread's head dim of every head

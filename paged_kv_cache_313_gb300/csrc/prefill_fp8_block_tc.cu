@@ -19,12 +19,12 @@
 //               came from.  (P as two e4m3 terms would spare the widening, but
 //               its floor, 2^-17 of the largest weight, is too coarse for long
 //               diffuse contexts, and the split costs twice the widening.)
-// ks multiplies a key's scores.  vs / R is part of the exponent, P' =
-// 2^(x + log2(vs / R) - m), so it costs nothing per element; the softmax's sum
-// takes the float P' of 8 keys of one block times R / vs.  R is a power of two;
-// it changes (and O is rescaled) only when a V scale passes 64 R.  Ratios below
-// 2^-40 are held there: such a weight is 0 in f16, and its P' still counts in
-// the sum.
+// ks multiplies a key's scores; vs is part of the exponent, P' = 2^(x + log2(vs) - m)
+// with m the running maximum of x + log2(vs), so it costs nothing per element and
+// a row's largest P' is about 1 whatever the scales: f16's floor, 2^-25, is relative
+// to the row's own largest p vs, not to blocks that it gives no weight or does not
+// see.  The softmax's sum takes the float P' of 8 keys of one block (of 32 where
+// blocks have 32 keys) times 1 / vs.
 //
 // Two softmax groups of four warps, a thread per row, take alternate pieces of
 // 64 keys (a half of every key tile each), with their own running maximum, sum
@@ -65,20 +65,21 @@ constexpr int kItems = 8;   // ring of item descriptions
 constexpr uint32_t kTO = 0, kTQ = 256, kTS = 320;
 constexpr float kMost = 512.f;  // largest sum of a piece's weights before a row's maximum is looked for again
 constexpr float kTiny = 1e-37f;  // the least factor of a score: 0 would make NaN of a masked key's -inf
-constexpr float kScaleFloor = 7.703719777548943e-34f;  // 2^-110, the smallest R
+// A V scale counts as at least 2^-80 of the item's largest so far and 2^-100 (the smallest that the write makes), so
+// that the weights of its keys stay in float's range; what such a V adds is below 2^-71 of that largest scale.
+constexpr float kHold = 8.271806125530277e-25f, kLeastScale = 7.888609052210118e-31f;
 
 // shared memory, offsets from a 1024-aligned base
 constexpr int kQ = 0;  // [hi, lo][128 rows][128], 16-byte pieces swizzled by row: staged for tensor memory
 constexpr int kK = kQ + 2 * kCodes;
 constexpr int kV = kK + kKStages * kCodes;
 constexpr int kVh = kV + kVStages * kCodes;
-constexpr int kConsts = kVh + kVhStages * 2 * kHalfBytes;  // float4 [kInfo][16]: per 8 keys ks', log2(vs/R), R/vs
+constexpr int kConsts = kVh + kVhStages * 2 * kHalfBytes;  // float4 [kInfo][16]: per 8 keys ks', log2(vs), 1/vs
 constexpr int kMask = kConsts + kInfo * 16 * 16;           // uint32 [kInfo][4]
 constexpr int kVMask = kMask + kInfo * 16;                 // uint32 [kVStages][4]: the same for the converters
-constexpr int kR = kVMask + kVStages * 16;                 // float [kInfo]
-constexpr int kQf = kR + kInfo * 4;                        // float [kQSlots][128]
-constexpr int kState = kQf + kQSlots * kTile * 4;          // float4 [2 items][2 groups][128]: m, l, R
-constexpr int kItem = kState + 2 * 2 * kTile * 16;  // Item [kItems]
+constexpr int kQf = kVMask + kVStages * 16;                // float [kQSlots][128]
+constexpr int kState = kQf + kQSlots * kTile * 4;          // float2 [2 items][2 groups][128]: m, l
+constexpr int kItem = kState + 2 * 2 * kTile * 8;          // Item [kItems]
 constexpr int kBars = kItem + kItems * 48;
 constexpr int kNumBars = 2 * kKStages + 2 * kVStages + kVhStages + 3 * kPieces + kQSlots + 1 + kInfo + 2 * kItems + 3;
 constexpr int kTmemSlot = kBars + kNumBars * 8;
@@ -336,7 +337,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             int raw = d.nt > 0 ? load_raw(0) : -1, raw_next = -1, pb = -1;
             float2 sc = load_scales(raw), sc_next = make_float2(0.f, 0.f);
-            float R = 0.f;
+            uint32_t valid = 0;                       // the chunk's blocks with a valid table entry
+            float ks = 0.f, off = 0.f, inv_vs = 0.f;  // of this lane's block: what the softmax needs of it
+            float top = 0.f;                          // the largest V scale of the item so far
             for (int j = 0, chunk = 0, l = 0; j < d.nt; ++j, ++g) {
                 if (l == 0) {
                     if (chunk > 0) {
@@ -348,9 +351,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (!v_side) count_error(p.error_count);
                         pb = -1;
                     }
+                    valid = __ballot_sync(0xffffffffu, pb >= 0);
+                    if (!v_side) {
+                        top = fmaxf(top, redux_max(sc.y));
+                        ks = sc.x * fabsf(p.scale_log2);
+                        off = __log2f(fmaxf(sc.y, fmaxf(top * kHold, kLeastScale)));
+                        inv_vs = fast_exp2(-off);
+                    }
                 }
-                const uint32_t valid = __ballot_sync(0xffffffffu, pb >= 0);
-                const uint32_t mine = (valid >> (l * bpt)) & ((1u << bpt) - 1u);
+                const uint32_t all = (1u << bpt) - 1u, mine = (valid >> (l * bpt)) & all;
                 const int stages = v_side ? kVStages : kKStages, st = v_side ? g % kVStages : g % kKStages;
                 const int round = v_side ? g / kVStages : g / kKStages;
                 uint64_t* full = v_side ? bars.v_full(st) : bars.k_full(st);
@@ -359,15 +368,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 const int slot = g % kInfo;
+                const int keys = d.last_key + 1 - (d.t0 + j) * kTile;  // of this tile
                 if (lane < 4) {  // key-validity mask: 32 keys a word
-                    const int left = d.last_key + 1 - (d.t0 + j) * kTile - 32 * lane;
-                    uint32_t m = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
-                    if (B >= 32) {
-                        if (!((mine >> ((32 * lane) >> log2b)) & 1u)) m = 0u;
-                    } else {
-                        const int per = 32 >> log2b;
-                        for (int b = 0; b < per; ++b)
-                            if (!((mine >> (lane * per + b)) & 1u)) m &= ~(((1u << B) - 1u) << (b * B));
+                    uint32_t m = ~0u;
+                    if (mine != all || keys < kTile) {
+                        const int left = keys - 32 * lane;
+                        m = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
+                        if (B >= 32) {
+                            if (!((mine >> ((32 * lane) >> log2b)) & 1u)) m = 0u;
+                        } else {
+                            const int per = 32 >> log2b;
+                            for (int b = 0; b < per; ++b)
+                                if (!((mine >> (lane * per + b)) & 1u)) m &= ~(((1u << B) - 1u) << (b * B));
+                        }
                     }
                     if (v_side) reinterpret_cast<uint32_t*>(smem + kVMask)[st * 4 + lane] = m;
                     else mask[slot * 4 + lane] = m;
@@ -382,19 +395,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 my_pb * B, d.kvh, full);
                 if (!v_side) {
                     // what the softmax needs of this tile's 16 groups of 8 keys
-                    const float my_vs = __shfl_sync(0xffffffffu, sc.y, src);
-                    const float vmax = redux_max(lane < bpt ? my_vs : 0.f);
-                    if (j == 0 || vmax > 64.f * R)
-                        R = __uint_as_float((__float_as_uint(fmaxf(vmax, kScaleFloor)) + 0x7FFFFFu) & 0x7F800000u);
-                    const int blk = ((lane & 15) * 8) >> log2b;  // block of this lane's group
-                    const float ks = __shfl_sync(0xffffffffu, sc.x, l * bpt + blk);
-                    const float vs = __shfl_sync(0xffffffffu, sc.y, l * bpt + blk);
-                    if (lane < 16) {
-                        const float off = __log2f(fmaxf(vs / R, 9.094947017729282e-13f));  // at least 2^-40
-                        reinterpret_cast<float4*>(smem + kConsts)[slot * 16 + lane] =
-                            make_float4(ks * fabsf(p.scale_log2), off, fast_exp2(-off), 0.f);
-                    }
-                    if (lane == 0) reinterpret_cast<float*>(smem + kR)[slot] = R;
+                    const int blk = l * bpt + (((lane & 15) * 8) >> log2b);  // block of this lane's group
+                    const float a = __shfl_sync(0xffffffffu, ks, blk), o = __shfl_sync(0xffffffffu, off, blk);
+                    const float z = __shfl_sync(0xffffffffu, inv_vs, blk);
+                    if (lane < 16) reinterpret_cast<float4*>(smem + kConsts)[slot * 16 + lane] = make_float4(a, o, z, 0.f);
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bars.info(slot));
                 }
@@ -614,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = (warp & 3) * 32 + lane;          // row = tensor-memory lane
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_o = tmem + lanes + kTO + x * 128;
-        float4* state = reinterpret_cast<float4*>(smem + kState);
+        float2* state = reinterpret_cast<float2*>(smem + kState);
         uint32_t g = 0, items = 0;  // key tiles (pieces of this group), and items with keys
         BoundedWarpBarrier joined{bars.joined(), 0};
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -626,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (uint32_t n = 0; take_item(n, d); ++n) {
             const bool row_ok = my_pos < d.nq;
             const int my_last = min(d.pos + min(my_pos, d.nq - 1), d.last_key);  // (unused rows mask as the last used one)
-            float m = -INFINITY, l = 0.f, Rc = 1.f, qf = 0.f;
+            float m = -INFINITY, l = 0.f, qf = 0.f;
             if (d.nt > 0) {
                 wait(bars.q_full(items % kQSlots), (items / kQSlots) & 1);
                 qf = reinterpret_cast<const float*>(smem + kQf)[items % kQSlots * kTile + r];
@@ -636,7 +640,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int slot = t % kInfo;
                 wait(bars.info(slot), (t / kInfo) & 1);
                 const float4* kc = reinterpret_cast<const float4*>(smem + kConsts) + slot * 16 + x * 8;
-                const float R = reinterpret_cast<const float*>(smem + kR)[slot];
                 const uint2 vm = *reinterpret_cast<const uint2*>(mask + slot * 4 + x * 2);
                 // (all of this before the wait for S, which it does not need)
                 const int key0 = (d.t0 + j) * kTile + x * 64;
@@ -646,11 +649,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t w1 = vm.y & (vis >= 64 ? ~0u : vis > 32 ? (1u << (vis - 32)) - 1u : 0u);
                 const bool dense = __all_sync(0xffffffffu, (w0 & w1) == ~0u);
                 const bool first = j == 0;  // nothing in O yet
-                if (first) Rc = R;
                 // The weights are taken with the maximum so far.  Only when a row's 64 of them come to more than 2^9
-                // (which is how a larger score shows, without a pass for the maximum), when R has changed or at the
-                // item's first piece, the maximum is looked for, O brought to it, and the weights taken again.
-                bool look = first || R != Rc || __any_sync(0xffffffffu, m == -INFINITY);
+                // (which is how a larger one shows, without a pass for the maximum) or at the item's first piece, the
+                // maximum is looked for, O brought to it, and the weights taken again.
+                bool look = first || __any_sync(0xffffffffu, m == -INFINITY);
                 float4 k4[64 / kKeys];
 #pragma unroll
                 for (int b = 0; b < 64 / kKeys; ++b) {
@@ -658,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     k4[b].x = fmaxf(k4[b].x * qf, kTiny);
                 }
                 uint32_t pk[32];
-                float sum;
+                float sum, most;
                 wait(bars.s_full(sb), (piece / kPieces) & 1);
                 if (!ok) break;
                 tc_fence_after();
@@ -684,29 +686,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float u[2] = {s[b], s[b + 1]};
 #pragma unroll
                             for (int i = 2; i < kKeys; i += 2) u[i / 2 & 1] = fmax3(u[i / 2 & 1], s[b + i], s[b + i + 1]);
-                            mt = fmaxf(mt, fmaxf(u[0], u[1]) * k4[b / kKeys].x);
+                            mt = fmaxf(mt, fmaf(fmaxf(u[0], u[1]), k4[b / kKeys].x, k4[b / kKeys].y));
                         }
                         if (!first) {
                             // the products issued so far have to be done before O changes
                             wait(bars.pv_done((piece - 2) % kPieces), ((piece - 2) / kPieces) & 1);
                             tc_fence_after();
-                            const float alpha = mt == m ? 1.f : fast_exp2(m - mt), f = alpha * (Rc / R);
+                            const float alpha = mt == m ? 1.f : fast_exp2(m - mt);
 #pragma unroll 1
                             for (int q = 0; q < 8; ++q) {
                                 float o[16];
                                 tmem_ld16(t_o + q * 16, o);
                                 tmem_wait_ld();
 #pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] *= f;
+                                for (int i = 0; i < 16; ++i) o[i] *= alpha;
                                 tmem_st16(t_o + q * 16, o);
                             }
                             tmem_wait_st();
                             l *= alpha;
-                            Rc = R;
                         }
                         m = mt;
                     }
-                    sum = 0.f;
+                    sum = most = 0.f;
                     const float m_fin = m == -INFINITY ? 0.f : m;  // no key yet: every P' is 2^-inf
 #pragma unroll
                     for (int b = 0; b < 64; b += kKeys) {
@@ -723,10 +724,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         float u, v;
                         f32x2_unpack(add_f32x2(part[0], part[1]), u, v);
+                        most += u + v;
                         sum = fmaf(u + v, k4[b / kKeys].z, sum);
                     }
-                    // (at most 2^9, times the 64 that vs / R may reach, is below f16's largest number)
-                    if (look || !__any_sync(0xffffffffu, sum > kMost)) break;
+                    if (look || !__any_sync(0xffffffffu, most > kMost)) break;
                     look = true;
                 }
                 {
@@ -739,29 +740,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // ---- the item's output: both groups' states joined, each group stores 64 columns of the row
-            float mo = -INFINITY, lo = 0.f, Ro = 1.f;
+            float mo = -INFINITY, lo = 0.f;
             if (d.nt > 0) {
                 const uint32_t last = 2 * (g + d.nt - 1) + x;  // this group's last piece
                 wait(bars.pv_done(last % kPieces), (last / kPieces) & 1);
                 // (two copies by item: the other group may be an item behind)
-                float4* st = state + (items & 1) * 2 * kTile;
-                st[x * kTile + r] = make_float4(m, l, Rc, 0.f);
+                float2* st = state + (items & 1) * 2 * kTile;
+                st[x * kTile + r] = make_float2(m, l);
                 tc_fence_before();
                 if (!ok || !joined.sync()) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                const float4 o = st[(x ^ 1) * kTile + r];
+                const float2 o = st[(x ^ 1) * kTile + r];
                 mo = o.x;
                 lo = o.y;
-                Ro = o.z;
             }
             const float M = fmaxf(m, mo);
             // (the weight of a state without a valid key is 0, and its O is not looked at)
             const float w_own = m == -INFINITY ? 0.f : fast_exp2(m - M), w_oth = mo == -INFINITY ? 0.f : fast_exp2(mo - M);
             const float L = w_own * l + w_oth * lo, inv = L == 0.f ? 0.f : 1.f / L;
-            const float f_own = w_own * Rc * inv, f_oth = w_oth * Ro * inv;
+            const float f_own = w_own * inv, f_oth = w_oth * inv;
             const bool use_own = w_own != 0.f, use_oth = w_oth != 0.f;
             const size_t row = (size_t)(d.row + my_pos) * p.num_q_heads + d.kvh * G + (r - my_pos * G);
             const bool direct = d.spans == 1;
@@ -896,14 +896,11 @@ long long work_items(int num_chunks, int max_q_len, int num_kv_heads, int group)
 
 // Key tiles per span and spans per query tile.  Where the tiles alone leave SMs idle their keys are cut so that the
 // items make up one round of the GPU, into spans of at least two key tiles (a span's partial rows cost about one key
-// tile's time to store and join); where they make up less than two rounds and have 16 key tiles or more, in two, so
-// that the second round is shorter.  The count comes from the largest context, the lengths live on the device.
+// tile's time to store and join).  The count comes from the largest context, the lengths live on the device.
 Spans plan_spans(int num_chunks, int max_q_len, int num_kv_heads, int group, int max_context_len, int num_sms) {
     const int tiles = max_context_len > 0 ? (max_context_len - 1) / kTile + 1 : 1;
     const long long items = work_items(num_chunks, max_q_len, num_kv_heads, group);
-    long long want = 1;
-    if (items > 0 && items < num_sms) want = num_sms / items;
-    else if (items < 2LL * num_sms && tiles >= 16) want = 2;
+    long long want = items > 0 && items < num_sms ? num_sms / items : 1;
     if (want > tiles / 2) want = tiles / 2;
     Spans s;
     s.tiles = tiles;
@@ -943,9 +940,7 @@ int launch_prefill_fp8_block_tc(const PrefillParams& p, void* workspace, int num
     if (rc != PA_OK) return rc;
     if ((rc = pool_tensor_map_rows(&tmv, p.v_cache, p.num_blocks, p.block_size, p.num_kv_heads, kD, true)) != PA_OK)
         return rc;
-    auto kernel = p.block_size == 8    ? prefill_fp8_block_tc_kernel<8>
-                  : p.block_size == 16 ? prefill_fp8_block_tc_kernel<16>
-                                       : prefill_fp8_block_tc_kernel<32>;
+    auto kernel = p.block_size >= 32 ? prefill_fp8_block_tc_kernel<32> : prefill_fp8_block_tc_kernel<8>;
     if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), kSmemBytes)) != PA_OK) return rc;
     Spans s = plan_spans(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group, p.max_context_len, num_sms);
     if (s.count > 1) {

@@ -495,6 +495,44 @@ def test_scales_far_apart(B):
     _close(out, want[2:], mag[2:], floor[2:])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("B", [8, 16, 64])
+def test_larger_scales_elsewhere_cost_no_precision(B):
+    """V scales 2^30 above the others, in a block of little weight and in one that only the last query sees: an output's
+    floor is 2^-22 of the largest p_j vs_j among the keys that it sees (see above: the weights are relative to it)."""
+    rng = np.random.default_rng(70 + B)
+    n, Hq, Q, scale = 5 * 64 + 1, 4, 66, 2.0 ** -5
+    table, P = _tables(rng, [n], B)
+    codes, scales = zip(_pools(rng, P, B, 1, 128), _pools(rng, P, B, 1, 128))
+    scales[0][:] = 2.0 ** -3
+    scales[1][table[0, 1], 0] = scales[1][table[0, (n - 1) // B], 0] = 2.0 ** 30
+    codes[0][table[0, 1]] = 0xb8  # -1: scores of about -50, for the queries are positive
+    scales[0][table[0, 1]] = 16.0
+    q = _bf16(rng, (Q, Hq, 128)).abs()
+    q[-1] = 0  # every weight alike
+    pools = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (*codes, *scales)]
+    K, V = (R.E4M3[c[table[0]].reshape(-1, 128)] * np.repeat(s[table[0], 0].astype(np.float64), B)[:, None]
+            for c, s in zip(codes, scales))
+    vs, code = np.repeat(scales[1][table[0], 0].astype(np.float64), B), np.abs(R.E4M3[codes[1][table[0]].reshape(-1, 128)])
+    want, mag, floor = (np.zeros((Q, Hq, 128)) for _ in range(3))
+    for i in range(Q):
+        N = n - Q + 1 + i
+        x = q[i].double().numpy() @ K[:N].T * scale
+        w = np.exp(x - x.max(axis=1, keepdims=True))
+        w /= w.sum(axis=1, keepdims=True)
+        want[i], mag[i] = w @ V[:N], w @ np.abs(V[:N])
+        floor[i] = (w * vs[:N]).max(axis=1)[:, None] * code[:N].sum(axis=0)
+    assert floor[-2].max() < 2.0 ** 13, "the block of little weight has some after all"
+    ws = pa.new_prefill_fp8_block_workspace(1, Q, Q, Hq, 1, 128, B, n)
+    out = pa.pa_prefill_chunk_fp8_block(q.cuda(), _i32([0, Q]), _i32([n - Q]), _i32([0]), Q, *pools, _i32(table), _i32([n]),
+                                        n, scale, ws)
+    _close(out, want, mag, floor)
+    for L, i in ((n - 1, Q - 2), (n, Q - 1)):
+        ws = pa.new_decode_fp8_block_workspace(1, Hq, 1, 128, B, n)
+        out = pa.pa_decode_fp8_block(q[i:i + 1].cuda(), *pools, _i32(table), _i32([L]), n, scale, ws)
+        _close(out, want[i:i + 1], mag[i:i + 1], floor[i:i + 1])
+
+
 # ---------------------------------------------------------------- GPU: together
 @pytest.mark.gpu
 def test_write_then_prefill_then_decode_then_read():
