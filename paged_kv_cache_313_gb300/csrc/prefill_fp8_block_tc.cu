@@ -251,9 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kKWarp || warp == kVWarp) {
         // ============================================================ producers
-        const bool v_side = warp == kVWarp;
         const int bpt = kTile >> log2b, tpc = 32 / bpt;  // blocks per tile, tiles per 32-entry chunk of the table
-        if (lane == 0) tma_prefetch_desc(v_side ? &tmv : &tmk);
+        if (lane == 0) tma_prefetch_desc(warp == kVWarp ? &tmv : &tmk);
         // The V warp describes the items.  (query tile rank, chunk, kv head, span), the latest tile of every chunk
         // first; CTA b takes one of every pass of gridDim.x items, in serpentine order, so that heavy and light ones
         // pair up.  It stays an item ahead of its own copies: when every warp described its items itself, that took
@@ -312,107 +311,109 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             ++published;
         };
-        uint32_t g = 0, items = 0;  // key tiles and items so far
-        Item d{}, ahead{};
-        if (v_side) publish(ahead);
-        for (; ok; ++items) {
-            if (v_side) {
-                d = ahead;
-                if (d.nt < 0) break;
-                publish(ahead);
-            } else if (!take_item(items, d)) {
-                break;
-            }
-            const int first = d.t0 * bpt;  // first block
-            const int nblk = min((d.last_key + B) >> log2b, (d.t0 + d.nt) * bpt) - first;
-            const int32_t* table = p.block_tables + (size_t)d.s * p.max_blocks_per_seq + first;
-            auto load_raw = [&](int chunk) {
-                const int i = chunk * 32 + lane;
-                return i < nblk ? table[i] : -1;
-            };
-            auto load_scales = [&](int pb) {
-                if (v_side || pb < 0 || pb >= p.num_blocks) return make_float2(0.f, 0.f);
-                const size_t i = (size_t)pb * Hkv + d.kvh;
-                return make_float2(__ldg(p.k_scales + i), __ldg(p.v_scales + i));
-            };
-            int raw = d.nt > 0 ? load_raw(0) : -1, raw_next = -1, pb = -1;
-            float2 sc = load_scales(raw), sc_next = make_float2(0.f, 0.f);
-            uint32_t valid = 0;                       // the chunk's blocks with a valid table entry
-            float ks = 0.f, off = 0.f, inv_vs = 0.f;  // of this lane's block: what the softmax needs of it
-            float top = 0.f;                          // the largest V scale of the item so far
-            for (int j = 0, chunk = 0, l = 0; j < d.nt; ++j, ++g) {
-                if (l == 0) {
-                    if (chunk > 0) {
-                        raw = raw_next;
-                        sc = sc_next;
-                    }
-                    pb = raw;
-                    if (chunk * 32 + lane < nblk && (raw < 0 || raw >= p.num_blocks)) {
-                        if (!v_side) count_error(p.error_count);
-                        pb = -1;
-                    }
-                    valid = __ballot_sync(0xffffffffu, pb >= 0);
-                    if (!v_side) {
-                        top = fmaxf(top, redux_max(sc.y));
-                        ks = sc.x * fabsf(p.scale_log2);
-                        off = __log2f(fmaxf(sc.y, fmaxf(top * kHold, kLeastScale)));
-                        inv_vs = fast_exp2(-off);
-                    }
-                }
-                const uint32_t all = (1u << bpt) - 1u, mine = (valid >> (l * bpt)) & all;
-                const int stages = v_side ? kVStages : kKStages, st = v_side ? g % kVStages : g % kKStages;
-                const int round = v_side ? g / kVStages : g / kKStages;
-                uint64_t* full = v_side ? bars.v_full(st) : bars.k_full(st);
-                if (g >= (uint32_t)stages && !mbar_wait_warp(v_side ? bars.v_empty(st) : bars.k_empty(st), (round - 1) & 1)) {
-                    ok = false;
+        // A tile of 16-token blocks is eight copies of about 75 cycles each to issue, so what else a warp does for it
+        // counts (factors and ring indices worked out for every tile anew took 2.9k cycles a tile, longer than the
+        // products).  One body for both sides: the warps share an instruction cache, and a body each, shorter as it was,
+        // cost 4 %.
+        {
+            const bool v_side = warp == kVWarp;
+            const uint32_t stages = v_side ? kVStages : kKStages;
+            const CUtensorMap* map = v_side ? &tmv : &tmk;
+            const uint32_t all = (1u << bpt) - 1u;
+            uint64_t *const fulls = v_side ? bars.v_full(0) : bars.k_full(0), *const empties = v_side ? bars.v_empty(0) : bars.k_empty(0);
+            uint32_t* const masks = v_side ? reinterpret_cast<uint32_t*>(smem + kVMask) : mask;
+            const int my_blk = ((lane & 15) * 8) >> log2b;  // block, in its tile, of this lane's group of 8 keys
+            uint8_t* my_dst = smem + (v_side ? kV : kK) + (lane << log2b) * kD;
+            uint32_t g = 0, items = 0, st = 0, round = 0;  // key tiles and items so far; the ring's stage and its round
+            Item d{}, ahead{};  // (the V warp's first has no tiles, so that there is one place to publish from)
+            for (; ok; ++items) {
+                if (v_side) {
+                    d = ahead;
+                    if (d.nt < 0) break;
+                    publish(ahead);
+                } else if (!take_item(items, d)) {
                     break;
                 }
-                const int slot = g % kInfo;
-                const int keys = d.last_key + 1 - (d.t0 + j) * kTile;  // of this tile
-                if (lane < 4) {  // key-validity mask: 32 keys a word
-                    uint32_t m = ~0u;
-                    if (mine != all || keys < kTile) {
-                        const int left = keys - 32 * lane;
-                        m = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
-                        if (B >= 32) {
-                            if (!((mine >> ((32 * lane) >> log2b)) & 1u)) m = 0u;
-                        } else {
-                            const int per = 32 >> log2b;
-                            for (int b = 0; b < per; ++b)
-                                if (!((mine >> (lane * per + b)) & 1u)) m &= ~(((1u << B) - 1u) << (b * B));
+                const int first = d.t0 * bpt;  // first block
+                const int nblk = min((d.last_key + B) >> log2b, (d.t0 + d.nt) * bpt) - first;
+                const int32_t* table = p.block_tables + (size_t)d.s * p.max_blocks_per_seq + first;
+                auto load_raw = [&](int chunk) {
+                    const int i = chunk * 32 + lane;
+                    return i < nblk ? table[i] : -1;
+                };
+                auto load_scales = [&](int pb) {
+                    if (v_side || pb < 0 || pb >= p.num_blocks) return make_float2(0.f, 0.f);
+                    const size_t i = (size_t)pb * Hkv + d.kvh;
+                    return make_float2(__ldg(p.k_scales + i), __ldg(p.v_scales + i));
+                };
+                int raw = d.nt > 0 ? load_raw(0) : -1, token = -1;  // table entry of this lane's block, its first token
+                float2 sc = load_scales(raw);
+                uint32_t valid = 0;                       // the chunk's blocks with a valid table entry
+                float ks = 0.f, off = 0.f, inv_vs = 0.f;  // of this lane's block: what the softmax needs of it
+                float top = 0.f;                          // the largest V scale of the item so far
+                int keys = d.last_key + 1 - d.t0 * kTile;  // visible from this tile on
+                for (int j = 0, chunk = 0, l = 0; j < d.nt; ++j, ++g, keys -= kTile) {
+                    if (l == 0) {
+                        const bool valid_raw = raw >= 0 && raw < p.num_blocks;
+                        if (!v_side && !valid_raw && chunk * 32 + lane < nblk) count_error(p.error_count);
+                        token = valid_raw ? raw << log2b : -1;
+                        valid = __ballot_sync(0xffffffffu, valid_raw);
+                        if (!v_side) {
+                            top = fmaxf(top, redux_max(sc.y));
+                            ks = sc.x * fabsf(p.scale_log2);
+                            off = __log2f(fmaxf(sc.y, fmaxf(top * kHold, kLeastScale)));
+                            inv_vs = fast_exp2(-off);
                         }
                     }
-                    if (v_side) reinterpret_cast<uint32_t*>(smem + kVMask)[st * 4 + lane] = m;
-                    else mask[slot * 4 + lane] = m;
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)__popc(mine) * B * kD);
-                __syncwarp();  // armed before any copy is issued
-                const int src = l * bpt + (lane < bpt ? lane : 0);
-                const int my_pb = __shfl_sync(0xffffffffu, pb, src);
-                if (lane < bpt && my_pb >= 0)
-                    tma_load_3d(smem + (v_side ? kV : kK) + st * kCodes + lane * B * kD, v_side ? &tmv : &tmk, 0,
-                                my_pb * B, d.kvh, full);
-                if (!v_side) {
-                    // what the softmax needs of this tile's 16 groups of 8 keys
-                    const int blk = l * bpt + (((lane & 15) * 8) >> log2b);  // block of this lane's group
-                    const float a = __shfl_sync(0xffffffffu, ks, blk), o = __shfl_sync(0xffffffffu, off, blk);
-                    const float z = __shfl_sync(0xffffffffu, inv_vs, blk);
-                    if (lane < 16) reinterpret_cast<float4*>(smem + kConsts)[slot * 16 + lane] = make_float4(a, o, z, 0.f);
+                    const uint32_t mine = (valid >> (l * bpt)) & all;
+                    uint64_t* full = fulls + st;
+                    if (round > 0 && !mbar_wait_warp(empties + st, (round - 1) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    const int slot = g % kInfo;
+                    if (lane < 4) {  // key-validity mask: 32 keys a word
+                        uint32_t m = ~0u;
+                        if (mine != all || keys < kTile) {
+                            const int left = keys - 32 * lane;
+                            m = left >= 32 ? ~0u : left > 0 ? (1u << left) - 1u : 0u;
+                            if (B >= 32) {
+                                if (!((mine >> ((32 * lane) >> log2b)) & 1u)) m = 0u;
+                            } else {
+                                const int per = 32 >> log2b;
+                                for (int b = 0; b < per; ++b)
+                                    if (!((mine >> (lane * per + b)) & 1u)) m &= ~(((1u << B) - 1u) << (b * B));
+                            }
+                        }
+                        masks[(v_side ? st : slot) * 4 + lane] = m;
+                    }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bars.info(slot));
+                    if (lane == 0) mbar_arrive_expect_tx(full, (uint32_t)__popc(mine) << (log2b + 7));
+                    const int my_token = __shfl_sync(0xffffffffu, token, l * bpt + lane);
+                    __syncwarp();  // armed before any copy is issued
+                    if (lane < bpt && my_token >= 0) tma_load_3d(my_dst + st * kCodes, map, 0, my_token, d.kvh, full);
+                    if (!v_side) {
+                        // what the softmax needs of this tile's 16 groups of 8 keys
+                        const int blk = l * bpt + my_blk;
+                        const float a = __shfl_sync(0xffffffffu, ks, blk), o = __shfl_sync(0xffffffffu, off, blk);
+                        const float z = __shfl_sync(0xffffffffu, inv_vs, blk);
+                        if (lane < 16) reinterpret_cast<float4*>(smem + kConsts)[slot * 16 + lane] = make_float4(a, o, z, 0.f);
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bars.info(slot));
+                    }
+                    if (++st == stages) st = 0, ++round;
+                    // the next chunk's entries, at the end of this one's first tile, and their scales a tile later
+                    if (l == 0) raw = load_raw(chunk + 1);
+                    if (l == 1) sc = load_scales(raw);  // (a chunk has two tiles at least)
+                    if (++l == tpc) l = 0, ++chunk;
                 }
-                if (l == 0) raw_next = load_raw(chunk + 1);
-                if (l == 1) sc_next = load_scales(raw_next);
-                if (++l == tpc) l = 0, ++chunk;
             }
+            if (lane == 0) {
+                if (!ok) count_error(p.error_count);
+                if (!drain_ring(fulls, stages, g)) count_error(p.error_count);
+            }
+            __syncwarp();
         }
-        if (lane == 0) {
-            if (!ok) count_error(p.error_count);
-            if (!drain_ring(v_side ? bars.v_full(0) : bars.k_full(0), v_side ? kVStages : kKStages, g))
-                count_error(p.error_count);
-        }
-        __syncwarp();
     } else if (warp == kMmaWarp || warp == kSWarp) {
         // ============================================================ MMA issuers
         // Warp kSWarp issues every piece's S = Q K^T, warp kMmaWarp every piece's O += P V: one warp doing both in
