@@ -21,7 +21,10 @@
 // Finding a block's tokens:
 //   * up to kScanTokens tokens (decode steps): one launch, a CTA per token;
 //     every CTA resolves all tokens itself and only the first token of each
-//     block goes on.  No workspace, no second launch.
+//     block goes on.  No workspace, no second launch.  (8 heads of 128, blocks
+//     of 16, this form / the other: 64 tokens of as many sequences 4.3 / 7.0 us,
+//     512 8.5 / 11.2, 1024 14.9 / 17.3, 2048 34.0 / 27.7; one chunk of 512
+//     tokens 7.3 / 7.5, of 1024 10.5 / 8.3.)
 //   * more tokens: a first launch resolves each token once, records it as its
 //     slot's writer (atomicMax, so of several tokens naming one slot the last
 //     is stored, as in the one-launch form) and lists each block once; a second
@@ -29,6 +32,10 @@
 //     among them.  It leaves the workspace zeroed again.
 //
 // Bound: HBM for long calls, launch and memory latency for a decode step.
+// Measured (8 heads of 128, blocks of 16): four prompts of 2048 tokens 18.8 us
+// (50.5 MB: 0.40 of the copy bandwidth, the two launches and their dependent
+// loads being about half of it); 256 decode tokens and 4 x 512 over blocks of 32
+// 14.8 us.  Read back of 89,556 tokens to bf16 88.6 us, 551 MB: 0.92.
 #include "pa_internal.cuh"
 
 namespace pa {
@@ -386,7 +393,8 @@ int launch_write_fp8_block(const void* k_new, const void* v_new, int num_tokens,
     const int slices = (2 * num_kv_heads + kWarps - 1) / kWarps, gy = slices < 64 ? slices : 64;
     if (num_tokens <= kScanTokens) {
         auto kernel = head_dim == 128 ? write_scan_kernel<16> : head_dim == 64 ? write_scan_kernel<8> : write_scan_kernel<0>;
-        // every slice scans the tokens again: worth it while the tokens alone leave SMs idle
+        // every slice scans the tokens again: worth it while the tokens alone leave SMs idle (in slices / in one: 64
+        // tokens 4.3 / 5.2 us, 256 5.4 / 7.4, 512 9.5 / 8.4, 1024 18.6 / 14.9)
         return launch_kernel(kernel, dim3(num_tokens, num_tokens < 2 * num_sms ? gy : 1), dim3(kThreads), 0, stream, p);
     }
     const WriteWorkspace w = write_workspace(num_tokens, num_blocks, block_size);

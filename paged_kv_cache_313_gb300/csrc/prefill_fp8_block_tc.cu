@@ -43,6 +43,13 @@
 //   warps 8-11  V widening, query terms         warp 14  V tiles
 //   warp 12     tensor memory, issue of P V     warp 15  issue of Q K^T
 // Waits are bounded, copies and MMAs drained, as in prefill_tc.cu.
+//
+// Bound: the softmax warps' issue and the hand-overs between the warps (the two
+// products are 1.05k cycles of a key tile's 2.2k).  Measured: 2048 queries at
+// position 5,916, 64/8 heads, 415 us over 64-token blocks (466 GFLOP: 1.12
+// PFLOP/s, 0.58 of cuBLAS bf16) and 432 over 16-token blocks, whose copies are
+// four times as many; four chunks of 512 queries at short offsets, 32/8 heads,
+// 34.6 us; 37 queries at 2,955 17.4 us.  On the CUDA cores 184, 5.0 and 1.3 ms.
 #include "pa_internal.cuh"
 #include "sm100_ptx.cuh"
 
@@ -190,8 +197,9 @@ __device__ __forceinline__ int key_cap(const PrefillParams& p, int s) {
     return (int)min(min((long long)p.context_lens[s], (long long)p.max_context_len), table);
 }
 
-// kKeys: keys that share a block, and so their factors, as far as the softmax goes by it: 8, 16 or 32 (the block size up
-// to 32).  Fewer factors are fewer instructions of the loop that sets the pace.
+// kKeys: keys that share a block, and so their factors, as far as the softmax goes by it: 32 where blocks have so many,
+// else 8.  (64-token blocks with 32 / 8: 2048 queries at 5,916 416 / 441 us, four chunks of 512 33.2 / 35.5; an own
+// variant for 16-token blocks was no faster than 8.)
 template <int kKeys>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_fp8_block_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -895,9 +903,10 @@ long long work_items(int num_chunks, int max_q_len, int num_kv_heads, int group)
     return (long long)((max_q_len + ppt - 1) / ppt) * num_chunks * num_kv_heads;
 }
 
-// Key tiles per span and spans per query tile.  Where the tiles alone leave SMs idle their keys are cut so that the
-// items make up one round of the GPU, into spans of at least two key tiles (a span's partial rows cost about one key
-// tile's time to store and join).  The count comes from the largest context, the lengths live on the device.
+// Key tiles per span and spans per query tile.  Where the tiles alone leave half of the SMs idle their keys are cut so
+// that the items make up one round of the GPU, into spans of at least two key tiles (a span's partial rows cost about
+// one key tile's time to store and join): 37 queries at 2,955, 8 kv heads, 17.4 us, uncut 36.2; but 160 query tiles of
+// 21 key tiles cut in two 64.9, uncut 51.8.  The count comes from the largest context, the lengths live on the device.
 Spans plan_spans(int num_chunks, int max_q_len, int num_kv_heads, int group, int max_context_len, int num_sms) {
     const int tiles = max_context_len > 0 ? (max_context_len - 1) / kTile + 1 : 1;
     const long long items = work_items(num_chunks, max_q_len, num_kv_heads, group);
