@@ -408,10 +408,10 @@ int launch_write_fp8_block(const void* k_new, const void* v_new, int num_tokens,
                                  stream, p);
     if (rc != PA_OK) return rc;
     const long long most = ((long long)(num_tokens < num_blocks ? num_tokens : num_blocks) * 2 * num_kv_heads + kWarps - 1) / kWarps;
-    const int fill = 4 * num_sms;  // CTAs that fit the GPU
+    const long long fill = 4LL * num_sms, ctas = most < 1 ? 1 : most < fill ? most : fill;  // (fill: CTAs that fit the GPU)
     auto kernel =
         head_dim == 128 ? write_listed_kernel<16> : head_dim == 64 ? write_listed_kernel<8> : write_listed_kernel<0>;
-    return launch_kernel(kernel, dim3((unsigned)(most < fill ? most : fill)), dim3(kThreads), 0, stream, p);
+    return launch_kernel(kernel, dim3((unsigned)ctas), dim3(kThreads), 0, stream, p);
 }
 
 int launch_read_fp8_block(void* k_out, void* v_out, int num_tokens, int num_kv_heads, int head_dim, int dtype,

@@ -227,6 +227,26 @@ def test_write_same_slot_last_token_is_stored(T):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T", [5, 1500])
+def test_write_to_a_pool_without_blocks_counts_every_token(lib, T):
+    """No block to store into: every token is counted and skipped, in both forms of the call."""
+    H, D, B = 2, 64, 16
+    x = torch.ones(T, H, D, dtype=BF, device="cuda")
+    pool, sc = torch.full((B * H * D,), 7, dtype=torch.uint8, device="cuda"), torch.ones(H, device="cuda")
+    bt, seq, pos = _i32([[0] * 200]), _i32([0] * T), _i32(range(T))
+    need = lib.pa_write_fp8_block_workspace_size(T, 0, B)
+    ws = torch.zeros(max(need, 256), dtype=torch.uint8, device="cuda")
+    err, slots = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(T, dtype=torch.int64, device="cuda")
+    ptr = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    for _ in range(2):
+        assert lib.pa_write_kv_paged_fp8_block(
+            ptr(x), ptr(x), T, H, D, ptr(pool), ptr(pool), ptr(sc), ptr(sc), 0, B, ptr(bt), 1, 200, ptr(seq), ptr(pos),
+            ptr(slots), ptr(ws), need, ptr(err), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)) == pa.PA_OK
+    assert int(err.item()) == 2 * T and bool((slots == -1).all()) and bool((pool == 7).all())
+    assert int(torch.count_nonzero(ws)) == 0
+
+
+@pytest.mark.gpu
 def test_write_special_values():
     """Zeros, infinities, NaN, subnormals and the largest numbers; a block of zeros only; scales of 0 and old scales
     that are no power of two."""
