@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(kFmaThreads) decode_fp8_block_fma_kernel(Decod
     for (int it = 0; it < S::kItems; ++it) {
         const int idx = threadIdx.x + it * kFmaThreads;
         if (idx >= G * D) continue;
-        const float l = l_s[idx / D], o = l > 0.f ? acc[it] / l : 0.f;
+        const float l = l_s[idx / D], o = l == 0.f ? 0.f : acc[it] / l;
         if (nsplit == 1) static_cast<Bf16*>(p.out)[row + idx] = from_float<Bf16>(o);
         else p.ws_o[slot * G * D + idx] = o;
     }
@@ -63,11 +63,8 @@ __global__ void __launch_bounds__(kFmaThreads) prefill_fp8_block_fma_kernel(Pref
     if (i >= n) return;
     const int cap = (int)min(min((long long)p.context_lens[s], (long long)p.max_context_len),
                              (long long)p.max_blocks_per_seq * p.block_size);
-    int L = start + i + 1;  // causal: keys 0..start+i
-    if (L > cap) {
-        if (threadIdx.x == 0 && kvh == 0) count_error(p.error_count);
-        L = cap;
-    }
+    if ((long long)start + i + 1 > cap && threadIdx.x == 0 && kvh == 0) count_error(p.error_count);
+    const int L = (int)min((long long)start + i + 1, (long long)cap);  // causal: keys 0..start+i
     extern __shared__ float smem[];
     __shared__ float m_s[kFmaMaxGroup], l_s[kFmaMaxGroup], alpha_s[kFmaMaxGroup];
     float acc[S::kItems];
@@ -82,7 +79,7 @@ __global__ void __launch_bounds__(kFmaThreads) prefill_fp8_block_fma_kernel(Pref
         const int idx = threadIdx.x + it * kFmaThreads;
         if (idx >= G * D) continue;
         const float l = l_s[idx / D];
-        static_cast<Bf16*>(p.out)[row + idx] = from_float<Bf16>(l > 0.f ? acc[it] / l : 0.f);
+        static_cast<Bf16*>(p.out)[row + idx] = from_float<Bf16>(l == 0.f ? 0.f : acc[it] / l);
     }
 }
 

@@ -403,7 +403,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                         const uint32_t m2 = __vmaxu2(x.x & 0x7FFF7FFFu, x.y & 0x7FFF7FFFu);
                         const uint32_t am = __reduce_max_sync(0xffffffffu, max(m2 & 0xFFFFu, m2 >> 16));
                         const int e = min(134 - (int)(am >> 7), 126);  // |x| 2^e in [128, 256)
-                        const float f = __uint_as_float((uint32_t)(e + 127) << 23);
+                        // (a row with an infinity or a NaN becomes NaN: the conversion would hold an infinity at 448)
+                        const float f = am >= 0x7F80u ? NAN : __uint_as_float((uint32_t)(e + 127) << 23);
                         float v[4] = {__uint_as_float(x.x << 16) * f, __uint_as_float(x.x & 0xFFFF0000u) * f,
                                       __uint_as_float(x.y << 16) * f, __uint_as_float(x.y & 0xFFFF0000u) * f};
                         uint32_t hi = 0, lo = 0;

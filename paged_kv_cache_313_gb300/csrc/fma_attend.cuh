@@ -131,7 +131,9 @@ __device__ void fma_attend(const T* __restrict__ q, int G, const TP* __restrict_
             const float m_new = fmaxf(m_old, mx);
             float sum = 0.f;
             for (int t = lane; t < n; t += 32) {
-                float e = m_new == -INFINITY ? 0.f : exp2f(p_s[g * kFmaSub + t] - m_new);
+                const float x = p_s[g * kFmaSub + t];
+                // (scores that are all NaN leave the maximum at -inf: with scaled pools they still count, and make NaN)
+                float e = (kScaled ? x : m_new) == -INFINITY ? 0.f : exp2f(x - m_new);
                 sum += e;
                 if (kScaled) {
                     const int pb = blk_s[(c0 + t) / B - lb0];

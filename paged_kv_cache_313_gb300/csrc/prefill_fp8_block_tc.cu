@@ -495,9 +495,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < kD / 8; ++k)
                 m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(x[k].x & 0x7FFF7FFFu, x[k].y & 0x7FFF7FFFu),
                                            __vmaxu2(x[k].z & 0x7FFF7FFFu, x[k].w & 0x7FFF7FFFu)));
-            const int e = min(134 - (int)(max(m2 & 0xFFFFu, m2 >> 16) >> 7), 126);  // |x| 2^e in [128, 256)
-            // a negative softmax scale negates the queries, so that scores only meet positive factors
-            const float f = copysignf(__uint_as_float((uint32_t)(e + 127) << 23), p.scale_log2);
+            const uint32_t am = max(m2 & 0xFFFFu, m2 >> 16);
+            const int e = min(134 - (int)(am >> 7), 126);  // |x| 2^e in [128, 256)
+            // a negative softmax scale negates the queries, so that scores only meet positive factors; a row with an
+            // infinity or a NaN becomes NaN (the conversion would hold an infinity at 448)
+            const float f = am >= 0x7F80u ? NAN : copysignf(__uint_as_float((uint32_t)(e + 127) << 23), p.scale_log2);
             uint8_t* row = smem + kQ + r * kD;
 #pragma unroll
             for (int k = 0; k < kD / 16; ++k) {
@@ -767,8 +769,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 lo = o.y;
             }
             const float M = fmaxf(m, mo);
-            // (the weight of a state without a valid key is 0, and its O is not looked at)
-            const float w_own = m == -INFINITY ? 0.f : fast_exp2(m - M), w_oth = mo == -INFINITY ? 0.f : fast_exp2(mo - M);
+            // (the weight of a state without a valid key is 0, and its O is not looked at; that of a state of NaN scores,
+            // which no maximum takes up, is NaN)
+            const float w_own = m == -INFINITY && l == 0.f ? 0.f : fast_exp2(m - M);
+            const float w_oth = mo == -INFINITY && lo == 0.f ? 0.f : fast_exp2(mo - M);
             const float L = w_own * l + w_oth * lo, inv = L == 0.f ? 0.f : 1.f / L;
             const float f_own = w_own * inv, f_oth = w_oth * inv;
             const bool use_own = w_own != 0.f, use_oth = w_oth != 0.f;

@@ -553,6 +553,37 @@ def test_larger_scales_elsewhere_cost_no_precision(B):
         _close(out, want[i:i + 1], mag[i:i + 1], floor[i:i + 1])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hq,D", [(4, 128), (4, 64), (12, 128)])
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+def test_queries_that_are_not_finite_give_nan(Hq, D, value):
+    """The softmax of scores that are infinite or NaN is NaN: for that query and head, and for no other."""
+    rng = np.random.default_rng(80 + Hq)
+    n, Q, B = 300, 5, 16
+    table, P = _tables(rng, [n], B)
+    codes, scales = zip(_pools(rng, P, B, 1, D), _pools(rng, P, B, 1, D))
+    pools = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (*codes, *scales)]
+    q = _bf16(rng, (Q, Hq, D))
+    limits = [n - Q + 1 + i for i in range(Q)]
+    s64 = [s.astype(np.float64) for s in scales]
+    want, mag = R.attend_rows(q.double().numpy(), codes[0], s64[0], codes[1], s64[1], table[0], limits, 0.1)
+    floor = R.floor_rows(codes[1], s64[1], table[0], limits, Hq)
+    q[1, 2, 17] = q[4, 0, D - 1] = value
+    hit = np.zeros((Q, Hq), bool)
+    hit[1, 2] = hit[4, 0] = True
+    for spans in (True, False):  # a limit of one key tile leaves nothing to cut
+        mx = 4096 if spans else n
+        ws = pa.new_prefill_fp8_block_workspace(1, Q, Q, Hq, 1, D, B, mx)
+        out = pa.pa_prefill_chunk_fp8_block(q.cuda(), _i32([0, Q]), _i32([n - Q]), _i32([0]), Q, *pools, _i32(table), _i32([n]),
+                                            mx, 0.1, ws)
+        assert bool(torch.isnan(out.cpu()[hit]).all())
+        _close(out.cpu()[~hit], want[~hit], mag[~hit], floor[~hit])
+    ws = pa.new_decode_fp8_block_workspace(1, Hq, 1, D, B, n)
+    out = pa.pa_decode_fp8_block(q[4:].cuda(), *pools, _i32(table), _i32([n]), n, 0.1, ws)
+    assert bool(torch.isnan(out.cpu()[hit[4:]]).all())
+    _close(out.cpu()[~hit[4:]], want[4:][~hit[4:]], mag[4:][~hit[4:]], floor[4:][~hit[4:]])
+
+
 # ---------------------------------------------------------------- GPU: together
 @pytest.mark.gpu
 def test_write_then_prefill_then_decode_then_read():
