@@ -50,6 +50,8 @@
 // PFLOP/s, 0.58 of cuBLAS bf16) and 432 over 16-token blocks, whose copies are
 // four times as many; four chunks of 512 queries at short offsets, 32/8 heads,
 // 34.6 us; 37 queries at 2,955 17.4 us.  On the CUDA cores 184, 5.0 and 1.3 ms.
+#include <climits>
+
 #include "pa_internal.cuh"
 #include "sm100_ptx.cuh"
 
@@ -67,6 +69,7 @@ constexpr int kKStages = 4, kVStages = 3, kVhStages = 2, kInfo = 8;
 // query factors, and the phase of its barrier, until the softmax has come to it.
 constexpr int kQSlots = 4;
 constexpr int kPieces = 3;  // ring of S pieces
+constexpr int kNanSlots = 8;  // a slot is reset two items before its own, when the softmax is past its last use
 constexpr int kItems = 8;   // ring of item descriptions
 // tensor memory columns: O of group 0 and 1, the query terms (hi, lo; four codes a column), the S pieces
 constexpr uint32_t kTO = 0, kTQ = 256, kTS = 320;
@@ -86,7 +89,8 @@ constexpr int kMask = kConsts + kInfo * 16 * 16;           // uint32 [kInfo][4]
 constexpr int kVMask = kMask + kInfo * 16;                 // uint32 [kVStages][4]: the same for the converters
 constexpr int kQf = kVMask + kVStages * 16;                // float [kQSlots][128]
 constexpr int kState = kQf + kQSlots * kTile * 4;          // float2 [2 items][2 groups][128]: m, l
-constexpr int kItem = kState + 2 * 2 * kTile * 8;          // Item [kItems]
+constexpr int kNan = kState + 2 * 2 * kTile * 8;           // int [kNanSlots][kD + 1]: see clear_nans
+constexpr int kItem = (kNan + kNanSlots * (kD + 1) * 4 + 15) / 16 * 16;  // Item [kItems]
 constexpr int kBars = kItem + kItems * 48;
 constexpr int kNumBars = 2 * kKStages + 2 * kVStages + kVhStages + 3 * kPieces + kQSlots + 1 + kInfo + 2 * kItems + 3;
 constexpr int kTmemSlot = kBars + kNumBars * 8;
@@ -197,9 +201,9 @@ __device__ __forceinline__ int key_cap(const PrefillParams& p, int s) {
     return (int)min(min((long long)p.context_lens[s], (long long)p.max_context_len), table);
 }
 
-// kKeys: keys that share a block, and so their factors, as far as the softmax goes by it: 32 where blocks have so many,
-// else 8.  (64-token blocks with 32 / 8: 2048 queries at 5,916 416 / 441 us, four chunks of 512 33.2 / 35.5; an own
-// variant for 16-token blocks was no faster than 8.)
+// kKeys: keys that share a block, and so their factors, as far as the softmax goes by it: 8, 16 or 32 (the block size up
+// to 32).  (2048 queries at 5,916 over 64-token blocks with 32 / 8: 390 / 405 us; over 16-token blocks with 16 / 8: 419 /
+// 438.)
 template <int kKeys>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_fp8_block_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -230,6 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         fence_mbar_init();
     }
+    for (int i = threadIdx.x; i < kNanSlots * (kD + 1); i += kThreads) reinterpret_cast<int*>(smem + kNan)[i] = INT_MAX;
     pdl_trigger();
     pdl_wait();
     if (warp == kMmaWarp) {
@@ -255,7 +260,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     // Registers: 128 a thread at launch (512 threads take all of the SM's).  The softmax warps get 152 of them, for 64
-    // scores and what becomes of them, the converters keep 120, the others 88: 2 * 152 + 120 + 88 = 4 * 128.
+    // scores and what becomes of them, the converters keep 120, the others 88: 2 * 152 + 120 + 88 = 4 * 128.  No role may
+    // spill: eight bytes spilled in the softmax took the long chunk from 387 to 416 us.
     if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kKWarp || warp == kVWarp) {
         // ============================================================ producers
@@ -484,6 +490,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // scaling.  In f16, which holds a scaled bf16 exactly down to 2^-24.
         auto stage_q = [&](const Item& d, uint32_t item) {
             const int r = w * 32 + lane, pos = r * inv_g >> 16;
+            // (a converter is less than two key tiles, so two items, ahead of another: no one has written there yet)
+            int* nan = reinterpret_cast<int*>(smem + kNan) + (item + 2) % kNanSlots * (kD + 1);
+            nan[r] = INT_MAX;
+            if (r == 0) nan[kD] = INT_MAX;
             const uint4* src = reinterpret_cast<const uint4*>(
                 static_cast<const __nv_bfloat16*>(p.q) +
                 ((size_t)(d.row + pos) * p.num_q_heads + d.kvh * G + (r - pos * G)) * kD);
@@ -503,6 +513,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint8_t* row = smem + kQ + r * kD;
 #pragma unroll
             for (int k = 0; k < kD / 16; ++k) {
+                if (k == kD / 32) {
+                    // (the second half of the row is loaded again, so that it need not be kept in registers meanwhile)
+                    if (pos < d.nq) {
+#pragma unroll
+                        for (int k = kD / 16; k < kD / 8; ++k)
+                            asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                         : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w)
+                                         : "l"(src + k));
+                    }
+                }
                 const uint32_t in[8] = {x[2 * k].x,     x[2 * k].y,     x[2 * k].z,     x[2 * k].w,
                                         x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
                 uint32_t hi[4], lo[4];
@@ -553,6 +573,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.q_full(item % kQSlots));
         };
+        // NaN codes in a tile whose keys not every row sees would reach every row through P = 0.  They are cleared, and
+        // the first key with one is noted for its column (and for all columns, at kD): the output of the rows that see
+        // it becomes NaN there.  This lane's codes are 16 bytes of every 16th key.
+        auto clear_nans = [&](uint8_t* src, int column, int key0, int first_key, const uint32_t* valid, uint32_t item) {
+            int* nan = reinterpret_cast<int*>(smem + kNan) + item % kNanSlots * (kD + 1);
+#pragma unroll 1
+            for (int i = 0; i < kTile / 16; ++i) {
+                const int key = key0 + 16 * i;
+#pragma unroll 1
+                for (int b = 0; b < 16; ++b) {
+                    uint8_t* code = src + i * 16 * kD + b;
+                    if ((*code & 0x7f) != 0x7f) continue;
+                    *code = 0;
+                    if (!((valid[key >> 5] >> (key & 31)) & 1u)) continue;
+                    atomicMin(nan + column + b, first_key + key);
+                    atomicMin(nan + kD, first_key + key);
+                }
+            }
+            fence_proxy_async_smem();  // before the buffer is copied to again
+        };
         uint32_t taken = 0;
         auto next_item = [&](Item& d) {  // the next item with keys; false at the end
             while (ok && take_item(taken++, d))
@@ -574,12 +614,26 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // a lane widens 16 codes of a key, 8 lanes a key; a warp takes keys 16 i + 4 w .. + 3, whose swizzle is
                 // the same for every i.  The codes are loaded while the buffer is still being read.
                 const uint32_t key0 = 4 * w + (lane >> 3), ch = lane & 7, sw = key0 & 7;
-                const uint8_t* src = smem + kV + vs * kCodes + key0 * kD + ((ch ^ sw) << 4);
+                uint8_t* src = smem + kV + vs * kCodes + key0 * kD + ((ch ^ sw) << 4);
                 uint8_t* dst = smem + kVh + vh * 2 * kHalfBytes + (ch >> 2) * kHalfBytes + key0 * 128;
                 uint8_t *dst0 = dst + ((((ch & 3) * 2) ^ sw) << 4), *dst1 = dst + ((((ch & 3) * 2 + 1) ^ sw) << 4);
                 if (!mbar_wait_warp(bars.v_full(vs), (g / kVStages) & 1)) {
                     ok = false;
                     break;
+                }
+                const int first_key = (d.t0 + j) * kTile;
+                if (first_key + kTile - 1 > d.pos) {
+                    uint32_t bad = 0;
+#pragma unroll 2
+                    for (int i = 0; i < kTile / 16; ++i) {
+                        const uint4 c = *reinterpret_cast<const uint4*>(src + i * 16 * kD);
+                        bad |= ((c.x & 0x7F7F7F7Fu) + 0x01010101u) | ((c.y & 0x7F7F7F7Fu) + 0x01010101u) |
+                               ((c.z & 0x7F7F7F7Fu) + 0x01010101u) | ((c.w & 0x7F7F7F7Fu) + 0x01010101u);
+                    }
+                    if (bad & 0x80808080u)
+                        clear_nans(src, ch * 16, key0, first_key, reinterpret_cast<const uint32_t*>(smem + kVMask + vs * 16),
+                                   items);
+                    __syncwarp();
                 }
                 uint4 x[kTile / 16];
 #pragma unroll
@@ -637,38 +691,47 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         const bool out_al32 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
         const int my_pos = r * inv_g >> 16;  // the row's position in a tile, and its head of the group
-        Item d;
-        for (uint32_t n = 0; take_item(n, d); ++n) {
-            const bool row_ok = my_pos < d.nq;
+        for (uint32_t n = 0;; ++n) {
+            // (the item's description stays in shared memory until the end of its epilogue, for the registers' sake)
+            wait(bars.item_full(n % kItems), (n / kItems) & 1);
+            if (!ok) break;
+            const Item& d = *reinterpret_cast<const Item*>(smem + kItem + n % kItems * sizeof(Item));
+            if (d.nt < 0) break;
+            const uint32_t end = g + d.nt;
             const int my_last = min(d.pos + min(my_pos, d.nq - 1), d.last_key);  // (unused rows mask as the last used one)
             float m = -INFINITY, l = 0.f, qf = 0.f;
-            if (d.nt > 0) {
+            int key0 = d.t0 * kTile + x * 64;  // the piece's first key
+            if (g != end) {
                 wait(bars.q_full(items % kQSlots), (items / kQSlots) & 1);
                 qf = reinterpret_cast<const float*>(smem + kQf)[items % kQSlots * kTile + r];
             }
-            for (int j = 0; j < d.nt; ++j) {
-                const uint32_t t = g + j, piece = 2 * t + x, sb = piece % kPieces, t_s = tmem + lanes + kTS + sb * 64;
-                const int slot = t % kInfo;
-                wait(bars.info(slot), (t / kInfo) & 1);
+            bool first = true;  // nothing in O yet
+            for (; g != end; ++g, key0 += kTile, first = false) {
+                const uint32_t piece = 2 * g + x, sb = piece % kPieces, t_s = tmem + lanes + kTS + sb * 64;
+                const int slot = g % kInfo;
+                wait(bars.info(slot), (g / kInfo) & 1);
                 const float4* kc = reinterpret_cast<const float4*>(smem + kConsts) + slot * 16 + x * 8;
                 const uint2 vm = *reinterpret_cast<const uint2*>(mask + slot * 4 + x * 2);
                 // (all of this before the wait for S, which it does not need)
-                const int key0 = (d.t0 + j) * kTile + x * 64;
                 // the row's visible and valid keys as 64 bits; dense: all of them, for every row of the warp
                 const int vis = my_last - key0 + 1;
                 const uint32_t w0 = vm.x & (vis >= 32 ? ~0u : vis > 0 ? (1u << vis) - 1u : 0u);
                 const uint32_t w1 = vm.y & (vis >= 64 ? ~0u : vis > 32 ? (1u << (vis - 32)) - 1u : 0u);
                 const bool dense = __all_sync(0xffffffffu, (w0 & w1) == ~0u);
-                const bool first = j == 0;  // nothing in O yet
                 // The weights are taken with the maximum so far.  Only when a row's 64 of them come to more than 2^9
                 // (which is how a larger one shows, without a pass for the maximum) or at the item's first piece, the
                 // maximum is looked for, O brought to it, and the weights taken again.
                 bool look = first || __any_sync(0xffffffffu, m == -INFINITY);
-                float4 k4[64 / kKeys];
+                constexpr bool kAhead = kKeys >= 16;  // up to four blocks' factors are read ahead, eight blocks' where they are used
+                float4 k4[kAhead ? 64 / kKeys : 1];
+                auto factors = [&](int b) {
+                    float4 f = kc[b * kKeys / 8];
+                    f.x = fmaxf(f.x * qf, kTiny);
+                    return f;
+                };
+                if constexpr (kAhead) {
 #pragma unroll
-                for (int b = 0; b < 64 / kKeys; ++b) {
-                    k4[b] = kc[b * kKeys / 8];
-                    k4[b].x = fmaxf(k4[b].x * qf, kTiny);
+                    for (int b = 0; b < 64 / kKeys; ++b) k4[b] = factors(b);
                 }
                 uint32_t pk[32];
                 float sum, most;
@@ -697,7 +760,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             float u[2] = {s[b], s[b + 1]};
 #pragma unroll
                             for (int i = 2; i < kKeys; i += 2) u[i / 2 & 1] = fmax3(u[i / 2 & 1], s[b + i], s[b + i + 1]);
-                            mt = fmaxf(mt, fmaf(fmaxf(u[0], u[1]), k4[b / kKeys].x, k4[b / kKeys].y));
+                            const float4 f = kAhead ? k4[kAhead ? b / kKeys : 0] : factors(b / kKeys);
+                            mt = fmaxf(mt, fmaf(fmaxf(u[0], u[1]), f.x, f.y));
                         }
                         if (!first) {
                             // the products issued so far have to be done before O changes
@@ -722,7 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const float m_fin = m == -INFINITY ? 0.f : m;  // no key yet: every P' is 2^-inf
 #pragma unroll
                     for (int b = 0; b < 64; b += kKeys) {
-                        const float a = k4[b / kKeys].x, o = k4[b / kKeys].y - m_fin;
+                        const float4 f = kAhead ? k4[kAhead ? b / kKeys : 0] : factors(b / kKeys);
+                        const float a = f.x, o = f.y - m_fin;
                         const unsigned long long a2 = f32x2_pack(a, a), o2 = f32x2_pack(o, o);
                         unsigned long long part[2];  // the keys' weights, in pairs and two chains
 #pragma unroll
@@ -736,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float u, v;
                         f32x2_unpack(add_f32x2(part[0], part[1]), u, v);
                         most += u + v;
-                        sum = fmaf(u + v, k4[b / kKeys].z, sum);
+                        sum = fmaf(u + v, f.z, sum);
                     }
                     if (look || !__any_sync(0xffffffffu, most > kMost)) break;
                     look = true;
@@ -751,9 +816,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             // ---- the item's output: both groups' states joined, each group stores 64 columns of the row
+            if (!ok) break;
             float mo = -INFINITY, lo = 0.f;
-            if (d.nt > 0) {
-                const uint32_t last = 2 * (g + d.nt - 1) + x;  // this group's last piece
+            if (!first) {
+                const uint32_t last = 2 * (g - 1) + x;  // this group's last piece
                 wait(bars.pv_done(last % kPieces), (last / kPieces) & 1);
                 // (two copies by item: the other group may be an item behind)
                 float2* st = state + (items & 1) * 2 * kTile;
@@ -771,11 +837,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float M = fmaxf(m, mo);
             // (the weight of a state without a valid key is 0, and its O is not looked at; that of a state of NaN scores,
             // which no maximum takes up, is NaN)
-            const float w_own = m == -INFINITY && l == 0.f ? 0.f : fast_exp2(m - M);
-            const float w_oth = mo == -INFINITY && lo == 0.f ? 0.f : fast_exp2(mo - M);
+            const bool use_own = !(m == -INFINITY && l == 0.f), use_oth = !(mo == -INFINITY && lo == 0.f);
+            const float w_own = use_own ? fast_exp2(m - M) : 0.f, w_oth = use_oth ? fast_exp2(mo - M) : 0.f;
             const float L = w_own * l + w_oth * lo, inv = L == 0.f ? 0.f : 1.f / L;
             const float f_own = w_own * inv, f_oth = w_oth * inv;
-            const bool use_own = w_own != 0.f, use_oth = w_oth != 0.f;
+            const bool row_ok = my_pos < d.nq;
             const size_t row = (size_t)(d.row + my_pos) * p.num_q_heads + d.kvh * G + (r - my_pos * G);
             const bool direct = d.spans == 1;
             const size_t part = (size_t)d.span * p.total_q * p.num_q_heads + row;
@@ -784,7 +850,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int col = x * 64; col < x * 64 + 64; col += 32) {
                 float o[32];
-                if (d.nt > 0) {
+                if (!first) {
                     float b[32];
                     tmem_ld32(t_o + col, o);
                     tmem_ld32(t_oth + col, b);
@@ -820,13 +886,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (d.nt > 0) {
+            if (!first) {
+                // NaN among the V of the tile's own keys (see clear_nans), where this row sees them
+                const int* nan = reinterpret_cast<const int*>(smem + kNan) + items % kNanSlots * (kD + 1);
+                if (nan[kD] != INT_MAX && row_ok) {
+                    const int my_last = min(d.pos + my_pos, d.last_key);
+#pragma unroll 1
+                    for (int col = x * 64; col < x * 64 + 64; ++col) {
+                        if (nan[col] > my_last) continue;
+                        if (direct) static_cast<__nv_bfloat16*>(p.out)[row * kD + col] = __float2bfloat16_rn(NAN);
+                        else spans.o[part * kD + col] = NAN;
+                    }
+                }
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0 && ok) mbar_arrive(bars.o_free());
                 ++items;
             }
-            g += d.nt;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bars.item_empty(n % kItems));
         }
         if (!ok && lane == 0) count_error(p.error_count);
     }
@@ -954,7 +1032,9 @@ int launch_prefill_fp8_block_tc(const PrefillParams& p, void* workspace, int num
     if (rc != PA_OK) return rc;
     if ((rc = pool_tensor_map_rows(&tmv, p.v_cache, p.num_blocks, p.block_size, p.num_kv_heads, kD, true)) != PA_OK)
         return rc;
-    auto kernel = p.block_size >= 32 ? prefill_fp8_block_tc_kernel<32> : prefill_fp8_block_tc_kernel<8>;
+    auto kernel = p.block_size == 8    ? prefill_fp8_block_tc_kernel<8>
+                  : p.block_size == 16 ? prefill_fp8_block_tc_kernel<16>
+                                       : prefill_fp8_block_tc_kernel<32>;
     if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), kSmemBytes)) != PA_OK) return rc;
     Spans s = plan_spans(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group, p.max_context_len, num_sms);
     if (s.count > 1) {

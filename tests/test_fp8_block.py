@@ -554,6 +554,38 @@ def test_larger_scales_elsewhere_cost_no_precision(B):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("Hq,B,n,Q", [(4, 16, 290, 170), (8, 64, 515, 140), (1, 32, 1500, 1400), (4, 5, 290, 170)])
+def test_a_nan_reaches_the_queries_that_see_it(Hq, B, n, Q):
+    """NaN codes in V of a chunk's own tokens: NaN in their columns for the queries at or after them, nothing for those
+    before, whatever tile they share; a NaN code in K likewise, for every column."""
+    rng = np.random.default_rng(90 + Hq)
+    lens = [n, 200]
+    table, P = _tables(rng, lens, B)
+    codes, scales = zip(_pools(rng, P, B, 1, 128), _pools(rng, P, B, 1, 128))
+    q = _bf16(rng, (Q + 150, Hq, 128))
+    nan = np.zeros(q.shape, bool)
+    cu, start = [0, Q, Q + 150], [n - Q, 50]
+    s64 = [s.astype(np.float64) for s in scales]
+    want, mag, floor = np.zeros(q.shape), np.zeros(q.shape), np.zeros(q.shape)
+    for c in range(2):
+        r, limits = slice(cu[c], cu[c + 1]), [start[c] + i + 1 for i in range(cu[c + 1] - cu[c])]
+        want[r], mag[r] = R.attend_rows(q[r].double().numpy(), codes[0], s64[0], codes[1], s64[1], table[c], limits, 0.1)
+        floor[r] = R.floor_rows(codes[1], s64[1], table[c], limits, Hq)
+    for c, pos, side, dims in ((0, n - 70, 1, [3, 77]), (0, n - 2, 1, [5, 127, 3]), (0, n - 1, 0, [64]), (1, 60, 1, [0]),
+                               (1, 140, 1, [1]), (1, 199, 1, list(range(128)))):
+        codes[side][table[c, pos // B], pos % B, 0, dims] = 0xff if pos % 2 else 0x7f
+        nan[max(cu[c] + pos - start[c], cu[c]):cu[c + 1], :, dims if side else slice(None)] = True
+    pools = [torch.from_numpy(np.ascontiguousarray(a)).cuda() for a in (*codes, *scales)]
+    for mx in (max(lens), 16384):
+        ws = pa.new_prefill_fp8_block_workspace(2, Q + 150, max(Q, 150), Hq, 1, 128, B, mx)
+        for _ in range(2):
+            out = pa.pa_prefill_chunk_fp8_block(q.cuda(), _i32(cu), _i32(start), _i32([0, 1]), max(Q, 150), *pools,
+                                                _i32(table), _i32(lens), mx, 0.1, ws).cpu()
+            assert np.array_equal(torch.isnan(out).numpy(), nan)
+            _close(out[~torch.from_numpy(nan)], want[~nan], mag[~nan], floor[~nan])
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("Hq,D", [(4, 128), (4, 64), (12, 128)])
 @pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
 def test_queries_that_are_not_finite_give_nan(Hq, D, value):
