@@ -432,9 +432,14 @@ PA_API int pa_read_kv_paged_fp8_block(void* k_out, void* v_out, int num_tokens, 
 /*
  * pa_decode over e4m3 pools with a scale per (block, kv head): the attention
  * of pa_decode on the values that pa_read_kv_paged_fp8_block reads back; q and
- * out bf16.  Scales must be finite and 0 or at least 2^-110 in the blocks that
- * hold a sequence's tokens; those of other blocks are not used.  Tokens in a
- * block with an invalid table entry are masked (and counted).  Shapes, context
+ * out bf16.  Scales must be finite and not negative in the blocks that hold a
+ * sequence's tokens; those of other blocks are not used.  Where the tensor cores
+ * run (head_dim 128, up to 8 query heads per kv head, block sizes 8, 16, 32, 64
+ * and 128, 16-byte aligned pools and q) a V scale below 2^-100, or 2^-80 of the
+ * largest of the context's blocks, counts as no more than that.  Tokens in a
+ * block with an invalid table entry are masked (and counted).  A query with an
+ * infinity or a NaN gives NaN, as does a NaN code in K or (in its column) in V
+ * for the queries that see its token.  Shapes, context
  * clamping and the workspace's rules are pa_decode's
  * (pa_decode_fp8_block_workspace_size bytes).
  */

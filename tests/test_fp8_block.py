@@ -616,6 +616,42 @@ def test_queries_that_are_not_finite_give_nan(Hq, D, value):
     _close(out.cpu()[~hit[4:]], want[4:][~hit[4:]], mag[4:][~hit[4:]], floor[4:][~hit[4:]])
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("Hkv,B", [(8, 16), (2, 64)])
+def test_pools_beyond_32_bit_offsets(Hkv, B):
+    """Blocks at the end of pools of more than 2^32 codes give what the same blocks give in a small pool, bit for bit."""
+    rng = np.random.default_rng(100 + B)
+    D, Hq, n = 128, 4 * Hkv, 1200
+    P = (1 << 32) // (B * Hkv * D) + 200
+    used = -(-n // B)
+    small = torch.from_numpy(rng.permutation(used + 2)[:used].astype(np.int32)).reshape(1, -1).cuda()
+    far = small + (P - used - 2)
+    T = n
+    k, v = _bf16(rng, (T, Hkv, D)).cuda(), _bf16(rng, (T, Hkv, D)).cuda()
+    seq, pos = _i32([0] * T), _i32(range(T))
+    q = _bf16(rng, (50, Hq, D)).cuda()
+    got = []
+    for table, blocks in ((small, used + 2), (far, P)):
+        kc, vc = (torch.zeros(blocks, B, Hkv, D, dtype=torch.uint8, device="cuda") for _ in range(2))
+        ks, vs = (torch.zeros(blocks, Hkv, device="cuda") for _ in range(2))
+        for a, b in ((0, 700), (700, T)):  # both forms of the write
+            pa.pa_write_kv_paged_fp8_block(k[a:b], v[a:b], kc, vc, ks, vs, table, seq[a:b], pos[a:b])
+        ws = pa.new_write_fp8_block_workspace(T, blocks, B)
+        pa.pa_write_kv_paged_fp8_block(k, v, kc, vc, ks, vs, table, seq, pos, ws)
+        outs = list(pa.pa_read_kv_paged_fp8_block(kc, vc, ks, vs, table, seq, pos))
+        ws = pa.new_decode_fp8_block_workspace(1, Hq, Hkv, D, B, n)
+        outs.append(pa.pa_decode_fp8_block(q[:1], kc, vc, ks, vs, table, _i32([n]), n, 0.1, ws))
+        ws = pa.new_prefill_fp8_block_workspace(1, 50, 50, Hq, Hkv, D, B, n)
+        outs.append(pa.pa_prefill_chunk_fp8_block(q, _i32([0, 50]), _i32([n - 50]), _i32([0]), 50, kc, vc, ks, vs, table,
+                                                  _i32([n]), n, 0.1, ws))
+        got.append([o.cpu() for o in outs])
+        assert int(torch.count_nonzero(ks)) == used * Hkv
+        del kc, vc
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    assert bool(torch.isfinite(got[0][3]).all()) and float(got[0][3].abs().max()) > 0
+
+
 # ---------------------------------------------------------------- GPU: together
 @pytest.mark.gpu
 def test_write_then_prefill_then_decode_then_read():
