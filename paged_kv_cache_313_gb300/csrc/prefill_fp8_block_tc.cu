@@ -260,9 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
 
     // Registers: 128 a thread at launch (512 threads take all of the SM's).  The softmax warps get 152 of them, for 64
-    // scores and what becomes of them, the converters keep 120, the others 88: 2 * 152 + 120 + 88 = 4 * 128.  No role may
-    // spill: eight bytes spilled in the softmax took the long chunk from 387 to 416 us.
-    if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    // scores and what becomes of them, the others 104: 2 * 152 + 104 + 104 = 4 * 128.  No role may spill: eight bytes
+    // spilled in the softmax took the long chunk from 387 to 416 us.
+    if (warp >= kMmaWarp) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == kKWarp || warp == kVWarp) {
         // ============================================================ producers
         const int bpt = kTile >> log2b, tpc = 32 / bpt;  // blocks per tile, tiles per 32-entry chunk of the table
@@ -483,67 +483,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp >= kConvWarp && warp < kMmaWarp) {
         // ============================================================ converters
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         const int w = warp - kConvWarp;
         uint32_t g = 0, items = 0;
-        // an item's query rows, one a lane: two e4m3 terms staged in shared memory, and the factor that undoes their
-        // scaling.  In f16, which holds a scaled bf16 exactly down to 2^-24.
+        // an item's query rows, half a row a lane and 16 rows at a time (a whole row a lane takes 64 registers for the row
+        // alone): two e4m3 terms staged in shared memory, and the factor that undoes their scaling.  In f16, which holds a
+        // scaled bf16 exactly down to 2^-24.
         auto stage_q = [&](const Item& d, uint32_t item) {
-            const int r = w * 32 + lane, pos = r * inv_g >> 16;
             // (a converter is less than two key tiles, so two items, ahead of another: no one has written there yet)
             int* nan = reinterpret_cast<int*>(smem + kNan) + (item + 2) % kNanSlots * (kD + 1);
-            nan[r] = INT_MAX;
-            if (r == 0) nan[kD] = INT_MAX;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                static_cast<const __nv_bfloat16*>(p.q) +
-                ((size_t)(d.row + pos) * p.num_q_heads + d.kvh * G + (r - pos * G)) * kD);
-            uint4 x[kD / 8];
+            nan[w * 32 + lane] = INT_MAX;
+            if (w == 0 && lane == 0) nan[kD] = INT_MAX;
+            const int half = lane & 1;
+#pragma unroll 1
+            for (int r = w * 32 + (lane >> 1), end = r + 32; r < end; r += 16) {
+                const int pos = r * inv_g >> 16;
+                const uint4* src = reinterpret_cast<const uint4*>(
+                    static_cast<const __nv_bfloat16*>(p.q) +
+                    ((size_t)(d.row + pos) * p.num_q_heads + d.kvh * G + (r - pos * G)) * kD) + half * (kD / 16);
+                uint4 x[kD / 16];
 #pragma unroll
-            for (int k = 0; k < kD / 8; ++k) x[k] = pos < d.nq ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
-            uint32_t m2 = 0;
+                for (int k = 0; k < kD / 16; ++k) x[k] = pos < d.nq ? __ldg(src + k) : make_uint4(0u, 0u, 0u, 0u);
+                uint32_t m2 = 0;
 #pragma unroll
-            for (int k = 0; k < kD / 8; ++k)
-                m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(x[k].x & 0x7FFF7FFFu, x[k].y & 0x7FFF7FFFu),
-                                           __vmaxu2(x[k].z & 0x7FFF7FFFu, x[k].w & 0x7FFF7FFFu)));
-            const uint32_t am = max(m2 & 0xFFFFu, m2 >> 16);
-            const int e = min(134 - (int)(am >> 7), 126);  // |x| 2^e in [128, 256)
-            // a negative softmax scale negates the queries, so that scores only meet positive factors; a row with an
-            // infinity or a NaN becomes NaN (the conversion would hold an infinity at 448)
-            const float f = am >= 0x7F80u ? NAN : copysignf(__uint_as_float((uint32_t)(e + 127) << 23), p.scale_log2);
-            uint8_t* row = smem + kQ + r * kD;
+                for (int k = 0; k < kD / 16; ++k)
+                    m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(x[k].x & 0x7FFF7FFFu, x[k].y & 0x7FFF7FFFu),
+                                               __vmaxu2(x[k].z & 0x7FFF7FFFu, x[k].w & 0x7FFF7FFFu)));
+                m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, 1));
+                const uint32_t am = max(m2 & 0xFFFFu, m2 >> 16);
+                const int e = min(134 - (int)(am >> 7), 126);  // |x| 2^e in [128, 256)
+                // a negative softmax scale negates the queries, so that scores only meet positive factors; a row with an
+                // infinity or a NaN becomes NaN (the conversion would hold an infinity at 448)
+                const float f = am >= 0x7F80u ? NAN : copysignf(__uint_as_float((uint32_t)(e + 127) << 23), p.scale_log2);
+                uint8_t* row = smem + kQ + r * kD;
 #pragma unroll
-            for (int k = 0; k < kD / 16; ++k) {
-                if (k == kD / 32) {
-                    // (the second half of the row is loaded again, so that it need not be kept in registers meanwhile)
-                    if (pos < d.nq) {
+                for (int k = 0; k < kD / 32; ++k) {
+                    const uint32_t in[8] = {x[2 * k].x,     x[2 * k].y,     x[2 * k].z,     x[2 * k].w,
+                                            x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                        for (int k = kD / 16; k < kD / 8; ++k)
-                            asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];"
-                                         : "=r"(x[k].x), "=r"(x[k].y), "=r"(x[k].z), "=r"(x[k].w)
-                                         : "l"(src + k));
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t c[2], b[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint32_t v = in[2 * i + j];
+                            const uint32_t h =
+                                pack_f16x2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
+                            c[j] = e4m3x2_of_f16x2(h);
+                            b[j] = e4m3x2_of_f16x2(sub_f16x2(h, e4m3x2_to_f16x2(c[j])));
+                        }
+                        hi[i] = c[0] | (c[1] << 16);
+                        lo[i] = b[0] | (b[1] << 16);
                     }
+                    const int at = ((half * 4 + k) ^ (r & 7)) << 4;
+                    *reinterpret_cast<uint4*>(row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(row + kCodes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
-                const uint32_t in[8] = {x[2 * k].x,     x[2 * k].y,     x[2 * k].z,     x[2 * k].w,
-                                        x[2 * k + 1].x, x[2 * k + 1].y, x[2 * k + 1].z, x[2 * k + 1].w};
-                uint32_t hi[4], lo[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t c[2], b[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t v = in[2 * i + j];
-                        const uint32_t h = pack_f16x2(__uint_as_float(v << 16) * f, __uint_as_float(v & 0xFFFF0000u) * f);
-                        c[j] = e4m3x2_of_f16x2(h);
-                        b[j] = e4m3x2_of_f16x2(sub_f16x2(h, e4m3x2_to_f16x2(c[j])));
-                    }
-                    hi[i] = c[0] | (c[1] << 16);
-                    lo[i] = b[0] | (b[1] << 16);
-                }
-                const int at = (k ^ (r & 7)) << 4;
-                *reinterpret_cast<uint4*>(row + at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                *reinterpret_cast<uint4*>(row + kCodes + at) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                if (half == 0)
+                    reinterpret_cast<float*>(smem + kQf)[item % kQSlots * kTile + r] = __uint_as_float((uint32_t)(127 - e) << 23);
             }
-            reinterpret_cast<float*>(smem + kQf)[item % kQSlots * kTile + r] = __uint_as_float((uint32_t)(127 - e) << 23);
         };
         // the staged rows into tensor memory (a lane's row is its tensor-memory lane), once the item before is through
         // its last S
@@ -699,29 +697,26 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (d.nt < 0) break;
             const uint32_t end = g + d.nt;
             const int my_last = min(d.pos + min(my_pos, d.nq - 1), d.last_key);  // (unused rows mask as the last used one)
+            const int least_last = __reduce_min_sync(0xffffffffu, my_last);
             float m = -INFINITY, l = 0.f, qf = 0.f;
             int key0 = d.t0 * kTile + x * 64;  // the piece's first key
             if (g != end) {
                 wait(bars.q_full(items % kQSlots), (items / kQSlots) & 1);
                 qf = reinterpret_cast<const float*>(smem + kQf)[items % kQSlots * kTile + r];
             }
-            bool first = true;  // nothing in O yet
+            bool first = true, open = true;  // nothing in O yet; there are rows without a key so far
             for (; g != end; ++g, key0 += kTile, first = false) {
                 const uint32_t piece = 2 * g + x, sb = piece % kPieces, t_s = tmem + lanes + kTS + sb * 64;
                 const int slot = g % kInfo;
                 wait(bars.info(slot), (g / kInfo) & 1);
                 const float4* kc = reinterpret_cast<const float4*>(smem + kConsts) + slot * 16 + x * 8;
-                const uint2 vm = *reinterpret_cast<const uint2*>(mask + slot * 4 + x * 2);
                 // (all of this before the wait for S, which it does not need)
-                // the row's visible and valid keys as 64 bits; dense: all of them, for every row of the warp
-                const int vis = my_last - key0 + 1;
-                const uint32_t w0 = vm.x & (vis >= 32 ? ~0u : vis > 0 ? (1u << vis) - 1u : 0u);
-                const uint32_t w1 = vm.y & (vis >= 64 ? ~0u : vis > 32 ? (1u << (vis - 32)) - 1u : 0u);
-                const bool dense = __all_sync(0xffffffffu, (w0 & w1) == ~0u);
+                const uint2 vm = *reinterpret_cast<const uint2*>(mask + slot * 4 + x * 2);
+                const bool dense = key0 + 63 <= least_last && (vm.x & vm.y) == ~0u;  // every key, for every row of the warp
                 // The weights are taken with the maximum so far.  Only when a row's 64 of them come to more than 2^9
-                // (which is how a larger one shows, without a pass for the maximum) or at the item's first piece, the
+                // (which is how a larger one shows, without a pass for the maximum) or a row has seen no key yet, the
                 // maximum is looked for, O brought to it, and the weights taken again.
-                bool look = first || __any_sync(0xffffffffu, m == -INFINITY);
+                bool look = open;
                 constexpr bool kAhead = kKeys >= 16;  // up to four blocks' factors are read ahead, eight blocks' where they are used
                 float4 k4[kAhead ? 64 / kKeys : 1];
                 auto factors = [&](int b) {
@@ -748,7 +743,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 32; ++i) s[i] = a[i], s[32 + i] = b[i];
                     }
                     tmem_wait_ld();
-                    if (!dense) {
+                    if (!dense) {  // the row's visible and valid keys as 64 bits
+                        const uint2 v = *reinterpret_cast<const uint2*>(mask + slot * 4 + x * 2);
+                        const int vis = my_last - key0 + 1;
+                        const uint32_t w0 = v.x & (vis >= 32 ? ~0u : vis > 0 ? (1u << vis) - 1u : 0u);
+                        const uint32_t w1 = v.y & (vis >= 64 ? ~0u : vis > 32 ? (1u << (vis - 32)) - 1u : 0u);
 #pragma unroll
                         for (int k = 0; k < 64; ++k)
                             if (!((k < 32 ? w0 : w1) & (1u << (k & 31)))) s[k] = -INFINITY;
@@ -781,6 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             l *= alpha;
                         }
                         m = mt;
+                        open = __any_sync(0xffffffffu, m == -INFINITY);
                     }
                     sum = most = 0.f;
                     const float m_fin = m == -INFINITY ? 0.f : m;  // no key yet: every P' is 2^-inf
