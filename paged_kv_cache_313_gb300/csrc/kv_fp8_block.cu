@@ -35,7 +35,7 @@
 // Measured (8 heads of 128, blocks of 16): four prompts of 2048 tokens 18.8 us
 // (50.5 MB: 0.40 of the copy bandwidth, the two launches and their dependent
 // loads being about half of it); 256 decode tokens and 4 x 512 over blocks of 32
-// 14.8 us.  Read back of 89,556 tokens to bf16 88.6 us, 551 MB: 0.92.
+// 13.8 us.  Read back of 89,556 tokens to bf16 88.6 us, 551 MB: 0.92.
 #include "pa_internal.cuh"
 
 namespace pa {
@@ -408,7 +408,9 @@ int launch_write_fp8_block(const void* k_new, const void* v_new, int num_tokens,
                                  stream, p);
     if (rc != PA_OK) return rc;
     const long long most = ((long long)(num_tokens < num_blocks ? num_tokens : num_blocks) * 2 * num_kv_heads + kWarps - 1) / kWarps;
-    const long long fill = 4LL * num_sms, ctas = most < 1 ? 1 : most < fill ? most : fill;  // (fill: CTAs that fit the GPU)
+    // CTAs that fit the GPU, and up to three times as many behind them, which start as those end: with one round only, some
+    // warps had two units where most had one (256 decode tokens and 4 x 512 over blocks of 32: 15.2 us, so 13.8)
+    const long long fill = 4LL * num_sms, ctas = most < 1 ? 1 : most < 4 * fill ? most : 4 * fill;
     auto kernel =
         head_dim == 128 ? write_listed_kernel<16> : head_dim == 64 ? write_listed_kernel<8> : write_listed_kernel<0>;
     return launch_kernel(kernel, dim3((unsigned)ctas), dim3(kThreads), 0, stream, p);
