@@ -46,10 +46,10 @@
 //
 // Bound: the softmax warps' issue and the hand-overs between the warps (the two
 // products are 1.05k cycles of a key tile's 2.0k).  Measured: 2048 queries at
-// position 5,916, 64/8 heads, 385 us over 64-token blocks (466 GFLOP: 1.21
-// PFLOP/s, 0.62 of cuBLAS bf16) and 398 over 16-token blocks, whose copies are
+// position 5,916, 64/8 heads, 384 us over 64-token blocks (466 GFLOP: 1.21
+// PFLOP/s, 0.62 of cuBLAS bf16) and 396 over 16-token blocks, whose copies are
 // four times as many; four chunks of 512 queries at short offsets, 32/8 heads,
-// 34.7 us; 37 queries at 2,955 17.7 us.  On the CUDA cores 184, 5.0 and 1.3 ms.
+// 33.4 us; 37 queries at 2,955 17.4 us.  On the CUDA cores 184, 5.0 and 1.3 ms.
 #include <climits>
 
 #include "pa_internal.cuh"
