@@ -801,6 +801,63 @@ def test_calls_on_another_stream_and_without_workspace():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("captured", [False, True])
+def test_two_streams_at_once(captured):
+    """Two sequences of calls on two streams, each with its own pools and workspaces, give what they give one after the
+    other, bit for bit; the same captured into a graph each and replayed at once."""
+    B, Hkv, Hq, D, rounds = 16, 2, 8, 128, 6
+
+    def job(seed):
+        rng = np.random.default_rng(seed)
+        lens = [1500 + seed, 40, 700]
+        table, P = _tables(rng, lens, B)
+        T = sum(lens)
+        k, v = _bf16(rng, (T, Hkv, D)).cuda(), _bf16(rng, (T, Hkv, D)).cuda()
+        seq, pos = _i32(np.repeat(range(3), lens)), _i32(np.concatenate([np.arange(L) for L in lens]))
+        bt, ctx, n = _i32(table), _i32(lens), max(lens)
+        q, qd = _bf16(rng, (90, Hq, D)).cuda(), _bf16(rng, (3, Hq, D)).cuda()
+        kc, vc = (torch.zeros(P, B, Hkv, D, dtype=torch.uint8, device="cuda") for _ in range(2))
+        ks, vs = (torch.zeros(P, Hkv, device="cuda") for _ in range(2))
+        ww, wd = pa.new_write_fp8_block_workspace(T, P, B), pa.new_decode_fp8_block_workspace(3, Hq, Hkv, D, B, n)
+        wp = pa.new_prefill_fp8_block_workspace(1, 90, 90, Hq, Hkv, D, B, n)
+        cu, start, which = _i32([0, 90]), _i32([lens[0] - 90]), _i32([0])
+        outs = [torch.zeros(3, Hq, D, dtype=BF, device="cuda"), torch.zeros(90, Hq, D, dtype=BF, device="cuda"),
+                torch.zeros(T, Hkv, D, dtype=BF, device="cuda"), torch.zeros(T, Hkv, D, dtype=BF, device="cuda")]
+
+        def run():
+            pa.pa_write_kv_paged_fp8_block(k, v, kc, vc, ks, vs, bt, seq, pos, ww)
+            pa.pa_decode_fp8_block(qd, kc, vc, ks, vs, bt, ctx, n, 0.1, wd, out=outs[0])
+            pa.pa_prefill_chunk_fp8_block(q, cu, start, which, 90, kc, vc, ks, vs, bt, ctx, n, 0.1, wp, out=outs[1])
+            pa.pa_read_kv_paged_fp8_block(kc, vc, ks, vs, bt, seq, pos, k_out=outs[2], v_out=outs[3])
+        return run, outs
+
+    jobs = [job(1), job(2)]
+    want = []
+    for run, outs in jobs:
+        run()
+        torch.cuda.synchronize()
+        want.append([o.clone() for o in outs])
+        assert all(bool(torch.isfinite(o).all()) and int(torch.count_nonzero(o)) for o in outs)
+        for o in outs:
+            o.zero_()
+    torch.cuda.synchronize()
+    streams, graphs = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    if captured:
+        for (run, _), st in zip(jobs, streams):
+            graphs.append(torch.cuda.CUDAGraph())
+            with torch.cuda.graph(graphs[-1], stream=st):
+                run()
+    for _ in range(rounds):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                graphs[i].replay() if captured else jobs[i][0]()
+    torch.cuda.synchronize()
+    for (_, outs), w in zip(jobs, want):
+        for o, x in zip(outs, w):
+            assert torch.equal(o, x)
+
+
+@pytest.mark.gpu
 def test_empty_calls():
     kc = torch.zeros(4, 16, 2, 128, dtype=torch.uint8, device="cuda")
     sc, i0 = torch.zeros(4, 2, device="cuda"), torch.zeros(0, dtype=torch.int32, device="cuda")
