@@ -44,10 +44,10 @@
 //
 // Bound: HBM.  A stage is 32 KB, 0.74 us of an SM's share of the measured copy
 // bandwidth; the softmax of a stage is about 250 warp instructions.  Measured: 64
-// sequences, 32/8 heads, 65,500 tokens 33.9 us (135 MB: 0.59 of the copy
+// sequences, 32/8 heads, 65,500 tokens 32.5 us (135 MB: 0.62 of the copy
 // bandwidth, start, uneven ends and join included); 16 long contexts, 64/8 heads,
-// 189,395 tokens 76.6 us (0.75; CTAs take a stage every 3.0k cycles, 0.93); four
-// sequences of up to 40 tokens 7.3 us.  On the CUDA cores the first two took 805
+// 189,395 tokens 74.9 us (0.77; CTAs take a stage every 3.0k cycles, 0.93); four
+// sequences of up to 40 tokens 6.8 us.  On the CUDA cores the first two took 805
 // and 3132 us.
 #include <atomic>
 #include <climits>
@@ -69,6 +69,11 @@ constexpr int kMaxBlocks = kTok / 8;  // blocks of a stage
 constexpr uint32_t kTmemCols = 64;    // S0 | S1 | O0 | O1, 16 columns each
 // A V scale below 2^-80 of the stage's largest or 2^-100 (the smallest that the write makes) counts as 0.
 constexpr float kHold = 8.271806125530277e-25f, kLeastScale = 7.888609052210118e-31f;
+
+// num_partitions for this file's partitions, which are powers of two.
+__device__ __forceinline__ int partitions(int L, int part) {
+    return L <= part ? 1 : ((L - 1) >> (31 - __clz(part))) + 1;
+}
 
 struct Stage {
     int s, kvh, split, flags;  // flags: 1 first stage of the item, 2 last, 4 the item writes the output, 8 no more
@@ -108,7 +113,7 @@ static_assert(kSmemBytes <= 228 * 1024 / 2 - 1024, "two CTAs per SM");
 template <int kHeads>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_fp8_block_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                               const DecodeParams p) {
+                               const DecodeParams p, const Divisor per_heads) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     int* cum = reinterpret_cast<int*>(smem + kCum);
@@ -147,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int n_first = N * Hkv;  // partition-0 items
     int early = -1, early_len = 0;
     if (warp == kProducer && (int)blockIdx.x < n_first) {
-        const int s0 = blockIdx.x / Hkv;
+        const int s0 = per_heads.div(blockIdx.x);
         early_len = p.context_lens[s0];
         if (lane < p.max_blocks_per_seq) early = p.block_tables[(size_t)s0 * p.max_blocks_per_seq + lane];
     }
@@ -161,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const uint32_t tmem = *tmem_slot;
 
     auto later_items = [&](int s) {
-        return (num_partitions(decode_context(p, s, false), partition_of(p, s)) - 1) * Hkv;
+        return (partitions(decode_context(p, s, false), partition_of(p, s)) - 1) * Hkv;
     };
     if (warp < 4) {  // prefix sum of the later partitions' counts, while the producer starts its first item
         const int per = (N + 127) / 128, first = threadIdx.x * per;
@@ -198,10 +203,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         struct Item {
             int s, split, kvh, nsplit, j0, ntok, nblk;
         };
+        const int log2b = 31 - __clz(B);
         auto describe = [&](int it, int known_len) {  // known_len: the item's context_lens entry, or INT_MIN
             Item d;
             if (it < n_first) {
-                d.s = it / Hkv;
+                d.s = per_heads.div(it);
                 d.split = 0;
                 d.kvh = it - d.s * Hkv;
             } else {
@@ -213,28 +219,28 @@ __global__ void __launch_bounds__(kThreads, 2)
                 }
                 d.s = lo;
                 const int r = it - cum[lo];
-                d.split = r / Hkv + 1;
+                d.split = per_heads.div(r) + 1;
                 d.kvh = r - (d.split - 1) * Hkv;
             }
             const int L = known_len == INT_MIN ? decode_context(p, d.s, false) : clamp_context(p, known_len);
             const int part = partition_of(p, d.s);
-            d.nsplit = num_partitions(L, part);
+            d.nsplit = partitions(L, part);
             d.j0 = d.split * part;
             d.ntok = max(0, min(L - d.j0, part));
-            d.nblk = (d.ntok + B - 1) / B;
+            d.nblk = (d.ntok + B - 1) >> log2b;
             return d;
         };
         // this lane's entry of a 32-block chunk of an item's table, and its scales (0 without a valid block)
         auto load_raw = [&](const Item& d, int chunk) {
             const int i = chunk * 32 + lane;
-            return i < d.nblk ? p.block_tables[(size_t)d.s * p.max_blocks_per_seq + d.j0 / B + i] : -1;
+            return i < d.nblk ? p.block_tables[(size_t)d.s * p.max_blocks_per_seq + (d.j0 >> log2b) + i] : -1;
         };
         auto load_scales = [&](const Item& d, int pb) {
             if (pb < 0 || pb >= p.num_blocks) return make_float2(0.f, 0.f);
             const size_t i = (size_t)pb * Hkv + d.kvh;
             return make_float2(__ldg(p.k_scales + i), __ldg(p.v_scales + i));
         };
-        const int bps = kTok / B, spc = 32 / bps;  // blocks per stage, stages per chunk
+        const int bps = kTok >> log2b, log2spc = log2b - 2;  // blocks per stage; 32-block chunks are 2^log2spc stages
         const uint64_t policy = l2_policy_evict_first();  // K and V are read once
         bool ok = true;
         int total = -1;
@@ -267,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             Item d2{};
             int pb = -1;
             for (int st = 0; st < nst; ++st, ++n) {
-                const int slot = n % kStages, chunk = st / spc, l = st - chunk * spc;
+                const int slot = n % kStages, chunk = st >> log2spc, l = st - (chunk << log2spc);
                 if (l == 0) {
                     if (chunk > 0) {
                         raw = raw_next;
@@ -656,7 +662,7 @@ int launch(const DecodeParams& p, int num_sms, cudaStream_t stream) {
     if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), kSmemBytes)) != PA_OK) return rc;
     const long long most = (long long)p.num_seqs * p.num_kv_heads * p.max_splits, slots = 2LL * num_sms;
     return launch_kernel(kernel, dim3((unsigned)(most < slots ? most : slots)), dim3(kThreads), kSmemBytes, stream,
-                         tmk, tmv, p);
+                         tmk, tmv, p, Divisor((uint32_t)p.num_kv_heads));
 }
 
 // The join of a split context's partials (m_i, l_i, o_i): out = sum_i w_i o_i / sum_i w_i, w_i = l_i 2^(m_i - max m).
@@ -671,9 +677,9 @@ __global__ void __launch_bounds__(128) decode_fp8_block_join_kernel(const Decode
     __shared__ float weight[128], warp_m[4], warp_w[4];
     __shared__ float4 sums[4][kCols];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, G = p.group, Hq = p.num_q_heads;
-    const long long u = blockIdx.x;
-    const int s = (int)(u / Hq), h = (int)(u - (long long)s * Hq);
-    const int n = num_partitions(decode_context(p, s, false), partition_of(p, s));
+    const uint32_t u = blockIdx.x;
+    const int s = (int)(u / (uint32_t)Hq), h = (int)(u - (uint32_t)s * (uint32_t)Hq);
+    const int n = partitions(decode_context(p, s, false), partition_of(p, s));
     if (n <= 1) return;  // stored by the decode kernel
     const int kvh = h / G;
     const size_t base = decode_unit(p, s, kvh) * p.max_splits * G + (h - kvh * G);  // (split 0, this head)
@@ -746,7 +752,9 @@ bool decode_fp8_block_tc_supported(const DecodeParams& p) {
     const int B = p.block_size;
     if (p.head_dim != kD || p.group > 8 || B < 8 || B > 128 || (B & (B - 1)) != 0) return false;
     if (((uintptr_t)p.k_cache & 15) || ((uintptr_t)p.v_cache & 15) || ((uintptr_t)p.q & 15)) return false;
-    return (long long)p.num_blocks * B < (1LL << 31) && p.num_blocks > 0 && p.partition % kTok == 0;
+    // (item numbers of a launch stay below 2^30)
+    return (long long)p.num_blocks * B < (1LL << 31) && p.num_blocks > 0 && p.partition % kTok == 0 &&
+           (long long)kMaxSeqs * p.num_kv_heads * p.max_splits < (1LL << 30);
 }
 
 int launch_decode_fp8_block_tc(const DecodeParams& p, int num_sms, cudaStream_t stream) {

@@ -32,10 +32,10 @@
 //     among them.  It leaves the workspace zeroed again.
 //
 // Bound: HBM for long calls, launch and memory latency for a decode step.
-// Measured (8 heads of 128, blocks of 16): four prompts of 2048 tokens 18.8 us
+// Measured (8 heads of 128, blocks of 16): four prompts of 2048 tokens 18.1 us
 // (50.5 MB: 0.40 of the copy bandwidth, the two launches and their dependent
 // loads being about half of it); 256 decode tokens and 4 x 512 over blocks of 32
-// 13.8 us.  Read back of 89,556 tokens to bf16 88.6 us, 551 MB: 0.92.
+// 13.5 us.  Read back of 89,556 tokens to bf16 87.2 us, 551 MB: 0.93.
 #include "pa_internal.cuh"
 
 namespace pa {
@@ -61,6 +61,7 @@ struct BlockWriteParams {
     int64_t* slots;
     int32_t* error_count;
     int num_tokens, num_kv_heads, head_dim, num_blocks, block_size, num_seqs, max_blocks_per_seq;
+    Divisor per_pairs;  // by 2 num_kv_heads
     // two-launch form (workspace)
     int32_t* counters;  // [0] blocks listed, [1] CTAs done
     int32_t* listed;    // [num_blocks] 1: the block is on the list
@@ -266,11 +267,18 @@ __global__ void __launch_bounds__(kThreads, 4) write_listed_kernel(const BlockWr
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, pairs = 2 * p.num_kv_heads, B = p.block_size;
-    const long long units = (long long)p.counters[0] * pairs, stride = (long long)gridDim.x * kWarps;
-    for (long long u = (long long)blockIdx.x * kWarps + (threadIdx.x >> 5); u < units; u += stride) {
-        const int b = (int)(u / pairs), pb = p.list[b];
+    // (unit = b * pairs + pair; below 2^30 warps, so the first unit and the stride are)
+    const int first = blockIdx.x * kWarps + (threadIdx.x >> 5), stride = gridDim.x * kWarps, listed = p.counters[0];
+    const int step_b = p.per_pairs.div(stride), step_pair = stride - step_b * pairs;
+    int b = p.per_pairs.div(first), pair = first - b * pairs;
+    for (; b < listed; b += step_b, pair += step_pair) {
+        if (pair >= pairs) {
+            pair -= pairs;
+            if (++b >= listed) break;
+        }
+        const int pb = p.list[b];
         int32_t* writer = p.writer + (size_t)pb * B;
-        store_rows<kPieces>(p, pb, (int)(u - (long long)b * pairs), writer, lane);
+        store_rows<kPieces>(p, pb, pair, writer, lane);
         // the last of the block's warps to have read its writers clears them for the next call
         int done = 0;
         if (lane == 0) done = atomicAdd(&p.finished[pb], 1);
@@ -297,11 +305,12 @@ constexpr int kReadTokens = 8;
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
-    read_kernel(T* __restrict__ k_out, T* __restrict__ v_out, int num_tokens, int num_kv_heads, int head_dim,
+    read_kernel(T* __restrict__ k_out, T* __restrict__ v_out, int num_tokens, int num_kv_heads,
                 const uint4* __restrict__ k_cache, const uint4* __restrict__ v_cache,
                 const float* __restrict__ k_scales, const float* __restrict__ v_scales, int num_blocks, int block_size,
                 const int32_t* __restrict__ block_tables, int num_seqs, int max_blocks_per_seq,
-                const int32_t* __restrict__ seq_idx, const int32_t* __restrict__ pos, int32_t* error_count) {
+                const int32_t* __restrict__ seq_idx, const int32_t* __restrict__ pos, int32_t* error_count,
+                const Divisor per_row, const Divisor per_head) {
     pdl_trigger();
     pdl_wait();
     __shared__ int s_block[kReadTokens], s_off[kReadTokens];
@@ -322,15 +331,15 @@ __global__ void __launch_bounds__(kThreads)
         s_off[threadIdx.x] = off;
     }
     __syncthreads();
-    const int per_head = head_dim / 16, pieces = num_kv_heads * per_head, total = 2 * nt * pieces;
+    const int pieces = (int)per_row.d, total = 2 * nt * pieces;  // 16-code pieces of a token's row; below 2^21
 #pragma unroll 4
     for (int i = threadIdx.x; i < total; i += kThreads) {
-        const int row = i / pieces, c = i - row * pieces, t = row >> 1;
+        const int row = per_row.div(i), c = i - row * pieces, t = row >> 1;
         const bool v_side = row & 1;
         const int pb = s_block[t];
         if (pb < 0) continue;
         const uint4 x = __ldg((v_side ? v_cache : k_cache) + ((size_t)pb * block_size + s_off[t]) * pieces + c);
-        const float s = __ldg((v_side ? v_scales : k_scales) + (size_t)pb * num_kv_heads + c / per_head);
+        const float s = __ldg((v_side ? v_scales : k_scales) + (size_t)pb * num_kv_heads + per_head.div(c));
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
         __align__(16) T y[16];
 #pragma unroll
@@ -390,6 +399,7 @@ int launch_write_fp8_block(const void* k_new, const void* v_new, int num_tokens,
     p.block_size = block_size;
     p.num_seqs = num_seqs;
     p.max_blocks_per_seq = max_blocks_per_seq;
+    p.per_pairs = Divisor((uint32_t)(2 * num_kv_heads));
     const int slices = (2 * num_kv_heads + kWarps - 1) / kWarps, gy = slices < 64 ? slices : 64;
     if (num_tokens <= kScanTokens) {
         auto kernel = head_dim == 128 ? write_scan_kernel<16> : head_dim == 64 ? write_scan_kernel<8> : write_scan_kernel<0>;
@@ -423,15 +433,16 @@ int launch_read_fp8_block(void* k_out, void* v_out, int num_tokens, int num_kv_h
                           cudaStream_t stream) {
     const dim3 grid((num_tokens + kReadTokens - 1) / kReadTokens), block(kThreads);
     const uint4 *kc = static_cast<const uint4*>(k_cache), *vc = static_cast<const uint4*>(v_cache);
+    const Divisor per_row((uint32_t)(num_kv_heads * (head_dim / 16))), per_head((uint32_t)(head_dim / 16));
     if (dtype == PA_F32)
         return launch_kernel(read_kernel<float>, grid, block, 0, stream, static_cast<float*>(k_out),
-                             static_cast<float*>(v_out), num_tokens, num_kv_heads, head_dim, kc, vc, k_scales,
+                             static_cast<float*>(v_out), num_tokens, num_kv_heads, kc, vc, k_scales,
                              v_scales, num_blocks, block_size, block_tables, num_seqs, max_blocks_per_seq, seq_idx, pos,
-                             error_count);
+                             error_count, per_row, per_head);
     return launch_kernel(read_kernel<__nv_bfloat16>, grid, block, 0, stream, static_cast<__nv_bfloat16*>(k_out),
-                         static_cast<__nv_bfloat16*>(v_out), num_tokens, num_kv_heads, head_dim, kc, vc, k_scales,
+                         static_cast<__nv_bfloat16*>(v_out), num_tokens, num_kv_heads, kc, vc, k_scales,
                          v_scales, num_blocks, block_size, block_tables, num_seqs, max_blocks_per_seq, seq_idx, pos,
-                         error_count);
+                         error_count, per_row, per_head);
 }
 
 }  // namespace pa

@@ -10,7 +10,7 @@ namespace pa {
 namespace {
 bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-// The split of pa_decode_fp8_block's contexts: partitions of whole 128-token stages, long enough that a partition's
+// The split of pa_decode_fp8_block's contexts: partitions of whole 128-token stages (powers of two), long enough that a partition's
 // partial result is small beside the codes it reads, short enough that the batch (at its longest context: the
 // lengths live on the device) gives every SM eight items; at most 128 partials per (sequence, head).  The last tenth of
 // the sequences is split in quarter partitions, so that the ends are less uneven.  Measured (64 sequences, 65,500 tokens,

@@ -124,18 +124,6 @@ struct Bars {
     __device__ uint64_t* drain() const { return item_full(2 * kItems + 1); }  // by both issuing warps
 };
 
-// Division of n < 2^30 by a number known to the host: n / d = (hi32(n mul) + n) >> shift with shift the least such that
-// 2^shift >= d and mul = floor(2^32 (2^shift - d) / d) + 1 (multiplication by a rounded-up reciprocal; checked against
-// the quotient for divisors up to 2^30).
-struct Divisor {
-    uint32_t mul, shift, d;
-    explicit Divisor(uint32_t d_ = 1) : mul(0), shift(0), d(d_) {
-        while ((1u << shift) < d) ++shift;
-        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - d)) / d + 1);
-    }
-    __device__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
-};
-
 // The kernel's own parameters: the plan's key tiles per span and spans per tile, and what items are numbered by.
 struct Spans {
     int tiles, count;
