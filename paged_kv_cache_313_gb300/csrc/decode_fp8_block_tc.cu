@@ -44,9 +44,9 @@
 //
 // Bound: HBM.  A stage is 32 KB, 0.74 us of an SM's share of the measured copy
 // bandwidth; the softmax of a stage is about 250 warp instructions.  Measured: 64
-// sequences, 32/8 heads, 65,500 tokens 32.5 us (135 MB: 0.62 of the copy
+// sequences, 32/8 heads, 65,500 tokens 31.9 us (135 MB: 0.63 of the copy
 // bandwidth, start, uneven ends and join included); 16 long contexts, 64/8 heads,
-// 189,395 tokens 74.9 us (0.77; CTAs take a stage every 3.0k cycles, 0.93); four
+// 189,395 tokens 74.0 us (0.78; CTAs take a stage every 3.0k cycles, 0.93); four
 // sequences of up to 40 tokens 6.8 us.  On the CUDA cores the first two took 805
 // and 3132 us.
 #include <atomic>

@@ -10,24 +10,30 @@ namespace pa {
 namespace {
 bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 
-// The split of pa_decode_fp8_block's contexts: partitions of whole 128-token stages (powers of two), long enough that a partition's
-// partial result is small beside the codes it reads, short enough that the batch (at its longest context: the
-// lengths live on the device) gives every SM eight items; at most 128 partials per (sequence, head).  The last tenth of
-// the sequences is split in quarter partitions, so that the ends are less uneven.  Measured (64 sequences, 65,500 tokens,
-// 32/8 heads; 16 long contexts, 189,395 tokens, 64/8 heads, us): partitions of 256 / 512 / 1024 / 2048 tokens 40.6 / 35.8
-// / 35.9 / 35.9 and 105.8 / 83.0 / 76.5 / 79.7; of 1024, with 0 / 10 / 20 / 30 % of the sequences in quarters 36.1 /
-// 34.4 / 34.6 / 35.1 and 76.6 / 76.8 / 81.6 / 81.5; four items per SM instead of eight, at 2048 tokens, 40.0.
+// The split of pa_decode_fp8_block's contexts: partitions of whole 128-token stages (powers of two), long enough that a
+// partition's partial result is small beside the codes it reads, short enough that the batch (at its longest context: the
+// lengths live on the device) gives every SM six items; at most 128 partials per (sequence, head).  The last fifth of the
+// sequences is split in half partitions, so that the ends are less uneven.  Measured, us (64 sequences, 65,500 tokens,
+// 32/8 heads; 16 long contexts, 189,395 tokens, 64/8 heads; 16 other long contexts, 32/8 heads; 64 contexts of 1000; 8 of
+// 2000 to 4000 tokens):
+//   a tenth in quarter partitions, eight items per SM   32.5   74.7   62.7   36.1   21.4
+//   a tenth in quarter partitions, six                  32.2   74.3   62.1   33.9   19.3
+//   15 % in halves, six                                 32.6   73.2   59.7   32.4   19.2
+//   a fifth in halves, six                              31.9   74.0   59.4   32.4   19.1
+//   a quarter in halves, six                            32.3   73.8   59.5   32.7   20.2
+//   a fifth in quarters, eight                          32.2   79.3   60.9   36.4   21.4
+//   partitions of 512 / 2048 (a tenth in quarters / eighths, eight)  34.0 / 32.6   80.0 / 78.1   63.0 / 66.6
 #ifndef PA_FP8_BLOCK_PARTITION
 #define PA_FP8_BLOCK_PARTITION 1024
 #endif
 #ifndef PA_FP8_BLOCK_ITEMS_PER_SM
-#define PA_FP8_BLOCK_ITEMS_PER_SM 8
+#define PA_FP8_BLOCK_ITEMS_PER_SM 6
 #endif
 #ifndef PA_FP8_BLOCK_TAIL_PCT
-#define PA_FP8_BLOCK_TAIL_PCT 10
+#define PA_FP8_BLOCK_TAIL_PCT 20
 #endif
 #ifndef PA_FP8_BLOCK_TAIL_DIV
-#define PA_FP8_BLOCK_TAIL_DIV 4
+#define PA_FP8_BLOCK_TAIL_DIV 2
 #endif
 DecodePlan plan_decode_fp8_block(int num_seqs, int num_kv_heads, int max_context_len, int num_sms) {
     auto splits = [&](long long part) { return max_context_len <= part ? 1LL : (max_context_len + part - 1) / part; };
