@@ -1009,7 +1009,7 @@ bool prefill_fp8_block_tc_supported(const PrefillParams& p) {
     if (p.head_dim != kD || p.group > 8 || B < 8 || B > 128 || (B & (B - 1)) != 0) return false;
     if (((uintptr_t)p.k_cache & 15) || ((uintptr_t)p.v_cache & 15) || ((uintptr_t)p.q & 15) || ((uintptr_t)p.out & 15))
         return false;
-    // (items: at most 2 * 152 more than the tiles of every chunk and kv head, by the spans' rule)
+    // (items: the tiles of every chunk and kv head, or, cut into spans, at most one a SM)
     return (long long)p.num_blocks * B < (1LL << 31) && p.num_blocks > 0 &&
            work_items(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group) < (1LL << 29);
 }
