@@ -543,9 +543,13 @@ __global__ void __launch_bounds__(kThreads, 2)
                 ok = false;
                 break;
             }
-            // the stage's maxima mx, the running ones, and what the state so far (alpha) and this stage's sums
-            // (beta) are multiplied with to come to the running maxima
-            float mx[kHeads], alpha[kHeads], beta[kHeads];
+            // the stage's maxima mx, the running ones, and what the state so far (where the stage's are larger: grow) or this
+            // stage's sums (where not) are multiplied with to come to the running maxima, as a factor that applies twice:
+            // the maxima have the V scales in them, so that they may be 2^220 apart between stages whose keys weigh the
+            // same, and the sums, which are divided by the scales, keep what one factor would flush to 0 (an output's
+            // part from so small a V is nothing, its product may flush)
+            float mx[kHeads], root[kHeads];
+            bool grow[kHeads];
 #pragma unroll
             for (int h4 = 0; h4 < kHeads / 4; ++h4) {
                 *reinterpret_cast<float4*>(mx + 4 * h4) = *reinterpret_cast<const float4*>(&red[b][0][4 * h4]);
@@ -560,13 +564,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             }
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
-                alpha[h] = beta[h] = 1.f;
-                if (mx[h] > m[h]) {
-                    alpha[h] = fast_exp2(m[h] - mx[h]);  // 0 at the first finite maximum
-                    m[h] = mx[h];
-                } else {
-                    beta[h] = mx[h] == -INFINITY ? 0.f : fast_exp2(mx[h] - m[h]);
-                }
+                grow[h] = mx[h] > m[h];
+                // (0 at the first finite maximum, and for a stage without one)
+                root[h] = mx[h] == -INFINITY ? 0.f : fast_exp2(0.5f * (fminf(m[h], mx[h]) - fmaxf(m[h], mx[h])));
+                m[h] = fmaxf(m[h], mx[h]);
             }
             uint32_t row[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
@@ -576,7 +577,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                 for (int j = 0; j < 2; ++j) {
                     const int h = 2 * h2 + j;
                     const float e = valid ? fast_exp2(x[h] - mx[h]) : 0.f;
-                    l[h] = fmaf(l[h], alpha[h], e * inv_vs * beta[h]);
+                    const float add = e * inv_vs;
+                    l[h] = fmaf((grow[h] ? l[h] : add) * root[h], root[h], grow[h] ? add : l[h]);
                     w[j] = e * unit;
                 }
                 const uint16_t hi = pack_e4m3x2(w[0], w[1]);
@@ -601,8 +603,9 @@ __global__ void __launch_bounds__(kThreads, 2)
             if (!ok) break;
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
-                acc[h] *= alpha[h];
-                bring[h] = beta[h] * (1.f / 256);
+                const float f = root[h] * root[h];
+                if (grow[h]) acc[h] *= f;
+                bring[h] = grow[h] ? 1.f / 256 : f * (1.f / 256);
             }
             if (!(g.flags & 2)) continue;
             // ---- end of the item: the sums over all tokens, then this thread's head dim of every head
@@ -694,7 +697,8 @@ __global__ void __launch_bounds__(128) decode_fp8_block_join_kernel(const Decode
     if (lane == 0) warp_m[warp] = mw;
     __syncthreads();
     const float m = fmaxf(fmaxf(warp_m[0], warp_m[1]), fmaxf(warp_m[2], warp_m[3]));
-    const float w = ml.y != 0.f ? ml.y * exp2f(ml.x - m) : 0.f;
+    const float e = exp2f(0.5f * (ml.x - m));  // (twice, as in the kernel above)
+    const float w = ml.y != 0.f ? ml.y * e * e : 0.f;
     weight[threadIdx.x] = w;
     const float ws = warp_sum(w);
     if (lane == 0) warp_w[warp] = ws;

@@ -754,7 +754,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                             // the products issued so far have to be done before O changes
                             wait(bars.pv_done((piece - 2) % kPieces), ((piece - 2) / kPieces) & 1);
                             tc_fence_after();
-                            const float alpha = mt == m ? 1.f : fast_exp2(m - mt);
+                            // (the factor's square root, twice for the sum: the maxima have the V scales in them and may
+                            // be 2^220 apart between keys of the same weight, and the sum, divided by the scales, keeps
+                            // what one factor would flush to 0)
+                            const float root = mt == m ? 1.f : fast_exp2(0.5f * (m - mt)), alpha = root * root;
 #pragma unroll 1
                             for (int q = 0; q < 8; ++q) {
                                 float o[16];
@@ -765,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 tmem_st16(t_o + q * 16, o);
                             }
                             tmem_wait_st();
-                            l *= alpha;
+                            l = l * root * root;
                         }
                         m = mt;
                         open = __any_sync(0xffffffffu, m == -INFINITY);
@@ -826,9 +829,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             // (the weight of a state without a valid key is 0, and its O is not looked at; that of a state of NaN scores,
             // which no maximum takes up, is NaN)
             const bool use_own = !(m == -INFINITY && l == 0.f), use_oth = !(mo == -INFINITY && lo == 0.f);
-            const float w_own = use_own ? fast_exp2(m - M) : 0.f, w_oth = use_oth ? fast_exp2(mo - M) : 0.f;
-            const float L = w_own * l + w_oth * lo, inv = L == 0.f ? 0.f : 1.f / L;
-            const float f_own = w_own * inv, f_oth = w_oth * inv;
+            const float w_own = use_own ? fast_exp2(0.5f * (m - M)) : 0.f, w_oth = use_oth ? fast_exp2(0.5f * (mo - M)) : 0.f;
+            const float L = w_own * l * w_own + w_oth * lo * w_oth, inv = L == 0.f ? 0.f : 1.f / L;
+            const float f_own = w_own * w_own * inv, f_oth = w_oth * w_oth * inv;
             const bool row_ok = my_pos < d.nq;
             const size_t row = (size_t)(d.row + my_pos) * p.num_q_heads + d.kvh * G + (r - my_pos * G);
             const bool direct = d.spans == 1;
@@ -946,14 +949,14 @@ __global__ void __launch_bounds__(128) prefill_fp8_block_join_kernel(const Prefi
 #pragma unroll
             for (int k = 0; k < kAhead; ++k)
                 if (i0 + k < count && ml[k].y != 0.f) mx = fmaxf(mx, ml[k].x);
-            const float f = m == mx ? 1.f : exp2f(m - mx);
+            const float r = m == mx ? 1.f : exp2f(0.5f * (m - mx));  // (twice, as in the kernel above)
             m = mx;
-            wsum *= f;
-            acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+            wsum = wsum * r * r;
+            acc = make_float4(acc.x * r * r, acc.y * r * r, acc.z * r * r, acc.w * r * r);
 #pragma unroll
             for (int k = 0; k < kAhead; ++k) {
                 if (i0 + k >= count || ml[k].y == 0.f) continue;
-                const float w = ml[k].y * exp2f(ml[k].x - m);
+                const float e = exp2f(0.5f * (ml[k].x - m)), w = ml[k].y * e * e;
                 wsum += w;
                 acc.x = fmaf(w, o[k].x, acc.x);
                 acc.y = fmaf(w, o[k].y, acc.y);
