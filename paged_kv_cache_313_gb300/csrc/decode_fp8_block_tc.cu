@@ -502,7 +502,8 @@ __global__ void __launch_bounds__(kThreads, 2)
             const float vs = reinterpret_cast<const float*>(smem + kVs)[slot * kMaxBlocks + (t >> log2b)];
             // (a V below `hold` adds nothing, its key's weight still counts in the sum)
             const float hold = fmaxf(g.vmax * kHold, kLeastScale);
-            const float off = __log2f(fmaxf(vs, hold)), inv_vs = fast_exp2(-off), unit = vs >= hold ? 256.f : 0.f;
+            const float off = __log2f(fmaxf(vs, hold)), unit = vs >= hold ? 256.f : 0.f;
+            const float inv_vs = exp2f(-off);  // (a subnormal beyond a scale of 2^126, where fast_exp2 gives 0)
             if (g.flags & 1) {
                 if (!mbar_wait_warp(&q_ready[items & 1], (items >> 1) & 1)) {
                     ok = false;

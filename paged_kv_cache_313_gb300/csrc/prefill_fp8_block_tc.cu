@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             top = fmaxf(top, redux_max(sc.y));
                             ks = sc.x * fabsf(p.scale_log2);
                             off = __log2f(fmaxf(sc.y, fmaxf(top * kHold, kLeastScale)));
-                            inv_vs = fast_exp2(-off);
+                            inv_vs = exp2f(-off);  // (a subnormal beyond a scale of 2^126, where fast_exp2 gives 0)
                         }
                     }
                     const uint32_t mine = (valid >> (l * bpt)) & all;

@@ -83,3 +83,20 @@ def test_prefill_keeps_the_weight_of_zeros_in_other_blocks(B, n, chunks, exponen
     pools = _pools(rng, n // B + 1, B, 8)
     _mark_zeros(pools, order, n // B, exponent)
     _prefill(pools, np.arange(n // B)[None], n, chunks, 16, 16, exponent, 0.05)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("exponent", [125, 126, 127])
+def test_the_largest_scales(exponent):
+    """V scales up to the largest powers of two that a float holds, K scales that the queries bring back; values that stay
+    within bf16's range."""
+    rng = np.random.default_rng(exponent)
+    n, B = 640, 16
+    pools = _pools(rng, n // B, B, 8)
+    pools[1][:] &= 0xbf  # values below 2
+    pools[2][:], pools[3][:] = np.float32(2.0 ** 100), np.float32(2.0 ** exponent)
+    table = np.arange(n // B)[None]
+    for rows in (1, 128):  # partitions of 128 tokens, joined, and of several stages
+        _decode(pools, table, n, rows, 32, exponent, 2.0 ** -104)
+    for chunks in (1, 20):
+        _prefill(pools, table, n, chunks, 16, 32, exponent, 2.0 ** -104)
