@@ -441,7 +441,8 @@ PA_API int pa_read_kv_paged_fp8_block(void* k_out, void* v_out, int num_tokens, 
  * infinity or a NaN gives NaN, as does a NaN code in K or (in its column) in V
  * for the queries that see its token.  Shapes, context
  * clamping and the workspace's rules are pa_decode's
- * (pa_decode_fp8_block_workspace_size bytes).
+ * (pa_decode_fp8_block_workspace_size bytes, which serve every call of no more
+ * sequences and no longer contexts as well).
  */
 PA_API size_t pa_decode_fp8_block_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                                  int block_size, int max_context_len);
@@ -457,7 +458,10 @@ PA_API int pa_decode_fp8_block(void* out, const void* q, int num_seqs, int num_q
  * bf16, the chunks' own K and V written by pa_write_kv_paged_fp8_block first.
  * max_context_len bounds q_start_pos[c] + n_c (keys at or beyond it are not
  * read, and counted).  workspace: pa_prefill_fp8_block_workspace_size bytes
- * (may be 0, then NULL is fine), 256-byte aligned; it needs no zeroing.  One
+ * (may be 0, then NULL is fine), 256-byte aligned; it needs no zeroing, and
+ * serves every call of no more chunks, queries and context as well (a call
+ * whose q has rows behind its chunks may cut its keys less than with a
+ * workspace of its own).  One
  * workspace must not serve two calls that may overlap on the GPU.  Scales as
  * for pa_decode_fp8_block, shapes as for pa_prefill_chunk.
  */

@@ -1,7 +1,8 @@
 // pa_api_fp8_block.cu — C ABI of the e4m3 pools with a scale per (block, kv
 // head): argument checks and dispatch.  Like pa_api.cu, every entry point
 // validates on the host and launches nothing when a check fails.
-#include <cmath>
+#include <algorithm>
+#include <climits>
 #include <cstdint>
 
 #include "pa_internal.cuh"
@@ -45,6 +46,21 @@ DecodePlan plan_decode_fp8_block(int num_seqs, int num_kv_heads, int max_context
     while (splits(small) > 128) small *= 2;
     const int tail = small < part ? (int)((long long)num_seqs * PA_FP8_BLOCK_TAIL_PCT / 100) : 0;
     return DecodePlan{(int)part, (int)splits(tail ? small : part), (int)small, num_seqs - tail};
+}
+
+// The most partial rows of a kv head that the plan of any call of up to num_seqs sequences and max_context_len tokens has,
+// so that one workspace serves a batch that shrinks (a smaller one is cut finer, and may have more of them than a larger).
+// With PA_FP8_BLOCK_PARTITION tokens a partition, sequences of half ones have the most.  Where the plan halved its
+// partitions, twice as long ones gave fewer than PA_FP8_BLOCK_ITEMS_PER_SM items per SM: halving them doubles the items at
+// most, and the tail's shorter ones do so PA_FP8_BLOCK_TAIL_DIV-fold; no partition is below 128 tokens.
+long long most_partials(int num_seqs, int num_kv_heads, int max_context_len, int num_sms) {
+    auto splits = [&](long long part) {
+        const long long n = max_context_len <= part ? 1LL : (max_context_len + part - 1) / part;
+        return n < 128 ? n : 128LL;
+    };
+    const long long halved = (2LL * PA_FP8_BLOCK_TAIL_DIV * PA_FP8_BLOCK_ITEMS_PER_SM * num_sms - 1) / num_kv_heads;
+    return std::max(num_seqs * splits(PA_FP8_BLOCK_PARTITION / PA_FP8_BLOCK_TAIL_DIV),
+                    std::min(num_seqs * splits(128), halved));
 }
 
 // Row shape of the write and the read back: 16-byte pieces of codes, blocks of at most 1024 slots.
@@ -117,8 +133,10 @@ size_t pa_decode_fp8_block_workspace_size(int num_seqs, int num_q_heads, int num
         return 0;
     int num_sms = 0;
     if (check_device(&num_sms) != PA_OK) return 0;
-    const DecodePlan plan = plan_decode_fp8_block(num_seqs, num_kv_heads, max_context_len, num_sms);
-    return decode_workspace_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, plan.max_splits).total;
+    // (as many sequences of one partial each)
+    const long long partials = most_partials(num_seqs, num_kv_heads, max_context_len, num_sms);
+    if (partials > INT_MAX) return 0;
+    return decode_workspace_layout((int)partials, num_q_heads, num_kv_heads, head_dim, 1).total;
 }
 
 int pa_decode_fp8_block(void* out, const void* q, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
@@ -230,10 +248,10 @@ int pa_prefill_chunk_fp8_block(void* out, const void* q, const int32_t* cu_q_len
     p.max_context_len = max_context_len;
     p.scale_log2 = scale * 1.4426950408889634f;
     if (!prefill_fp8_block_tc_supported(p)) return launch_prefill_fp8_block_fma(p, static_cast<cudaStream_t>(stream));
-    const size_t need = prefill_fp8_block_workspace(num_chunks, total_q, max_q_len, num_q_heads, num_kv_heads,
-                                                    max_context_len, num_sms);
+    const size_t need = prefill_fp8_block_need(p, num_sms);
     if (need > 0 && (!workspace || workspace_bytes < need || !aligned(workspace, 256))) return PA_ERR_WORKSPACE;
-    return launch_prefill_fp8_block_tc(p, workspace, num_sms, static_cast<cudaStream_t>(stream));
+    return launch_prefill_fp8_block_tc(p, workspace, need > 0 ? workspace_bytes : 0, num_sms,
+                                       static_cast<cudaStream_t>(stream));
 }
 
 }  // extern "C"

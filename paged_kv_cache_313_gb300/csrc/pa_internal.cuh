@@ -194,11 +194,14 @@ bool decode_fp8_block_tc_supported(const DecodeParams& p);
 int launch_decode_fp8_block_tc(const DecodeParams& p, int num_sms, cudaStream_t stream);
 int launch_decode_fp8_block_join(const DecodeParams& p, cudaStream_t stream);
 int launch_decode_fp8_block_fma(const DecodeParams& p, cudaStream_t stream);
-// Workspace of the block-scaled prefill: the partial rows of query tiles whose keys are cut into spans.
+// Workspace of the block-scaled prefill, the partial rows of query tiles whose keys are cut into spans: what serves calls
+// of up to these sizes, and what one call needs.
 size_t prefill_fp8_block_workspace(int num_chunks, int total_q, int max_q_len, int num_q_heads, int num_kv_heads,
                                    int max_context_len, int num_sms);
 bool prefill_fp8_block_tc_supported(const PrefillParams& p);
-int launch_prefill_fp8_block_tc(const PrefillParams& p, void* workspace, int num_sms, cudaStream_t stream);
+size_t prefill_fp8_block_need(const PrefillParams& p, int num_sms);
+int launch_prefill_fp8_block_tc(const PrefillParams& p, void* workspace, size_t workspace_bytes, int num_sms,
+                                cudaStream_t stream);
 int launch_prefill_fp8_block_fma(const PrefillParams& p, cudaStream_t stream);
 int launch_copy_blocks(void* k_cache, void* v_cache, int num_blocks, int block_size, int row_bytes,
                        const int32_t* src, const int32_t* dst, const int32_t* num_valid, int num_copies,

@@ -50,6 +50,7 @@
 // PFLOP/s, 0.62 of cuBLAS bf16) and 396 over 16-token blocks, whose copies are
 // four times as many; four chunks of 512 queries at short offsets, 32/8 heads,
 // 33.4 us; 37 queries at 2,955 17.4 us.  On the CUDA cores 184, 5.0 and 1.3 ms.
+#include <algorithm>
 #include <climits>
 
 #include "pa_internal.cuh"
@@ -976,35 +977,58 @@ long long work_items(int num_chunks, int max_q_len, int num_kv_heads, int group)
     return (long long)((max_q_len + ppt - 1) / ppt) * num_chunks * num_kv_heads;
 }
 
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+size_t partial_bytes(size_t rows) { return rows == 0 ? 0 : up256(rows * kD * sizeof(float)) + up256(rows * sizeof(float2)); }
+
 // Key tiles per span and spans per query tile.  Where the tiles alone leave half of the SMs idle their keys are cut so
 // that the items make up one round of the GPU, into spans of at least two key tiles (a span's partial rows cost about
 // one key tile's time to store and join): 37 queries at 2,955, 8 kv heads, 17.4 us, uncut 36.2; but 160 query tiles of
 // 21 key tiles cut in two 64.9, uncut 51.8.  The count comes from the largest context, the lengths live on the device.
-Spans plan_spans(int num_chunks, int max_q_len, int num_kv_heads, int group, int max_context_len, int num_sms) {
+// No more spans than `workspace_bytes` holds the partial rows of, for all `total_rows` (query, head) rows of q.
+Spans plan_spans(int num_chunks, int max_q_len, int num_kv_heads, int group, int max_context_len, int num_sms,
+                 size_t total_rows, size_t workspace_bytes) {
     const int tiles = max_context_len > 0 ? (max_context_len - 1) / kTile + 1 : 1;
     const long long items = work_items(num_chunks, max_q_len, num_kv_heads, group);
     long long want = items > 0 && items < num_sms ? num_sms / items : 1;
     if (want > tiles / 2) want = tiles / 2;
     Spans s;
-    s.tiles = tiles;
     s.o = nullptr;
     s.ml = nullptr;
-    if (want > 1) s.tiles = (int)((tiles + want - 1) / want);
-    s.count = (tiles + s.tiles - 1) / s.tiles;
+    do {
+        s.tiles = want > 1 ? (int)((tiles + want - 1) / want) : tiles;
+        s.count = (tiles + s.tiles - 1) / s.tiles;
+    } while (s.count > 1 && partial_bytes(s.count * total_rows) > workspace_bytes && --want > 0);
     return s;
 }
 
-size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+// The rows of q that a call's chunks can have: there may be others behind the last one.
+size_t chunk_rows(int num_chunks, int total_q, int max_q_len, int num_q_heads) {
+    return (size_t)std::min<long long>(total_q, (long long)num_chunks * max_q_len) * num_q_heads;
+}
 
 }  // namespace
 
+// What the calls of these sizes need, with room for the rows behind the chunks; and at least what every call of no more
+// chunks, queries and context needs: such a call has more spans where it has fewer tiles, at most one item a SM.
 size_t prefill_fp8_block_workspace(int num_chunks, int total_q, int max_q_len, int num_q_heads, int num_kv_heads,
                                    int max_context_len, int num_sms) {
+    const int group = num_q_heads / num_kv_heads;
+    const size_t all = (size_t)total_q * num_q_heads;
+    const Spans s = plan_spans(num_chunks, max_q_len, num_kv_heads, group, max_context_len, num_sms, all, SIZE_MAX);
+    const size_t these = s.count > 1 ? partial_bytes(s.count * all) : 0;
+    const size_t tiles = max_context_len > 0 ? (max_context_len - 1) / kTile + 1 : 1;
+    const size_t count = std::min<size_t>(num_sms / num_kv_heads, tiles / 2);
+    if (count < 2) return these;
+    const size_t rows = std::min(count * chunk_rows(num_chunks, total_q, max_q_len, num_q_heads),
+                                 (size_t)num_sms * (kTile / group) / num_kv_heads * num_q_heads);
+    return std::max(these, partial_bytes(rows));
+}
+
+size_t prefill_fp8_block_need(const PrefillParams& p, int num_sms) {
+    const size_t rows = chunk_rows(p.num_chunks, p.total_q, p.max_q_len, p.num_q_heads);
     const Spans s =
-        plan_spans(num_chunks, max_q_len, num_kv_heads, num_q_heads / num_kv_heads, max_context_len, num_sms);
-    if (s.count <= 1) return 0;
-    const size_t rows = (size_t)s.count * total_q * num_q_heads;
-    return up256(rows * kD * sizeof(float)) + up256(rows * sizeof(float2));
+        plan_spans(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group, p.max_context_len, num_sms, rows, SIZE_MAX);
+    return s.count > 1 ? partial_bytes(s.count * rows) : 0;
 }
 
 bool prefill_fp8_block_tc_supported(const PrefillParams& p) {
@@ -1017,7 +1041,8 @@ bool prefill_fp8_block_tc_supported(const PrefillParams& p) {
            work_items(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group) < (1LL << 29);
 }
 
-int launch_prefill_fp8_block_tc(const PrefillParams& p, void* workspace, int num_sms, cudaStream_t stream) {
+int launch_prefill_fp8_block_tc(const PrefillParams& p, void* workspace, size_t workspace_bytes, int num_sms,
+                                cudaStream_t stream) {
     CUtensorMap tmk, tmv;
     int rc = pool_tensor_map_rows(&tmk, p.k_cache, p.num_blocks, p.block_size, p.num_kv_heads, kD, true);
     if (rc != PA_OK) return rc;
@@ -1027,11 +1052,12 @@ int launch_prefill_fp8_block_tc(const PrefillParams& p, void* workspace, int num
                   : p.block_size == 16 ? prefill_fp8_block_tc_kernel<16>
                                        : prefill_fp8_block_tc_kernel<32>;
     if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(kernel), kSmemBytes)) != PA_OK) return rc;
-    Spans s = plan_spans(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group, p.max_context_len, num_sms);
+    const size_t total_rows = (size_t)p.total_q * p.num_q_heads;
+    Spans s = plan_spans(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group, p.max_context_len, num_sms, total_rows,
+                         workspace_bytes);
     if (s.count > 1) {
-        const size_t rows = (size_t)s.count * p.total_q * p.num_q_heads;
         s.o = static_cast<float*>(workspace);
-        s.ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + up256(rows * kD * sizeof(float)));
+        s.ml = reinterpret_cast<float2*>(static_cast<char*>(workspace) + up256(s.count * total_rows * kD * sizeof(float)));
     }
     const long long items = work_items(p.num_chunks, p.max_q_len, p.num_kv_heads, p.group) * s.count;
     s.items = (int)items;

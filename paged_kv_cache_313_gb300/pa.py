@@ -445,7 +445,7 @@ def pa_read_kv_paged_fp8_block(k_cache, v_cache, k_scales, v_scales, block_table
 
 def new_decode_fp8_block_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
                                    device=None) -> torch.Tensor:
-    """A zeroed workspace of the size pa_decode_fp8_block needs (reusable across calls on one stream)."""
+    """A zeroed workspace for pa_decode_fp8_block calls of up to these sizes (reusable across calls on one stream)."""
     n = int(lib().pa_decode_fp8_block_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
                                                      max_context_len))
     if n == 0:
@@ -465,7 +465,7 @@ def pa_decode_fp8_block(q, k_cache, v_cache, k_scales, v_scales, block_tables, c
 
 def new_prefill_fp8_block_workspace(num_chunks, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
                                     max_context_len, device=None) -> torch.Tensor | None:
-    """A workspace of the size pa_prefill_chunk_fp8_block needs for these sizes (None when it needs none)."""
+    """A workspace for pa_prefill_chunk_fp8_block calls of up to these sizes (None when they need none)."""
     n = int(lib().pa_prefill_fp8_block_workspace_size(num_chunks, total_q, max_q_len, num_q_heads, num_kv_heads,
                                                       head_dim, block_size, max_context_len))
     return torch.empty(n, dtype=torch.uint8, device=device or "cuda") if n else None
