@@ -122,6 +122,12 @@ struct Workspace {
 
 const int32_t* i32(void* p) { return static_cast<const int32_t*>(p); }
 
+// Without the interpreter lock while it lives: a launch may wait for room in its queue, and other threads go on meanwhile.
+struct Unlocked {
+    PyThreadState* state = PyEval_SaveThread();
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // Runs `call(stream)` with the pools' device current, on the given stream (None: the device's current one).
 template <typename F>
 int on_device(const Pools& p, PyObject* stream, F call) {
@@ -138,6 +144,7 @@ int on_device(const Pools& p, PyObject* stream, F call) {
         Py_DECREF(raw);
         if (PyErr_Occurred()) throw Refused{};
     }
+    const Unlocked unlocked;
     return call(s);
 }
 
