@@ -128,22 +128,40 @@ struct Unlocked {
     ~Unlocked() { PyEval_RestoreThread(state); }
 };
 
+// The handle of a stream given as an object with cuda_stream, or as a number.
+cudaStream_t handle_of(PyObject* stream) {
+    PyObject* raw = PyObject_HasAttrString(stream, "cuda_stream") ? PyObject_GetAttrString(stream, "cuda_stream")
+                                                                 : (Py_INCREF(stream), stream);
+    if (!raw) throw Refused{};
+    void* s = PyLong_AsVoidPtr(raw);
+    Py_DECREF(raw);
+    if (PyErr_Occurred()) throw Refused{};
+    return static_cast<cudaStream_t>(s);
+}
+
+// Memory for an output on the pools' device.  Where the caller gives a stream it is that stream's, as if allocated with it
+// current: memory that the current stream has freed may still be in use by its earlier work, which the given stream does
+// not wait for.  The current stream, where the caller takes the output up, is noted as a user.
+at::Tensor new_output(const Pools& p, PyObject* stream, at::IntArrayRef shape, at::ScalarType type) {
+    const auto options = p.k.options().dtype(type);
+    if (stream == Py_None || !p.k.is_cuda()) return at::empty(shape, options);
+    const c10::DeviceIndex device = p.k.device().index();
+    const c10::cuda::CUDAStream current = c10::cuda::getCurrentCUDAStream(device);
+    cudaStream_t handle = handle_of(stream);
+    if (handle == cudaStreamLegacy) handle = nullptr;
+    if (handle == current.stream()) return at::empty(shape, options);
+    const c10::cuda::CUDAStreamGuard guard(c10::cuda::getStreamFromExternal(handle, device));
+    at::Tensor t = at::empty(shape, options);
+    t.record_stream(current.unwrap());
+    return t;
+}
+
 // Runs `call(stream)` with the pools' device current, on the given stream (None: the device's current one).
 template <typename F>
 int on_device(const Pools& p, PyObject* stream, F call) {
     if (!p.k.is_cuda()) refuse(PyExc_ValueError, "the pools must be CUDA tensors");
     const c10::cuda::CUDAGuard guard(p.k.device());
-    void* s = nullptr;
-    if (stream == Py_None) {
-        s = c10::cuda::getCurrentCUDAStream(p.k.device().index()).stream();
-    } else {
-        PyObject* raw = PyObject_HasAttrString(stream, "cuda_stream") ? PyObject_GetAttrString(stream, "cuda_stream")
-                                                                     : (Py_INCREF(stream), stream);
-        if (!raw) throw Refused{};
-        s = PyLong_AsVoidPtr(raw);
-        Py_DECREF(raw);
-        if (PyErr_Occurred()) throw Refused{};
-    }
+    void* s = stream == Py_None ? c10::cuda::getCurrentCUDAStream(p.k.device().index()).stream() : handle_of(stream);
     const Unlocked unlocked;
     return call(s);
 }
@@ -219,7 +237,7 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
             refuse(PyExc_TypeError, std::string("unsupported dtype ") + type_name(type) + " (float32 or bfloat16)");
         const int64_t shape[3] = {T, p.heads, p.dim};
         auto out = [&](PyObject* o, const char* name) {
-            return o != Py_None ? tensor(o, name) : at::empty(shape, p.k.options().dtype(type));
+            return o != Py_None ? tensor(o, name) : new_output(p, a[11], shape, type);
         };
         const at::Tensor ko = out(a[7], "k_out"), vo = out(a[8], "v_out");
         if (!ko.sizes().equals(shape) || !vo.sizes().equals(shape) || vo.scalar_type() != type)
@@ -244,10 +262,10 @@ PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     });
 }
 
-at::Tensor out_like(const Pools& p, PyObject* o, const at::Tensor& q) {
+at::Tensor out_like(const Pools& p, PyObject* o, const at::Tensor& q, PyObject* stream) {
     if (!p.k.is_cuda()) refuse(PyExc_ValueError, "the pools must be CUDA tensors");
     (void)p.at(q, "q", at::kBFloat16);  // before anything is allocated like it
-    return o == Py_None ? at::empty_like(q) : tensor(o, "out");
+    return o == Py_None ? new_output(p, stream, q.sizes(), at::kBFloat16) : tensor(o, "out");
 }
 
 // q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, max_context_len, scale, workspace, out,
@@ -266,7 +284,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int max_ctx = int_of(a[7]);
         const float scale = float_of(a[8]);
         const Workspace ws(p, a[9]);
-        const at::Tensor out = out_like(p, a[10], q);
+        const at::Tensor out = out_like(p, a[10], q, a[12]);
         void *op = p.at(out, "out", at::kBFloat16, true), *qp = p.at(q, "q", at::kBFloat16), *kp = p.kp(), *vp = p.vp();
         float *ks = p.ksp(), *vs = p.vsp();
         const int32_t *btp = i32(p.at(bt, "block_tables", at::kInt)), *cp = i32(p.at(ctx, "context_lens", at::kInt));
@@ -299,7 +317,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const int max_q = int_of(a[4]), max_ctx = int_of(a[11]);
         const float scale = float_of(a[12]);
         const Workspace ws(p, a[13]);
-        const at::Tensor out = out_like(p, a[14], q);
+        const at::Tensor out = out_like(p, a[14], q, a[16]);
         void *op = p.at(out, "out", at::kBFloat16, true), *qp = p.at(q, "q", at::kBFloat16), *kp = p.kp(), *vp = p.vp();
         float *ks = p.ksp(), *vs = p.vsp();
         const int32_t *cup = i32(p.at(cu, "cu_q_lens", at::kInt)), *st = i32(p.at(start, "q_start_pos", at::kInt)),

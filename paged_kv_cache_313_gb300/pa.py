@@ -3,6 +3,9 @@ CUDA tensors in and out.  Argument marshalling only (in ctypes, and in the
 compiled module _pa_bind.so for the calls over block-scaled e4m3 pools) — every step runs in the
 library's CUDA kernels.  There is no CPU fallback: if the library is missing
 or fails to load, every call raises.
+
+A call runs on the current stream, or on `stream`.  An output that is not given is then allocated for that stream, as if
+it were current; the current one is noted as a user of it.  Inputs are the caller's to order and to keep.
 """
 from __future__ import annotations
 

@@ -48,3 +48,63 @@ def test_a_full_launch_queue_stops_no_other_thread():
     torch.cuda.synchronize()
     assert times["end"] - times["start"] > 0.2, "the queue took every call at once: the test shows nothing"
     assert gap < 0.1, f"another thread stood still for {gap:.2f} s"
+
+
+def _calls():
+    """Calls that take a stream and allocate their output, by name; their inputs are ready and kept."""
+    args = _decode_args()
+    q, *pools, bt, ctx, n, scale, _ = args
+    cu, start, seq, pos = _i32([0, 1]), _i32([n - 1]), _i32([0]), _i32(range(4))
+    first = _i32([0] * 4)
+    return {
+        "decode": lambda stream: pa.pa_decode_fp8_block(*args, stream=stream),
+        "prefill": lambda stream: pa.pa_prefill_chunk_fp8_block(q, cu, start, seq, 1, *pools, bt, ctx, n, scale,
+                                                                stream=stream),
+        "read": lambda stream: pa.pa_read_kv_paged_fp8_block(*pools, bt, first, pos, stream=stream)[0],
+    }
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["decode", "prefill", "read"])
+def test_outputs_that_are_not_given_belong_to_the_given_stream(name):
+    """Memory that other streams may still use is not handed out: of what the current stream freed, to a call on another;
+    of a dropped output, to the current stream; of an output in use by the current stream, to the given one."""
+    call = _calls()[name]
+    want = call(None)
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    cycles = int(2e8)  # a tenth of a second
+
+    held = torch.empty_like(want)
+    freed = held.data_ptr()
+    torch.cuda._sleep(cycles)
+    held.fill_(3)  # still to come when the call below runs
+    del held
+    got = call(other)
+    assert got.data_ptr() != freed
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+    with torch.cuda.stream(other):
+        torch.cuda._sleep(cycles)
+    got = call(other)
+    dropped = got.data_ptr()
+    del got
+    again = torch.empty_like(want)
+    assert again.data_ptr() != dropped
+    torch.cuda.synchronize()
+
+    got = call(other)
+    torch.cuda.current_stream().wait_stream(other)
+    torch.cuda._sleep(cycles)
+    copy, used = got.clone(), got.data_ptr()
+    del got
+    with torch.cuda.stream(other):
+        more = [torch.empty_like(want) for _ in range(4)]
+    assert all(m.data_ptr() != used for m in more)
+    torch.cuda.synchronize()
+    assert torch.equal(copy, want)
+    for handle in (other.cuda_stream, torch.cuda.default_stream().cuda_stream):  # a stream given as a number
+        got = call(handle)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
