@@ -137,6 +137,21 @@ def _stream(stream) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _new_output(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for an output that is not given: the given stream's, as if allocated with it current.  (What the current
+    stream has freed may still be in use by its earlier work, which the given stream does not wait for.)"""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    handle, current = _stream(stream), torch.cuda.current_stream(device)
+    if handle == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    legacy = handle in (0, 1)  # the default stream, by either of its names
+    with torch.cuda.stream(torch.cuda.default_stream(device) if legacy else torch.cuda.ExternalStream(handle, device)):
+        out = torch.empty(shape, dtype=dtype, device=device)
+    out.record_stream(current)
+    return out
+
+
 def pa_version() -> int:
     return lib().pa_version()
 
@@ -146,7 +161,7 @@ def pa_slot_mapping(block_tables, seq_idx, pos, block_size: int, num_blocks: int
     """slot = block_tables[seq, pos // B] * B + pos % B for each new token (int64, -1 = skip)."""
     T = seq_idx.numel()
     if slot_mapping is None:
-        slot_mapping = torch.empty(T, dtype=torch.int64, device=seq_idx.device)
+        slot_mapping = _new_output((T,), torch.int64, seq_idx.device, stream)
     S, W = block_tables.shape
     _check("pa_slot_mapping", lib().pa_slot_mapping(
         _dev(block_tables, "block_tables", torch.int32), S, W, _dev(seq_idx, "seq_idx", torch.int32),
@@ -235,7 +250,7 @@ def pa_decode(q, k_cache, v_cache, block_tables, context_lens, max_context_len: 
     if D2 != D:
         raise ValueError("head_dim of q and k_cache differ")
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_output(q.shape, q.dtype, q.device, stream)
     _check("pa_decode", lib().pa_decode(
         _dev(out, "out", q.dtype, host_ok=True),
         _dev(q, "q"), N, Hq, Hkv, D, _dtype_code(q), _dev(k_cache, "k_cache", q.dtype),
@@ -256,7 +271,7 @@ def pa_decode_fp8(q, k_cache, v_cache, block_tables, context_lens, max_context_l
     if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8:
         raise TypeError("fp8 pools are uint8 tensors of e4m3 codes")
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_output(q.shape, q.dtype, q.device, stream)
     _check("pa_decode_fp8", lib().pa_decode_fp8(
         _dev(out, "out", torch.bfloat16, host_ok=True),
         _dev(q, "q", torch.bfloat16), N, Hq, Hkv, D, _dev(k_cache, "k_cache"),
@@ -279,7 +294,7 @@ def pa_decode_write_fp8(q, k_cache, v_cache, block_tables, context_lens, max_con
     if k_cache.dtype != torch.uint8 or v_cache.dtype != torch.uint8:
         raise TypeError("fp8 pools are uint8 tensors of e4m3 codes")
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_output(q.shape, q.dtype, q.device, stream)
     _check("pa_decode_write_fp8", lib().pa_decode_write_fp8(
         _dev(out, "out", torch.bfloat16, host_ok=True),
         _dev(q, "q", torch.bfloat16), N, Hq, Hkv, D, _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), P, B,
@@ -301,7 +316,7 @@ def pa_decode_write(q, k_cache, v_cache, block_tables, context_lens, max_context
     if D2 != D or tuple(k_new.shape) != (N, Hkv, D) or tuple(v_new.shape) != (N, Hkv, D):
         raise ValueError("shapes of q, k_cache, k_new, v_new disagree")
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_output(q.shape, q.dtype, q.device, stream)
     _check("pa_decode_write", lib().pa_decode_write(
         _dev(out, "out", q.dtype, host_ok=True),
         _dev(q, "q"), N, Hq, Hkv, D, _dtype_code(q), _dev(k_cache, "k_cache", q.dtype),
@@ -333,7 +348,7 @@ def pa_decode_cascade(q, k_cache, v_cache, block_tables, context_lens, max_conte
     if D2 != D:
         raise ValueError("head_dim of q and k_cache differ")
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_output(q.shape, q.dtype, q.device, stream)
     G = group_offsets.numel() - 1
     _check("pa_decode_cascade", lib().pa_decode_cascade(
         _dev(out, "out", q.dtype, host_ok=True),
@@ -358,7 +373,7 @@ def pa_decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, max_conte
     if D2 != D:
         raise ValueError("head_dim of q and k_cache differ")
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_output(q.shape, q.dtype, q.device, stream)
     _check("pa_decode_noalloc", lib().pa_decode_noalloc(
         _dev(out, "out", q.dtype, host_ok=True),
         _dev(q, "q"), N, Hq, Hkv, D, _dtype_code(q), _dev(k_cache, "k_cache", q.dtype),
@@ -382,7 +397,7 @@ def pa_prefill_chunk(q, cu_q_lens, q_start_pos, seq_of_chunk, max_q_len: int, k_
     if D2 != D:
         raise ValueError("head_dim of q and k_cache differ")
     if out is None:
-        out = torch.empty_like(q)
+        out = _new_output(q.shape, q.dtype, q.device, stream)
     C = q_start_pos.numel()
     ws_ptr = _dev(workspace, "workspace") if workspace is not None else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
@@ -515,7 +530,7 @@ def pa_map_to_kernel_blocks(mgr_tables, ratio: int, kernel_tables=None, stream=N
     mgr_tables[s, j // ratio] * ratio + j % ratio (-1 for -1)."""
     S, W = mgr_tables.shape
     if kernel_tables is None:
-        kernel_tables = torch.empty(S, W * ratio, dtype=torch.int32, device=mgr_tables.device)
+        kernel_tables = _new_output((S, W * ratio), torch.int32, mgr_tables.device, stream)
     _check("pa_map_to_kernel_blocks", lib().pa_map_to_kernel_blocks(
         _dev(mgr_tables, "mgr_tables", torch.int32), S, W, int(ratio),
         _dev(kernel_tables, "kernel_tables", torch.int32), kernel_tables.shape[1], _stream(stream)))

@@ -1,4 +1,4 @@
-"""The compiled binding beside other threads and streams."""
+"""The Python binding beside other threads and streams."""
 import threading
 import time
 
@@ -56,16 +56,23 @@ def _calls():
     q, *pools, bt, ctx, n, scale, _ = args
     cu, start, seq, pos = _i32([0, 1]), _i32([n - 1]), _i32([0]), _i32(range(4))
     first = _i32([0] * 4)
+    kb, vb = (torch.ones(8, 16, 1, 128, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    ws = pa.new_decode_workspace(1, 4, 1, 128, 16, n)
     return {
         "decode": lambda stream: pa.pa_decode_fp8_block(*args, stream=stream),
         "prefill": lambda stream: pa.pa_prefill_chunk_fp8_block(q, cu, start, seq, 1, *pools, bt, ctx, n, scale,
                                                                 stream=stream),
         "read": lambda stream: pa.pa_read_kv_paged_fp8_block(*pools, bt, first, pos, stream=stream)[0],
+        "bf16 decode": lambda stream: pa.pa_decode(q, kb, vb, bt, ctx, n, scale, ws, stream=stream),
+        "bf16 prefill": lambda stream: pa.pa_prefill_chunk(q, cu, start, seq, 1, kb, vb, bt, ctx, scale, stream=stream),
+        "slots": lambda stream: pa.pa_slot_mapping(bt, first, pos, 16, 8, stream=stream),
+        "tables": lambda stream: pa.pa_map_to_kernel_blocks(bt, 2, stream=stream),
     }
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("name", ["decode", "prefill", "read"])
+@pytest.mark.parametrize("name", ["decode", "prefill", "read", "bf16 decode", "bf16 prefill", "slots",
+                                  "tables"])
 def test_outputs_that_are_not_given_belong_to_the_given_stream(name):
     """Memory that other streams may still use is not handed out: of what the current stream freed, to a call on another;
     of a dropped output, to the current stream; of an output in use by the current stream, to the given one."""
