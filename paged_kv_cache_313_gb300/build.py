@@ -42,23 +42,37 @@ def _sources():
 
 
 def _deps():
-    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "pa.h"),
-                                                                 os.path.join(CSRC, "bind.cpp")]
+    return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + [os.path.join(INCLUDE, "pa.h")]
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BIND):
+def _older(target, deps) -> bool:
+    """Whether target is missing or older than one of deps."""
+    return not os.path.exists(target) or any(os.path.getmtime(f) > os.path.getmtime(target) for f in deps)
+
+
+def _bind_made_for() -> str:
+    """The Python and the PyTorch that a binding built now is for (PyTorch's version file holds its commit too)."""
+    with open(os.path.join(_torch_dir(), "version.py")) as f:
+        return "\n".join([sys.version, sysconfig.get_config_var("SOABI") or "", _torch_dir(), f.read()])
+
+
+def _bind_stale() -> bool:
+    """Whether the binding is missing, older than its sources, or made for another Python or PyTorch."""
+    if _older(BIND, [os.path.join(CSRC, "bind.cpp"), os.path.join(INCLUDE, "pa.h")]):
         return True
-    t = os.path.getmtime(LIB)
-    return any(os.path.getmtime(f) > t for f in _deps())
+    try:
+        with open(BIND + ".for") as f:
+            return f.read() != _bind_made_for()
+    except OSError:
+        return True
 
 
-def _torch_dir() -> str:
-    """Where PyTorch is installed (found without importing it)."""
+def _torch_dir() -> str | None:
+    """Where PyTorch is installed (found without importing it), or None."""
     import importlib.util
     spec = importlib.util.find_spec("torch")
     if spec is None or not spec.submodule_search_locations:
-        raise RuntimeError("PyTorch not found: the Python binding is built against its headers")
+        return None
     return list(spec.submodule_search_locations)[0]
 
 
@@ -83,15 +97,32 @@ def _link_bind(obj: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"linking the Python binding failed:\n{r.stderr}")
+    if os.path.exists(BIND + ".for"):
+        os.remove(BIND + ".for")
     os.replace(tmp, BIND)
+    with open(BIND + ".for", "w") as f:
+        f.write(_bind_made_for())
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
-    """Compile every .cu under csrc/ and bind.cpp, link _build/libpa.so and _build/_pa_bind.so; returns the library's
-    path."""
-    if not force and not _stale():
+    """Compile every .cu under csrc/ and link _build/libpa.so, and build _build/_pa_bind.so from bind.cpp, each where it is
+    stale; returns the library's path.  The library does not need PyTorch, and is linked before the binding is looked at;
+    the binding is left out where there is no PyTorch."""
+    library = force or _older(LIB, _deps())
+    binding = _torch_dir() is not None and (force or _bind_stale())
+    if not library and not binding:
         return LIB
     os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        bind = ex.submit(_compile_bind) if binding else None
+        if library:
+            _build_library(verbose, extra_flags)
+        if binding:
+            _link_bind(bind.result())
+    return LIB
+
+
+def _build_library(verbose: bool, extra_flags) -> None:
     cc = nvcc()
     srcs = _sources()
 
@@ -106,17 +137,13 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         return obj
 
     with cf.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
-        bind = ex.submit(_compile_bind)
         objs = list(ex.map(compile_one, srcs))
-        bind_obj = bind.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-Xlinker", "--no-undefined"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stderr}")
     os.replace(tmp, LIB)
-    _link_bind(bind_obj)
-    return LIB
 
 
 if __name__ == "__main__":
