@@ -393,8 +393,12 @@ PA_API int pa_prefill_chunk(void* out, const void* q, const int32_t* cu_q_lens, 
  * are powers of two, but for e4m3's subnormals.  Tokens may come in any order
  * and several sequences may store into one block; of several tokens for one
  * slot the last in the arrays is stored.  Nothing outside the named blocks is
- * written.  Copying a block (pa_copy_blocks moves the codes of pools viewed as
- * bf16 of half the head_dim) takes its scales along.
+ * written.
+ * Who copies a block copies its scales too: pa_copy_blocks moves codes only (of
+ * pools viewed as bf16 of half the head_dim).  Rows src_blocks[i] of k_scales
+ * and v_scales have to become rows dst_blocks[i] on the same stream before the
+ * copy is read or written to; under scales of their own the copied codes would
+ * be other values, and the next token's write would keep those.
  *   k_new, v_new        bf16 [num_tokens][num_kv_heads][head_dim]  (read)
  *   k_scales, v_scales  float [num_blocks][num_kv_heads] (read and written);
  *                       finite, and 0 or positive (0: nothing stored yet)

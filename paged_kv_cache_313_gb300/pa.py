@@ -502,7 +502,10 @@ def pa_prefill_chunk_fp8_block(q, cu_q_lens, q_start_pos, seq_of_chunk, max_q_le
 
 
 def pa_copy_blocks(k_cache, v_cache, src_blocks, dst_blocks, num_valid, error_count=None, stream=None) -> None:
-    """Copy-on-write: copy the first num_valid[i] slots of block src_blocks[i] into dst_blocks[i]."""
+    """Copy-on-write: copy the first num_valid[i] slots of block src_blocks[i] into dst_blocks[i].
+
+    Of e4m3 pools with a scale per (block, kv head) these are the codes, as ``k_cache.view(torch.bfloat16)``; the scales
+    are the caller's to copy on the same stream: ``k_scales[dst] = k_scales[src]``, and v_scales."""
     P, B, H, D = k_cache.shape
     _check("pa_copy_blocks", lib().pa_copy_blocks(
         _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache", k_cache.dtype), P, B, H, D, _dtype_code(k_cache),
