@@ -49,7 +49,6 @@
 // 189,395 tokens 74.0 us (0.78; CTAs take a stage every 3.0k cycles, 0.93); four
 // sequences of up to 40 tokens 6.8 us.  On the CUDA cores the first two took 805
 // and 3132 us.
-#include <atomic>
 #include <climits>
 
 #include "decode_common.cuh"

@@ -24,42 +24,32 @@ bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_
 //   a quarter in halves, six                            32.3   73.8   59.5   32.7   20.2
 //   a fifth in quarters, eight                          32.2   79.3   60.9   36.4   21.4
 //   partitions of 512 / 2048 (a tenth in quarters / eighths, eight)  34.0 / 32.6   80.0 / 78.1   63.0 / 66.6
-#ifndef PA_FP8_BLOCK_PARTITION
-#define PA_FP8_BLOCK_PARTITION 1024
-#endif
-#ifndef PA_FP8_BLOCK_ITEMS_PER_SM
-#define PA_FP8_BLOCK_ITEMS_PER_SM 6
-#endif
-#ifndef PA_FP8_BLOCK_TAIL_PCT
-#define PA_FP8_BLOCK_TAIL_PCT 20
-#endif
-#ifndef PA_FP8_BLOCK_TAIL_DIV
-#define PA_FP8_BLOCK_TAIL_DIV 2
-#endif
+constexpr int kPartition = 1024, kItemsPerSm = 6, kTailPercent = 20, kTailDivisor = 2;
+
 DecodePlan plan_decode_fp8_block(int num_seqs, int num_kv_heads, int max_context_len, int num_sms) {
     auto splits = [&](long long part) { return max_context_len <= part ? 1LL : (max_context_len + part - 1) / part; };
-    long long part = PA_FP8_BLOCK_PARTITION;
-    while (part > 128 && splits(part) * num_seqs * num_kv_heads < (long long)PA_FP8_BLOCK_ITEMS_PER_SM * num_sms)
+    long long part = kPartition;
+    while (part > 128 && splits(part) * num_seqs * num_kv_heads < (long long)kItemsPerSm * num_sms)
         part /= 2;
     while (splits(part) > 128) part *= 2;
-    long long small = part / PA_FP8_BLOCK_TAIL_DIV < 128 ? 128 : part / PA_FP8_BLOCK_TAIL_DIV;
+    long long small = part / kTailDivisor < 128 ? 128 : part / kTailDivisor;
     while (splits(small) > 128) small *= 2;
-    const int tail = small < part ? (int)((long long)num_seqs * PA_FP8_BLOCK_TAIL_PCT / 100) : 0;
+    const int tail = small < part ? (int)((long long)num_seqs * kTailPercent / 100) : 0;
     return DecodePlan{(int)part, (int)splits(tail ? small : part), (int)small, num_seqs - tail};
 }
 
 // The most partial rows of a kv head that the plan of any call of up to num_seqs sequences and max_context_len tokens has,
 // so that one workspace serves a batch that shrinks (a smaller one is cut finer, and may have more of them than a larger).
-// With PA_FP8_BLOCK_PARTITION tokens a partition, sequences of half ones have the most.  Where the plan halved its
-// partitions, twice as long ones gave fewer than PA_FP8_BLOCK_ITEMS_PER_SM items per SM: halving them doubles the items at
-// most, and the tail's shorter ones do so PA_FP8_BLOCK_TAIL_DIV-fold; no partition is below 128 tokens.
+// With kPartition tokens a partition, sequences of half ones have the most.  Where the plan halved its
+// partitions, twice as long ones gave fewer than kItemsPerSm items per SM: halving them doubles the items at
+// most, and the tail's shorter ones do so kTailDivisor-fold; no partition is below 128 tokens.
 long long most_partials(int num_seqs, int num_kv_heads, int max_context_len, int num_sms) {
     auto splits = [&](long long part) {
         const long long n = max_context_len <= part ? 1LL : (max_context_len + part - 1) / part;
         return n < 128 ? n : 128LL;
     };
-    const long long halved = (2LL * PA_FP8_BLOCK_TAIL_DIV * PA_FP8_BLOCK_ITEMS_PER_SM * num_sms - 1) / num_kv_heads;
-    return std::max(num_seqs * splits(PA_FP8_BLOCK_PARTITION / PA_FP8_BLOCK_TAIL_DIV),
+    const long long halved = (2LL * kTailDivisor * kItemsPerSm * num_sms - 1) / num_kv_heads;
+    return std::max(num_seqs * splits(kPartition / kTailDivisor),
                     std::min(num_seqs * splits(128), halved));
 }
 

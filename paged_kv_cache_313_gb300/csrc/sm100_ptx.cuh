@@ -330,7 +330,7 @@ __device__ __forceinline__ void umma_bf16_ta_warp(uint32_t d_tmem, uint32_t a_tm
         ::"r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate ? 1u : 0u)
         : "memory");
 }
-// The same two with e4m3 operands, 32 elements of K each (A in tensor memory: four codes to a 32-bit column).
+// The same with e4m3 operands, both in shared memory, 32 elements of K.
 __device__ __forceinline__ void umma_e4m3_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                bool accumulate) {
     asm volatile(
