@@ -290,10 +290,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 d.last_key = cap - 1;
             }
             const int all = d.last_key >= 0 ? d.last_key / kTile + 1 : 0;
-            d.spans = max(1, spans.per_tiles.div(all + spans.tiles - 1));  // (tiles of 128 keys: below 2^25)
+            d.spans = spans.per_tiles.div(all + spans.tiles - 1);  // (tiles of 128 keys: below 2^25)
             d.t0 = d.span * spans.tiles;
-            d.nt = max(0, min(spans.tiles, all - d.t0));
-            return d.span < d.spans;  // without any key, span 0 stores zeros
+            d.nt = min(spans.tiles, all - d.t0);
+            if (all == 0 && d.span == 0) {
+                // Without any key the output is zeros, stored here: every item that is passed on has keys.  (Passed on like
+                // the others, such an item behind one of more tiles than the ring of V holds stopped the kernel: the
+                // converters looked past it for their next one, this warp waited for them before it passed that on.)
+#pragma unroll 1
+                for (int r = 0; r < d.nq * G; ++r) {
+                    const int pos = r * inv_g >> 16;
+                    const size_t row = (size_t)(d.row + pos) * p.num_q_heads + d.kvh * G + (r - pos * G);
+                    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + row * kD)[lane] = make_uint2(0u, 0u);
+                }
+            }
+            return d.span < d.spans;
         };
         auto publish = [&](Item& d) {  // the next item, or the end
             d.nt = -1;
@@ -433,11 +444,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && !mbar_wait_warp(bar, parity)) ok = false;
             return ok;
         };
-        uint32_t g = 0, items = 0, sb = 0, round = 0;  // key tiles, items with keys; the piece's buffer and its round
+        uint32_t g = 0, items = 0, sb = 0, round = 0;  // key tiles, items; the piece's buffer and its round
         Item d;
         for (uint32_t n = 0; ok && take_item(n, d); ++n) {
             const uint32_t nt = uniform(d.nt);
-            if (nt == 0) continue;
             // an item's first S waits for its query terms, its first product until the last item's epilogue has read O
             if (s_side) wait(bars.q_full(items % kQSlots), (items / kQSlots) & 1);
             else if (items > 0) wait(bars.o_free(), (items - 1) & 1);
@@ -580,20 +590,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             fence_proxy_async_smem();  // before the buffer is copied to again
         };
-        uint32_t taken = 0;
-        auto next_item = [&](Item& d) {  // the next item with keys; false at the end
-            while (ok && take_item(taken++, d))
-                if (d.nt > 0) return true;
-            return false;
-        };
         Item d, nx;
-        bool have = next_item(d);
+        bool have = take_item(0, d);
         if (have) {
             stage_q(d, 0);
             finish_q(0);
         }
         while (have && ok) {
-            const bool have_next = next_item(nx);
+            const bool have_next = take_item(items + 1, nx);
             if (!ok) break;
             for (int j = 0; j < d.nt; ++j, ++g) {
                 const uint32_t vs = g % kVStages, vh = g % kVhStages;
@@ -671,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t t_o = tmem + lanes + kTO + x * 128;
         float2* state = reinterpret_cast<float2*>(smem + kState);
-        uint32_t g = 0, items = 0;  // key tiles (pieces of this group), and items with keys
+        uint32_t g = 0;  // key tiles (pieces of this group)
         BoundedWarpBarrier joined{bars.joined(), 0};
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             if (ok && !mbar_wait_warp(bar, parity)) ok = false;
@@ -689,10 +693,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int least_last = __reduce_min_sync(0xffffffffu, my_last);
             float m = -INFINITY, l = 0.f, qf = 0.f;
             int key0 = d.t0 * kTile + x * 64;  // the piece's first key
-            if (g != end) {
-                wait(bars.q_full(items % kQSlots), (items / kQSlots) & 1);
-                qf = reinterpret_cast<const float*>(smem + kQf)[items % kQSlots * kTile + r];
-            }
+            wait(bars.q_full(n % kQSlots), (n / kQSlots) & 1);
+            qf = reinterpret_cast<const float*>(smem + kQf)[n % kQSlots * kTile + r];
             bool first = true, open = true;  // nothing in O yet; there are rows without a key so far
             for (; g != end; ++g, key0 += kTile, first = false) {
                 const uint32_t piece = 2 * g + x, sb = piece % kPieces, t_s = tmem + lanes + kTS + sb * 64;
@@ -809,12 +811,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             // ---- the item's output: both groups' states joined, each group stores 64 columns of the row
             if (!ok) break;
-            float mo = -INFINITY, lo = 0.f;
-            if (!first) {
+            float mo, lo;
+            {
                 const uint32_t last = 2 * (g - 1) + x;  // this group's last piece
                 wait(bars.pv_done(last % kPieces), (last / kPieces) & 1);
                 // (two copies by item: the other group may be an item behind)
-                float2* st = state + (items & 1) * 2 * kTile;
+                float2* st = state + (n & 1) * 2 * kTile;
                 st[x * kTile + r] = make_float2(m, l);
                 tc_fence_before();
                 if (!ok || !joined.sync()) {
@@ -842,16 +844,13 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
             for (int col = x * 64; col < x * 64 + 64; col += 32) {
                 float o[32];
-                if (!first) {
+                {
                     float b[32];
                     tmem_ld32(t_o + col, o);
                     tmem_ld32(t_oth + col, b);
                     tmem_wait_ld();
 #pragma unroll
                     for (int i = 0; i < 32; ++i) o[i] = (use_own ? o[i] * f_own : 0.f) + (use_oth ? b[i] * f_oth : 0.f);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) o[i] = 0.f;
                 }
                 if (!row_ok) continue;
                 if (direct) {
@@ -878,23 +877,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
             }
-            if (!first) {
-                // NaN among the V of the tile's own keys (see clear_nans), where this row sees them
-                const int* nan = reinterpret_cast<const int*>(smem + kNan) + items % kNanSlots * (kD + 1);
-                if (nan[kD] != INT_MAX && row_ok) {
-                    const int my_last = min(d.pos + my_pos, d.last_key);
+            // NaN among the V of the tile's own keys (see clear_nans), where this row sees them
+            const int* nan = reinterpret_cast<const int*>(smem + kNan) + n % kNanSlots * (kD + 1);
+            if (nan[kD] != INT_MAX && row_ok) {
+                const int my_last = min(d.pos + my_pos, d.last_key);
 #pragma unroll 1
-                    for (int col = x * 64; col < x * 64 + 64; ++col) {
-                        if (nan[col] > my_last) continue;
-                        if (direct) static_cast<__nv_bfloat16*>(p.out)[row * kD + col] = __float2bfloat16_rn(NAN);
-                        else spans.o[part * kD + col] = NAN;
-                    }
+                for (int col = x * 64; col < x * 64 + 64; ++col) {
+                    if (nan[col] > my_last) continue;
+                    if (direct) static_cast<__nv_bfloat16*>(p.out)[row * kD + col] = __float2bfloat16_rn(NAN);
+                    else spans.o[part * kD + col] = NAN;
                 }
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(bars.o_free());
-                ++items;
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && ok) mbar_arrive(bars.o_free());
             __syncwarp();
             if (lane == 0) mbar_arrive(bars.item_empty(n % kItems));
         }
