@@ -440,13 +440,16 @@ PA_API int pa_read_kv_paged_fp8_block(void* k_out, void* v_out, int num_tokens, 
  * sequence's tokens; those of other blocks are not used.  Where the tensor cores
  * run (head_dim 128, up to 8 query heads per kv head, block sizes 8, 16, 32, 64
  * and 128, 16-byte aligned pools and q) a V scale below 2^-100, or 2^-80 of the
- * largest of the context's blocks, counts as no more than that.  Tokens in a
+ * largest of the context's blocks, counts as no more than that; its keys keep
+ * their weight.  Tokens in a
  * block with an invalid table entry are masked (and counted).  A query with an
  * infinity or a NaN gives NaN, as does a NaN code in K or (in its column) in V
  * for the queries that see its token.  Shapes, context
  * clamping and the workspace's rules are pa_decode's
  * (pa_decode_fp8_block_workspace_size bytes, which serve every call of no more
- * sequences and no longer contexts as well).
+ * sequences and no longer contexts as well).  The contexts are split by
+ * max_context_len: the batch's longest length serves best, a limit far above it
+ * leaves them in few pieces.
  */
 PA_API size_t pa_decode_fp8_block_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                                  int block_size, int max_context_len);
@@ -461,7 +464,8 @@ PA_API int pa_decode_fp8_block(void* out, const void* q, int num_seqs, int num_q
  * attention of pa_prefill_chunk on the values that are read back; q and out
  * bf16, the chunks' own K and V written by pa_write_kv_paged_fp8_block first.
  * max_context_len bounds q_start_pos[c] + n_c (keys at or beyond it are not
- * read, and counted).  workspace: pa_prefill_fp8_block_workspace_size bytes
+ * read, and counted), and plans the split as for pa_decode_fp8_block.  A query
+ * that sees no key gives zeros.  workspace: pa_prefill_fp8_block_workspace_size bytes
  * (may be 0, then NULL is fine), 256-byte aligned; it needs no zeroing, and
  * serves every call of no more chunks, queries and context as well (a call
  * whose q has rows behind its chunks may cut its keys less than with a

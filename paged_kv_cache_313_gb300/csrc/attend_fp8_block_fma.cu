@@ -7,8 +7,8 @@
 // staged rows.  Decode: one CTA per (sequence, kv head, partition), joined as in
 // decode_fp8_block_tc.cu.  Prefill: one CTA per (query, kv head).  Bound by
 // instructions, far from HBM (64 sequences, 32/8 heads of 128, 65,500 tokens:
-// 805 us, 0.025 of the copy bandwidth; four chunks of 512 queries at short
-// offsets: 5.0 ms; the tensor-core kernels take 34 us for each).
+// 750 us, 0.027 of the copy bandwidth, where the tensor-core kernel takes 31;
+// four chunks of 512 queries at short offsets: 4.9 ms, where it takes 33 us).
 #include "decode_common.cuh"
 #include "fma_attend.cuh"
 

@@ -44,11 +44,11 @@
 //
 // Bound: HBM.  A stage is 32 KB, 0.74 us of an SM's share of the measured copy
 // bandwidth; the softmax of a stage is about 250 warp instructions.  Measured: 64
-// sequences, 32/8 heads, 65,500 tokens 31.9 us (135 MB: 0.63 of the copy
+// sequences, 32/8 heads, 65,500 tokens 31.2 us (135 MB: 0.64 of the copy
 // bandwidth, start, uneven ends and join included); 16 long contexts, 64/8 heads,
-// 189,395 tokens 74.0 us (0.78; CTAs take a stage every 3.0k cycles, 0.93); four
-// sequences of up to 40 tokens 6.8 us.  On the CUDA cores the first two took 805
-// and 3132 us.
+// 189,395 tokens 73.1 us (0.79; CTAs take a stage every 3.0k cycles, 0.93); four
+// sequences of up to 40 tokens 6.6 us.  On the CUDA cores the first two take 750
+// and 2953 us.
 #include <climits>
 
 #include "decode_common.cuh"
@@ -107,8 +107,8 @@ static_assert(kQp % 1024 == 0 && kP % 16 == 0 && kQ % 16 == 0 && kRed % 16 == 0 
 static_assert(kSmemBytes <= 228 * 1024 / 2 - 1024, "two CTAs per SM");
 
 // kHeads: columns kept for query heads, 4 (groups up to 4) or 8; hi terms are columns 0..kHeads-1, lo terms the next.
-// (Groups of 4 with 4 columns / with 8: 64 sequences 37.2 / 39.9 us, 16 long contexts 64.3 / 67.1, one 8000-token
-// context 16.9 / 17.5.)
+// (Groups of 4 with 4 columns / with 8: 64 sequences 30.9 / 32.9 us, 16 long contexts 67.5 / 70.1, one 8000-token
+// context 15.3 / 15.7.)
 template <int kHeads>
 __global__ void __launch_bounds__(kThreads, 2)
     decode_fp8_block_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,

@@ -31,11 +31,15 @@
 //     launch walks the list, a warp per (block, head, side) without a barrier
 //     among them.  It leaves the workspace zeroed again.
 //
-// Bound: HBM for long calls, launch and memory latency for a decode step.
+// Bound: a decode step by its launch and the latency of its dependent loads.
+// Longer calls by the second launch, and there not by HBM (26 % of the DRAM
+// peak): each warp walks list, writers, rows and stores alone, with nothing of
+// its next unit under way, and the 256 pieces that it keeps spill (68 bytes of
+// stores and 104 of loads a thread; 36 and 76 in the one-launch form).
 // Measured (8 heads of 128, blocks of 16): four prompts of 2048 tokens 18.1 us
-// (50.5 MB: 0.40 of the copy bandwidth, the two launches and their dependent
-// loads being about half of it); 256 decode tokens and 4 x 512 over blocks of 32
-// 13.5 us.  Read back of 89,556 tokens to bf16 87.2 us, 551 MB: 0.93.
+// (50.5 MB: 0.41 of the copy bandwidth; about 14 us of it the second launch);
+// 256 decode tokens and 4 x 512 over blocks of 32 13.5 us.  Read back of 89,556
+// tokens to bf16 87.0 us, 551 MB: 0.94; to fp32 202 us, 917 MB: 0.67.
 #include "pa_internal.cuh"
 
 namespace pa {

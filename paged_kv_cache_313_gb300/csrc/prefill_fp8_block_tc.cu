@@ -46,10 +46,11 @@
 //
 // Bound: the softmax warps' issue and the hand-overs between the warps (the two
 // products are 1.05k cycles of a key tile's 2.0k).  Measured: 2048 queries at
-// position 5,916, 64/8 heads, 384 us over 64-token blocks (466 GFLOP: 1.21
-// PFLOP/s, 0.62 of cuBLAS bf16) and 396 over 16-token blocks, whose copies are
-// four times as many; four chunks of 512 queries at short offsets, 32/8 heads,
-// 33.4 us; 37 queries at 2,955 17.4 us.  On the CUDA cores 184, 5.0 and 1.3 ms.
+// position 5,916, 64/8 heads, 391 us over 64-token blocks (466 GFLOP: 1.19
+// PFLOP/s, 0.61 of cuBLAS bf16; 407 among other calls) and 401 over 16-token
+// blocks, whose copies are four times as many; four chunks of 512 queries at
+// short offsets, 32/8 heads, 33.0 us; 37 queries at 2,955 16.5 us.  On the CUDA
+// cores the last two take 4.9 and 1.2 ms.
 #include <algorithm>
 #include <climits>
 
@@ -191,8 +192,8 @@ __device__ __forceinline__ int key_cap(const PrefillParams& p, int s) {
 }
 
 // kKeys: keys that share a block, and so their factors, as far as the softmax goes by it: 8, 16 or 32 (the block size up
-// to 32).  (2048 queries at 5,916 over 64-token blocks with 32 / 8: 390 / 405 us; over 16-token blocks with 16 / 8: 419 /
-// 438.)
+// to 32).  (2048 queries at 5,916 over 64-token blocks with 32 / 8: 391 / 433 us; over 16-token blocks with 16 / 8: 401 /
+// 445.)
 template <int kKeys>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_fp8_block_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -978,8 +979,8 @@ size_t partial_bytes(size_t rows) { return rows == 0 ? 0 : up256(rows * kD * siz
 
 // Key tiles per span and spans per query tile.  Where the tiles alone leave half of the SMs idle their keys are cut so
 // that the items make up one round of the GPU, into spans of at least two key tiles (a span's partial rows cost about
-// one key tile's time to store and join): 37 queries at 2,955, 8 kv heads, 17.4 us, uncut 36.2; but 160 query tiles of
-// 21 key tiles cut in two 64.9, uncut 51.8.  The count comes from the largest context, the lengths live on the device.
+// one key tile's time to store and join): 37 queries at 2,955, 8 kv heads, 16.5 us, uncut 35.5; but 160 query tiles of
+// 21 key tiles cut in two 62.7, uncut 53.4.  The count comes from the largest context, the lengths live on the device.
 // No more spans than `workspace_bytes` holds the partial rows of, for all `total_rows` (query, head) rows of q.
 Spans plan_spans(int num_chunks, int max_q_len, int num_kv_heads, int group, int max_context_len, int num_sms,
                  size_t total_rows, size_t workspace_bytes) {
