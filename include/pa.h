@@ -486,6 +486,142 @@ PA_API int pa_prefill_chunk_fp8_block(void* out, const void* q, const int32_t* c
                                       size_t workspace_bytes, int32_t* error_count, void* stream);
 
 /*
+ * Caches kept short by eviction.  The pages keep every token ([P1] 工作原理,
+ * [P3] KV size formula: the cache grows with the context); these calls keep the
+ * tokens that attention looks at.  Beside the block tables a caller holds, one
+ * row for each sequence and kv head,
+ *   key_weights  float [num_seqs][num_kv_heads][key_width]: the attention
+ *                weight that each cached token has drawn so far,
+ *   key_pos      int32 of the same shape: each cached token's place in the
+ *                sequence, which after an eviction is not its index in the cache,
+ * indexed like the cache (token j of sequence s is pool row block_tables[s][j/B]
+ * * B + j%B); key_width must be no less than max_context_len.  A row belongs to
+ * a sequence, not to blocks: sequences that share blocks have weights of their
+ * own.
+ *
+ * Rotary positions with several axes (time, height, width; one for text): pair i
+ * of a head, elements (i, rot_dim/2 + i), or (2i, 2i + 1) where interleaved is
+ * not 0, becomes
+ *     (a cos - b sin, b cos + a sin),  angle = rope_pos[axis[i]][t] * inv_freq[i]
+ * for i < rot_dim/2; elements from rot_dim on stay as they are.  The angle is
+ * taken modulo a turn without a rounding that grows with the position (better
+ * than 2^-22 rad at every 32-bit position), the product is rounded once.
+ *   q, k          [num_tokens][heads][head_dim], heads and elements contiguous,
+ *                 tokens q_stride, k_stride elements apart (parts of one fused
+ *                 projection may be given as they are)
+ *   q_out, k_out  contiguous; q_out may be q and k_out may be k where those are
+ *   rope_pos      int32 [num_axes][num_tokens], any value
+ *   inv_freq      float [rot_dim/2]
+ *   axis          int32 [rot_dim/2], each in [0, num_axes) (others count one error
+ *                 per token, and their pairs stay as they are); NULL: all 0
+ * Any even rot_dim <= head_dim <= 1024, (heads of q and k) * head_dim <= 2^20; no
+ * alignment is needed, 16-byte aligned rows of rot_dim/2 a multiple of 16 bytes run
+ * on wide accesses.
+ */
+PA_API int pa_rope(void* q_out, void* k_out, const void* q, const void* k, int num_tokens, int num_q_heads,
+                   int num_kv_heads, int head_dim, int dtype, long long q_stride, long long k_stride,
+                   const int32_t* rope_pos, int num_axes, const float* inv_freq, const int32_t* axis, int rot_dim,
+                   int interleaved, int32_t* error_count, void* stream);
+
+/*
+ * pa_rope on q and k_new and pa_write_kv_paged of the turned k_new and of v_new,
+ * in one launch: positions (rope_pos) and slots (pos, the token's index in the
+ * cache) are apart.  Slots, padding (pos < 0: nothing of the token is written,
+ * its row of q_out included) and errors are pa_write_kv_paged's; the query of a
+ * token whose slot is invalid is turned all the same.  With key_weights and
+ * key_pos (both or neither), the written token's weight becomes 0 and its place
+ * token_pos[t] (token_pos NULL: pos[t]) for every kv head; pos[t] >= key_width is then
+ * an invalid index.  rot_dim 0 turns nothing.  num_q_heads may be 0.  Slots must
+ * be distinct.
+ */
+PA_API int pa_rope_write_kv_paged(void* q_out, const void* q, const void* k_new, const void* v_new, int num_tokens,
+                                  int num_q_heads, int num_kv_heads, int head_dim, int dtype, long long q_stride,
+                                  long long k_stride, long long v_stride, const int32_t* rope_pos, int num_axes,
+                                  const float* inv_freq, const int32_t* axis, int rot_dim, int interleaved,
+                                  void* k_cache, void* v_cache, int num_blocks, int block_size,
+                                  const int32_t* block_tables, int num_seqs, int max_blocks_per_seq,
+                                  const int32_t* seq_idx, const int32_t* pos, float* key_weights, int32_t* key_pos,
+                                  int key_width, const int32_t* token_pos, int64_t* slot_mapping,
+                                  int32_t* error_count, void* stream);
+
+/*
+ * pa_decode that also adds to each key's weight what its kv head's query heads
+ * give it:
+ *     key_weights[s][kv][j] += sum over the heads h of kv head kv of
+ *                              softmax_j(scale * q[s][h] . K[s][j][kv])
+ * for j < L; weights at and beyond L, and those of tokens in blocks with an invalid
+ * table entry, stay as they are.  Arguments, shapes, clamping and errors are
+ * pa_decode's; the order of every sum is fixed.  workspace:
+ * pa_decode_weights_workspace_size bytes (which serve every call of no more
+ * sequences and no longer contexts as well; it holds every score, 4 bytes for each
+ * query head and token), 256-byte aligned, zeroed once.  One workspace must not
+ * serve two calls that may overlap on the GPU.  A query with a NaN makes the
+ * weights of its sequence's keys NaN.
+ */
+PA_API size_t pa_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                               int block_size, int max_context_len);
+PA_API int pa_decode_weights(void* out, const void* q, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                             int dtype, const void* k_cache, const void* v_cache, int num_blocks, int block_size,
+                             const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                             int max_context_len, float scale, float* key_weights, int key_width, void* workspace,
+                             size_t workspace_bytes, int32_t* error_count, void* stream);
+
+/*
+ * pa_prefill_chunk that also adds to each key's weight, for every query of a chunk
+ * that sees the key, what the query's heads give it (as pa_decode_weights does for
+ * one query); key_weights has a row for each of the num_seqs sequences.
+ * max_context_len bounds q_start_pos[c] + n_c: keys at or beyond it are not read
+ * (and counted).  Several chunks may belong to one sequence.  The order of every sum is
+ * fixed.  workspace: pa_prefill_weights_workspace_size bytes, 256-byte aligned; it needs no
+ * zeroing, and serves every call of no more chunks, queries and context as well.
+ * One workspace must not serve two calls that may overlap on the GPU.  q and the
+ * pools 16-byte aligned, else PA_ERR_UNSUPPORTED; other shapes as for
+ * pa_prefill_chunk.
+ */
+PA_API size_t pa_prefill_weights_workspace_size(int num_chunks, int total_q, int max_q_len, int num_q_heads,
+                                                int num_kv_heads, int head_dim, int block_size, int max_context_len);
+PA_API int pa_prefill_chunk_weights(void* out, const void* q, const int32_t* cu_q_lens, const int32_t* q_start_pos,
+                                    const int32_t* seq_of_chunk, int num_chunks, int total_q, int max_q_len,
+                                    int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int dtype,
+                                    const void* k_cache, const void* v_cache, int num_blocks, int block_size,
+                                    const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                                    int max_context_len, float scale, float* key_weights, int key_width,
+                                    void* workspace, size_t workspace_bytes, int32_t* error_count, void* stream);
+
+/*
+ * Eviction.  Every (sequence, kv head) of a sequence with more than `budget` cached
+ * tokens keeps `budget` of them: first its protected tokens, those with key_pos <
+ * keep_first or key_pos >= next_pos[s] - keep_recent (next_pos[s]: the place of the
+ * sequence's next token), then the others from the largest key_weights down (-0 equals
+ * 0, NaN counts as -inf); of equal ones, and among protected ones, the lowest index in the
+ * cache is kept.  Each head keeps tokens of its own choice.  Then the kept tokens at
+ * indices >= budget move, in ascending order, to the indices < budget that are no longer
+ * taken, in ascending order: their rows of K and V, their weights and their places.
+ * Nothing else changes; what lies at indices >= budget stays there, unused.
+ * new_lens[s] = min(L, budget) (new_lens may be context_lens itself).  The blocks
+ * beyond the budget may then be freed, and the sequence goes on at index budget.
+ *   key_weights, key_pos  read and written
+ *   next_pos, context_lens, new_lens  int32 [num_seqs]; context_lens above max_context_len or
+ *                         max_blocks_per_seq*B are clamped and counted
+ * The blocks of a sequence with more than `budget` tokens must be its own: no other
+ * sequence's table may name them (copy shared ones first, pa_copy_blocks).  A move from or
+ * to a block with an invalid table entry is counted and moves no rows.  budget >= 1,
+ * keep_first + keep_recent <= budget; head_dim * element size a multiple of 16 bytes, the pools
+ * 16-byte aligned.  (e4m3 pools of one scale: as bf16 of half the head_dim; pools with a scale
+ * per block cannot be moved between blocks row by row.)  workspace:
+ * pa_evict_workspace_size bytes, 256-byte aligned; it needs no zeroing, and serves calls of
+ * the same budget with no more sequences and no longer contexts as well.  One workspace must
+ * not serve two calls that may overlap on the GPU.
+ */
+PA_API size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_len, int budget);
+PA_API int pa_evict_tokens(void* k_cache, void* v_cache, int num_blocks, int block_size, int num_kv_heads,
+                           int head_dim, int dtype, const int32_t* block_tables, int num_seqs,
+                           int max_blocks_per_seq, const int32_t* context_lens, int max_context_len,
+                           float* key_weights, int32_t* key_pos, int key_width, const int32_t* next_pos, int budget,
+                           int keep_first, int keep_recent, int32_t* new_lens, void* workspace,
+                           size_t workspace_bytes, int32_t* error_count, void* stream);
+
+/*
  * Kernel-side block tables for a block manager whose blocks hold `ratio`
  * kernel blocks ("PagedAttention学习笔记", 代码实现部分 › 块表与槽位映射, 混合块:
  * map_to_kernel_blocks).  The manager's pool [P][ratio*B][Hkv][D] is the same

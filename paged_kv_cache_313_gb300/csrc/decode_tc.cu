@@ -116,6 +116,7 @@ struct StageInfo {
     int ntok;   // tokens of this stage (0..64)
     unsigned long long valid;  // bit r: token row r holds a valid token
     int new_row;         // pa_decode_write: row of the sequence's newest token in this stage, or -1
+    int tok0;            // pa_decode_weights: the stage's first token
     long long new_slot;  // and its pool slot
 };
 
@@ -200,7 +201,8 @@ __device__ __forceinline__ void decode_item(const int* cum, int N, int Hkv, int 
 
 // kPrefix: the cascade's kernel, whose queue begins with shared-prefix items (a separate instantiation, so that
 // the prefix items' four-chunk code does not shape the plain decode kernel's)
-template <int D, bool kFp8, bool kPair, bool kPrefix>
+// kScores: pa_decode_weights, which leaves the scores and every item's (m, l) in the workspace (bf16 pools)
+template <int D, bool kFp8, bool kPair, bool kPrefix, bool kScores>
 __global__ void __launch_bounds__(TcCfg<D, kFp8, kPair>::kThreads, TcCfg<D, kFp8, kPair>::kCtasPerSm)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      const DecodeParams p, int* work) {
@@ -474,6 +476,7 @@ __global__ void __launch_bounds__(TcCfg<D, kFp8, kPair>::kThreads, TcCfg<D, kFp8
                     inf.ntok = nt;
                     inf.valid = valid;
                     inf.new_row = new_row;
+                    if (kScores) inf.tok0 = d.j0 + t0;
                     inf.new_slot = new_slot;
                     mbar_arrive_expect_tx(&full[slot], bytes);
                     if (C::kNewBytes && new_row >= 0) {  // bf16 pools: stage the newest token's rows
@@ -760,6 +763,23 @@ __global__ void __launch_bounds__(TcCfg<D, kFp8, kPair>::kThreads, TcCfg<D, kFp8
                         x[c][3] = vhi ? (sa[3] + sb[3]) * sl2 : -INFINITY;
                     }
                 }
+                if constexpr (kScores) {
+                    // every token of the stage up to its last one: heads 2 c4 and 2 c4 + 1 of tokens g4 and g4 + 8
+                    static_assert(NC == 1, "bf16 pools, plain items");
+                    float* sc = p.ws_scores +
+                                (decode_unit(p, inf.s, inf.kvh) * p.score_width + inf.tok0 + r0 + g4) * G + 2 * c4;
+#pragma unroll
+                    for (int hi = 0; hi < 2; ++hi) {
+                        if (r0 + g4 + 8 * hi >= inf.ntok) continue;
+                        float* to = sc + (size_t)hi * 8 * G;
+                        if (!(G & 1)) {
+                            if (2 * c4 < G) *reinterpret_cast<float2*>(to) = make_float2(x[0][2 * hi], x[0][2 * hi + 1]);
+                        } else {
+                            if (2 * c4 < G) to[0] = x[0][2 * hi];
+                            if (2 * c4 + 1 < G) to[1] = x[0][2 * hi + 1];
+                        }
+                    }
+                }
                 float mx0 = fmaxf(x[0][0], x[0][2]), mx1 = fmaxf(x[0][1], x[0][3]);
 #pragma unroll
                 for (int c = 1; c < NC; ++c) {
@@ -1027,6 +1047,7 @@ __global__ void __launch_bounds__(TcCfg<D, kFp8, kPair>::kThreads, TcCfg<D, kFp8
                 if (inf.flags & 4) {
                     *reinterpret_cast<uint2*>(out + idx) =
                         make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+                    if (kScores && dc == 0) p.ws_ml[slot_ws * G + h] = make_float2(M, Ls);
                 } else {
                     *reinterpret_cast<float4*>(wo) = acc;
                     if (dc == 0) p.ws_ml[slot_ws * G + h] = make_float2(M, Ls);
@@ -1048,7 +1069,7 @@ __global__ void __launch_bounds__(TcCfg<D, kFp8, kPair>::kThreads, TcCfg<D, kFp8
     }
 }
 
-template <int D, bool kFp8, bool kPair, bool kPrefix = false>
+template <int D, bool kFp8, bool kPair, bool kPrefix = false, bool kScores = false>
 int launch(const DecodeParams& p, int num_sms, cudaStream_t stream) {
     using C = TcCfg<D, kFp8, kPair>;
     CUtensorMap tmk, tmv;
@@ -1057,7 +1078,7 @@ int launch(const DecodeParams& p, int num_sms, cudaStream_t stream) {
     if ((rc = pool_tensor_map_rows(&tmv, p.v_cache, p.num_blocks, p.block_size, p.num_kv_heads, D, kFp8,
                                    C::kHeads)) != PA_OK)
         return rc;
-    if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(decode_tc_kernel<D, kFp8, kPair, kPrefix>), C::kSmemBytes)) !=
+    if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(decode_tc_kernel<D, kFp8, kPair, kPrefix, kScores>), C::kSmemBytes)) !=
         PA_OK)
         return rc;
     // C::kCtasPerSm CTAs per SM (or as many as are resident at once, should fewer fit), never more
@@ -1069,7 +1090,7 @@ int launch(const DecodeParams& p, int num_sms, cudaStream_t stream) {
     int resident = resident_cache.load(std::memory_order_relaxed);
     if (resident == 0) {
         int n = 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_tc_kernel<D, kFp8, kPair, kPrefix>, C::kThreads,
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, decode_tc_kernel<D, kFp8, kPair, kPrefix, kScores>, C::kThreads,
                                                           C::kSmemBytes) != cudaSuccess)
             return check_launch();
         if (n < 1) return PA_ERR_UNSUPPORTED;
@@ -1079,7 +1100,7 @@ int launch(const DecodeParams& p, int num_sms, cudaStream_t stream) {
     long long max_items = (long long)p.num_seqs * p.num_kv_heads * p.max_splits;
     const long long slots = (long long)num_sms * resident;
     int grid = (int)(max_items < slots ? max_items : slots);
-    return launch_kernel(decode_tc_kernel<D, kFp8, kPair, kPrefix>, dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream,
+    return launch_kernel(decode_tc_kernel<D, kFp8, kPair, kPrefix, kScores>, dim3(grid), dim3(C::kThreads), C::kSmemBytes, stream,
                          tmk, tmv, p, p.work);
 }
 
@@ -1155,6 +1176,9 @@ int launch_decode_tc(const DecodeParams& p, int num_sms, cudaStream_t stream) {
                                                              : launch<128, true, false>(p, num_sms, stream);
     if (p.group_offsets)  // cascade prefix items (pa_decode_cascade takes head_dim 128 only)
         return p.head_dim == 128 ? launch<128, false, false, true>(p, num_sms, stream) : PA_ERR_UNSUPPORTED;
+    if (p.ws_scores)
+        return p.head_dim == 64 ? launch<64, false, false, false, true>(p, num_sms, stream)
+                                : launch<128, false, false, false, true>(p, num_sms, stream);
     return p.head_dim == 64 ? launch<64, false, false>(p, num_sms, stream)
                             : launch<128, false, false>(p, num_sms, stream);
 }

@@ -1,0 +1,362 @@
+// pa_api_weights.cu — C ABI of the caches that evict tokens: rotary positions
+// and their paged write, attention that accumulates each key's weight, the
+// eviction.  Like pa_api.cu, every entry point validates on the host and
+// launches nothing when a check fails.
+#include <algorithm>
+#include <climits>
+#include <cstdint>
+
+#include "pa_internal.cuh"
+
+namespace pa {
+namespace {
+
+bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
+
+// Shapes of the rotary calls.
+int rope_ok(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int dtype, int num_axes, int rot_dim) {
+    if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads < 0 || head_dim < 1 || rot_dim < 0 || rot_dim > head_dim ||
+        rot_dim % 2 != 0 || (rot_dim > 0 && num_axes < 1))
+        return PA_ERR_INVALID_ARG;
+    if (dtype != PA_F32 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if (head_dim > 1024 || (long long)(num_q_heads + (long long)num_kv_heads) * head_dim > (1 << 20))
+        return PA_ERR_UNSUPPORTED;
+    return PA_OK;
+}
+
+// Partial rows ((sequence, kv head, partition)) that pa_decode's plan of any call of up to num_seqs sequences and
+// max_context_len tokens has, so that one workspace serves a batch that shrinks: a smaller batch is cut finer.  For each
+// batch size and each partition of the plan's halvings the most rows are those of the longest context for which the plan
+// stops there: the next longer partition must give fewer than two items per SM.
+long long most_partials(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len, int num_sms) {
+    long long most = 1;
+    for (long long n = 1; n <= num_seqs; ++n) {
+        // the plan at these lengths, where its partition changes: the longest context that has it
+        long long ctx = max_context_len;
+        while (ctx > 0) {
+            const DecodePlan plan = plan_decode((int)n, num_q_heads, num_kv_heads, head_dim, (int)ctx, num_sms, SIZE_MAX);
+            const long long small = std::max(64, (plan.partition / 4) & ~63);
+            most = std::max(most, n * num_kv_heads * std::min(128LL, (ctx + small - 1) / small));
+            if (plan.partition <= 64) break;
+            // the longest shorter context with a shorter partition
+            long long lo = 0, hi = ctx;  // plan(lo) shorter (or lo == 0), plan(hi) this long
+            while (hi - lo > 1) {
+                const long long mid = (lo + hi) / 2;
+                (plan_decode((int)n, num_q_heads, num_kv_heads, head_dim, (int)mid, num_sms, SIZE_MAX).partition <
+                 plan.partition ? lo : hi) = mid;
+            }
+            ctx = lo;
+        }
+    }
+    return most;
+}
+
+// Workspace of pa_prefill_chunk_weights: the rows' lse, then the keys' partial sums.
+struct PrefillWeightsWorkspace {
+    size_t lse, partial, total;
+};
+PrefillWeightsWorkspace prefill_weights_layout(int num_chunks, int total_q, int num_q_heads, int num_kv_heads,
+                                               int max_context_len, int pieces) {
+    PrefillWeightsWorkspace w;
+    w.lse = 0;
+    w.partial = round_up((size_t)total_q * num_q_heads * 4 + 1);  // (never empty)
+    w.total = w.partial + round_up((size_t)num_chunks * num_kv_heads * pieces * max_context_len * 4);
+    return w;
+}
+
+}  // namespace
+}  // namespace pa
+
+using namespace pa;
+
+extern "C" {
+
+int pa_rope(void* q_out, void* k_out, const void* q, const void* k, int num_tokens, int num_q_heads, int num_kv_heads,
+            int head_dim, int dtype, long long q_stride, long long k_stride, const int32_t* rope_pos, int num_axes,
+            const float* inv_freq, const int32_t* axis, int rot_dim, int interleaved, int32_t* error_count,
+            void* stream) {
+    int rc = rope_ok(num_tokens, num_q_heads, num_kv_heads, head_dim, dtype, num_axes, rot_dim);
+    if (rc != PA_OK) return rc;
+    if (num_tokens == 0 || num_q_heads + num_kv_heads == 0) return PA_OK;
+    if ((num_q_heads > 0 && (!q || !q_out)) || (num_kv_heads > 0 && (!k || !k_out)) ||
+        (rot_dim > 0 && (!rope_pos || !inv_freq)))
+        return PA_ERR_INVALID_ARG;
+    if ((rc = check_device(nullptr)) != PA_OK) return rc;
+    RopeParams p;
+    p.q = q;
+    p.k = k;
+    p.v = nullptr;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.v_out = nullptr;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = 0;
+    p.rope_pos = rope_pos;
+    p.inv_freq = inv_freq;
+    p.axis = axis;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.rot_dim = rot_dim;
+    p.num_axes = num_axes;
+    p.interleaved = interleaved != 0;
+    p.error_count = error_count;
+    return launch_rope(p, dtype, static_cast<cudaStream_t>(stream));
+}
+
+int pa_rope_write_kv_paged(void* q_out, const void* q, const void* k_new, const void* v_new, int num_tokens,
+                           int num_q_heads, int num_kv_heads, int head_dim, int dtype, long long q_stride,
+                           long long k_stride, long long v_stride, const int32_t* rope_pos, int num_axes,
+                           const float* inv_freq, const int32_t* axis, int rot_dim, int interleaved, void* k_cache,
+                           void* v_cache, int num_blocks, int block_size, const int32_t* block_tables, int num_seqs,
+                           int max_blocks_per_seq, const int32_t* seq_idx, const int32_t* pos, float* key_weights,
+                           int32_t* key_pos, int key_width, const int32_t* token_pos, int64_t* slot_mapping,
+                           int32_t* error_count, void* stream) {
+    int rc = rope_ok(num_tokens, num_q_heads, num_kv_heads, head_dim, dtype, num_axes, rot_dim);
+    if (rc != PA_OK) return rc;
+    if (num_kv_heads < 1 || num_blocks < 0 || block_size < 1 || num_seqs < 0 || max_blocks_per_seq < 0 || key_width < 0 ||
+        (key_weights == nullptr) != (key_pos == nullptr) || (key_weights != nullptr && key_width < 1))
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if ((num_q_heads > 0 && (!q || !q_out)) || !k_new || !v_new || !k_cache || !v_cache || !seq_idx || !pos ||
+        (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables) || (rot_dim > 0 && (!rope_pos || !inv_freq)))
+        return PA_ERR_INVALID_ARG;
+    if ((rc = check_device(nullptr)) != PA_OK) return rc;
+    RopeParams p;
+    p.q = q;
+    p.k = k_new;
+    p.v = v_new;
+    p.q_out = q_out;
+    p.k_out = k_cache;
+    p.v_out = v_cache;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.rope_pos = rope_pos;
+    p.inv_freq = inv_freq;
+    p.axis = axis;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.rot_dim = rot_dim;
+    p.num_axes = num_axes;
+    p.interleaved = interleaved != 0;
+    p.block_tables = block_tables;
+    p.seq_idx = seq_idx;
+    p.pos = pos;
+    p.token_pos = token_pos;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.num_seqs = num_seqs;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.key_weights = key_weights;
+    p.key_pos = key_pos;
+    p.key_width = key_weights ? key_width : 0;
+    p.slot_mapping = slot_mapping;
+    p.error_count = error_count;
+    return launch_rope(p, dtype, static_cast<cudaStream_t>(stream));
+}
+
+size_t pa_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
+                                        int max_context_len) {
+    if (num_seqs < 0 || max_context_len < 0 || decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size))
+        return 0;
+    int num_sms = 0;
+    if (check_device(&num_sms) != PA_OK) return 0;
+    const long long partials = most_partials(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, num_sms);
+    if (partials > INT_MAX) return 0;
+    // (as many sequences of one kv head and one partial each)
+    const int group = num_q_heads / num_kv_heads;
+    return decode_workspace_layout((int)partials, group, 1, head_dim, 1).total +
+           round_up((size_t)num_seqs * num_q_heads * max_context_len * 4);
+}
+
+int pa_decode_weights(void* out, const void* q, int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                      int dtype, const void* k_cache, const void* v_cache, int num_blocks, int block_size,
+                      const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                      int max_context_len, float scale, float* key_weights, int key_width, void* workspace,
+                      size_t workspace_bytes, int32_t* error_count, void* stream) {
+    if (num_seqs < 0 || num_blocks < 0 || max_blocks_per_seq < 0 || max_context_len < 0 || key_width < max_context_len)
+        return PA_ERR_INVALID_ARG;
+    int rc = decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size);
+    if (rc != PA_OK) return rc;
+    if (dtype != PA_F32 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!out || !q || !k_cache || !v_cache || !context_lens || (key_width > 0 && !key_weights) ||
+        (max_blocks_per_seq > 0 && !block_tables))
+        return PA_ERR_INVALID_ARG;
+    int num_sms = 0;
+    if ((rc = check_device(&num_sms)) != PA_OK) return rc;
+    const DecodePlan plan =
+        plan_decode(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, num_sms, SIZE_MAX);
+    const DecodeWorkspace lay =
+        decode_workspace_layout(num_seqs, num_q_heads, num_kv_heads, head_dim, plan.max_splits);
+    const size_t scores = (size_t)num_seqs * num_q_heads * max_context_len * 4;
+    if (!workspace || workspace_bytes < lay.total + scores || !aligned(workspace, 256)) return PA_ERR_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    DecodeParams p;
+    p.out = out;
+    p.q = q;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.error_count = error_count;
+    p.work = reinterpret_cast<int*>(ws + lay.work);
+    p.ws_ml = reinterpret_cast<float2*>(ws + lay.ml);
+    p.ws_o = reinterpret_cast<float*>(ws + lay.o);
+    p.ws_scores = reinterpret_cast<float*>(ws + lay.total);
+    p.score_width = max_context_len;
+    p.key_weights = key_weights;
+    p.key_width = key_width;
+    p.num_seqs = num_seqs;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.group = num_q_heads / num_kv_heads;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.max_context_len = max_context_len;
+    p.partition = plan.partition;
+    p.small_partition = plan.small_partition;
+    p.small_from = plan.small_from;
+    p.max_splits = plan.max_splits;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (decode_tc_supported(p, dtype)) {
+        rc = launch_decode_tc(p, num_sms, st);
+    } else {
+        p.small_from = 1 << 30;  // one CTA for each partition: uniform ones
+        rc = launch_decode_fma(p, dtype, st);
+    }
+    return rc != PA_OK ? rc : launch_decode_weights(p, dtype, st);
+}
+
+size_t pa_prefill_weights_workspace_size(int num_chunks, int total_q, int max_q_len, int num_q_heads, int num_kv_heads,
+                                         int head_dim, int block_size, int max_context_len) {
+    if (num_chunks < 0 || total_q < 0 || max_q_len < 0 || max_context_len < 0 ||
+        decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size))
+        return 0;
+    return prefill_weights_layout(num_chunks, total_q, num_q_heads, num_kv_heads, max_context_len, 1).total;
+}
+
+int pa_prefill_chunk_weights(void* out, const void* q, const int32_t* cu_q_lens, const int32_t* q_start_pos,
+                             const int32_t* seq_of_chunk, int num_chunks, int total_q, int max_q_len, int num_seqs,
+                             int num_q_heads, int num_kv_heads, int head_dim, int dtype, const void* k_cache,
+                             const void* v_cache, int num_blocks, int block_size, const int32_t* block_tables,
+                             int max_blocks_per_seq, const int32_t* context_lens, int max_context_len, float scale,
+                             float* key_weights, int key_width, void* workspace, size_t workspace_bytes,
+                             int32_t* error_count, void* stream) {
+    if (num_chunks < 0 || total_q < 0 || max_q_len < 0 || num_seqs < 0 || num_blocks < 0 || max_blocks_per_seq < 0 ||
+        max_context_len < 0 || key_width < max_context_len)
+        return PA_ERR_INVALID_ARG;
+    int rc = decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size);
+    if (rc != PA_OK) return rc;
+    if (dtype != PA_F32 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if (num_chunks == 0 || total_q == 0 || max_q_len == 0) return PA_OK;
+    if (!out || !q || !cu_q_lens || !q_start_pos || !seq_of_chunk || !k_cache || !v_cache || !context_lens ||
+        !block_tables || num_seqs == 0 || (key_width > 0 && !key_weights))
+        return PA_ERR_INVALID_ARG;
+    int num_sms = 0;
+    if ((rc = check_device(&num_sms)) != PA_OK) return rc;
+    PrefillParams p;
+    p.out = out;
+    p.q = q;
+    p.cu_q_lens = cu_q_lens;
+    p.q_start_pos = q_start_pos;
+    p.seq_of_chunk = seq_of_chunk;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.error_count = error_count;
+    p.num_chunks = num_chunks;
+    p.total_q = total_q;
+    p.max_q_len = max_q_len;
+    p.num_seqs = num_seqs;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.group = num_q_heads / num_kv_heads;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.max_context_len = max_context_len;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    const PrefillWeightsWorkspace lay =
+        prefill_weights_layout(num_chunks, total_q, num_q_heads, num_kv_heads, max_context_len, 1);
+    if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return PA_ERR_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    p.lse = reinterpret_cast<float*>(ws + lay.lse);
+    p.partial = reinterpret_cast<float*>(ws + lay.partial);
+    p.partial_width = max_context_len;
+    p.pieces = 1;
+    p.key_weights = key_weights;
+    p.key_width = key_width;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    rc = launch_prefill_weights_fma(p, dtype, st);
+    return rc != PA_OK ? rc : launch_prefill_weights_add(p, st);
+}
+
+size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_len, int budget) {
+    if (num_seqs < 0 || num_kv_heads < 1 || max_context_len < 0 || budget < 1) return 0;
+    return evict_workspace_layout(num_seqs, num_kv_heads, max_context_len, budget).total;
+}
+
+int pa_evict_tokens(void* k_cache, void* v_cache, int num_blocks, int block_size, int num_kv_heads, int head_dim,
+                    int dtype, const int32_t* block_tables, int num_seqs, int max_blocks_per_seq,
+                    const int32_t* context_lens, int max_context_len, float* key_weights, int32_t* key_pos,
+                    int key_width, const int32_t* next_pos, int budget, int keep_first, int keep_recent,
+                    int32_t* new_lens, void* workspace, size_t workspace_bytes, int32_t* error_count, void* stream) {
+    if (num_blocks < 0 || block_size < 1 || num_kv_heads < 1 || head_dim < 1 || num_seqs < 0 || max_blocks_per_seq < 0 ||
+        max_context_len < 0 || key_width < max_context_len || budget < 1 || keep_first < 0 || keep_recent < 0 ||
+        (long long)keep_first + keep_recent > budget)
+        return PA_ERR_INVALID_ARG;
+    if (dtype != PA_F32 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if (num_seqs == 0) return PA_OK;
+    if (!k_cache || !v_cache || !context_lens || !next_pos || !new_lens || (key_width > 0 && (!key_weights || !key_pos)) ||
+        (max_blocks_per_seq > 0 && !block_tables))
+        return PA_ERR_INVALID_ARG;
+    const long long row_bytes = (long long)head_dim * elem_size(dtype);
+    if (row_bytes % 16 != 0 || row_bytes > (1 << 20) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        (long long)num_seqs * num_kv_heads > INT_MAX)
+        return PA_ERR_UNSUPPORTED;
+    int rc = check_device(nullptr);
+    if (rc != PA_OK) return rc;
+    const EvictWorkspace lay = evict_workspace_layout(num_seqs, num_kv_heads, max_context_len, budget);
+    if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return PA_ERR_WORKSPACE;
+    char* ws = static_cast<char*>(workspace);
+    EvictParams p;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.num_blocks = num_blocks;
+    p.block_size = block_size;
+    p.num_kv_heads = num_kv_heads;
+    p.block_tables = block_tables;
+    p.num_seqs = num_seqs;
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.context_lens = context_lens;
+    p.max_context_len = max_context_len;
+    p.key_weights = key_weights;
+    p.key_pos = key_pos;
+    p.key_width = key_width;
+    p.next_pos = next_pos;
+    p.budget = budget;
+    p.keep_first = keep_first;
+    p.keep_recent = keep_recent;
+    p.new_lens = new_lens;
+    p.counts = reinterpret_cast<int*>(ws + lay.counts);
+    p.lens = reinterpret_cast<int*>(ws + lay.lens);
+    p.src = reinterpret_cast<int*>(ws + lay.src);
+    p.dst = reinterpret_cast<int*>(ws + lay.dst);
+    p.max_moves = lay.max_moves;
+    p.error_count = error_count;
+    return launch_evict(p, (int)row_bytes, static_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

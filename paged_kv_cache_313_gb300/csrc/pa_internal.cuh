@@ -49,6 +49,20 @@ int launch_kernel(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, 
     return e == cudaSuccess ? PA_OK : set_cuda_error(e);
 }
 
+// Division of n < 2^30 by a number known to the host: n / d = (hi32(n mul) + n) >> shift with shift the least such that
+// 2^shift >= d and mul = floor(2^32 (2^shift - d) / d) + 1 (multiplication by a rounded-up reciprocal; checked against
+// the quotient for divisors up to 2^30).  A division by a runtime number is some 20 instructions; on the cold path to a
+// kernel's first loads they cost more than the loop they save (decode of four short sequences 7.2 us with, 6.7 without).
+struct Divisor {
+    uint32_t mul, shift, d;
+    Divisor() = default;
+    explicit Divisor(uint32_t d_) : mul(0), shift(0), d(d_) {
+        while ((1u << shift) < d) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - d)) / d + 1);
+    }
+    __device__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
+};
+
 inline int elem_size(int dtype) { return dtype == PA_F32 ? 4 : 2; }
 
 // Shapes pa_decode takes: PA_OK, PA_ERR_INVALID_ARG (head counts that do not
@@ -126,6 +140,13 @@ struct DecodeParams {
     // e4m3 pools with a scale per (block, kv head) (pa_decode_fp8_block): float [num_blocks][num_kv_heads]
     const float* k_scales = nullptr;
     const float* v_scales = nullptr;
+    // pa_decode_weights: the decode kernel leaves every score (base-2 units, -inf for a masked token) in ws_scores, float
+    // [num_seqs][num_kv_heads][score_width][G], and every item its (m, l); the softmax weights of the last kernel
+    // are added to key_weights, float [num_seqs][num_kv_heads][key_width].
+    float* ws_scores = nullptr;
+    int score_width = 0;
+    float* key_weights = nullptr;
+    int key_width = 0;
 };
 
 struct PrefillParams {
@@ -157,7 +178,66 @@ struct PrefillParams {
     // e4m3 pools with a scale per (block, kv head) (pa_prefill_chunk_fp8_block): float [num_blocks][num_kv_heads]
     const float* k_scales = nullptr;
     const float* v_scales = nullptr;
-    int max_context_len = 0x7FFFFFFF;  // keys at or beyond it are not read (block-scaled pools)
+    int max_context_len = 0x7FFFFFFF;  // keys at or beyond it are not read (block-scaled pools, key weights)
+    // pa_prefill_chunk_weights: the attention kernel leaves each row's log2 of its softmax sum in base-2 units, m + log2(l),
+    // in lse, float [num_kv_heads][total_q * G] (+inf for a row without a key, whose weights are then all zero); a second
+    // kernel leaves each key's summed weights in partial, float [num_chunks][num_kv_heads][pieces][partial_width], and a
+    // third adds those to key_weights, float [num_seqs][num_kv_heads][key_width], in a fixed order.
+    float* lse = nullptr;
+    float* partial = nullptr;
+    int pieces = 1, partial_width = 0;
+    float* key_weights = nullptr;
+    int key_width = 0;
+};
+
+// pa_rope and pa_rope_write_kv_paged (the latter: pos set).
+struct RopeParams {
+    const void *q, *k, *v;
+    void *q_out, *k_out, *v_out;  // k_out, v_out: dense rows, or the pools
+    long long q_stride, k_stride, v_stride;  // elements from a token's rows to the next token's
+    const int32_t* rope_pos;  // [num_axes][num_tokens]
+    const float* inv_freq;    // [rot_dim / 2]
+    const int32_t* axis;      // [rot_dim / 2], or nullptr: all of axis 0
+    int num_tokens, num_q_heads, num_kv_heads, head_dim, rot_dim, num_axes, interleaved;
+    const int32_t* block_tables = nullptr;
+    const int32_t* seq_idx = nullptr;
+    const int32_t* pos = nullptr;
+    const int32_t* token_pos = nullptr;
+    int num_blocks = 0, block_size = 1, num_seqs = 0, max_blocks_per_seq = 0;
+    float* key_weights = nullptr;
+    int32_t* key_pos = nullptr;
+    int key_width = 0;  // 0: no key state
+    int64_t* slot_mapping = nullptr;
+    int32_t* error_count = nullptr;
+    Divisor by_head;
+};
+
+// pa_evict_tokens.
+struct EvictWorkspace {
+    size_t counts, lens, src, dst, total;  // byte offsets
+    int max_moves;
+};
+EvictWorkspace evict_workspace_layout(int num_seqs, int num_kv_heads, int max_context_len, int budget);
+struct EvictParams {
+    void* k_cache;
+    void* v_cache;
+    int num_blocks, block_size, num_kv_heads;
+    const int32_t* block_tables;
+    int num_seqs, max_blocks_per_seq;
+    const int32_t* context_lens;
+    int max_context_len;
+    float* key_weights;
+    int32_t* key_pos;
+    int key_width;
+    const int32_t* next_pos;
+    int budget, keep_first, keep_recent;
+    int32_t* new_lens;
+    int* counts;  // moves of each (sequence, kv head)
+    int* lens;    // what new_lens becomes
+    int* src;     // [pair][max_moves]
+    int* dst;
+    int max_moves;
+    int32_t* error_count;
 };
 
 // Kernel launchers (defined in the .cu files).
@@ -213,6 +293,13 @@ int launch_decode_merge(const DecodeParams& p, int dtype, int num_sms, cudaStrea
 // The decode kernel for these parameters (tensor-core or FMA), then the
 // split-KV merge when there is more than one partition.
 int run_decode(const DecodeParams& p, int dtype, int num_sms, cudaStream_t stream);
+// After run_decode with ws_scores set: the merge of the partials, and the scores' softmax weights added to key_weights.
+int launch_decode_weights(const DecodeParams& p, int dtype, cudaStream_t stream);
+// Prefill with lse, partial and key_weights set: the attention with its rows' lse, the keys' partial sums, their addition.
+int launch_prefill_weights_fma(const PrefillParams& p, int dtype, cudaStream_t stream);
+int launch_prefill_weights_add(const PrefillParams& p, cudaStream_t stream);
+int launch_rope(const RopeParams& p, int dtype, cudaStream_t stream);
+int launch_evict(const EvictParams& p, int row_bytes, cudaStream_t stream);
 bool prefill_tc_supported(const PrefillParams& p, int dtype);
 int launch_prefill_tc(const PrefillParams& p, cudaStream_t stream);
 
@@ -273,20 +360,6 @@ __device__ __forceinline__ float to_float(e4m3_t x) { return e4m3x2_to_float2(x.
 __device__ __forceinline__ void count_error(int32_t* error_count, int n = 1) {
     if (error_count != nullptr && n != 0) atomicAdd(error_count, n);
 }
-
-// Division of n < 2^30 by a number known to the host: n / d = (hi32(n mul) + n) >> shift with shift the least such that
-// 2^shift >= d and mul = floor(2^32 (2^shift - d) / d) + 1 (multiplication by a rounded-up reciprocal; checked against
-// the quotient for divisors up to 2^30).  A division by a runtime number is some 20 instructions; on the cold path to a
-// kernel's first loads they cost more than the loop they save (decode of four short sequences 7.2 us with, 6.7 without).
-struct Divisor {
-    uint32_t mul, shift, d;
-    Divisor() = default;
-    explicit Divisor(uint32_t d_) : mul(0), shift(0), d(d_) {
-        while ((1u << shift) < d) ++shift;
-        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - d)) / d + 1);
-    }
-    __device__ int div(int n) const { return (int)((__umulhi((uint32_t)n, mul) + (uint32_t)n) >> shift); }
-};
 
 // Number of token partitions of a context of length L (>= 1 so that an empty
 // context still has one owner that writes its zero output).

@@ -1,0 +1,329 @@
+// prefill_weights_fma.cu — pa_prefill_chunk_weights on the CUDA cores: fp32
+// pools, and the shapes that the tensor-core kernels do not take; and the
+// addition of the keys' partial sums, for both.
+//
+// A key's weight needs the final softmax sum of every row that sees it, so
+// there are two passes over Q K^T.  attend_kernel: a tile of 64 query rows
+// (positions times the G heads of a kv head) against tiles of 64 keys, with an
+// online softmax; it leaves the output and each row's lse = m + log2(l).
+// column_kernel: a tile of 64 keys against the row tiles that see it, summing
+// 2^(x - lse) down the rows in registers.  Both hold their tiles in shared
+// memory in 32 bits and compute 4 x 4 scores a thread.
+#include "prefill_weights.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;
+
+template <int D>
+struct Shape {
+    static constexpr int kPad = D + 4;  // floats in a staged row: 16-byte accesses of 8 rows touch all banks
+    static constexpr size_t kSmem = sizeof(float) * (2 * kTile * kPad + kTile * (kTile + 1));
+};
+
+// One row of `src` (D elements, 16-byte aligned) or zeros to shared memory, a 16-byte piece a thread: thread `lane` of the
+// D / VEC that share the row.
+template <typename T> __device__ __forceinline__ void widen(float* dst, const T* src, bool have);
+template <> __device__ __forceinline__ void widen<float>(float* dst, const float* src, bool have) {
+    *reinterpret_cast<float4*>(dst) = have ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+}
+template <> __device__ __forceinline__ void widen<__nv_bfloat16>(float* dst, const __nv_bfloat16* src, bool have) {
+    uint2 v = have ? *reinterpret_cast<const uint2*>(src) : make_uint2(0u, 0u);
+    *reinterpret_cast<float4*>(dst) =
+        make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                    __uint_as_float(v.y & 0xFFFF0000u));
+}
+
+// kTile rows into shared memory; row_of(r) gives the row's first element or nullptr.
+template <typename T, int D, typename F>
+__device__ __forceinline__ void stage(float* dst, F row_of) {
+    constexpr int kPieces = D / 4;
+    for (int i = threadIdx.x; i < kTile * kPieces; i += kThreads) {
+        const int r = i / kPieces, c = i - r * kPieces;
+        const T* src = row_of(r);
+        widen<T>(dst + r * Shape<D>::kPad + 4 * c, src + 4 * c, src != nullptr);
+    }
+}
+
+// acc[i][j] = a row (ty + 16 i) . b row (tx + 16 j)
+template <int D>
+__device__ __forceinline__ void scores(const float* a, const float* b, int ty, int tx, float (&acc)[4][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+    for (int d = 0; d < D; d += 4) {
+        float4 x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(a + (ty + 16 * i) * Shape<D>::kPad + d);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = *reinterpret_cast<const float4*>(b + (tx + 16 * j) * Shape<D>::kPad + d);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                acc[i][j] = fmaf(x[i].x, y[j].x, fmaf(x[i].y, y[j].y, fmaf(x[i].z, y[j].z, fmaf(x[i].w, y[j].w, acc[i][j]))));
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) attend_kernel(const PrefillParams p) {
+    constexpr int kPad = Shape<D>::kPad, kCols = D / 64;  // float4 columns a thread holds of each output row
+    extern __shared__ float smem[];
+    float *qs = smem, *ks = smem + kTile * kPad, *ps = ks + kTile * kPad;  // ps: [kTile][kTile + 1]
+    __shared__ int block_s[kTile];
+    pdl_trigger();
+    pdl_wait();
+    const int c = blockIdx.y, kvh = blockIdx.z, G = p.group, B = p.block_size;
+    WeightChunk d;
+    if (!weight_chunk(p, c, d)) {
+        if (blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) count_error(p.error_count);
+        return;
+    }
+    const int per_tile = kTile / G, i0 = blockIdx.x * per_tile;
+    if (i0 >= d.n) return;
+    const int nq = min(per_tile, d.n - i0);
+    const int want = d.start + i0 + nq, nkeys = max(0, min(want, d.cap));  // keys [0, nkeys) for the tile's last row
+    if (want > d.cap && kvh == 0 && threadIdx.x == 0) count_error(p.error_count);
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int32_t* table = p.block_tables + (size_t)d.s * p.max_blocks_per_seq;
+    const T* q = static_cast<const T*>(p.q) + ((size_t)(d.r0 + i0) * p.num_q_heads + (size_t)kvh * G) * D;
+    stage<T, D>(qs, [&](int r) { return r < nq * G ? q + ((size_t)(r / G) * p.num_q_heads + r % G) * D : nullptr; });
+
+    float m[4], l[4], o[4][kCols][4];
+    int limit[4];  // keys that the row sees
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty + 16 * i;
+        m[i] = -INFINITY;
+        l[i] = 0.f;
+        limit[i] = r < nq * G ? min(d.start + i0 + r / G + 1, d.cap) : 0;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k) o[i][k][0] = o[i][k][1] = o[i][k][2] = o[i][k][3] = 0.f;
+    }
+    for (int j0 = 0; j0 < nkeys; j0 += kTile) {
+        __syncthreads();
+        if ((int)threadIdx.x < kTile) {
+            const int j = j0 + threadIdx.x;
+            int pb = -1;
+            if (j < nkeys) {
+                pb = table[j / B];
+                if (pb < 0 || pb >= p.num_blocks) {
+                    if (i0 + nq == d.n && (j % B == 0 || threadIdx.x == 0)) count_error(p.error_count);
+                    pb = -1;
+                }
+            }
+            block_s[threadIdx.x] = pb;
+        }
+        __syncthreads();
+        auto row_of = [&](const void* pool) {
+            return [&, pool](int r) {
+                const int pb = block_s[r];
+                return pb < 0 ? nullptr
+                              : static_cast<const T*>(pool) + (((size_t)pb * B + (j0 + r) % B) * p.num_kv_heads + kvh) * D;
+            };
+        };
+        stage<T, D>(ks, row_of(p.k_cache));
+        __syncthreads();
+        float x[4][4];
+        scores<D>(qs, ks, ty, tx, x);
+        float alpha[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float mx = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const int k = tx + 16 * j;
+                x[i][j] = j0 + k < limit[i] && block_s[k] >= 0 ? x[i][j] * p.scale_log2 : -INFINITY;
+                mx = fmaxf(mx, x[i][j]);
+            }
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const float now = fmaxf(m[i], mx);
+            float sum = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                // (all scores -inf: nothing; NaN scores leave the maximum and make the sum NaN)
+                const float e = x[i][j] == -INFINITY ? 0.f : exp2f(x[i][j] - now);
+                ps[(ty + 16 * i) * (kTile + 1) + tx + 16 * j] = e;
+                sum += e;
+            }
+#pragma unroll
+            for (int off = 1; off < 16; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            alpha[i] = m[i] == -INFINITY ? (l[i] == 0.f ? 0.f : 1.f) : exp2f(m[i] - now);
+            l[i] = l[i] * alpha[i] + sum;
+            m[i] = now;
+        }
+        __syncthreads();
+        stage<T, D>(ks, row_of(p.v_cache));
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < kCols; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][k][e] *= alpha[i];
+#pragma unroll 4
+        for (int j = 0; j < kTile; ++j) {
+            float4 v[kCols];
+#pragma unroll
+            for (int k = 0; k < kCols; ++k) v[k] = *reinterpret_cast<const float4*>(ks + j * kPad + 64 * k + 4 * tx);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float w = ps[(ty + 16 * i) * (kTile + 1) + j];
+                // a row does not see the keys behind it, whatever they hold
+                if (j0 + j >= limit[i]) continue;
+#pragma unroll
+                for (int k = 0; k < kCols; ++k) {
+                    o[i][k][0] = fmaf(w, v[k].x, o[i][k][0]);
+                    o[i][k][1] = fmaf(w, v[k].y, o[i][k][1]);
+                    o[i][k][2] = fmaf(w, v[k].z, o[i][k][2]);
+                    o[i][k][3] = fmaf(w, v[k].w, o[i][k][3]);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = ty + 16 * i;
+        if (r >= nq * G) continue;
+        const size_t row = (size_t)(d.r0 + i0) * G + r;
+        const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        if (tx == 0) p.lse[(size_t)kvh * p.total_q * G + row] = l[i] == 0.f ? INFINITY : m[i] + log2f(l[i]);
+        T* out = static_cast<T*>(p.out) + ((size_t)(d.r0 + i0 + r / G) * p.num_q_heads + (size_t)kvh * G + r % G) * D;
+#pragma unroll
+        for (int k = 0; k < kCols; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) out[64 * k + 4 * tx + e] = from_float<T>(o[i][k][e] * inv);
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads) column_kernel(const PrefillParams p) {
+    constexpr int kPad = Shape<D>::kPad;
+    extern __shared__ float smem[];
+    float *ks = smem, *qs = smem + kTile * kPad, *sums = qs + kTile * kPad;  // sums: [16][kTile]
+    __shared__ float lse_s[kTile];
+    pdl_trigger();
+    pdl_wait();
+    const int c = blockIdx.y, kvh = blockIdx.z, G = p.group, B = p.block_size;
+    const int j0 = blockIdx.x * kTile;
+    WeightChunk d;
+    if (!weight_chunk(p, c, d) || j0 >= d.nkeys) return;
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const int32_t* table = p.block_tables + (size_t)d.s * p.max_blocks_per_seq;
+    auto block_of = [&](int r) {
+        const int j = j0 + r;
+        if (j >= d.nkeys) return -1;
+        const int pb = table[j / B];
+        return pb >= 0 && pb < p.num_blocks ? pb : -1;
+    };
+    stage<T, D>(ks, [&](int r) {
+        const int pb = block_of(r);
+        return pb < 0 ? nullptr
+                      : static_cast<const T*>(p.k_cache) + (((size_t)pb * B + (j0 + r) % B) * p.num_kv_heads + kvh) * D;
+    });
+    const int per_tile = kTile / G;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    bool valid[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) valid[j] = block_of(tx + 16 * j) >= 0;
+    // the first tile of rows that sees a key of this tile
+    for (int i0 = max(0, j0 - d.start) / per_tile * per_tile; i0 < d.n; i0 += per_tile) {
+        const int nq = min(per_tile, d.n - i0);
+        const T* q = static_cast<const T*>(p.q) + ((size_t)(d.r0 + i0) * p.num_q_heads + (size_t)kvh * G) * D;
+        __syncthreads();
+        stage<T, D>(qs, [&](int r) { return r < nq * G ? q + ((size_t)(r / G) * p.num_q_heads + r % G) * D : nullptr; });
+        if ((int)threadIdx.x < kTile)
+            lse_s[threadIdx.x] = (int)threadIdx.x < nq * G
+                                     ? p.lse[(size_t)kvh * p.total_q * G + (size_t)(d.r0 + i0) * G + threadIdx.x]
+                                     : INFINITY;
+        __syncthreads();
+        float x[4][4];
+        scores<D>(qs, ks, ty, tx, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = ty + 16 * i, limit = min(d.start + i0 + r / G + 1, d.cap);
+            if (r >= nq * G) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (valid[j] && j0 + tx + 16 * j < limit) sum[j] += exp2f(x[i][j] * p.scale_log2 - lse_s[r]);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sums[ty * kTile + tx + 16 * j] = sum[j];
+    __syncthreads();
+    if ((int)threadIdx.x < kTile && j0 + (int)threadIdx.x < d.nkeys) {
+        float total = 0.f;
+        for (int i = 0; i < 16; ++i) total += sums[i * kTile + threadIdx.x];
+        p.partial[((size_t)c * p.num_kv_heads + kvh) * p.partial_width + j0 + threadIdx.x] = total;
+    }
+}
+
+template <typename T, int D>
+int launch(const PrefillParams& p, cudaStream_t stream) {
+    int rc = ensure_dynamic_smem(reinterpret_cast<const void*>(attend_kernel<T, D>), Shape<D>::kSmem);
+    if (rc == PA_OK) rc = ensure_dynamic_smem(reinterpret_cast<const void*>(column_kernel<T, D>), Shape<D>::kSmem);
+    if (rc != PA_OK) return rc;
+    const int per_tile = kTile / p.group;
+    rc = launch_kernel(attend_kernel<T, D>, dim3((p.max_q_len + per_tile - 1) / per_tile, p.num_chunks, p.num_kv_heads),
+                       dim3(kThreads), Shape<D>::kSmem, stream, p);
+    if (rc != PA_OK || p.max_context_len == 0) return rc;
+    return launch_kernel(column_kernel<T, D>, dim3((p.max_context_len + kTile - 1) / kTile, p.num_chunks, p.num_kv_heads),
+                         dim3(kThreads), Shape<D>::kSmem, stream, p);
+}
+
+// The chunks' partial sums added to their sequences' weights.  The first usable chunk of a sequence adds those of all its
+// chunks, in the order of the chunks and of the pieces: one owner for each element, and one order.
+constexpr int kAddThreads = 256;
+__global__ void __launch_bounds__(kAddThreads) add_kernel(const PrefillParams p) {
+    pdl_trigger();
+    pdl_wait();
+    const int c = blockIdx.y, kvh = blockIdx.z, j = blockIdx.x * kAddThreads + threadIdx.x;
+    WeightChunk d;
+    if (!weight_chunk(p, c, d)) return;
+    bool mine = true;
+    for (int e = threadIdx.x; e < c && mine; e += kAddThreads) {
+        WeightChunk o;
+        if (p.seq_of_chunk[e] == d.s && weight_chunk(p, e, o)) mine = false;
+    }
+    if (!__syncthreads_and(mine)) return;
+    float sum = 0.f;
+    bool any = false;
+    __shared__ int later[kAddThreads];
+    for (int e0 = c; e0 < p.num_chunks; e0 += kAddThreads) {  // this sequence's chunks among the next kAddThreads
+        __syncthreads();
+        const int e = e0 + threadIdx.x;
+        const bool same = e < p.num_chunks && p.seq_of_chunk[e] == d.s;
+        later[threadIdx.x] = same;
+        if (!__syncthreads_or(same)) continue;
+        for (int k = 0; k < kAddThreads && e0 + k < p.num_chunks; ++k) {
+            WeightChunk o;
+            if (!later[k] || !weight_chunk(p, e0 + k, o) || j >= o.nkeys) continue;
+            any = true;
+            const float* part = p.partial + ((size_t)(e0 + k) * p.num_kv_heads + kvh) * p.pieces * p.partial_width + j;
+            for (int i = 0; i < p.pieces; ++i) sum += part[(size_t)i * p.partial_width];
+        }
+    }
+    if (any) p.key_weights[((size_t)d.s * p.num_kv_heads + kvh) * p.key_width + j] += sum;
+}
+
+}  // namespace
+
+int launch_prefill_weights_fma(const PrefillParams& p, int dtype, cudaStream_t stream) {
+    if (p.group > 16 || p.num_chunks > 65535 || p.num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (((uintptr_t)p.q & 15) || ((uintptr_t)p.k_cache & 15) || ((uintptr_t)p.v_cache & 15)) return PA_ERR_UNSUPPORTED;
+    if (dtype == PA_F32) return p.head_dim == 64 ? launch<float, 64>(p, stream) : launch<float, 128>(p, stream);
+    return p.head_dim == 64 ? launch<__nv_bfloat16, 64>(p, stream) : launch<__nv_bfloat16, 128>(p, stream);
+}
+
+int launch_prefill_weights_add(const PrefillParams& p, cudaStream_t stream) {
+    if (p.max_context_len == 0) return PA_OK;
+    return launch_kernel(add_kernel, dim3((p.max_context_len + kAddThreads - 1) / kAddThreads, p.num_chunks, p.num_kv_heads),
+                         dim3(kAddThreads), 0, stream, p);
+}
+
+}  // namespace pa

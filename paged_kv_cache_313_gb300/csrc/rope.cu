@@ -1,0 +1,216 @@
+// rope.cu — rotary positions with several axes on a step's queries and keys,
+// alone (pa_rope) or with the paged write (pa_rope_write_kv_paged).
+//
+// Pair i of a head (elements i and R/2 + i, or 2i and 2i + 1 where pairs are
+// interleaved) is the complex number a + ib; at position pos[axis[i]] it is
+// multiplied by e^(i angle), angle = pos[axis[i]] * inv_freq[i].  Elements from
+// R on stay as they are.
+//
+// The angle is wanted modulo a turn.  A float product loses that for far
+// positions (10^5 rad is known to 2^-7 in 24 bits), and 64-bit floats are slow
+// here, so it is counted in whole numbers: inv_freq = m 2^e with a 24-bit m, and
+//     turns per position * 2^64 = m K 2^(e-2),  K = round(2^66 / (2 pi)),
+// kept modulo 2^64; times the position, modulo 2^64, is the fraction of a turn,
+// exact to 2^-32 for every 32-bit position.  Its upper half as a signed number
+// is the angle in half turns for sincospi.
+//
+// Bound by memory: q, k and v are read once and written once.  One CTA per
+// token: its first loads go out before the angles are worked out (once per
+// token and pair, shared by all heads through shared memory).
+#include "pa_internal.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kAhead = 2;  // items whose loads a thread issues before the angles
+
+template <typename T, int VEC> struct Chunk;  // VEC elements moved by one access
+template <> struct Chunk<__nv_bfloat16, 8> { using type = uint4; };
+template <> struct Chunk<float, 4> { using type = uint4; };
+template <> struct Chunk<__nv_bfloat16, 1> { using type = uint16_t; };
+template <> struct Chunk<float, 1> { using type = uint32_t; };
+
+// inv_freq as turns per position, 2^-64 turns, modulo a turn (see above); *finite false for an infinity or NaN.
+__device__ __forceinline__ uint64_t turns_of(float inv_freq, bool* finite) {
+    constexpr uint64_t kInvTau = 0xA2F9836E4E44152Aull;  // 2^66 / (2 pi), rounded
+    const uint32_t u = __float_as_uint(inv_freq), ex = (u >> 23) & 255u;
+    *finite = ex != 255u;
+    const uint64_t m = (u & 0x7FFFFFu) | (ex ? 0x800000u : 0u);
+    const uint64_t lo = m * kInvTau, hi = __umul64hi(m, kInvTau);
+    const int right = 2 - ((int)(ex ? ex : 1u) - 150);  // inv_freq = m 2^(ex - 150)
+    uint64_t t;
+    if (right <= 0) t = -right < 64 ? lo << -right : 0;
+    else if (right < 64) t = (lo >> right) | (hi << (64 - right));
+    else t = right < 128 ? hi >> (right - 64) : 0;
+    return (u >> 31) ? 0 - t : t;
+}
+
+template <typename T, int VEC, bool kWrite>
+__global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
+    using C = typename Chunk<T, VEC>::type;
+    extern __shared__ float2 turn[];  // cos and sin of each pair
+    pdl_trigger();
+    pdl_wait();
+    const long long t = blockIdx.x;
+    const int D = p.head_dim, half = p.rot_dim / 2;
+    const int per_head = half / VEC + (D - p.rot_dim) / VEC;  // pair items, then pass-through items
+    const int items = (p.num_q_heads + p.num_kv_heads) * per_head + (kWrite ? p.num_kv_heads * (D / VEC) : 0);
+
+    int s = 0, at = 0;
+    long long slot = t;  // the row of K and V that is written, -1 for none
+    if (kWrite) {
+        at = p.pos[t];
+        if (at < 0) {  // padding: nothing of the token is written
+            if (threadIdx.x == 0 && p.slot_mapping) p.slot_mapping[t] = -1;
+            return;
+        }
+        s = p.seq_idx[t];
+        slot = -1;
+        const int block = at / p.block_size;
+        if (s >= 0 && s < p.num_seqs && block < p.max_blocks_per_seq && (!p.key_width || at < p.key_width)) {
+            const int physical = p.block_tables[(long long)s * p.max_blocks_per_seq + block];
+            if (physical >= 0 && physical < p.num_blocks)
+                slot = (long long)physical * p.block_size + (at - block * p.block_size);
+        }
+        if (threadIdx.x == 0) {
+            if (slot < 0) count_error(p.error_count);
+            if (p.slot_mapping) p.slot_mapping[t] = slot;
+        }
+    }
+
+    // where item i of the token reads and writes; pairs: b is the partner's chunk
+    struct Item {
+        const C* src;
+        C* dst;
+        int b, pair;  // distance to the partner's chunk in chunks (0: copied), first pair
+    };
+    auto item_of = [&](int i) {
+        Item it;
+        const int rotated = (p.num_q_heads + p.num_kv_heads) * per_head;
+        const T *src;
+        T* dst;
+        if (kWrite && i >= rotated) {  // V
+            const int e = (i - rotated) * VEC;
+            src = static_cast<const T*>(p.v) + t * p.v_stride + e;
+            dst = slot < 0 ? nullptr : static_cast<T*>(p.v_out) + slot * p.num_kv_heads * D + e;
+            it.b = 0;
+        } else {
+            const int h = p.by_head.div(i), c = i - h * per_head;
+            int e;
+            if (c < half / VEC) {
+                e = p.interleaved ? 2 * c * VEC : c * VEC;
+                it.b = p.interleaved ? 1 : half / VEC;
+                it.pair = c * VEC;
+            } else {
+                e = p.rot_dim + (c - half / VEC) * VEC;
+                it.b = 0;
+            }
+            if (h < p.num_q_heads) {
+                src = static_cast<const T*>(p.q) + t * p.q_stride + (long long)h * D + e;
+                dst = static_cast<T*>(p.q_out) + (t * p.num_q_heads + h) * D + e;
+            } else {
+                const int kh = h - p.num_q_heads;
+                src = static_cast<const T*>(p.k) + t * p.k_stride + (long long)kh * D + e;
+                dst = slot < 0 ? nullptr : static_cast<T*>(p.k_out) + (slot * p.num_kv_heads + kh) * D + e;
+            }
+        }
+        it.src = reinterpret_cast<const C*>(src);
+        it.dst = reinterpret_cast<C*>(dst);
+        return it;
+    };
+    Item it[kAhead];
+    C a[kAhead], b[kAhead];
+    auto load = [&](int k, int i) {
+        it[k] = item_of(i);
+        a[k] = *it[k].src;
+        if (it[k].b) b[k] = it[k].src[it[k].b];
+    };
+    auto store = [&](int k) {
+        if (it[k].b) {
+            T* x = reinterpret_cast<T*>(&a[k]);
+            T* y = reinterpret_cast<T*>(&b[k]);
+            auto pair = [&](T& re, T& im, int i) {
+                const float2 cs = turn[it[k].pair + i];
+                const float r = to_float(re), m = to_float(im);
+                re = from_float<T>(r * cs.x - m * cs.y);
+                im = from_float<T>(m * cs.x + r * cs.y);
+            };
+            if (p.interleaved) {
+                if constexpr (VEC == 1) {
+                    pair(x[0], y[0], 0);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VEC / 2; ++i) {
+                        pair(x[2 * i], x[2 * i + 1], i);
+                        pair(y[2 * i], y[2 * i + 1], VEC / 2 + i);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < VEC; ++i) pair(x[i], y[i], i);
+            }
+        }
+        if (it[k].dst) {
+            *it[k].dst = a[k];
+            if (it[k].b) it[k].dst[it[k].b] = b[k];
+        }
+    };
+
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        if ((int)threadIdx.x + k * kThreads < items) load(k, threadIdx.x + k * kThreads);
+    for (int i = threadIdx.x; i < half; i += kThreads) {
+        int axis = p.axis ? p.axis[i] : 0;
+        const bool known = axis >= 0 && axis < p.num_axes;
+        if (!known) count_error(p.error_count);
+        bool finite;
+        const uint64_t per = turns_of(p.inv_freq[i], &finite);
+        const int where = known ? p.rope_pos[(long long)axis * p.num_tokens + t] : 0;
+        const int32_t turns = (int32_t)((per * (uint64_t)(int64_t)where) >> 32);  // fraction of a turn, 2^-32
+        float2 cs;
+        sincospif((float)turns * 0x1p-31f, &cs.y, &cs.x);
+        if (!finite) cs = make_float2(NAN, NAN);
+        turn[i] = cs;
+    }
+    if (kWrite && p.key_width && slot >= 0)
+        for (int h = threadIdx.x; h < p.num_kv_heads; h += kThreads) {
+            const long long e = ((long long)s * p.num_kv_heads + h) * p.key_width + at;
+            p.key_weights[e] = 0.f;
+            p.key_pos[e] = p.token_pos ? p.token_pos[t] : at;
+        }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        if ((int)threadIdx.x + k * kThreads < items) store(k);
+    for (int i = threadIdx.x + kAhead * kThreads; i < items; i += kThreads) {
+        load(0, i);
+        store(0);
+    }
+}
+
+template <typename T, int VEC>
+int launch(const RopeParams& p, cudaStream_t stream) {
+    const int half = p.rot_dim / 2;
+    RopeParams r = p;
+    r.by_head = Divisor((uint32_t)(half / VEC + (p.head_dim - p.rot_dim) / VEC));
+    const size_t smem = sizeof(float2) * half;
+    return p.block_tables || p.pos
+               ? launch_kernel(rope_kernel<T, VEC, true>, dim3(p.num_tokens), dim3(kThreads), smem, stream, r)
+               : launch_kernel(rope_kernel<T, VEC, false>, dim3(p.num_tokens), dim3(kThreads), smem, stream, r);
+}
+
+}  // namespace
+
+int launch_rope(const RopeParams& p, int dtype, cudaStream_t stream) {
+    // 16-byte accesses where every chunk that they touch starts on 16 bytes, single elements otherwise
+    const int es = elem_size(dtype);
+    const uintptr_t mix = (uintptr_t)p.q | (uintptr_t)p.k | (uintptr_t)p.v | (uintptr_t)p.q_out | (uintptr_t)p.k_out |
+                          (uintptr_t)p.v_out | (uintptr_t)(p.q_stride * es) | (uintptr_t)(p.k_stride * es) |
+                          (uintptr_t)(p.v_stride * es) | (uintptr_t)(p.head_dim * es) | (uintptr_t)(p.rot_dim / 2 * es);
+    const bool wide = (mix & 15u) == 0;
+    if (dtype == PA_F32) return wide ? launch<float, 4>(p, stream) : launch<float, 1>(p, stream);
+    return wide ? launch<__nv_bfloat16, 8>(p, stream) : launch<__nv_bfloat16, 1>(p, stream);
+}
+
+}  // namespace pa

@@ -1,6 +1,7 @@
 """Python binding of libpa.so: the C ABI in include/pa.h, same names, torch
 CUDA tensors in and out.  Argument marshalling only (in ctypes, and in the
-compiled module _pa_bind.so for the calls over block-scaled e4m3 pools) — every step runs in the
+compiled module _pa_bind.so for the calls over block-scaled e4m3 pools and for
+those of caches that evict tokens) — every step runs in the
 library's CUDA kernels.  There is no CPU fallback: if the library is missing
 or fails to load, every call raises.
 
@@ -31,7 +32,9 @@ SYMBOLS = ("pa_version", "pa_status_string", "pa_last_cuda_error", "pa_slot_mapp
            "pa_decode_cascade_workspace_size", "pa_decode_cascade", "pa_decode_noalloc", "pa_prefill_workspace_size",
            "pa_prefill_chunk", "pa_write_fp8_block_workspace_size", "pa_write_kv_paged_fp8_block",
            "pa_read_kv_paged_fp8_block", "pa_decode_fp8_block_workspace_size", "pa_decode_fp8_block",
-           "pa_prefill_fp8_block_workspace_size", "pa_prefill_chunk_fp8_block", "pa_copy_blocks", "pa_map_to_kernel_blocks", "pa_stage_copy",
+           "pa_prefill_fp8_block_workspace_size", "pa_prefill_chunk_fp8_block", "pa_rope", "pa_rope_write_kv_paged",
+           "pa_decode_weights_workspace_size", "pa_decode_weights", "pa_prefill_weights_workspace_size",
+           "pa_prefill_chunk_weights", "pa_evict_workspace_size", "pa_evict_tokens", "pa_copy_blocks", "pa_map_to_kernel_blocks", "pa_stage_copy",
            "pa_check_bounded_wait")
 
 
@@ -45,7 +48,7 @@ class PaError(RuntimeError):
 _lock = threading.Lock()
 _lib = None
 
-_i, _sz, _p, _f = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float
+_i, _sz, _p, _f, _ll = ctypes.c_int, ctypes.c_size_t, ctypes.c_void_p, ctypes.c_float, ctypes.c_longlong
 _SIGNATURES = {
     "pa_version": ([], _i),
     "pa_status_string": ([_i], ctypes.c_char_p),
@@ -78,6 +81,17 @@ _SIGNATURES = {
     "pa_prefill_fp8_block_workspace_size": ([_i, _i, _i, _i, _i, _i, _i, _i], _sz),
     "pa_prefill_chunk_fp8_block": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _p, _p, _p, _p, _i, _i, _p, _i,
                                     _p, _i, _f, _p, _sz, _p, _p], _i),
+    "pa_rope": ([_p, _p, _p, _p, _i, _i, _i, _i, _i, _ll, _ll, _p, _i, _p, _p, _i, _i, _p, _p], _i),
+    "pa_rope_write_kv_paged": ([_p, _p, _p, _p, _i, _i, _i, _i, _i, _ll, _ll, _ll, _p, _i, _p, _p, _i, _i, _p, _p, _i, _i,
+                                _p, _i, _i, _p, _p, _p, _p, _i, _p, _p, _p, _p], _i),
+    "pa_decode_weights_workspace_size": ([_i, _i, _i, _i, _i, _i], _sz),
+    "pa_decode_weights": ([_p, _p, _i, _i, _i, _i, _i, _p, _p, _i, _i, _p, _i, _p, _i, _f, _p, _i, _p, _sz, _p, _p], _i),
+    "pa_prefill_weights_workspace_size": ([_i, _i, _i, _i, _i, _i, _i, _i], _sz),
+    "pa_prefill_chunk_weights": ([_p, _p, _p, _p, _p, _i, _i, _i, _i, _i, _i, _i, _i, _p, _p, _i, _i, _p, _i, _p, _i, _f,
+                                  _p, _i, _p, _sz, _p, _p], _i),
+    "pa_evict_workspace_size": ([_i, _i, _i, _i], _sz),
+    "pa_evict_tokens": ([_p, _p, _i, _i, _i, _i, _i, _p, _i, _i, _p, _i, _p, _p, _i, _p, _i, _i, _i, _p, _p, _sz, _p, _p],
+                        _i),
     "pa_stage_copy": ([_p, _p, _sz, _p], _i),
     "pa_check_bounded_wait": ([_i, _i, _p, _p, _p], _i),
     "pa_map_to_kernel_blocks": ([_p, _i, _i, _i, _p, _i, _p], _i),
@@ -415,7 +429,8 @@ _bind_module = None
 
 
 def _bind():
-    """The compiled binding of the calls over block-scaled e4m3 pools (csrc/bind.cpp; raises if it was not built)."""
+    """The compiled binding of the calls over block-scaled e4m3 pools and of those of caches that evict tokens
+    (csrc/bind.cpp; raises if it was not built)."""
     global _bind_module
     if _bind_module is None:
         lib()
@@ -498,6 +513,98 @@ def pa_prefill_chunk_fp8_block(q, cu_q_lens, q_start_pos, seq_of_chunk, max_q_le
                                           error_count, stream)
     if r.__class__ is int:
         _check("pa_prefill_chunk_fp8_block", r)
+    return r
+
+
+def pa_rope(q, k, rope_pos, inv_freq, axis=None, interleaved: bool = False, q_out=None, k_out=None, error_count=None,
+            stream=None):
+    """(q, k) with each head's pairs turned by rope_pos[axis[i], t] * inv_freq[i] radians: [T, heads, head_dim], float32 or
+    bfloat16, of which only the tokens may lie apart (parts of one fused projection).  rope_pos int32 [num_axes, T] (or
+    [T]); inv_freq float32 [rot_dim / 2]; axis int32 [rot_dim / 2] (None: all of axis 0)."""
+    r = (_bind_module or _bind()).rope(q, k, rope_pos, inv_freq, axis, interleaved, q_out, k_out, error_count, stream)
+    if r.__class__ is int:
+        _check("pa_rope", r)
+    return r
+
+
+def pa_rope_write_kv_paged(q, k_new, v_new, rope_pos, inv_freq, axis, k_cache, v_cache, block_tables, seq_idx, pos,
+                           interleaved: bool = False, q_out=None, key_weights=None, key_pos=None, token_pos=None,
+                           slot_mapping=None, error_count=None, stream=None) -> torch.Tensor:
+    """pa_rope on q and k_new (q is returned) and the paged write of k_new and v_new at index pos[t] of sequence seq_idx[t],
+    in one launch.  With key_weights and key_pos (float32 and int32 [num_seqs, Hkv, width]) the written tokens' weights
+    become 0 and their places token_pos (None: pos)."""
+    r = (_bind_module or _bind()).rope_write(q, k_new, v_new, rope_pos, inv_freq, axis, interleaved, k_cache, v_cache,
+                                             block_tables, seq_idx, pos, q_out, key_weights, key_pos, token_pos,
+                                             slot_mapping, error_count, stream)
+    if r.__class__ is int:
+        _check("pa_rope_write_kv_paged", r)
+    return r
+
+
+def new_decode_weights_workspace(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size, max_context_len,
+                                 device=None) -> torch.Tensor:
+    """A workspace for pa_decode_weights calls of up to these sizes (reusable across calls on one stream); the part that
+    must be zeroed once is."""
+    n = int(lib().pa_decode_weights_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, block_size,
+                                                   max_context_len))
+    if n == 0:
+        raise PaError("pa_decode_weights_workspace_size", PA_ERR_UNSUPPORTED, "unsupported sizes or device")
+    return torch.zeros(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_decode_weights(q, k_cache, v_cache, block_tables, context_lens, max_context_len: int, scale: float, key_weights,
+                      workspace, out=None, error_count=None, stream=None) -> torch.Tensor:
+    """pa_decode that also adds each key's softmax weights, summed over the query heads of its kv head, to key_weights
+    (float32 [N, Hkv, width], width >= max_context_len)."""
+    r = (_bind_module or _bind()).decode_weights(q, k_cache, v_cache, block_tables, context_lens, max_context_len, scale,
+                                                 key_weights, workspace, out, error_count, stream)
+    if r.__class__ is int:
+        _check("pa_decode_weights", r)
+    return r
+
+
+def new_prefill_weights_workspace(num_chunks, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim, block_size,
+                                  max_context_len, device=None) -> torch.Tensor:
+    """A workspace for pa_prefill_chunk_weights calls of up to these sizes."""
+    n = int(lib().pa_prefill_weights_workspace_size(num_chunks, total_q, max_q_len, num_q_heads, num_kv_heads, head_dim,
+                                                    block_size, max_context_len))
+    if n == 0:
+        raise PaError("pa_prefill_weights_workspace_size", PA_ERR_UNSUPPORTED, "unsupported sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_prefill_chunk_weights(q, cu_q_lens, q_start_pos, seq_of_chunk, max_q_len: int, k_cache, v_cache, block_tables,
+                             context_lens, max_context_len: int, scale: float, key_weights, workspace, out=None,
+                             error_count=None, stream=None) -> torch.Tensor:
+    """pa_prefill_chunk that also adds each key's softmax weights, over the chunks' queries that see it and the query heads
+    of its kv head, to key_weights (float32 [num_seqs, Hkv, width], width >= max_context_len)."""
+    r = (_bind_module or _bind()).prefill_weights(q, cu_q_lens, q_start_pos, seq_of_chunk, max_q_len, k_cache, v_cache,
+                                                  block_tables, context_lens, max_context_len, scale, key_weights,
+                                                  workspace, out, error_count, stream)
+    if r.__class__ is int:
+        _check("pa_prefill_chunk_weights", r)
+    return r
+
+
+def new_evict_workspace(num_seqs, num_kv_heads, max_context_len, budget, device=None) -> torch.Tensor:
+    """A workspace for pa_evict_tokens calls of up to these sizes with this budget."""
+    n = int(lib().pa_evict_workspace_size(int(num_seqs), int(num_kv_heads), int(max_context_len), int(budget)))
+    if n == 0:
+        raise PaError("pa_evict_workspace_size", PA_ERR_INVALID_ARG, "invalid sizes")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def pa_evict_tokens(k_cache, v_cache, block_tables, context_lens, max_context_len: int, key_weights, key_pos, next_pos,
+                    budget: int, keep_first: int, keep_recent: int, workspace, new_lens=None, error_count=None,
+                    stream=None) -> torch.Tensor:
+    """Cut every sequence of more than `budget` cached tokens down to `budget`: each kv head keeps its first keep_first and
+    last keep_recent tokens of the sequence (by key_pos and next_pos) and those with the largest key_weights; kept tokens
+    at indices beyond the budget move into the places below it that are free.  Returns new_lens, min(context_lens, budget)
+    (context_lens itself may be given for it)."""
+    r = (_bind_module or _bind()).evict(k_cache, v_cache, block_tables, context_lens, max_context_len, key_weights, key_pos,
+                                        next_pos, budget, keep_first, keep_recent, workspace, new_lens, error_count, stream)
+    if r.__class__ is int:
+        _check("pa_evict_tokens", r)
     return r
 
 
