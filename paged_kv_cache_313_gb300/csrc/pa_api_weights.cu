@@ -52,16 +52,34 @@ long long most_partials(int num_seqs, int num_q_heads, int num_kv_heads, int hea
     return most;
 }
 
-// Workspace of pa_prefill_chunk_weights: the rows' lse, then the keys' partial sums.
+// pa_prefill_chunk_weights on the tensor cores cuts a chunk's query tiles into pieces, so that the items, (chunk, kv head,
+// piece, 256 keys), are about kItemsPerSm for each SM, of kPieceTiles 128-row tiles at least (fewer are mostly set-up).
+constexpr int kItemsPerSm = 8, kPieceTiles = 4, kItemKeys = 256;
+struct Pieces {
+    int count, tiles;
+};
+Pieces pieces_of(int num_chunks, int max_q_len, int group, int num_kv_heads, int max_context_len, int num_sms) {
+    const int per_tile = 128 / group;
+    const long long tiles = std::max(1, (max_q_len + per_tile - 1) / per_tile);
+    const long long items = std::max(1LL, (long long)num_chunks * num_kv_heads * ((max_context_len + kItemKeys - 1) / kItemKeys));
+    long long count = std::min(((long long)kItemsPerSm * num_sms + items - 1) / items, tiles / kPieceTiles);
+    count = std::max(1LL, count);
+    const long long each = (tiles + count - 1) / count;
+    return Pieces{(int)((tiles + each - 1) / each), (int)each};
+}
+
+// Workspace of pa_prefill_chunk_weights: the rows' lse, then the keys' partial sums: 256 of them an item, of which there are
+// never more than kItemsPerSm for each SM and one for each (chunk, kv head, 256 keys).
 struct PrefillWeightsWorkspace {
     size_t lse, partial, total;
 };
 PrefillWeightsWorkspace prefill_weights_layout(int num_chunks, int total_q, int num_q_heads, int num_kv_heads,
-                                               int max_context_len, int pieces) {
+                                               int max_context_len, int num_sms) {
     PrefillWeightsWorkspace w;
+    const size_t items = (size_t)num_chunks * num_kv_heads * (((size_t)max_context_len + kItemKeys - 1) / kItemKeys);
     w.lse = 0;
-    w.partial = round_up((size_t)total_q * num_q_heads * 4 + 1);  // (never empty)
-    w.total = w.partial + round_up((size_t)num_chunks * num_kv_heads * pieces * max_context_len * 4);
+    w.partial = round_up((size_t)total_q * num_q_heads * 4);
+    w.total = w.partial + (items + (size_t)kItemsPerSm * num_sms) * kItemKeys * 4;
     return w;
 }
 
@@ -120,6 +138,7 @@ int pa_rope_write_kv_paged(void* q_out, const void* q, const void* k_new, const 
     if (num_kv_heads < 1 || num_blocks < 0 || block_size < 1 || num_seqs < 0 || max_blocks_per_seq < 0 || key_width < 0 ||
         (key_weights == nullptr) != (key_pos == nullptr) || (key_weights != nullptr && key_width < 1))
         return PA_ERR_INVALID_ARG;
+    if (block_size > (1 << 30)) return PA_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PA_OK;
     if ((num_q_heads > 0 && (!q || !q_out)) || !k_new || !v_new || !k_cache || !v_cache || !seq_idx || !pos ||
         (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables) || (rot_dim > 0 && (!rope_pos || !inv_freq)))
@@ -242,7 +261,9 @@ size_t pa_prefill_weights_workspace_size(int num_chunks, int total_q, int max_q_
     if (num_chunks < 0 || total_q < 0 || max_q_len < 0 || max_context_len < 0 ||
         decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size))
         return 0;
-    return prefill_weights_layout(num_chunks, total_q, num_q_heads, num_kv_heads, max_context_len, 1).total;
+    int num_sms = 0;
+    if (check_device(&num_sms) != PA_OK) return 0;
+    return prefill_weights_layout(num_chunks, total_q, num_q_heads, num_kv_heads, max_context_len, num_sms).total;
 }
 
 int pa_prefill_chunk_weights(void* out, const void* q, const int32_t* cu_q_lens, const int32_t* q_start_pos,
@@ -289,17 +310,26 @@ int pa_prefill_chunk_weights(void* out, const void* q, const int32_t* cu_q_lens,
     p.max_context_len = max_context_len;
     p.scale_log2 = scale * 1.4426950408889634f;
     const PrefillWeightsWorkspace lay =
-        prefill_weights_layout(num_chunks, total_q, num_q_heads, num_kv_heads, max_context_len, 1);
+        prefill_weights_layout(num_chunks, total_q, num_q_heads, num_kv_heads, max_context_len, num_sms);
     if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return PA_ERR_WORKSPACE;
     char* ws = static_cast<char*>(workspace);
     p.lse = reinterpret_cast<float*>(ws + lay.lse);
     p.partial = reinterpret_cast<float*>(ws + lay.partial);
     p.partial_width = max_context_len;
-    p.pieces = 1;
     p.key_weights = key_weights;
     p.key_width = key_width;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    rc = launch_prefill_weights_fma(p, dtype, st);
+    const Pieces pieces = pieces_of(num_chunks, max_q_len, p.group, num_kv_heads, max_context_len, num_sms);
+    const long long items =
+        (long long)num_chunks * num_kv_heads * pieces.count * (((long long)max_context_len + kItemKeys - 1) / kItemKeys);
+    if (prefill_tc_supported(p, dtype) && items <= INT_MAX) {
+        rc = launch_prefill_tc(p, st);
+        p.pieces = pieces.count;
+        p.piece_positions = (int)std::min((long long)INT_MAX, (long long)pieces.tiles * (128 / p.group));
+        if (rc == PA_OK) rc = launch_prefill_weights_tc(p, pieces.tiles, num_sms, st);
+    } else {
+        rc = launch_prefill_weights_fma(p, dtype, st);
+    }
     return rc != PA_OK ? rc : launch_prefill_weights_add(p, st);
 }
 

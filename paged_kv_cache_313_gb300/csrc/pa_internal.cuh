@@ -186,6 +186,7 @@ struct PrefillParams {
     float* lse = nullptr;
     float* partial = nullptr;
     int pieces = 1, partial_width = 0;
+    int piece_positions = 0x7FFFFFFF;  // queries of a piece
     float* key_weights = nullptr;
     int key_width = 0;
 };
@@ -209,7 +210,7 @@ struct RopeParams {
     int key_width = 0;  // 0: no key state
     int64_t* slot_mapping = nullptr;
     int32_t* error_count = nullptr;
-    Divisor by_head;
+    Divisor by_head, by_block;
 };
 
 // pa_evict_tokens.
@@ -297,6 +298,7 @@ int run_decode(const DecodeParams& p, int dtype, int num_sms, cudaStream_t strea
 int launch_decode_weights(const DecodeParams& p, int dtype, cudaStream_t stream);
 // Prefill with lse, partial and key_weights set: the attention with its rows' lse, the keys' partial sums, their addition.
 int launch_prefill_weights_fma(const PrefillParams& p, int dtype, cudaStream_t stream);
+int launch_prefill_weights_tc(const PrefillParams& p, int piece_tiles, int num_sms, cudaStream_t stream);
 int launch_prefill_weights_add(const PrefillParams& p, cudaStream_t stream);
 int launch_rope(const RopeParams& p, int dtype, cudaStream_t stream);
 int launch_evict(const EvictParams& p, int row_bytes, cudaStream_t stream);

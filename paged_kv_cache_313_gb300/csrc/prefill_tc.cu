@@ -120,6 +120,9 @@ struct Bars {
     __device__ uint64_t* mma_drain() const { return base + 9 + 2 * kKStages + 2 * kVStages + kMaskSlots; }
 };
 
+// kLse: pa_prefill_chunk_weights, which also leaves each row's log2 softmax sum.  The sums then are of 32-bit exponentials
+// (the pairs' rounding would go into every weight), and groups that do not divide 128 leave a tile's last rows unused.
+template <bool kLse>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                       const __grid_constant__ CUtensorMap tmv, const PrefillParams p) {
@@ -165,7 +168,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (rank >= ntiles_q) return false;
         d.i0 = (ntiles_q - 1 - rank) * pos_per_tile;
         d.nq = min(pos_per_tile, n - d.i0);
-        const int cap = min(p.context_lens[d.s], p.max_blocks_per_seq * B);
+        const int cap = min(min(p.context_lens[d.s], p.max_blocks_per_seq * B), kLse ? p.max_context_len : 0x7FFFFFFF);
         // the tile's last query position; a cascade prefix pass reads keys [0, start) for every row
         d.last_key = prefix_mode ? d.start - 1 : d.start + d.i0 + d.nq - 1;
         if (d.last_key >= cap) {
@@ -250,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     break;
                 }
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(bars.q_full(), 2 * kHalf);
+                    mbar_arrive_expect_tx(bars.q_full(), kLse ? 2 * pos_per_tile * G * 128 : 2 * kHalf);
                     for (int h = 0; h < 2; ++h)
                         tma_load_3d(smem + kQ + h * kHalf, &tmq, h * 64, kvh * G, d.r0 + d.i0, bars.q_full());
                 }
@@ -520,7 +523,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 {
                     uint32_t pk[32];
                     float ls4[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (PA_PREFILL_EXP2_PAIRS && dense) {
+                    if (kLse && dense) {
+                        const unsigned long long s2 = f32x2_pack(sl2, sl2), m2 = f32x2_pack(neg_m, neg_m);
+                        unsigned long long acc2[2] = {f32x2_pack(0.f, 0.f), f32x2_pack(0.f, 0.f)};
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            float y0, y1;
+                            f32x2_unpack(fma_f32x2(f32x2_pack(sv[2 * i], sv[2 * i + 1]), s2, m2), y0, y1);
+                            y0 = fast_exp2(y0);
+                            y1 = fast_exp2(y1);
+                            pk[i] = pack_bf16x2(y0, y1);
+                            acc2[i & 1] = add_f32x2(acc2[i & 1], f32x2_pack(y0, y1));
+                        }
+                        f32x2_unpack(acc2[0], ls4[0], ls4[1]);
+                        f32x2_unpack(acc2[1], ls4[2], ls4[3]);
+                    } else if (PA_PREFILL_EXP2_PAIRS && dense) {
                         // two keys per instruction throughout: x - m by a paired FMA, rounded to a bf16
                         // pair, 2^x of the pair (which is P itself), and the sum of the same bf16 values
                         // by a paired add
@@ -549,7 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
 #pragma unroll
                             for (int k = 0; k < 64; ++k)
-                                sv[k] = (sv[k] == -INFINITY || m_run == -INFINITY) ? 0.f : fast_exp2(sv[k] + neg_m);
+                                // (kLse: a row of NaN, whose maximum stays -inf, keeps them)
+                                sv[k] = (sv[k] == -INFINITY || (!kLse && m_run == -INFINITY)) ? 0.f
+                                                                                               : fast_exp2(sv[k] + neg_m);
                         }
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
@@ -608,6 +627,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f_b = m_b == -INFINITY ? 0.f : fast_exp2(m_b - m_row);
             const float l_row = f_a * l_a + f_b * l_b;
             const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
+            if (kLse && half == 0 && row_ok)
+                p.lse[((size_t)kvh * p.total_q + r0 + pos) * G + r % G] = l_row == 0.f ? INFINITY : m_row + log2f(l_row);
             const float wa = f_a * inv, wb = f_b * inv;  // weights of O_a and O_b in this row's output
             // member sequence r0 + pos, head r % G of a cascade prefix pass: its partial (o, m, l) goes to
             // workspace slot 0; a member whose own prefix length differs from the group's gets an empty one
@@ -683,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 bool prefill_tc_supported(const PrefillParams& p, int dtype) {
     const int G = p.group, B = p.block_size;
     if (dtype != PA_BF16 || p.head_dim != kD) return false;
-    if (G != 1 && G != 2 && G != 4 && G != 8) return false;
+    if (p.lse == nullptr && G != 1 && G != 2 && G != 4 && G != 8) return false;
     if (B != 8 && B != 16 && B != 32 && B != 64 && B != 128) return false;
     if (((uintptr_t)p.q & 15) || ((uintptr_t)p.k_cache & 15) || ((uintptr_t)p.v_cache & 15) ||
         ((uintptr_t)p.out & 15))
@@ -692,7 +713,8 @@ bool prefill_tc_supported(const PrefillParams& p, int dtype) {
     return p.num_chunks <= 65535 && p.num_kv_heads <= 65535;
 }
 
-int launch_prefill_tc(const PrefillParams& p, cudaStream_t stream) {
+template <bool kLse>
+static int launch(const PrefillParams& p, cudaStream_t stream) {
     CUtensorMap tmq, tmk, tmv;
     {
         auto enc = tensor_map_encoder();
@@ -711,7 +733,7 @@ int launch_prefill_tc(const PrefillParams& p, cudaStream_t stream) {
     int rc = pool_tensor_map(&tmk, p.k_cache, p.num_blocks, p.block_size, p.num_kv_heads, kD);
     if (rc != PA_OK) return rc;
     if ((rc = pool_tensor_map(&tmv, p.v_cache, p.num_blocks, p.block_size, p.num_kv_heads, kD)) != PA_OK) return rc;
-    if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(prefill_tc_kernel), kSmemBytes)) != PA_OK) return rc;
+    if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(prefill_tc_kernel<kLse>), kSmemBytes)) != PA_OK) return rc;
     // persistent: one CTA per SM (or per work item, if fewer), each walking its share of the items
     const int pos_per_tile = kTileQ / p.group;
     const long long items = (long long)((p.max_q_len + pos_per_tile - 1) / pos_per_tile) * p.num_chunks *
@@ -722,7 +744,11 @@ int launch_prefill_tc(const PrefillParams& p, cudaStream_t stream) {
                                                   cudaSuccess)
         return check_launch();
     const int grid = (int)(items < num_sms ? items : num_sms);
-    return launch_kernel(prefill_tc_kernel, dim3(grid), dim3(kThreads), kSmemBytes, stream, tmq, tmk, tmv, p);
+    return launch_kernel(prefill_tc_kernel<kLse>, dim3(grid), dim3(kThreads), kSmemBytes, stream, tmq, tmk, tmv, p);
+}
+
+int launch_prefill_tc(const PrefillParams& p, cudaStream_t stream) {
+    return p.lse ? launch<true>(p, stream) : launch<false>(p, stream);
 }
 
 }  // namespace pa

@@ -305,7 +305,10 @@ __global__ void __launch_bounds__(kAddThreads) add_kernel(const PrefillParams p)
             if (!later[k] || !weight_chunk(p, e0 + k, o) || j >= o.nkeys) continue;
             any = true;
             const float* part = p.partial + ((size_t)(e0 + k) * p.num_kv_heads + kvh) * p.pieces * p.partial_width + j;
-            for (int i = 0; i < p.pieces; ++i) sum += part[(size_t)i * p.partial_width];
+            for (int i = 0; i < p.pieces; ++i) {  // the pieces that have a query which sees key j
+                const long long begin = (long long)i * p.piece_positions, end = min(begin + p.piece_positions, (long long)o.n);
+                if (begin < end && o.start + end > j) sum += part[(size_t)i * p.partial_width];
+            }
         }
     }
     if (any) p.key_weights[((size_t)d.s * p.num_kv_heads + kvh) * p.key_width + j] += sum;

@@ -57,76 +57,42 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
     const int per_head = half / VEC + (D - p.rot_dim) / VEC;  // pair items, then pass-through items
     const int items = (p.num_q_heads + p.num_kv_heads) * per_head + (kWrite ? p.num_kv_heads * (D / VEC) : 0);
 
-    int s = 0, at = 0;
-    long long slot = t;  // the row of K and V that is written, -1 for none
-    if (kWrite) {
-        at = p.pos[t];
-        if (at < 0) {  // padding: nothing of the token is written
-            if (threadIdx.x == 0 && p.slot_mapping) p.slot_mapping[t] = -1;
-            return;
-        }
-        s = p.seq_idx[t];
-        slot = -1;
-        const int block = at / p.block_size;
-        if (s >= 0 && s < p.num_seqs && block < p.max_blocks_per_seq && (!p.key_width || at < p.key_width)) {
-            const int physical = p.block_tables[(long long)s * p.max_blocks_per_seq + block];
-            if (physical >= 0 && physical < p.num_blocks)
-                slot = (long long)physical * p.block_size + (at - block * p.block_size);
-        }
-        if (threadIdx.x == 0) {
-            if (slot < 0) count_error(p.error_count);
-            if (p.slot_mapping) p.slot_mapping[t] = slot;
-        }
-    }
-
-    // where item i of the token reads and writes; pairs: b is the partner's chunk
+    // Item i of the token: a chunk and, where it is turned, its partner's chunk, `b` chunks further on (0: copied); the first
+    // of its pairs; its element's offset within a row of q (row 0), k (1) or v (2).
     struct Item {
-        const C* src;
-        C* dst;
-        int b, pair;  // distance to the partner's chunk in chunks (0: copied), first pair
+        int row, offset, b, pair;
     };
     auto item_of = [&](int i) {
-        Item it;
+        Item it{};
         const int rotated = (p.num_q_heads + p.num_kv_heads) * per_head;
-        const T *src;
-        T* dst;
-        if (kWrite && i >= rotated) {  // V
-            const int e = (i - rotated) * VEC;
-            src = static_cast<const T*>(p.v) + t * p.v_stride + e;
-            dst = slot < 0 ? nullptr : static_cast<T*>(p.v_out) + slot * p.num_kv_heads * D + e;
-            it.b = 0;
+        if (kWrite && i >= rotated) {
+            it.row = 2;
+            it.offset = (i - rotated) * VEC;
         } else {
             const int h = p.by_head.div(i), c = i - h * per_head;
-            int e;
+            it.row = h >= p.num_q_heads;
+            it.offset = (h - (it.row ? p.num_q_heads : 0)) * D;
             if (c < half / VEC) {
-                e = p.interleaved ? 2 * c * VEC : c * VEC;
+                it.offset += p.interleaved ? 2 * c * VEC : c * VEC;
                 it.b = p.interleaved ? 1 : half / VEC;
                 it.pair = c * VEC;
             } else {
-                e = p.rot_dim + (c - half / VEC) * VEC;
-                it.b = 0;
-            }
-            if (h < p.num_q_heads) {
-                src = static_cast<const T*>(p.q) + t * p.q_stride + (long long)h * D + e;
-                dst = static_cast<T*>(p.q_out) + (t * p.num_q_heads + h) * D + e;
-            } else {
-                const int kh = h - p.num_q_heads;
-                src = static_cast<const T*>(p.k) + t * p.k_stride + (long long)kh * D + e;
-                dst = slot < 0 ? nullptr : static_cast<T*>(p.k_out) + (slot * p.num_kv_heads + kh) * D + e;
+                it.offset += p.rot_dim + (c - half / VEC) * VEC;
             }
         }
-        it.src = reinterpret_cast<const C*>(src);
-        it.dst = reinterpret_cast<C*>(dst);
         return it;
     };
     Item it[kAhead];
     C a[kAhead], b[kAhead];
     auto load = [&](int k, int i) {
         it[k] = item_of(i);
-        a[k] = *it[k].src;
-        if (it[k].b) b[k] = it[k].src[it[k].b];
+        const void* base = it[k].row == 0 ? p.q : it[k].row == 1 ? p.k : p.v;
+        const long long stride = it[k].row == 0 ? p.q_stride : it[k].row == 1 ? p.k_stride : p.v_stride;
+        const C* src = reinterpret_cast<const C*>(static_cast<const T*>(base) + t * stride + it[k].offset);
+        a[k] = *src;
+        if (it[k].b) b[k] = src[it[k].b];
     };
-    auto store = [&](int k) {
+    auto store = [&](int k, long long slot) {
         if (it[k].b) {
             T* x = reinterpret_cast<T*>(&a[k]);
             T* y = reinterpret_cast<T*>(&b[k]);
@@ -151,27 +117,59 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
                 for (int i = 0; i < VEC; ++i) pair(x[i], y[i], i);
             }
         }
-        if (it[k].dst) {
-            *it[k].dst = a[k];
-            if (it[k].b) it[k].dst[it[k].b] = b[k];
-        }
+        if (it[k].row && slot < 0) return;
+        void* base = it[k].row == 0 ? p.q_out : it[k].row == 1 ? p.k_out : p.v_out;
+        const long long row = it[k].row == 0 ? t * p.num_q_heads : slot * p.num_kv_heads;
+        C* dst = reinterpret_cast<C*>(static_cast<T*>(base) + row * D + it[k].offset);
+        *dst = a[k];
+        if (it[k].b) dst[it[k].b] = b[k];
     };
 
+    // the rows' loads first: nothing that they wait for is behind the look-ups below
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
         if ((int)threadIdx.x + k * kThreads < items) load(k, threadIdx.x + k * kThreads);
+    // then what the look-ups begin with, all at once: index and sequence, and this thread's first pair
+    int s = 0, at = 0;
+    if (kWrite) {
+        at = p.pos[t];
+        s = p.seq_idx[t];
+    }
+    auto axis_of = [&](int i) { return i < half && p.axis ? p.axis[i] : 0; };
+    auto freq_of = [&](int i) { return i < half ? p.inv_freq[i] : 0.f; };
+    int axis = axis_of(threadIdx.x);
+    float freq = freq_of(threadIdx.x);
+    long long slot = t;  // the row of K and V that is written, -1 for none
+    if (kWrite) {
+        slot = -1;
+        const int block = p.by_block.div(max(at, 0) & 0x3FFFFFFF);
+        if (at >= 0 && at < (1 << 30) && s >= 0 && s < p.num_seqs && block < p.max_blocks_per_seq &&
+            (!p.key_width || at < p.key_width)) {
+            const int physical = p.block_tables[(long long)s * p.max_blocks_per_seq + block];
+            if (physical >= 0 && physical < p.num_blocks)
+                slot = (long long)physical * p.block_size + (at - block * p.block_size);
+        }
+    }
     for (int i = threadIdx.x; i < half; i += kThreads) {
-        int axis = p.axis ? p.axis[i] : 0;
         const bool known = axis >= 0 && axis < p.num_axes;
+        const int where = known ? p.rope_pos[(long long)axis * p.num_tokens + t] : 0;
         if (!known) count_error(p.error_count);
         bool finite;
-        const uint64_t per = turns_of(p.inv_freq[i], &finite);
-        const int where = known ? p.rope_pos[(long long)axis * p.num_tokens + t] : 0;
+        const uint64_t per = turns_of(freq, &finite);
         const int32_t turns = (int32_t)((per * (uint64_t)(int64_t)where) >> 32);  // fraction of a turn, 2^-32
         float2 cs;
         sincospif((float)turns * 0x1p-31f, &cs.y, &cs.x);
         if (!finite) cs = make_float2(NAN, NAN);
         turn[i] = cs;
+        axis = axis_of(i + kThreads);
+        freq = freq_of(i + kThreads);
+    }
+    if (kWrite) {
+        if (threadIdx.x == 0) {
+            if (at >= 0 && slot < 0) count_error(p.error_count);
+            if (p.slot_mapping) p.slot_mapping[t] = slot;
+        }
+        if (at < 0) return;  // padding: nothing of the token is written
     }
     if (kWrite && p.key_width && slot >= 0)
         for (int h = threadIdx.x; h < p.num_kv_heads; h += kThreads) {
@@ -182,10 +180,10 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const RopeParams p) {
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < kAhead; ++k)
-        if ((int)threadIdx.x + k * kThreads < items) store(k);
+        if ((int)threadIdx.x + k * kThreads < items) store(k, slot);
     for (int i = threadIdx.x + kAhead * kThreads; i < items; i += kThreads) {
         load(0, i);
-        store(0);
+        store(0, slot);
     }
 }
 
@@ -193,6 +191,7 @@ template <typename T, int VEC>
 int launch(const RopeParams& p, cudaStream_t stream) {
     const int half = p.rot_dim / 2;
     RopeParams r = p;
+    r.by_block = Divisor((uint32_t)p.block_size);
     r.by_head = Divisor((uint32_t)(half / VEC + (p.head_dim - p.rot_dim) / VEC));
     const size_t smem = sizeof(float2) * half;
     return p.block_tables || p.pos
