@@ -52,34 +52,19 @@ long long most_partials(int num_seqs, int num_q_heads, int num_kv_heads, int hea
     return most;
 }
 
-// pa_prefill_chunk_weights on the tensor cores cuts a chunk's query tiles into pieces, so that the items, (chunk, kv head,
-// piece, 256 keys), are about kItemsPerSm for each SM, of kPieceTiles 128-row tiles at least (fewer are mostly set-up).
-constexpr int kItemsPerSm = 8, kPieceTiles = 4, kItemKeys = 256;
-struct Pieces {
-    int count, tiles;
-};
-Pieces pieces_of(int num_chunks, int max_q_len, int group, int num_kv_heads, int max_context_len, int num_sms) {
-    const int per_tile = 128 / group;
-    const long long tiles = std::max(1, (max_q_len + per_tile - 1) / per_tile);
-    const long long items = std::max(1LL, (long long)num_chunks * num_kv_heads * ((max_context_len + kItemKeys - 1) / kItemKeys));
-    long long count = std::min(((long long)kItemsPerSm * num_sms + items - 1) / items, tiles / kPieceTiles);
-    count = std::max(1LL, count);
-    const long long each = (tiles + count - 1) / count;
-    return Pieces{(int)((tiles + each - 1) / each), (int)each};
-}
-
-// Workspace of pa_prefill_chunk_weights: the rows' lse, then the keys' partial sums: 256 of them an item, of which there are
-// never more than kItemsPerSm for each SM and one for each (chunk, kv head, 256 keys).
+// Workspace of pa_prefill_chunk_weights: the rows' lse, what comes before each chunk, then the keys' partial sums: rows of 256
+// keys, one for each (chunk, kv head, 256 keys) and one more for each SM, in kKeyParts parts.
 struct PrefillWeightsWorkspace {
-    size_t lse, partial, total;
+    size_t lse, runs, partial, total;
 };
 PrefillWeightsWorkspace prefill_weights_layout(int num_chunks, int total_q, int num_q_heads, int num_kv_heads,
                                                int max_context_len, int num_sms) {
     PrefillWeightsWorkspace w;
-    const size_t items = (size_t)num_chunks * num_kv_heads * (((size_t)max_context_len + kItemKeys - 1) / kItemKeys);
+    const size_t rows = (size_t)num_chunks * num_kv_heads * (((size_t)max_context_len + 255) / 256) + num_sms;
     w.lse = 0;
-    w.partial = round_up((size_t)total_q * num_q_heads * 4);
-    w.total = w.partial + (items + (size_t)kItemsPerSm * num_sms) * kItemKeys * 4;
+    w.runs = round_up((size_t)total_q * num_q_heads * 4);
+    w.partial = w.runs + round_up(((size_t)num_chunks + 1) * sizeof(KeyRuns));
+    w.total = w.partial + rows * 256 * kKeyParts * 4;
     return w;
 }
 
@@ -315,18 +300,14 @@ int pa_prefill_chunk_weights(void* out, const void* q, const int32_t* cu_q_lens,
     char* ws = static_cast<char*>(workspace);
     p.lse = reinterpret_cast<float*>(ws + lay.lse);
     p.partial = reinterpret_cast<float*>(ws + lay.partial);
-    p.partial_width = max_context_len;
     p.key_weights = key_weights;
     p.key_width = key_width;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const Pieces pieces = pieces_of(num_chunks, max_q_len, p.group, num_kv_heads, max_context_len, num_sms);
-    const long long items =
-        (long long)num_chunks * num_kv_heads * pieces.count * (((long long)max_context_len + kItemKeys - 1) / kItemKeys);
-    if (prefill_tc_supported(p, dtype) && items <= INT_MAX) {
+    // (the second kernel keeps 8 bytes for each chunk in its 128 KB of key buffers at first)
+    if (prefill_tc_supported(p, dtype) && num_chunks <= 16384 && max_context_len > 0) {
+        p.runs = reinterpret_cast<KeyRuns*>(ws + lay.runs);
         rc = launch_prefill_tc(p, st);
-        p.pieces = pieces.count;
-        p.piece_positions = (int)std::min((long long)INT_MAX, (long long)pieces.tiles * (128 / p.group));
-        if (rc == PA_OK) rc = launch_prefill_weights_tc(p, pieces.tiles, num_sms, st);
+        if (rc == PA_OK) rc = launch_prefill_weights_tc(p, num_sms, st);
     } else {
         rc = launch_prefill_weights_fma(p, dtype, st);
     }

@@ -149,6 +149,13 @@ struct DecodeParams {
     int key_width = 0;
 };
 
+// What comes before a chunk in prefill_weights_tc.cu's order; entry num_chunks holds the units of a CTA.
+struct KeyRuns {
+    unsigned long long units;
+    int runs;
+};
+constexpr int kKeyParts = 2;  // rows of partial that a part of a run's sums are in, one for each warp that adds some of them
+
 struct PrefillParams {
     void* out;
     const void* q;
@@ -181,12 +188,12 @@ struct PrefillParams {
     int max_context_len = 0x7FFFFFFF;  // keys at or beyond it are not read (block-scaled pools, key weights)
     // pa_prefill_chunk_weights: the attention kernel leaves each row's log2 of its softmax sum in base-2 units, m + log2(l),
     // in lse, float [num_kv_heads][total_q * G] (+inf for a row without a key, whose weights are then all zero); a second
-    // kernel leaves each key's summed weights in partial, float [num_chunks][num_kv_heads][pieces][partial_width], and a
-    // third adds those to key_weights, float [num_seqs][num_kv_heads][key_width], in a fixed order.
+    // kernel leaves each key's summed weights in partial, and a third adds those to key_weights, float
+    // [num_seqs][num_kv_heads][key_width], in a fixed order.  partial is float [num_chunks][num_kv_heads][max_context_len]
+    // from the CUDA cores, and rows of 256 keys from the tensor cores (runs set): see prefill_weights_tc.cu.
     float* lse = nullptr;
     float* partial = nullptr;
-    int pieces = 1, partial_width = 0;
-    int piece_positions = 0x7FFFFFFF;  // queries of a piece
+    KeyRuns* runs = nullptr;
     float* key_weights = nullptr;
     int key_width = 0;
 };
@@ -298,7 +305,7 @@ int run_decode(const DecodeParams& p, int dtype, int num_sms, cudaStream_t strea
 int launch_decode_weights(const DecodeParams& p, int dtype, cudaStream_t stream);
 // Prefill with lse, partial and key_weights set: the attention with its rows' lse, the keys' partial sums, their addition.
 int launch_prefill_weights_fma(const PrefillParams& p, int dtype, cudaStream_t stream);
-int launch_prefill_weights_tc(const PrefillParams& p, int piece_tiles, int num_sms, cudaStream_t stream);
+int launch_prefill_weights_tc(const PrefillParams& p, int num_sms, cudaStream_t stream);
 int launch_prefill_weights_add(const PrefillParams& p, cudaStream_t stream);
 int launch_rope(const RopeParams& p, int dtype, cudaStream_t stream);
 int launch_evict(const EvictParams& p, int row_bytes, cudaStream_t stream);

@@ -27,4 +27,22 @@ __device__ __forceinline__ bool weight_chunk(const PrefillParams& p, int c, Weig
     return true;
 }
 
+// The tensor-core path (prefill_weights_tc.cu): pairs of 128-key tiles, tiles of 128 query rows (128 / G positions).
+constexpr int kKeys = 256;
+__device__ __forceinline__ int key_pairs(const WeightChunk& d) { return (d.nkeys + kKeys - 1) / kKeys; }
+__device__ __forceinline__ int key_tiles(const WeightChunk& d, int per_tile) { return (d.n + per_tile - 1) / per_tile; }
+// The first query tile that sees a key of the pair (there is one: its first key is below nkeys).
+__device__ __forceinline__ int key_first_tile(const WeightChunk& d, int pair, int per_tile) {
+    return max(0, pair * kKeys - d.start) / per_tile;
+}
+// (pair, query tile) units of one kv head, those of pairs below `pairs`.
+__device__ __forceinline__ long long key_units(const WeightChunk& d, int per_tile, int pairs) {
+    long long units = (long long)pairs * key_tiles(d, per_tile);
+    for (int pair = d.start / kKeys + 1; pair < pairs; ++pair) units -= key_first_tile(d, pair, per_tile);
+    return units;
+}
+__device__ __forceinline__ long long key_units(const WeightChunk& d, int per_tile) {
+    return key_units(d, per_tile, key_pairs(d));
+}
+
 }  // namespace pa

@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kThreads) column_kernel(const PrefillParams p)
     if ((int)threadIdx.x < kTile && j0 + (int)threadIdx.x < d.nkeys) {
         float total = 0.f;
         for (int i = 0; i < 16; ++i) total += sums[i * kTile + threadIdx.x];
-        p.partial[((size_t)c * p.num_kv_heads + kvh) * p.partial_width + j0 + threadIdx.x] = total;
+        p.partial[((size_t)c * p.num_kv_heads + kvh) * p.max_context_len + j0 + threadIdx.x] = total;
     }
 }
 
@@ -304,11 +304,22 @@ __global__ void __launch_bounds__(kAddThreads) add_kernel(const PrefillParams p)
             WeightChunk o;
             if (!later[k] || !weight_chunk(p, e0 + k, o) || j >= o.nkeys) continue;
             any = true;
-            const float* part = p.partial + ((size_t)(e0 + k) * p.num_kv_heads + kvh) * p.pieces * p.partial_width + j;
-            for (int i = 0; i < p.pieces; ++i) {  // the pieces that have a query which sees key j
-                const long long begin = (long long)i * p.piece_positions, end = min(begin + p.piece_positions, (long long)o.n);
-                if (begin < end && o.start + end > j) sum += part[(size_t)i * p.partial_width];
+            if (!p.runs) {
+                sum += p.partial[((size_t)(e0 + k) * p.num_kv_heads + kvh) * p.max_context_len + j];
+                continue;
             }
+            // the run of key j's pair: its units, and the CTAs that took them
+            const int per_tile = 128 / p.group, pair = j / kKeys;
+            const unsigned long long per = p.runs[p.num_chunks].units;
+            const KeyRuns at = p.runs[e0 + k];
+            const unsigned long long first =
+                at.units + (unsigned long long)kvh * key_units(o, per_tile) + key_units(o, per_tile, pair);
+            const unsigned long long last =
+                first + key_tiles(o, per_tile) - key_first_tile(o, pair, per_tile) - 1;
+            const int run = at.runs + kvh * key_pairs(o) + pair;
+            for (unsigned long long b = first / per; b <= last / per; ++b)
+                for (int h = 0; h < kKeyParts; ++h)
+                    sum += p.partial[((size_t)(run + b) * kKeyParts + h) * kKeys + j % kKeys];
         }
     }
     if (any) p.key_weights[((size_t)d.s * p.num_kv_heads + kvh) * p.key_width + j] += sum;

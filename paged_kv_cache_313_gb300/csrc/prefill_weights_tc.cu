@@ -8,18 +8,24 @@
 // nothing crosses threads.  Bound by the tensor cores (half the attention's
 // products) and the exponentials alike.
 //
-// A work item is (chunk, kv head, piece of the chunk's query tiles, pair of
-// 128-key tiles).  Its 256 keys stay in shared memory while the piece's 128-row
-// query tiles (positions times the G heads of the kv head) stream through a
-// ring, so that a query tile's 32 KB feed two products.  The kernel is
-// persistent, one CTA per SM; the next item's keys are loaded into the other of
-// two buffers meanwhile.
+// A run is a pair of 128-key tiles of one (chunk, kv head) against the 128-row query
+// tiles (positions times the G heads of the kv head) that see a key of it, in order.
+// The 256 keys stay in shared memory while the query tiles stream through a ring, so
+// that a query tile's 32 KB feed two products.  The kernel is persistent, one CTA per
+// SM: all runs in order, (chunk, kv head, pair), are one sequence of (pair, query tile)
+// units, and CTA b takes units [b per, (b + 1) per) of it, wherever they begin and end.
+// Each part of a run leaves a row of 256 sums: run number + CTA number is a row of its
+// own.  The next run's keys are loaded into the other of two buffers meanwhile.
 //
 // Warp roles (352 threads):
 //   warp 0     producer: key tiles (one TMA box per block and 64-column half) and
 //              query tiles (one box per half)
 //   warp 1     owner of the tensor memory and issuer of the products
-//   warps 2-9  the sums: four warps for each of the two key tiles, a thread a key
+//   warps 2-9  the sums, in two groups of four that take the query tiles in turns, so
+//              that one exponentiates while the other waits for its scores; a thread
+//              takes one key of either key tile, so that an lse read from shared
+//              memory, whose bandwidth the products' operands take up, serves two
+//              scores
 //   warp 10    the query tiles' lse, to shared memory
 // Every wait is bounded, tensor memory is always freed, and copies and products
 // in flight are waited for before a CTA exits, as in prefill_tc.cu.
@@ -31,21 +37,32 @@ namespace {
 
 constexpr int kTile = 128;
 constexpr int kD = 128;
-constexpr int kKeys = 2 * kTile;           // keys of an item
+static_assert(kKeys == 2 * kTile, "keys of a run");
+constexpr int kMinUnits = 2;
 constexpr int kHalf = 128 * 128;           // bytes of a 64-column half of a 128-row tile
 constexpr int kTileBytes = 2 * kHalf;
-constexpr int kThreads = 352;
-constexpr int kLseWarp = 10;
+constexpr int kSumWarps = 4;  // of a group
+constexpr int kThreads = (2 * kSumWarps + 3) * 32;
+constexpr int kLseWarp = 2 * kSumWarps + 2;
 constexpr uint32_t kTmemCols = 512;        // two buffers of two key tiles' scores
 constexpr int kQStages = 3;
 constexpr int kK = 0;                      // [2 buffers][2 tiles]
 constexpr int kQ = kK + 4 * kTileBytes;
 constexpr int kLse = kQ + kQStages * kTileBytes;  // float [kQStages][128]
 constexpr int kBars = kLse + kQStages * kTile * 4;
-// k_full[2], k_empty[2], q_full[3], q_empty[3], l_full[3], l_empty[3], s_full[2][2], s_empty[2][2], drain
-constexpr int kNumBars = 4 + 4 * kQStages + 8 + 1;
+// k_full[2], k_empty[2], q_full[3], q_empty[3], l_full[3], l_empty[3], s_full[2], s_empty[2], d_empty[2], drain
+constexpr int kNumBars = 4 + 4 * kQStages + 6 + 1;
 constexpr int kTmemSlot = kBars + kNumBars * 8;
-constexpr size_t kSmemBytes = 1024 + kTmemSlot + 16;
+constexpr int kStart = (kTmemSlot + 4 + 7) / 8 * 8;
+struct Start {  // where a CTA's units begin
+    int c, kvh, pair, tile;
+    long long units;
+};
+struct Run {  // as the producer describes it to the other warps; nt == 0: no more
+    int s, kvh, r0, n, start, nkeys, j0, t0, nt, row;
+};
+constexpr int kRuns = kStart + sizeof(Start);  // Run [2]
+constexpr size_t kSmemBytes = 1024 + kRuns + 2 * sizeof(Run);
 static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
 
 struct Bars {
@@ -56,61 +73,39 @@ struct Bars {
     __device__ uint64_t* q_empty(int i) const { return base + 4 + kQStages + i; }
     __device__ uint64_t* l_full(int i) const { return base + 4 + 2 * kQStages + i; }
     __device__ uint64_t* l_empty(int i) const { return base + 4 + 3 * kQStages + i; }
-    __device__ uint64_t* s_full(int b, int t) const { return base + 4 + 4 * kQStages + 2 * b + t; }
-    __device__ uint64_t* s_empty(int b, int t) const { return base + 8 + 4 * kQStages + 2 * b + t; }
-    __device__ uint64_t* drain() const { return base + 12 + 4 * kQStages; }
+    __device__ uint64_t* s_full(int i) const { return base + 4 + 4 * kQStages + i; }
+    __device__ uint64_t* s_empty(int i) const { return base + 6 + 4 * kQStages + i; }
+    __device__ uint64_t* d_empty(int i) const { return base + 8 + 4 * kQStages + i; }
+    __device__ uint64_t* drain() const { return base + 10 + 4 * kQStages; }
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
     key_weights_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                       const PrefillParams p, const int piece_tiles) {
+                       const PrefillParams p) {
     pdl_trigger();
     pdl_wait();
     const int G = p.group, B = p.block_size, Hkv = p.num_kv_heads;
     const int per_tile = kTile / G;  // positions of a query tile
-    const int pairs_max = (p.max_context_len + kKeys - 1) / kKeys;
-    const int num_items = p.num_chunks * Hkv * p.pieces * pairs_max;
-
-    struct Item {
-        WeightChunk d;
-        int c, kvh, piece, j0, t0, nt;  // first key, first query tile, query tiles
-    };
-    // item k: neighbours differ in the keys and share the queries; false for one without a key that a query of it sees
-    auto describe = [&](int k, Item& it) {
-        const int pair = k % pairs_max;
-        k /= pairs_max;
-        it.piece = k % p.pieces;
-        k /= p.pieces;
-        it.kvh = k % Hkv;
-        it.c = k / Hkv;
-        if (!weight_chunk(p, it.c, it.d)) return false;
-        it.j0 = pair * kKeys;
-        if (it.j0 >= it.d.nkeys) return false;
-        const int tiles = (it.d.n + per_tile - 1) / per_tile;
-        it.t0 = max(it.piece * piece_tiles, max(0, it.j0 - it.d.start) / per_tile);
-        it.nt = min(tiles, (it.piece + 1) * piece_tiles) - it.t0;
-        return it.nt > 0;
-    };
-
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const Bars bars{reinterpret_cast<uint64_t*>(smem + kBars)};
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kTmemSlot);
+    Start* start = reinterpret_cast<Start*>(smem + kStart);
+    Run* runs = reinterpret_cast<Run*>(smem + kRuns);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars.k_full(i), 1);
             mbar_init(bars.k_empty(i), 1);
-            for (int t = 0; t < 2; ++t) {
-                mbar_init(bars.s_full(i, t), 1);
-                mbar_init(bars.s_empty(i, t), 4);
-            }
+            mbar_init(bars.s_full(i), 2);  // the products' commit, and the issuer, which has seen the lse
+            mbar_init(bars.s_empty(i), kSumWarps);
+            mbar_init(bars.d_empty(i), 2 * kSumWarps + 2);
         }
         for (int i = 0; i < kQStages; ++i) {
             mbar_init(bars.q_full(i), 1);
             mbar_init(bars.q_empty(i), 1);
             mbar_init(bars.l_full(i), 1);
-            mbar_init(bars.l_empty(i), 8);
+            mbar_init(bars.l_empty(i), kSumWarps);
         }
         mbar_init(bars.drain(), 1);
         fence_mbar_init();
@@ -123,12 +118,90 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // ---- this CTA's units.  The chunks' units, then the sums before each chunk, in the key buffers (not yet in use); CTA 0
+    // leaves what the addition needs to find a key's rows.
+    unsigned long long* before = reinterpret_cast<unsigned long long*>(smem + kK);
+    for (int c = threadIdx.x; c < p.num_chunks; c += kThreads) {
+        WeightChunk d;
+        before[c] = weight_chunk(p, c, d) ? (unsigned long long)key_units(d, per_tile) * Hkv : 0ull;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        unsigned long long units = 0;
+        int runs = 0;
+        const int n32 = (p.num_chunks + 31) / 32 * 32;
+        for (int c = lane; c < n32; c += 32) {
+            WeightChunk d;
+            const bool have = c < p.num_chunks && weight_chunk(p, c, d);
+            unsigned long long u = have ? before[c] : 0ull;
+            int r = have ? key_pairs(d) * Hkv : 0;
+            const unsigned long long mine = u;
+            const int mine_r = r;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const unsigned long long v = __shfl_up_sync(0xffffffffu, u, off);
+                const int w = __shfl_up_sync(0xffffffffu, r, off);
+                if (lane >= off) {
+                    u += v;
+                    r += w;
+                }
+            }
+            if (c < p.num_chunks) {
+                before[c] = units + u - mine;
+                if (blockIdx.x == 0) p.runs[c] = KeyRuns{units + u - mine, runs + r - mine_r};
+            }
+            units += __shfl_sync(0xffffffffu, u, 31);
+            runs += __shfl_sync(0xffffffffu, r, 31);
+        }
+        const unsigned long long per = max((units + gridDim.x - 1) / gridDim.x, (unsigned long long)kMinUnits);
+        if (blockIdx.x == 0 && lane == 0) p.runs[p.num_chunks] = KeyRuns{per, 0};
+        __syncwarp();
+        const unsigned long long first = blockIdx.x * per;
+        if (lane == 0) {
+            *start = Start{0, 0, 0, 0, first < units ? (long long)min(per, units - first) : 0LL};
+            if (first < units) {
+                int lo = 0, hi = p.num_chunks - 1;  // the last chunk that begins at or before `first` (empty ones before it)
+                while (lo < hi) {
+                    const int mid = (lo + hi + 1) >> 1;
+                    if (before[mid] <= first) lo = mid; else hi = mid - 1;
+                }
+                WeightChunk d;
+                weight_chunk(p, lo, d);
+                const unsigned long long in_chunk = first - before[lo], each = key_units(d, per_tile);
+                start->c = lo;
+                start->kvh = (int)(in_chunk / each);
+                long long left = (long long)(in_chunk - start->kvh * each);
+                int pair = 0;
+                // the pairs that every query sees, all of one length, then the others
+                const int tiles = key_tiles(d, per_tile), whole = min(key_pairs(d), d.start / kKeys + 1);
+                pair = (int)min((long long)whole, left / tiles);
+                left -= (long long)pair * tiles;
+                while (left >= tiles - key_first_tile(d, pair, per_tile)) left -= tiles - key_first_tile(d, pair++, per_tile);
+                start->pair = pair;
+                start->tile = key_first_tile(d, pair, per_tile) + (int)left;
+            }
+        }
+    }
+    fence_proxy_async_smem();  // the key buffers go to the copies
+    __syncthreads();
+
     bool ok = true;
-    int ni = 0;           // items taken
+    int ni = 0;           // runs taken
     uint32_t g = 0;       // query tiles taken
     // waits until use number n of a ring of `stages` may overwrite what use n - stages left
     auto free_slot = [&](uint64_t* bar, uint32_t n, uint32_t stages) {
         return n < stages || mbar_wait_warp(bar, (n / stages - 1) & 1);
+    };
+
+    // the next run, once its keys have landed; false when there is none
+    auto next_run = [&](Run& run) {
+        if (!mbar_wait_warp(bars.k_full(ni & 1), (ni >> 1) & 1)) ok = false;
+        if (!ok) return false;
+        run = runs[ni & 1];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars.d_empty(ni & 1));
+        ++ni;
+        return run.nt > 0;
     };
 
     if (warp == 0) {
@@ -137,32 +210,49 @@ __global__ void __launch_bounds__(kThreads, 1)
             tma_prefetch_desc(&tmq);
             tma_prefetch_desc(&tmk);
         }
-        for (int k = blockIdx.x; k < num_items && ok; k += gridDim.x) {
-            Item it;
-            if (!describe(k, it)) continue;
-            const int kb = ni & 1, bpi = kKeys / B;  // blocks of an item
-            const int first = it.j0 / B, nblk = (it.d.nkeys + B - 1) / B - first;
+        WeightChunk d;
+        int c = start->c, kvh = start->kvh, pair = start->pair, tile = start->tile, row = 0;
+        long long left = start->units;
+        if (left > 0) {
+            for (int e = lane; e < c; e += 32)  // runs before this CTA's first one
+                if (weight_chunk(p, e, d)) row += key_pairs(d) * Hkv;
+            row = __reduce_add_sync(0xffffffffu, row);
+            weight_chunk(p, c, d);
+            row += kvh * key_pairs(d) + pair + blockIdx.x;
+        }
+        const int bpi = kKeys / B;  // blocks of a run
+        while (ok) {
+            const int kb = ni & 1;
+            const int j0 = pair * kKeys;
+            const int nt = left > 0 ? (int)min((long long)(key_tiles(d, per_tile) - tile), left) : 0;
             int pb = -1;
-            if (lane < bpi && lane < nblk) {
-                pb = p.block_tables[(size_t)it.d.s * p.max_blocks_per_seq + first + lane];
-                if (pb >= p.num_blocks) pb = -1;  // (the attention kernel has counted it)
+            if (nt > 0) {
+                const int first = j0 / B, nblk = (d.nkeys + B - 1) / B - first;
+                if (lane < bpi && lane < nblk) {
+                    pb = p.block_tables[(size_t)d.s * p.max_blocks_per_seq + first + lane];
+                    if (pb >= p.num_blocks) pb = -1;  // (the attention kernel has counted it)
+                }
             }
             const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, pb >= 0)) * 2u * B * 128u;
-            if (!free_slot(bars.k_empty(kb), ni, 2)) {
+            if (!free_slot(bars.k_empty(kb), ni, 2) || !free_slot(bars.d_empty(kb), ni, 2)) {
                 ok = false;
                 break;
             }
-            if (lane == 0) mbar_arrive_expect_tx(bars.k_full(kb), bytes);
-            __syncwarp();
-            if (pb >= 0) {
-                // block `lane` of the item: rows lane * B on of tile (lane * B) / 128
-                const int row = lane * B, tile = row / kTile;
-                uint8_t* dst = smem + kK + (2 * kb + tile) * kTileBytes + (row - tile * kTile) * 128;
-                for (int h = 0; h < 2; ++h)
-                    tma_load_2d(dst + h * kHalf, &tmk, it.kvh * kD + h * 64, pb * B, bars.k_full(kb));
+            if (lane == 0) {
+                runs[kb] = Run{d.s, kvh, d.r0, d.n, d.start, d.nkeys, j0, tile, nt, row};
+                mbar_arrive_expect_tx(bars.k_full(kb), bytes);
             }
+            __syncwarp();
             ++ni;
-            for (int t = 0; t < it.nt; ++t, ++g) {
+            if (nt == 0) break;
+            if (pb >= 0) {
+                // block `lane` of the run: rows lane * B on of tile (lane * B) / 128
+                const int at = lane * B, half_run = at / kTile;
+                uint8_t* dst = smem + kK + (2 * kb + half_run) * kTileBytes + (at - half_run * kTile) * 128;
+                for (int h = 0; h < 2; ++h)
+                    tma_load_2d(dst + h * kHalf, &tmk, kvh * kD + h * 64, pb * B, bars.k_full(kb));
+            }
+            for (int t = 0; t < nt; ++t, ++g) {
                 const int st = g % kQStages;
                 if (!free_slot(bars.q_empty(st), g, kQStages)) {
                     ok = false;
@@ -171,10 +261,24 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0) {
                     mbar_arrive_expect_tx(bars.q_full(st), 2 * per_tile * G * 128);
                     for (int h = 0; h < 2; ++h)
-                        tma_load_3d(smem + kQ + st * kTileBytes + h * kHalf, &tmq, h * 64, it.kvh * G,
-                                    it.d.r0 + (it.t0 + t) * per_tile, bars.q_full(st));
+                        tma_load_3d(smem + kQ + st * kTileBytes + h * kHalf, &tmq, h * 64, kvh * G,
+                                    d.r0 + (tile + t) * per_tile, bars.q_full(st));
                 }
                 __syncwarp();
+            }
+            // the next run in order: (chunk, kv head, pair), chunks without keys passed over
+            left -= nt;
+            ++row;
+            if (left > 0) {
+                if (++pair == key_pairs(d)) {
+                    pair = 0;
+                    if (++kvh == Hkv) {
+                        kvh = 0;
+                        do ++c;
+                        while (!(weight_chunk(p, c, d) && key_pairs(d) > 0));
+                    }
+                }
+                tile = key_first_tile(d, pair, per_tile);
             }
         }
         if (!ok && lane == 0) count_error(p.error_count);
@@ -186,26 +290,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t idesc = umma_idesc_bf16(128, 128, false, false);
         const uint64_t dk0 = umma_desc_sw128(smem_u32(smem + kK), 16, 1024);
         const uint64_t dq0 = umma_desc_sw128(smem_u32(smem + kQ), 16, 1024);
-        for (int k = blockIdx.x; k < num_items && ok; k += gridDim.x) {
-            Item it;
-            if (!describe(k, it)) continue;
-            const int kb = ni & 1;
-            if (!mbar_wait_warp(bars.k_full(kb), (ni >> 1) & 1)) {
-                ok = false;
-                break;
-            }
+        for (Run it; next_run(it);) {
+            const int kb = (ni - 1) & 1;
             for (int t = 0; t < it.nt && ok; ++t, ++g) {
                 const int st = g % kQStages, sb = g & 1;
                 if (!mbar_wait_warp(bars.q_full(st), (g / kQStages) & 1)) {
                     ok = false;
                     break;
                 }
+                if (!free_slot(bars.s_empty(sb), g, 2) || !mbar_wait_warp(bars.l_full(st), (g / kQStages) & 1)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
                 for (int tile = 0; tile < 2; ++tile) {
-                    if (!free_slot(bars.s_empty(sb, tile), g, 2)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
                     const uint64_t dk = dk0 + (uint64_t)(((2 * kb + tile) * kTileBytes) >> 4);
                     const uint64_t dq = dq0 + (uint64_t)((st * kTileBytes) >> 4);
 #pragma unroll
@@ -213,13 +311,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
                         umma_bf16_warp(tmem + sb * 256 + tile * 128, dk + off, dq + off, idesc, kk > 0);
                     }
-                    umma_commit_warp(bars.s_full(sb, tile));
                 }
-                if (!ok) break;
+                umma_commit_warp(bars.s_full(sb));
+                if (lane == 0) mbar_arrive(bars.s_full(sb));
                 umma_commit_warp(bars.q_empty(st));
             }
             umma_commit_warp(bars.k_empty(kb));
-            ++ni;
         }
         if (!ok && lane == 0) count_error(p.error_count);
         umma_commit_warp(bars.drain());
@@ -227,13 +324,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == kLseWarp) {
         // ============================================================ lse
-        for (int k = blockIdx.x; k < num_items && ok; k += gridDim.x) {
-            Item it;
-            if (!describe(k, it)) continue;
-            const float* lse = p.lse + ((size_t)it.kvh * p.total_q + it.d.r0) * G;
+        for (Run it; ok && next_run(it);) {
+            const float* lse = p.lse + ((size_t)it.kvh * p.total_q + it.r0) * G;
             for (int t = 0; t < it.nt; ++t, ++g) {
                 const int st = g % kQStages, i0 = (it.t0 + t) * per_tile;
-                const int rows = min(per_tile, it.d.n - i0) * G;
+                const int rows = min(per_tile, it.n - i0) * G;
                 float v[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
@@ -252,71 +347,87 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok && lane == 0) count_error(p.error_count);
     } else {
         // ============================================================ sums
-        const int quarter = warp & 3, tile = (warp - 2) >> 2;
-        const int r = quarter * 32 + lane;  // this thread's key of the tile
-        const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+        const int quarter = warp & 3, group = (warp - 2) >> 2;
+        const int r = quarter * 32 + lane;  // this thread's key of either tile
+        const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + group * 256;
         const float sl2 = p.scale_log2;
         const unsigned long long s2 = f32x2_pack(sl2, sl2);
-        for (int k = blockIdx.x; k < num_items; k += gridDim.x) {
-            Item it;
-            if (!describe(k, it)) continue;
-            const int j = it.j0 + tile * kTile + r;
-            bool valid = j < it.d.nkeys;
-            if (valid) {
-                const int pb = p.block_tables[(size_t)it.d.s * p.max_blocks_per_seq + j / B];
-                valid = pb >= 0 && pb < p.num_blocks;
+        for (Run it; next_run(it);) {
+            bool valid[2];
+#pragma unroll
+            for (int tile = 0; tile < 2; ++tile) {
+                const int j = it.j0 + tile * kTile + r;
+                valid[tile] = j < it.nkeys;
+                if (valid[tile]) {
+                    const int pb = p.block_tables[(size_t)it.s * p.max_blocks_per_seq + j / B];
+                    valid[tile] = pb >= 0 && pb < p.num_blocks;
+                }
             }
-            unsigned long long sum2[2] = {f32x2_pack(0.f, 0.f), f32x2_pack(0.f, 0.f)};
+            unsigned long long sum2[2][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum2[i >> 1][i & 1] = f32x2_pack(0.f, 0.f);
             for (int t = 0; t < it.nt; ++t, ++g) {
-                const int st = g % kQStages, sb = g & 1, i0 = (it.t0 + t) * per_tile;
-                // rows [lo, hi) of the tile see key j
-                const int hi = valid ? min(per_tile, it.d.n - i0) * G : 0;
-                const int lo = max(0, j - it.d.start - i0) * G;
-                if (ok && !mbar_wait(bars.l_full(st), (g / kQStages) & 1)) ok = false;
-                if (ok && !mbar_wait(bars.s_full(sb, tile), (g >> 1) & 1)) ok = false;
+                if ((g & 1) != group) continue;
+                const int st = g % kQStages, i0 = (it.t0 + t) * per_tile;
+                const int rows = min(per_tile, it.n - i0) * G;
+                const float4* lse = reinterpret_cast<const float4*>(smem + kLse) + st * (kTile / 4);
+                // the first row that sees this thread's key, in the second tile (the later key)
+                const int lo1 = max(0, it.j0 + kTile + r - it.start - i0) * G;
+                const bool dense = __all_sync(0xffffffffu, lo1 == 0 && rows == kTile && valid[0] && valid[1]);
+                // (the issuer of the products waits for the lse too before it lets s_full complete)
+                if (ok && !mbar_wait(bars.s_full(group), (g >> 1) & 1)) ok = false;
                 __syncwarp();
                 tc_fence_after();
-                const float4* lse = reinterpret_cast<const float4*>(smem + kLse) + st * (kTile / 4);
-                const uint32_t at = tmem + lane_off + sb * 256 + tile * 128;
-                const bool dense = __all_sync(0xffffffffu, lo == 0 && hi == kTile);
-                float x[2][32];
-                tmem_ld32(at, x[0]);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    tmem_wait_ld32(x[q & 1]);
-                    if (q < 3) tmem_ld32(at + (q + 1) * 32, x[(q + 1) & 1]);
-                    float(&v)[32] = x[q & 1];
+                for (int half = 0; half < 2; ++half) {  // 64 rows against both keys
+                    float x[2][2][32];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) tmem_ld32(at0 + (i & 1) * 128 + half * 64 + (i >> 1) * 32, x[i & 1][i >> 1]);
+                    tmem_wait_ld();
+                    if (half == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0 && ok) mbar_arrive(bars.s_empty(group));
+                    }
                     if (dense) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float4 l = lse[q * 8 + i];
-                            float y0, y1, y2, y3;
-                            f32x2_unpack(fma_f32x2(f32x2_pack(v[4 * i], v[4 * i + 1]), s2, f32x2_pack(l.x, l.y)), y0, y1);
-                            f32x2_unpack(fma_f32x2(f32x2_pack(v[4 * i + 2], v[4 * i + 3]), s2, f32x2_pack(l.z, l.w)), y2, y3);
-                            sum2[0] = add_f32x2(sum2[0], f32x2_pack(fast_exp2(y0), fast_exp2(y1)));
-                            sum2[1] = add_f32x2(sum2[1], f32x2_pack(fast_exp2(y2), fast_exp2(y3)));
+                        for (int i = 0; i < 16; ++i) {
+                            const float4 l = lse[half * 16 + i];
+                            const unsigned long long l01 = f32x2_pack(l.x, l.y), l23 = f32x2_pack(l.z, l.w);
+#pragma unroll
+                            for (int tile = 0; tile < 2; ++tile) {
+                                const float* v = &x[tile][i >> 3][4 * (i & 7)];
+                                float y0, y1, y2, y3;
+                                f32x2_unpack(fma_f32x2(f32x2_pack(v[0], v[1]), s2, l01), y0, y1);
+                                f32x2_unpack(fma_f32x2(f32x2_pack(v[2], v[3]), s2, l23), y2, y3);
+                                sum2[tile][0] = add_f32x2(sum2[tile][0], f32x2_pack(fast_exp2(y0), fast_exp2(y1)));
+                                sum2[tile][1] = add_f32x2(sum2[tile][1], f32x2_pack(fast_exp2(y2), fast_exp2(y3)));
+                            }
                         }
                     } else {
-                        const float* l1 = reinterpret_cast<const float*>(lse) + q * 32;
-                        float a = 0.f;
+                        const float* l = reinterpret_cast<const float*>(lse) + half * 64;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (q * 32 + i >= lo && q * 32 + i < hi) a += fast_exp2(fmaf(v[i], sl2, l1[i]));
-                        sum2[0] = add_f32x2(sum2[0], f32x2_pack(a, 0.f));
+                        for (int tile = 0; tile < 2; ++tile) {
+                            const int lo = max(0, it.j0 + tile * kTile + r - it.start - i0) * G - half * 64;
+                            const int hi = valid[tile] ? rows - half * 64 : 0;
+                            float a = 0.f;
+#pragma unroll
+                            for (int i = 0; i < 64; ++i)
+                                if (i >= lo && i < hi) a += fast_exp2(fmaf(x[tile][i >> 5][i & 31], sl2, l[i]));
+                            sum2[tile][0] = add_f32x2(sum2[tile][0], f32x2_pack(a, 0.f));
+                        }
                     }
                 }
-                tc_fence_before();
                 __syncwarp();
-                if (lane == 0 && ok) {
-                    mbar_arrive(bars.s_empty(sb, tile));
-                    mbar_arrive(bars.l_empty(st));
-                }
+                if (lane == 0 && ok) mbar_arrive(bars.l_empty(st));
             }
-            float a, b, c, d;
-            f32x2_unpack(sum2[0], a, b);
-            f32x2_unpack(sum2[1], c, d);
-            if (j < it.d.nkeys)
-                p.partial[(((size_t)it.c * Hkv + it.kvh) * p.pieces + it.piece) * p.partial_width + j] = (a + b) + (c + d);
+#pragma unroll
+            for (int tile = 0; tile < 2; ++tile) {
+                float a, b, c, d;
+                f32x2_unpack(sum2[tile][0], a, b);
+                f32x2_unpack(sum2[tile][1], c, d);
+                p.partial[((size_t)(it.row) * kKeyParts + group) * kKeys + tile * kTile + r] = (a + b) + (c + d);
+            }
         }
         if (!ok && lane == 0) count_error(p.error_count);
     }
@@ -330,7 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-int launch_prefill_weights_tc(const PrefillParams& p, int piece_tiles, int num_sms, cudaStream_t stream) {
+int launch_prefill_weights_tc(const PrefillParams& p, int num_sms, cudaStream_t stream) {
     CUtensorMap tmq, tmk;
     auto enc = tensor_map_encoder();
     if (!enc) return PA_ERR_CUDA;
@@ -346,10 +457,7 @@ int launch_prefill_weights_tc(const PrefillParams& p, int piece_tiles, int num_s
     int rc = pool_tensor_map(&tmk, p.k_cache, p.num_blocks, p.block_size, p.num_kv_heads, kD);
     if (rc != PA_OK) return rc;
     if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(key_weights_kernel), kSmemBytes)) != PA_OK) return rc;
-    const long long items = (long long)p.num_chunks * p.num_kv_heads * p.pieces * ((p.max_context_len + kKeys - 1) / kKeys);
-    if (items == 0) return PA_OK;
-    return launch_kernel(key_weights_kernel, dim3((unsigned)(items < num_sms ? items : num_sms)), dim3(kThreads), kSmemBytes,
-                         stream, tmq, tmk, p, piece_tiles);
+    return launch_kernel(key_weights_kernel, dim3((unsigned)num_sms), dim3(kThreads), kSmemBytes, stream, tmq, tmk, p);
 }
 
 }  // namespace pa
