@@ -7,9 +7,11 @@
 //     key_weights[s][kv head][j] += sum over the group's heads g of 2^(x_jg - lse_g)
 // and, where a context has several partitions, out = sum_i 2^(m_i - lse) l_i o_i.
 //
-// A CTA takes kTokens tokens of one (sequence, kv head); the CTA of the first
-// ones combines the partial outputs too.  An element of key_weights has one
-// owner: no atomics, and the sums' order is fixed.
+// A CTA takes kTokens tokens of one (sequence, kv head), and one more CTA the
+// partial outputs.  What a CTA reads (scores, weights, the partitions' states) is
+// loaded all at once, before the first of it is used: bound by the latency of the
+// scores, which lie in L2.  An element of key_weights has one owner: no atomics, and
+// the sums' order is fixed.
 #include "decode_common.cuh"
 
 namespace pa {
@@ -17,21 +19,57 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kTokens = 1024;
+constexpr int kEach = kTokens / kThreads;
 constexpr int kMaxGroup = 16, kMaxSplits = 128;
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) decode_weights_kernel(const DecodeParams p) {
+// G consecutive scores.
+template <int G>
+__device__ __forceinline__ void load_scores(const float* x, float (&v)[G]) {
+    if constexpr (G % 4 == 0) {
+#pragma unroll
+        for (int g = 0; g < G; g += 4) {
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(x + g));
+            v[g] = t.x;
+            v[g + 1] = t.y;
+            v[g + 2] = t.z;
+            v[g + 3] = t.w;
+        }
+    } else if constexpr (G == 2) {
+        const float2 t = __ldcg(reinterpret_cast<const float2*>(x));
+        v[0] = t.x;
+        v[1] = t.y;
+    } else {
+#pragma unroll
+        for (int g = 0; g < G; ++g) v[g] = __ldcg(x + g);
+    }
+}
+
+// kG: the group's heads, 0 for a number without an instance of its own.
+template <typename T, int D, int kG>
+__global__ void __launch_bounds__(kThreads, 4) decode_weights_kernel(const DecodeParams p) {
     __shared__ float lse_s[kMaxGroup];
     __shared__ float share[kMaxSplits][kMaxGroup];  // a partition's part of the output
     pdl_trigger();
     pdl_wait();
     const int unit = blockIdx.x, s = unit / p.num_kv_heads, kvh = unit - s * p.num_kv_heads;
-    const int G = p.group, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int G = kG ? kG : p.group, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int L = decode_context(p, s, false);
-    const int first = blockIdx.y * kTokens;
-    if (first >= max(L, 1)) return;
     const int nsplit = num_partitions(L, partition_of(p, s));
-    const bool merge = blockIdx.y == 0 && nsplit > 1;
+    const bool merge = blockIdx.y == 0;  // the CTA of the partial outputs
+    const int first = ((int)blockIdx.y - 1) * kTokens;
+    if (merge ? nsplit <= 1 : first >= L) return;
+    const float* scores = p.ws_scores + (size_t)unit * p.score_width * G;
+    float* weights = p.key_weights + (size_t)unit * p.key_width;
+    float x[kEach][kG ? kG : 1], w[kEach];
+    if (!merge) {
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const int j = first + e * kThreads + threadIdx.x;
+            if (j >= L) continue;
+            w[e] = weights[j];
+            if constexpr (kG != 0) load_scores<kG>(scores + (size_t)j * kG, x[e]);
+        }
+    }
     const float2* ml = p.ws_ml + (size_t)unit * p.max_splits * G;
     for (int g = warp; g < G; g += kThreads / 32) {
         float2 v[kMaxSplits / 32];
@@ -48,8 +86,7 @@ __global__ void __launch_bounds__(kThreads) decode_weights_kernel(const DecodePa
         for (int k = 0; k < kMaxSplits / 32; ++k)
             if (v[k].y != 0.f) sum += v[k].y * exp2f(v[k].x - m);  // (a NaN counts: it is not 0)
         sum = warp_sum(sum);
-        const float lse = sum == 0.f ? INFINITY : m + log2f(sum);  // no key: every weight is 0
-        if (lane == 0) lse_s[g] = lse;
+        if (lane == 0) lse_s[g] = sum == 0.f ? INFINITY : m + log2f(sum);  // no key: every weight is 0
         if (merge)
 #pragma unroll
             for (int k = 0; k < kMaxSplits / 32; ++k)
@@ -58,24 +95,24 @@ __global__ void __launch_bounds__(kThreads) decode_weights_kernel(const DecodePa
     }
     __syncthreads();
     if (merge) {
-        constexpr int kAhead = 16;
+        constexpr int kAhead = 8;
         const float4* o = reinterpret_cast<const float4*>(p.ws_o + (size_t)unit * p.max_splits * G * D);
         for (int i = threadIdx.x; i < G * (D / 4); i += kThreads) {
             const int g = i / (D / 4);
             float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
             for (int k0 = 0; k0 < nsplit; k0 += kAhead) {
-                float4 x[kAhead];
+                float4 y[kAhead];
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k)
-                    if (k0 + k < nsplit) x[k] = __ldcg(o + (size_t)(k0 + k) * G * (D / 4) + i);
+                    if (k0 + k < nsplit) y[k] = __ldcg(o + (size_t)(k0 + k) * G * (D / 4) + i);
 #pragma unroll
                 for (int k = 0; k < kAhead; ++k)
                     if (k0 + k < nsplit) {
-                        const float w = share[k0 + k][g];
-                        acc.x = fmaf(w, x[k].x, acc.x);
-                        acc.y = fmaf(w, x[k].y, acc.y);
-                        acc.z = fmaf(w, x[k].z, acc.z);
-                        acc.w = fmaf(w, x[k].w, acc.w);
+                        const float f = share[k0 + k][g];
+                        acc.x = fmaf(f, y[k].x, acc.x);
+                        acc.y = fmaf(f, y[k].y, acc.y);
+                        acc.z = fmaf(f, y[k].z, acc.z);
+                        acc.w = fmaf(f, y[k].w, acc.w);
                     }
             }
             T* out = static_cast<T*>(p.out) + ((size_t)s * p.num_q_heads + (size_t)kvh * G) * D + 4 * i;
@@ -84,24 +121,32 @@ __global__ void __launch_bounds__(kThreads) decode_weights_kernel(const DecodePa
             out[2] = from_float<T>(acc.z);
             out[3] = from_float<T>(acc.w);
         }
+        return;
     }
-    const float* scores = p.ws_scores + (size_t)unit * p.score_width * G;
-    float* weights = p.key_weights + (size_t)unit * p.key_width;
-    const int last = min(L, first + kTokens);
-#pragma unroll 4
-    for (int j = first + threadIdx.x; j < last; j += kThreads) {
-        const float* x = scores + (size_t)j * G;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int j = first + e * kThreads + threadIdx.x;
+        if (j >= L) continue;
         float sum = 0.f;
-        if ((G & 3) == 0) {
-            for (int g = 0; g < G; g += 4) {
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(x + g));
-                sum += (exp2f(v.x - lse_s[g]) + exp2f(v.y - lse_s[g + 1])) +
-                       (exp2f(v.z - lse_s[g + 2]) + exp2f(v.w - lse_s[g + 3]));
-            }
+        if constexpr (kG != 0) {
+#pragma unroll
+            for (int g = 0; g < kG; ++g) sum += exp2f(x[e][g] - lse_s[g]);
         } else {
-            for (int g = 0; g < G; ++g) sum += exp2f(__ldcg(x + g) - lse_s[g]);
+            for (int g = 0; g < G; ++g) sum += exp2f(__ldcg(scores + (size_t)j * G + g) - lse_s[g]);
         }
-        weights[j] += sum;
+        weights[j] = w[e] + sum;
+    }
+}
+
+template <typename T, int D>
+int launch(const DecodeParams& p, dim3 grid, cudaStream_t stream) {
+    const dim3 block(kThreads);
+    switch (p.group) {
+        case 1: return launch_kernel(decode_weights_kernel<T, D, 1>, grid, block, 0, stream, p);
+        case 2: return launch_kernel(decode_weights_kernel<T, D, 2>, grid, block, 0, stream, p);
+        case 4: return launch_kernel(decode_weights_kernel<T, D, 4>, grid, block, 0, stream, p);
+        case 8: return launch_kernel(decode_weights_kernel<T, D, 8>, grid, block, 0, stream, p);
+        default: return launch_kernel(decode_weights_kernel<T, D, 0>, grid, block, 0, stream, p);
     }
 }
 
@@ -109,14 +154,12 @@ __global__ void __launch_bounds__(kThreads) decode_weights_kernel(const DecodePa
 
 int launch_decode_weights(const DecodeParams& p, int dtype, cudaStream_t stream) {
     if (p.group > kMaxGroup || p.max_splits > kMaxSplits) return PA_ERR_UNSUPPORTED;
-    const int pieces = p.max_context_len > kTokens ? (p.max_context_len + kTokens - 1) / kTokens : 1;
-    if (pieces > 65535) return PA_ERR_UNSUPPORTED;
-    const dim3 grid(p.num_seqs * p.num_kv_heads, pieces), block(kThreads);
+    const int pieces = (p.max_context_len + kTokens - 1) / kTokens;
+    if (pieces >= 65535) return PA_ERR_UNSUPPORTED;
+    const dim3 grid(p.num_seqs * p.num_kv_heads, 1 + pieces);
     if (dtype == PA_F32)
-        return p.head_dim == 64 ? launch_kernel(decode_weights_kernel<float, 64>, grid, block, 0, stream, p)
-                                : launch_kernel(decode_weights_kernel<float, 128>, grid, block, 0, stream, p);
-    return p.head_dim == 64 ? launch_kernel(decode_weights_kernel<__nv_bfloat16, 64>, grid, block, 0, stream, p)
-                            : launch_kernel(decode_weights_kernel<__nv_bfloat16, 128>, grid, block, 0, stream, p);
+        return p.head_dim == 64 ? launch<float, 64>(p, grid, stream) : launch<float, 128>(p, grid, stream);
+    return p.head_dim == 64 ? launch<__nv_bfloat16, 64>(p, grid, stream) : launch<__nv_bfloat16, 128>(p, grid, stream);
 }
 
 }  // namespace pa

@@ -85,7 +85,8 @@ int pa_rope(void* q_out, void* k_out, const void* q, const void* k, int num_toke
     if ((num_q_heads > 0 && (!q || !q_out)) || (num_kv_heads > 0 && (!k || !k_out)) ||
         (rot_dim > 0 && (!rope_pos || !inv_freq)))
         return PA_ERR_INVALID_ARG;
-    if ((rc = check_device(nullptr)) != PA_OK) return rc;
+    int num_sms = 0;
+    if ((rc = check_device(&num_sms)) != PA_OK) return rc;
     RopeParams p;
     p.q = q;
     p.k = k;
@@ -107,7 +108,7 @@ int pa_rope(void* q_out, void* k_out, const void* q, const void* k, int num_toke
     p.num_axes = num_axes;
     p.interleaved = interleaved != 0;
     p.error_count = error_count;
-    return launch_rope(p, dtype, static_cast<cudaStream_t>(stream));
+    return launch_rope(p, dtype, num_sms, static_cast<cudaStream_t>(stream));
 }
 
 int pa_rope_write_kv_paged(void* q_out, const void* q, const void* k_new, const void* v_new, int num_tokens,
@@ -128,7 +129,8 @@ int pa_rope_write_kv_paged(void* q_out, const void* q, const void* k_new, const 
     if ((num_q_heads > 0 && (!q || !q_out)) || !k_new || !v_new || !k_cache || !v_cache || !seq_idx || !pos ||
         (num_seqs > 0 && max_blocks_per_seq > 0 && !block_tables) || (rot_dim > 0 && (!rope_pos || !inv_freq)))
         return PA_ERR_INVALID_ARG;
-    if ((rc = check_device(nullptr)) != PA_OK) return rc;
+    int num_sms = 0;
+    if ((rc = check_device(&num_sms)) != PA_OK) return rc;
     RopeParams p;
     p.q = q;
     p.k = k_new;
@@ -162,7 +164,7 @@ int pa_rope_write_kv_paged(void* q_out, const void* q, const void* k_new, const 
     p.key_width = key_weights ? key_width : 0;
     p.slot_mapping = slot_mapping;
     p.error_count = error_count;
-    return launch_rope(p, dtype, static_cast<cudaStream_t>(stream));
+    return launch_rope(p, dtype, num_sms, static_cast<cudaStream_t>(stream));
 }
 
 size_t pa_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,

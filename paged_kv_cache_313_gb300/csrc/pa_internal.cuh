@@ -154,7 +154,7 @@ struct KeyRuns {
     unsigned long long units;
     int runs;
 };
-constexpr int kKeyParts = 2;  // rows of partial that a part of a run's sums are in, one for each warp that adds some of them
+constexpr int kKeyParts = 4;  // rows of partial that a part of a run's sums are in, one for each 32 query rows
 
 struct PrefillParams {
     void* out;
@@ -246,6 +246,8 @@ struct EvictParams {
     int* dst;
     int max_moves;
     int32_t* error_count;
+    int vecs = 0;  // 16-byte pieces in a row of one kv head
+    Divisor by_vecs;
 };
 
 // Kernel launchers (defined in the .cu files).
@@ -307,7 +309,7 @@ int launch_decode_weights(const DecodeParams& p, int dtype, cudaStream_t stream)
 int launch_prefill_weights_fma(const PrefillParams& p, int dtype, cudaStream_t stream);
 int launch_prefill_weights_tc(const PrefillParams& p, int num_sms, cudaStream_t stream);
 int launch_prefill_weights_add(const PrefillParams& p, cudaStream_t stream);
-int launch_rope(const RopeParams& p, int dtype, cudaStream_t stream);
+int launch_rope(const RopeParams& p, int dtype, int num_sms, cudaStream_t stream);
 int launch_evict(const EvictParams& p, int row_bytes, cudaStream_t stream);
 bool prefill_tc_supported(const PrefillParams& p, int dtype);
 int launch_prefill_tc(const PrefillParams& p, cudaStream_t stream);

@@ -2,11 +2,14 @@
 // 5th-gen tensor cores (tcgen05, accumulators in TMEM), bf16, head_dim 128.
 //
 // The attention kernel (prefill_tc.cu) has left every row's lse.  Here
-//     partial[chunk][kv head][piece][j] = sum over the piece's rows r of 2^(x_rj - lse_r)
-// with x = scale log2(e) Q K^T.  The product is taken transposed, K Q^T: a row of
-// tensor memory is a key, so a thread sums its key's weights in a register and
-// nothing crosses threads.  Bound by the tensor cores (half the attention's
-// products) and the exponentials alike.
+//     sum over the rows r that see key j of 2^(x_rj - lse_r),  x = scale log2(e) Q K^T
+// for every key.  A row of tensor memory is a query row, so its lse is one register of
+// one thread; a thread keeps a sum for each of 128 keys over all its rows, and the 32
+// lanes' sums are added only when the keys change.  (With a key a row, each score's lse
+// came from shared memory, whose bandwidth the products' operands take up: 2.3 times
+// the time of the products.)  Bound by the tensor cores (half the attention's products),
+// shared memory (a 128 x 256 x 16 product reads 12 KB in 128 cycles, and the query tiles'
+// copies write) and the exponentials alike.
 //
 // A run is a pair of 128-key tiles of one (chunk, kv head) against the 128-row query
 // tiles (positions times the G heads of the kv head) that see a key of it, in order.
@@ -17,16 +20,12 @@
 // Each part of a run leaves a row of 256 sums: run number + CTA number is a row of its
 // own.  The next run's keys are loaded into the other of two buffers meanwhile.
 //
-// Warp roles (352 threads):
-//   warp 0     producer: key tiles (one TMA box per block and 64-column half) and
-//              query tiles (one box per half)
-//   warp 1     owner of the tensor memory and issuer of the products
-//   warps 2-9  the sums, in two groups of four that take the query tiles in turns, so
-//              that one exponentiates while the other waits for its scores; a thread
-//              takes one key of either key tile, so that an lse read from shared
-//              memory, whose bandwidth the products' operands take up, serves two
-//              scores
-//   warp 10    the query tiles' lse, to shared memory
+// Warp roles (384 threads):
+//   warp 0      producer: keys (one TMA box per block and 64-column half) and query
+//               tiles (one box per half)
+//   warp 1      owner of the tensor memory and issuer of the products
+//   warps 4-11  the sums: a thread a query row and 128 of the 256 keys; they take the
+//               registers that warps 0-3 give up
 // Every wait is bounded, tensor memory is always freed, and copies and products
 // in flight are waited for before a CTA exits, as in prefill_tc.cu.
 #include "prefill_weights.cuh"
@@ -41,17 +40,19 @@ static_assert(kKeys == 2 * kTile, "keys of a run");
 constexpr int kMinUnits = 2;
 constexpr int kHalf = 128 * 128;           // bytes of a 64-column half of a 128-row tile
 constexpr int kTileBytes = 2 * kHalf;
-constexpr int kSumWarps = 4;  // of a group
-constexpr int kThreads = (2 * kSumWarps + 3) * 32;
-constexpr int kLseWarp = 2 * kSumWarps + 2;
+constexpr int kSumWarps = 8;
+constexpr int kThreads = (kSumWarps + 4) * 32;
+// registers a thread: 4 warps of 56 and 8 of 224 are the 12 of 168 that the block is launched with
+#define PA_OTHER_REGS "56"
+#define PA_SUM_REGS "224"
+constexpr int kKeyHalf = kKeys * 128;      // bytes of a 64-column half of the run's keys
 constexpr uint32_t kTmemCols = 512;        // two buffers of two key tiles' scores
 constexpr int kQStages = 3;
-constexpr int kK = 0;                      // [2 buffers][2 tiles]
+constexpr int kK = 0;                      // [2 buffers][2 halves][256 keys]
 constexpr int kQ = kK + 4 * kTileBytes;
-constexpr int kLse = kQ + kQStages * kTileBytes;  // float [kQStages][128]
-constexpr int kBars = kLse + kQStages * kTile * 4;
-// k_full[2], k_empty[2], q_full[3], q_empty[3], l_full[3], l_empty[3], s_full[2], s_empty[2], d_empty[2], drain
-constexpr int kNumBars = 4 + 4 * kQStages + 6 + 1;
+constexpr int kBars = kQ + kQStages * kTileBytes;
+// k_full[2], k_empty[2], q_full[3], q_empty[3], s_full[2], s_empty[2], d_empty[2], drain
+constexpr int kNumBars = 4 + 2 * kQStages + 6 + 1;
 constexpr int kTmemSlot = kBars + kNumBars * 8;
 constexpr int kStart = (kTmemSlot + 4 + 7) / 8 * 8;
 struct Start {  // where a CTA's units begin
@@ -71,12 +72,10 @@ struct Bars {
     __device__ uint64_t* k_empty(int i) const { return base + 2 + i; }
     __device__ uint64_t* q_full(int i) const { return base + 4 + i; }
     __device__ uint64_t* q_empty(int i) const { return base + 4 + kQStages + i; }
-    __device__ uint64_t* l_full(int i) const { return base + 4 + 2 * kQStages + i; }
-    __device__ uint64_t* l_empty(int i) const { return base + 4 + 3 * kQStages + i; }
-    __device__ uint64_t* s_full(int i) const { return base + 4 + 4 * kQStages + i; }
-    __device__ uint64_t* s_empty(int i) const { return base + 6 + 4 * kQStages + i; }
-    __device__ uint64_t* d_empty(int i) const { return base + 8 + 4 * kQStages + i; }
-    __device__ uint64_t* drain() const { return base + 10 + 4 * kQStages; }
+    __device__ uint64_t* s_full(int i) const { return base + 4 + 2 * kQStages + i; }
+    __device__ uint64_t* s_empty(int i) const { return base + 6 + 2 * kQStages + i; }
+    __device__ uint64_t* d_empty(int i) const { return base + 8 + 2 * kQStages + i; }
+    __device__ uint64_t* drain() const { return base + 10 + 2 * kQStages; }
 };
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -97,15 +96,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(bars.k_full(i), 1);
             mbar_init(bars.k_empty(i), 1);
-            mbar_init(bars.s_full(i), 2);  // the products' commit, and the issuer, which has seen the lse
+            mbar_init(bars.s_full(i), 1);
             mbar_init(bars.s_empty(i), kSumWarps);
-            mbar_init(bars.d_empty(i), 2 * kSumWarps + 2);
+            mbar_init(bars.d_empty(i), kSumWarps + 1);
         }
         for (int i = 0; i < kQStages; ++i) {
             mbar_init(bars.q_full(i), 1);
             mbar_init(bars.q_empty(i), 1);
-            mbar_init(bars.l_full(i), 1);
-            mbar_init(bars.l_empty(i), kSumWarps);
         }
         mbar_init(bars.drain(), 1);
         fence_mbar_init();
@@ -182,8 +179,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    fence_proxy_async_smem();  // the key buffers go to the copies
+    // rows of a query tile that no copy fills (groups that do not divide 128): zeros, whose scores are finite
+    if (per_tile * G < kTile)
+        for (int i = threadIdx.x; i < kQStages * kTileBytes / 16; i += kThreads)
+            reinterpret_cast<uint4*>(smem + kQ)[i] = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();  // the key buffers (and these) go to the copies
     __syncthreads();
+    if (warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 " PA_OTHER_REGS ";");
 
     bool ok = true;
     int ni = 0;           // runs taken
@@ -246,11 +248,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++ni;
             if (nt == 0) break;
             if (pb >= 0) {
-                // block `lane` of the run: rows lane * B on of tile (lane * B) / 128
-                const int at = lane * B, half_run = at / kTile;
-                uint8_t* dst = smem + kK + (2 * kb + half_run) * kTileBytes + (at - half_run * kTile) * 128;
+                uint8_t* dst = smem + kK + 2 * kb * kKeyHalf + lane * B * 128;  // block `lane` of the run
                 for (int h = 0; h < 2; ++h)
-                    tma_load_2d(dst + h * kHalf, &tmk, kvh * kD + h * 64, pb * B, bars.k_full(kb));
+                    tma_load_2d(dst + h * kKeyHalf, &tmk, kvh * kD + h * 64, pb * B, bars.k_full(kb));
             }
             for (int t = 0; t < nt; ++t, ++g) {
                 const int st = g % kQStages;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else if (warp == 1) {
         // ============================================================ products
-        constexpr uint32_t idesc = umma_idesc_bf16(128, 128, false, false);
+        constexpr uint32_t idesc = umma_idesc_bf16(kTile, kKeys, false, false);
         const uint64_t dk0 = umma_desc_sw128(smem_u32(smem + kK), 16, 1024);
         const uint64_t dq0 = umma_desc_sw128(smem_u32(smem + kQ), 16, 1024);
         for (Run it; next_run(it);) {
@@ -298,22 +298,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ok = false;
                     break;
                 }
-                if (!free_slot(bars.s_empty(sb), g, 2) || !mbar_wait_warp(bars.l_full(st), (g / kQStages) & 1)) {
+                if (!free_slot(bars.s_empty(sb), g, 2)) {
                     ok = false;
                     break;
                 }
                 tc_fence_after();
-                for (int tile = 0; tile < 2; ++tile) {
-                    const uint64_t dk = dk0 + (uint64_t)(((2 * kb + tile) * kTileBytes) >> 4);
-                    const uint64_t dq = dq0 + (uint64_t)((st * kTileBytes) >> 4);
+                const uint64_t dk = dk0 + (uint64_t)((2 * kb * kKeyHalf) >> 4);
+                const uint64_t dq = dq0 + (uint64_t)((st * kTileBytes) >> 4);
 #pragma unroll
-                    for (int kk = 0; kk < kD / 16; ++kk) {
-                        const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-                        umma_bf16_warp(tmem + sb * 256 + tile * 128, dk + off, dq + off, idesc, kk > 0);
-                    }
-                }
+                for (int kk = 0; kk < kD / 16; ++kk)
+                    umma_bf16_warp(tmem + sb * kKeys, dq + (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4),
+                                   dk + (uint64_t)(((kk >> 2) * kKeyHalf + (kk & 3) * 32) >> 4), idesc, kk > 0);
                 umma_commit_warp(bars.s_full(sb));
-                if (lane == 0) mbar_arrive(bars.s_full(sb));
                 umma_commit_warp(bars.q_empty(st));
             }
             umma_commit_warp(bars.k_empty(kb));
@@ -322,112 +318,95 @@ __global__ void __launch_bounds__(kThreads, 1)
         umma_commit_warp(bars.drain());
         if (!mbar_wait_warp(bars.drain(), 0) && lane == 0) count_error(p.error_count);
         __syncwarp();
-    } else if (warp == kLseWarp) {
-        // ============================================================ lse
-        for (Run it; ok && next_run(it);) {
-            const float* lse = p.lse + ((size_t)it.kvh * p.total_q + it.r0) * G;
-            for (int t = 0; t < it.nt; ++t, ++g) {
-                const int st = g % kQStages, i0 = (it.t0 + t) * per_tile;
-                const int rows = min(per_tile, it.n - i0) * G;
-                float v[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    v[i] = lane + 32 * i < rows ? -lse[(size_t)i0 * G + lane + 32 * i] : -INFINITY;
-                if (!free_slot(bars.l_empty(st), g, kQStages)) {
-                    ok = false;
-                    break;
-                }
-                float* to = reinterpret_cast<float*>(smem + kLse) + st * kTile;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) to[lane + 32 * i] = v[i];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bars.l_full(st));
-            }
-        }
-        if (!ok && lane == 0) count_error(p.error_count);
-    } else {
+    } else if (warp >= 4) {
         // ============================================================ sums
-        const int quarter = warp & 3, group = (warp - 2) >> 2;
-        const int r = quarter * 32 + lane;  // this thread's key of either tile
-        const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + group * 256;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 " PA_SUM_REGS ";");
+        const int quarter = warp & 3, col0 = ((warp - 4) >> 2) * 128;
+        const int r = quarter * 32 + lane;  // this thread's row of a query tile
+        const uint32_t at0 = tmem + ((uint32_t)(quarter * 32) << 16) + col0;
+        const int r_pos = r / G;            // and its position
         const float sl2 = p.scale_log2;
         const unsigned long long s2 = f32x2_pack(sl2, sl2);
         for (Run it; next_run(it);) {
-            bool valid[2];
+            // the lse of this thread's row in query tile t of the run; loaded a tile ahead, and not touched before it is needed
+            const float* lse = p.lse + ((size_t)it.kvh * p.total_q + it.r0) * G + r;
+            auto has_row = [&](int t) { return t < it.nt && r < min(per_tile, it.n - (it.t0 + t) * per_tile) * G; };
+            auto load_lse = [&](int t) { return has_row(t) ? __ldg(lse + (size_t)(it.t0 + t) * per_tile * G) : 0.f; };
+            unsigned long long sum2[64];  // sums of keys col0 + 2 i and col0 + 2 i + 1
 #pragma unroll
-            for (int tile = 0; tile < 2; ++tile) {
-                const int j = it.j0 + tile * kTile + r;
-                valid[tile] = j < it.nkeys;
-                if (valid[tile]) {
-                    const int pb = p.block_tables[(size_t)it.s * p.max_blocks_per_seq + j / B];
-                    valid[tile] = pb >= 0 && pb < p.num_blocks;
-                }
-            }
-            unsigned long long sum2[2][2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) sum2[i >> 1][i & 1] = f32x2_pack(0.f, 0.f);
+            for (int i = 0; i < 64; ++i) sum2[i] = f32x2_pack(0.f, 0.f);
+            const int see0 = it.start + r_pos + 1 - it.j0 - col0;
+            float lse_next = load_lse(0);
             for (int t = 0; t < it.nt; ++t, ++g) {
-                if ((g & 1) != group) continue;
-                const int st = g % kQStages, i0 = (it.t0 + t) * per_tile;
-                const int rows = min(per_tile, it.n - i0) * G;
-                const float4* lse = reinterpret_cast<const float4*>(smem + kLse) + st * (kTile / 4);
-                // the first row that sees this thread's key, in the second tile (the later key)
-                const int lo1 = max(0, it.j0 + kTile + r - it.start - i0) * G;
-                const bool dense = __all_sync(0xffffffffu, lo1 == 0 && rows == kTile && valid[0] && valid[1]);
-                // (the issuer of the products waits for the lse too before it lets s_full complete)
-                if (ok && !mbar_wait(bars.s_full(group), (g >> 1) & 1)) ok = false;
+                const int sb = g & 1, i0 = (it.t0 + t) * per_tile;
+                const float nl = has_row(t) ? -lse_next : -INFINITY;
+                lse_next = load_lse(t + 1);
+                // this row sees the first `see` of the thread's keys
+                int see = see0 + i0;
+                const bool dense = it.n - i0 >= per_tile && see - r_pos >= 128;  // every row, the first one's position too
+                if (nl == -INFINITY) see = 0;  // (no such row; or one without keys, or with an infinite lse: weights of 0)
+                if (ok && !mbar_wait(bars.s_full(sb), (g >> 1) & 1)) ok = false;
                 __syncwarp();
                 tc_fence_after();
+                const unsigned long long nl2 = f32x2_pack(nl, nl);
+                // 32 keys at a time, the next ones on their way.  (Dense tiles have a loop of their own: their instructions lie
+                // together.)
+                auto add_tile = [&](auto add) {
+                    float xs[2][32];
+                    tmem_ld32(at0 + sb * kKeys, xs[0]);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {  // 64 rows against both keys
-                    float x[2][2][32];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) tmem_ld32(at0 + (i & 1) * 128 + half * 64 + (i >> 1) * 32, x[i & 1][i >> 1]);
-                    tmem_wait_ld();
-                    if (half == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0 && ok) mbar_arrive(bars.s_empty(group));
-                    }
-                    if (dense) {
+                    for (int q = 0; q < 4; ++q) {
+                        float(&x)[32] = xs[q & 1];
+                        tmem_wait_ld32(x);
+                        if (q < 3) tmem_ld32(at0 + sb * kKeys + (q + 1) * 32, xs[(q + 1) & 1]);
+                        if (q == 3) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0 && ok) mbar_arrive(bars.s_empty(sb));
+                        }
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const float4 l = lse[half * 16 + i];
-                            const unsigned long long l01 = f32x2_pack(l.x, l.y), l23 = f32x2_pack(l.z, l.w);
-#pragma unroll
-                            for (int tile = 0; tile < 2; ++tile) {
-                                const float* v = &x[tile][i >> 3][4 * (i & 7)];
-                                float y0, y1, y2, y3;
-                                f32x2_unpack(fma_f32x2(f32x2_pack(v[0], v[1]), s2, l01), y0, y1);
-                                f32x2_unpack(fma_f32x2(f32x2_pack(v[2], v[3]), s2, l23), y2, y3);
-                                sum2[tile][0] = add_f32x2(sum2[tile][0], f32x2_pack(fast_exp2(y0), fast_exp2(y1)));
-                                sum2[tile][1] = add_f32x2(sum2[tile][1], f32x2_pack(fast_exp2(y2), fast_exp2(y3)));
-                            }
-                        }
-                    } else {
-                        const float* l = reinterpret_cast<const float*>(lse) + half * 64;
-#pragma unroll
-                        for (int tile = 0; tile < 2; ++tile) {
-                            const int lo = max(0, it.j0 + tile * kTile + r - it.start - i0) * G - half * 64;
-                            const int hi = valid[tile] ? rows - half * 64 : 0;
-                            float a = 0.f;
-#pragma unroll
-                            for (int i = 0; i < 64; ++i)
-                                if (i >= lo && i < hi) a += fast_exp2(fmaf(x[tile][i >> 5][i & 31], sl2, l[i]));
-                            sum2[tile][0] = add_f32x2(sum2[tile][0], f32x2_pack(a, 0.f));
+                            float y0, y1;
+                            add(q * 32 + 2 * i, x[2 * i], x[2 * i + 1], y0, y1);
+                            sum2[q * 16 + i] = add_f32x2(sum2[q * 16 + i], f32x2_pack(fast_exp2(y0), fast_exp2(y1)));
                         }
                     }
-                }
-                __syncwarp();
-                if (lane == 0 && ok) mbar_arrive(bars.l_empty(st));
+                };
+                if (dense)
+                    add_tile([&](int, float x0, float x1, float& y0, float& y1) {
+                        f32x2_unpack(fma_f32x2(f32x2_pack(x0, x1), s2, nl2), y0, y1);
+                    });
+                else
+                    add_tile([&](int key, float x0, float x1, float& y0, float& y1) {
+                        y0 = key < see ? fmaf(x0, sl2, nl) : -INFINITY;
+                        y1 = key + 1 < see ? fmaf(x1, sl2, nl) : -INFINITY;
+                    });
             }
+            // the lanes' sums added, halving what a lane holds each time: 4 keys are left to each
+            float v[128];
 #pragma unroll
-            for (int tile = 0; tile < 2; ++tile) {
-                float a, b, c, d;
-                f32x2_unpack(sum2[tile][0], a, b);
-                f32x2_unpack(sum2[tile][1], c, d);
-                p.partial[((size_t)(it.row) * kKeyParts + group) * kKeys + tile * kTile + r] = (a + b) + (c + d);
+            for (int i = 0; i < 64; ++i) f32x2_unpack(sum2[i], v[2 * i], v[2 * i + 1]);
+            int first = 0;
+#pragma unroll
+            for (int n = 64; n >= 4; n >>= 1) {
+                const int bit = n >> 2;
+                const bool upper = lane & bit;
+                first += upper ? n : 0;
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const float give = upper ? v[i] : v[i + n], keep = upper ? v[i + n] : v[i];
+                    v[i] = keep + __shfl_xor_sync(0xffffffffu, give, bit);
+                }
             }
+            // keys of an invalid block draw nothing (4 keys from a multiple of 4 are of one block)
+            const int j = it.j0 + col0 + first;
+            bool valid = j < it.nkeys;
+            if (valid) {
+                const int pb = p.block_tables[(size_t)it.s * p.max_blocks_per_seq + j / B];
+                valid = pb >= 0 && pb < p.num_blocks;
+            }
+            *reinterpret_cast<float4*>(p.partial + ((size_t)it.row * kKeyParts + quarter) * kKeys + col0 + first) =
+                valid ? make_float4(v[0], v[1], v[2], v[3]) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         if (!ok && lane == 0) count_error(p.error_count);
     }

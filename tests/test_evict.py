@@ -33,6 +33,9 @@ CASES = [
     (BF16, 1, 64, 16, [100, 200], 64, 64, 0, "random"),   # all of the budget protected
     (BF16, 1, 64, 16, [100, 200], 64, 0, 64, "random"),
     (BF16, 2, 64, 16, [200, 300], 64, 10, 20, "places"),  # places that make more than the budget protected
+    (BF16, 1, 64, 16, [6000, 9000], 3000, 4, 50, "few"),        # thousands of equal weights
+    (BF16, 2, 64, 16, [9000, 5000], 4500, 0, 0, "special"),
+    (BF16, 1, 64, 16, [1000, 1128, 1129], 1000, 2, 30, "random"),  # up to 129 moves
     (BF16, 1, 64, 64, [45000, 41000], 1000, 4, 100, "random"),  # longer than the keys held in shared memory
 ]
 
