@@ -154,6 +154,7 @@ struct KeyRuns {
     unsigned long long units;
     int runs;
 };
+constexpr int kMaxSpans = 64;
 constexpr int kKeyParts = 4;  // rows of partial that a part of a run's sums are in, one for each 32 query rows
 
 struct PrefillParams {
@@ -191,7 +192,10 @@ struct PrefillParams {
     // kernel leaves each key's summed weights in partial, and a third adds those to key_weights, float
     // [num_seqs][num_kv_heads][key_width], in a fixed order.  partial is float [num_chunks][num_kv_heads][max_context_len]
     // from the CUDA cores, and rows of 256 keys from the tensor cores (runs set): see prefill_weights_tc.cu.
+    // Few query tiles: their keys are cut into `spans` spans, whose rows go to part_o / part_ml,
+    // [span][num_kv_heads][total_q * G], and are joined by one more kernel.
     float* lse = nullptr;
+    int spans = 1;
     float* partial = nullptr;
     KeyRuns* runs = nullptr;
     float* key_weights = nullptr;

@@ -45,6 +45,7 @@
 // shared memory and no MMA is writing tensor memory when the CTA frees its
 // tensor memory and exits.
 #include "pa_internal.cuh"
+#include "prefill_weights.cuh"
 #include "sm100_ptx.cuh"
 
 namespace pa {
@@ -139,9 +140,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     // work queue instead was measured 10-25% slower.)
     const int tiles_max = (p.max_q_len + pos_per_tile - 1) / pos_per_tile;
     const int per_rank = p.num_chunks * p.num_kv_heads;
-    const int num_items = tiles_max * per_rank;
+    // (kLse) where there are fewer tiles than SMs, a tile's keys are cut into spans, an item each, whose partial rows
+    // another kernel joins
+    const int spans = kLse ? p.spans : 1;
+    const int num_items = tiles_max * per_rank * spans;
     struct Item {
         int kvh, r0, s, start, i0, nq, last_key, nkeys, nt;
+        int span, key0;  // (kLse) the span, its first key
     };
     auto item_of = [&](int c) {  // this CTA's item of pass c
         const int b = blockIdx.x, g = gridDim.x;
@@ -149,6 +154,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     // false for an empty item (a tile past its chunk's queries, or an invalid chunk)
     auto describe = [&](int k, Item& d) {
+        d.span = 0;
+        d.key0 = 0;
+        if (kLse && spans > 1) {
+            d.span = k % spans;
+            k /= spans;
+        }
         const int rank = k / per_rank, rem = k - rank * per_rank;
         const int c = rem / p.num_kv_heads;
         d.kvh = rem - c * p.num_kv_heads;
@@ -161,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (chunk_ok && prefix_mode && n > 0) d.start = p.prefix_lens[d.s];  // the group's shared prefix length
         chunk_ok = chunk_ok && d.start >= 0;
         if (!chunk_ok) {
-            if (rank == 0 && d.kvh == 0 && threadIdx.x == 0) count_error(p.error_count);
+            if (rank == 0 && d.kvh == 0 && d.span == 0 && threadIdx.x == 0) count_error(p.error_count);
             return false;
         }
         const int ntiles_q = (n + pos_per_tile - 1) / pos_per_tile;
@@ -172,11 +183,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // the tile's last query position; a cascade prefix pass reads keys [0, start) for every row
         d.last_key = prefix_mode ? d.start - 1 : d.start + d.i0 + d.nq - 1;
         if (d.last_key >= cap) {
-            if (threadIdx.x == 0) count_error(p.error_count);
+            if (threadIdx.x == 0 && d.span == 0) count_error(p.error_count);
             d.last_key = cap - 1;
         }
         d.nkeys = d.last_key + 1;  // keys 0..last_key are read
         d.nt = d.nkeys > 0 ? (d.nkeys + kTileK - 1) / kTileK : 0;
+        if (kLse && spans > 1) {  // this span's tiles, the keys counted from its first one
+            const int each = (d.nt + spans - 1) / spans;
+            d.key0 = min(d.nt, d.span * each) * kTileK;
+            d.nt = min(each, d.nt - d.key0 / kTileK);
+            d.nkeys = max(0, min(d.nkeys - d.key0, d.nt * kTileK));
+            d.last_key -= d.key0;
+        }
         return true;
     };
 
@@ -244,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             Item d;
             if (k >= num_items || !describe(k, d)) continue;
             const int kvh = d.kvh, nkeys = d.nkeys, nt = d.nt;
-            const int32_t* table = p.block_tables + (size_t)d.s * p.max_blocks_per_seq;
+            const int32_t* table = p.block_tables + (size_t)d.s * p.max_blocks_per_seq + (kLse ? d.key0 / B : 0);
             const int nblk = (nkeys + B - 1) / B;
             if (!v_side && nt > 0) {  // with no keys nothing is loaded (nor left in flight)
                 // the Q tile; its buffer is free once the previous item's last QK^T completed
@@ -444,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int kvh = d.kvh, r0 = d.r0, start = d.start, i0 = d.i0, nq = d.nq, last_key = d.last_key, nt = d.nt;
             const int pos = i0 + r / G;  // chunk-relative position
             const bool row_ok = pos - i0 < nq;
-            const int my_last = prefix_mode ? last_key : min(start + pos, last_key);  // last key this row may see
+            const int my_last = prefix_mode ? last_key : min(start + pos - d.key0, last_key);  // last key this row may see
             float m_run = -INFINITY, l_run = 0.f;
             for (int j = 0; j < nt; ++j) {
                 const int g = gt + j, st = g & 1;
@@ -627,7 +645,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f_b = m_b == -INFINITY ? 0.f : fast_exp2(m_b - m_row);
             const float l_row = f_a * l_a + f_b * l_b;
             const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
-            if (kLse && half == 0 && row_ok)
+            // (kLse) a span's rows go to part_o / part_ml, and their lse is the join's
+            const bool span_mode = kLse && spans > 1;
+            const size_t span_row = ((size_t)(d.span * p.num_kv_heads + kvh) * p.total_q + r0 + pos) * G + r % G;
+            if (span_mode && half == 0 && row_ok) p.part_ml[span_row] = make_float2(m_row, l_row);
+            if (kLse && !span_mode && half == 0 && row_ok)
                 p.lse[((size_t)kvh * p.total_q + r0 + pos) * G + r % G] = l_row == 0.f ? INFINITY : m_row + log2f(l_row);
             const float wa = f_a * inv, wb = f_b * inv;  // weights of O_a and O_b in this row's output
             // member sequence r0 + pos, head r % G of a cascade prefix pass: its partial (o, m, l) goes to
@@ -638,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t slot = ((size_t)sm * p.num_kv_heads + kvh) * p.part_splits * G + (r % G);
             if (prefix_mode && row_ok && half == 0)
                 p.part_ml[slot] = same ? make_float2(m_row, l_row) : make_float2(-INFINITY, 0.f);
-            __nv_bfloat16* out = prefix_mode ? nullptr
+            __nv_bfloat16* out = prefix_mode || span_mode ? nullptr
                                              : static_cast<__nv_bfloat16*>(p.out) +
                                                    ((size_t)(r0 + pos) * p.num_q_heads + (size_t)kvh * G + (r % G)) * kD +
                                                    col0;
@@ -659,9 +681,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!row_ok) continue;
                 // (the workspace partials are 256-byte aligned; the output takes 32-byte stores when its base
                 // allows, 16-byte ones otherwise)
-                if (prefix_mode) {
-                    float* po = p.part_o + slot * kD + col0 + q4 * 16;
-                    const float f = same ? 1.f : 0.f;
+                if (prefix_mode || span_mode) {
+                    float* po = p.part_o + (span_mode ? span_row : slot) * kD + col0 + q4 * 16;
+                    const float f = same || span_mode ? 1.f : 0.f;
 #pragma unroll
                     for (int h8 = 0; h8 < 2; ++h8) {
                         uint32_t w8[8];
@@ -737,7 +759,7 @@ static int launch(const PrefillParams& p, cudaStream_t stream) {
     // persistent: one CTA per SM (or per work item, if fewer), each walking its share of the items
     const int pos_per_tile = kTileQ / p.group;
     const long long items = (long long)((p.max_q_len + pos_per_tile - 1) / pos_per_tile) * p.num_chunks *
-                            p.num_kv_heads;
+                            p.num_kv_heads * (kLse ? p.spans : 1);
     if (items == 0) return PA_OK;
     int dev = 0, num_sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&num_sms, cudaDevAttrMultiProcessorCount, dev) !=
@@ -747,7 +769,68 @@ static int launch(const PrefillParams& p, cudaStream_t stream) {
     return launch_kernel(prefill_tc_kernel<kLse>, dim3(grid), dim3(kThreads), kSmemBytes, stream, tmq, tmk, tmv, p);
 }
 
+// The spans' partial rows joined, and their lse: a warp a (query, head).  Row = chunk row, the heads of a row together.
+static __global__ void __launch_bounds__(256) prefill_spans_join_kernel(const PrefillParams p) {
+    pdl_trigger();
+    pdl_wait();
+    WeightChunk d;
+    if (!weight_chunk(p, blockIdx.y, d)) return;
+    const int G = p.group, Hq = p.num_q_heads, lane = threadIdx.x & 31;
+    const long long rows = (long long)d.n * Hq, row0 = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row0 >= rows) return;
+    const int i = (int)(row0 / Hq), h = (int)(row0 - (long long)i * Hq), kvh = h / G;
+    const size_t stride = (size_t)p.num_kv_heads * p.total_q * G;
+    const size_t row = ((size_t)kvh * p.total_q + d.r0 + i) * G + (h - kvh * G);
+    float2 v[kMaxSpans / 32];
+    float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kMaxSpans / 32; ++k) {
+        const int e = lane + 32 * k;
+        v[k] = e < p.spans ? __ldcg(p.part_ml + e * stride + row) : make_float2(-INFINITY, 0.f);
+        if (v[k].y != 0.f) m = fmaxf(m, v[k].x);
+    }
+    m = warp_max(m);
+    float w[kMaxSpans / 32], sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxSpans / 32; ++k) {
+        w[k] = v[k].y != 0.f ? v[k].y * exp2f(v[k].x - m) : 0.f;  // (a NaN counts)
+        sum += w[k];
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) p.lse[row] = sum == 0.f ? INFINITY : m + log2f(sum);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    const float4* o = reinterpret_cast<const float4*>(p.part_o + row * kD) + lane;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    constexpr int kAhead = 8;
+    for (int e0 = 0; e0 < p.spans; e0 += kAhead) {
+        float4 x[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            if (e0 + k < p.spans) x[k] = __ldcg(o + (e0 + k) * stride * (kD / 4));
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int e = e0 + k;
+            const float f = __shfl_sync(0xffffffffu, e < 32 ? w[0] : w[1], e & 31) * inv;
+            if (e < p.spans) {
+                acc.x = fmaf(f, x[k].x, acc.x);
+                acc.y = fmaf(f, x[k].y, acc.y);
+                acc.z = fmaf(f, x[k].z, acc.z);
+                acc.w = fmaf(f, x[k].w, acc.w);
+            }
+        }
+    }
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + ((size_t)(d.r0 + i) * Hq + h) * kD + 4 * lane;
+    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+}
+
 int launch_prefill_tc(const PrefillParams& p, cudaStream_t stream) {
+    if (p.lse && p.spans > 1) {
+        const int rc = launch<true>(p, stream);
+        if (rc != PA_OK) return rc;
+        const long long rows = (long long)p.max_q_len * p.num_q_heads;
+        return launch_kernel(prefill_spans_join_kernel, dim3((unsigned)((rows + 7) / 8), p.num_chunks), dim3(256), 0, stream,
+                             p);
+    }
     return p.lse ? launch<true>(p, stream) : launch<false>(p, stream);
 }
 
