@@ -53,15 +53,15 @@ long long most_partials(int num_seqs, int num_q_heads, int num_kv_heads, int hea
 }
 
 // Spans that the keys of pa_prefill_chunk_weights's query tiles are cut into: as many as SMs that the tiles leave idle can
-// take, of two 128-key tiles at least; one where the tiles fill the GPU.  (37 queries over 3000 keys, 16 tiles: 54.1 us
-// with one span, 8 spans 27.)
+// take, of three 128-key tiles at least; one where the tiles fill the GPU.  (37 queries over 3000 keys, 16 tiles: 54.4 us
+// with one span, 35.5 with spans of two key tiles, 34.0 of three, 36.1 of four.)
 int spans_of(int num_chunks, int total_q, int max_q_len, int group, int num_kv_heads, int max_context_len, int num_sms) {
     const int per_tile = 128 / group;
     const long long tiles = (long long)num_chunks * num_kv_heads * ((max_q_len + per_tile - 1) / per_tile);
     const long long key_tiles = ((long long)max_context_len + 127) / 128;
     // (q may have rows behind its chunks; the workspace holds 128 rows for each SM)
     const long long fit = 128LL * num_sms / ((long long)total_q * group * num_kv_heads);
-    return (int)std::max(1LL, std::min({(long long)kMaxSpans, num_sms / std::max(1LL, tiles), key_tiles / 2, fit}));
+    return (int)std::max(1LL, std::min({(long long)kMaxSpans, num_sms / std::max(1LL, tiles), key_tiles / 3, fit}));
 }
 
 // Workspace of pa_prefill_chunk_weights: the rows' lse, what comes before each chunk, the keys' partial sums (rows of 256
