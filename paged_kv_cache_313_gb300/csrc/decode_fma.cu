@@ -31,12 +31,8 @@ __global__ void __launch_bounds__(kFmaThreads) decode_fma_kernel(DecodeParams p)
     const T* q = static_cast<const T*>(p.q) + ((size_t)s * p.num_q_heads + (size_t)kvh * G) * D;
     fma_attend<T, D>(q, G, static_cast<const T*>(p.k_cache), static_cast<const T*>(p.v_cache),
                      p.block_tables + (size_t)s * p.max_blocks_per_seq, p.block_size, p.num_kv_heads, kvh,
-                     p.num_blocks, j0, j1, p.scale_log2, p.error_count, smem, acc, m_s, l_s, alpha_s, nullptr, nullptr,
-                     p.ws_scores ? p.ws_scores + decode_unit(p, s, kvh) * p.score_width * G : nullptr);
+                     p.num_blocks, j0, j1, p.scale_log2, p.error_count, smem, acc, m_s, l_s, alpha_s);
 
-    if (p.ws_scores && threadIdx.x < G)
-        p.ws_ml[(decode_unit(p, s, kvh) * p.max_splits + split) * G + threadIdx.x] =
-            make_float2(m_s[threadIdx.x], l_s[threadIdx.x]);
     if (nsplit == 1) {
         T* out = static_cast<T*>(p.out) + ((size_t)s * p.num_q_heads + (size_t)kvh * G) * D;
 #pragma unroll

@@ -1,7 +1,7 @@
 // decode_weights.cu — the second launch of pa_decode_weights: the split-KV
 // combine, and the softmax weight of every key added to its accumulated weight.
 //
-// The decode kernel (decode_tc.cu, decode_fma.cu) has left each score x (base-2
+// The decode kernel (decode_tc.cu, decode_weights_fma.cu) has left each score x (base-2
 // units, -inf for a masked token) and each partition's (m, l) in the workspace.
 // With lse_g = m* + log2(sum_i l_i 2^(m_i - m*)) over a head's partitions,
 //     key_weights[s][kv head][j] += sum over the group's heads g of 2^(x_jg - lse_g)

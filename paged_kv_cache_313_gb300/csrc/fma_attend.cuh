@@ -44,15 +44,13 @@ struct FmaShape {
 // Attend q (G rows of D, storage type T) to tokens [j0, j1) of pools of TP (T itself, or e4m3_t with a scale per
 // (block, kv head): a token's K scale multiplies its scores, its V scale its weight).  On return (after
 // a __syncthreads) m_s[g], l_s[g] hold the softmax state and acc[it] the
-// unnormalised output of item threadIdx.x + it*kFmaThreads = g*D + d.  scores (may be nullptr) receives the base-2
-// score of head g and token j at j*G + g.
+// unnormalised output of item threadIdx.x + it*kFmaThreads = g*D + d.
 template <typename T, int D, typename TP = T>
 __device__ void fma_attend(const T* __restrict__ q, int G, const TP* __restrict__ kc, const TP* __restrict__ vc,
                            const int32_t* __restrict__ table, int block_size, int num_kv_heads, int kvh,
                            int num_blocks, int j0, int j1, float scale_log2, int32_t* error_count, float* smem,
                            float (&acc)[FmaShape<D>::kItems], float* m_s, float* l_s, float* alpha_s,
-                           const float* __restrict__ k_scales = nullptr, const float* __restrict__ v_scales = nullptr,
-                           float* __restrict__ scores = nullptr) {
+                           const float* __restrict__ k_scales = nullptr, const float* __restrict__ v_scales = nullptr) {
     constexpr bool kScaled = !std::is_same<T, TP>::value;
     using S = FmaShape<D>;
     constexpr int kPerLane = S::kPerLane;
@@ -120,11 +118,7 @@ __device__ void fma_attend(const T* __restrict__ q, int G, const TP* __restrict_
 #pragma unroll
                     for (int e = 0; e < kPerLane; ++e) part = fmaf(q_s[g * D + lane * kPerLane + e], kr[e], part);
                     part = warp_sum(part);
-                    if (lane == 0) {
-                        const float x = pb >= 0 ? part * to_log2 : -INFINITY;
-                        p_s[g * kFmaSub + p0 + t] = x;
-                        if (scores) scores[(size_t)j * G + g] = x;
-                    }
+                    if (lane == 0) p_s[g * kFmaSub + p0 + t] = pb >= 0 ? part * to_log2 : -INFINITY;
                 }
             }
         }

@@ -255,7 +255,7 @@ int pa_decode_weights(void* out, const void* q, int num_seqs, int num_q_heads, i
         rc = launch_decode_tc(p, num_sms, st);
     } else {
         p.small_from = 1 << 30;  // one CTA for each partition: uniform ones
-        rc = launch_decode_fma(p, dtype, st);
+        rc = launch_decode_weights_fma(p, dtype, st);
     }
     return rc != PA_OK ? rc : launch_decode_weights(p, dtype, st);
 }

@@ -307,7 +307,9 @@ int launch_decode_merge(const DecodeParams& p, int dtype, int num_sms, cudaStrea
 // The decode kernel for these parameters (tensor-core or FMA), then the
 // split-KV merge when there is more than one partition.
 int run_decode(const DecodeParams& p, int dtype, int num_sms, cudaStream_t stream);
-// After run_decode with ws_scores set: the merge of the partials, and the scores' softmax weights added to key_weights.
+// pa_decode_weights: the attention on the CUDA cores (on the tensor cores: launch_decode_tc with ws_scores set); then, after
+// either, the merge of the partials, and the scores' softmax weights added to key_weights.
+int launch_decode_weights_fma(const DecodeParams& p, int dtype, cudaStream_t stream);
 int launch_decode_weights(const DecodeParams& p, int dtype, cudaStream_t stream);
 // Prefill with lse, partial and key_weights set: the attention with its rows' lse, the keys' partial sums, their addition.
 int launch_prefill_weights_fma(const PrefillParams& p, int dtype, cudaStream_t stream);
