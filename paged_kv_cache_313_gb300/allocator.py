@@ -148,6 +148,34 @@ class BlockAllocator:
         self._seqs[sid] = _Seq(blocks=list(p.blocks), length=p.length)
         return sid
 
+    def make_private(self, seq: int) -> list:
+        """Give ``seq`` a copy of its own of every block that other sequences reference too (an eviction moves tokens
+        within a sequence's blocks).  Returns the copies the caller must perform, whole blocks but for the tail.  On
+        exhaustion raises NoBlocks and leaves every sequence unchanged."""
+        s = self._seqs[seq]
+        shared = [i for i, b in enumerate(s.blocks) if self.ref_cnt[b] > 1]
+        copies = []
+        for i, dst in zip(shared, self._take(len(shared))):
+            src = s.blocks[i]
+            copies.append(CowCopy(src=src, dst=dst, num_valid=min(self.block_size, s.length - i * self.block_size)))
+            self._release(src)
+            s.blocks[i] = dst
+        return copies
+
+    def truncate(self, seq: int, num_tokens: int) -> None:
+        """Shorten ``seq`` to its first ``num_tokens`` cached tokens, as an eviction does: blocks that hold none of them
+        lose this sequence's reference.  A length that is no shorter changes nothing."""
+        s = self._seqs[seq]
+        if num_tokens < 0:
+            raise ValueError("num_tokens must not be negative")
+        if num_tokens >= s.length:
+            return
+        keep = self.blocks_for(num_tokens)
+        for b in s.blocks[keep:]:
+            self._release(b)
+        del s.blocks[keep:]
+        s.length = int(num_tokens)
+
     def free(self, seq: int) -> None:
         """Finish ``seq``: drop one reference to each of its blocks."""
         s = self._seqs.pop(seq)

@@ -43,8 +43,12 @@ def _packed_views(buf, like):
 
 class DeviceStep:
     def __init__(self, w: Workload, device: str | torch.device = "cuda", with_error_count: bool = True,
-                 cascade: bool = True, fused_decode_write: bool = True):
+                 cascade: bool = True, fused_decode_write: bool = True, key_weights: bool = False):
         dev = torch.device(device)
+        # key_weights: decode and prefill accumulate the weight that each cached token draws, and evict() can cut the
+        # sequences down by it (bf16 and fp32 pools)
+        if key_weights and w.kv_fp8:
+            raise ValueError("key weights are accumulated over bf16 or fp32 pools")
         self.w = w
         self.device = dev
         up = lambda t: t.to(dev).contiguous()  # noqa: E731
@@ -91,7 +95,11 @@ class DeviceStep:
         newest = bool(nd) and torch.equal(w.seq_idx[:nd], torch.arange(nd, dtype=w.seq_idx.dtype)) and \
             torch.equal(w.pos[:nd], w.context_lens[:nd].to(w.pos.dtype) - 1)
         dims = (128,) if w.kv_fp8 else (64, 128)  # e4m3 pools: the decode kernel takes head_dim 128
-        self.fused_decode_write = bool(fused_decode_write and newest and not self.use_cascade
+        self.track_weights = bool(key_weights)
+        if self.track_weights:
+            self.use_cascade, self.cascade_workspace = False, None
+            self._init_key_state(dev)
+        self.fused_decode_write = bool(fused_decode_write and newest and not self.use_cascade and not self.track_weights
                                        and not self.block_scales and w.dtype == torch.bfloat16 and w.head_dim in dims and G <= 8
                                        and w.block_size in (8, 16, 32, 64))
         if self.block_scales:
@@ -103,6 +111,38 @@ class DeviceStep:
         n = pa.pa_prefill_workspace_size(w.num_chunks, w.max_q_len, w.num_q_heads, w.num_kv_heads, w.head_dim,
                                          w.block_size) if w.num_chunks else 0
         self.prefill_workspace = torch.zeros(max(n, 1), dtype=torch.uint8, device=dev) if n else None
+
+    # eviction -------------------------------------------------------------
+    def _init_key_state(self, dev):
+        w, n = self.w, self.w.block_tables.shape[0]
+        self.max_any_context = int(w.context_lens.max()) if n else 0
+        shape = (n, w.num_kv_heads, max(1, self.max_any_context))
+        self.key_weights = torch.zeros(shape, dtype=torch.float32, device=dev)
+        self.key_pos = torch.arange(shape[2], dtype=torch.int32, device=dev).expand(shape).contiguous()
+        self.next_pos = self.context_lens.clone()
+        self._no_q = torch.empty(w.seq_idx.numel(), 0, w.head_dim, dtype=w.dtype, device=dev)
+        self._no_freq = torch.empty(0, dtype=torch.float32, device=dev)
+        sizes = (w.num_q_heads, w.num_kv_heads, w.head_dim, w.block_size)
+        nd = w.num_decode
+        self.workspace = pa.new_decode_weights_workspace(nd, *sizes, self.max_context_len, device=dev) if nd else None
+        self.prefill_weights_workspace = pa.new_prefill_weights_workspace(
+            w.num_chunks, int(w.cu_q_lens[-1]), w.max_q_len, *sizes, self.max_any_context,
+            device=dev) if w.num_chunks else None
+
+    def evict(self, budget: int, keep_first: int = 0, keep_recent: int = 0, stream=None):
+        """Cut every sequence of more than `budget` tokens down to the `budget` that have drawn the most weight (its first
+        keep_first and last keep_recent tokens stay in any case); context_lens follows on the device.  The sequences'
+        blocks must be their own."""
+        if not self.track_weights:
+            raise ValueError("evict() needs DeviceStep(key_weights=True)")
+        if getattr(self, "evict_budget", None) != budget:
+            self.evict_workspace = pa.new_evict_workspace(self.w.block_tables.shape[0], self.w.num_kv_heads,
+                                                          self.max_any_context, budget, device=self.device)
+            self.evict_budget = budget
+        return pa.pa_evict_tokens(self.k_cache, self.v_cache, self.block_tables, self.context_lens, self.max_any_context,
+                                  self.key_weights, self.key_pos, self.next_pos, budget, keep_first, keep_recent,
+                                  self.evict_workspace, new_lens=self.context_lens, error_count=self.error_count,
+                                  stream=stream)
 
     # individual stages --------------------------------------------------
     def slot_mapping(self, stream=None):
@@ -116,6 +156,12 @@ class DeviceStep:
 
     def write_kv_paged(self, stream=None):
         """Slot mapping and K/V write in one call (the slots are still recorded)."""
+        if self.track_weights:  # the new tokens begin without weight, at their places
+            pa.pa_rope_write_kv_paged(self._no_q, self.k_new, self.v_new, self.pos, self._no_freq, None, self.k_cache,
+                                      self.v_cache, self.block_tables, self.seq_idx, self.pos,
+                                      key_weights=self.key_weights, key_pos=self.key_pos, slot_mapping=self.slots,
+                                      error_count=self.error_count, stream=stream)
+            return
         if self.block_scales:
             pa.pa_write_kv_paged_fp8_block(self.k_new, self.v_new, self.k_cache, self.v_cache, self.k_scales,
                                            self.v_scales, self.block_tables, self.seq_idx, self.pos,
@@ -135,6 +181,10 @@ class DeviceStep:
         if not w.num_decode:
             return self.out_decode
         nd = w.num_decode
+        if self.track_weights:
+            return pa.pa_decode_weights(self.q_decode, self.k_cache, self.v_cache, self.block_tables[:nd],
+                                        self.context_lens[:nd], self.max_context_len, w.scale, self.key_weights[:nd],
+                                        self.workspace, out=self.out_decode, error_count=self.error_count, stream=stream)
         if self.block_scales:
             return pa.pa_decode_fp8_block(self.q_decode, self.k_cache, self.v_cache, self.k_scales, self.v_scales,
                                           self.block_tables[:nd], self.context_lens[:nd], self.max_context_len,
@@ -158,6 +208,12 @@ class DeviceStep:
         w = self.w
         if not w.num_chunks:
             return self.out_prefill
+        if self.track_weights:
+            return pa.pa_prefill_chunk_weights(self.q_prefill, self.cu_q_lens, self.q_start_pos, self.seq_of_chunk,
+                                               w.max_q_len, self.k_cache, self.v_cache, self.block_tables,
+                                               self.context_lens, self.max_any_context, w.scale, self.key_weights,
+                                               self.prefill_weights_workspace, out=self.out_prefill,
+                                               error_count=self.error_count, stream=stream)
         if self.block_scales:
             return pa.pa_prefill_chunk_fp8_block(self.q_prefill, self.cu_q_lens, self.q_start_pos, self.seq_of_chunk,
                                                  w.max_q_len, self.k_cache, self.v_cache, self.k_scales,
