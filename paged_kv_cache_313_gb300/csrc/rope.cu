@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeParams p, c
         const T* row = h < Hq ? static_cast<const T*>(p.q) + t * p.q_stride + (long long)h * D
                               : static_cast<const T*>(p.k) + t * p.k_stride + (long long)(h - Hq) * D;
         const uint4* src = reinterpret_cast<const uint4*>(row) + chunk0;
-        a = src[0];
-        b = src[apart];
+        a = __ldcs(src);
+        b = __ldcs(src + apart);
     };
     // the first heads' loads, then the look-ups' first loads, then what follows from those
     uint4 a[kBatch], b[kBatch];
@@ -171,8 +171,8 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeParams p, c
         T* row = h < Hq ? static_cast<T*>(p.q_out) + (t * Hq + h) * D
                         : static_cast<T*>(p.k_out) + (slot * Hkv + (h - Hq)) * D;
         uint4* dst = reinterpret_cast<uint4*>(row) + chunk0;
-        dst[0] = a;
-        dst[apart] = b;
+        __stcs(dst, a);
+        __stcs(dst + apart, b);
     };
     for (int h = h0; h < heads; h += kBatch * step) {
         if (h != h0)
@@ -189,12 +189,12 @@ __global__ void __launch_bounds__(kWarps * 32) rope_kernel(const RopeParams p, c
             uint4 v[kBatch];
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
-                if (i0 + k * 32 * parts < n) v[k] = *src_of(i0 + k * 32 * parts);
+                if (i0 + k * 32 * parts < n) v[k] = __ldcs(src_of(i0 + k * 32 * parts));
 #pragma unroll
             for (int k = 0; k < kBatch; ++k)
                 if (i0 + k * 32 * parts < n) {
                     uint4* dst = dst_of(i0 + k * 32 * parts);
-                    if (dst) *dst = v[k];
+                    if (dst) __stcs(dst, v[k]);
                 }
         }
     };
