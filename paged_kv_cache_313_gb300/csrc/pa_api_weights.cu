@@ -30,7 +30,7 @@ int rope_ok(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int
 // batch size and each partition of the plan's halvings the most rows are those of the longest context for which the plan
 // stops there: the next longer partition must give fewer than two items per SM.
 long long most_partials(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_context_len, int num_sms) {
-    long long most = 1;
+    long long most = std::max(1LL, (long long)num_seqs * num_kv_heads);  // one each, with no token too
     for (long long n = 1; n <= num_seqs; ++n) {
         // the plan at these lengths, where its partition changes: the longest context that has it
         long long ctx = max_context_len;
