@@ -531,7 +531,7 @@ PA_API int pa_rope(void* q_out, void* k_out, const void* q, const void* k, int n
  * token whose slot is invalid is turned all the same.  With key_weights and
  * key_pos (both or neither), the written token's weight becomes 0 and its place
  * token_pos[t] (token_pos NULL: pos[t]) for every kv head; pos[t] >= key_width is then
- * an invalid index.  rot_dim 0 turns nothing.  num_q_heads may be 0.  Slots must
+ * an invalid index (and pos[t] >= 2^30 always is).  rot_dim 0 turns nothing.  num_q_heads may be 0.  Slots must
  * be distinct.
  */
 PA_API int pa_rope_write_kv_paged(void* q_out, const void* q, const void* k_new, const void* v_new, int num_tokens,
@@ -556,7 +556,8 @@ PA_API int pa_rope_write_kv_paged(void* q_out, const void* q, const void* k_new,
  * sequences and no longer contexts as well; it holds every score, 4 bytes for each
  * query head and token), 256-byte aligned, zeroed once.  One workspace must not
  * serve two calls that may overlap on the GPU.  A query with a NaN makes the
- * weights of its sequence's keys NaN.
+ * weights of its sequence's keys NaN.  The pools must be 16-byte aligned, else
+ * PA_ERR_UNSUPPORTED.
  */
 PA_API size_t pa_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                                int block_size, int max_context_len);
@@ -576,7 +577,9 @@ PA_API int pa_decode_weights(void* out, const void* q, int num_seqs, int num_q_h
  * zeroing, and serves every call of no more chunks, queries and context as well.
  * One workspace must not serve two calls that may overlap on the GPU.  q and the
  * pools 16-byte aligned, else PA_ERR_UNSUPPORTED; other shapes as for
- * pa_prefill_chunk.
+ * pa_prefill_chunk.  bf16 of head_dim 128 in blocks of 8 to 128 runs on the tensor
+ * cores, any group of up to 16 query heads.  An infinity or a NaN in V stays with the queries that see its token
+ * (in its column; where the tensor cores run, it may be NaN for them instead of the infinity).
  */
 PA_API size_t pa_prefill_weights_workspace_size(int num_chunks, int total_q, int max_q_len, int num_q_heads,
                                                 int num_kv_heads, int head_dim, int block_size, int max_context_len);

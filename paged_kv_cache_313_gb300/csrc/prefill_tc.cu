@@ -81,8 +81,13 @@ constexpr int kBars = kV + kVStages * kTileBytes;
 constexpr int kNumBars = 1 + 2 * kKStages + 2 * kVStages + 2 + 2 + 2 + kMaskSlots + 3;
 constexpr int kMask = kBars + kNumBars * 8;  // uint32 [8][4]: key-validity mask of tile j in slot j%8
 constexpr int kTmemSlot = kMask + kMaskSlots * 4 * 4;
-constexpr size_t kSmemBytes = 1024 + kTmemSlot + 16;
-static_assert(kSmemBytes <= 227 * 1024, "shared memory per CTA");
+// (kLse) the first key, by column, whose V is an infinity or NaN in a tile of which not every row sees every key, and the
+// first of any column; three items' worth, one reset two items before its next use
+constexpr int kNan = kTmemSlot + 16;
+constexpr int kNanSlots = 3, kNanInts = kD + 1;
+constexpr size_t kSmemBytes = 1024 + kNan;
+constexpr size_t kSmemBytesLse = kSmemBytes + kNanSlots * kNanInts * 4;
+static_assert(kSmemBytesLse <= 227 * 1024, "shared memory per CTA");
 
 // Dense tiles exponentiate in bf16 pairs (one instruction per two keys; P is
 // rounded to bf16 for its MMA either way, the pair form also rounds x - m).
@@ -228,6 +233,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_init(bars.mma_drain(), 1);
         fence_mbar_init();
     }
+    int* nan_s = reinterpret_cast<int*>(smem + kNan);
+    if (kLse)
+        for (int i = threadIdx.x; i < kNanSlots * kNanInts; i += kThreads) nan_s[i] = 0x7FFFFFFF;
     if (warp == 1) {
         tmem_alloc(tmem_slot, kTmemCols);
         tmem_relinquish();
@@ -457,6 +465,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float sl2 = p.scale_log2;
         const bool out_al32 = (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
         int gt = 0;  // key tiles taken so far
+        int items_seen = 0;  // (kLse) items with keys
         for (int c = 0; c * (int)gridDim.x < num_items; ++c) {
             const int k = item_of(c);
             Item d;
@@ -466,6 +475,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool row_ok = pos - i0 < nq;
             const int my_last = prefix_mode ? last_key : min(start + pos - d.key0, last_key);  // last key this row may see
             float m_run = -INFINITY, l_run = 0.f;
+            // (kLse) this item's record of V that is no number.  The one that is reset here belongs to the next item; its last
+            // reader was two items ago, before the barrier of the last item's epilogue.
+            int* nan = nan_s + (kLse ? items_seen % kNanSlots * kNanInts : 0);
+            const int all_see = min(start + i0 - d.key0, last_key);  // the last key that every row sees
+            if (kLse && nt > 0) {
+                int* next = nan_s + (items_seen + 1) % kNanSlots * kNanInts;
+                for (int i = threadIdx.x - 64; i < kNanInts; i += 256) next[i] = 0x7FFFFFFF;
+                ++items_seen;
+            }
             for (int j = 0; j < nt; ++j) {
                 const int g = gt + j, st = g & 1;
                 // validity of the tile's 128 keys (inside the context, in a block with a valid table
@@ -625,7 +643,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int c8 = 0; c8 < 8; ++c8) *reinterpret_cast<uint4*>(vrow + h * kHalf + r * 128 + c8 * 16) = z;
                 }
-                if (need_zero) fence_proxy_async_smem();  // the zeroed rows before the PV MMA reads them
+                // (kLse) an infinity or NaN of V would reach every row through P = 0: in a tile of which not every row sees
+                // every key it is cleared, and the rows that see its key store NaN in its column.  This thread looks at
+                // its half of key r's V.
+                bool cleared = false;
+                if (kLse && __builtin_expect(j * kTileK + kTileK - 1 > all_see, 0)) {
+                    if (!need_zero && ok && !mbar_wait(bars.v_full(vs), (g / kVStages) & 1)) ok = false;
+                    if (ok && ((vm[r >> 5] >> (r & 31)) & 1u)) {
+                        uint4* vrow = reinterpret_cast<uint4*>(smem + kV + vs * kTileBytes + half * kHalf + r * 128);
+                        uint32_t found = 0;
+#pragma unroll
+                        for (int c8 = 0; c8 < 8; ++c8) {
+                            const uint4 v = vrow[c8 ^ (r & 7)];  // (eight lanes on different banks)
+                            found |= ((v.x & 0x7F807F80u) + 0x00800080u) | ((v.y & 0x7F807F80u) + 0x00800080u) |
+                                     ((v.z & 0x7F807F80u) + 0x00800080u) | ((v.w & 0x7F807F80u) + 0x00800080u);
+                        }
+                        if (found & 0x80008000u) {  // (an exponent of ones carries into the sign's place)
+                            cleared = true;
+                            uint16_t* e = reinterpret_cast<uint16_t*>(vrow);
+#pragma unroll 1
+                            for (int i = 0; i < 64; ++i) {
+                                if ((e[i] & 0x7F80u) != 0x7F80u) continue;
+                                e[i] = 0;
+                                // 16-byte piece c of row r lies at piece c ^ (r & 7)
+                                const int column = half * 64 + (((i >> 3) ^ (r & 7)) << 3) + (i & 7);
+                                atomicMin(nan + column, j * kTileK + r);
+                                atomicMin(nan + kD, j * kTileK + r);
+                            }
+                        }
+                    }
+                }
+                if (need_zero || cleared) fence_proxy_async_smem();  // the changed rows before the PV MMA reads them
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0 && ok) mbar_arrive(bars.p_full(st));
@@ -677,6 +725,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                              : static_cast<__nv_bfloat16*>(p.out) +
                                                    ((size_t)(r0 + pos) * p.num_q_heads + (size_t)kvh * G + (r % G)) * kD +
                                                    col0;
+            const bool bad_values = kLse && nt > 0 && nan[kD] <= my_last;
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4) {  // my 64 output columns, 16 at a time
                 float t[16];
@@ -692,6 +741,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     for (int i = 0; i < 16; ++i) t[i] = 0.f;
                 }
                 if (!row_ok) continue;
+                if (kLse && bad_values) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (nan[col0 + q4 * 16 + i] <= my_last) t[i] = NAN;
+                }
                 // (the workspace partials are 256-byte aligned; the output takes 32-byte stores when its base
                 // allows, 16-byte ones otherwise)
                 if (prefix_mode || span_mode) {
@@ -750,6 +804,7 @@ bool prefill_tc_supported(const PrefillParams& p, int dtype) {
 
 template <bool kLse>
 static int launch(const PrefillParams& p, cudaStream_t stream) {
+    constexpr size_t kSmem = kLse ? kSmemBytesLse : kSmemBytes;
     CUtensorMap tmq, tmk, tmv;
     {
         auto enc = tensor_map_encoder();
@@ -768,7 +823,7 @@ static int launch(const PrefillParams& p, cudaStream_t stream) {
     int rc = pool_tensor_map(&tmk, p.k_cache, p.num_blocks, p.block_size, p.num_kv_heads, kD);
     if (rc != PA_OK) return rc;
     if ((rc = pool_tensor_map(&tmv, p.v_cache, p.num_blocks, p.block_size, p.num_kv_heads, kD)) != PA_OK) return rc;
-    if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(prefill_tc_kernel<kLse>), kSmemBytes)) != PA_OK) return rc;
+    if ((rc = ensure_dynamic_smem(reinterpret_cast<const void*>(prefill_tc_kernel<kLse>), kSmem)) != PA_OK) return rc;
     // persistent: one CTA per SM (or per work item, if fewer), each walking its share of the items
     const int pos_per_tile = kTileQ / p.group;
     const long long items = (long long)((p.max_q_len + pos_per_tile - 1) / pos_per_tile) * p.num_chunks *
@@ -779,7 +834,7 @@ static int launch(const PrefillParams& p, cudaStream_t stream) {
                                                   cudaSuccess)
         return check_launch();
     const int grid = (int)(items < num_sms ? items : num_sms);
-    return launch_kernel(prefill_tc_kernel<kLse>, dim3(grid), dim3(kThreads), kSmemBytes, stream, tmq, tmk, tmv, p);
+    return launch_kernel(prefill_tc_kernel<kLse>, dim3(grid), dim3(kThreads), kSmem, stream, tmq, tmk, tmv, p);
 }
 
 // The spans' partial rows joined, and their lse: a warp a (query, head).  Row = chunk row, the heads of a row together.

@@ -209,3 +209,33 @@ def test_rope_no_heads_of_one_kind():
     empty = torch.empty(0, 3, 128, device="cuda")
     q, k = pa.pa_rope(empty, empty, _i32(np.zeros(0)), freq)
     assert q.shape == empty.shape
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", [(BF16, 128, 4, 1, 16, [(0, 0, 90)], ()), (BF16, 128, 8, 2, 32, [(0, 60, 140), (1, 3, 200)], ()),
+                                  (BF16, 128, 3, 1, 8, [(0, 500, 9)], ()), (F32, 64, 2, 1, 16, [(0, 10, 70)], ())],
+                         ids=["one", "two", "spans", "f32"])
+def test_prefill_values_that_are_no_numbers_stay_with_the_queries_that_see_them(case):
+    """NaN and infinities among V, next to the diagonal: queries before their keys are as if they were not there."""
+    dtype, D, Hq, Hkv, B, chunks, _ = case
+    lens, k, v, table, q, before, cu, scale = _prefill_case(case)
+    bad = {}  # (sequence, key) -> column
+    for s, st, n in chunks:
+        for key, col, x in ((st + n // 2, 5, np.nan), (st + n // 2 + 1, D - 3, np.inf), (st + n - 1, 40, -np.inf)):
+            v[table[s, key // B], key % B, Hkv - 1, col] = float(x)
+            bad.setdefault((s, Hkv - 1), []).append((key, col))
+    weights = torch.tensor(before).cuda()
+    out = pa.pa_prefill_chunk_weights(*_prefill_args(case, lens, q, k, v, table, cu, scale), weights,
+                                      _prefill_ws(case, lens, q)).double().cpu().numpy()
+    clean = torch.where(torch.isfinite(v), v, torch.zeros_like(v))
+    want, mag, add, rel = _prefill_want(case, lens, q, k, clean, table, cu, scale, before.shape[2])
+    g = Hq // Hkv
+    sees = np.zeros(out.shape, bool)
+    for c, (s, st, n) in enumerate(chunks):
+        for (s2, h), items in bad.items():
+            if s2 == s:
+                for key, col in items:
+                    sees[cu[c] + max(0, key - st):cu[c + 1], h * g:(h + 1) * g, col] = True
+    assert np.isfinite(out[~sees]).all() and not np.isfinite(out[sees]).any() and sees.any()
+    _check_out(torch.tensor(np.where(sees, 0, out)), np.where(sees, 0, want), mag, rel, dtype)
+    _check_weights(weights, before, add, rel, q.shape[0] * g)
