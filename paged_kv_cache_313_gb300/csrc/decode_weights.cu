@@ -12,6 +12,12 @@
 // loaded all at once, before the first of it is used: bound by the latency of the
 // scores, which lie in L2.  An element of key_weights has one owner: no atomics, and
 // the sums' order is fixed.
+//
+// 64 sequences (60,000 tokens, 32/8 heads): 52.4 us with the decode kernel, 46.6 without
+// the scores and this launch; 16 contexts of 1k to 32k (190,000 tokens, 64/8 heads): 155 us,
+// 126 without (48 MB of scores written and read).  Loading scores as they are used took
+// 60.1 and 170; 2048 tokens a CTA 165, 512 tokens 160; persistent CTAs that pass over the
+// items of shorter contexts 168 to 233.
 #include "decode_common.cuh"
 
 namespace pa {

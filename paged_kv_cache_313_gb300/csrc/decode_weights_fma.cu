@@ -9,6 +9,11 @@
 // P V: a thread four columns and a share of the tile's tokens, its share of the output
 // in registers until the partition ends.  Scores go to the workspace and every
 // partition's (m, l) too; decode_weights.cu does the rest.
+//
+// 64 fp32 sequences (18,000 tokens, 32/8 heads): 96 us, 1.5 TB/s; four of 1 to 40 tokens 7.1 us
+// with both launches.  The CUDA-core decode kernel with the scores added (a warp a token, 64-token
+// pieces one after the other) took 498 and 19.0, and 1054 instead of 166 with 16 bf16 heads a kv
+// head.
 #include "decode_common.cuh"
 
 namespace pa {
