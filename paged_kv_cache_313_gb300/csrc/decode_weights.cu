@@ -17,7 +17,7 @@
 // the scores and this launch; 16 contexts of 1k to 32k (190,000 tokens, 64/8 heads): 155 us,
 // 126 without (48 MB of scores written and read).  Loading scores as they are used took
 // 60.1 and 170; 2048 tokens a CTA 165, 512 tokens 160; persistent CTAs that pass over the
-// items of shorter contexts 168 to 233.
+// items of shorter contexts 168 to 233 (two to six an SM; their registers spilled).
 #include "decode_common.cuh"
 
 namespace pa {

@@ -17,9 +17,9 @@
 // weights and places.  Where there can be few moves (a cache kept near its budget),
 // select_kernel makes them itself.
 //
-// 64 sequences of 2064 tokens, 8 heads, cut to 2048: 13.0 us (one launch; bound by the chain of
+// 64 sequences of 2064 tokens, 8 heads, cut to 2048: 14.3 us (one launch; bound by the chain of
 // its barriers and look-ups, 17 MB would take 2.5).  16 prompts of 1k to 32k tokens cut to 4096:
-// about 48 us, half of it the selection of the longest, half the moves of 138 MB (5.3 TB/s).
+// 47 to 52 us (with cold caches 25 the selection, which the longest context bounds, and 25 the moves).
 #include "pa_internal.cuh"
 
 namespace pa {

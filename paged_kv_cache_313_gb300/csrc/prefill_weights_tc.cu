@@ -10,10 +10,10 @@
 // the time of the products.)  Bound by the tensor cores (half the attention's products),
 // shared memory (a 128 x 256 x 16 product reads 12 KB in 128 cycles, and the query tiles'
 // copies write) and the exponentials alike: 2048 queries at 5900, 64/8 heads, 235 GFLOP,
-// 190 us = 1.24 PFLOP/s = 0.63 of the bf16 peak; the products alone take 127.  Steps, us:
-// a key a row 276; a query row a row 253; the rows' lse loaded a tile ahead 223; four chunks
-// of scores with the next one's load on its way 211; dense and masked tiles in loops of
-// their own 195.
+// 192 us = 1.23 PFLOP/s = 0.63 of the bf16 peak (without the exponentials and sums 127).
+// A key a row took 276, this layout 253 at first, 223 with the rows' lse loaded a tile ahead
+// and not touched before its use, 201 with dense and masked tiles in loops apart, 195 with the
+// choice between them made without a vote.
 //
 // A run is a pair of 128-key tiles of one (chunk, kv head) against the 128-row query
 // tiles (positions times the G heads of the kv head) that see a key of it, in order.

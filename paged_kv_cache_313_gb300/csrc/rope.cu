@@ -20,11 +20,11 @@
 // per token (or per part of its heads, where tokens are few), a lane always on the
 // same pairs, so that their angles stay in its registers: each is worked out by one
 // lane and handed round once, and a head costs a lane two loads, its products and two
-// stores.  (A CTA a token with the angles in shared memory spent 3200 warp instructions
-// a token, and took 61.5 us for the write of 8448 tokens of 32/8 heads; this takes 41.4,
-// and 35.8 = 5.8 TB/s = 0.86 of the copy bandwidth with streaming loads and stores.  Four
-// prompts of 2047 tokens without the write: 28.3 us = 5.9 TB/s; a step of 64 tokens: 2.5
-// and 3.4 us in a stream of such calls, the launch's time.)  rope_any_kernel, for the other
+// stores.  (A CTA a token with the angles in shared memory spent about 3200 warp
+// instructions a token, and took 66.9 us for the write of 8448 tokens of 32/8 heads; this
+// takes 41.4, and 35.8 to 36.1 = 5.8 TB/s = 0.86 of the copy bandwidth with streaming loads and stores.  Four
+// prompts of 2047 tokens without the write: 28.3 us = 5.9 TB/s; a step of 64 tokens: 2.6
+// and 3.7 us in a stream of such calls, the launch's time.)  rope_any_kernel, for the other
 // shapes: a CTA per token, the angles in shared memory.
 #include <algorithm>
 
