@@ -601,7 +601,7 @@ PA_API int pa_prefill_chunk_weights(void* out, const void* q, const int32_t* cu_
  * indices >= budget move, in ascending order, to the indices < budget that are no longer
  * taken, in ascending order: their rows of K and V, their weights and their places.
  * Nothing else changes; what lies at indices >= budget stays there, unused.
- * new_lens[s] = min(L, budget) (new_lens may be context_lens itself).  The blocks
+ * new_lens[s] = min(L, budget) (new_lens may be context_lens or next_pos itself).  The blocks
  * beyond the budget may then be freed, and the sequence goes on at index budget.
  *   key_weights, key_pos  read and written
  *   next_pos, context_lens, new_lens  int32 [num_seqs]; context_lens above max_context_len or

@@ -318,12 +318,16 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictParams p)
     move_rows(p, list, n, kMoveThreads);
 }
 
-// new_lens after select_kernel, where it is context_lens itself, which every CTA of that kernel reads.
+// new_lens after select_kernel, where it lies in context_lens or next_pos, which every CTA of that kernel reads.
 __global__ void lens_kernel(const EvictParams p) {
     pdl_trigger();
     pdl_wait();
     const int s = blockIdx.x * blockDim.x + threadIdx.x;
     if (s < p.num_seqs) p.new_lens[s] = p.lens[s];
+}
+
+bool overlap(const int32_t* a, const int32_t* b, int n) {
+    return (uintptr_t)a < (uintptr_t)(b + n) && (uintptr_t)b < (uintptr_t)(a + n);
 }
 
 }  // namespace
@@ -352,7 +356,7 @@ int launch_evict(const EvictParams& params, int row_bytes, cudaStream_t stream) 
     if (rc != PA_OK) return rc;
     const int pairs = p.num_seqs * p.num_kv_heads;
     const dim3 block(p.max_context_len > 16384 ? 1024 : p.max_context_len > 4096 ? 512 : 256);
-    const bool own = p.max_moves <= kOwnMoves, aliased = p.new_lens == p.context_lens;
+    const bool own = p.max_moves <= kOwnMoves, aliased = overlap(p.new_lens, p.context_lens, p.num_seqs) || overlap(p.new_lens, p.next_pos, p.num_seqs);
     if (own && !aliased) p.lens = p.new_lens;
     rc = own ? launch_kernel(select_kernel<true>, dim3(pairs), block, smem, stream, p, held)
              : launch_kernel(select_kernel<false>, dim3(pairs), block, smem, stream, p, held);

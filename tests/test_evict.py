@@ -147,6 +147,22 @@ def test_evict_lengths_in_place_stream_and_graph():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("case", CASES[:2], ids=["few-moves", "moves"])
+def test_evict_lengths_over_the_next_places(case):
+    """next_pos given for new_lens: every head of a sequence sees the places from before the call."""
+    state = _case(case)
+    dev, want = _run(case, *state)
+    again = dict(k=state[0].cuda(), v=state[1].cuda(), w=torch.tensor(state[3]).cuda(), p=_i32(state[4]))
+    nxt = _i32(state[5])
+    ws = pa.new_evict_workspace(len(case[4]), case[1], max(case[4]), case[5])
+    got = pa.pa_evict_tokens(again["k"], again["v"], _i32(state[2]), _i32(case[4]), max(case[4]), again["w"], again["p"], nxt,
+                             case[5], case[6], case[7], ws, new_lens=nxt)
+    torch.cuda.synchronize()
+    assert got is nxt and torch.equal(got, want)
+    _check(case, again, got, *state)
+
+
+@pytest.mark.gpu
 def test_evict_bad_blocks_and_lengths_are_counted():
     case = (BF16, 1, 64, 16, [200, 90], 64, 0, 0, "random")
     k, v, table, w, places, nxt = _case(case)
