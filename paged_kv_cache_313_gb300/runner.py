@@ -120,6 +120,7 @@ class DeviceStep:
         self.key_weights = torch.zeros(shape, dtype=torch.float32, device=dev)
         self.key_pos = torch.arange(shape[2], dtype=torch.int32, device=dev).expand(shape).contiguous()
         self.next_pos = self.context_lens.clone()
+        self.evict_workspaces = {}  # by budget
         self._no_q = torch.empty(w.seq_idx.numel(), 0, w.head_dim, dtype=w.dtype, device=dev)
         self._no_freq = torch.empty(0, dtype=torch.float32, device=dev)
         sizes = (w.num_q_heads, w.num_kv_heads, w.head_dim, w.block_size)
@@ -135,13 +136,12 @@ class DeviceStep:
         blocks must be their own."""
         if not self.track_weights:
             raise ValueError("evict() needs DeviceStep(key_weights=True)")
-        if getattr(self, "evict_budget", None) != budget:
-            self.evict_workspace = pa.new_evict_workspace(self.w.block_tables.shape[0], self.w.num_kv_heads,
-                                                          self.max_any_context, budget, device=self.device)
-            self.evict_budget = budget
+        if budget not in self.evict_workspaces:  # (kept: a captured eviction goes on using its own)
+            self.evict_workspaces[budget] = pa.new_evict_workspace(self.w.block_tables.shape[0], self.w.num_kv_heads,
+                                                                   self.max_any_context, budget, device=self.device)
         return pa.pa_evict_tokens(self.k_cache, self.v_cache, self.block_tables, self.context_lens, self.max_any_context,
                                   self.key_weights, self.key_pos, self.next_pos, budget, keep_first, keep_recent,
-                                  self.evict_workspace, new_lens=self.context_lens, error_count=self.error_count,
+                                  self.evict_workspaces[budget], new_lens=self.context_lens, error_count=self.error_count,
                                   stream=stream)
 
     # individual stages --------------------------------------------------

@@ -146,6 +146,21 @@ def test_device_step_with_key_weights_captured():
     assert torch.equal(st.key_weights, once) and st.errors() == 0
 
 
+def test_evictions_to_several_budgets_keep_their_workspaces(monkeypatch):
+    """A workspace that a captured eviction may still use is not given up for another budget's."""
+    st = DeviceStep.__new__(DeviceStep)
+    st.__dict__.update(track_weights=True, w=W.tiny_fp32(3), max_any_context=40, device="cpu", evict_workspaces={}, k_cache=None,
+                       v_cache=None, block_tables=None, context_lens=None, key_weights=None, key_pos=None, next_pos=None,
+                       error_count=None)
+    made, used = [], []
+    monkeypatch.setattr("paged_kv_cache_313_gb300.pa.new_evict_workspace", lambda *a, **kw: made.append(torch.zeros(4)) or made[-1])
+    monkeypatch.setattr("paged_kv_cache_313_gb300.pa.pa_evict_tokens", lambda *a, **kw: used.append(a[11]))
+    for budget in (8, 16, 8):
+        st.evict(budget)
+    assert len(made) == 2 and used[0] is used[2] is made[0] and used[1] is made[1]
+    assert any(t is made[0] for t in st.evict_workspaces.values())
+
+
 def test_evict_needs_key_weights():
     class Without(DeviceStep):
         def __init__(self):
