@@ -302,7 +302,7 @@ int pa_prefill_chunk_weights(void* out, const void* q, const int32_t* cu_q_lens,
     p.error_count = error_count;
     p.num_chunks = num_chunks;
     p.total_q = total_q;
-    p.max_q_len = max_q_len;
+    p.max_q_len = max_q_len = std::min(max_q_len, total_q);  // (no usable chunk is longer)
     p.num_seqs = num_seqs;
     p.num_q_heads = num_q_heads;
     p.num_kv_heads = num_kv_heads;

@@ -333,6 +333,23 @@ def test_prefill_weights_bad_chunks_are_counted_and_left():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("case", [PREFILLS[1], PREFILLS[3], PREFILLS[10]], ids=["tail", "chunks", "f32"])
+def test_prefill_weights_loose_bound_of_the_chunks(case):
+    """max_q_len far above every chunk, up to the largest int: the same work."""
+    lens, k, v, table, q, before, cu, scale = _prefill_case(case)
+    args = list(_prefill_args(case, lens, q, k, v, table, cu, scale))
+    got = []
+    for longest in (q.shape[0], 2 ** 31 - 1):
+        args[4] = longest
+        weights = torch.tensor(before).cuda()
+        got.append((pa.pa_prefill_chunk_weights(*args, weights, _prefill_ws(case, lens, q)), weights))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    want, mag, add, rel = _prefill_want(case, lens, q, k, v, table, cu, scale, before.shape[2])
+    _check_out(got[1][0], want, mag, rel, case[0])
+    _check_weights(got[1][1], before, add, rel, q.shape[0] * case[2] // case[3])
+
+
+@pytest.mark.gpu
 def test_prefill_weights_many_chunks_of_few_sequences():
     """More chunks than a launch looks at together, in mixed order: the sums are those of one chunk after the other."""
     rng = np.random.default_rng(11)
