@@ -572,7 +572,7 @@ PA_API int pa_decode_weights(void* out, const void* q, int num_seqs, int num_q_h
  * that sees the key, what the query's heads give it (as pa_decode_weights does for
  * one query); key_weights has a row for each of the num_seqs sequences.
  * max_context_len bounds q_start_pos[c] + n_c: keys at or beyond it are not read
- * (and counted).  Several chunks may belong to one sequence.  The order of every sum is
+ * (and counted); a chunk whose q_start_pos[c] + n_c passes 2^31 - 1 is invalid.  Several chunks may belong to one sequence.  The order of every sum is
  * fixed.  workspace: pa_prefill_weights_workspace_size bytes, 256-byte aligned; it needs no
  * zeroing, and serves every call of no more chunks, queries and context as well.
  * One workspace must not serve two calls that may overlap on the GPU.  q and the

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool chunk_ok =
             n >= 0 && d.r0 >= 0 && d.r0 + n <= p.total_q && n <= p.max_q_len && d.s >= 0 && d.s < p.num_seqs;
         if (chunk_ok && prefix_mode && n > 0) d.start = p.prefix_lens[d.s];  // the group's shared prefix length
-        chunk_ok = chunk_ok && d.start >= 0;
+        chunk_ok = chunk_ok && d.start >= 0 && (!kLse || d.start <= 0x7FFFFFFF - n);
         if (!chunk_ok) {
             if (rank == 0 && d.kvh == 0 && d.span == 0 && threadIdx.x == 0) count_error(p.error_count);
             return false;

@@ -18,7 +18,7 @@ __device__ __forceinline__ bool weight_chunk(const PrefillParams& p, int c, Weig
     d.s = p.seq_of_chunk[c];
     d.start = p.q_start_pos[c];
     if (d.n < 0 || d.r0 < 0 || d.r0 + d.n > p.total_q || d.n > p.max_q_len || d.s < 0 || d.s >= p.num_seqs ||
-        d.start < 0)
+        d.start < 0 || d.start > 0x7FFFFFFF - d.n)
         return false;
     d.cap = min(min(p.context_lens[d.s], p.max_context_len),
                 (int)min((long long)p.max_blocks_per_seq * p.block_size, 0x7FFFFFFFLL));

@@ -333,6 +333,35 @@ def test_prefill_weights_bad_chunks_are_counted_and_left():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_prefill_weights_positions_beyond_the_largest_int(dtype):
+    """A chunk whose last position is no int is counted and left; one that ends at the largest is clamped to its context."""
+    case = (dtype, 128, 4, 1, 16, [(0, 10, 20), (1, 0, 30), (0, 30, 10)], ())
+    lens, k, v, table, q, before, cu, scale = _prefill_case(case)
+    args = list(_prefill_args(case, lens, q, k, v, table, cu, scale))
+    args[2] = _i32([10, 2 ** 31 - 10, 30])
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    weights = torch.tensor(before).cuda()
+    out = torch.full(q.shape, 3.0, dtype=dtype, device="cuda")
+    pa.pa_prefill_chunk_weights(*args, weights, _prefill_ws(case, lens, q), out=out, error_count=err)
+    good = case[:5] + ([case[5][0], case[5][2]], ())
+    rows = np.r_[0:20, 50:60]
+    want, mag, add, rel = _prefill_want(good, lens, q[rows], k, v, table, np.array([0, 20, 30]), scale, before.shape[2])
+    assert int(err) == 1 and torch.all(out[20:50] == 3.0)
+    _check_out(out[torch.tensor(rows)], want, mag, rel, dtype)
+    _check_weights(weights, before, add, rel, 30 * 4)
+
+    args[2] = _i32([10, 2 ** 31 - 1 - 30, 30])
+    weights = torch.tensor(before).cuda()
+    out = pa.pa_prefill_chunk_weights(*args, weights, _prefill_ws(case, lens, q), error_count=err)
+    o, m, w, r = ref.attend(_np(q[20:50]), _np(k), _np(v), table[1], [lens[1]] * 30, scale)
+    add[1, :, :lens[1]] += w
+    assert int(err) > 1
+    _check_out(out[20:50], o, m, r, dtype)
+    _check_weights(weights, before, add, max(rel, r), 60 * 4)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("case", [PREFILLS[1], PREFILLS[3], PREFILLS[10]], ids=["tail", "chunks", "f32"])
 def test_prefill_weights_loose_bound_of_the_chunks(case):
     """max_q_len far above every chunk, up to the largest int: the same work."""
