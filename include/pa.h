@@ -497,7 +497,8 @@ PA_API int pa_prefill_chunk_fp8_block(void* out, const void* q, const int32_t* c
  * indexed like the cache (token j of sequence s is pool row block_tables[s][j/B]
  * * B + j%B); key_width must be no less than max_context_len.  A row belongs to
  * a sequence, not to blocks: sequences that share blocks have weights of their
- * own.
+ * own.  max_context_len beyond 2^30 (pa_decode_weights: 65534 * 1024) is
+ * PA_ERR_UNSUPPORTED.
  *
  * Rotary positions with several axes (time, height, width; one for text): pair i
  * of a head, elements (i, rot_dim/2 + i), or (2i, 2i + 1) where interleaved is
@@ -609,7 +610,8 @@ PA_API int pa_prefill_chunk_weights(void* out, const void* q, const int32_t* cu_
  * The blocks of a sequence with more than `budget` tokens must be its own: no other
  * sequence's table may name them (copy shared ones first, pa_copy_blocks).  A move from or
  * to a block with an invalid table entry is counted and moves no rows.  budget >= 1,
- * keep_first + keep_recent <= budget; head_dim * element size a multiple of 16 bytes, the pools
+ * keep_first + keep_recent <= budget; no head may have more than 65535 * 64 moves to make
+ * (min(budget, max_context_len - budget), else PA_ERR_UNSUPPORTED); head_dim * element size a multiple of 16 bytes, the pools
  * 16-byte aligned.  (e4m3 pools of one scale: as bf16 of half the head_dim; pools with a scale
  * per block cannot be moved between blocks row by row.)  workspace:
  * pa_evict_workspace_size bytes, 256-byte aligned; it needs no zeroing, and serves calls of

@@ -161,7 +161,6 @@ int launch(const DecodeParams& p, dim3 grid, cudaStream_t stream) {
 int launch_decode_weights(const DecodeParams& p, int dtype, cudaStream_t stream) {
     if (p.group > kMaxGroup || p.max_splits > kMaxSplits) return PA_ERR_UNSUPPORTED;
     const int pieces = (p.max_context_len + kTokens - 1) / kTokens;
-    if (pieces >= 65535) return PA_ERR_UNSUPPORTED;
     const dim3 grid(p.num_seqs * p.num_kv_heads, 1 + pieces);
     if (dtype == PA_F32)
         return p.head_dim == 64 ? launch<float, 64>(p, grid, stream) : launch<float, 128>(p, grid, stream);

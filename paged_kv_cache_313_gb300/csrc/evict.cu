@@ -29,7 +29,7 @@ constexpr int kMaxWarps = 32;
 constexpr int kBins = 4096, kLastBins = 256;
 constexpr int kKeysMax = 40 * 1024;  // keys held in shared memory; those of longer contexts are made again when needed
 constexpr int kEarly = 8;  // tokens of a lane that are loaded before the length is known
-constexpr int kMoves = 64, kMoveThreads = 256;
+constexpr int kMoves = kMaxMoves / 65535, kMoveThreads = 256;
 constexpr int kOwnMoves = 128;  // the most moves that select_kernel makes itself
 
 // Larger keys rank first: protected tokens, then weights from +inf down to -inf, -0 as 0, NaN as -inf.

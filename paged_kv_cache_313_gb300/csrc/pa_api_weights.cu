@@ -14,6 +14,10 @@ namespace {
 bool aligned(const void* p, uintptr_t bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
 size_t round_up(size_t n) { return (n + 255) / 256 * 256; }
 
+// Longest contexts: the decode's second launch has a CTA for every 1024 tokens, and 65535 rows of CTAs; elsewhere indices are
+// 32-bit integers that pass a context's end by less than 2^30.
+constexpr int kMaxDecodeContext = 65534 * 1024, kMaxContext = 1 << 30;
+
 // Shapes of the rotary calls.
 int rope_ok(int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int dtype, int num_axes, int rot_dim) {
     if (num_tokens < 0 || num_q_heads < 0 || num_kv_heads < 0 || head_dim < 1 || rot_dim < 0 || rot_dim > head_dim ||
@@ -186,7 +190,8 @@ int pa_rope_write_kv_paged(void* q_out, const void* q, const void* k_new, const 
 
 size_t pa_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int block_size,
                                         int max_context_len) {
-    if (num_seqs < 0 || max_context_len < 0 || decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size))
+    if (num_seqs < 0 || max_context_len < 0 || max_context_len > kMaxDecodeContext ||
+        decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size))
         return 0;
     int num_sms = 0;
     if (check_device(&num_sms) != PA_OK) return 0;
@@ -207,7 +212,7 @@ int pa_decode_weights(void* out, const void* q, int num_seqs, int num_q_heads, i
         return PA_ERR_INVALID_ARG;
     int rc = decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size);
     if (rc != PA_OK) return rc;
-    if (dtype != PA_F32 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if ((dtype != PA_F32 && dtype != PA_BF16) || max_context_len > kMaxDecodeContext) return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
     if (!out || !q || !k_cache || !v_cache || !context_lens || (key_width > 0 && !key_weights) ||
         (max_blocks_per_seq > 0 && !block_tables))
@@ -262,7 +267,7 @@ int pa_decode_weights(void* out, const void* q, int num_seqs, int num_q_heads, i
 
 size_t pa_prefill_weights_workspace_size(int num_chunks, int total_q, int max_q_len, int num_q_heads, int num_kv_heads,
                                          int head_dim, int block_size, int max_context_len) {
-    if (num_chunks < 0 || total_q < 0 || max_q_len < 0 || max_context_len < 0 ||
+    if (num_chunks < 0 || total_q < 0 || max_q_len < 0 || max_context_len < 0 || max_context_len > kMaxContext ||
         decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size))
         return 0;
     int num_sms = 0;
@@ -282,7 +287,7 @@ int pa_prefill_chunk_weights(void* out, const void* q, const int32_t* cu_q_lens,
         return PA_ERR_INVALID_ARG;
     int rc = decode_shape_ok(num_q_heads, num_kv_heads, head_dim, block_size);
     if (rc != PA_OK) return rc;
-    if (dtype != PA_F32 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if ((dtype != PA_F32 && dtype != PA_BF16) || max_context_len > kMaxContext) return PA_ERR_UNSUPPORTED;
     if (num_chunks == 0 || total_q == 0 || max_q_len == 0) return PA_OK;
     if (!out || !q || !cu_q_lens || !q_start_pos || !seq_of_chunk || !k_cache || !v_cache || !context_lens ||
         !block_tables || num_seqs == 0 || (key_width > 0 && !key_weights))
@@ -337,8 +342,9 @@ int pa_prefill_chunk_weights(void* out, const void* q, const int32_t* cu_q_lens,
 }
 
 size_t pa_evict_workspace_size(int num_seqs, int num_kv_heads, int max_context_len, int budget) {
-    if (num_seqs < 0 || num_kv_heads < 1 || max_context_len < 0 || budget < 1) return 0;
-    return evict_workspace_layout(num_seqs, num_kv_heads, max_context_len, budget).total;
+    if (num_seqs < 0 || num_kv_heads < 1 || max_context_len < 0 || max_context_len > kMaxContext || budget < 1) return 0;
+    const EvictWorkspace lay = evict_workspace_layout(num_seqs, num_kv_heads, max_context_len, budget);
+    return lay.max_moves > kMaxMoves ? 0 : lay.total;
 }
 
 int pa_evict_tokens(void* k_cache, void* v_cache, int num_blocks, int block_size, int num_kv_heads, int head_dim,
@@ -350,7 +356,7 @@ int pa_evict_tokens(void* k_cache, void* v_cache, int num_blocks, int block_size
         max_context_len < 0 || key_width < max_context_len || budget < 1 || keep_first < 0 || keep_recent < 0 ||
         (long long)keep_first + keep_recent > budget)
         return PA_ERR_INVALID_ARG;
-    if (dtype != PA_F32 && dtype != PA_BF16) return PA_ERR_UNSUPPORTED;
+    if ((dtype != PA_F32 && dtype != PA_BF16) || max_context_len > kMaxContext) return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0) return PA_OK;
     if (!k_cache || !v_cache || !context_lens || !next_pos || !new_lens || (key_width > 0 && (!key_weights || !key_pos)) ||
         (max_blocks_per_seq > 0 && !block_tables))
@@ -359,9 +365,10 @@ int pa_evict_tokens(void* k_cache, void* v_cache, int num_blocks, int block_size
     if (row_bytes % 16 != 0 || row_bytes > (1 << 20) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         (long long)num_seqs * num_kv_heads > INT_MAX)
         return PA_ERR_UNSUPPORTED;
+    const EvictWorkspace lay = evict_workspace_layout(num_seqs, num_kv_heads, max_context_len, budget);
+    if (lay.max_moves > kMaxMoves) return PA_ERR_UNSUPPORTED;
     int rc = check_device(nullptr);
     if (rc != PA_OK) return rc;
-    const EvictWorkspace lay = evict_workspace_layout(num_seqs, num_kv_heads, max_context_len, budget);
     if (!workspace || workspace_bytes < lay.total || !aligned(workspace, 256)) return PA_ERR_WORKSPACE;
     char* ws = static_cast<char*>(workspace);
     EvictParams p;

@@ -225,6 +225,7 @@ struct RopeParams {
 };
 
 // pa_evict_tokens.
+constexpr int kMaxMoves = 65535 * 64;  // of a (sequence, kv head): rows of CTAs, 64 moves each
 struct EvictWorkspace {
     size_t counts, lens, src, dst, total;  // byte offsets
     int max_moves;

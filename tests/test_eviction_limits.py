@@ -239,3 +239,26 @@ def test_prefill_values_that_are_no_numbers_stay_with_the_queries_that_see_them(
     assert np.isfinite(out[~sees]).all() and not np.isfinite(out[sees]).any() and sees.any()
     _check_out(torch.tensor(np.where(sees, 0, out)), np.where(sees, 0, want), mag, rel, dtype)
     _check_weights(weights, before, add, rel, q.shape[0] * g)
+
+
+def test_contexts_longer_than_launches_reach_are_refused():
+    """On the host, before anything is read: the largest ints are no launch's."""
+    L, ptr, most = pa.lib(), 256, 2 ** 31 - 1
+    for ctx in (65534 * 1024 + 1, 2 ** 30 + 1, most):
+        assert L.pa_decode_weights(ptr, ptr, 1, 2, 1, 64, pa.PA_BF16, ptr, ptr, 4, 16, ptr, 2, ptr, ctx, 1.0, ptr, most, ptr, 0,
+                                   None, None) == pa.PA_ERR_UNSUPPORTED
+        assert L.pa_decode_weights_workspace_size(1, 2, 1, 64, 16, ctx) == 0
+    for ctx in (2 ** 30 + 1, most):
+        assert L.pa_prefill_chunk_weights(ptr, ptr, ptr, ptr, ptr, 1, 1, 1, 1, 2, 1, 64, pa.PA_BF16, ptr, ptr, 4, 16, ptr, 2, ptr,
+                                          ctx, 1.0, ptr, most, ptr, 0, None, None) == pa.PA_ERR_UNSUPPORTED
+        assert L.pa_prefill_weights_workspace_size(1, 1, 1, 2, 1, 64, 16, ctx) == 0
+
+    def evict(ctx, budget):
+        return L.pa_evict_tokens(ptr, ptr, 4, 16, 1, 64, pa.PA_BF16, ptr, 1, 2, ptr, ctx, ptr, ptr, most, ptr, budget, 0, 0, ptr,
+                                 None, 0, None, None)
+
+    for ctx, budget in ((2 ** 30 + 1, 4), (most, 2 ** 30), (2 ** 30, 65535 * 64 + 1), (65535 * 128 + 2, 65535 * 64 + 1)):
+        assert evict(ctx, budget) == pa.PA_ERR_UNSUPPORTED, (ctx, budget)
+        assert L.pa_evict_workspace_size(1, 1, ctx, budget) == 0
+    assert L.pa_evict_workspace_size(1, 1, 65535 * 128, 65535 * 64) > 0
+    assert L.pa_evict_workspace_size(1, 1, 2 ** 30, 2 ** 30 - 5) > 0
