@@ -163,6 +163,22 @@ def test_evict_lengths_over_the_next_places(case):
 
 
 @pytest.mark.gpu
+def test_evict_moves_codes_of_any_bits():
+    """Pools of one-byte codes, given as bf16 of half the head_dim: every pattern of bits arrives as it was."""
+    case = (BF16, 2, 32, 16, [200, 90, 300], 64, 2, 8, "random")
+    state = _case(case)
+    rng = np.random.default_rng(5)
+    codes = [torch.tensor(rng.integers(0, 256, tuple(state[0].shape[:3]) + (64,)), dtype=torch.uint8) for _ in range(2)]
+    dev, new = _run(case, *(c.view(BF16) for c in codes), *state[2:])
+    want = [c.numpy().astype(np.float64) for c in codes]
+    w, places = state[3].copy(), state[4].copy()
+    lens = ref.evict(*want, state[2], case[4], w, places, state[5], 64, 2, 8)
+    assert new.cpu().tolist() == list(lens) and np.array_equal(dev["p"].cpu().numpy(), places)
+    for got, exact in zip((dev["k"], dev["v"]), want):
+        assert np.array_equal(got.cpu().view(torch.uint8).numpy(), exact)
+
+
+@pytest.mark.gpu
 def test_evict_bad_blocks_and_lengths_are_counted():
     case = (BF16, 1, 64, 16, [200, 90], 64, 0, 0, "random")
     k, v, table, w, places, nxt = _case(case)
