@@ -600,7 +600,7 @@ def pa_evict_tokens(k_cache, v_cache, block_tables, context_lens, max_context_le
     """Cut every sequence of more than `budget` cached tokens down to `budget`: each kv head keeps its first keep_first and
     last keep_recent tokens of the sequence (by key_pos and next_pos) and those with the largest key_weights; kept tokens
     at indices beyond the budget move into the places below it that are free.  Returns new_lens, min(context_lens, budget)
-    (context_lens itself may be given for it)."""
+    (context_lens or next_pos itself may be given for it)."""
     r = (_bind_module or _bind()).evict(k_cache, v_cache, block_tables, context_lens, max_context_len, key_weights, key_pos,
                                         next_pos, budget, keep_first, keep_recent, workspace, new_lens, error_count, stream)
     if r.__class__ is int:
