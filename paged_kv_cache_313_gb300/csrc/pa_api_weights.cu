@@ -56,16 +56,19 @@ long long most_partials(int num_seqs, int num_q_heads, int num_kv_heads, int hea
     return most;
 }
 
-// Spans that the keys of pa_prefill_chunk_weights's query tiles are cut into: as many as SMs that the tiles leave idle can
-// take, of three 128-key tiles at least; one where the tiles fill the GPU.  (37 queries over 3000 keys, 16 tiles: 54.4 us
-// with one span, 35.5 with spans of two key tiles, 34.0 of three, 36.1 of four.)
-int spans_of(int num_chunks, int total_q, int max_q_len, int group, int num_kv_heads, int max_context_len, int num_sms) {
-    const int per_tile = 128 / group;
+// Spans that the keys of pa_prefill_chunk_weights's query tiles are cut into: as many as places for CTAs that the tiles leave
+// idle can take; one where the tiles fill the GPU.  On the tensor cores (tiles of 128 rows and 128 keys, a CTA an SM) a span
+// has three key tiles at least: 37 queries over 3000 keys, 16 tiles, 54.4 us with one span, 35.5 with spans of two key tiles,
+// 34.0 of three, 36.1 of four.  On the CUDA cores (tiles of 64, two CTAs an SM) a key tile takes so long that each may be a
+// span: 20 fp32 queries over 235 keys, 32/8 heads, 99 us with spans of three tiles or more, 66 of two, 57 of one.
+int spans_of(int num_chunks, int total_q, int max_q_len, int group, int num_kv_heads, int max_context_len, int num_sms,
+             bool tc) {
+    const int tile = tc ? 128 : 64, ctas = tc ? num_sms : 2 * num_sms, least = tc ? 3 : 1, per_tile = tile / group;
     const long long tiles = (long long)num_chunks * num_kv_heads * ((max_q_len + per_tile - 1) / per_tile);
-    const long long key_tiles = ((long long)max_context_len + 127) / 128;
+    const long long key_tiles = ((long long)max_context_len + tile - 1) / tile;
     // (q may have rows behind its chunks; the workspace holds 128 rows for each SM)
     const long long fit = 128LL * num_sms / ((long long)total_q * group * num_kv_heads);
-    return (int)std::max(1LL, std::min({(long long)kMaxSpans, num_sms / std::max(1LL, tiles), key_tiles / 3, fit}));
+    return (int)std::max(1LL, std::min({(long long)kMaxSpans, ctas / std::max(1LL, tiles), key_tiles / least, fit}));
 }
 
 // Workspace of pa_prefill_chunk_weights: the rows' lse, what comes before each chunk, the keys' partial sums (rows of 256
@@ -328,11 +331,12 @@ int pa_prefill_chunk_weights(void* out, const void* q, const int32_t* cu_q_lens,
     p.key_width = key_width;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     // (the second kernel keeps 8 bytes for each chunk in its 128 KB of key buffers at first)
-    if (prefill_tc_supported(p, dtype) && num_chunks <= 16384 && max_context_len > 0) {
+    const bool tc = prefill_tc_supported(p, dtype) && num_chunks <= 16384 && max_context_len > 0;
+    p.spans = spans_of(num_chunks, total_q, max_q_len, p.group, num_kv_heads, max_context_len, num_sms, tc);
+    p.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
+    p.part_o = reinterpret_cast<float*>(ws + lay.o);
+    if (tc) {
         p.runs = reinterpret_cast<KeyRuns*>(ws + lay.runs);
-        p.spans = spans_of(num_chunks, total_q, max_q_len, p.group, num_kv_heads, max_context_len, num_sms);
-        p.part_ml = reinterpret_cast<float2*>(ws + lay.ml);
-        p.part_o = reinterpret_cast<float*>(ws + lay.o);
         rc = launch_prefill_tc(p, st);
         if (rc == PA_OK) rc = launch_prefill_weights_tc(p, num_sms, st);
     } else {

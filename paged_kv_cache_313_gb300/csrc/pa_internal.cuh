@@ -315,6 +315,7 @@ int launch_decode_weights(const DecodeParams& p, int dtype, cudaStream_t stream)
 // Prefill with lse, partial and key_weights set: the attention with its rows' lse, the keys' partial sums, their addition.
 int launch_prefill_weights_fma(const PrefillParams& p, int dtype, cudaStream_t stream);
 int launch_prefill_weights_tc(const PrefillParams& p, int num_sms, cudaStream_t stream);
+int launch_prefill_spans_join(const PrefillParams& p, int dtype, cudaStream_t stream);
 int launch_prefill_weights_add(const PrefillParams& p, cudaStream_t stream);
 int launch_rope(const RopeParams& p, int dtype, int num_sms, cudaStream_t stream);
 int launch_evict(const EvictParams& p, int row_bytes, cudaStream_t stream);

@@ -838,67 +838,11 @@ static int launch(const PrefillParams& p, cudaStream_t stream) {
     return launch_kernel(prefill_tc_kernel<kLse>, dim3(grid), dim3(kThreads), kSmem, stream, tmq, tmk, tmv, p);
 }
 
-// The spans' partial rows joined, and their lse: a warp a (query, head).  Row = chunk row, the heads of a row together.
-static __global__ void __launch_bounds__(256) prefill_spans_join_kernel(const PrefillParams p) {
-    pdl_trigger();
-    pdl_wait();
-    WeightChunk d;
-    if (!weight_chunk(p, blockIdx.y, d)) return;
-    const int G = p.group, Hq = p.num_q_heads, lane = threadIdx.x & 31;
-    const long long rows = (long long)d.n * Hq, row0 = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    if (row0 >= rows) return;
-    const int i = (int)(row0 / Hq), h = (int)(row0 - (long long)i * Hq), kvh = h / G;
-    const size_t stride = (size_t)p.num_kv_heads * p.total_q * G;
-    const size_t row = ((size_t)kvh * p.total_q + d.r0 + i) * G + (h - kvh * G);
-    float2 v[kMaxSpans / 32];
-    float m = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < kMaxSpans / 32; ++k) {
-        const int e = lane + 32 * k;
-        v[k] = e < p.spans ? __ldcg(p.part_ml + e * stride + row) : make_float2(-INFINITY, 0.f);
-        if (v[k].y != 0.f) m = fmaxf(m, v[k].x);
-    }
-    m = warp_max(m);
-    float w[kMaxSpans / 32], sum = 0.f;
-#pragma unroll
-    for (int k = 0; k < kMaxSpans / 32; ++k) {
-        w[k] = v[k].y != 0.f ? v[k].y * exp2f(v[k].x - m) : 0.f;  // (a NaN counts)
-        sum += w[k];
-    }
-    sum = warp_sum(sum);
-    if (lane == 0) p.lse[row] = sum == 0.f ? INFINITY : m + log2f(sum);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const float4* o = reinterpret_cast<const float4*>(p.part_o + row * kD) + lane;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kAhead = 8;
-    for (int e0 = 0; e0 < p.spans; e0 += kAhead) {
-        float4 x[kAhead];
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k)
-            if (e0 + k < p.spans) x[k] = __ldcg(o + (e0 + k) * stride * (kD / 4));
-#pragma unroll
-        for (int k = 0; k < kAhead; ++k) {
-            const int e = e0 + k;
-            const float f = __shfl_sync(0xffffffffu, e < 32 ? w[0] : w[1], e & 31) * inv;
-            if (e < p.spans) {
-                acc.x = fmaf(f, x[k].x, acc.x);
-                acc.y = fmaf(f, x[k].y, acc.y);
-                acc.z = fmaf(f, x[k].z, acc.z);
-                acc.w = fmaf(f, x[k].w, acc.w);
-            }
-        }
-    }
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + ((size_t)(d.r0 + i) * Hq + h) * kD + 4 * lane;
-    *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
-}
-
 int launch_prefill_tc(const PrefillParams& p, cudaStream_t stream) {
     if (p.lse && p.spans > 1) {
         const int rc = launch<true>(p, stream);
         if (rc != PA_OK) return rc;
-        const long long rows = (long long)p.max_q_len * p.num_q_heads;
-        return launch_kernel(prefill_spans_join_kernel, dim3((unsigned)((rows + 7) / 8), p.num_chunks), dim3(256), 0, stream,
-                             p);
+        return launch_prefill_spans_join(p, PA_BF16, stream);
     }
     return p.lse ? launch<true>(p, stream) : launch<false>(p, stream);
 }

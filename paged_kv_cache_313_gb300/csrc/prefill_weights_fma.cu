@@ -6,11 +6,13 @@
 // there are two passes over Q K^T.  attend_kernel: a tile of 64 query rows
 // (positions times the G heads of a kv head) against tiles of 64 keys, with an
 // online softmax; it leaves the output and each row's lse = m + log2(l).
+// Few tiles share their keys' tiles out to several CTAs (spans), whose rows another launch joins.
 // column_kernel: a tile of 64 keys against the row tiles that see it, summing
 // 2^(x - lse) down the rows in registers.  Both hold their tiles in shared
 // memory in 32 bits and compute 4 x 4 scores a thread: bound by the CUDA cores and their
-// shared-memory reads.  Four 512-query fp32 chunks at 1 to 4096, 32/8 heads: 1.62 ms
-// (2.60 as matrix products of a library in 32 bits).
+// shared-memory reads.  Four 512-query fp32 chunks at offsets drawn from 1 to 4096, 32/8 heads: 1.62 ms
+// (2.60 as matrix products of a library in 32 bits); two 60-query chunks over 238 and 522 keys, 8/2 heads, 63 us
+// (196 without the spans).
 #include "prefill_weights.cuh"
 
 namespace pa {
@@ -79,17 +81,21 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const PrefillParams p)
     __shared__ int block_s[kTile];
     pdl_trigger();
     pdl_wait();
-    const int c = blockIdx.y, kvh = blockIdx.z, G = p.group, B = p.block_size;
+    // a tile's keys are cut into spans where there are few tiles
+    const int c = blockIdx.y, kvh = blockIdx.z / p.spans, span = blockIdx.z - kvh * p.spans, G = p.group, B = p.block_size;
     WeightChunk d;
     if (!weight_chunk(p, c, d)) {
-        if (blockIdx.x == 0 && kvh == 0 && threadIdx.x == 0) count_error(p.error_count);
+        if (blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) count_error(p.error_count);
         return;
     }
     const int per_tile = kTile / G, i0 = blockIdx.x * per_tile;
     if (i0 >= d.n) return;
     const int nq = min(per_tile, d.n - i0);
     const int want = d.start + i0 + nq, nkeys = max(0, min(want, d.cap));  // keys [0, nkeys) for the tile's last row
-    if (want > d.cap && kvh == 0 && threadIdx.x == 0) count_error(p.error_count);
+    if (want > d.cap && blockIdx.z == 0 && threadIdx.x == 0) count_error(p.error_count);
+    const int span_keys = ((nkeys + kTile - 1) / kTile + p.spans - 1) / p.spans * kTile;
+    const int key0 = (int)min((long long)nkeys, (long long)span * span_keys);
+    const int key1 = (int)min((long long)nkeys, (long long)key0 + span_keys);
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const int32_t* table = p.block_tables + (size_t)d.s * p.max_blocks_per_seq;
     const T* q = static_cast<const T*>(p.q) + ((size_t)(d.r0 + i0) * p.num_q_heads + (size_t)kvh * G) * D;
@@ -106,12 +112,12 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const PrefillParams p)
 #pragma unroll
         for (int k = 0; k < kCols; ++k) o[i][k][0] = o[i][k][1] = o[i][k][2] = o[i][k][3] = 0.f;
     }
-    for (int j0 = 0; j0 < nkeys; j0 += kTile) {
+    for (int j0 = key0; j0 < key1; j0 += kTile) {
         __syncthreads();
         if ((int)threadIdx.x < kTile) {
             const int j = j0 + threadIdx.x;
             int pb = -1;
-            if (j < nkeys) {
+            if (j < key1) {
                 pb = table[j / B];
                 if (pb < 0 || pb >= p.num_blocks) {
                     if (i0 + nq == d.n && (j % B == 0 || threadIdx.x == 0)) count_error(p.error_count);
@@ -194,6 +200,15 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const PrefillParams p)
         if (r >= nq * G) continue;
         const size_t row = (size_t)(d.r0 + i0) * G + r;
         const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
+        if (p.spans > 1) {
+            const size_t at = ((size_t)span * p.num_kv_heads + kvh) * p.total_q * G + row;
+            if (tx == 0) p.part_ml[at] = make_float2(m[i], l[i]);
+#pragma unroll
+            for (int k = 0; k < kCols; ++k)
+                *reinterpret_cast<float4*>(p.part_o + at * D + 64 * k + 4 * tx) =
+                    make_float4(o[i][k][0] * inv, o[i][k][1] * inv, o[i][k][2] * inv, o[i][k][3] * inv);
+            continue;
+        }
         if (tx == 0) p.lse[(size_t)kvh * p.total_q * G + row] = l[i] == 0.f ? INFINITY : m[i] + log2f(l[i]);
         T* out = static_cast<T*>(p.out) + ((size_t)(d.r0 + i0 + r / G) * p.num_q_heads + (size_t)kvh * G + r % G) * D;
 #pragma unroll
@@ -271,11 +286,82 @@ int launch(const PrefillParams& p, cudaStream_t stream) {
     if (rc == PA_OK) rc = ensure_dynamic_smem(reinterpret_cast<const void*>(column_kernel<T, D>), Shape<D>::kSmem);
     if (rc != PA_OK) return rc;
     const int per_tile = kTile / p.group;
-    rc = launch_kernel(attend_kernel<T, D>, dim3((p.max_q_len + per_tile - 1) / per_tile, p.num_chunks, p.num_kv_heads),
-                       dim3(kThreads), Shape<D>::kSmem, stream, p);
+    rc = launch_kernel(attend_kernel<T, D>,
+                       dim3((p.max_q_len + per_tile - 1) / per_tile, p.num_chunks, p.num_kv_heads * p.spans), dim3(kThreads),
+                       Shape<D>::kSmem, stream, p);
+    if (rc == PA_OK && p.spans > 1) rc = launch_prefill_spans_join(p, sizeof(T) == 4 ? PA_F32 : PA_BF16, stream);
     if (rc != PA_OK || p.max_context_len == 0) return rc;
     return launch_kernel(column_kernel<T, D>, dim3((p.max_context_len + kTile - 1) / kTile, p.num_chunks, p.num_kv_heads),
                          dim3(kThreads), Shape<D>::kSmem, stream, p);
+}
+
+// The spans' partial rows joined, and their lse: a warp a (query, head).  Row = chunk row, the heads of a row together.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) spans_join_kernel(const PrefillParams p) {
+    pdl_trigger();
+    pdl_wait();
+    WeightChunk d;
+    if (!weight_chunk(p, blockIdx.y, d)) return;
+    const int G = p.group, Hq = p.num_q_heads, lane = threadIdx.x & 31;
+    const long long rows = (long long)d.n * Hq, row0 = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    if (row0 >= rows) return;
+    const int i = (int)(row0 / Hq), h = (int)(row0 - (long long)i * Hq), kvh = h / G;
+    const size_t stride = (size_t)p.num_kv_heads * p.total_q * G;
+    const size_t row = ((size_t)kvh * p.total_q + d.r0 + i) * G + (h - kvh * G);
+    float2 v[kMaxSpans / 32];
+    float m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kMaxSpans / 32; ++k) {
+        const int e = lane + 32 * k;
+        v[k] = e < p.spans ? __ldcg(p.part_ml + e * stride + row) : make_float2(-INFINITY, 0.f);
+        if (v[k].y != 0.f) m = fmaxf(m, v[k].x);
+    }
+    m = warp_max(m);
+    float w[kMaxSpans / 32], sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < kMaxSpans / 32; ++k) {
+        w[k] = v[k].y != 0.f ? v[k].y * exp2f(v[k].x - m) : 0.f;  // (a NaN counts)
+        sum += w[k];
+    }
+    sum = warp_sum(sum);
+    if (lane == 0) p.lse[row] = sum == 0.f ? INFINITY : m + log2f(sum);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    constexpr int kPairs = D / 64, kAhead = 8;  // pairs of columns a lane has, 64 columns apart
+    const float2* o = reinterpret_cast<const float2*>(p.part_o + row * D) + lane;
+    float2 acc[kPairs];
+#pragma unroll
+    for (int c = 0; c < kPairs; ++c) acc[c] = make_float2(0.f, 0.f);
+    for (int e0 = 0; e0 < p.spans; e0 += kAhead) {
+        float2 x[kAhead][kPairs];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+            for (int c = 0; c < kPairs; ++c)
+                if (e0 + k < p.spans) x[k][c] = __ldcg(o + (e0 + k) * stride * (D / 2) + 32 * c);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int e = e0 + k;
+            const float f = __shfl_sync(0xffffffffu, e < 32 ? w[0] : w[1], e & 31) * inv;
+            if (e < p.spans)
+#pragma unroll
+                for (int c = 0; c < kPairs; ++c) {
+                    acc[c].x = fmaf(f, x[k][c].x, acc[c].x);
+                    acc[c].y = fmaf(f, x[k][c].y, acc[c].y);
+                }
+        }
+    }
+    T* out = static_cast<T*>(p.out) + ((size_t)(d.r0 + i) * Hq + h) * D + 2 * lane;
+#pragma unroll
+    for (int c = 0; c < kPairs; ++c) {
+        out[64 * c] = from_float<T>(acc[c].x);
+        out[64 * c + 1] = from_float<T>(acc[c].y);
+    }
+}
+
+template <typename T, int D>
+int launch_join(const PrefillParams& p, cudaStream_t stream) {
+    const long long rows = (long long)p.max_q_len * p.num_q_heads;
+    return launch_kernel(spans_join_kernel<T, D>, dim3((unsigned)((rows + 7) / 8), p.num_chunks), dim3(256), 0, stream, p);
 }
 
 // The chunks' partial sums added to their sequences' weights.  The first usable chunk of a sequence adds those of all its
@@ -330,10 +416,15 @@ __global__ void __launch_bounds__(kAddThreads) add_kernel(const PrefillParams p)
 }  // namespace
 
 int launch_prefill_weights_fma(const PrefillParams& p, int dtype, cudaStream_t stream) {
-    if (p.group > 16 || p.num_chunks > 65535 || p.num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (p.group > 16 || p.num_chunks > 65535 || (long long)p.num_kv_heads * p.spans > 65535) return PA_ERR_UNSUPPORTED;
     if (((uintptr_t)p.q & 15) || ((uintptr_t)p.k_cache & 15) || ((uintptr_t)p.v_cache & 15)) return PA_ERR_UNSUPPORTED;
     if (dtype == PA_F32) return p.head_dim == 64 ? launch<float, 64>(p, stream) : launch<float, 128>(p, stream);
     return p.head_dim == 64 ? launch<__nv_bfloat16, 64>(p, stream) : launch<__nv_bfloat16, 128>(p, stream);
+}
+
+int launch_prefill_spans_join(const PrefillParams& p, int dtype, cudaStream_t stream) {
+    if (dtype == PA_F32) return p.head_dim == 64 ? launch_join<float, 64>(p, stream) : launch_join<float, 128>(p, stream);
+    return p.head_dim == 64 ? launch_join<__nv_bfloat16, 64>(p, stream) : launch_join<__nv_bfloat16, 128>(p, stream);
 }
 
 int launch_prefill_weights_add(const PrefillParams& p, cudaStream_t stream) {

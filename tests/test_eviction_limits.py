@@ -117,6 +117,29 @@ def test_prefill_few_queries_over_many_keys():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("shape", [(F32, 128, 4, 1, 16), (F32, 64, 6, 2, 8), (BF16, 64, 8, 1, 32), (BF16, 128, 4, 2, 24)], ids=str)
+def test_prefill_few_queries_over_many_keys_on_the_cuda_cores(shape):
+    """As above: contexts around the spans' borders, chunks of different lengths, spans of masked blocks alone, NaN queries."""
+    for chunks, holes in (([(0, 3000, 5)], ()), ([(0, 191, 1)], ()), ([(0, 383, 2), (1, 384, 70), (0, 0, 3)], ()),
+                          ([(0, 1535, 17), (1, 2, 4)], tuple((0, i) for i in range(3, 60)))):
+        case = shape + (chunks, holes)
+        lens, k, v, table, q, before, cu, scale = _prefill_case(case)
+        want, mag, add, rel = _prefill_want(case, lens, q, k, v, table, cu, scale, before.shape[2])
+        args, ws, got = _prefill_args(case, lens, q, k, v, table, cu, scale), _prefill_ws(case, lens, q), []
+        for _ in range(2):
+            weights = torch.tensor(before).cuda()
+            out = torch.full(q.shape, 3.0, dtype=shape[0], device="cuda")
+            got.append((pa.pa_prefill_chunk_weights(*args, weights, ws, out=out), weights))
+            ws.fill_(255)
+        _check_out(got[0][0], want, mag, rel, shape[0])
+        _check_weights(got[0][1], before, add, rel, q.shape[0] * shape[2] // shape[3])
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    q[0] = float("nan")
+    out = pa.pa_prefill_chunk_weights(q.cuda(), *args[1:], torch.tensor(before).cuda(), ws)
+    assert torch.all(torch.isnan(out[0])) and torch.equal(out[1:], got[0][0][1:])
+
+
+@pytest.mark.gpu
 def test_calls_on_two_streams_at_once():
     """Each with a workspace of its own, on their streams' order alone."""
     dcase, pcase = (BF16, 128, 8, 2, 16, [700, 1300, 5], ()), (BF16, 128, 8, 2, 16, [(0, 100, 150), (1, 0, 33)], ())
