@@ -27,27 +27,33 @@ struct Shape {
     static constexpr size_t kSmem = sizeof(float) * (2 * kTile * kPad + kTile * (kTile + 1));
 };
 
-// One row of `src` (D elements, 16-byte aligned) or zeros to shared memory, a 16-byte piece a thread: thread `lane` of the
-// D / VEC that share the row.
-template <typename T> __device__ __forceinline__ void widen(float* dst, const T* src, bool have);
-template <> __device__ __forceinline__ void widen<float>(float* dst, const float* src, bool have) {
-    *reinterpret_cast<float4*>(dst) = have ? *reinterpret_cast<const float4*>(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-}
-template <> __device__ __forceinline__ void widen<__nv_bfloat16>(float* dst, const __nv_bfloat16* src, bool have) {
-    uint2 v = have ? *reinterpret_cast<const uint2*>(src) : make_uint2(0u, 0u);
-    *reinterpret_cast<float4*>(dst) =
-        make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
-                    __uint_as_float(v.y & 0xFFFF0000u));
+// 4 elements as they lie in memory, and as floats.
+template <typename T> struct Four;
+template <> struct Four<float> { using type = float4; };
+template <> struct Four<__nv_bfloat16> { using type = uint2; };
+__device__ __forceinline__ float4 widen(float4 v) { return v; }
+__device__ __forceinline__ float4 widen(uint2 v) {
+    return make_float4(__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u), __uint_as_float(v.y << 16),
+                       __uint_as_float(v.y & 0xFFFF0000u));
 }
 
-// kTile rows into shared memory; row_of(r) gives the row's first element or nullptr.
+// kTile rows into shared memory; row_of(r) gives the row's first element or nullptr (zeros).  A thread's loads are all on
+// their way before the first of them is stored.
 template <typename T, int D, typename F>
 __device__ __forceinline__ void stage(float* dst, F row_of) {
-    constexpr int kPieces = D / 4;
-    for (int i = threadIdx.x; i < kTile * kPieces; i += kThreads) {
-        const int r = i / kPieces, c = i - r * kPieces;
+    using V = typename Four<T>::type;
+    constexpr int kPieces = D / 4, kEach = kTile * kPieces / kThreads;
+    V v[kEach];
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int i = threadIdx.x + k * kThreads, r = i / kPieces, c = i - r * kPieces;
         const T* src = row_of(r);
-        widen<T>(dst + r * Shape<D>::kPad + 4 * c, src + 4 * c, src != nullptr);
+        v[k] = src ? *reinterpret_cast<const V*>(src + 4 * c) : V{};
+    }
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int i = threadIdx.x + k * kThreads, r = i / kPieces, c = i - r * kPieces;
+        *reinterpret_cast<float4*>(dst + r * Shape<D>::kPad + 4 * c) = widen(v[k]);
     }
 }
 
