@@ -10,9 +10,13 @@
 // column_kernel: a tile of 64 keys against the row tiles that see it, summing
 // 2^(x - lse) down the rows in registers.  Both hold their tiles in shared
 // memory in 32 bits and compute 4 x 4 scores a thread: bound by the CUDA cores and their
-// shared-memory reads.  Four 512-query fp32 chunks at offsets drawn from 1 to 4096, 32/8 heads: 1.62 ms
-// (2.60 as matrix products of a library in 32 bits); two 60-query chunks over 238 and 522 keys, 8/2 heads, 63 us
-// (196 without the spans).
+// shared-memory reads.  Four 512-query fp32 chunks at 26 to 587, 32/8 heads: 0.99 ms (1.34
+// with a tile's loads one after the other, a check of each row against each key of V and the
+// probabilities read one by one; with 8 x 4 scores a thread 1.11, but three 100-query bf16
+// chunks of head_dim 64 45 us instead of 33: half as many warps); two 60-query fp32 chunks
+// over 238 and 522 keys, 8/2 heads, 49 us (196 without the spans).
+#include <type_traits>
+
 #include "prefill_weights.cuh"
 
 namespace pa {
@@ -24,7 +28,8 @@ constexpr int kTile = 64;
 template <int D>
 struct Shape {
     static constexpr int kPad = D + 4;  // floats in a staged row: 16-byte accesses of 8 rows touch all banks
-    static constexpr size_t kSmem = sizeof(float) * (2 * kTile * kPad + kTile * (kTile + 1));
+    static constexpr int kPRow = kTile + 4;  // 16-byte aligned
+    static constexpr size_t kSmem = sizeof(float) * (2 * kTile * kPad + kTile * kPRow);
 };
 
 // 4 elements as they lie in memory, and as floats.
@@ -64,7 +69,7 @@ __device__ __forceinline__ void scores(const float* a, const float* b, int ty, i
     for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-#pragma unroll 4
+#pragma unroll 8
     for (int d = 0; d < D; d += 4) {
         float4 x[4], y[4];
 #pragma unroll
@@ -81,9 +86,9 @@ __device__ __forceinline__ void scores(const float* a, const float* b, int ty, i
 
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads) attend_kernel(const PrefillParams p) {
-    constexpr int kPad = Shape<D>::kPad, kCols = D / 64;  // float4 columns a thread holds of each output row
+    constexpr int kPad = Shape<D>::kPad, kPRow = Shape<D>::kPRow, kCols = D / 64;  // float4 columns a thread holds of each output row
     extern __shared__ float smem[];
-    float *qs = smem, *ks = smem + kTile * kPad, *ps = ks + kTile * kPad;  // ps: [kTile][kTile + 1]
+    float *qs = smem, *ks = smem + kTile * kPad, *ps = ks + kTile * kPad;  // ps: [kTile][kPRow]
     __shared__ int block_s[kTile];
     pdl_trigger();
     pdl_wait();
@@ -162,7 +167,7 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const PrefillParams p)
             for (int j = 0; j < 4; ++j) {
                 // (all scores -inf: nothing; NaN scores leave the maximum and make the sum NaN)
                 const float e = x[i][j] == -INFINITY ? 0.f : exp2f(x[i][j] - now);
-                ps[(ty + 16 * i) * (kTile + 1) + tx + 16 * j] = e;
+                ps[(ty + 16 * i) * kPRow + tx + 16 * j] = e;
                 sum += e;
             }
 #pragma unroll
@@ -180,25 +185,36 @@ __global__ void __launch_bounds__(kThreads) attend_kernel(const PrefillParams p)
             for (int k = 0; k < kCols; ++k)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][k][e] *= alpha[i];
-#pragma unroll 4
-        for (int j = 0; j < kTile; ++j) {
-            float4 v[kCols];
+        auto add_values = [&](auto all_see) {
+#pragma unroll 2
+        for (int j = 0; j < kTile; j += 4) {
+            float4 w[4];
 #pragma unroll
-            for (int k = 0; k < kCols; ++k) v[k] = *reinterpret_cast<const float4*>(ks + j * kPad + 64 * k + 4 * tx);
+            for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(ps + (ty + 16 * i) * kPRow + j);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float w = ps[(ty + 16 * i) * (kTile + 1) + j];
-                // a row does not see the keys behind it, whatever they hold
-                if (j0 + j >= limit[i]) continue;
+            for (int e = 0; e < 4; ++e) {
+                float4 v[kCols];
 #pragma unroll
-                for (int k = 0; k < kCols; ++k) {
-                    o[i][k][0] = fmaf(w, v[k].x, o[i][k][0]);
-                    o[i][k][1] = fmaf(w, v[k].y, o[i][k][1]);
-                    o[i][k][2] = fmaf(w, v[k].z, o[i][k][2]);
-                    o[i][k][3] = fmaf(w, v[k].w, o[i][k][3]);
+                for (int k = 0; k < kCols; ++k) v[k] = *reinterpret_cast<const float4*>(ks + (j + e) * kPad + 64 * k + 4 * tx);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float f = e == 0 ? w[i].x : e == 1 ? w[i].y : e == 2 ? w[i].z : w[i].w;
+                    // a row does not see the keys behind it, whatever they hold
+                    if (!all_see && j0 + j + e >= limit[i]) continue;
+#pragma unroll
+                    for (int k = 0; k < kCols; ++k) {
+                        o[i][k][0] = fmaf(f, v[k].x, o[i][k][0]);
+                        o[i][k][1] = fmaf(f, v[k].y, o[i][k][1]);
+                        o[i][k][2] = fmaf(f, v[k].z, o[i][k][2]);
+                        o[i][k][3] = fmaf(f, v[k].w, o[i][k][3]);
+                    }
                 }
             }
         }
+        };
+        // (rows behind the tile's last one are not stored)
+        if (j0 + kTile <= min(d.start + i0 + 1, d.cap)) add_values(std::true_type{});
+        else add_values(std::false_type{});
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
