@@ -91,6 +91,7 @@ __global__ void __launch_bounds__(1024) select_kernel(const EvictParams p, int k
     __shared__ int4 runs[kMaxWarps];
     __shared__ int2 own[kOwn ? kOwnMoves : 1];     // (from, to) as cache indices
     __shared__ Move own_rows[kOwn ? kOwnMoves : 1];
+    __shared__ int own_moves;  // (not in `runs`: other warps may still be reading it when the last one knows the number)
     pdl_trigger();
     pdl_wait();
     const int pair = blockIdx.x, s = pair / p.num_kv_heads, threads = blockDim.x, warps = threads >> 5;
@@ -284,9 +285,9 @@ __global__ void __launch_bounds__(1024) select_kernel(const EvictParams p, int k
         if (warp == warps - 1 && lane == 0) p.counts[pair] = move_at;
         return;
     }
-    if (warp == warps - 1 && lane == 0) runs[0].x = move_at;
+    if (warp == warps - 1 && lane == 0) own_moves = move_at;
     __syncthreads();
-    const int n = runs[0].x;
+    const int n = own_moves;
     if ((int)threadIdx.x < n) {
         const int2 m = own[threadIdx.x];
         own_rows[threadIdx.x] = move_of(p, s, pair - s * p.num_kv_heads, m.x, m.y);
