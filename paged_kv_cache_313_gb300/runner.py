@@ -16,6 +16,9 @@ from .workloads import Workload
 # Per-step inputs, in the order they sit in the packed input buffer, and outputs.
 STEP_INPUTS = ("q_decode", "k_new", "v_new", "block_tables", "context_lens", "seq_idx", "pos", "q_prefill",
                "cu_q_lens", "q_start_pos", "seq_of_chunk", "group_offsets", "prefix_lens")
+# With key_weights two more, behind those: the place in its sequence of each new token (pos is its index in the cache, which
+# after an eviction is another number), and each sequence's next place.
+KEY_INPUTS = ("token_pos", "next_pos")
 STEP_OUTPUTS = ("out_decode", "out_prefill")
 _ALIGN = 256
 
@@ -58,8 +61,12 @@ class DeviceStep:
         # another), so that a serving loop moves a step's inputs in with one
         # host-to-device copy and its outputs out with one copy back.
         host_in = [getattr(w, name).contiguous() for name in STEP_INPUTS]
+        self.step_inputs = STEP_INPUTS
+        if key_weights:  # (before any eviction a token's place is its index)
+            self.step_inputs += KEY_INPUTS
+            host_in += [w.pos.to(torch.int32).contiguous(), w.context_lens.to(torch.int32).contiguous()]
         self.inbuf, views = _packed(host_in, dev)
-        for name, v, t in zip(STEP_INPUTS, views, host_in):
+        for name, v, t in zip(self.step_inputs, views, host_in):
             v.copy_(t)
             setattr(self, name, v)
         self.outbuf, views = _packed([w.q_decode, w.q_prefill], dev)
@@ -119,8 +126,8 @@ class DeviceStep:
         shape = (n, w.num_kv_heads, max(1, self.max_any_context))
         self.key_weights = torch.zeros(shape, dtype=torch.float32, device=dev)
         self.key_pos = torch.arange(shape[2], dtype=torch.int32, device=dev).expand(shape).contiguous()
-        self.next_pos = self.context_lens.clone()
         self.evict_workspaces = {}  # by budget
+        self._inputs_used_up = False  # evict() has been called since the step's inputs were given
         self._no_q = torch.empty(w.seq_idx.numel(), 0, w.head_dim, dtype=w.dtype, device=dev)
         self._no_freq = torch.empty(0, dtype=torch.float32, device=dev)
         sizes = (w.num_q_heads, w.num_kv_heads, w.head_dim, w.block_size)
@@ -133,16 +140,38 @@ class DeviceStep:
     def evict(self, budget: int, keep_first: int = 0, keep_recent: int = 0, stream=None):
         """Cut every sequence of more than `budget` tokens down to the `budget` that have drawn the most weight (its first
         keep_first and last keep_recent tokens stay in any case); context_lens follows on the device.  The sequences'
-        blocks must be their own."""
+        blocks must be their own.  The next step goes on behind the shortened caches: its inputs (context_lens, pos and
+        q_start_pos by the new lengths, token_pos and next_pos by the places in the sequences, which go on counting) come
+        with set_inputs or from host memory, and run() and replay() refuse until they have."""
         if not self.track_weights:
             raise ValueError("evict() needs DeviceStep(key_weights=True)")
         if budget not in self.evict_workspaces:  # (kept: a captured eviction goes on using its own)
             self.evict_workspaces[budget] = pa.new_evict_workspace(self.w.block_tables.shape[0], self.w.num_kv_heads,
                                                                    self.max_any_context, budget, device=self.device)
-        return pa.pa_evict_tokens(self.k_cache, self.v_cache, self.block_tables, self.context_lens, self.max_any_context,
+        lens = pa.pa_evict_tokens(self.k_cache, self.v_cache, self.block_tables, self.context_lens, self.max_any_context,
                                   self.key_weights, self.key_pos, self.next_pos, budget, keep_first, keep_recent,
                                   self.evict_workspaces[budget], new_lens=self.context_lens, error_count=self.error_count,
                                   stream=stream)
+        self._inputs_used_up = True
+        return lens
+
+    def set_inputs(self, **tensors):
+        """Copy a step's inputs (by their names in step_inputs, of the shapes that they have) into their places on the
+        device; those not named stay as they are."""
+        for name, t in tensors.items():
+            if name not in self.step_inputs:
+                raise ValueError(f"{name} is not one of the step's inputs {self.step_inputs}")
+            here = getattr(self, name)
+            if t.shape != here.shape or t.dtype != here.dtype:
+                raise ValueError(f"{name} must be {tuple(here.shape)} of {here.dtype}, got {tuple(t.shape)} of {t.dtype}")
+        for name, t in tensors.items():
+            getattr(self, name).copy_(t)
+        self._inputs_used_up = False
+
+    def _check_inputs(self):
+        if self.track_weights and self._inputs_used_up:
+            raise RuntimeError("evict() has shortened the caches that this step's inputs were made for: give the next step's "
+                               "(set_inputs, step_from_host)")
 
     # individual stages --------------------------------------------------
     def slot_mapping(self, stream=None):
@@ -159,7 +188,8 @@ class DeviceStep:
         if self.track_weights:  # the new tokens begin without weight, at their places
             pa.pa_rope_write_kv_paged(self._no_q, self.k_new, self.v_new, self.pos, self._no_freq, None, self.k_cache,
                                       self.v_cache, self.block_tables, self.seq_idx, self.pos,
-                                      key_weights=self.key_weights, key_pos=self.key_pos, slot_mapping=self.slots,
+                                      key_weights=self.key_weights, key_pos=self.key_pos, token_pos=self.token_pos,
+                                      slot_mapping=self.slots,
                                       error_count=self.error_count, stream=stream)
             return
         if self.block_scales:
@@ -254,6 +284,7 @@ class DeviceStep:
     def run(self, stream=None):
         """The whole step: write this step's K/V, then attend (the decode tokens' K/V written by the decode
         kernel itself when fused_decode_write)."""
+        self._check_inputs()
         self.write_stage(stream)
         self.decode_stage(stream)
         self.prefill(stream)
@@ -276,6 +307,7 @@ class DeviceStep:
 
     def replay(self):
         """Replay the captured step on the current stream."""
+        self._check_inputs()
         self.graph.replay()
         return self.out_decode, self.out_prefill
 
@@ -291,8 +323,8 @@ class DeviceStep:
 
     def input_views(self, host_in: torch.Tensor) -> dict:
         """Name -> view of a packed input buffer (for filling the next step's inputs)."""
-        _, views = _packed_views(host_in, [getattr(self, n) for n in STEP_INPUTS])
-        return dict(zip(STEP_INPUTS, views))
+        _, views = _packed_views(host_in, [getattr(self, n) for n in self.step_inputs])
+        return dict(zip(self.step_inputs, views))
 
     def output_views(self, host_out: torch.Tensor):
         """(decode output, prefill output) as views of a packed output buffer."""
@@ -311,6 +343,7 @@ class DeviceStep:
         buffer through its device mapping; a large output is copied out after
         the step."""
         pa.pa_stage_copy(self.inbuf, host_in, stream=stream)
+        self._inputs_used_up = False
         dev_out = (self.out_decode, self.out_prefill)
         host_views = self.output_views(host_out)
         direct = [t.numel() * t.element_size() <= self.DIRECT_OUTPUT_BYTES for t in dev_out]
@@ -348,6 +381,7 @@ class DeviceStep:
         hg = getattr(self, "host_graph", None)
         if graph and hg is not None and hg[1] == host_in.data_ptr() and hg[2] == host_out.data_ptr():
             hg[0].replay()
+            self._inputs_used_up = False
         else:
             self.step_from_host(host_in, host_out)
         return host_out
