@@ -50,6 +50,9 @@ __device__ __forceinline__ void load_scores(const float* x, float (&v)[G]) {
     }
 }
 
+// A score's softmax weight.  A masked token's (-inf) is 0 whatever the head's sum is, NaN too.
+__device__ __forceinline__ float weight(float x, float lse) { return x == -INFINITY ? 0.f : exp2f(x - lse); }
+
 // kG: the group's heads, 0 for a number without an instance of its own.
 template <typename T, int D, int kG>
 __global__ void __launch_bounds__(kThreads, 4) decode_weights_kernel(const DecodeParams p) {
@@ -136,9 +139,9 @@ __global__ void __launch_bounds__(kThreads, 4) decode_weights_kernel(const Decod
         float sum = 0.f;
         if constexpr (kG != 0) {
 #pragma unroll
-            for (int g = 0; g < kG; ++g) sum += exp2f(x[e][g] - lse_s[g]);
+            for (int g = 0; g < kG; ++g) sum += weight(x[e][g], lse_s[g]);
         } else {
-            for (int g = 0; g < G; ++g) sum += exp2f(__ldcg(scores + (size_t)j * G + g) - lse_s[g]);
+            for (int g = 0; g < G; ++g) sum += weight(__ldcg(scores + (size_t)j * G + g), lse_s[g]);
         }
         weights[j] = w[e] + sum;
     }

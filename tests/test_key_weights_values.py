@@ -1,0 +1,47 @@
+"""Infinities and NaN in the attention that accumulates the weight each key draws."""
+import numpy as np
+import pytest
+import torch
+
+from test_key_weights import BF16, F32, _decode_case, _i32, lib  # noqa: F401
+from paged_kv_cache_313_gb300 import pa
+
+# dtype, D, Hq, Hkv, B, lengths, blocks without a valid entry: tensor cores (one partition, several, head_dim 64, a group
+# without an instance of its own), CUDA cores (16 heads, blocks of 24, fp32)
+PATHS = [
+    (BF16, 128, 8, 2, 16, [50, 50], ((0, 1), (1, 0))),
+    (BF16, 128, 8, 1, 16, [3000, 90], ((0, 3), (0, 100), (1, 5))),
+    (BF16, 64, 4, 2, 32, [200, 70], ((0, 0),)),
+    (BF16, 128, 6, 2, 16, [100, 40], ((0, 2),)),
+    (BF16, 128, 16, 1, 16, [300, 5], ((0, 7),)),
+    (BF16, 128, 4, 2, 24, [301, 50], ((0, 3),)),
+    (F32, 128, 4, 1, 16, [2500, 40], ((0, 2), (0, 60))),
+]
+_IDS = [f"{c[0]}-{c[1]}-{c[2]}-{c[3]}-{c[4]}"[6:] for c in PATHS]
+
+
+def _decode(case, q, k, v, table, before, scale):
+    dtype, D, Hq, Hkv, B, lens, holes = case
+    weights = torch.tensor(before).cuda()
+    ws = pa.new_decode_weights_workspace(len(lens), Hq, Hkv, D, B, max(lens))
+    out = pa.pa_decode_weights(q.cuda(), k.cuda(), v.cuda(), _i32(table), _i32(lens), max(lens), scale, weights, ws)
+    torch.cuda.synchronize()
+    return out.float().cpu().numpy(), weights.cpu().numpy()
+
+
+def _in_holes(case, s):
+    n, B = case[5][s], case[4]
+    return np.array([(s, j // B) in case[6] for j in range(n)])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", PATHS, ids=_IDS)
+def test_nan_query_leaves_weights_in_invalid_blocks(case):
+    rng, k, v, table, q, before, scale = _decode_case(case)
+    q[0, 0, 7] = float("nan")  # head 0: kv head 0 of sequence 0
+    _, w = _decode(case, q, k, v, table, before, scale)
+    n, hole = case[5][0], _in_holes(case, 0)
+    assert hole.any()
+    assert np.array_equal(w[0, 0, :n][hole], before[0, 0, :n][hole]) and np.isnan(w[0, 0, :n][~hole]).all()
+    assert np.array_equal(w[0, 0, n:], before[0, 0, n:])
+    assert np.isfinite(w[0, 1:]).all() and np.isfinite(w[1:]).all()
