@@ -50,9 +50,6 @@ __device__ __forceinline__ void load_scores(const float* x, float (&v)[G]) {
     }
 }
 
-// A score's softmax weight.  A masked token's (-inf) is 0 whatever the head's sum is, NaN too.
-__device__ __forceinline__ float weight(float x, float lse) { return x == -INFINITY ? 0.f : exp2f(x - lse); }
-
 // kG: the group's heads, 0 for a number without an instance of its own.
 template <typename T, int D, int kG>
 __global__ void __launch_bounds__(kThreads, 4) decode_weights_kernel(const DecodeParams p) {
@@ -80,6 +77,7 @@ __global__ void __launch_bounds__(kThreads, 4) decode_weights_kernel(const Decod
         }
     }
     const float2* ml = p.ws_ml + (size_t)unit * p.max_splits * G;
+    bool nan = false;
     for (int g = warp; g < G; g += kThreads / 32) {
         float2 v[kMaxSplits / 32];
         float m = -INFINITY;
@@ -95,14 +93,16 @@ __global__ void __launch_bounds__(kThreads, 4) decode_weights_kernel(const Decod
         for (int k = 0; k < kMaxSplits / 32; ++k)
             if (v[k].y != 0.f) sum += v[k].y * exp2f(v[k].x - m);  // (a NaN counts: it is not 0)
         sum = warp_sum(sum);
-        if (lane == 0) lse_s[g] = sum == 0.f ? INFINITY : m + log2f(sum);  // no key: every weight is 0
+        const float lse = sum == 0.f ? INFINITY : m + log2f(sum);  // no key: every weight is 0
+        nan |= isnan(lse);
+        if (lane == 0) lse_s[g] = lse;
         if (merge)
 #pragma unroll
             for (int k = 0; k < kMaxSplits / 32; ++k)
                 if (lane + 32 * k < nsplit)
                     share[lane + 32 * k][g] = v[k].y == 0.f ? 0.f : v[k].y * exp2f(v[k].x - m) / sum;
     }
-    __syncthreads();
+    nan = __syncthreads_or(nan);
     if (merge) {
         constexpr int kAhead = 8;
         const float4* o = reinterpret_cast<const float4*>(p.ws_o + (size_t)unit * p.max_splits * G * D);
@@ -137,12 +137,23 @@ __global__ void __launch_bounds__(kThreads, 4) decode_weights_kernel(const Decod
         const int j = first + e * kThreads + threadIdx.x;
         if (j >= L) continue;
         float sum = 0.f;
+        bool masked = true;  // -inf for every head
         if constexpr (kG != 0) {
 #pragma unroll
-            for (int g = 0; g < kG; ++g) sum += weight(x[e][g], lse_s[g]);
+            for (int g = 0; g < kG; ++g) sum += exp2f(x[e][g] - lse_s[g]);
+            if (nan)
+#pragma unroll
+                for (int g = 0; g < kG; ++g) masked = masked && x[e][g] == -INFINITY;
         } else {
-            for (int g = 0; g < G; ++g) sum += weight(__ldcg(scores + (size_t)j * G + g), lse_s[g]);
+            for (int g = 0; g < G; ++g) {
+                const float y = __ldcg(scores + (size_t)j * G + g);
+                sum += exp2f(y - lse_s[g]);
+                masked = masked && y == -INFINITY;
+            }
         }
+        // (-inf - NaN would reach masked tokens.  A look at each score, instead of where a sum is NaN: 156 -> 161 us for 16
+        // long contexts.)
+        if (nan && masked) sum = 0.f;
         weights[j] = w[e] + sum;
     }
 }
