@@ -795,12 +795,17 @@ __global__ void __launch_bounds__(TcCfg<D, kFp8, kPair>::kThreads, TcCfg<D, kFp8
                 const float a0 = mn0 == -INFINITY ? 1.f : fast_exp2(m0 - mn0);
                 const float a1 = mn1 == -INFINITY ? 1.f : fast_exp2(m1 - mn1);
                 float s0 = 0.f, s1 = 0.f;  // (x becomes p = 2^(x - m))
+                // (kScores: NaN scores, which leave the maximum at -inf where they are a head's only ones, stay NaN)
+                auto prob = [](float x_, float mn) {
+                    if (kScores) return fast_exp2(x_ - (mn == -INFINITY ? 0.f : mn));
+                    return mn == -INFINITY ? 0.f : fast_exp2(x_ - mn);
+                };
 #pragma unroll
                 for (int c = 0; c < NC; ++c) {
-                    x[c][0] = mn0 == -INFINITY ? 0.f : fast_exp2(x[c][0] - mn0);
-                    x[c][2] = mn0 == -INFINITY ? 0.f : fast_exp2(x[c][2] - mn0);
-                    x[c][1] = mn1 == -INFINITY ? 0.f : fast_exp2(x[c][1] - mn1);
-                    x[c][3] = mn1 == -INFINITY ? 0.f : fast_exp2(x[c][3] - mn1);
+                    x[c][0] = prob(x[c][0], mn0);
+                    x[c][2] = prob(x[c][2], mn0);
+                    x[c][1] = prob(x[c][1], mn1);
+                    x[c][3] = prob(x[c][3], mn1);
                     s0 += x[c][0] + x[c][2];
                     s1 += x[c][1] + x[c][3];
                 }
@@ -1027,6 +1032,7 @@ __global__ void __launch_bounds__(TcCfg<D, kFp8, kPair>::kThreads, TcCfg<D, kFp8
                 for (int w = 0; w < C::kWarpsPerHead; ++w) {
                     const float mw = red_m[par][w0 + w][h];
                     if (mw != -INFINITY) Ls += red_l[par][w0 + w][h] * fast_exp2(mw - M);
+                    else if (kScores) Ls += red_l[par][w0 + w][h];  // 0, or NaN
                 }
                 float4 acc = *reinterpret_cast<const float4*>(slabs + (w0 * 8 + h) * D + dc);
 #pragma unroll

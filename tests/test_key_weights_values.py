@@ -45,3 +45,30 @@ def test_nan_query_leaves_weights_in_invalid_blocks(case):
     assert np.array_equal(w[0, 0, :n][hole], before[0, 0, :n][hole]) and np.isnan(w[0, 0, :n][~hole]).all()
     assert np.array_equal(w[0, 0, n:], before[0, 0, n:])
     assert np.isfinite(w[0, 1:]).all() and np.isfinite(w[1:]).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", PATHS, ids=_IDS)
+def test_nan_query_gives_nan_on_every_path(case):
+    """A query head with a NaN: its outputs are NaN, those of every other head and sequence are not."""
+    rng, k, v, table, q, before, scale = _decode_case(case)
+    q[0, 1, 3] = float("nan")
+    out, _ = _decode(case, q, k, v, table, before, scale)
+    assert np.isnan(out[0, 1]).all() and np.isnan(out).sum() == case[1]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", PATHS, ids=_IDS)
+@pytest.mark.parametrize("keys", ["one", "half"])
+def test_nan_keys_reach_their_sequence(case, keys):
+    """A NaN in a key of kv head 0: that head's sums over the sequence are NaN, whichever partition the key is in and whether or
+    not that partition has another key."""
+    rng, k, v, table, q, before, scale = _decode_case(case)
+    n, B, G = case[5][0], case[4], case[2] // case[3]
+    hole = _in_holes(case, 0)
+    tokens = np.arange(n)[~hole]
+    for j in tokens[:1] if keys == "one" else tokens[:len(tokens) // 2]:
+        k[table[0, j // B], j % B, 0, 5] = float("nan")
+    out, w = _decode(case, q, k, v, table, before, scale)
+    assert np.isnan(out[0, :G]).all() and np.isnan(out).sum() == G * case[1]
+    assert np.isnan(w[0, 0, :n][~hole]).all() and np.isnan(w).sum() == (~hole).sum()
