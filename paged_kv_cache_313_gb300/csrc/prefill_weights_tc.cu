@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     }
-    // rows of a query tile that no copy fills (groups that do not divide 128): zeros, whose scores are finite
+    // rows of a query tile that no copy fills (groups that do not divide 128): zeros, whose scores are finite for finite keys
     if (per_tile * G < kTile)
         for (int i = threadIdx.x; i < kQStages * kTileBytes / 16; i += kThreads)
             reinterpret_cast<uint4*>(smem + kQ)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -390,6 +390,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float v[128];
 #pragma unroll
             for (int i = 0; i < 64; ++i) f32x2_unpack(sum2[i], v[2 * i], v[2 * i + 1]);
+            if (r >= per_tile * G) {  // a row that no query fills: 0 times an infinity among the keys is NaN
+#pragma unroll
+                for (int i = 0; i < 128; ++i) v[i] = 0.f;
+            }
             int first = 0;
 #pragma unroll
             for (int n = 64; n >= 4; n >>= 1) {

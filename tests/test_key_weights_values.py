@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_key_weights import BF16, F32, _decode_case, _i32, lib  # noqa: F401
+from test_key_weights import BF16, F32, _decode_case, _i32, _prefill_args, _prefill_case, _prefill_ws, lib  # noqa: F401
 from paged_kv_cache_313_gb300 import pa
 
 # dtype, D, Hq, Hkv, B, lengths, blocks without a valid entry: tensor cores (one partition, several, head_dim 64, a group
@@ -72,3 +72,41 @@ def test_nan_keys_reach_their_sequence(case, keys):
     out, w = _decode(case, q, k, v, table, before, scale)
     assert np.isnan(out[0, :G]).all() and np.isnan(out).sum() == G * case[1]
     assert np.isnan(w[0, 0, :n][~hole]).all() and np.isnan(w).sum() == (~hole).sum()
+
+
+# dtype, D, Hq, Hkv, B, chunks: tensor cores with groups that leave rows of a query tile unused, and that do not; CUDA cores
+PREFILLS = [
+    (BF16, 128, 3, 1, 16, [(0, 300, 100)], ()),
+    (BF16, 128, 10, 2, 32, [(0, 400, 60), (1, 260, 26)], ()),
+    (BF16, 128, 12, 2, 16, [(0, 0, 300)], ()),
+    (BF16, 128, 8, 2, 16, [(0, 300, 100)], ()),
+    (BF16, 64, 3, 1, 16, [(0, 100, 50)], ()),
+    (F32, 128, 3, 1, 16, [(0, 100, 50)], ()),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", PREFILLS, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}-{c[3]}-{len(c[5])}"[6:])
+def test_infinite_keys_that_no_query_looks_at(case):
+    """Keys with an infinity that every query scores -inf draw nothing: as keys whose weights are too small for a number."""
+    lens, k, v, table, q, before, cu, scale = _prefill_case(case)
+    B = case[4]
+    q[..., 9] = -1 - q[..., 9].abs()
+    results = []
+    for far in (1e4, float("inf")):  # (1e4: a score below -880, 2^-1270)
+        for j in (0, 3, 77, 130, 131):
+            k[table[0, j // B], j % B, :, 9] = far
+        weights = torch.tensor(before).cuda()
+        out = pa.pa_prefill_chunk_weights(*_prefill_args(case, lens, q, k, v, table, cu, scale), weights,
+                                          _prefill_ws(case, lens, q))
+        results.append((out[:int(cu[1])], weights))
+    torch.cuda.synchronize()
+    (a, wa), (b, wb) = results
+    assert torch.isfinite(wb).all()
+    # (a chunk that begins at 0 has queries that see no key but such ones: their scores are -inf, their weights those of no
+    # key, where the finite ones have a largest)
+    first = 4 if case[5][0][1] == 0 else 0
+    assert torch.equal(a[first:], b[first:])
+    far = torch.zeros(wa.shape, dtype=torch.bool)
+    far[0, :, :first] = True
+    assert torch.equal(wa.cpu()[~far], wb.cpu()[~far])
