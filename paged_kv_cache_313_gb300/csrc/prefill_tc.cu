@@ -130,6 +130,13 @@ struct Bars {
 
 // kLse: pa_prefill_chunk_weights, which also leaves each row's log2 softmax sum.  The sums then are of 32-bit exponentials
 // (the pairs' rounding would go into every weight), and groups that do not divide 128 leave a tile's last rows unused.
+// P is rounded to bf16 for its MMA here too, whose operands are of one type, V's.  The output is divided by a second sum, of
+// the rounded values: its weights then add up to 1, and what the rounding of a row's largest weights has in common cancels.
+// What is left is the rounding of single weights, up to 2^-9 of each: the output's relative error against 64 bits is 0.0018 for
+// 37 queries over 3000 keys and 0.0019 for four 512-query chunks, where the rounding of the output alone makes 0.0016 and
+// 0.0017 (with the one sum 0.0019 and 0.0020; 2048 queries at 5900 604 us instead of 630, the chunks 68.0 instead of 68.6).
+// P in two bf16 terms, with a second MMA for what the first leaves, errs no more than the output's rounding, but takes 36.0,
+// 73 and 721 us where this takes 34.8, 69 and 630.
 template <bool kLse>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
@@ -475,6 +482,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool row_ok = pos - i0 < nq;
             const int my_last = prefix_mode ? last_key : min(start + pos - d.key0, last_key);  // last key this row may see
             float m_run = -INFINITY, l_run = 0.f;
+            float r_run = 0.f;  // (kLse) the sum of the rounded P; l_run that of the 32-bit ones
             // (kLse) this item's record of V that is no number.  The one that is reset here belongs to the next item; its last
             // reader was two items ago, before the barrier of the last item's epilogue.
             int* nan = nan_s + (kLse ? items_seen % kNanSlots * kNanInts : 0);
@@ -537,6 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (__any_sync(0xffffffffu, rescale)) {
                     const float alpha = rescale ? fast_exp2(m_run - mt) : 1.f;
                     l_run *= alpha;
+                    if (kLse) r_run *= alpha;
                     if (j > 0) {
                         // every PV issued so far (the last is PV_{j-1}) must be done before O changes
                         if (ok && !mbar_wait(bars.o_done((g - 1) & 1), ((g - 1) >> 1) & 1)) ok = false;
@@ -558,25 +567,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // P = 2^(x - m) in bf16, my 64 keys of row r packed in pairs into 32 columns of S buffer j%2
                 // (its first 32 columns for keys 0-63, columns 64-95 for keys 64-127: each thread
                 // overwrites only S values it has already read)
-                float lsum = 0.f;
-                const float neg_m = -m_run;
+                float lsum = 0.f, rsum = 0.f;
+                // (kLse: without a key so far 0, so that 2^(x - m) is 0 for masked keys and NaN for NaN scores, which leave the
+                // maximum at -inf, without a look at each)
+                const float neg_m = kLse && m_run == -INFINITY ? 0.f : -m_run;
                 {
                     uint32_t pk[32];
                     float ls4[4] = {0.f, 0.f, 0.f, 0.f};
-                    if (kLse && dense) {
+                    if (kLse) {
                         const unsigned long long s2 = f32x2_pack(sl2, sl2), m2 = f32x2_pack(neg_m, neg_m);
                         unsigned long long acc2[2] = {f32x2_pack(0.f, 0.f), f32x2_pack(0.f, 0.f)};
+                        unsigned long long rounded2[2] = {f32x2_pack(0.f, 0.f), f32x2_pack(0.f, 0.f)};
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             float y0, y1;
-                            f32x2_unpack(fma_f32x2(f32x2_pack(sv[2 * i], sv[2 * i + 1]), s2, m2), y0, y1);
+                            if (dense) {
+                                f32x2_unpack(fma_f32x2(f32x2_pack(sv[2 * i], sv[2 * i + 1]), s2, m2), y0, y1);
+                            } else {
+                                y0 = sv[2 * i] + neg_m;
+                                y1 = sv[2 * i + 1] + neg_m;
+                            }
                             y0 = fast_exp2(y0);
                             y1 = fast_exp2(y1);
                             pk[i] = pack_bf16x2(y0, y1);
+                            rounded2[i & 1] =
+                                add_f32x2(rounded2[i & 1], f32x2_pack(__uint_as_float(pk[i] << 16),
+                                                                      __uint_as_float(pk[i] & 0xFFFF0000u)));
                             acc2[i & 1] = add_f32x2(acc2[i & 1], f32x2_pack(y0, y1));
                         }
                         f32x2_unpack(acc2[0], ls4[0], ls4[1]);
                         f32x2_unpack(acc2[1], ls4[2], ls4[3]);
+                        float even, odd;
+                        f32x2_unpack(add_f32x2(rounded2[0], rounded2[1]), even, odd);
+                        rsum = even + odd;
                     } else if (PA_PREFILL_EXP2_PAIRS && dense) {
                         // two keys per instruction throughout: x - m by a paired FMA, rounded to a bf16
                         // pair, 2^x of the pair (which is P itself), and the sum of the same bf16 values
@@ -606,9 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         } else {
 #pragma unroll
                             for (int k = 0; k < 64; ++k)
-                                // (kLse: a row of NaN, whose maximum stays -inf, keeps them)
-                                sv[k] = (sv[k] == -INFINITY || (!kLse && m_run == -INFINITY)) ? 0.f
-                                                                                               : fast_exp2(sv[k] + neg_m);
+                                sv[k] = (sv[k] == -INFINITY || m_run == -INFINITY) ? 0.f : fast_exp2(sv[k] + neg_m);
                         }
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
@@ -621,6 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tmem_wait_st();
                 }
                 l_run += lsum;
+                if (kLse) r_run += rsum;
                 };
                 // (kLse: either kind in one piece, so that its instructions lie together: 2048 queries at 5900, 391 -> 373 us)
                 if constexpr (kLse) {
@@ -683,20 +705,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (ok && nt > 0 && !mbar_wait(bars.o_done(g_last & 1), (g_last >> 1) & 1)) ok = false;
             tc_fence_after();
             // combine the halves: M = max(m_a, m_b), O = (f_a O_a + f_b O_b) / (f_a l_a + f_b l_b),
-            // f_x = 2^(m_x - M); the states cross through TMEM columns 0-3 of S0 (free now: the MMA warp
+            // f_x = 2^(m_x - M); the states cross through TMEM columns 0-3 (kLse: 0-5) of S0 (free now: the MMA warp
             // starts the next item only after o_free)
             // (an item without keys has no state to combine and must not touch tensor memory, which the MMA
             // warp may already be filling for the next item)
-            float m_oth = -INFINITY, l_oth = 0.f;
+            float m_oth = -INFINITY, l_oth = 0.f, r_oth = 0.f;
             if (nt > 0) {
                 tmem_st1(tmem + lane_off + half, m_run);
                 tmem_st1(tmem + lane_off + 2 + half, l_run);
+                if (kLse) tmem_st1(tmem + lane_off + 4 + half, r_run);
                 tmem_wait_st();
                 tc_fence_before();
                 softmax_bar();
                 tc_fence_after();
                 m_oth = tmem_ld1(tmem + lane_off + (half ^ 1));
                 l_oth = tmem_ld1(tmem + lane_off + 2 + (half ^ 1));
+                if (kLse) r_oth = tmem_ld1(tmem + lane_off + 4 + (half ^ 1));
                 tmem_wait_ld();
             }
             const float m_a = half ? m_oth : m_run, m_b = half ? m_run : m_oth;
@@ -705,7 +729,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const float f_a = m_a == -INFINITY ? 0.f : fast_exp2(m_a - m_row);
             const float f_b = m_b == -INFINITY ? 0.f : fast_exp2(m_b - m_row);
             const float l_row = f_a * l_a + f_b * l_b;
-            const float inv = l_row > 0.f ? 1.f / l_row : 0.f;
+            const float over = kLse ? (half ? f_a * r_oth + f_b * r_run : f_a * r_run + f_b * r_oth) : l_row;
+            const float inv = over > 0.f ? 1.f / over : 0.f;
             // (kLse) a span's rows go to part_o / part_ml, and their lse is the join's
             const bool span_mode = kLse && spans > 1;
             const size_t span_row = ((size_t)(d.span * p.num_kv_heads + kvh) * p.total_q + r0 + pos) * G + r % G;
