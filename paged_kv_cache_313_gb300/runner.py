@@ -19,6 +19,8 @@ STEP_INPUTS = ("q_decode", "k_new", "v_new", "block_tables", "context_lens", "se
 # With key_weights two more, behind those: the place in its sequence of each new token (pos is its index in the cache, which
 # after an eviction is another number), and each sequence's next place.
 KEY_INPUTS = ("token_pos", "next_pos")
+# With inv_freq two more: the positions that turn the decode tokens' and the chunks' tokens' queries and keys, [axes, tokens].
+ROPE_INPUTS = ("rope_pos_decode", "rope_pos_prefill")
 STEP_OUTPUTS = ("out_decode", "out_prefill")
 _ALIGN = 256
 
@@ -46,12 +48,18 @@ def _packed_views(buf, like):
 
 class DeviceStep:
     def __init__(self, w: Workload, device: str | torch.device = "cuda", with_error_count: bool = True,
-                 cascade: bool = True, fused_decode_write: bool = True, key_weights: bool = False):
+                 cascade: bool = True, fused_decode_write: bool = True, key_weights: bool = False, inv_freq=None, axis=None,
+                 interleaved: bool = False):
         dev = torch.device(device)
         # key_weights: decode and prefill accumulate the weight that each cached token draws, and evict() can cut the
         # sequences down by it (bf16 and fp32 pools)
         if key_weights and w.kv_fp8:
             raise ValueError("key weights are accumulated over bf16 or fp32 pools")
+        # inv_freq, axis, interleaved (as pa_rope's, with key_weights): the step turns its queries and new keys by rotary
+        # positions, inputs of the step (at first the tokens' places, on every axis); the keys in the pools are turned already
+        self.turns = inv_freq is not None
+        if self.turns and not key_weights:
+            raise ValueError("rotary positions are turned by the write of DeviceStep(key_weights=True)")
         self.w = w
         self.device = dev
         up = lambda t: t.to(dev).contiguous()  # noqa: E731
@@ -65,6 +73,9 @@ class DeviceStep:
         if key_weights:  # (before any eviction a token's place is its index)
             self.step_inputs += KEY_INPUTS
             host_in += [w.pos.to(torch.int32).contiguous(), w.context_lens.to(torch.int32).contiguous()]
+        if self.turns:
+            self.step_inputs += ROPE_INPUTS
+            host_in += self._init_turns(inv_freq, axis, interleaved)
         self.inbuf, views = _packed(host_in, dev)
         for name, v, t in zip(self.step_inputs, views, host_in):
             v.copy_(t)
@@ -118,6 +129,25 @@ class DeviceStep:
         n = pa.pa_prefill_workspace_size(w.num_chunks, w.max_q_len, w.num_q_heads, w.num_kv_heads, w.head_dim,
                                          w.block_size) if w.num_chunks else 0
         self.prefill_workspace = torch.zeros(max(n, 1), dtype=torch.uint8, device=dev) if n else None
+
+    # rotary positions -----------------------------------------------------
+    def _init_turns(self, inv_freq, axis, interleaved):
+        """Returns the first step's positions."""
+        w, nd = self.w, self.w.num_decode
+        order = torch.cat([torch.arange(nd), w.seq_of_chunk.long().repeat_interleave((w.cu_q_lens[1:] - w.cu_q_lens[:-1]).long())])
+        if not torch.equal(w.seq_idx.long(), order):
+            raise ValueError("the new tokens must be the decode sequences', then the chunks', one for each query")
+        self.inv_freq = torch.as_tensor(inv_freq, dtype=torch.float32).to(self.device).contiguous()
+        if axis is not None:
+            axis = torch.as_tensor(axis, dtype=torch.int32)
+            if axis.shape != self.inv_freq.shape or (axis.numel() and int(axis.min()) < 0):
+                raise ValueError("axis must have one entry, 0 or more, for each of inv_freq's")
+        self.interleaved = bool(interleaved)
+        axes = int(axis.max()) + 1 if axis is not None and axis.numel() else 1
+        self.axis = None if axis is None else axis.to(self.device).contiguous()
+        self.turned_q_decode = torch.empty(w.q_decode.shape, dtype=w.dtype, device=self.device)
+        self.turned_q_prefill = torch.empty(w.q_prefill.shape, dtype=w.dtype, device=self.device)
+        return [w.pos[part].to(torch.int32).expand(axes, -1).contiguous() for part in (slice(0, nd), slice(nd, None))]
 
     # eviction -------------------------------------------------------------
     def _init_key_state(self, dev):
@@ -185,12 +215,15 @@ class DeviceStep:
 
     def write_kv_paged(self, stream=None):
         """Slot mapping and K/V write in one call (the slots are still recorded)."""
-        if self.track_weights:  # the new tokens begin without weight, at their places
-            pa.pa_rope_write_kv_paged(self._no_q, self.k_new, self.v_new, self.pos, self._no_freq, None, self.k_cache,
-                                      self.v_cache, self.block_tables, self.seq_idx, self.pos,
-                                      key_weights=self.key_weights, key_pos=self.key_pos, token_pos=self.token_pos,
-                                      slot_mapping=self.slots,
-                                      error_count=self.error_count, stream=stream)
+        if self.track_weights:
+            if not self.turns:
+                self._write_with_places(0, self.k_new.shape[0], self._no_q, None, self.pos, self._no_freq, stream)
+                return
+            nd, T = self.w.num_decode, self.k_new.shape[0]
+            if nd:
+                self._write_with_places(0, nd, self.q_decode, self.turned_q_decode, self.rope_pos_decode, self.inv_freq, stream)
+            if T > nd:
+                self._write_with_places(nd, T, self.q_prefill, self.turned_q_prefill, self.rope_pos_prefill, self.inv_freq, stream)
             return
         if self.block_scales:
             pa.pa_write_kv_paged_fp8_block(self.k_new, self.v_new, self.k_cache, self.v_cache, self.k_scales,
@@ -206,15 +239,24 @@ class DeviceStep:
         pa.pa_write_kv_paged(self.k_new, self.v_new, self.k_cache, self.v_cache, self.block_tables, self.seq_idx,
                              self.pos, slot_mapping=self.slots, error_count=self.error_count, stream=stream)
 
+    def _write_with_places(self, a, b, q, q_out, rope_pos, inv_freq, stream):
+        """New tokens [a, b), which begin without weight, at their places; their queries and keys turned."""
+        pa.pa_rope_write_kv_paged(q, self.k_new[a:b], self.v_new[a:b], rope_pos, inv_freq, self.axis if self.turns else None,
+                                  self.k_cache, self.v_cache, self.block_tables, self.seq_idx[a:b], self.pos[a:b],
+                                  interleaved=self.turns and self.interleaved, q_out=q_out, key_weights=self.key_weights,
+                                  key_pos=self.key_pos, token_pos=self.token_pos[a:b], slot_mapping=self.slots[a:b],
+                                  error_count=self.error_count, stream=stream)
+
     def decode(self, stream=None):
         w = self.w
         if not w.num_decode:
             return self.out_decode
         nd = w.num_decode
         if self.track_weights:
-            return pa.pa_decode_weights(self.q_decode, self.k_cache, self.v_cache, self.block_tables[:nd],
-                                        self.context_lens[:nd], self.max_context_len, w.scale, self.key_weights[:nd],
-                                        self.workspace, out=self.out_decode, error_count=self.error_count, stream=stream)
+            return pa.pa_decode_weights(self.turned_q_decode if self.turns else self.q_decode, self.k_cache, self.v_cache,
+                                        self.block_tables[:nd], self.context_lens[:nd], self.max_context_len, w.scale,
+                                        self.key_weights[:nd], self.workspace, out=self.out_decode,
+                                        error_count=self.error_count, stream=stream)
         if self.block_scales:
             return pa.pa_decode_fp8_block(self.q_decode, self.k_cache, self.v_cache, self.k_scales, self.v_scales,
                                           self.block_tables[:nd], self.context_lens[:nd], self.max_context_len,
@@ -239,11 +281,11 @@ class DeviceStep:
         if not w.num_chunks:
             return self.out_prefill
         if self.track_weights:
-            return pa.pa_prefill_chunk_weights(self.q_prefill, self.cu_q_lens, self.q_start_pos, self.seq_of_chunk,
-                                               w.max_q_len, self.k_cache, self.v_cache, self.block_tables,
-                                               self.context_lens, self.max_any_context, w.scale, self.key_weights,
-                                               self.prefill_weights_workspace, out=self.out_prefill,
-                                               error_count=self.error_count, stream=stream)
+            return pa.pa_prefill_chunk_weights(self.turned_q_prefill if self.turns else self.q_prefill, self.cu_q_lens,
+                                               self.q_start_pos, self.seq_of_chunk, w.max_q_len, self.k_cache,
+                                               self.v_cache, self.block_tables, self.context_lens, self.max_any_context,
+                                               w.scale, self.key_weights, self.prefill_weights_workspace,
+                                               out=self.out_prefill, error_count=self.error_count, stream=stream)
         if self.block_scales:
             return pa.pa_prefill_chunk_fp8_block(self.q_prefill, self.cu_q_lens, self.q_start_pos, self.seq_of_chunk,
                                                  w.max_q_len, self.k_cache, self.v_cache, self.k_scales,

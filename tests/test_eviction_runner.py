@@ -238,3 +238,67 @@ def test_a_captured_step_with_its_eviction_goes_on():
         runs.append(trace)
     for a, b in zip(*runs):
         assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+# ------------------------------------------------------------------ rotary positions
+def test_rotary_positions_of_a_step_are_checked(monkeypatch):
+    _stubs(monkeypatch)
+    freq = torch.full((32,), 0.1)
+    with pytest.raises(ValueError, match="key_weights=True"):
+        DeviceStep(_decode_only(torch.float32), "cpu", inv_freq=freq)
+    with pytest.raises(ValueError, match="axis must"):
+        DeviceStep(_decode_only(torch.float32), "cpu", key_weights=True, inv_freq=freq, axis=[0] * 31)
+    with pytest.raises(ValueError, match="axis must"):
+        DeviceStep(_decode_only(torch.float32), "cpu", key_weights=True, inv_freq=freq, axis=[-1] * 32)
+    w = _mixed(torch.float32)
+    w.seq_idx = w.seq_idx.flip(0)
+    with pytest.raises(ValueError, match="one for each query"):
+        DeviceStep(w, "cpu", key_weights=True, inv_freq=freq)
+    st = DeviceStep(_mixed(torch.float32), "cpu", key_weights=True, inv_freq=freq, axis=[0, 1] * 16)
+    assert st.rope_pos_decode.tolist() == [[89, 32]] * 2 and st.rope_pos_prefill.shape == (2, 30)
+    st.run()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("make,dtype,interleaved", [(_decode_only, torch.bfloat16, False), (_mixed, torch.bfloat16, True),
+                                                    (_mixed, torch.float32, False)], ids=["decode", "mixed", "mixed-fp32"])
+def test_device_step_turns_queries_and_keys(make, dtype, interleaved):
+    """Steps with positions of their own on two axes, between evictions: the turned queries and stored keys, and the attention
+    over them."""
+    w = make(dtype)
+    freq, axis = (1e4 ** (-np.arange(48) / 48)).astype(np.float32), np.arange(48) % 2
+    st = DeviceStep(w, key_weights=True, inv_freq=torch.tensor(freq), axis=torch.tensor(axis), interleaved=interleaved)
+    loop = _Loop(w, budget=60, first=2, recent=8)
+    host_in, host_out = st.pinned_inputs(), st.pinned_outputs()
+    inputs = {n: t.clone() for n, t in st.input_views(host_in).items()}
+    nd, half = w.num_decode, torch.finfo(dtype).eps / 2
+    for step in range(3):
+        if step:
+            inputs = loop.inputs()
+            places = inputs["token_pos"]
+            both = torch.stack([places, places // 3 + 1000])
+            inputs["rope_pos_decode"], inputs["rope_pos_prefill"] = both[:, :nd], both[:, nd:]
+            for name, t in inputs.items():
+                st.input_views(host_in)[name].copy_(t)
+        st.step_from_host(host_in, host_out)
+        torch.cuda.synchronize()
+        rope = torch.cat([inputs["rope_pos_decode"], inputs["rope_pos_prefill"]], dim=1).numpy()
+        q = _double(torch.cat([inputs["q_decode"], inputs["q_prefill"]]))
+        rows = w.block_tables.long()[w.seq_idx.long(), inputs["pos"].long() // 16], inputs["pos"].long() % 16
+        got_q = _double(torch.cat([st.turned_q_decode, st.turned_q_prefill]))
+        for got, x in ((got_q, q), (_double(st.k_cache.cpu()[rows]), _double(inputs["k_new"]))):
+            want, mag = ref.turn(x, rope, freq, axis, interleaved)
+            assert np.all(np.abs(got - want) <= half * np.abs(want) + 2.0 ** -20 * mag)
+        assert np.array_equal(_double(st.v_cache.cpu()[rows]), _double(inputs["v_new"]))
+        dec, pre = st.output_views(host_out)
+        if w.num_decode:
+            st.out_decode.copy_(dec)
+        if w.num_chunks:
+            st.out_prefill.copy_(pre)
+        _check_outputs(st, w, loop, dict(q_decode=st.turned_q_decode, q_prefill=st.turned_q_prefill))
+        before = _before(st, w)
+        st.evict(60, keep_first=2, keep_recent=8)
+        torch.cuda.synchronize()
+        loop.check_cut(st, before)
+        loop.cut()
+    assert st.errors() == 0
