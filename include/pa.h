@@ -556,9 +556,9 @@ PA_API int pa_rope_write_kv_paged(void* q_out, const void* q, const void* k_new,
  * pa_decode_weights_workspace_size bytes (which serve every call of no more
  * sequences and no longer contexts as well; it holds every score, 4 bytes for each
  * query head and token), 256-byte aligned, zeroed once.  One workspace must not
- * serve two calls that may overlap on the GPU.  A query with a NaN makes the
- * weights of its sequence's keys in valid blocks NaN.  The pools must be 16-byte aligned, else
- * PA_ERR_UNSUPPORTED.
+ * serve two calls that may overlap on the GPU.  A query head with a NaN
+ * has NaN for its output and makes the weights of its kv head's keys in valid blocks
+ * NaN.  The pools must be 16-byte aligned, else PA_ERR_UNSUPPORTED.
  */
 PA_API size_t pa_decode_weights_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                                int block_size, int max_context_len);

@@ -3,15 +3,20 @@
 //
 // One CTA per (sequence, kv head, partition of the context).  Tiles of 32 tokens
 // come in through a ring of two (cp.async, 16 bytes a thread, rows of tokens without a
-// valid block filled with zeros), so that a tile is on its way while one is worked on:
-// bound by memory.  Scores: eight lanes a token, each on every eighth 16-byte piece of
+// valid block filled with zeros), so that a tile is on its way while one is worked on.  Scores: eight lanes a token, each on every eighth 16-byte piece of
 // its row against all G query heads.  Softmax: a warp a head, a lane a token, online.
 // P V: a thread four columns and a share of the tile's tokens, its share of the output
 // in registers until the partition ends.  Scores go to the workspace and every
 // partition's (m, l) too; decode_weights.cu does the rest.
 //
-// 64 fp32 sequences (18,000 tokens, 32/8 heads): 96 us, 1.5 TB/s; four of 1 to 40 tokens 7.1 us
-// with both launches.  The CUDA-core decode kernel with the scores added (a warp a token, 64-token
+// Bound by latency, not by memory: 64 fp32 sequences (12,500 tokens, 32/8 heads), 79 us under the
+// profiler, have DRAM at 17% and issue in 45% of the cycles with 16 warps an SM, whose wait is for
+// shared memory (2.1 cycles an instruction), instructions' own latency (2.0) and the blocks'
+// look-ups (1.2).  With 16 bf16 heads a kv head one CTA fits an SM: issue in 27%, 3.5 cycles an
+// instruction for shared memory.
+//
+// 64 fp32 sequences (18,000 tokens, 32/8 heads): 96 us, 1.5 TB/s = 0.22 of the copy bandwidth; four
+// of 1 to 40 tokens 7.1 us with both launches.  The CUDA-core decode kernel with the scores added (a warp a token, 64-token
 // pieces one after the other) took 498 and 19.0, and 1054 instead of 166 with 16 bf16 heads a kv
 // head.
 #include "decode_common.cuh"

@@ -133,8 +133,9 @@ struct Bars {
 // P is rounded to bf16 for its MMA here too, whose operands are of one type, V's.  The output is divided by a second sum, of
 // the rounded values: its weights then add up to 1, and what the rounding of a row's largest weights has in common cancels.
 // What is left is the rounding of single weights, up to 2^-9 of each: the output's relative error against 64 bits is 0.0018 for
-// 37 queries over 3000 keys and 0.0019 for four 512-query chunks, where the rounding of the output alone makes 0.0016 and
-// 0.0017 (with the one sum 0.0019 and 0.0020; 2048 queries at 5900 604 us instead of 630, the chunks 68.0 instead of 68.6).
+// 37 queries over 3000 keys, 0.0019 for four 512-query chunks and 0.0021 for 2048 queries at 5900, where the rounding of the
+// output alone makes 0.0016 to 0.0017 (with the one sum 0.0019, 0.0020 and 0.0021, the last in 604 us instead of 630, the
+// chunks in 68.0 instead of 68.6).
 // P in two bf16 terms, with a second MMA for what the first leaves, errs no more than the output's rounding, but takes 36.0,
 // 73 and 721 us where this takes 34.8, 69 and 630.
 template <bool kLse>

@@ -110,3 +110,24 @@ def test_infinite_keys_that_no_query_looks_at(case):
     far = torch.zeros(wa.shape, dtype=torch.bool)
     far[0, :, :first] = True
     assert torch.equal(wa.cpu()[~far], wb.cpu()[~far])
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("case", PREFILLS, ids=lambda c: f"{c[0]}-{c[1]}-{c[2]}-{c[3]}-{len(c[5])}"[6:])
+@pytest.mark.parametrize("j", [5, 290])
+def test_nan_key_reaches_the_queries_that_see_it(case, j):
+    """A NaN in a key of kv head 0: NaN for the queries from its own on, and for the weights of all keys that those see."""
+    lens, k, v, table, q, before, cu, scale = _prefill_case(case)
+    dtype, D, Hq, Hkv, B, chunks, holes = case
+    s, start, n = chunks[0]
+    j = min(j, start + n - 2)
+    k[table[s, j // B], j % B, 0, 3] = float("nan")
+    weights = torch.tensor(before).cuda()
+    out = pa.pa_prefill_chunk_weights(*_prefill_args(case, lens, q, k, v, table, cu, scale), weights, _prefill_ws(case, lens, q))
+    o, w = out.float().cpu().numpy(), weights.cpu().numpy()
+    nan = np.zeros(o.shape, bool)
+    nan[max(0, j - start):n, :Hq // Hkv] = True
+    assert np.array_equal(np.isnan(o), nan)
+    nan = np.zeros(w.shape, bool)
+    nan[s, 0, :start + n] = True
+    assert np.array_equal(np.isnan(w), nan)
