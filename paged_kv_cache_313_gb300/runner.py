@@ -187,7 +187,7 @@ class DeviceStep:
 
     def set_inputs(self, **tensors):
         """Copy a step's inputs (by their names in step_inputs, of the shapes that they have) into their places on the
-        device; those not named stay as they are."""
+        device, on the current stream; those not named stay as they are."""
         for name, t in tensors.items():
             if name not in self.step_inputs:
                 raise ValueError(f"{name} is not one of the step's inputs {self.step_inputs}")
@@ -332,15 +332,22 @@ class DeviceStep:
         self.prefill(stream)
         return self.out_decode, self.out_prefill
 
+    def _rehearse(self, step):
+        """One step on a stream of its own before it is captured; the weights that it adds are taken back."""
+        weights = self.key_weights.clone() if self.track_weights else None
+        side = torch.cuda.Stream(self.device)
+        side.wait_stream(torch.cuda.current_stream(self.device))
+        with torch.cuda.stream(side):
+            step()
+        torch.cuda.current_stream(self.device).wait_stream(side)
+        if weights is not None:
+            self.key_weights.copy_(weights)
+
     def capture(self) -> "torch.cuda.CUDAGraph":
         """Record one whole step (the four library calls) as a CUDA graph, so a
         serving loop replays it with one launch.  Call after at least one eager
         step (first calls configure the kernels)."""
-        side = torch.cuda.Stream(self.device)
-        side.wait_stream(torch.cuda.current_stream(self.device))
-        with torch.cuda.stream(side):
-            self.run()
-        torch.cuda.current_stream(self.device).wait_stream(side)
+        self._rehearse(self.run)
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             self.run()
@@ -404,11 +411,7 @@ class DeviceStep:
         bound to these two pinned buffers: a serving loop writes the next step's
         inputs into host_in, replays, and reads host_out once the stream is
         synchronised.  Call after one eager step."""
-        side = torch.cuda.Stream(self.device)
-        side.wait_stream(torch.cuda.current_stream(self.device))
-        with torch.cuda.stream(side):
-            self.step_from_host(host_in, host_out)
-        torch.cuda.current_stream(self.device).wait_stream(side)
+        self._rehearse(lambda: self.step_from_host(host_in, host_out))
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             self.step_from_host(host_in, host_out)

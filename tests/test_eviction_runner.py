@@ -302,3 +302,21 @@ def test_device_step_turns_queries_and_keys(make, dtype, interleaved):
         loop.check_cut(st, before)
         loop.cut()
     assert st.errors() == 0
+
+
+@pytest.mark.gpu
+def test_capturing_a_step_adds_no_weight():
+    """The step that is run before a capture is not counted again."""
+    w = _mixed(torch.bfloat16)
+    st = DeviceStep(w, key_weights=True)
+    host_in, host_out = st.pinned_inputs(), st.pinned_outputs()
+    st.step_from_host(host_in, host_out)
+    torch.cuda.synchronize()
+    want, places = st.key_weights.clone(), st.key_pos.clone()
+    assert float(want.sum()) > 0
+    st.capture()
+    torch.cuda.synchronize()
+    assert torch.equal(st.key_weights, want) and torch.equal(st.key_pos, places)
+    st.capture_from_host(host_in, host_out)
+    torch.cuda.synchronize()
+    assert torch.equal(st.key_weights, want) and torch.equal(st.key_pos, places)
