@@ -202,9 +202,10 @@ __device__ __forceinline__ void decode_item(const int* cum, int N, int Hkv, int 
 // kPrefix: the cascade's kernel, whose queue begins with shared-prefix items (a separate instantiation, so that
 // the prefix items' four-chunk code does not shape the plain decode kernel's)
 // kScores: pa_decode_weights, which leaves the scores and every item's (m, l) in the workspace (bf16 pools)
-// Its P is rounded to bf16 for P V as pa_decode's is, so that either call gives the other's output.  A warp's largest weight is
-// 1, which is exact; what the others lose makes the output's relative error against 64 bits 0.0017 for 64 sequences and for 16
-// long contexts, where the rounding of the output alone makes 0.0016.  Weights and sums are of 32-bit exponentials.
+// Its P is rounded to bf16 for P V as pa_decode's is, so that the two calls' outputs agree to their last rounding.  A warp's
+// largest weight is 1, which is exact; what the others lose makes the output's relative error against 64 bits 0.0016 to 0.0018
+// (64 sequences, 16 long contexts), where the rounding of the output alone makes 0.0016 to 0.0017.  The keys' weights and the
+// sums are of 32-bit exponentials.
 template <int D, bool kFp8, bool kPair, bool kPrefix, bool kScores>
 __global__ void __launch_bounds__(TcCfg<D, kFp8, kPair>::kThreads, TcCfg<D, kFp8, kPair>::kCtasPerSm)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
